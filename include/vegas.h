@@ -285,6 +285,100 @@ vegas_status_t vegas_decode_iteration(
     size_t workspace_bytes, void* stream, void* select_stream);
 
 /* ------------------------------------------------------------------------
+ * (5) Prompts.  The paper starts from a filled cache; these calls fill it and
+ * attend it for any number of new rows per sequence: whole prompts, chunks of
+ * them behind a cached prefix, and single decode tokens, mixed in one batch.
+ *
+ * Rows are packed: sequence b owns rows row_start[b] .. row_start[b + 1] - 1
+ * (n_b of them, possibly none), row t of it at cache position
+ * ctx_lens[b] + t.  row_start is device int32 [batch + 1], ascending;
+ * total_rows is the number of rows in the tensors, at least row_start[batch]:
+ * rows behind the last sequence are neither read nor written.  Needs
+ * 0 <= ctx_lens[b] and ctx_lens[b] + n_b <= 16 * max_pages_per_seq; a sequence
+ * that breaks this is recorded as a device fault and skipped.  total_rows < 2^24.
+ *
+ * vegas_rope_append turns the query and key heads of every row by their
+ * positions and appends keys and values to the cache.  Pair j < rot_dim / 2
+ * turns by positions[pair_axis[j]][row] * inv_freq[j] (the angle is reduced in
+ * fp64, so far positions are as exact as near ones), multiplied by rope_scale:
+ *   (x, y) -> rope_scale * (x cos - y sin, y cos + x sin),
+ * pair j being elements (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved
+ * is not 0.  Elements from rot_dim on pass through.  K and V rows go to
+ * position ctx_lens[b] + t of the caches of kv, which this call writes.
+ *   q, k, v: device bf16, 16-byte aligned, rows of Hq (Hkv) x head_dim
+ *            contiguous elements *_stride elements apart (a multiple of 8; the
+ *            parts of one fused projection are three pointers into it)
+ *   q_out: device bf16 [total_rows][Hq][head_dim], 16-byte aligned; may be q
+ *          when q_stride = Hq * head_dim
+ *   positions: device int32 [num_axes][total_rows], or NULL for the cache
+ *          position on every axis
+ *   pair_axis: device int32 [rot_dim / 2], each in [0, num_axes); NULL = axis 0
+ *          (num_axes 1, or positions NULL)
+ *   inv_freq: device fp32 [rot_dim / 2]
+ * Supported: rot_dim a multiple of 16 in [0, head_dim].  No two rows may go to
+ * the same slot of the same page.
+ *
+ * vegas_prompt_attn attends causally over the cache: query head h of row t
+ * reads positions [0, ctx_lens[b] + t] of KV head h / G,
+ *   o = sum_i softmax(softmax_scale * q . k_i) v_i,
+ * with K and V of the rows themselves already in the cache.  Slots past a
+ * sequence's last position may hold anything; K and V inside it must be finite.
+ *   q:   device bf16, 16-byte aligned, rows q_stride elements apart (a
+ *        multiple of 8, at least Hq * head_dim)
+ *   out: device bf16 [total_rows][Hq][head_dim], 16-byte aligned, not q
+ *   workspace: vegas_prompt_workspace_size() bytes for the same total_rows,
+ *        batch and kv (a larger one serves smaller calls of the same device;
+ *        not one that other entry points use), 256-byte aligned
+ * Supported: head_dim 64 and 128, G <= 64, softmax_scale > 0.
+ * ---------------------------------------------------------------------- */
+vegas_status_t vegas_rope_append(
+    const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
+    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
+    int batch, void* stream);
+
+size_t vegas_prompt_workspace_size(const vegas_paged_kv_t* kv, int total_rows, int batch);
+
+vegas_status_t vegas_prompt_attn(
+    const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, void* out,
+    const int32_t* row_start, const int32_t* ctx_lens, int total_rows, int batch,
+    float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (6) Log probabilities of given tokens: what accepting or rejecting the
+ * drafted tokens of a verified window, and scoring a prompt, need of the
+ * logits.  For every row r, with x its logits, a = inv_temperature (> 0),
+ * m = max x and Z = sum_i exp(a * (x_i - m)):
+ *   logprob[r] = a * (x_tok - m) - ln Z,      tok = tokens[r]
+ *   rank[r]    = #{i : x_i > x_tok} + #{i < tok : x_i = x_tok}
+ *                (0: the token is the greedy choice)
+ *   entropy[r] = -sum_i p_i ln p_i
+ *   top_ids[r][j], top_logprobs[r][j], j < top_n: the top_n largest logits and
+ *                their log probabilities, largest first, ties to the lower index.
+ * A logit of -inf is a masked token: probability 0, never an alternative; where
+ * fewer than top_n are left the ids are -1 and the log probabilities -inf.  A
+ * row whose mask leaves nothing has entropy 0 and log probabilities -inf.
+ * tokens[r] < 0 means no token: logprob 0, rank -1 (a token >= vocab is
+ * recorded as a device fault and treated so).  NaN and +inf logits are outside
+ * the contract (they spoil their own row only).
+ *   logits: device, dtype VEGAS_DTYPE_BF16 or VEGAS_DTYPE_FP32, rows
+ *           row_stride >= vocab elements apart, aligned to the type
+ *   tokens: device int32 [rows]; may be NULL when logprob and rank are
+ *   logprob, entropy: device fp32 [rows]; rank: device int32 [rows]; each may
+ *           be NULL
+ *   top_ids, top_logprobs: device int32 / fp32 [rows][top_n]
+ * Supported: top_n in [0, 32], rows <= 2^26, vocab <= 2^28.  No workspace.
+ * ---------------------------------------------------------------------- */
+#define VEGAS_DTYPE_BF16 0
+#define VEGAS_DTYPE_FP32 1
+
+vegas_status_t vegas_token_logprobs(
+    const void* logits, int dtype, int64_t row_stride, const int32_t* tokens, int rows,
+    int vocab, float inv_temperature, float* logprob, float* entropy, int32_t* rank, int top_n,
+    int32_t* top_ids, float* top_logprobs, void* stream);
+
+/* ------------------------------------------------------------------------
  * Failure-detection check (the paper has no counterpart).
  *
  * Every wait of these kernels on an on-chip barrier (a TMA tile landing, an

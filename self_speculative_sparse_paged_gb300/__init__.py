@@ -23,6 +23,8 @@ __all__ = [
     "vegas_sparse_decode_attn", "vegas_synth_paged_kv", "vegas_verify_attn_capture_noalloc",
     "vegas_verify_noalloc_max_scratch_bytes", "vegas_check_bounded_wait", "Layer", "layer",
     "vegas_decode_iteration",
+    "vegas_rope_append", "vegas_prompt_workspace_size", "vegas_prompt_attn",
+    "vegas_token_logprobs", "VEGAS_BF16", "VEGAS_FP32",
     "vegas_read_device_status", "vegas_status_string", "vegas_last_error_detail",
     "vegas_abi_version",
 ]
@@ -32,6 +34,10 @@ STATUS = {
     3: "VEGAS_ERR_WORKSPACE_TOO_SMALL", 4: "VEGAS_ERR_CUDA", 5: "VEGAS_ERR_DEVICE_FAULT",
     6: "VEGAS_ERR_DEVICE_TIMEOUT",
 }
+
+
+# Element types of vegas_token_logprobs (VEGAS_DTYPE_*).
+VEGAS_BF16, VEGAS_FP32 = 0, 1
 
 
 class VegasError(RuntimeError):
@@ -129,6 +135,18 @@ class Layer(ctypes.Structure):
 _iteration = _sig("vegas_decode_iteration", _i32,
                   [ctypes.POINTER(Layer), _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
                    _i32, _i32, _i32, _f32, _c_void_p, _sz, _c_void_p, _c_void_p])
+_i64 = ctypes.c_int64
+_rope = _sig("vegas_rope_append", _i32,
+             [_P_KV, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p,
+              _c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _f32, _i32, _i32,
+              _c_void_p])
+_prompt_ws = _sig("vegas_prompt_workspace_size", _sz, [_P_KV, _i32, _i32])
+_prompt = _sig("vegas_prompt_attn", _i32,
+               [_P_KV, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _i32, _i32, _f32,
+                _c_void_p, _sz, _c_void_p])
+_logprobs = _sig("vegas_token_logprobs", _i32,
+                 [_c_void_p, _i32, _i64, _c_void_p, _i32, _i32, _f32, _c_void_p, _c_void_p,
+                  _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p])
 _wait_check = _sig("vegas_check_bounded_wait", _i32, [_i32, _c_void_p, _c_void_p])
 _read_status = _sig("vegas_read_device_status", _i32, [_c_void_p])
 _status_string = _sig("vegas_status_string", ctypes.c_char_p, [_i32])
@@ -274,6 +292,39 @@ def vegas_decode_iteration(layers, ctx_lens, k_per_seq, tail_lens, max_tail: int
     _check(_iteration(arr, len(layers), _ptr(ctx_lens), _ptr(k_per_seq), _ptr(tail_lens),
                       max_tail, batch, gamma, score_stride, k_max, softmax_scale,
                       _ptr(workspace), workspace_bytes, _stream(stream), sel))
+
+
+def vegas_rope_append(kv: PagedKV, q, q_stride: int, k, k_stride: int, v, v_stride: int, q_out,
+                      row_start, ctx_lens, positions, pair_axis, num_axes: int, inv_freq,
+                      rot_dim: int, interleaved: bool, rope_scale: float, total_rows: int,
+                      batch: int, stream=None) -> None:
+    """Rotary positions on packed rows' queries and keys; keys and values go to the cache."""
+    _check(_rope(ctypes.byref(kv), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                 _ptr(q_out), _ptr(row_start), _ptr(ctx_lens), _ptr(positions), _ptr(pair_axis),
+                 num_axes, _ptr(inv_freq), rot_dim, int(interleaved), rope_scale, total_rows,
+                 batch, _stream(stream)))
+
+
+def vegas_prompt_workspace_size(kv: PagedKV, total_rows: int, batch: int) -> int:
+    return _prompt_ws(ctypes.byref(kv), total_rows, batch)
+
+
+def vegas_prompt_attn(kv: PagedKV, q, q_stride: int, out, row_start, ctx_lens, total_rows: int,
+                      batch: int, softmax_scale: float, workspace, workspace_bytes: int,
+                      stream=None) -> None:
+    """Causal attention of packed ragged rows over their sequences' cached positions."""
+    _check(_prompt(ctypes.byref(kv), _ptr(q), q_stride, _ptr(out), _ptr(row_start),
+                   _ptr(ctx_lens), total_rows, batch, softmax_scale, _ptr(workspace),
+                   workspace_bytes, _stream(stream)))
+
+
+def vegas_token_logprobs(logits, dtype: int, row_stride: int, tokens, rows: int, vocab: int,
+                         inv_temperature: float, logprob, entropy, rank, top_n: int, top_ids,
+                         top_logprobs, stream=None) -> None:
+    """Log probability and rank of each row's token, its entropy and top_n alternatives."""
+    _check(_logprobs(_ptr(logits), dtype, row_stride, _ptr(tokens), rows, vocab,
+                     inv_temperature, _ptr(logprob), _ptr(entropy), _ptr(rank), top_n,
+                     _ptr(top_ids), _ptr(top_logprobs), _stream(stream)))
 
 
 def vegas_check_bounded_wait(limit_us: int, outcome=None, stream=None) -> None:

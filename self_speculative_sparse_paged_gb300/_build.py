@@ -38,6 +38,9 @@ UNITS = [
     ("raw_aggregate.cu", "raw_aggregate.o", []),
     ("wait_check.cu", "wait_check.o", []),
     ("sparse_decode.cu", "sparse_decode.o", []),
+    ("prompt_attn.cu", "prompt_attn.o", []),
+    ("rope_append.cu", "rope_append.o", []),
+    ("token_logprobs.cu", "token_logprobs.o", []),
     ("verify_attn.cu", "verify_d128_c1.o", ["-DVEGAS_D=128", "-DVEGAS_CAP=1"]),
     ("verify_attn.cu", "verify_d128_c0.o", ["-DVEGAS_D=128", "-DVEGAS_CAP=0"]),
     ("verify_attn.cu", "verify_d64_c1.o", ["-DVEGAS_D=64", "-DVEGAS_CAP=1"]),

@@ -83,6 +83,60 @@ struct WindowParams {
   int* err;
 };
 
+struct PromptParams {
+  void* out;                // bf16 [total_rows][Hq][D]
+  const int32_t* block_table;
+  const int32_t* row_start; // [B + 1]
+  const int32_t* ctx_lens;  // [B]
+  int total_rows, batch;
+  int num_pages, max_pages;
+  int hq, hkv, group;
+  int tile_tokens;          // tokens per query tile: floor(128 / group)
+  int pair_tokens;          // tokens per item: two tiles
+  float scale_log2;
+  int* tickets;             // [CTAs][2]
+  float* part_ml;           // [CTAs][2 slots][2 tiles][128] (m, l)
+  float* part_o;            // [CTAs][2 slots][2 tiles][D / 4][128] float4
+  int* err;
+};
+
+struct RopeParams {
+  const void *q, *k, *v;    // bf16 rows, strides in elements
+  long long q_stride, k_stride, v_stride;
+  void* q_out;              // bf16 [total_rows][Hq][D]
+  void *k_cache, *v_cache;  // bf16 [pages][Hkv][16][D]
+  const int32_t* block_table;
+  const int32_t* row_start; // [B + 1]
+  const int32_t* ctx_lens;  // [B]
+  const int32_t* positions; // [num_axes][total_rows], or null: the cache position
+  const int32_t* pair_axis; // [rot / 2], or null: axis 0
+  const float* inv_freq;    // [rot / 2]
+  int num_axes, rot, interleaved;
+  float scale;
+  int total_rows, batch;
+  int num_pages, max_pages;
+  int hq, hkv, head_dim;
+  int* err;
+};
+
+struct LogprobParams {
+  const void* logits;       // [rows], row_stride elements apart
+  const int32_t* tokens;    // [rows] or null
+  long long row_stride;
+  int rows, vocab;
+  float inv_temperature;
+  float* logprob;           // [rows] or null
+  float* entropy;           // [rows] or null
+  int32_t* rank;            // [rows] or null
+  int top_n;                // 0 .. kMaxTopLogprobs
+  int32_t* top_ids;         // [rows][top_n]
+  float* top_logprobs;      // [rows][top_n]
+  int cluster;              // CTAs per row
+  int* err;
+};
+constexpr int kMaxTopLogprobs = 32;
+constexpr int kMaxLogprobCluster = 16;
+
 struct RawAggParams {
   const float* raw;         // [B][R][Hq][raw_stride]
   float* scores;            // [B][Hkv][score_stride]
@@ -174,6 +228,13 @@ cudaError_t launch_raw_aggregate(const RawAggParams& p, int batch, int max_len,
 int select_max_chunk();
 int select_chunk_quantum();   // a CTA's chunk is a multiple of this
 cudaError_t launch_select(const SelectParams& p, int cluster, int batch, cudaStream_t stream);
+
+// qmap: 3-D (head_dim, Hq, rows), box (64, group, tile_tokens).
+cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          const CUtensorMap& qmap, const PromptParams& p, int head_dim, int grid,
+                          cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_token_logprobs(const LogprobParams& p, bool bf16, cudaStream_t stream);
 
 // One CTA waits on an mbarrier nothing arrives on, bounded by limit_ns; on
 // running out it records kErrDeviceTimeout in *err and writes 0 to *outcome.

@@ -1,0 +1,746 @@
+// Attention over whole prompts on the 5th-generation tensor cores, head_dim
+// 128 or 64: every row of a packed batch of ragged sequences attends its own
+// sequence's cache causally.
+//
+// For row t of sequence b (n_b rows behind a cached prefix of c_b positions),
+// query head h, KV head g = h / G:
+//   o_t^h = sum_{i <= c_b + t} softmax_i(scale * q_t^h . k_i) v_i.
+//
+// A work item is one pair of query tiles (A, B) of one (sequence, KV head):
+// each tile holds TT = floor(128 / G) consecutive tokens times the G query
+// heads of the group (row r = token * G + head), so a KV tile is read once for
+// the whole group and for both query tiles.  Per KV tile of 128 positions (8
+// pages) the tensor cores compute
+//   S_X[128 x 128] = Q_X . K^T      (both operands in shared memory, K-major)
+//   O_X[128 x D]  += P_X . V        (P_X in tensor memory, V MN-major)
+// with S_A, S_B, O_A, O_B in tensor memory; P_X (bf16) overwrites the first 64
+// columns of S_X.  The softmax is the running one: thread r of X's warpgroup
+// owns row r (tensor-memory lane r), keeps the row's reference maximum m and
+// sum l in registers, and raises m (rescaling l and its O row) only when a
+// logit exceeds it by 2^8, so O is touched about once per item.
+//
+// Warps 0-3: softmax of A; 4-7: softmax of B; 8, 9: TMA of K and V tiles into
+// one ring; 10: MMA issue; 11: Q tiles.
+//
+// Work division: items carry the cost c0 + (positions up to the item's last
+// row), whose prefix sums have a closed form, and CTA i of N takes the i-th of
+// N equal ranges of the summed cost.  A range may begin and end inside an
+// item; such an item's partial (m, l, O) go through the workspace and the
+// CTA that arrives last joins them in range order.  So a single decode row
+// with a long cache spreads over all SMs, and a large batch keeps every SM
+// busy to the end, with no plan kernel and at most two partial items a CTA.
+#include "kernels.h"
+#include "vegas_common.cuh"
+
+namespace vegas {
+
+namespace {
+
+constexpr int kPThreads = 384;
+constexpr int kTile = 128;            // KV positions per tile, query rows per tile
+constexpr int kItemCost = 256;        // an item's fixed cost, in positions
+constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
+constexpr float kNoMax = -1e30f;      // reference maximum of a row that has seen nothing
+constexpr float kSlack = 8.f;         // log2 units a logit may exceed the reference by
+
+template <int D>
+struct PCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kQ = kHalves * 128 * 128;      // one query tile [half][128 rows][128 B]
+  static constexpr int kSlot = kHalves * 128 * 128;   // one K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kOffRing = 2 * kQ;
+  static constexpr int kOffBar = kOffRing + kSlots * kSlot;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr size_t kSmem = kOffMisc + 128 + 1024;
+  static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
+};
+
+// One point of the linear order of all (sequence, KV head, query-tile pair) items.
+struct Point {
+  int seq, g, p, k;    // k: KV tile inside the item
+  long long us;        // cost before the item
+};
+
+// A sequence's rows and its geometry.
+struct Seq {
+  int row0, n, ctx, pairs;
+  long long per_head;  // summed cost of one head's items
+};
+
+struct Piece {
+  int seq, g, p;
+  int row0, n, ctx;
+  int k0, k1, nt;      // KV tiles of this piece, and of the whole item
+  int nx[2];           // KV tiles query tile A / B needs
+  long long us;
+};
+
+__device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
+  Seq r;
+  r.row0 = q.row_start[s];
+  const int end = q.row_start[s + 1];
+  r.ctx = q.ctx_lens[s];
+  r.n = end - r.row0;
+  const bool bad = r.row0 < 0 || end < r.row0 || end > q.total_rows || r.ctx < 0 ||
+                   (long long)r.ctx + r.n > (long long)q.max_pages * 16;
+  if (bad) {
+    set_error(q.err, kErrDeviceFault);
+    r.n = 0;
+  }
+  r.pairs = (r.n + q.pair_tokens - 1) / q.pair_tokens;
+  const long long P = r.pairs;
+  r.per_head = P * (r.ctx + kItemCost) + q.pair_tokens * (P * (P + 1) / 2);
+  return r;
+}
+
+// Summed cost of a head's items before item p.
+__device__ __forceinline__ long long cost_before(const PromptParams& q, const Seq& s, long long p) {
+  return p * (s.ctx + kItemCost) + q.pair_tokens * (p * (p + 1) / 2);
+}
+
+__device__ __forceinline__ int tiles_of(const PromptParams& q, const Seq& s, int p, int x) {
+  const int first = p * q.pair_tokens + x * q.tile_tokens;
+  if (first >= s.n) return 0;
+  const int last = min(s.n, first + q.tile_tokens) - 1;
+  return (s.ctx + last) / kTile + 1;
+}
+
+// Sum over all sequences (whole warp).
+__device__ __forceinline__ long long total_cost(const PromptParams& q) {
+  long long w = 0;
+  for (int s = threadIdx.x & 31; s < q.batch; s += 32) w += load_seq(q, s).per_head;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w * q.hkv;
+}
+
+// The point at cost u, moved to an item boundary when it would leave fewer
+// than two tiles on one side of it (whole warp; every lane gets the result).
+__device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
+  const int lane = threadIdx.x & 31;
+  Point r;
+  r.seq = q.batch;
+  r.g = r.p = r.k = 0;
+  r.us = 0;
+  long long base = 0;
+  for (int s0 = 0; s0 < q.batch; s0 += 32) {
+    const int s = s0 + lane;
+    Seq sq{};
+    if (s < q.batch) sq = load_seq(q, s);
+    const long long mine = sq.per_head * q.hkv;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const bool hit = mine > 0 && u < base + incl;
+    const unsigned who = __ballot_sync(0xffffffffu, hit);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      sq.row0 = __shfl_sync(0xffffffffu, sq.row0, src);
+      sq.n = __shfl_sync(0xffffffffu, sq.n, src);
+      sq.ctx = __shfl_sync(0xffffffffu, sq.ctx, src);
+      sq.pairs = __shfl_sync(0xffffffffu, sq.pairs, src);
+      sq.per_head = __shfl_sync(0xffffffffu, sq.per_head, src);
+      const long long sbase = base + __shfl_sync(0xffffffffu, incl - mine, src);
+      r.seq = s0 + src;
+      r.g = (int)((u - sbase) / sq.per_head);
+      const long long hbase = sbase + r.g * sq.per_head;
+      const long long rem = u - hbase;
+      int lo = 0, hi = sq.pairs - 1;   // the last p with cost_before(p) <= rem
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cost_before(q, sq, mid) <= rem)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      r.p = lo;
+      r.us = hbase + cost_before(q, sq, lo);
+      const long long o = u - r.us;
+      const int nt = max(tiles_of(q, sq, lo, 0), tiles_of(q, sq, lo, 1));
+      const long long k = o < kItemCost ? 0 : (o - kItemCost + kTile / 2) / kTile;
+      if (k < 2) {
+        r.k = 0;
+      } else if (k <= nt - 2) {
+        r.k = (int)k;
+      } else {   // the next item
+        r.us = hbase + cost_before(q, sq, lo + 1);
+        r.k = 0;
+        if (++r.p == sq.pairs) {
+          r.p = 0;
+          if (++r.g == q.hkv) {
+            r.g = 0;
+            ++r.seq;   // may be an empty sequence: the walk skips those
+          }
+        }
+      }
+      return r;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  r.us = base;
+  return r;
+}
+
+// Walks the items of a CTA's range; every warp walks by itself.
+struct Walk {
+  Point at, end;
+  Seq s;
+  bool have;
+
+  __device__ __forceinline__ Walk(const Point& a, const Point& e) : at(a), end(e), have(false) {}
+
+  __device__ __forceinline__ bool next(const PromptParams& q, Piece& w) {
+    while (true) {
+      if (at.seq >= q.batch || at.seq > end.seq) return false;
+      if (!have) {
+        s = load_seq(q, at.seq);
+        have = true;
+      }
+      if (s.pairs == 0) {
+        ++at.seq;
+        have = false;
+        continue;
+      }
+      const bool last = at.seq == end.seq && at.g == end.g && at.p == end.p;
+      if (last && end.k <= at.k) return false;
+      w.seq = at.seq;
+      w.g = at.g;
+      w.p = at.p;
+      w.row0 = s.row0;
+      w.n = s.n;
+      w.ctx = s.ctx;
+      w.nx[0] = tiles_of(q, s, at.p, 0);
+      w.nx[1] = tiles_of(q, s, at.p, 1);
+      w.nt = max(w.nx[0], w.nx[1]);
+      w.k0 = at.k;
+      w.k1 = last ? end.k : w.nt;
+      w.us = at.us;
+      if (last) {
+        at.seq = q.batch;   // done
+      } else {
+        at.us += s.ctx + kItemCost + (long long)q.pair_tokens * (at.p + 1);
+        at.k = 0;
+        if (++at.p == s.pairs) {
+          at.p = 0;
+          if (++at.g == q.hkv) {
+            at.g = 0;
+            ++at.seq;
+            have = false;
+          }
+        }
+      }
+      return true;
+    }
+  }
+};
+
+// CTAs whose ranges meet the item that costs [us, ...) and has nt tiles.
+__device__ __forceinline__ void sharers(const Piece& w, long long total, int ncta, int& first,
+                                        int& last) {
+  const long long a = w.us + kItemCost + 2 * kTile - kTile / 2;
+  const long long b = w.us + kItemCost + (long long)kTile * w.nt - 2 * kTile + kTile / 2;
+  // boundary i sits at floor(i * total / ncta) >= x exactly when i >= ceil(x * ncta / total)
+  first = (int)((a * ncta + total - 1) / total) - 1;
+  last = (int)((b * ncta + total - 1) / total) - 1;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ CUtensorMap qmap, const PromptParams q) {
+  using Cfg = PCfg<D>;
+  constexpr int NS = Cfg::kSlots;
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + Cfg::kOffBar;
+  auto full = [&](uint32_t s) { return bar0 + 8 * s; };
+  auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
+  auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
+  auto pready = [&](int x) { return bar0 + 8 * (2 * NS + 2 + x); };
+  auto odone = [&](int x) { return bar0 + 8 * (2 * NS + 4 + x); };
+  const uint32_t qfull = bar0 + 8 * (2 * NS + 6), qfree = bar0 + 8 * (2 * NS + 7);
+  const uint32_t drain = bar0 + 8 * (2 * NS + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
+  int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6], cost, CTAs
+  int* failed = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 96);        // [2]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    failed[0] = failed[1] = 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(freed(s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(sfull(x), 1);
+      mbar_init(pready(x), 128);
+      mbar_init(odone(x), 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qfree, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 10) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  griddep_wait();
+
+  // The CTA's range of the summed cost: warp 8 finds its begin, warp 9 its end.
+  if (warp >= 8 && warp < 10) {
+    const long long total = total_cost(q);
+    const int ncta = (int)min((long long)gridDim.x, max(1ll, total / kMinShare));
+    const int i = (int)blockIdx.x + (warp - 8);
+    Point pt;
+    if (i >= ncta || total == 0) {
+      pt.seq = q.batch;
+      pt.g = pt.p = pt.k = 0;
+      pt.us = total;
+    } else {
+      pt = locate(q, i * total / ncta);
+    }
+    if (lane == 0) {
+      int* e = ends + 6 * (warp - 8);
+      e[0] = pt.seq;
+      e[1] = pt.g;
+      e[2] = pt.p;
+      e[3] = pt.k;
+      e[4] = (int)(pt.us & 0xffffffffll);
+      e[5] = (int)(pt.us >> 32);
+      if (warp == 8) {
+        long long* tc = reinterpret_cast<long long*>(ends + 12);
+        tc[0] = total;
+        tc[1] = ncta;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto point = [&](int w) {
+    const int* e = ends + 6 * w;
+    Point r;
+    r.seq = e[0];
+    r.g = e[1];
+    r.p = e[2];
+    r.k = e[3];
+    r.us = ((long long)e[5] << 32) | (uint32_t)e[4];
+    return r;
+  };
+  Walk walk(point(0), point(1));
+  Piece w;
+  bool ok = true;
+
+  if (warp == 8 || warp == 9) {
+    // ------------------------------------------------------------ K (8) and V (9) tiles
+    // Lane j < 8 * D/64 issues box (page j % 8, half j / 8): 16 positions x 64 dims.
+    const bool is_v = warp == 9;
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
+    const int page = lane & 7, half = lane >> 3;
+    uint32_t c = 0;       // tiles so far
+    uint32_t issued = 0;  // of them, issued
+    while (ok && walk.next(q, w)) {
+      const int32_t* row = q.block_table + size_t(w.seq) * q.max_pages;
+      const int npages = (w.ctx + w.n + 15) / 16;
+      int phys = __ldg(&row[min(8 * w.k0 + page, npages - 1)]);
+      for (int t = w.k0; t < w.k1; ++t, ++c) {
+        // a tile's pages past the sequence's end are loaded as its last page (their
+        // positions are masked)
+        const int now = phys;
+        if (t + 1 < w.k1) phys = __ldg(&row[min(8 * (t + 1) + page, npages - 1)]);
+        int pg = now;
+        if (pg < 0 || pg >= q.num_pages) {
+          set_error(q.err, kErrDeviceFault);
+          pg = 0;
+        }
+        const uint32_t j = 2 * c + (is_v ? 1 : 0), s = j % NS, use = j / NS;
+        if (use > 0 &&
+            !__all_sync(0xffffffffu, mbar_wait_bounded(freed(s), (use - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full(s), Cfg::kSlot);
+        __syncwarp();
+        if (half < Cfg::kHalves)
+          tma_load_2d(sbase + Cfg::kOffRing + s * Cfg::kSlot + half * 16384 + page * 2048, map,
+                      64 * half, (pg * q.hkv + w.g) * 16, full(s));
+        __syncwarp();
+        issued = c + 1;
+      }
+    }
+    // every copy in flight lands before the CTA ends (the ring's last NS tiles)
+    for (uint32_t t = issued > NS ? issued - NS : 0; t < issued; ++t) {
+      const uint32_t j = 2 * t + (is_v ? 1 : 0);
+      if (j + NS >= 2 * issued) (void)mbar_wait_bounded(full(j % NS), (j / NS) & 1);
+    }
+    if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ Q tiles
+    uint32_t c = 0;
+    while (ok && walk.next(q, w)) {
+      if (c > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree, (c - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      const int tiles = w.nx[1] > 0 ? 2 : 1;
+      const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qfull, bytes * tiles * Cfg::kHalves);
+        for (int x = 0; x < tiles; ++x)
+          for (int h = 0; h < Cfg::kHalves; ++h)
+            tma_load_3d(sbase + x * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
+                        w.row0 + w.p * q.pair_tokens + x * q.tile_tokens, qfull);
+      }
+      __syncwarp();
+      ++c;
+    }
+    if (c > 0) (void)mbar_wait_bounded(qfull, (c - 1) & 1);   // landed before the CTA ends
+    if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
+    const bool leader = elect_one();
+    const uint64_t dSw = smem_desc(0, 16, 1024, 2);       // K-major, 128-byte swizzle
+    const uint64_t dVmn = smem_desc(0, 16384, 1024, 2);   // MN-major, 64-dim halves 16 KB apart
+    auto with_addr = [](uint64_t d, uint32_t a16) { return d | uint64_t(a16 & 0x3FFFu); };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+    };
+    auto wait_slot = [&](uint32_t j) { return wait_all(full(j % NS), (j / NS) & 1); };
+    auto slot16 = [&](uint32_t j) { return (sbase + Cfg::kOffRing + (j % NS) * Cfg::kSlot) >> 4; };
+    auto issue_s = [&](int x, uint32_t jk) {
+      const uint32_t a = (sbase + x * Cfg::kQ) >> 4, b = slot16(jk);
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma(tmem + 128 * x, with_addr(dSw, a + (ks >> 2) * 1024 + (ks & 3) * 2),
+                 with_addr(dSw, b + (ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
+        tc_commit(sfull(x));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int x, uint32_t jv, bool accumulate) {
+      const uint32_t b = slot16(jv);
+      if (leader) {
+#pragma unroll
+        for (int kp = 0; kp < 8; ++kp)
+          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + 8 * kp, with_addr(dVmn, b + kp * 128),
+                    idPV, accumulate || kp > 0);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint32_t bar) {
+      if (leader) tc_commit(bar);
+      __syncwarp();
+    };
+    uint32_t c = 0, pieces = 0;
+    uint32_t np[2] = {0, 0};   // P tiles consumed of A, B
+    while (ok && walk.next(q, w)) {
+      const int ex[2] = {min(w.k1, w.nx[0]), min(w.k1, w.nx[1])};
+      if (!wait_all(qfull, pieces & 1) || !wait_slot(2 * c)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int x = 0; x < 2; ++x)
+        if (w.k0 < ex[x]) issue_s(x, 2 * c);
+      commit(freed((2 * c) % NS));
+      if (w.k0 + 1 == w.k1) commit(qfree);
+      for (int t = w.k0; t < w.k1 && ok; ++t, ++c) {
+        const uint32_t jv = 2 * c + 1, jk = 2 * c + 2;
+        const bool more = t + 1 < w.k1;
+        if (!wait_slot(jv)) {
+          ok = false;
+          break;
+        }
+        bool have_k = false;
+        for (int x = 0; x < 2; ++x) {
+          if (t >= ex[x]) continue;
+          if (!wait_all(pready(x), np[x] & 1)) {
+            ok = false;
+            break;
+          }
+          ++np[x];
+          tc_fence_after();
+          issue_pv(x, jv, t > w.k0);
+          if (t + 1 == ex[x]) commit(odone(x));
+          if (x == 1 || t >= ex[1]) commit(freed(jv % NS));
+          if (t + 1 < ex[x]) {
+            if (!have_k && !wait_slot(jk)) {
+              ok = false;
+              break;
+            }
+            have_k = true;
+            tc_fence_after();
+            issue_s(x, jk);
+          }
+        }
+        if (ok && more) {
+          commit(freed(jk % NS));
+          if (t + 2 == w.k1) commit(qfree);
+        }
+      }
+      ++pieces;
+    }
+    if (!ok && leader) set_error(q.err, kErrDeviceTimeout);
+    // every MMA issued has completed before tensor memory is released
+    if (leader) tc_commit(drain);
+    __syncwarp();
+    (void)mbar_wait_bounded(drain, 0);
+  } else {
+    // ------------------------------------------------------------ softmax of tile X
+    const int x = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
+    const int tok_r = r / q.group;
+    const int head_r = r - tok_r * q.group;
+    const long long* tc = reinterpret_cast<const long long*>(ends + 12);
+    uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
+    while (ok && walk.next(q, w)) {
+      const int first_tok = w.p * q.pair_tokens + x * q.tile_tokens;
+      const int kend = min(w.k1, w.nx[x]);
+      const int kv_len = w.ctx + w.n;
+      // the last position this row may see (rows behind the sequence: its last)
+      const int lim = w.ctx + min(first_tok + tok_r, w.n - 1);
+      float m = kNoMax, l = 0.f;
+      for (int t = w.k0; t < kend; ++t) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(sfull(x), ns & 1))) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
+        tmem_ld_wait();
+        const int pos0 = t * kTile;
+        if (pos0 + kTile - 1 > w.ctx + first_tok) {
+          // masked: positions the row may not see, whatever their logits hold
+          const int cut = lim - pos0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > cut) s[i] = -INFINITY;
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
+        mx *= q.scale_log2;
+        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
+          const float m2 = fmaxf(m, mx);
+          const float f = ex2(m - m2);
+          m = m2;
+          l *= f;
+          if (t > w.k0) {
+            // the row's earlier P . V products are complete: S of this tile was issued after them
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tmem_ld32(tl + ocol + 32 * i, o);
+              tmem_ld_wait();
+              uint32_t ob[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * f);
+              tmem_st32(tl + ocol + 32 * i, ob);
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ex2(fmaf(s[64 * i + 2 * e], q.scale_log2, -m));
+            const float b = ex2(fmaf(s[64 * i + 2 * e + 1], q.scale_log2, -m));
+            sum[e & 3] += a + b;
+            pk[e] = pack_bf16x2(a, b);   // P to 8 bits of mantissa: the tensor cores' operand type
+          }
+          tmem_st32(tl + scol + 32 * i, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (pos0 + kTile > kv_len && (x == 0 || t >= w.nx[0])) {
+          // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
+          const uint32_t j = 2 * (c + (t - w.k0)) + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(j % NS), (j / NS) & 1));
+          if (ok && pos0 + r >= kv_len) {
+            uint8_t* row = smem + Cfg::kOffRing + (j % NS) * Cfg::kSlot + r * 128;
+#pragma unroll
+            for (int h = 0; h < Cfg::kHalves; ++h)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(row + h * 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(pready(x));
+        if (!ok) break;
+      }
+      c += w.k1 - w.k0;
+      const bool any = kend > w.k0;
+      if (any) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1))) ok = false;
+        ++no;
+        tc_fence_after();
+      }
+      // a wait that ran out in one warp ends all four, which share the barriers below
+      if (!ok) failed[x] = 1;
+      named_bar(1 + x, 128);
+      if (failed[x]) {
+        ok = false;
+        break;
+      }
+      if (w.nx[x] == 0) continue;   // no such rows
+      const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;   // rows 0 .. rows - 1 exist
+      __nv_bfloat16* out0 = reinterpret_cast<__nv_bfloat16*>(q.out) +
+                            ((size_t(w.row0) + first_tok) * q.hq + size_t(w.g) * q.group) * D;
+      auto out_row = [&](int rr) {
+        const int tk = rr / q.group;
+        return out0 + (size_t(tk) * q.hq + (rr - tk * q.group)) * D;
+      };
+      const bool whole = w.k0 == 0 && w.k1 == w.nt;
+      if (whole) {
+        const float inv = 1.f / l;
+        __nv_bfloat16* o_row = out0 + (size_t(tok_r) * q.hq + head_r) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tmem_ld32(tl + ocol + 32 * i, o);
+          tmem_ld_wait();
+          if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(o_row)[4 * i + e] =
+                  make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                             pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                             pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                             pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          }
+        }
+        tc_fence_before();
+        continue;
+      }
+      // A partial item.  Slot 2 * CTA + 1 holds the piece that the CTA leaves
+      // unfinished, slot 2 * CTA the end of an item begun by an earlier CTA;
+      // O as [D / 4][128 rows] float4.
+      int first, last;
+      sharers(w, tc[0], (int)tc[1], first, last);
+      const int me = blockIdx.x;
+      auto slot_of = [&](int cta) { return (2 * cta + (cta == last ? 0 : 1)) * 2 + x; };
+      {
+        float4* po = reinterpret_cast<float4*>(q.part_o) + size_t(slot_of(me)) * (D / 4) * 128;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          if (any) {
+            tmem_ld32(tl + ocol + 32 * i, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              po[(8 * i + e) * 128 + r] =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+        if (r < rows)
+          reinterpret_cast<float2*>(q.part_ml)[size_t(slot_of(me)) * 128 + r] = make_float2(m, l);
+      }
+      __threadfence();
+      named_bar(1 + x, 128);
+      if (r == 0) flags[x] = atomicAdd(&q.tickets[2 * first + x], 1) == last - first;
+      named_bar(1 + x, 128);
+      if (flags[x]) {
+        __threadfence();
+        const float2* ml = reinterpret_cast<const float2*>(q.part_ml);
+        const float4* po = reinterpret_cast<const float4*>(q.part_o);
+        for (int e = r; e < rows * (D / 4); e += 128) {
+          const int d4 = e / rows, rr = e - d4 * rows;
+          float mm = kNoMax;
+          for (int cc = first; cc <= last; ++cc)
+            mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]).x);
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float lsum = 0.f;
+#pragma unroll 4
+          for (int cc = first; cc <= last; ++cc) {
+            const float2 v = __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]);
+            const float4 o = __ldcg(&po[(size_t(slot_of(cc)) * (D / 4) + d4) * 128 + rr]);
+            const float f = ex2(v.x - mm);
+            lsum += f * v.y;
+            acc.x += f * o.x;
+            acc.y += f * o.y;
+            acc.z += f * o.z;
+            acc.w += f * o.w;
+          }
+          const float inv = 1.f / lsum;
+          *reinterpret_cast<uint2*>(out_row(rr) + 4 * d4) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                         pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        if (r == 0) q.tickets[2 * first + x] = 0;
+      }
+      named_bar(1 + x, 128);   // flags[x] is rewritten by the next partial item
+    }
+    if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+static cudaError_t launch_prompt_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   const CUtensorMap& qmap, const PromptParams& p, int grid,
+                                   cudaStream_t stream) {
+  static std::atomic<uint32_t> configured{0};
+  cudaError_t e = once_per_device(configured, [] {
+    return cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)PCfg<D>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kPThreads, 1, 1);
+  cfg.dynamicSmemBytes = PCfg<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<D>, kmap, vmap, qmap, p);
+}
+
+cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          const CUtensorMap& qmap, const PromptParams& p, int head_dim, int grid,
+                          cudaStream_t stream) {
+  return head_dim == 64 ? launch_prompt_t<64>(kmap, vmap, qmap, p, grid, stream)
+                        : launch_prompt_t<128>(kmap, vmap, qmap, p, grid, stream);
+}
+
+}  // namespace vegas

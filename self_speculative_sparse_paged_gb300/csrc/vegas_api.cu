@@ -647,6 +647,270 @@ VEGAS_API vegas_status_t vegas_sparse_decode_attn(
 }
 
 // =========================================================================
+// Prompts: rotary positions with the cache append, attention over whole prompts
+// =========================================================================
+namespace {
+
+// Packed ragged rows as the prompt calls take them.
+vegas_status_t check_packed(const int32_t* row_start, const int32_t* ctx_lens, int total_rows,
+                            int batch) {
+  if (!row_start || !ctx_lens) return fail(VEGAS_ERR_INVALID_ARG, "NULL row_start or ctx_lens");
+  if (total_rows < 0 || batch < 0)
+    return fail(VEGAS_ERR_INVALID_ARG, "total_rows %d, batch %d", total_rows, batch);
+  if (total_rows >= (1 << 24))
+    return fail(VEGAS_ERR_UNSUPPORTED, "total_rows %d (must be < 2^24)", total_rows);
+  return VEGAS_OK;
+}
+
+vegas_status_t check_rows(const char* name, const void* p, int64_t stride, int heads, int d) {
+  if (!p) return fail(VEGAS_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(VEGAS_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < (int64_t)heads * d)
+    return fail(VEGAS_ERR_INVALID_ARG, "%s_stride %lld is less than a row's %d elements", name,
+                (long long)stride, heads * d);
+  if (stride % 8 != 0)
+    return fail(VEGAS_ERR_UNSUPPORTED, "%s_stride %lld must be a multiple of 8 elements", name,
+                (long long)stride);
+  if (stride >= (1ll << 32))
+    return fail(VEGAS_ERR_UNSUPPORTED, "%s_stride %lld must be < 2^32", name, (long long)stride);
+  return VEGAS_OK;
+}
+
+// Largest query group of the prompt kernel (a query tile holds whole tokens).
+constexpr int kMaxPromptGroup = 64;
+
+struct PromptPlan {
+  int tile_tokens, ctas;
+  size_t ml_off, o_off, bytes;
+};
+
+// At most one CTA per SM; fewer when the batch cannot hold that many shares of
+// the least useful size (two KV tiles).
+PromptPlan plan_prompt(const vegas_paged_kv_t* kv, int total_rows, int batch, int sms) {
+  PromptPlan pl{};
+  pl.tile_tokens = 128 / (kv->num_q_heads / kv->num_kv_heads);
+  const long long items =
+      (long long)kv->num_kv_heads * (total_rows / (2 * pl.tile_tokens) + (long long)batch);
+  const long long shares =
+      items * (((long long)kv->max_pages_per_seq * VEGAS_PAGE_SIZE + 256) / 256 + 1);
+  pl.ctas = (int)std::max(1ll, std::min((long long)sms, shares));
+  // (the tickets' room does not depend on the call: no call's partial states
+  // may come to lie where a larger call keeps its counters)
+  pl.ml_off = align256(size_t(sms) * 2 * sizeof(int));
+  pl.o_off = pl.ml_off + align256(size_t(pl.ctas) * 4 * 128 * 2 * sizeof(float));
+  pl.bytes = pl.o_off + size_t(pl.ctas) * 4 * 128 * kv->head_dim * sizeof(float);
+  return pl;
+}
+
+// 3-D view of packed query rows: (head_dim, Hq, rows); box 64 elements x one
+// KV head's query heads x a tile's tokens, 128-byte swizzle.
+vegas_status_t make_rows_map(CUtensorMap* map, const void* base, const vegas_paged_kv_t* kv,
+                             int64_t stride, int total_rows, int tile_tokens) {
+  EncodeTiledFn enc;
+  vegas_status_t st = get_encoder(&enc);
+  if (st != VEGAS_OK) return st;
+  cuuint64_t dims[3] = {(cuuint64_t)kv->head_dim, (cuuint64_t)kv->num_q_heads,
+                        (cuuint64_t)total_rows};
+  cuuint64_t strides[2] = {(cuuint64_t)kv->head_dim * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)(kv->num_q_heads / kv->num_kv_heads),
+                       (cuuint32_t)tile_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VEGAS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return VEGAS_OK;
+}
+
+}  // namespace
+
+VEGAS_API vegas_status_t vegas_rope_append(
+    const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
+    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
+    int batch, void* stream) {
+  vegas_status_t st = check_kv(kv);
+  if (st != VEGAS_OK) return st;
+  if ((st = check_packed(row_start, ctx_lens, total_rows, batch)) != VEGAS_OK) return st;
+  const int d = kv->head_dim;
+  if ((st = check_rows("q", q, q_stride, kv->num_q_heads, d)) != VEGAS_OK) return st;
+  if ((st = check_rows("k", k, k_stride, kv->num_kv_heads, d)) != VEGAS_OK) return st;
+  if ((st = check_rows("v", v, v_stride, kv->num_kv_heads, d)) != VEGAS_OK) return st;
+  if (!q_out || !aligned16(q_out))
+    return fail(VEGAS_ERR_INVALID_ARG, "q_out must be a 16-byte aligned pointer");
+  if (rot_dim < 0 || rot_dim > d)
+    return fail(VEGAS_ERR_INVALID_ARG, "rot_dim %d outside [0, %d]", rot_dim, d);
+  if (rot_dim % 16 != 0)
+    return fail(VEGAS_ERR_UNSUPPORTED, "rot_dim %d must be a multiple of 16", rot_dim);
+  if (rot_dim > 0 && !inv_freq) return fail(VEGAS_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (num_axes < 1) return fail(VEGAS_ERR_INVALID_ARG, "num_axes %d", num_axes);
+  if (positions && num_axes > 1 && !pair_axis)
+    return fail(VEGAS_ERR_INVALID_ARG, "pair_axis is NULL with %d axes", num_axes);
+  if (!std::isfinite(rope_scale)) return fail(VEGAS_ERR_INVALID_ARG, "rope_scale not finite");
+  if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
+  vegas::RopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = q_out;
+  p.k_cache = const_cast<void*>(kv->k_cache);
+  p.v_cache = const_cast<void*>(kv->v_cache);
+  p.block_table = kv->block_table;
+  p.row_start = row_start;
+  p.ctx_lens = ctx_lens;
+  p.positions = positions;
+  p.pair_axis = pair_axis;
+  p.inv_freq = inv_freq;
+  p.num_axes = num_axes;
+  p.rot = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.scale = rope_scale;
+  p.total_rows = total_rows;
+  p.batch = batch;
+  p.num_pages = kv->num_pages;
+  p.max_pages = kv->max_pages_per_seq;
+  p.hq = kv->num_q_heads;
+  p.hkv = kv->num_kv_heads;
+  p.head_dim = d;
+  p.err = err;
+  cudaError_t e = vegas::launch_rope_append(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope append launch");
+  return VEGAS_OK;
+}
+
+VEGAS_API size_t vegas_prompt_workspace_size(const vegas_paged_kv_t* kv, int total_rows,
+                                             int batch) {
+  if (check_kv(kv) != VEGAS_OK || total_rows < 0 || batch < 0) return 0;
+  if (kv->num_q_heads / kv->num_kv_heads > kMaxPromptGroup) return 0;
+  int sms = 0;
+  if (device_info(nullptr, &sms) != VEGAS_OK || sms < 1) sms = 148;
+  return plan_prompt(kv, total_rows, batch, sms).bytes;
+}
+
+VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const void* q,
+                                           int64_t q_stride, void* out, const int32_t* row_start,
+                                           const int32_t* ctx_lens, int total_rows, int batch,
+                                           float softmax_scale, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  vegas_status_t st = check_kv(kv);
+  if (st != VEGAS_OK) return st;
+  if ((st = check_packed(row_start, ctx_lens, total_rows, batch)) != VEGAS_OK) return st;
+  if ((st = check_rows("q", q, q_stride, kv->num_q_heads, kv->head_dim)) != VEGAS_OK) return st;
+  if (!out || !aligned16(out))
+    return fail(VEGAS_ERR_INVALID_ARG, "out must be a 16-byte aligned pointer");
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
+    return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale must be finite and positive");
+  const int G = kv->num_q_heads / kv->num_kv_heads;
+  if (G > kMaxPromptGroup)
+    return fail(VEGAS_ERR_UNSUPPORTED, "group size %d (at most %d)", G, kMaxPromptGroup);
+  if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  int sms = 0;
+  if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
+  const PromptPlan pl = plan_prompt(kv, total_rows, batch, sms);
+  if (!workspace || workspace_bytes < pl.bytes)
+    return fail(VEGAS_ERR_WORKSPACE_TOO_SMALL, "prompt workspace %zu < %zu bytes", workspace_bytes,
+                pl.bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(VEGAS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  CUtensorMap km, vm, qm;
+  if ((st = make_cache_map(&km, kv->k_cache, kv)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&vm, kv->v_cache, kv)) != VEGAS_OK) return st;
+  if ((st = make_rows_map(&qm, q, kv, q_stride, total_rows, pl.tile_tokens)) != VEGAS_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  vegas::PromptParams p{};
+  p.out = out;
+  p.block_table = kv->block_table;
+  p.row_start = row_start;
+  p.ctx_lens = ctx_lens;
+  p.total_rows = total_rows;
+  p.batch = batch;
+  p.num_pages = kv->num_pages;
+  p.max_pages = kv->max_pages_per_seq;
+  p.hq = kv->num_q_heads;
+  p.hkv = kv->num_kv_heads;
+  p.group = G;
+  p.tile_tokens = pl.tile_tokens;
+  p.pair_tokens = 2 * pl.tile_tokens;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.tickets = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pl.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + pl.o_off);
+  p.err = err;
+  cudaError_t e = vegas::launch_prompt(km, vm, qm, p, kv->head_dim, pl.ctas,
+                                       static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+  return VEGAS_OK;
+}
+
+// =========================================================================
+// Log probabilities of given tokens
+// =========================================================================
+VEGAS_API vegas_status_t vegas_token_logprobs(const void* logits, int dtype, int64_t row_stride,
+                                              const int32_t* tokens, int rows, int vocab,
+                                              float inv_temperature, float* logprob,
+                                              float* entropy, int32_t* rank, int top_n,
+                                              int32_t* top_ids, float* top_logprobs,
+                                              void* stream) {
+  if (dtype != VEGAS_DTYPE_BF16 && dtype != VEGAS_DTYPE_FP32)
+    return fail(VEGAS_ERR_UNSUPPORTED, "dtype %d (bf16 or fp32)", dtype);
+  if (!logits) return fail(VEGAS_ERR_INVALID_ARG, "logits is NULL");
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == VEGAS_DTYPE_BF16 ? 2 : 4))
+    return fail(VEGAS_ERR_INVALID_ARG, "logits are not aligned to their type");
+  if (rows < 0 || vocab < 1 || row_stride < vocab)
+    return fail(VEGAS_ERR_INVALID_ARG, "rows %d, vocab %d, row_stride %lld", rows, vocab,
+                (long long)row_stride);
+  if (rows > (1 << 26) || vocab > (1 << 28))
+    return fail(VEGAS_ERR_UNSUPPORTED, "rows %d (at most 2^26), vocab %d (at most 2^28)", rows,
+                vocab);
+  if (!std::isfinite(inv_temperature) || !(inv_temperature > 0.f))
+    return fail(VEGAS_ERR_INVALID_ARG, "inv_temperature must be finite and positive");
+  if ((logprob || rank) && !tokens)
+    return fail(VEGAS_ERR_INVALID_ARG, "logprob and rank need tokens");
+  if (top_n < 0 || top_n > vegas::kMaxTopLogprobs)
+    return fail(VEGAS_ERR_UNSUPPORTED, "top_n %d (0..%d)", top_n, vegas::kMaxTopLogprobs);
+  if (top_n > 0 && (!top_ids || !top_logprobs))
+    return fail(VEGAS_ERR_INVALID_ARG, "NULL top_ids or top_logprobs");
+  if (!logprob && !entropy && !rank && top_n == 0)
+    return fail(VEGAS_ERR_INVALID_ARG, "no output asked for");
+  if (rows == 0) return VEGAS_OK;
+  int* err = nullptr;
+  int sms = 0;
+  vegas_status_t st = device_info(&err, &sms);
+  if (st != VEGAS_OK) return st;
+  vegas::LogprobParams p{};
+  p.logits = logits;
+  p.tokens = tokens;
+  p.row_stride = row_stride;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.inv_temperature = inv_temperature;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.rank = rank;
+  p.top_n = top_n;
+  p.top_ids = top_ids;
+  p.top_logprobs = top_logprobs;
+  // CTAs per row: spread few rows until the SMs hold two CTAs each, with 4096
+  // logits or more a CTA.
+  p.cluster = 1;
+  while (p.cluster < vegas::kMaxLogprobCluster && (long long)rows * p.cluster * 2 <= 2ll * sms &&
+         vocab / (2 * p.cluster) >= 4096)
+    p.cluster *= 2;
+  p.err = err;
+  cudaError_t e = vegas::launch_token_logprobs(p, dtype == VEGAS_DTYPE_BF16,
+                                               static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "token logprobs launch");
+  return VEGAS_OK;
+}
+
+// =========================================================================
 // Synthetic input generator
 // =========================================================================
 VEGAS_API vegas_status_t vegas_synth_paged_kv(void* cache, int which, uint64_t seed, int layer,
