@@ -20,7 +20,8 @@
 // logit exceeds it by 2^8, so O is touched about once per item.
 //
 // Warps 0-3: softmax of A; 4-7: softmax of B; 8, 9: TMA of K and V tiles into
-// one ring; 10: MMA issue; 11: Q tiles.
+// one ring; 10: MMA issue; 11: walks the CTA's items, publishes them in a small
+// shared ring and loads the Q tiles.
 //
 // Work division: items carry the cost c0 + (positions up to the item's last
 // row), whose prefix sums have a closed form, and CTA i of N takes the i-th of
@@ -43,6 +44,16 @@ constexpr int kMinShare = 256;        // a CTA's least share of the cost, in pos
 constexpr float kNoMax = -1e30f;      // reference maximum of a row that has seen nothing
 constexpr float kSlack = 8.f;         // log2 units a logit may exceed the reference by
 
+// An item, or the part of it in one CTA's range, as published to all warps.
+struct Piece {
+  int seq, g, tok0;    // tok0: first token of tile A in its sequence; seq < 0: no more
+  int row0, n, ctx;
+  int k0, k1;          // KV tiles of this piece
+  int na, nb;          // KV tiles that query tiles A and B need
+  int first, last;     // CTAs that share the item
+};
+constexpr int kPieces = 4;   // depth of the ring of published items
+
 template <int D>
 struct PCfg {
   static constexpr int kHalves = D / 64;
@@ -51,9 +62,10 @@ struct PCfg {
   static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 1;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + 2 + 2 + 1 + 2 * kPieces;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr size_t kSmem = kOffMisc + 128 + 1024;
+  static constexpr int kOffPieces = kOffMisc + 112;
+  static constexpr size_t kSmem = kOffPieces + kPieces * sizeof(Piece) + 1024;
   static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
 };
 
@@ -69,13 +81,6 @@ struct Seq {
   long long per_head;  // summed cost of one head's items
 };
 
-struct Piece {
-  int seq, g, p;
-  int row0, n, ctx;
-  int k0, k1, nt;      // KV tiles of this piece, and of the whole item
-  int nx[2];           // KV tiles query tile A / B needs
-  long long us;
-};
 
 __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
   Seq r;
@@ -186,7 +191,7 @@ __device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
   return r;
 }
 
-// Walks the items of a CTA's range; every warp walks by itself.
+// Walks the items of a CTA's range.
 struct Walk {
   Point at, end;
   Seq s;
@@ -194,7 +199,7 @@ struct Walk {
 
   __device__ __forceinline__ Walk(const Point& a, const Point& e) : at(a), end(e), have(false) {}
 
-  __device__ __forceinline__ bool next(const PromptParams& q, Piece& w) {
+  __device__ __forceinline__ bool next(const PromptParams& q, long long total, int ncta, Piece& w) {
     while (true) {
       if (at.seq >= q.batch || at.seq > end.seq) return false;
       if (!have) {
@@ -206,21 +211,29 @@ struct Walk {
         have = false;
         continue;
       }
-      const bool last = at.seq == end.seq && at.g == end.g && at.p == end.p;
-      if (last && end.k <= at.k) return false;
+      const bool stop = at.seq == end.seq && at.g == end.g && at.p == end.p;
+      if (stop && end.k <= at.k) return false;
       w.seq = at.seq;
       w.g = at.g;
-      w.p = at.p;
+      w.tok0 = at.p * q.pair_tokens;
       w.row0 = s.row0;
       w.n = s.n;
       w.ctx = s.ctx;
-      w.nx[0] = tiles_of(q, s, at.p, 0);
-      w.nx[1] = tiles_of(q, s, at.p, 1);
-      w.nt = max(w.nx[0], w.nx[1]);
+      w.na = tiles_of(q, s, at.p, 0);
+      w.nb = tiles_of(q, s, at.p, 1);
+      const int nt = max(w.na, w.nb);
       w.k0 = at.k;
-      w.k1 = last ? end.k : w.nt;
-      w.us = at.us;
-      if (last) {
+      w.k1 = stop ? end.k : nt;
+      w.first = w.last = blockIdx.x;
+      if (w.k0 > 0 || w.k1 < nt) {
+        // Boundary i sits at floor(i * total / ncta), which is >= x exactly when
+        // i >= ceil(x * ncta / total); those in [a, b) fall inside the item (locate()).
+        const long long a = at.us + kItemCost + 2 * kTile - kTile / 2;
+        const long long b = at.us + kItemCost + (long long)kTile * nt - 2 * kTile + kTile / 2;
+        w.first = (int)((a * ncta + total - 1) / total) - 1;
+        w.last = (int)((b * ncta + total - 1) / total) - 1;
+      }
+      if (stop) {
         at.seq = q.batch;   // done
       } else {
         at.us += s.ctx + kItemCost + (long long)q.pair_tokens * (at.p + 1);
@@ -238,16 +251,6 @@ struct Walk {
     }
   }
 };
-
-// CTAs whose ranges meet the item that costs [us, ...) and has nt tiles.
-__device__ __forceinline__ void sharers(const Piece& w, long long total, int ncta, int& first,
-                                        int& last) {
-  const long long a = w.us + kItemCost + 2 * kTile - kTile / 2;
-  const long long b = w.us + kItemCost + (long long)kTile * w.nt - 2 * kTile + kTile / 2;
-  // boundary i sits at floor(i * total / ncta) >= x exactly when i >= ceil(x * ncta / total)
-  first = (int)((a * ncta + total - 1) / total) - 1;
-  last = (int)((b * ncta + total - 1) / total) - 1;
-}
 
 }  // namespace
 
@@ -267,14 +270,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto full = [&](uint32_t s) { return bar0 + 8 * s; };
   auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
-  auto pready = [&](int x) { return bar0 + 8 * (2 * NS + 2 + x); };
-  auto odone = [&](int x) { return bar0 + 8 * (2 * NS + 4 + x); };
-  const uint32_t qfull = bar0 + 8 * (2 * NS + 6), qfree = bar0 + 8 * (2 * NS + 7);
-  const uint32_t drain = bar0 + 8 * (2 * NS + 8);
+  auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + 2 * x + h); };
+  auto odone = [&](int x) { return bar0 + 8 * (2 * NS + 6 + x); };
+  const uint32_t qfull = bar0 + 8 * (2 * NS + 8), qfree = bar0 + 8 * (2 * NS + 9);
+  const uint32_t drain = bar0 + 8 * (2 * NS + 10);
+  auto pcfull = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + i); };
+  auto pcfree = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6], cost, CTAs
   int* failed = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 96);        // [2]
+  Piece* pieces = reinterpret_cast<Piece*>(smem + Cfg::kOffPieces);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -285,12 +291,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(sfull(x), 1);
-      mbar_init(pready(x), 128);
+      mbar_init(pready(x, 0), 128);
+      mbar_init(pready(x, 1), 128);
       mbar_init(odone(x), 1);
     }
     mbar_init(qfull, 1);
     mbar_init(qfree, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(pcfull(i), 1);
+      mbar_init(pcfree(i), 11);   // one arrival per reading warp
+    }
     fence_mbar_init();
   }
   if (warp == 10) {
@@ -331,21 +342,26 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto point = [&](int w) {
-    const int* e = ends + 6 * w;
-    Point r;
-    r.seq = e[0];
-    r.g = e[1];
-    r.p = e[2];
-    r.k = e[3];
-    r.us = ((long long)e[5] << 32) | (uint32_t)e[4];
-    return r;
+  uint32_t pc = 0;   // items read so far
+  // The next published item (whole warp); false when there is none.
+  auto next_piece = [&](Piece& w, bool& ok) {
+    const uint32_t i = pc % kPieces;
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(pcfull(i), (pc / kPieces) & 1))) {
+      ok = false;
+      return false;
+    }
+    w = pieces[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pcfree(i));
+    ++pc;
+    return w.seq >= 0;
   };
-  Walk walk(point(0), point(1));
   Piece w;
   bool ok = true;
-
+  // 384 threads launch with 168 registers each: 2 x 128 x 208 + 128 x 80 fit in that.
+  // (Set inside each role's branch: where the branches join the smaller count would rule.)
   if (warp == 8 || warp == 9) {
+    leave_registers<80>();
     // ------------------------------------------------------------ K (8) and V (9) tiles
     // Lane j < 8 * D/64 issues box (page j % 8, half j / 8): 16 positions x 64 dims.
     const bool is_v = warp == 9;
@@ -353,7 +369,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int page = lane & 7, half = lane >> 3;
     uint32_t c = 0;       // tiles so far
     uint32_t issued = 0;  // of them, issued
-    while (ok && walk.next(q, w)) {
+    while (ok && next_piece(w, ok)) {
       const int32_t* row = q.block_table + size_t(w.seq) * q.max_pages;
       const int npages = (w.ctx + w.n + 15) / 16;
       int phys = __ldg(&row[min(8 * w.k0 + page, npages - 1)]);
@@ -389,21 +405,50 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   } else if (warp == 11) {
-    // ------------------------------------------------------------ Q tiles
+    leave_registers<80>();
+    // ------------------------------------------------------------ items, Q tiles
+    auto point = [&](int e0) {
+      const int* e = ends + 6 * e0;
+      Point r;
+      r.seq = e[0];
+      r.g = e[1];
+      r.p = e[2];
+      r.k = e[3];
+      r.us = ((long long)e[5] << 32) | (uint32_t)e[4];
+      return r;
+    };
+    Walk walk(point(0), point(1));
+    const long long* tc = reinterpret_cast<const long long*>(ends + 12);
+    const long long total = tc[0];
+    const int ncta = (int)tc[1];
     uint32_t c = 0;
-    while (ok && walk.next(q, w)) {
+    while (ok) {
+      const bool more = walk.next(q, total, ncta, w);
+      if (!more) w.seq = -1;
+      const uint32_t i = c % kPieces;
+      if (c >= kPieces &&
+          !__all_sync(0xffffffffu, mbar_wait_bounded(pcfree(i), (c / kPieces - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        pieces[i] = w;
+        mbar_arrive(pcfull(i));
+      }
+      __syncwarp();
+      if (!more) break;
       if (c > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree, (c - 1) & 1))) {
         ok = false;
         break;
       }
-      const int tiles = w.nx[1] > 0 ? 2 : 1;
+      const int tiles = w.nb > 0 ? 2 : 1;
       const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
       if (lane == 0) {
         mbar_arrive_expect_tx(qfull, bytes * tiles * Cfg::kHalves);
         for (int x = 0; x < tiles; ++x)
           for (int h = 0; h < Cfg::kHalves; ++h)
             tma_load_3d(sbase + x * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
-                        w.row0 + w.p * q.pair_tokens + x * q.tile_tokens, qfull);
+                        w.row0 + w.tok0 + x * q.tile_tokens, qfull);
       }
       __syncwarp();
       ++c;
@@ -411,6 +456,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (c > 0) (void)mbar_wait_bounded(qfull, (c - 1) & 1);   // landed before the CTA ends
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   } else if (warp == 10) {
+    leave_registers<80>();
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
@@ -434,13 +480,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int x, uint32_t jv, bool accumulate) {
+    auto issue_pv = [&](int x, int h, uint32_t jv, bool accumulate) {
       const uint32_t b = slot16(jv);
       if (leader) {
 #pragma unroll
-        for (int kp = 0; kp < 8; ++kp)
-          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + 8 * kp, with_addr(dVmn, b + kp * 128),
-                    idPV, accumulate || kp > 0);
+        for (int kp = 0; kp < 4; ++kp)
+          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + 32 * h + 8 * kp,
+                    with_addr(dVmn, b + (4 * h + kp) * 128), idPV, accumulate || h > 0 || kp > 0);
       }
       __syncwarp();
     };
@@ -448,17 +494,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (leader) tc_commit(bar);
       __syncwarp();
     };
-    uint32_t c = 0, pieces = 0;
-    uint32_t np[2] = {0, 0};   // P tiles consumed of A, B
-    while (ok && walk.next(q, w)) {
-      const int ex[2] = {min(w.k1, w.nx[0]), min(w.k1, w.nx[1])};
-      if (!wait_all(qfull, pieces & 1) || !wait_slot(2 * c)) {
+    uint32_t c = 0, items = 0;
+    uint32_t npa = 0, npb = 0;   // P tiles consumed of A, B
+    while (ok && next_piece(w, ok)) {
+      const int ea = min(w.k1, w.na), eb = min(w.k1, w.nb);
+      if (!wait_all(qfull, items & 1) || !wait_slot(2 * c)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      for (int x = 0; x < 2; ++x)
-        if (w.k0 < ex[x]) issue_s(x, 2 * c);
+      if (w.k0 < ea) issue_s(0, 2 * c);
+      if (w.k0 < eb) issue_s(1, 2 * c);
       commit(freed((2 * c) % NS));
       if (w.k0 + 1 == w.k1) commit(qfree);
       for (int t = w.k0; t < w.k1 && ok; ++t, ++c) {
@@ -469,18 +515,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
           break;
         }
         bool have_k = false;
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (t >= ex[x]) continue;
-          if (!wait_all(pready(x), np[x] & 1)) {
-            ok = false;
-            break;
+          const int ex = x ? eb : ea;
+          if (t >= ex) continue;
+          for (int h = 0; h < 2; ++h) {   // positions 0-63 go ahead of 64-127
+            if (!wait_all(pready(x, h), (x ? npb : npa) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(x, h, jv, t > w.k0);
           }
-          ++np[x];
-          tc_fence_after();
-          issue_pv(x, jv, t > w.k0);
-          if (t + 1 == ex[x]) commit(odone(x));
-          if (x == 1 || t >= ex[1]) commit(freed(jv % NS));
-          if (t + 1 < ex[x]) {
+          if (!ok) break;
+          x ? ++npb : ++npa;
+          if (t + 1 == ex) commit(odone(x));
+          if (x == 1 || t >= eb) commit(freed(jv % NS));
+          if (t + 1 < ex) {
             if (!have_k && !wait_slot(jk)) {
               ok = false;
               break;
@@ -495,7 +546,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (t + 2 == w.k1) commit(qfree);
         }
       }
-      ++pieces;
+      ++items;
     }
     if (!ok && leader) set_error(q.err, kErrDeviceTimeout);
     // every MMA issued has completed before tensor memory is released
@@ -503,6 +554,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncwarp();
     (void)mbar_wait_bounded(drain, 0);
   } else {
+    take_registers<208>();
     // ------------------------------------------------------------ softmax of tile X
     const int x = warp >> 2;
     const int r = tid & 127;
@@ -510,11 +562,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
     const int tok_r = r / q.group;
     const int head_r = r - tok_r * q.group;
-    const long long* tc = reinterpret_cast<const long long*>(ends + 12);
     uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
-    while (ok && walk.next(q, w)) {
-      const int first_tok = w.p * q.pair_tokens + x * q.tile_tokens;
-      const int kend = min(w.k1, w.nx[x]);
+    while (ok && next_piece(w, ok)) {
+      const int first_tok = w.tok0 + x * q.tile_tokens;
+      const int kend = min(w.k1, (x ? w.nb : w.na));
       const int kv_len = w.ctx + w.n;
       // the last position this row may see (rows behind the sequence: its last)
       const int lim = w.ctx + min(first_tok + tok_r, w.n - 1);
@@ -550,32 +601,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (t > w.k0) {
             // the row's earlier P . V products are complete: S of this tile was issued after them
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              float o[32];
-              tmem_ld32(tl + ocol + 32 * i, o);
+            for (int i = 0; i < D / 16; ++i) {
+              float o[16];
+              tmem_ld16(tl + ocol + 16 * i, o);
               tmem_ld_wait();
-              uint32_t ob[32];
+              uint32_t ob[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * f);
-              tmem_st32(tl + ocol + 32 * i, ob);
+              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
+              tmem_st16(tl + ocol + 16 * i, ob);
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float a = ex2(fmaf(s[64 * i + 2 * e], q.scale_log2, -m));
-            const float b = ex2(fmaf(s[64 * i + 2 * e + 1], q.scale_log2, -m));
-            sum[e & 3] += a + b;
-            pk[e] = pack_bf16x2(a, b);   // P to 8 bits of mantissa: the tensor cores' operand type
-          }
-          tmem_st32(tl + scol + 32 * i, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (pos0 + kTile > kv_len && (x == 0 || t >= w.nx[0])) {
+        if (pos0 + kTile > kv_len && (x == 0 || t >= w.na)) {
           // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
           const uint32_t j = 2 * (c + (t - w.k0)) + 1;
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(j % NS), (j / NS) & 1));
@@ -589,9 +626,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(pready(x));
+        const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2), nm2 = pair_f32(-m, -m);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            unpair_f32(fma_f32x2(pair_f32(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, nm2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
+            pk[e] = pack_bf16x2(a, b);   // P to 8 bits of mantissa: the tensor cores' operand type
+          }
+          tmem_st16(tl + scol + 16 * i, pk);
+          if (i & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(pready(x, i >> 1));
+          }
+        }
+        float la, lb;
+        unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
+        l += la + lb;
         if (!ok) break;
       }
       c += w.k1 - w.k0;
@@ -608,7 +666,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ok = false;
         break;
       }
-      if (w.nx[x] == 0) continue;   // no such rows
+      if ((x ? w.nb : w.na) == 0) continue;   // no such rows
       const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;   // rows 0 .. rows - 1 exist
       __nv_bfloat16* out0 = reinterpret_cast<__nv_bfloat16*>(q.out) +
                             ((size_t(w.row0) + first_tok) * q.hq + size_t(w.g) * q.group) * D;
@@ -616,8 +674,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int tk = rr / q.group;
         return out0 + (size_t(tk) * q.hq + (rr - tk * q.group)) * D;
       };
-      const bool whole = w.k0 == 0 && w.k1 == w.nt;
-      if (whole) {
+      if (w.first == w.last) {
         const float inv = 1.f / l;
         __nv_bfloat16* o_row = out0 + (size_t(tok_r) * q.hq + head_r) * D;
 #pragma unroll
@@ -641,9 +698,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // A partial item.  Slot 2 * CTA + 1 holds the piece that the CTA leaves
       // unfinished, slot 2 * CTA the end of an item begun by an earlier CTA;
       // O as [D / 4][128 rows] float4.
-      int first, last;
-      sharers(w, tc[0], (int)tc[1], first, last);
-      const int me = blockIdx.x;
+      const int first = w.first, last = w.last, me = blockIdx.x;
       auto slot_of = [&](int cta) { return (2 * cta + (cta == last ? 0 : 1)) * 2 + x; };
       {
         float4* po = reinterpret_cast<float4*>(q.part_o) + size_t(slot_of(me)) * (D / 4) * 128;
