@@ -15,9 +15,13 @@
 //   O_X[128 x D]  += P_X . V        (P_X in tensor memory, V MN-major)
 // with S_A, S_B, O_A, O_B in tensor memory; P_X (bf16) overwrites the first 64
 // columns of S_X.  The softmax is the running one: thread r of X's warpgroup
-// owns row r (tensor-memory lane r), keeps the row's reference maximum m and
-// sum l in registers, and raises m (rescaling l and its O row) only when a
-// logit exceeds it by 2^8, so O is touched about once per item.
+// owns row r (tensor-memory lane r) and keeps the row's reference m and sum l
+// in registers.  m is the row's maximum over the item's first tile; any other
+// reference gives the same quotient, so later tiles take p = 2^(x - m) without
+// looking for their maximum and only check the sum of each half tile: past
+// 2^20 (or where nothing had been seen) m is raised to the half's maximum, l
+// and the row of O are rescaled, and the half is taken again.  bf16 and fp32
+// hold numbers of that size as exactly as smaller ones.
 //
 // Warps 0-3: softmax of A; 4-7: softmax of B; 8, 9: TMA of K and V tiles into
 // one ring; 10: MMA issue; 11: walks the CTA's items, publishes them in a small
@@ -41,8 +45,8 @@ constexpr int kPThreads = 384;
 constexpr int kTile = 128;            // KV positions per tile, query rows per tile
 constexpr int kItemCost = 256;        // an item's fixed cost, in positions
 constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
-constexpr float kNoMax = -1e30f;      // reference maximum of a row that has seen nothing
-constexpr float kSlack = 8.f;         // log2 units a logit may exceed the reference by
+constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
+constexpr float kSumLimit = 1048576.f;   // a half tile's sum that makes a row raise its reference
 
 // An item, or the part of it in one CTA's range, as published to all warps.
 struct Piece {
@@ -62,7 +66,7 @@ struct PCfg {
   static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + 2 + 2 + 1 + 2 * kPieces;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + 2 + 2 + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
   static constexpr size_t kSmem = kOffPieces + kPieces * sizeof(Piece) + 1024;
@@ -274,6 +278,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto odone = [&](int x) { return bar0 + 8 * (2 * NS + 6 + x); };
   const uint32_t qfull = bar0 + 8 * (2 * NS + 8), qfree = bar0 + 8 * (2 * NS + 9);
   const uint32_t drain = bar0 + 8 * (2 * NS + 10);
+  auto pvhalf = [&](int x) { return bar0 + 8 * (2 * NS + 11 + 2 * kPieces + x); };
   auto pcfull = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + i); };
   auto pcfree = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
@@ -294,6 +299,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(pready(x, 0), 128);
       mbar_init(pready(x, 1), 128);
       mbar_init(odone(x), 1);
+      mbar_init(pvhalf(x), 1);
     }
     mbar_init(qfull, 1);
     mbar_init(qfree, 1);
@@ -526,6 +532,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             tc_fence_after();
             issue_pv(x, h, jv, t > w.k0);
+            if (h == 0) commit(pvhalf(x));
           }
           if (!ok) break;
           x ? ++npb : ++npa;
@@ -569,6 +576,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int kv_len = w.ctx + w.n;
       // the last position this row may see (rows behind the sequence: its last)
       const int lim = w.ctx + min(first_tok + tok_r, w.n - 1);
+      const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;   // rows 0 .. rows - 1 exist
+      const bool live = r < rows;
       float m = kNoMax, l = 0.f;
       for (int t = w.k0; t < kend; ++t) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(sfull(x), ns & 1))) {
@@ -589,28 +598,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int i = 0; i < 128; ++i)
             if (i > cut) s[i] = -INFINITY;
         }
-        float mx = s[0];
+        if (t == w.k0) {
+          float mx = s[0];
 #pragma unroll
-        for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
-        mx *= q.scale_log2;
-        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
-          const float m2 = fmaxf(m, mx);
-          const float f = ex2(m - m2);
-          m = m2;
-          l *= f;
-          if (t > w.k0) {
-            // the row's earlier P . V products are complete: S of this tile was issued after them
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              float o[16];
-              tmem_ld16(tl + ocol + 16 * i, o);
-              tmem_ld_wait();
-              uint32_t ob[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
-              tmem_st16(tl + ocol + 16 * i, ob);
-            }
-          }
+          for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
+          m = fmaxf(mx * q.scale_log2, kNoMax);
         }
         if (pos0 + kTile > kv_len && (x == 0 || t >= w.na)) {
           // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
@@ -626,30 +618,63 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2), nm2 = pair_f32(-m, -m);
-        uint64_t sum[2] = {0ull, 0ull};
+        const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];   // P to 8 bits of mantissa: the tensor cores' operand type
+          float hs;
+          auto take = [&]() {
+            const uint64_t nm2 = pair_f32(-m, -m);
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a, b;
-            unpair_f32(fma_f32x2(pair_f32(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, nm2), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
-            pk[e] = pack_bf16x2(a, b);   // P to 8 bits of mantissa: the tensor cores' operand type
+            for (int e = 0; e < 32; ++e) {
+              float a, b;
+              unpair_f32(fma_f32x2(pair_f32(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), sc2, nm2), a,
+                         b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
+              pk[e] = pack_bf16x2(a, b);
+            }
+            float la, lb;
+            unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
+            hs = la + lb;
+          };
+          take();
+          if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
+            float mx = s[64 * h];
+#pragma unroll
+            for (int i = 1; i < 64; ++i) mx = fmaxf(mx, s[64 * h + i]);
+            const float m2 = fmaxf(m, mx * q.scale_log2);
+            const float f = ex2(m - m2);
+            m = m2;
+            l *= f;
+            // O holds the row's earlier tiles (S of this one was issued after their
+            // products), and in the second half this tile's first one
+            if (h == 1)
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvhalf(x), (ns - 1) & 1)) && ok;
+            tc_fence_after();
+            if (t > w.k0 || h == 1) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                float o[16];
+                tmem_ld16(tl + ocol + 16 * i, o);
+                tmem_ld_wait();
+                uint32_t ob[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
+                tmem_st16(tl + ocol + 16 * i, ob);
+              }
+            }
+            take();
           }
-          tmem_st16(tl + scol + 16 * i, pk);
-          if (i & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(pready(x, i >> 1));
-          }
+          l += hs;
+          tmem_st16(tl + scol + 32 * h, pk);
+          tmem_st16(tl + scol + 32 * h + 16, pk + 16);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(pready(x, h));
         }
-        float la, lb;
-        unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
-        l += la + lb;
         if (!ok) break;
       }
       c += w.k1 - w.k0;
@@ -667,7 +692,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         break;
       }
       if ((x ? w.nb : w.na) == 0) continue;   // no such rows
-      const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;   // rows 0 .. rows - 1 exist
       __nv_bfloat16* out0 = reinterpret_cast<__nv_bfloat16*>(q.out) +
                             ((size_t(w.row0) + first_tok) * q.hq + size_t(w.g) * q.group) * D;
       auto out_row = [&](int rr) {
@@ -682,7 +706,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           float o[32];
           tmem_ld32(tl + ocol + 32 * i, o);
           tmem_ld_wait();
-          if (r < rows) {
+          if (live) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               reinterpret_cast<uint4*>(o_row)[4 * i + e] =
@@ -712,7 +736,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
-          if (r < rows) {
+          if (live) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               po[(8 * i + e) * 128 + r] =
@@ -720,7 +744,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
         tc_fence_before();
-        if (r < rows)
+        if (live)
           reinterpret_cast<float2*>(q.part_ml)[size_t(slot_of(me)) * 128 + r] = make_float2(m, l);
       }
       __threadfence();
@@ -731,28 +755,43 @@ __global__ void __launch_bounds__(kPThreads, 1)
         __threadfence();
         const float2* ml = reinterpret_cast<const float2*>(q.part_ml);
         const float4* po = reinterpret_cast<const float4*>(q.part_o);
-        for (int e = r; e < rows * (D / 4); e += 128) {
-          const int d4 = e / rows, rr = e - d4 * rows;
+        // thread r: row r % rows, every sub-th float4 of it, eight in flight at a time
+        const int subs = 128 / rows, rr = r % rows, sub = r / rows;
+        if (sub < subs) {
           float mm = kNoMax;
           for (int cc = first; cc <= last; ++cc)
             mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]).x);
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float lsum = 0.f;
-#pragma unroll 4
-          for (int cc = first; cc <= last; ++cc) {
-            const float2 v = __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]);
-            const float4 o = __ldcg(&po[(size_t(slot_of(cc)) * (D / 4) + d4) * 128 + rr]);
-            const float f = ex2(v.x - mm);
-            lsum += f * v.y;
-            acc.x += f * o.x;
-            acc.y += f * o.y;
-            acc.z += f * o.z;
-            acc.w += f * o.w;
+          __nv_bfloat16* o_row = out_row(rr);
+          for (int d0 = sub; d0 < D / 4; d0 += 8 * subs) {
+            float4 acc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            float lsum = 0.f;
+            for (int cc = first; cc <= last; ++cc) {
+              const float2 v = __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]);
+              const float4* src = po + size_t(slot_of(cc)) * (D / 4) * 128 + rr;
+              float4 o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                o[i] = __ldcg(&src[min(d0 + i * subs, D / 4 - 1) * 128]);
+              const float f = ex2(v.x - mm);
+              lsum += f * v.y;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[i].x += f * o[i].x;
+                acc[i].y += f * o[i].y;
+                acc[i].z += f * o[i].z;
+                acc[i].w += f * o[i].w;
+              }
+            }
+            const float inv = 1.f / lsum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (d0 + i * subs < D / 4)
+                *reinterpret_cast<uint2*>(o_row + 4 * (d0 + i * subs)) =
+                    make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
+                               pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
           }
-          const float inv = 1.f / lsum;
-          *reinterpret_cast<uint2*>(out_row(rr) + 4 * d4) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                         pack_bf16x2(acc.z * inv, acc.w * inv));
         }
         if (r == 0) q.tickets[2 * first + x] = 0;
       }
