@@ -27,13 +27,14 @@
 // one ring; 10: MMA issue; 11: walks the CTA's items, publishes them in a small
 // shared ring and loads the Q tiles.
 //
-// Work division: items carry the cost c0 + (positions up to the item's last
-// row), whose prefix sums have a closed form, and CTA i of N takes the i-th of
-// N equal ranges of the summed cost.  A range may begin and end inside an
-// item; such an item's partial (m, l, O) go through the workspace and the
-// CTA that arrives last joins them in range order.  So a single decode row
-// with a long cache spreads over all SMs, and a large batch keeps every SM
-// busy to the end, with no plan kernel and at most two partial items a CTA.
+// Work division, found by every CTA from the lengths alone (no plan kernel):
+// with enough items they are dealt out whole, longest first and back and forth
+// over the CTAs.  Otherwise items carry the cost c0 + (positions up to the
+// item's last row), whose prefix sums have a closed form, and CTA i of N takes
+// the i-th of N equal ranges of the summed cost.  A range may begin and end
+// inside an item; such an item's partial (m, l, O) go through the workspace and
+// the CTA that arrives last joins them in range order.  So a single decode row
+// with a long cache spreads over all SMs, with at most two partial items a CTA.
 #include "kernels.h"
 #include "vegas_common.cuh"
 
@@ -45,6 +46,7 @@ constexpr int kPThreads = 384;
 constexpr int kTile = 128;            // KV positions per tile, query rows per tile
 constexpr int kItemCost = 256;        // an item's fixed cost, in positions
 constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
+constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
 constexpr float kSumLimit = 1048576.f;   // a half tile's sum that makes a row raise its reference
 
@@ -116,13 +118,81 @@ __device__ __forceinline__ int tiles_of(const PromptParams& q, const Seq& s, int
   return (s.ctx + last) / kTile + 1;
 }
 
-// Sum over all sequences (whole warp).
-__device__ __forceinline__ long long total_cost(const PromptParams& q) {
+// What the division of the work goes by, the same in every CTA.
+struct Division {
+  long long total;     // summed cost of all items
+  int items;
+  int ncta;            // CTAs that take part
+  int whole;           // 1: items are dealt out whole, longest first; 0: equal ranges of the cost
+};
+
+// Items by falling cost: positions up to the item's last row, as ctx + (p + 1) * pair_tokens.
+// With at most 32 sequences each lane holds one, and an item's rank is found by bisection.
+__device__ __forceinline__ int items_from(const PromptParams& q, const Seq& s, int cost) {
+  // items of this lane's sequence whose cost is at least `cost`
+  const int above = cost - s.ctx;   // (p + 1) * pair_tokens >= above
+  const int skip = above <= 0 ? 0 : (above + q.pair_tokens - 1) / q.pair_tokens - 1;
+  return max(0, s.pairs - max(skip, 0)) * q.hkv;
+}
+
+// The item of rank k (whole warp; sq: lane's sequence; hi: an upper bound of its cost, lowered to it).
+__device__ __forceinline__ void ranked(const PromptParams& q, const Seq& sq, int k, int& hi, int& seq,
+                                       int& g, int& p) {
+  int lo = 0;                       // the largest cost c with more than k items of cost >= c
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (__reduce_add_sync(0xffffffffu, items_from(q, sq, mid)) > k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int before = __reduce_add_sync(0xffffffffu, items_from(q, sq, lo + 1));
+  // at this cost each sequence has one item a head, or none
+  const bool one = items_from(q, sq, lo) > items_from(q, sq, lo + 1);
+  const unsigned who = __ballot_sync(0xffffffffu, one);
+  const int nth = (k - before) / q.hkv;
+  g = (k - before) - nth * q.hkv;
+  seq = __fns(who, 0, nth + 1);
+  const int mine = (lo - sq.ctx) / q.pair_tokens - 1;
+  p = __shfl_sync(0xffffffffu, mine, seq & 31);
+}
+
+// Whole items keep every CTA busy when there are enough of them: the makespan is then about the
+// mean plus the part of the last round's items that not every CTA gets, and at least the longest
+// item.  Splitting costs a CTA the partial states it writes and joins (kSplitCost).
+__device__ __forceinline__ Division divide(const PromptParams& q) {
+  const int lane = threadIdx.x & 31;
   long long w = 0;
-  for (int s = threadIdx.x & 31; s < q.batch; s += 32) w += load_seq(q, s).per_head;
+  int items = 0, longest = 0;
+  Seq sq{};
+  for (int s = lane; s < q.batch; s += 32) {
+    sq = load_seq(q, s);
+    w += sq.per_head;
+    items += sq.pairs;
+    if (sq.n > 0) longest = max(longest, sq.ctx + sq.n);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-  return w * q.hkv;
+  Division d;
+  d.total = w * q.hkv;
+  d.items = __reduce_add_sync(0xffffffffu, items) * q.hkv;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  const int grid = gridDim.x;
+  d.ncta = (int)min((long long)grid, max(1ll, d.total / kMinShare));
+  d.whole = 0;
+  const long long limit = d.total / d.ncta + kSplitCost;
+  if (q.batch <= 32 && longest + kItemCost <= limit) {
+    long long span = 0;
+    const int rounds = (d.items + grid - 1) / grid, rest = d.items - (rounds - 1) * grid;
+    if (rounds > 1 && rest < grid) {
+      int cost = longest + q.pair_tokens, seq, g, p;
+      ranked(q, sq, (rounds - 1) * grid, cost, seq, g, p);
+      span = (long long)(cost + kItemCost) * (grid - rest) / grid;
+    }
+    d.whole = d.total / grid + span <= limit;
+  }
+  if (d.whole) d.ncta = grid;
+  return d;
 }
 
 // The point at cost u, moved to an item boundary when it would leave fewer
@@ -198,12 +268,52 @@ __device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
 // Walks the items of a CTA's range.
 struct Walk {
   Point at, end;
-  Seq s;
+  Seq s;               // the sequence at `at`; whole items: the lane's sequence
   bool have;
+  int round, cost;     // whole items: rounds dealt so far, the last item's cost
 
-  __device__ __forceinline__ Walk(const Point& a, const Point& e) : at(a), end(e), have(false) {}
+  __device__ __forceinline__ Walk(const Point& a, const Point& e)
+      : at(a), end(e), have(false), round(0), cost(0) {}
 
-  __device__ __forceinline__ bool next(const PromptParams& q, long long total, int ncta, Piece& w) {
+  __device__ __forceinline__ void fill(const PromptParams& q, const Seq& sq, int seq, int g, int p,
+                                       Piece& w) {
+    w.seq = seq;
+    w.g = g;
+    w.tok0 = p * q.pair_tokens;
+    w.row0 = sq.row0;
+    w.n = sq.n;
+    w.ctx = sq.ctx;
+    w.na = tiles_of(q, sq, p, 0);
+    w.nb = tiles_of(q, sq, p, 1);
+    w.k0 = 0;
+    w.k1 = max(w.na, w.nb);
+    w.first = w.last = blockIdx.x;
+  }
+
+  // Items dealt out whole, longest first, back and forth over the CTAs.
+  __device__ __forceinline__ bool next_whole(const PromptParams& q, const Division& d, Piece& w) {
+    const int lane = threadIdx.x & 31;
+    if (round == 0) {
+      s = Seq{};
+      if (lane < q.batch) s = load_seq(q, lane);
+      cost = __reduce_max_sync(0xffffffffu, s.pairs > 0 ? s.ctx + s.pairs * q.pair_tokens : 0);
+    }
+    const int N = gridDim.x;
+    const int k = round * N + ((round & 1) ? N - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    ++round;
+    if (k >= d.items) return false;
+    int seq, g, p;
+    ranked(q, s, k, cost, seq, g, p);
+    Seq sq;
+    sq.row0 = __shfl_sync(0xffffffffu, s.row0, seq & 31);
+    sq.n = __shfl_sync(0xffffffffu, s.n, seq & 31);
+    sq.ctx = __shfl_sync(0xffffffffu, s.ctx, seq & 31);
+    fill(q, sq, seq, g, p, w);
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const PromptParams& q, const Division& d, Piece& w) {
+    if (d.whole) return next_whole(q, d, w);
     while (true) {
       if (at.seq >= q.batch || at.seq > end.seq) return false;
       if (!have) {
@@ -217,25 +327,17 @@ struct Walk {
       }
       const bool stop = at.seq == end.seq && at.g == end.g && at.p == end.p;
       if (stop && end.k <= at.k) return false;
-      w.seq = at.seq;
-      w.g = at.g;
-      w.tok0 = at.p * q.pair_tokens;
-      w.row0 = s.row0;
-      w.n = s.n;
-      w.ctx = s.ctx;
-      w.na = tiles_of(q, s, at.p, 0);
-      w.nb = tiles_of(q, s, at.p, 1);
-      const int nt = max(w.na, w.nb);
+      fill(q, s, at.seq, at.g, at.p, w);
+      const int nt = w.k1;
       w.k0 = at.k;
       w.k1 = stop ? end.k : nt;
-      w.first = w.last = blockIdx.x;
       if (w.k0 > 0 || w.k1 < nt) {
         // Boundary i sits at floor(i * total / ncta), which is >= x exactly when
         // i >= ceil(x * ncta / total); those in [a, b) fall inside the item (locate()).
         const long long a = at.us + kItemCost + 2 * kTile - kTile / 2;
         const long long b = at.us + kItemCost + (long long)kTile * nt - 2 * kTile + kTile / 2;
-        w.first = (int)((a * ncta + total - 1) / total) - 1;
-        w.last = (int)((b * ncta + total - 1) / total) - 1;
+        w.first = (int)((a * d.ncta + d.total - 1) / d.total) - 1;
+        w.last = (int)((b * d.ncta + d.total - 1) / d.total) - 1;
       }
       if (stop) {
         at.seq = q.batch;   // done
@@ -283,7 +385,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto pcfree = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
-  int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6], cost, CTAs
+  int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
+  Division* division = reinterpret_cast<Division*>(smem + Cfg::kOffMisc + 64);
   int* failed = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 96);        // [2]
   Piece* pieces = reinterpret_cast<Piece*>(smem + Cfg::kOffPieces);
 
@@ -318,16 +421,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   // The CTA's range of the summed cost: warp 8 finds its begin, warp 9 its end.
   if (warp >= 8 && warp < 10) {
-    const long long total = total_cost(q);
-    const int ncta = (int)min((long long)gridDim.x, max(1ll, total / kMinShare));
+    const Division d = divide(q);
     const int i = (int)blockIdx.x + (warp - 8);
     Point pt;
-    if (i >= ncta || total == 0) {
+    if (i >= d.ncta || d.total == 0 || d.whole) {
       pt.seq = q.batch;
       pt.g = pt.p = pt.k = 0;
-      pt.us = total;
+      pt.us = d.total;
     } else {
-      pt = locate(q, i * total / ncta);
+      pt = locate(q, i * d.total / d.ncta);
     }
     if (lane == 0) {
       int* e = ends + 6 * (warp - 8);
@@ -337,11 +439,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       e[3] = pt.k;
       e[4] = (int)(pt.us & 0xffffffffll);
       e[5] = (int)(pt.us >> 32);
-      if (warp == 8) {
-        long long* tc = reinterpret_cast<long long*>(ends + 12);
-        tc[0] = total;
-        tc[1] = ncta;
-      }
+      if (warp == 8) *division = d;
     }
   }
   tc_fence_before();
@@ -424,12 +522,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       return r;
     };
     Walk walk(point(0), point(1));
-    const long long* tc = reinterpret_cast<const long long*>(ends + 12);
-    const long long total = tc[0];
-    const int ncta = (int)tc[1];
+    const Division d = *division;
     uint32_t c = 0;
     while (ok) {
-      const bool more = walk.next(q, total, ncta, w);
+      const bool more = walk.next(q, d, w);
       if (!more) w.seq = -1;
       const uint32_t i = c % kPieces;
       if (c >= kPieces &&
