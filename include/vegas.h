@@ -325,7 +325,7 @@ vegas_status_t vegas_decode_iteration(
  * sequence's last position may hold anything; K and V inside it must be finite.
  *   q:   device bf16, 16-byte aligned, rows q_stride elements apart (a
  *        multiple of 8, at least Hq * head_dim)
- *   out: device bf16 [total_rows][Hq][head_dim], 16-byte aligned, not q
+ *   out: device bf16 [total_rows][Hq][head_dim], 32-byte aligned, not q
  *   workspace: vegas_prompt_workspace_size() bytes for the same total_rows,
  *        batch and kv (a larger one serves smaller calls of the same device;
  *        not one that other entry points use), 256-byte aligned

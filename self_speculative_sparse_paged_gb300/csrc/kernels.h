@@ -93,6 +93,7 @@ struct PromptParams {
   int hq, hkv, group;
   int tile_tokens;          // tokens per query tile: floor(128 / group)
   int pair_tokens;          // tokens per item: two tiles
+  uint32_t pair_inverse;    // ceil(2^32 / pair_tokens)
   float scale_log2;
   int* tickets;             // [CTAs][2]
   float* part_ml;           // [CTAs][2 slots][2 tiles][128] (m, l)

@@ -18,9 +18,9 @@
 // owns row r (tensor-memory lane r) and keeps the row's reference m and sum l
 // in registers.  m is the row's maximum over the item's first tile; any other
 // reference gives the same quotient, so later tiles take p = 2^(x - m) without
-// looking for their maximum and only check the sum of each half tile: past
-// 2^20 (or where nothing had been seen) m is raised to the half's maximum, l
-// and the row of O are rescaled, and the half is taken again.  bf16 and fp32
+// looking for their maximum and only check the sum of each part of the tile:
+// past 2^20 (or where nothing had been seen) m is raised to the part's maximum,
+// l and the row of O are rescaled, and the part is taken again.  bf16 and fp32
 // hold numbers of that size as exactly as smaller ones.
 //
 // Warps 0-3: softmax of A; 4-7: softmax of B; 8, 9: TMA of K and V tiles into
@@ -48,7 +48,10 @@ constexpr int kItemCost = 256;        // an item's fixed cost, in positions
 constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
-constexpr float kSumLimit = 1048576.f;   // a half tile's sum that makes a row raise its reference
+// Parts of a tile whose P goes to the tensor cores by itself.  (Four parts: 16K prompt 10 % slower.)
+constexpr int kParts = 2;
+constexpr int kPart = kTile / kParts; // positions per part
+constexpr float kSumLimit = 1048576.f;   // a part's sum that makes a row raise its reference
 
 // An item, or the part of it in one CTA's range, as published to all warps.
 struct Piece {
@@ -68,7 +71,7 @@ struct PCfg {
   static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + 2 + 2 + 1 + 2 * kPieces + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
   static constexpr size_t kSmem = kOffPieces + kPieces * sizeof(Piece) + 1024;
@@ -88,6 +91,12 @@ struct Seq {
 };
 
 
+// n / pair_tokens for 0 <= n < 2^24 + 2 * pair_tokens: with M = ceil(2^32 / d) the product's
+// excess n * (M * d - 2^32) < n * d stays below 2^32 (d <= 256; a power of two has none).
+__device__ __forceinline__ int pairs_in(const PromptParams& q, int n) {
+  return (int)__umulhi((uint32_t)n, q.pair_inverse);
+}
+
 __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
   Seq r;
   r.row0 = q.row_start[s];
@@ -100,7 +109,7 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
     set_error(q.err, kErrDeviceFault);
     r.n = 0;
   }
-  r.pairs = (r.n + q.pair_tokens - 1) / q.pair_tokens;
+  r.pairs = pairs_in(q, r.n + q.pair_tokens - 1);
   const long long P = r.pairs;
   r.per_head = P * (r.ctx + kItemCost) + q.pair_tokens * (P * (P + 1) / 2);
   return r;
@@ -131,7 +140,7 @@ struct Division {
 __device__ __forceinline__ int items_from(const PromptParams& q, const Seq& s, int cost) {
   // items of this lane's sequence whose cost is at least `cost`
   const int above = cost - s.ctx;   // (p + 1) * pair_tokens >= above
-  const int skip = above <= 0 ? 0 : (above + q.pair_tokens - 1) / q.pair_tokens - 1;
+  const int skip = above <= 0 ? 0 : pairs_in(q, above + q.pair_tokens - 1) - 1;
   return max(0, s.pairs - max(skip, 0)) * q.hkv;
 }
 
@@ -153,7 +162,7 @@ __device__ __forceinline__ void ranked(const PromptParams& q, const Seq& sq, int
   const int nth = (k - before) / q.hkv;
   g = (k - before) - nth * q.hkv;
   seq = __fns(who, 0, nth + 1);
-  const int mine = (lo - sq.ctx) / q.pair_tokens - 1;
+  const int mine = pairs_in(q, max(0, lo - sq.ctx)) - 1;
   p = __shfl_sync(0xffffffffu, mine, seq & 31);
 }
 
@@ -376,13 +385,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto full = [&](uint32_t s) { return bar0 + 8 * s; };
   auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
-  auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + 2 * x + h); };
-  auto odone = [&](int x) { return bar0 + 8 * (2 * NS + 6 + x); };
-  const uint32_t qfull = bar0 + 8 * (2 * NS + 8), qfree = bar0 + 8 * (2 * NS + 9);
-  const uint32_t drain = bar0 + 8 * (2 * NS + 10);
-  auto pvhalf = [&](int x) { return bar0 + 8 * (2 * NS + 11 + 2 * kPieces + x); };
-  auto pcfull = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + i); };
-  auto pcfree = [&](uint32_t i) { return bar0 + 8 * (2 * NS + 11 + kPieces + i); };
+  constexpr int B1 = 2 * NS + 2 + 2 * kParts;
+  auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + kParts * x + h); };
+  auto odone = [&](int x) { return bar0 + 8 * (B1 + x); };
+  auto pvpart = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
+  const uint32_t qfull = bar0 + 8 * (B1 + 4), qfree = bar0 + 8 * (B1 + 5);
+  const uint32_t drain = bar0 + 8 * (B1 + 6);
+  auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + i); };
+  auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
@@ -399,10 +409,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(sfull(x), 1);
-      mbar_init(pready(x, 0), 128);
-      mbar_init(pready(x, 1), 128);
+      for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 128);
       mbar_init(odone(x), 1);
-      mbar_init(pvhalf(x), 1);
+      mbar_init(pvpart(x), 1);
     }
     mbar_init(qfull, 1);
     mbar_init(qfree, 1);
@@ -413,6 +422,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     fence_mbar_init();
   }
+  if (tid == 32) prefetch_tensormap(&kmap);
+  if (tid == 64) prefetch_tensormap(&vmap);
+  if (tid == 96) prefetch_tensormap(&qmap);
   if (warp == 10) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -539,18 +551,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       __syncwarp();
       if (!more) break;
+      const int tiles = w.nb > 0 ? 2 : 1;
+      const int qrow = w.row0 + w.tok0;
+      if (c > 0 && lane < tiles * Cfg::kHalves)   // on their way while the last item still uses the buffer
+        tma_prefetch_3d(&qmap, 64 * (lane % Cfg::kHalves), w.g * q.group,
+                        qrow + lane / Cfg::kHalves * q.tile_tokens);
       if (c > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree, (c - 1) & 1))) {
         ok = false;
         break;
       }
-      const int tiles = w.nb > 0 ? 2 : 1;
       const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
       if (lane == 0) {
         mbar_arrive_expect_tx(qfull, bytes * tiles * Cfg::kHalves);
         for (int x = 0; x < tiles; ++x)
           for (int h = 0; h < Cfg::kHalves; ++h)
             tma_load_3d(sbase + x * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
-                        w.row0 + w.tok0 + x * q.tile_tokens, qfull);
+                        qrow + x * q.tile_tokens, qfull);
       }
       __syncwarp();
       ++c;
@@ -586,9 +602,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint32_t b = slot16(jv);
       if (leader) {
 #pragma unroll
-        for (int kp = 0; kp < 4; ++kp)
-          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + 32 * h + 8 * kp,
-                    with_addr(dVmn, b + (4 * h + kp) * 128), idPV, accumulate || h > 0 || kp > 0);
+        for (int kp = 0; kp < kPart / 16; ++kp)
+          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + (kPart / 2) * h + 8 * kp,
+                    with_addr(dVmn, b + (kPart / 16 * h + kp) * 128), idPV,
+                    accumulate || h > 0 || kp > 0);
       }
       __syncwarp();
     };
@@ -621,14 +638,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int x = 0; x < 2; ++x) {
           const int ex = x ? eb : ea;
           if (t >= ex) continue;
-          for (int h = 0; h < 2; ++h) {   // positions 0-63 go ahead of 64-127
+          for (int h = 0; h < kParts; ++h) {   // part by part, as the softmax finishes them
             if (!wait_all(pready(x, h), (x ? npb : npa) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
             issue_pv(x, h, jv, t > w.k0);
-            if (h == 0) commit(pvhalf(x));
+            if (h + 1 < kParts) commit(pvpart(x));
           }
           if (!ok) break;
           x ? ++npb : ++npa;
@@ -683,13 +700,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ++ns;
         tc_fence_after();
         float s[128];
+        const int pos0 = t * kTile;
+        const bool diagonal = pos0 + kTile - 1 > w.ctx + first_tok;
+        const int cut = lim - pos0;   // the row's last visible position in the tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
         tmem_ld_wait();
-        const int pos0 = t * kTile;
-        if (pos0 + kTile - 1 > w.ctx + first_tok) {
-          // masked: positions the row may not see, whatever their logits hold
-          const int cut = lim - pos0;
+        if (diagonal) {   // whatever the logits hold
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i > cut) s[i] = -INFINITY;
@@ -716,16 +733,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];   // P to 8 bits of mantissa: the tensor cores' operand type
+        for (int h = 0; h < kParts; ++h) {
+          constexpr int P = kPart;
+          uint32_t pk[P / 2];   // P to 8 bits of mantissa: the tensor cores' operand type
           float hs;
           auto take = [&]() {
             const uint64_t nm2 = pair_f32(-m, -m);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < P / 2; ++e) {
               float a, b;
-              unpair_f32(fma_f32x2(pair_f32(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), sc2, nm2), a,
+              unpair_f32(fma_f32x2(pair_f32(s[P * h + 2 * e], s[P * h + 2 * e + 1]), sc2, nm2), a,
                          b);
               a = ex2(a);
               b = ex2(b);
@@ -738,19 +756,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
           };
           take();
           if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
-            float mx = s[64 * h];
+            float mx = s[P * h];
 #pragma unroll
-            for (int i = 1; i < 64; ++i) mx = fmaxf(mx, s[64 * h + i]);
+            for (int i = 1; i < P; ++i) mx = fmaxf(mx, s[P * h + i]);
             const float m2 = fmaxf(m, mx * q.scale_log2);
             const float f = ex2(m - m2);
             m = m2;
             l *= f;
             // O holds the row's earlier tiles (S of this one was issued after their
-            // products), and in the second half this tile's first one
-            if (h == 1)
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvhalf(x), (ns - 1) & 1)) && ok;
+            // products), and from the second part on this tile's earlier parts
+            static_assert(kParts == 2, "one pvpart phase a tile");
+            if (h > 0)
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvpart(x), (ns - 1) & 1)) && ok;
             tc_fence_after();
-            if (t > w.k0 || h == 1) {
+            if (t > w.k0 || h > 0) {
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 float o[16];
@@ -765,8 +784,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             take();
           }
           l += hs;
-          tmem_st16(tl + scol + 32 * h, pk);
-          tmem_st16(tl + scol + 32 * h + 16, pk + 16);
+#pragma unroll
+          for (int i = 0; i < P / 32; ++i) tmem_st16(tl + scol + P / 2 * h + 16 * i, pk + 16 * i);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(pready(x, h));
@@ -804,12 +823,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tmem_ld_wait();
           if (live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              reinterpret_cast<uint4*>(o_row)[4 * i + e] =
-                  make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                             pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                             pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                             pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 2; ++e) {   // whole 32-byte sectors
+              uint32_t v[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                v[u] = pack_bf16x2(o[16 * e + 2 * u] * inv, o[16 * e + 2 * u + 1] * inv);
+              store_32_bytes(o_row + 32 * i + 16 * e, v);
+            }
           }
         }
         tc_fence_before();

@@ -802,8 +802,8 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
   if (st != VEGAS_OK) return st;
   if ((st = check_packed(row_start, ctx_lens, total_rows, batch)) != VEGAS_OK) return st;
   if ((st = check_rows("q", q, q_stride, kv->num_q_heads, kv->head_dim)) != VEGAS_OK) return st;
-  if (!out || !aligned16(out))
-    return fail(VEGAS_ERR_INVALID_ARG, "out must be a 16-byte aligned pointer");
+  if (!out || (reinterpret_cast<uintptr_t>(out) & 31u))   // the kernel stores whole sectors
+    return fail(VEGAS_ERR_INVALID_ARG, "out must be a 32-byte aligned pointer");
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
     return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale must be finite and positive");
   const int G = kv->num_q_heads / kv->num_kv_heads;
@@ -838,6 +838,7 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
   p.group = G;
   p.tile_tokens = pl.tile_tokens;
   p.pair_tokens = 2 * pl.tile_tokens;
+  p.pair_inverse = (uint32_t)(((1ull << 32) + p.pair_tokens - 1) / p.pair_tokens);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.tickets = reinterpret_cast<int*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + pl.ml_off);

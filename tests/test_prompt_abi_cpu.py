@@ -41,14 +41,14 @@ def test_rope_append_refusals(vg):  # noqa: F811
 
 def test_prompt_attn_refusals(vg):  # noqa: F811
     kv = vg.PagedKV(16, 16, 16, 4, 16, 8, 2, 64, 4)
-    good = dict(kv=kv, q=16, q_stride=512, out=16, row_start=16, ctx_lens=16, total_rows=5,
+    good = dict(kv=kv, q=16, q_stride=512, out=32, row_start=16, ctx_lens=16, total_rows=5,
                 batch=1, softmax_scale=0.1, workspace=256, workspace_bytes=1 << 30, stream=0)
     for change, status, word in (
             (dict(kv=vg.PagedKV(16, 16, 16, 4, 8, 8, 2, 64, 4)), 2, "page_size"),
             (dict(kv=vg.PagedKV(16, 16, 16, 4, 16, 65, 1, 64, 4), q_stride=65 * 64), 2, "group"),
             (dict(q=None), 1, "q is NULL"), (dict(q=8), 1, "16-byte"),
             (dict(q_stride=511), 1, "q_stride"), (dict(q_stride=516), 2, "q_stride"),
-            (dict(out=None), 1, "out"), (dict(out=40), 1, "out"),
+            (dict(out=None), 1, "out"), (dict(out=48), 1, "out"),
             (dict(row_start=None), 1, "row_start"), (dict(ctx_lens=None), 1, "ctx_lens"),
             (dict(total_rows=-2), 1, "total_rows"), (dict(batch=-1), 1, "batch"),
             (dict(softmax_scale=0.0), 1, "softmax_scale"),
