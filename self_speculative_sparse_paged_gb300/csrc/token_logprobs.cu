@@ -8,15 +8,21 @@
 //   top n   = the n largest logits above -inf, ties to the lower index.
 //
 // A cluster of CTAs shares a row.  Each thread streams 16-byte chunks with a
-// running reference maximum (raised only when exceeded by 2^8, so the sums are
-// rescaled a few times a row), fp32 sums of e and e * y, the rank's count and
-// its own largest logit.  The n-th largest of the threads' maxima bounds the
-// n-th largest logit from below, so only threads whose maximum reaches it read
-// their chunks again (from L2) and post the logits that reach it as unique
-// 64-bit keys (value, then lower index first); the n best of those are found
-// by counting larger keys.  Should ties post more keys than the list holds,
-// the n best are found one by one over the whole slice.  The cluster's first
-// CTA joins sums, counts and the CTAs' n keys through distributed shared memory.
+// running reference m (raised only when exceeded by 2^8, so the sums are
+// rescaled a few times a row), fp32 sums of e and e (x - m), the rank's count
+// and its own largest logit.  Instructions bound the stream before memory does,
+// so pairs go through packed fp32 and (the maximum, the mask's clamp, the
+// count) packed bf16 operations: about 8 instructions a logit.
+// The n-th largest of the warps' four largest thread maxima bounds the n-th
+// largest logit from below, so only the chunks of threads whose maximum reaches
+// it are read again (by their whole warp, from L2); the logits that reach it
+// are posted as unique 64-bit keys (value, then lower index first), and the n
+// best of those are found by counting larger keys.  Should ties post more keys
+// than the list holds, the n best are found one by one over the whole slice.
+// Every CTA pushes its sums and its n keys to the cluster's first one through
+// distributed shared memory, which joins them.
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -33,41 +39,98 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpList = 1024;          // candidate keys a CTA can hold
 constexpr float kLpSlack = 8.f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
+// A 16-byte chunk of logits: as fp32, its maximum (of the raw values), the
+// values with -inf raised to the type's lowest, and how many lie above cmp
+// (unordered: all of them where cmp is NaN).
 template <typename T>
 struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __nv_bfloat162 w[4];
+  __device__ __forceinline__ explicit Chunk(const uint4& v) {
+    w[0] = *reinterpret_cast<const __nv_bfloat162*>(&v.x);
+    w[1] = *reinterpret_cast<const __nv_bfloat162*>(&v.y);
+    w[2] = *reinterpret_cast<const __nv_bfloat162*>(&v.z);
+    w[3] = *reinterpret_cast<const __nv_bfloat162*>(&v.w);
+  }
+  static __device__ __forceinline__ float2 wide(__nv_bfloat162 v) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  __device__ __forceinline__ float largest() const {
+    const float2 f = wide(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+    return fmaxf(f.x, f.y);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      const float2 f = wide(w[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
     }
   }
+  __device__ __forceinline__ void finite(float (&x)[8]) const {
+    const uint32_t low = 0xff7fff7fu;   // the lowest finite bf16, twice
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = wide(__hmax2(w[e], *reinterpret_cast<const __nv_bfloat162*>(&low)));
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ int above(float cmp) const {
+    const __nv_bfloat162 c = __float2bfloat162_rn(cmp);   // exact: cmp is a bf16 number
+    const float2 f = wide(__hadd2(__hadd2(__hgtu2(w[0], c), __hgtu2(w[1], c)),
+                                  __hadd2(__hgtu2(w[2], c), __hgtu2(w[3], c))));
+    return (int)(f.x + f.y);
+  }
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  // the next number below x (not -inf) of this type
+  static __device__ __forceinline__ float below(float x) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b << 1) == 0) return __uint_as_float(0x80010000u);
+    return __uint_as_float((b & 0x80000000u) ? b + 0x10000u : b - 0x10000u);
+  }
 };
 template <>
 struct Chunk<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+  float w[4];
+  __device__ __forceinline__ explicit Chunk(const uint4& v) {
+    w[0] = __uint_as_float(v.x);
+    w[1] = __uint_as_float(v.y);
+    w[2] = __uint_as_float(v.z);
+    w[3] = __uint_as_float(v.w);
+  }
+  __device__ __forceinline__ float largest() const {
+    return fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+  }
+  __device__ __forceinline__ void values(float (&x)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = w[e];
+  }
+  __device__ __forceinline__ void finite(float (&x)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fmaxf(w[e], -FLT_MAX);
+  }
+  __device__ __forceinline__ int above(float cmp) const {
+    return (int)(!(w[0] <= cmp)) + (int)(!(w[1] <= cmp)) + (int)(!(w[2] <= cmp)) +
+           (int)(!(w[3] <= cmp));
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ float below(float x) { return nextafterf(x, -INFINITY); }
 };
 
 // Unique order-preserving key: larger logit first, then the lower index.
 // (x + 0 makes -0 equal to +0.)  A key of 0 stands for none.
-__device__ __forceinline__ unsigned long long key_of(float x, int i) {
+__device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((unsigned long long)o << 32) | (uint32_t)~i;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long key_of(float x, int i) {
+  return ((unsigned long long)order_of(x) << 32) | (uint32_t)~i;
 }
 __device__ __forceinline__ float value_of(unsigned long long k) {
   const uint32_t o = (uint32_t)(k >> 32);
@@ -75,31 +138,52 @@ __device__ __forceinline__ float value_of(unsigned long long k) {
 }
 __device__ __forceinline__ int index_of(unsigned long long k) { return (int)~(uint32_t)k; }
 
+constexpr int kLpLead = 4;              // thread maxima a warp offers for the bound
+
 struct LpShared {
   float m[kLpWarps], s[kLpWarps], t[kLpWarps];
   int cnt[kLpWarps];
-  unsigned long long best[kLpWarps];
-  float tmax[kLpThreads];
-  float bound;
+  uint32_t lead[kLpWarps * kLpLead];    // as order_of()
+  uint32_t bound;
   int posted;
+  unsigned long long best[kLpWarps];
   unsigned long long list[kLpList];
-  // the CTA's result, read by the cluster's first CTA
-  float M, S, Tt;
-  int count;
-  unsigned long long top[32];
-  unsigned long long all[32 * 16];
+  // in the cluster's first CTA: what every CTA pushed
+  float M[kMaxLogprobCluster], S[kMaxLogprobCluster], Tt[kMaxLogprobCluster];
+  int count[kMaxLogprobCluster];
+  unsigned long long all[kMaxLogprobCluster * kMaxTopLogprobs];
+  float row_max, ln_z;
 };
+
+// (s, t) = sums of 2^((x - from) k) and of that times (x - from), moved to the reference `to`
+// (>= from - slack; t stays in logit units).  Terms that vanish leave exact zeros.
+__device__ __forceinline__ void move_sums(float from, float to, float k, float& s, float& t) {
+  if (from > -INFINITY) {
+    const float d = fmaxf(from - to, -FLT_MAX), f = ex2(d * k);
+    t = f > 0.f ? f * fmaf(s, d, t) : 0.f;
+    s *= f;
+  } else {
+    s = t = 0.f;
+  }
+}
 
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
+    token_logprobs_kernel(const LogprobParams p) {
   constexpr int N = Chunk<T>::N;
   __shared__ LpShared sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = p.cluster, r = C > 1 ? (int)cluster.block_rank() : 0;
+  const int C = p.cluster, r = (int)cluster.block_rank();
   const int row = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = p.top_n;
+  if (r == 0)
+    for (int i = tid; i < C * n; i += kLpThreads) sh.all[i] = 0;
+  if (tid == 0) sh.posted = 0;
+  // (waited for before the first push: the first CTA runs and its list is clear)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_begin();
 
   const T* x = reinterpret_cast<const T*>(p.logits) + size_t(row) * p.row_stride;
@@ -121,47 +205,71 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
   const bool has_single = r == 0 && tid < singles;
 
   const float xt = tok >= 0 ? Chunk<T>::one(x + tok) : INFINITY;
-  // x counts before the token when x > xt, or x >= xt at a lower index:
-  // there x > (the number below xt), or any x when xt = -inf (not x <= NaN)
-  const float xt_low = xt == -INFINITY ? NAN : nextafterf(xt, -INFINITY);
-  const float k = p.inv_temperature * kLog2e;
+  // x counts when x > xt, or x >= xt at a lower index: there x > (the number
+  // below xt), or any x when xt = -inf (compared, unordered, with NaN)
+  const float xt_low = xt == -INFINITY ? NAN : Chunk<T>::below(xt);
+  const float k = p.inv_temperature * kLog2e, slack = kLpSlack / k;
 
-  float m = -INFINITY, s = 0.f, t = 0.f, tm = -INFINITY;
+  float m = -INFINITY, tm = -INFINITY;
+  uint64_t s2 = 0, t2 = 0;   // pairs of partial sums
   int cnt = 0;
-  auto raise = [&](float to) {   // the reference maximum, with the sums moved to it
-    if (to > -INFINITY && (m == -INFINITY || (to - m) * k > kLpSlack)) {
+  auto raise = [&](float to) {
+    if (to > m + slack) {   // (from -inf: any number)
       if (m > -INFINITY) {
-        const float d = (m - to) * k, f = ex2(d);
-        t = f > 0.f ? f * (t + s * d) : 0.f;
-        s *= f;
+        float sa, sb, ta, tb;
+        unpair_f32(s2, sa, sb);
+        unpair_f32(t2, ta, tb);
+        move_sums(m, to, k, sa, ta);
+        move_sums(m, to, k, sb, tb);
+        s2 = pair_f32(sa, sb);
+        t2 = pair_f32(ta, tb);
       }
       m = to;
     }
   };
-  auto add = [&](float v) {
-    const float y = fmaxf((v - m) * k, -200.f);   // (a masked logit: 2^-200 flushes to 0)
-    const float e = ex2(y);
-    s += e;
-    t = fmaf(e, y, t);
+  const uint64_t k2 = pair_f32(k, k);
+  auto add2 = [&](float a, float b) {   // a, b finite or as low as the type goes
+    uint64_t u = add_f32x2(pair_f32(a, b), pair_f32(-m, -m));
+    float ya, yb;
+    if (m > 1e30f) {   // where the lowest number minus m would be -inf
+      unpair_f32(u, ya, yb);
+      u = pair_f32(fmaxf(ya, -FLT_MAX), fmaxf(yb, -FLT_MAX));
+    }
+    unpair_f32(mul_f32x2(u, k2), ya, yb);
+    const uint64_t e = pair_f32(ex2(ya), ex2(yb));
+    s2 = add_f32x2(s2, e);
+    t2 = fma_f32x2(e, u, t2);
+  };
+  auto add1 = [&](float v) {
+    const float u = fmaxf(v - m, -FLT_MAX), e = ex2(u * k);
+    s2 = add_f32x2(s2, pair_f32(e, 0.f));
+    t2 = add_f32x2(t2, pair_f32(e * u, 0.f));
   };
   auto take = [&](const uint4& raw, int c) {
-    float v[N];
-    Chunk<T>::unpack(raw, v);
-    float mx = v[0];
-#pragma unroll
-    for (int e = 1; e < N; ++e) mx = fmaxf(mx, v[e]);
+    const Chunk<T> ch(raw);
+    const float mx = ch.largest();
     tm = fmaxf(tm, mx);
     raise(mx);
+    if (m > -1e30f) {
+      float v[N];
+      ch.finite(v);   // a masked logit counts 2^(-3e38 k) = 0
 #pragma unroll
-    for (int e = 0; e < N; ++e) add(v[e]);
+      for (int e = 0; e < N; e += 2) add2(v[e], v[e + 1]);
+    } else {
+      float v[N];
+      ch.values(v);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (v[e] > -INFINITY) add1(v[e]);
+    }
     const int i0 = head + c * N;
-    if (tok >= i0 && tok < i0 + N) {
+    if ((unsigned)(tok - i0) < (unsigned)N) {
+      float v[N];
+      ch.values(v);
 #pragma unroll
       for (int e = 0; e < N; ++e) cnt += v[e] > xt || (v[e] == xt && i0 + e < tok);
     } else {
-      const float cmp = i0 < tok ? xt_low : xt;
-#pragma unroll
-      for (int e = 0; e < N; ++e) cnt += !(v[e] <= cmp);
+      cnt += ch.above(i0 < tok ? xt_low : xt);
     }
   };
   int c = c0 + tid;
@@ -178,75 +286,102 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
     const float v = Chunk<T>::one(x + i);
     tm = fmaxf(tm, v);
     raise(v);
-    add(v);
+    if (v > -INFINITY) add1(v);
     cnt += v > xt || (v == xt && i < tok);
   }
 
-  // ---- sums of the CTA
-  float M = tm;
+  // ---- the warp's sums, relative to its maximum, and its largest thread maxima
+  {
+    uint32_t left = order_of(tm);
+    float Mw = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) sh.m[warp] = M;
-  sh.tmax[tid] = tm;
-  if (tid == 0) sh.posted = 0;
+    for (int j = 0; j < kLpLead; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, left);
+      if (j == 0) Mw = value_of((unsigned long long)top << 32);
+      if (lane == 0) sh.lead[warp * kLpLead + j] = top;
+      const unsigned who = __ballot_sync(0xffffffffu, left == top);
+      if (lane == __ffs(who) - 1) left = 0;
+      if (n <= 1) break;
+    }
+    float s, t, sb, tb;
+    unpair_f32(s2, s, sb);
+    unpair_f32(t2, t, tb);
+    s += sb;
+    t += tb;
+    move_sums(m, Mw, k, s, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) {
+      sh.m[warp] = Mw;
+      sh.s[warp] = s;
+      sh.t[warp] = t;
+      sh.cnt[warp] = cnt;
+    }
+  }
   __syncthreads();
-  M = sh.m[0];
-#pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) M = fmaxf(M, sh.m[w]);
-  auto move_to = [&](float from, float to, float& ss, float& tt) {
-    if (from > -INFINITY) {
-      const float d = fmaxf((from - to) * k, -200.f), f = ex2(d);
-      tt = f * (tt + ss * d);
-      ss *= f;
-    } else {
-      ss = tt = 0.f;
-    }
-  };
-  move_to(m, M, s, t);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    t += __shfl_xor_sync(0xffffffffu, t, o);
-    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-  }
-  if (lane == 0) {
-    sh.s[warp] = s;
-    sh.t[warp] = t;
-    sh.cnt[warp] = cnt;
-  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  LpShared* first = cluster.map_shared_rank(&sh, 0);
 
-  // ---- the CTA's n best
-  const int n = p.top_n;
-  if (n > 0) {
-    // the n-th largest of the threads' maxima
-    int above = 0;
-    const float4* t4 = reinterpret_cast<const float4*>(sh.tmax);
-#pragma unroll 8
-    for (int j = 0; j < kLpThreads / 4; ++j) {
-      const float4 v = t4[j];
-      above += (v.x > tm || (v.x == tm && 4 * j < tid)) + (v.y > tm || (v.y == tm && 4 * j + 1 < tid)) +
-               (v.z > tm || (v.z == tm && 4 * j + 2 < tid)) + (v.w > tm || (v.w == tm && 4 * j + 3 < tid));
-    }
-    if (above == n - 1) sh.bound = tm;
-    if (tid < 32) sh.top[tid] = 0;
-    __syncthreads();
-    const float bound = sh.bound;
-    auto each = [&](auto&& f) {   // this thread's logits again
-      for (int cc = c0 + tid; cc < c1; cc += kLpThreads) {
-        float v[N];
-        Chunk<T>::unpack(__ldg(&xc[cc]), v);
+  // the CTA's sums (warp 2) and the bound on its n-th largest logit (warps 0 and 1)
+  if (warp == 2) {
+    const bool has = lane < kLpWarps;
+    float M = has ? sh.m[lane] : -INFINITY, s = has ? sh.s[lane] : 0.f, t = has ? sh.t[lane] : 0.f;
+    const float from = M;
 #pragma unroll
-        for (int e = 0; e < N; ++e) f(v[e], head + cc * N + e);
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    move_sums(from, M, k, s, t);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    const int total = __reduce_add_sync(0xffffffffu, has ? sh.cnt[lane] : 0);
+    if (lane == 0) {
+      first->M[r] = M;
+      first->S[r] = s;
+      first->Tt[r] = t;
+      first->count[r] = total;
+    }
+  }
+  if (n > 0) {
+    const int offered = kLpWarps * (n <= 1 ? 1 : kLpLead), step = n <= 1 ? kLpLead : 1;
+    if (tid < offered) {
+      const uint32_t mine = sh.lead[tid * step];
+      int above = 0;
+      for (int j = 0; j < offered; ++j) {
+        const uint32_t other = sh.lead[j * step];
+        above += other > mine || (other == mine && j < tid);
       }
-      if (has_single) f(Chunk<T>::one(x + single_at(tid)), single_at(tid));
+      if (above == n - 1) sh.bound = mine;
+    }
+    __syncthreads();
+    const uint32_t bound = sh.bound;
+    auto post = [&](float v, int i) {
+      if (v > -INFINITY && order_of(v) >= bound) {
+        const int at = atomicAdd(&sh.posted, 1);
+        if (at < kLpList) sh.list[at] = key_of(v, i);
+      }
     };
-    if (tm >= bound && tm > -INFINITY)
-      each([&](float v, int i) {
-        if (v >= bound && v > -INFINITY) {
-          const int at = atomicAdd(&sh.posted, 1);
-          if (at < kLpList) sh.list[at] = key_of(v, i);
+    const bool reaches = tm > -INFINITY && order_of(tm) >= bound;
+    unsigned who = __ballot_sync(0xffffffffu, reaches);
+    if (reaches && has_single) post(Chunk<T>::one(x + single_at(tid)), single_at(tid));
+    while (who) {   // the warp reads the chunks of one such thread
+      const int owner = tid - lane + __ffs(who) - 1;
+      who &= who - 1;
+      for (int cc = c0 + owner + lane * kLpThreads; cc < c1; cc += 32 * kLpThreads) {
+        const Chunk<T> ch(__ldg(&xc[cc]));
+        if (order_of(ch.largest()) >= bound) {
+          float v[N];
+          ch.values(v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) post(v[e], head + cc * N + e);
         }
-      });
+      }
+    }
     __syncthreads();
     const int posted = sh.posted;
     if (posted <= kLpList) {
@@ -254,18 +389,25 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
         const unsigned long long mine = sh.list[i];
         int larger = 0;
         for (int j = 0; j < posted; ++j) larger += sh.list[j] > mine;
-        if (larger < n) sh.top[larger] = mine;
+        if (larger < n) first->all[r * n + larger] = mine;
       }
     } else {
       unsigned long long last = ~0ull;
       for (int q = 0; q < n; ++q) {
         unsigned long long best = 0;
-        each([&](float v, int i) {
+        auto see = [&](float v, int i) {
           if (v > -INFINITY) {
             const unsigned long long kk = key_of(v, i);
             if (kk < last && kk > best) best = kk;
           }
-        });
+        };
+        for (int cc = c0 + tid; cc < c1; cc += kLpThreads) {
+          float v[N];
+          Chunk<T>(__ldg(&xc[cc])).values(v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) see(v[e], head + cc * N + e);
+        }
+        if (has_single) see(Chunk<T>::one(x + single_at(tid)), single_at(tid));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
@@ -275,79 +417,64 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
         __syncthreads();
         for (int w = 0; w < kLpWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
         __syncthreads();
-        if (tid == 0) sh.top[q] = best;
+        if (tid == 0) first->all[r * n + q] = best;
         last = best;
         if (best == 0) break;
       }
     }
   }
-  __syncthreads();
-  if (tid == 0) {
-    float S = 0.f, Tt = 0.f;
-    int count = 0;
-    for (int w = 0; w < kLpWarps; ++w) {
-      S += sh.s[w];
-      Tt += sh.t[w];
-      count += sh.cnt[w];
-    }
-    sh.M = M;
-    sh.S = S;
-    sh.Tt = Tt;
-    sh.count = count;
-  }
 
-  // ---- the row, in the cluster's first CTA
-  if (C > 1)
-    cluster.sync();
-  else
-    __syncthreads();
-  if (r == 0) {
-    float Mr = sh.M;
-    for (int q = 1; q < C; ++q) Mr = fmaxf(Mr, cluster.map_shared_rank(&sh, q)->M);
-    float S = 0.f, Tt = 0.f;
-    int count = 0;
-    for (int q = 0; q < C; ++q) {
-      const LpShared* o = C > 1 ? cluster.map_shared_rank(&sh, q) : &sh;
-      float ss = o->S, tt = o->Tt;
-      move_to(o->M, Mr, ss, tt);
-      S += ss;
-      Tt += tt;
-      count += o->count;
+  // ---- the row, in the cluster's first CTA; nothing reads the others' shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (r != 0) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return;
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 0) {
+    const bool has = lane < C;
+    float M = has ? sh.M[lane] : -INFINITY, s = has ? sh.S[lane] : 0.f, t = has ? sh.Tt[lane] : 0.f;
+    const float from = M;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    move_sums(from, M, k, s, t);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
     }
-    const float lnZ = S > 0.f ? logf(S) : 0.f;
-    if (tid == 0) {
+    const int count = __reduce_add_sync(0xffffffffu, has ? sh.count[lane] : 0);
+    if (lane == 0) {
+      const float ln_z = s > 0.f ? logf(s) : 0.f;
+      sh.row_max = M;
+      sh.ln_z = ln_z;
       if (p.logprob) {
         float lp = 0.f;
-        if (tok >= 0) lp = xt > -INFINITY ? (xt - Mr) * p.inv_temperature - lnZ : -INFINITY;
+        if (tok >= 0) lp = xt > -INFINITY ? (xt - M) * p.inv_temperature - ln_z : -INFINITY;
         p.logprob[row] = lp;
       }
       if (p.rank) p.rank[row] = tok >= 0 ? count : -1;
-      if (p.entropy) p.entropy[row] = S > 0.f ? lnZ - kLn2 * (Tt / S) : 0.f;
-    }
-    if (n > 0) {
-      for (int i = tid; i < C * n; i += kLpThreads) {
-        const int q = i / n;
-        sh.all[i] = (C > 1 ? cluster.map_shared_rank(&sh, q) : &sh)->top[i - q * n];
-      }
-      if (tid < n) {
-        p.top_ids[size_t(row) * n + tid] = -1;
-        p.top_logprobs[size_t(row) * n + tid] = -INFINITY;
-      }
-      __syncthreads();
-      for (int i = tid; i < C * n; i += kLpThreads) {
-        const unsigned long long mine = sh.all[i];
-        if (mine == 0) continue;
-        int larger = 0;
-        for (int j = 0; j < C * n; ++j) larger += sh.all[j] > mine;
-        if (larger < n) {
-          p.top_ids[size_t(row) * n + larger] = index_of(mine);
-          p.top_logprobs[size_t(row) * n + larger] =
-              (value_of(mine) - Mr) * p.inv_temperature - lnZ;
-        }
-      }
+      if (p.entropy) p.entropy[row] = s > 0.f ? ln_z - p.inv_temperature * (t / s) : 0.f;
     }
   }
-  if (C > 1) cluster.sync();   // no CTA leaves while its shared memory is read
+  if (n > 0) {
+    const int mine_at = tid;   // C * n <= 512 = kLpThreads keys
+    static_assert(kMaxLogprobCluster * kMaxTopLogprobs <= kLpThreads, "a thread a key");
+    const unsigned long long mine = mine_at < C * n ? sh.all[mine_at] : 0;
+    int larger = 0;
+    if (mine)
+      for (int j = 0; j < C * n; ++j) larger += sh.all[j] > mine;
+    const int found = __syncthreads_count(mine != 0);
+    if (mine && larger < n) {
+      p.top_ids[size_t(row) * n + larger] = index_of(mine);
+      p.top_logprobs[size_t(row) * n + larger] =
+          (value_of(mine) - sh.row_max) * p.inv_temperature - sh.ln_z;
+    }
+    if (tid >= found && tid < n) {   // fewer than n logits are left
+      p.top_ids[size_t(row) * n + tid] = -1;
+      p.top_logprobs[size_t(row) * n + tid] = -INFINITY;
+    }
+  }
 }
 
 template <typename T>

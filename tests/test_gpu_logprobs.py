@@ -124,6 +124,8 @@ def test_masks_empty_rows_and_padding_tokens():
     tok[1] = 777
     tok[2] = 4321
     tok[6] = int((x[6] == -math.inf).nonzero()[5])    # a masked token given
+    x[7] = -math.inf                                  # lowest values among masked ones
+    x[7, 100:140] = torch.finfo(torch.float32).min
     for t in (1.0, 1.7, 0.3):
         check(run(x, tok, 6, t), x, tok, 6, t)
 
