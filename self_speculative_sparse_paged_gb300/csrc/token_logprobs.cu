@@ -22,6 +22,7 @@
 // Every CTA pushes its sums and its n keys to the cluster's first one through
 // distributed shared memory, which joins them.
 #include <cfloat>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -40,15 +41,16 @@ constexpr int kLpList = 1024;          // candidate keys a CTA can hold
 constexpr float kLpSlack = 8.f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A 16-byte chunk of logits: as fp32, its maximum (of the raw values), the
-// values with -inf raised to the type's lowest, and how many lie above cmp
-// (unordered: all of them where cmp is NaN).
+// A 16-byte chunk of logits: its values as fp32, or with -inf raised to the
+// type's lowest; the maximum (of the raw values) of B chunks, and how many of
+// their values lie above cmp (unordered: all of them where cmp is NaN).
 template <typename T>
 struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
   static constexpr int N = 8;
   __nv_bfloat162 w[4];
+  Chunk() = default;
   __device__ __forceinline__ explicit Chunk(const uint4& v) {
     w[0] = *reinterpret_cast<const __nv_bfloat162*>(&v.x);
     w[1] = *reinterpret_cast<const __nv_bfloat162*>(&v.y);
@@ -59,8 +61,13 @@ struct Chunk<__nv_bfloat16> {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
-  __device__ __forceinline__ float largest() const {
-    const float2 f = wide(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+  template <int B>
+  static __device__ __forceinline__ float largest(const Chunk (&c)[B]) {
+    __nv_bfloat162 m = __hmax2(__hmax2(c[0].w[0], c[0].w[1]), __hmax2(c[0].w[2], c[0].w[3]));
+#pragma unroll
+    for (int u = 1; u < B; ++u)
+      m = __hmax2(m, __hmax2(__hmax2(c[u].w[0], c[u].w[1]), __hmax2(c[u].w[2], c[u].w[3])));
+    const float2 f = wide(m);
     return fmaxf(f.x, f.y);
   }
   __device__ __forceinline__ void values(float (&x)[8]) const {
@@ -80,11 +87,17 @@ struct Chunk<__nv_bfloat16> {
       x[2 * e + 1] = f.y;
     }
   }
-  __device__ __forceinline__ int above(float cmp) const {
-    const __nv_bfloat162 c = __float2bfloat162_rn(cmp);   // exact: cmp is a bf16 number
-    const float2 f = wide(__hadd2(__hadd2(__hgtu2(w[0], c), __hgtu2(w[1], c)),
-                                  __hadd2(__hgtu2(w[2], c), __hgtu2(w[3], c))));
-    return (int)(f.x + f.y);
+  using Cmp = __nv_bfloat162;
+  static __device__ __forceinline__ Cmp pack(float x) { return __float2bfloat162_rn(x); }   // exact
+  template <int B>
+  static __device__ __forceinline__ float above(const Chunk (&c)[B], const Cmp (&cmp)[B]) {
+    __nv_bfloat162 sum = __float2bfloat162_rn(0.f);   // counts to 4 B: exact in bf16
+#pragma unroll
+    for (int u = 0; u < B; ++u)
+      sum = __hadd2(sum, __hadd2(__hadd2(__hgtu2(c[u].w[0], cmp[u]), __hgtu2(c[u].w[1], cmp[u])),
+                                 __hadd2(__hgtu2(c[u].w[2], cmp[u]), __hgtu2(c[u].w[3], cmp[u]))));
+    const float2 f = wide(sum);
+    return f.x + f.y;
   }
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   // the next number below x (not -inf) of this type
@@ -98,14 +111,19 @@ template <>
 struct Chunk<float> {
   static constexpr int N = 4;
   float w[4];
+  Chunk() = default;
   __device__ __forceinline__ explicit Chunk(const uint4& v) {
     w[0] = __uint_as_float(v.x);
     w[1] = __uint_as_float(v.y);
     w[2] = __uint_as_float(v.z);
     w[3] = __uint_as_float(v.w);
   }
-  __device__ __forceinline__ float largest() const {
-    return fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+  template <int B>
+  static __device__ __forceinline__ float largest(const Chunk (&c)[B]) {
+    float m = c[0].w[0];
+#pragma unroll
+    for (int i = 1; i < 4 * B; ++i) m = fmaxf(m, c[i >> 2].w[i & 3]);
+    return m;
   }
   __device__ __forceinline__ void values(float (&x)[4]) const {
 #pragma unroll
@@ -115,9 +133,24 @@ struct Chunk<float> {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = fmaxf(w[e], -FLT_MAX);
   }
-  __device__ __forceinline__ int above(float cmp) const {
-    return (int)(!(w[0] <= cmp)) + (int)(!(w[1] <= cmp)) + (int)(!(w[2] <= cmp)) +
-           (int)(!(w[3] <= cmp));
+  using Cmp = float;
+  static __device__ __forceinline__ Cmp pack(float x) { return x; }
+  template <int B>
+  static __device__ __forceinline__ float above(const Chunk (&c)[B], const Cmp (&cmp)[B]) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      sum = add_f32x2(sum, pair_f32(set_gtu(c[u].w[0], cmp[u]), set_gtu(c[u].w[1], cmp[u])));
+      sum = add_f32x2(sum, pair_f32(set_gtu(c[u].w[2], cmp[u]), set_gtu(c[u].w[3], cmp[u])));
+    }
+    float a, b;
+    unpair_f32(sum, a, b);
+    return a + b;
+  }
+  static __device__ __forceinline__ float set_gtu(float a, float b) {   // 1 or 0
+    float r;
+    asm("set.gtu.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ float below(float x) { return nextafterf(x, -INFINITY); }
@@ -146,6 +179,7 @@ struct LpShared {
   uint32_t lead[kLpWarps * kLpLead];    // as order_of()
   uint32_t bound;
   int posted;
+  uint8_t owner[kLpWarps][32];
   unsigned long long best[kLpWarps];
   unsigned long long list[kLpList];
   // in the cluster's first CTA: what every CTA pushed
@@ -189,10 +223,6 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   const T* x = reinterpret_cast<const T*>(p.logits) + size_t(row) * p.row_stride;
   const int V = p.vocab;
   int tok = p.tokens ? p.tokens[row] : -1;
-  if (tok >= V) {
-    if (tid == 0) set_error(p.err, kErrDeviceFault);
-    tok = -1;
-  }
   // Elements before the first 16-byte boundary and behind the last whole chunk
   // are taken one by one, by rank 0.
   const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
@@ -204,15 +234,22 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   auto single_at = [&](int i) { return i < head ? i : tail0 + (i - head); };
   const bool has_single = r == 0 && tid < singles;
 
+  if (tok >= V) {
+    if (tid == 0) set_error(p.err, kErrDeviceFault);
+    tok = -1;
+  }
   const float xt = tok >= 0 ? Chunk<T>::one(x + tok) : INFINITY;
   // x counts when x > xt, or x >= xt at a lower index: there x > (the number
   // below xt), or any x when xt = -inf (compared, unordered, with NaN)
   const float xt_low = xt == -INFINITY ? NAN : Chunk<T>::below(xt);
+  const typename Chunk<T>::Cmp above_xt = Chunk<T>::pack(xt), above_low = Chunk<T>::pack(xt_low);
   const float k = p.inv_temperature * kLog2e, slack = kLpSlack / k;
 
+  const int ctok = tok <= head ? 0 : (tok - head + N - 1) / N;   // chunks that begin before the token
   float m = -INFINITY, tm = -INFINITY;
   uint64_t s2 = 0, t2 = 0;   // pairs of partial sums
   int cnt = 0;
+  float many = 0.f;          // counted in whole chunks: exact below 2^24 a thread
   auto raise = [&](float to) {
     if (to > m + slack) {   // (from -inf: any number)
       if (m > -INFINITY) {
@@ -229,12 +266,8 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   };
   const uint64_t k2 = pair_f32(k, k);
   auto add2 = [&](float a, float b) {   // a, b finite or as low as the type goes
-    uint64_t u = add_f32x2(pair_f32(a, b), pair_f32(-m, -m));
+    const uint64_t u = add_f32x2(pair_f32(a, b), pair_f32(-m, -m));
     float ya, yb;
-    if (m > 1e30f) {   // where the lowest number minus m would be -inf
-      unpair_f32(u, ya, yb);
-      u = pair_f32(fmaxf(ya, -FLT_MAX), fmaxf(yb, -FLT_MAX));
-    }
     unpair_f32(mul_f32x2(u, k2), ya, yb);
     const uint64_t e = pair_f32(ex2(ya), ex2(yb));
     s2 = add_f32x2(s2, e);
@@ -245,42 +278,60 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
     s2 = add_f32x2(s2, pair_f32(e, 0.f));
     t2 = add_f32x2(t2, pair_f32(e * u, 0.f));
   };
-  auto take = [&](const uint4& raw, int c) {
-    const Chunk<T> ch(raw);
-    const float mx = ch.largest();
+  // B chunks, kLpThreads apart.  The branches are taken once per call.
+  auto take = [&](auto batch, const uint4* raw, int c) {
+    constexpr int B = decltype(batch)::value;
+    Chunk<T> ch[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u) ch[u] = Chunk<T>(raw[u]);
+    const float mx = Chunk<T>::template largest<B>(ch);
     tm = fmaxf(tm, mx);
     raise(mx);
-    if (m > -1e30f) {
-      float v[N];
-      ch.finite(v);   // a masked logit counts 2^(-3e38 k) = 0
+    if (fabsf(m) < 1e30f) {
 #pragma unroll
-      for (int e = 0; e < N; e += 2) add2(v[e], v[e + 1]);
+      for (int u = 0; u < B; ++u) {
+        float v[N];
+        ch[u].finite(v);   // a masked logit counts 2^(-3e38 k) = 0, at a finite distance from m
+#pragma unroll
+        for (int e = 0; e < N; e += 2) add2(v[e], v[e + 1]);
+      }
     } else {
-      float v[N];
-      ch.values(v);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (v[e] > -INFINITY) add1(v[e]);
-    }
-    const int i0 = head + c * N;
-    if ((unsigned)(tok - i0) < (unsigned)N) {
-      float v[N];
-      ch.values(v);
+      for (int u = 0; u < B; ++u) {
+        float v[N];
+        ch[u].values(v);
 #pragma unroll
-      for (int e = 0; e < N; ++e) cnt += v[e] > xt || (v[e] == xt && i0 + e < tok);
-    } else {
-      cnt += ch.above(i0 < tok ? xt_low : xt);
+        for (int e = 0; e < N; ++e)
+          if (v[e] > -INFINITY) add1(v[e]);
+      }
     }
+    // a chunk that begins before the token counts >= (the token's own is put right below)
+    typename Chunk<T>::Cmp cmp[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u)
+      cmp[u] = c + u * kLpThreads < ctok ? above_low : above_xt;
+    many += Chunk<T>::template above<B>(ch, cmp);
   };
   int c = c0 + tid;
   for (; c + 3 * kLpThreads < c1; c += 4 * kLpThreads) {
     uint4 raw[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) raw[u] = __ldg(&xc[c + u * kLpThreads]);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) take(raw[u], c + u * kLpThreads);
+    take(std::integral_constant<int, 4>{}, raw, c);
   }
-  for (; c < c1; c += kLpThreads) take(__ldg(&xc[c]), c);
+  for (; c < c1; c += kLpThreads) {
+    const uint4 raw = __ldg(&xc[c]);
+    take(std::integral_constant<int, 1>{}, &raw, c);
+  }
+  if (tok > head && tok < tail0) {
+    const int own = (tok - head) / N;   // its chunk counted the equal logits from the token on
+    if (own < ctok && own >= c0 && own < c1 && (own - c0) % kLpThreads == tid) {
+      float v[N];
+      Chunk<T>(__ldg(&xc[own])).values(v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) cnt -= v[e] == xt && head + own * N + e >= tok;
+    }
+  }
   if (has_single) {
     const int i = single_at(tid);
     const float v = Chunk<T>::one(x + i);
@@ -301,7 +352,6 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
       if (lane == 0) sh.lead[warp * kLpLead + j] = top;
       const unsigned who = __ballot_sync(0xffffffffu, left == top);
       if (lane == __ffs(who) - 1) left = 0;
-      if (n <= 1) break;
     }
     float s, t, sb, tb;
     unpair_f32(s2, s, sb);
@@ -314,7 +364,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
       s += __shfl_xor_sync(0xffffffffu, s, o);
       t += __shfl_xor_sync(0xffffffffu, t, o);
     }
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    cnt = __reduce_add_sync(0xffffffffu, cnt + (int)many);
     if (lane == 0) {
       sh.m[warp] = Mw;
       sh.s[warp] = s;
@@ -326,8 +376,8 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   LpShared* first = cluster.map_shared_rank(&sh, 0);
 
-  // the CTA's sums (warp 2) and the bound on its n-th largest logit (warps 0 and 1)
-  if (warp == 2) {
+  // the CTA's sums (last warp) and the bound on its n-th largest logit (first warps)
+  if (warp == kLpWarps - 1) {
     const bool has = lane < kLpWarps;
     float M = has ? sh.m[lane] : -INFINITY, s = has ? sh.s[lane] : 0.f, t = has ? sh.t[lane] : 0.f;
     const float from = M;
@@ -348,15 +398,17 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
     }
   }
   if (n > 0) {
-    const int offered = kLpWarps * (n <= 1 ? 1 : kLpLead), step = n <= 1 ? kLpLead : 1;
-    if (tid < offered) {
-      const uint32_t mine = sh.lead[tid * step];
-      int above = 0;
-      for (int j = 0; j < offered; ++j) {
-        const uint32_t other = sh.lead[j * step];
-        above += other > mine || (other == mine && j < tid);
-      }
-      if (above == n - 1) sh.bound = mine;
+    // the n-th largest of the offered maxima; each warp ranks its own against 32 at a time
+    static_assert(kLpWarps * kLpLead == 64 && kLpLead * 16 >= kMaxTopLogprobs, "two per lane");
+    const uint32_t lead0 = sh.lead[lane], lead1 = sh.lead[32 + lane];
+#pragma unroll
+    for (int j = 0; j < kLpLead; ++j) {
+      const int i = warp * kLpLead + j;
+      const uint32_t mine = __shfl_sync(0xffffffffu, i < 32 ? lead0 : lead1, i & 31);
+      const int above =
+          __popc(__ballot_sync(0xffffffffu, lead0 > mine || (lead0 == mine && lane < i))) +
+          __popc(__ballot_sync(0xffffffffu, lead1 > mine || (lead1 == mine && 32 + lane < i)));
+      if (above == n - 1 && lane == 0) sh.bound = mine;
     }
     __syncthreads();
     const uint32_t bound = sh.bound;
@@ -367,29 +419,43 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
       }
     };
     const bool reaches = tm > -INFINITY && order_of(tm) >= bound;
-    unsigned who = __ballot_sync(0xffffffffu, reaches);
+    const unsigned who = __ballot_sync(0xffffffffu, reaches);
+    if (reaches) sh.owner[warp][__popc(who & ((1u << lane) - 1u))] = (uint8_t)lane;
+    __syncwarp();
     if (reaches && has_single) post(Chunk<T>::one(x + single_at(tid)), single_at(tid));
-    while (who) {   // the warp reads the chunks of one such thread
-      const int owner = tid - lane + __ffs(who) - 1;
-      who &= who - 1;
-      for (int cc = c0 + owner + lane * kLpThreads; cc < c1; cc += 32 * kLpThreads) {
-        const Chunk<T> ch(__ldg(&xc[cc]));
-        if (order_of(ch.largest()) >= bound) {
-          float v[N];
-          ch.values(v);
+    // the warp reads those threads' chunks, four a lane at a time
+    const int each = (c1 - c0 + kLpThreads - 1) / kLpThreads, all = __popc(who) * each;
+    for (int q0 = lane; q0 < all; q0 += 128) {
+      uint4 raw[4];
+      int at[4];
 #pragma unroll
-          for (int e = 0; e < N; ++e) post(v[e], head + cc * N + e);
+      for (int u = 0; u < 4; ++u) {
+        const int q = q0 + 32 * u, o = q / each;
+        at[u] = q < all ? c0 + warp * 32 + sh.owner[warp][o] + (q - o * each) * kLpThreads : c1;
+        if (at[u] < c1) raw[u] = __ldg(&xc[at[u]]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (at[u] >= c1) continue;
+        const Chunk<T> ch[1] = {Chunk<T>(raw[u])};
+        if (order_of(Chunk<T>::template largest<1>(ch)) >= bound) {
+          float v[N];
+          ch[0].values(v);
+#pragma unroll
+          for (int e = 0; e < N; ++e) post(v[e], head + at[u] * N + e);
         }
       }
     }
     __syncthreads();
     const int posted = sh.posted;
     if (posted <= kLpList) {
-      for (int i = tid; i < posted; i += kLpThreads) {
+      for (int i = warp; i < posted; i += kLpWarps) {   // a warp a key
         const unsigned long long mine = sh.list[i];
         int larger = 0;
-        for (int j = 0; j < posted; ++j) larger += sh.list[j] > mine;
-        if (larger < n) first->all[r * n + larger] = mine;
+        for (int j = 0; j < posted; j += 32)
+          larger += __popc(__ballot_sync(0xffffffffu,
+                                         j + lane < posted && sh.list[j + lane] > mine));
+        if (larger < n && lane == 0) first->all[r * n + larger] = mine;
       }
     } else {
       unsigned long long last = ~0ull;
@@ -458,17 +524,21 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
     }
   }
   if (n > 0) {
-    const int mine_at = tid;   // C * n <= 512 = kLpThreads keys
-    static_assert(kMaxLogprobCluster * kMaxTopLogprobs <= kLpThreads, "a thread a key");
-    const unsigned long long mine = mine_at < C * n ? sh.all[mine_at] : 0;
-    int larger = 0;
-    if (mine)
-      for (int j = 0; j < C * n; ++j) larger += sh.all[j] > mine;
-    const int found = __syncthreads_count(mine != 0);
-    if (mine && larger < n) {
-      p.top_ids[size_t(row) * n + larger] = index_of(mine);
-      p.top_logprobs[size_t(row) * n + larger] =
-          (value_of(mine) - sh.row_max) * p.inv_temperature - sh.ln_z;
+    __syncthreads();   // row_max, ln_z
+    int found = 0;
+    for (int j = lane; j < C * n; j += 32) found += sh.all[j] != 0;
+    found = __reduce_add_sync(0xffffffffu, found);
+    for (int i = warp; i < C * n; i += kLpWarps) {
+      const unsigned long long mine = sh.all[i];
+      if (mine == 0) continue;
+      int larger = 0;
+      for (int j = 0; j < C * n; j += 32)
+        larger += __popc(__ballot_sync(0xffffffffu, j + lane < C * n && sh.all[j + lane] > mine));
+      if (larger < n && lane == 0) {
+        p.top_ids[size_t(row) * n + larger] = index_of(mine);
+        p.top_logprobs[size_t(row) * n + larger] =
+            (value_of(mine) - sh.row_max) * p.inv_temperature - sh.ln_z;
+      }
     }
     if (tid >= found && tid < n) {   // fewer than n logits are left
       p.top_ids[size_t(row) * n + tid] = -1;
