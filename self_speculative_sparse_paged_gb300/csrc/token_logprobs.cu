@@ -37,6 +37,8 @@ namespace {
 
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
+// Batches of four chunks a thread asked for in L2 ahead of the loads (2 to 6 measured up to 15 % slower).
+constexpr int kLpAhead = 1;
 constexpr int kLpList = 1024;          // candidate keys a CTA can hold
 constexpr float kLpSlack = 8.f;        // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
@@ -238,6 +240,14 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
     if (tid == 0) set_error(p.err, kErrDeviceFault);
     tok = -1;
   }
+  // One thread asks for the slice in L2 a few batches ahead of the loads.
+  auto ahead = [&](int from, int chunks_wanted) {
+    const int n16 = min(chunks_wanted, c1 - from);
+    if (tid == 0 && n16 > 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(xc + from), "r"(n16 * 16)
+                   : "memory");
+  };
+  ahead(c0, kLpAhead * 4 * kLpThreads);
   const float xt = tok >= 0 ? Chunk<T>::one(x + tok) : INFINITY;
   // x counts when x > xt, or x >= xt at a lower index: there x > (the number
   // below xt), or any x when xt = -inf (compared, unordered, with NaN)
@@ -314,6 +324,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   };
   int c = c0 + tid;
   for (; c + 3 * kLpThreads < c1; c += 4 * kLpThreads) {
+    ahead(c + kLpAhead * 4 * kLpThreads, 4 * kLpThreads);
     uint4 raw[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) raw[u] = __ldg(&xc[c + u * kLpThreads]);
