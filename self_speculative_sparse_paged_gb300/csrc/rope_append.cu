@@ -13,134 +13,171 @@
 // product and the reduction to [-1/2, 1/2] turn are done in fp64, once per
 // (row, pair) and shared by all heads through shared memory; the remainder
 // goes to sine and cosine in fp32.  The rotation is fp32, rounded once to bf16.
+//
+// Memory bounds the call.  A warp takes a row, or with few rows a fourth of one:
+// lane i turns unit i % (rot / 16) (8 pairs) of head i / (rot / 16) and the heads
+// a fixed stride on, so its cosines and sines stay in registers and a head costs
+// two 16-byte loads, 32 multiply-adds and two 16-byte stores, with no barrier
+// between warps.
 #include "kernels.h"
 #include "vegas_common.cuh"
 
 namespace vegas {
 
 namespace {
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 4;        // warps of a block
+constexpr int kRopeBatch = 3;        // heads a lane has in flight
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 }  // namespace
 
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
-  __shared__ float2 cs[64];          // (cos, sin) of each pair
-  __shared__ int where[2];           // sequence, cache position
+// Split: warps that share a row (1 or kRopeWarps).
+template <int Split>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const RopeParams p) {
+  __shared__ float2 cs_all[kRopeWarps][64];   // scaled (cos, sin) of each pair
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = Split == 1 ? blockIdx.x * kRopeWarps + warp : (int)blockIdx.x;
+  const int part = Split == 1 ? 0 : warp;
+  float2* cs = cs_all[warp];
   griddep_begin();
-  const int row = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) where[0] = -1;
-  __syncthreads();
-  for (int s = tid; s < p.batch; s += kRopeThreads) {
-    const int beg = p.row_start[s], end = p.row_start[s + 1];
-    if (end < beg) set_error(p.err, kErrDeviceFault);
-    if (row >= beg && row < end) {
-      const int ctx = p.ctx_lens[s];
-      if (beg < 0 || end > p.total_rows || ctx < 0 ||
-          (long long)ctx + (end - beg) > (long long)p.max_pages * 16) {
-        set_error(p.err, kErrDeviceFault);
-      } else {
-        where[0] = s;
-        where[1] = ctx + (row - beg);
-      }
-    }
+  if (row >= p.total_rows) return;
+
+  // The row's sequence: the last one that begins at or before it, found 32 at a time.
+  int s = 0;
+  for (int n = p.batch; n > 0;) {
+    const int step = (n + 31) >> 5, at = s + lane * step;
+    const bool before = lane * step < n && p.row_start[at] <= row;
+    const unsigned m = __ballot_sync(0xffffffffu, before);
+    if (!m) return;                  // (no sequence begins that early)
+    const int l = 31 - __clz(m);
+    n = min(step, n - l * step);
+    s += l * step;
+    if (step == 1) break;
   }
-  __syncthreads();
-  const int seq = where[0], pos = where[1];
-  if (seq < 0) return;               // a row behind the last sequence
-  const int page = p.block_table[size_t(seq) * p.max_pages + (pos >> 4)];
+  const int beg = p.row_start[s], end = p.row_start[s + 1], ctx = p.ctx_lens[s];
+  if (end < beg) {
+    if (lane == 0) set_error(p.err, kErrDeviceFault);
+    return;
+  }
+  if (row >= end) return;            // a row behind the last sequence
+  if (beg < 0 || end > p.total_rows || ctx < 0 ||
+      (long long)ctx + (end - beg) > (long long)p.max_pages * 16) {
+    if (lane == 0) set_error(p.err, kErrDeviceFault);
+    return;
+  }
+  const int pos = ctx + (row - beg);
+  const int page = p.block_table[size_t(s) * p.max_pages + (pos >> 4)];
   const bool page_ok = page >= 0 && page < p.num_pages;
-  if (!page_ok && tid == 0) set_error(p.err, kErrDeviceFault);
-  const int half = p.rot >> 1;
-  if (tid < half) {
+  if (!page_ok && lane == 0) set_error(p.err, kErrDeviceFault);
+
+  const int D = p.head_dim, half = p.rot >> 1;
+  for (int j = lane; j < half; j += 32) {
     int at = pos;
     if (p.positions) {
-      int a = p.pair_axis ? p.pair_axis[tid] : 0;
-      if (a < 0 || a >= p.num_axes) {
+      int axis = p.pair_axis ? p.pair_axis[j] : 0;
+      if (axis < 0 || axis >= p.num_axes) {
         set_error(p.err, kErrDeviceFault);
-        a = 0;
+        axis = 0;
       }
-      at = p.positions[size_t(a) * p.total_rows + row];
+      at = p.positions[size_t(axis) * p.total_rows + row];
     }
-    double turns = double(at) * double(p.inv_freq[tid]) * 0.15915494309189533577;   // 1 / (2 pi)
+    double turns = double(at) * double(p.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
     turns -= rint(turns);
     float sn, cn;
     sincospif(2.f * float(turns), &sn, &cn);
-    cs[tid] = make_float2(cn * p.scale, sn * p.scale);
+    cs[j] = make_float2(cn * p.scale, sn * p.scale);
   }
-  __syncthreads();
+  __syncwarp();
 
-  const int D = p.head_dim, hr = p.hq + p.hkv;
-  const int pc = half >> 3;                 // units of 8 pairs per head
-  const int rest = (D - p.rot) >> 3;        // 16-byte chunks per head that pass through
-  const int n_rot = hr * pc, n_pass = hr * rest, n_v = p.hkv * (D >> 3);
   const uint16_t* qrow = reinterpret_cast<const uint16_t*>(p.q) + size_t(row) * p.q_stride;
   const uint16_t* krow = reinterpret_cast<const uint16_t*>(p.k) + size_t(row) * p.k_stride;
   const uint16_t* vrow = reinterpret_cast<const uint16_t*>(p.v) + size_t(row) * p.v_stride;
   uint16_t* qout = reinterpret_cast<uint16_t*>(p.q_out) + size_t(row) * p.hq * D;
-  auto cache_row = [&](void* cache, int g) {
-    return reinterpret_cast<uint16_t*>(cache) +
-           ((size_t(page) * p.hkv + g) * 16 + (pos & 15)) * D;
-  };
-  for (int i = tid; i < n_rot + n_pass + n_v; i += kRopeThreads) {
-    if (i < n_rot) {
-      const int h = i / pc, u = i - h * pc;
-      const bool is_q = h < p.hq;
-      if (!is_q && !page_ok) continue;
-      const uint16_t* src = is_q ? qrow + h * D : krow + (h - p.hq) * D;
-      uint16_t* dst = is_q ? qout + h * D : cache_row(p.k_cache, h - p.hq);
-      const int o0 = p.interleaved ? 16 * u : 8 * u, o1 = p.interleaved ? o0 + 8 : o0 + half;
-      const uint4 A = *reinterpret_cast<const uint4*>(src + o0);
-      const uint4 B = *reinterpret_cast<const uint4*>(src + o1);
-      const uint32_t a[4] = {A.x, A.y, A.z, A.w}, b[4] = {B.x, B.y, B.z, B.w};
-      uint32_t ra[4], rb[4];
-      if (p.interleaved) {
+  const size_t slot = (size_t(page_ok ? page : 0) * p.hkv * 16 + (pos & 15)) * D;
+  uint16_t* kslot = reinterpret_cast<uint16_t*>(p.k_cache) + slot;
+  uint16_t* vslot = reinterpret_cast<uint16_t*>(p.v_cache) + slot;
+  const int heads = page_ok ? p.hq + p.hkv : p.hq;   // (a key without a page goes nowhere)
+  auto source = [&](int h) { return h < p.hq ? qrow + h * D : krow + (h - p.hq) * D; };
+  auto target = [&](int h) { return h < p.hq ? qout + h * D : kslot + (h - p.hq) * 16 * D; };
+
+  if (p.rot > 0) {
+    const int units = p.rot >> 4, per_pass = 32 / units, hl = lane / units, u = lane - hl * units;
+    const int o0 = p.interleaved ? 16 * u : 8 * u, o1 = p.interleaved ? o0 + 8 : o0 + half;
+    float2 c[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = unpack_bf16x2(a[e]), y = unpack_bf16x2(b[e]);
-          const float2 c0 = cs[8 * u + e], c1 = cs[8 * u + 4 + e];
-          ra[e] = pack_bf16x2(x.x * c0.x - x.y * c0.y, x.y * c0.x + x.x * c0.y);
-          rb[e] = pack_bf16x2(y.x * c1.x - y.y * c1.y, y.y * c1.x + y.x * c1.y);
-        }
-      } else {
+    for (int e = 0; e < 8; ++e) c[e] = cs[8 * u + e];
+    const int h0 = hl < per_pass ? hl + part * per_pass : heads, stride = per_pass * Split;
+    for (int h = h0; h < heads; h += kRopeBatch * stride) {
+      uint4 A[kRopeBatch], B[kRopeBatch];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = unpack_bf16x2(a[e]), y = unpack_bf16x2(b[e]);
-          const float2 c0 = cs[8 * u + 2 * e], c1 = cs[8 * u + 2 * e + 1];
-          ra[e] = pack_bf16x2(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
-          rb[e] = pack_bf16x2(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
-        }
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int hh = h + i * stride;
+        if (hh >= heads) continue;
+        const uint16_t* src = source(hh);
+        A[i] = *reinterpret_cast<const uint4*>(src + o0);
+        B[i] = *reinterpret_cast<const uint4*>(src + o1);
       }
-      *reinterpret_cast<uint4*>(dst + o0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-      *reinterpret_cast<uint4*>(dst + o1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
-    } else if (i < n_rot + n_pass) {
-      const int k = i - n_rot, h = k / rest, c = p.rot + 8 * (k - h * rest);
-      const bool is_q = h < p.hq;
-      if (!is_q && !page_ok) continue;
-      const uint16_t* src = is_q ? qrow + h * D : krow + (h - p.hq) * D;
-      uint16_t* dst = is_q ? qout + h * D : cache_row(p.k_cache, h - p.hq);
-      *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-    } else if (page_ok) {
-      const int k = i - n_rot - n_pass, per = D >> 3, g = k / per, c = 8 * (k - g * per);
-      *reinterpret_cast<uint4*>(cache_row(p.v_cache, g) + c) =
-          *reinterpret_cast<const uint4*>(vrow + g * D + c);
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int hh = h + i * stride;
+        if (hh >= heads) continue;
+        uint32_t a[4] = {A[i].x, A[i].y, A[i].z, A[i].w}, b[4] = {B[i].x, B[i].y, B[i].z, B[i].w};
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack_bf16x2(a[e]), y = unpack_bf16x2(b[e]);
+            a[e] = pack_bf16x2(x.x * c[e].x - x.y * c[e].y, x.y * c[e].x + x.x * c[e].y);
+            b[e] = pack_bf16x2(y.x * c[4 + e].x - y.y * c[4 + e].y,
+                               y.y * c[4 + e].x + y.x * c[4 + e].y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack_bf16x2(a[e]), y = unpack_bf16x2(b[e]);
+            const float2 p0 = c[2 * e], p1 = c[2 * e + 1];
+            a[e] = pack_bf16x2(x.x * p0.x - y.x * p0.y, x.y * p1.x - y.y * p1.y);
+            b[e] = pack_bf16x2(y.x * p0.x + x.x * p0.y, y.y * p1.x + x.y * p1.y);
+          }
+        }
+        uint16_t* dst = target(hh);
+        *reinterpret_cast<uint4*>(dst + o0) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4*>(dst + o1) = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+  }
+  const int first = lane + 32 * part, step = 32 * Split;
+  const int rest = (D - p.rot) >> 3;   // 16-byte chunks of a head that pass through
+  for (int i = first; i < heads * rest; i += step) {
+    const int h = i / rest, o = p.rot + 8 * (i - h * rest);
+    *reinterpret_cast<uint4*>(target(h) + o) = *reinterpret_cast<const uint4*>(source(h) + o);
+  }
+  if (page_ok) {
+    const int shift = D == 128 ? 4 : 3;   // chunks of a value head
+#pragma unroll 4
+    for (int i = first; i < p.hkv << shift; i += step) {
+      const int g = i >> shift, o = 8 * (i - (g << shift));
+      *reinterpret_cast<uint4*>(vslot + g * 16 * D + o) =
+          *reinterpret_cast<const uint4*>(vrow + g * D + o);
     }
   }
 }
 
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
+  // A warp a row once the rows fill the SMs' warps.
+  const bool split = p.total_rows < 2048;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.total_rows, 1, 1);
-  cfg.blockDim = dim3(kRopeThreads, 1, 1);
+  cfg.gridDim = dim3(split ? p.total_rows : (p.total_rows + kRopeWarps - 1) / kRopeWarps, 1, 1);
+  cfg.blockDim = dim3(32 * kRopeWarps, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel, p);
+  return split ? cudaLaunchKernelEx(&cfg, rope_append_kernel<kRopeWarps>, p)
+               : cudaLaunchKernelEx(&cfg, rope_append_kernel<1>, p);
 }
 
 }  // namespace vegas
