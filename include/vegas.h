@@ -293,9 +293,10 @@ vegas_status_t vegas_decode_iteration(
  * (n_b of them, possibly none), row t of it at cache position
  * ctx_lens[b] + t.  row_start is device int32 [batch + 1], ascending;
  * total_rows is the number of rows in the tensors, at least row_start[batch]:
- * rows behind the last sequence are neither read nor written.  Needs
+ * rows behind the last sequence may hold anything and are never written.  Needs
  * 0 <= ctx_lens[b] and ctx_lens[b] + n_b <= 16 * max_pages_per_seq; a sequence
- * that breaks this is recorded as a device fault and skipped.  total_rows < 2^24.
+ * with rows that breaks this is recorded as a device fault and skipped.
+ * total_rows < 2^24.
  *
  * vegas_rope_append turns the query and key heads of every row by their
  * positions and appends keys and values to the cache.  Pair j < rot_dim / 2

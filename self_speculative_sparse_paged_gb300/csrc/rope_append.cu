@@ -26,23 +26,48 @@ namespace vegas {
 
 namespace {
 constexpr int kRopeWarps = 4;        // warps of a block
-constexpr int kRopeBatch = 3;        // heads a lane has in flight
+constexpr int Batch = 2;        // heads a lane has in flight
+
+constexpr int kRopeOneWarp = 6000, kRopeTwoWarps = 2000;
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 }  // namespace
 
-// Split: warps that share a row (1 or kRopeWarps).
-template <int Split>
+// Split: warps that share a row (1, 2 or kRopeWarps); Batch: heads a lane has in flight.
+template <int Split, int Batch>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs_all[kRopeWarps][64];   // scaled (cos, sin) of each pair
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = Split == 1 ? blockIdx.x * kRopeWarps + warp : (int)blockIdx.x;
-  const int part = Split == 1 ? 0 : warp;
+  const int row = blockIdx.x * (kRopeWarps / Split) + warp / Split, part = warp % Split;
   float2* cs = cs_all[warp];
   griddep_begin();
   if (row >= p.total_rows) return;
+
+  const uint16_t* qrow = reinterpret_cast<const uint16_t*>(p.q) + size_t(row) * p.q_stride;
+  const uint16_t* krow = reinterpret_cast<const uint16_t*>(p.k) + size_t(row) * p.k_stride;
+  const uint16_t* vrow = reinterpret_cast<const uint16_t*>(p.v) + size_t(row) * p.v_stride;
+  const int D = p.head_dim, half = p.rot >> 1;
+  auto source = [&](int h) { return h < p.hq ? qrow + h * D : krow + (h - p.hq) * D; };
+  // the lane's unit, its two chunks of a head, its first head and the step to the next
+  const int units = p.rot >> 4, per_pass = units ? 32 / units : 0, hl = units ? lane / units : 0;
+  const int u = lane - hl * units, o0 = p.interleaved ? 16 * u : 8 * u;
+  const int o1 = p.interleaved ? o0 + 8 : o0 + half;
+  const int all_heads = p.hq + p.hkv, stride = per_pass * Split;
+  const int h0 = hl < per_pass ? hl + part * per_pass : all_heads;
+  uint4 A[Batch], B[Batch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < Batch; ++i) {
+      const int hh = h + i * stride;
+      if (hh >= all_heads) continue;
+      const uint16_t* src = source(hh);
+      A[i] = *reinterpret_cast<const uint4*>(src + o0);
+      B[i] = *reinterpret_cast<const uint4*>(src + o1);
+    }
+  };
+  if (units) load(h0);   // the first heads are on their way under the lookups below
 
   // The row's sequence: the last one that begins at or before it, found 32 at a time.
   int s = 0;
@@ -72,7 +97,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
   const bool page_ok = page >= 0 && page < p.num_pages;
   if (!page_ok && lane == 0) set_error(p.err, kErrDeviceFault);
 
-  const int D = p.head_dim, half = p.rot >> 1;
   for (int j = lane; j < half; j += 32) {
     int at = pos;
     if (p.positions) {
@@ -91,36 +115,21 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
   }
   __syncwarp();
 
-  const uint16_t* qrow = reinterpret_cast<const uint16_t*>(p.q) + size_t(row) * p.q_stride;
-  const uint16_t* krow = reinterpret_cast<const uint16_t*>(p.k) + size_t(row) * p.k_stride;
-  const uint16_t* vrow = reinterpret_cast<const uint16_t*>(p.v) + size_t(row) * p.v_stride;
   uint16_t* qout = reinterpret_cast<uint16_t*>(p.q_out) + size_t(row) * p.hq * D;
   const size_t slot = (size_t(page_ok ? page : 0) * p.hkv * 16 + (pos & 15)) * D;
   uint16_t* kslot = reinterpret_cast<uint16_t*>(p.k_cache) + slot;
   uint16_t* vslot = reinterpret_cast<uint16_t*>(p.v_cache) + slot;
-  const int heads = page_ok ? p.hq + p.hkv : p.hq;   // (a key without a page goes nowhere)
-  auto source = [&](int h) { return h < p.hq ? qrow + h * D : krow + (h - p.hq) * D; };
+  const int heads = page_ok ? all_heads : p.hq;   // (a key without a page goes nowhere)
   auto target = [&](int h) { return h < p.hq ? qout + h * D : kslot + (h - p.hq) * 16 * D; };
 
   if (p.rot > 0) {
-    const int units = p.rot >> 4, per_pass = 32 / units, hl = lane / units, u = lane - hl * units;
-    const int o0 = p.interleaved ? 16 * u : 8 * u, o1 = p.interleaved ? o0 + 8 : o0 + half;
     float2 c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e] = cs[8 * u + e];
-    const int h0 = hl < per_pass ? hl + part * per_pass : heads, stride = per_pass * Split;
-    for (int h = h0; h < heads; h += kRopeBatch * stride) {
-      uint4 A[kRopeBatch], B[kRopeBatch];
+    for (int h = h0; h < heads; h += Batch * stride) {
+      if (h != h0) load(h);
 #pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const int hh = h + i * stride;
-        if (hh >= heads) continue;
-        const uint16_t* src = source(hh);
-        A[i] = *reinterpret_cast<const uint4*>(src + o0);
-        B[i] = *reinterpret_cast<const uint4*>(src + o1);
-      }
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
+      for (int i = 0; i < Batch; ++i) {
         const int hh = h + i * stride;
         if (hh >= heads) continue;
         uint32_t a[4] = {A[i].x, A[i].y, A[i].z, A[i].w}, b[4] = {B[i].x, B[i].y, B[i].z, B[i].w};
@@ -165,10 +174,13 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
 }
 
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
-  // A warp a row once the rows fill the SMs' warps.
-  const bool split = p.total_rows < 2048;
+  // Warps a row: one when the rows alone keep the SMs busy, else two, else four (32 query and
+  // 8 KV heads of 128: 1000 rows 11.6 / 8.3 / 6.7 us, 2000 rows 14.6 / 13.1 / 14.5 us, 4000 rows
+  // 20.7 / 22.0 / 24.3 us with one / two / four).
+  const int split = p.total_rows >= 3000 ? 1 : p.total_rows >= 1500 ? 2 : kRopeWarps;
+  const int rows = kRopeWarps / split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split ? p.total_rows : (p.total_rows + kRopeWarps - 1) / kRopeWarps, 1, 1);
+  cfg.gridDim = dim3((p.total_rows + rows - 1) / rows, 1, 1);
   cfg.blockDim = dim3(32 * kRopeWarps, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -176,8 +188,13 @@ cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return split ? cudaLaunchKernelEx(&cfg, rope_append_kernel<kRopeWarps>, p)
-               : cudaLaunchKernelEx(&cfg, rope_append_kernel<1>, p);
+  // Heads in flight: four of 64, two of 128 (3021 rows of 64: 15.1 us against 17.2 with two;
+  // 32768 rows of 128: 131 us against 128 with four).
+  if (split == 1)
+    return p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, rope_append_kernel<1, 4>, p)
+                            : cudaLaunchKernelEx(&cfg, rope_append_kernel<1, 2>, p);
+  if (split == 2) return cudaLaunchKernelEx(&cfg, rope_append_kernel<2, 2>, p);
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<kRopeWarps, 3>, p);
 }
 
 }  // namespace vegas
