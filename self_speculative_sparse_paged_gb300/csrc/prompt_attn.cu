@@ -46,6 +46,7 @@ constexpr int kPThreads = 384;
 constexpr int kTile = 128;            // KV positions per tile, query rows per tile
 constexpr int kItemCost = 256;        // an item's fixed cost, in positions
 constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
+constexpr int kFewRows = 32;          // an item of at most so many rows is shared by A and B (and joined by any thread)
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
 // Parts of a tile whose P goes to the tensor cores by itself.  (Four parts: 16K prompt 10 % slower.)
@@ -60,6 +61,7 @@ struct Piece {
   int k0, k1;          // KV tiles of this piece
   int na, nb;          // KV tiles that query tiles A and B need
   int first, last;     // CTAs that share the item
+  int alt;             // 1: few rows, all in tile A: A and B take its KV tiles in turn
 };
 constexpr int kPieces = 4;   // depth of the ring of published items
 
@@ -71,10 +73,12 @@ struct PCfg {
   static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 1 + 2 * kPieces + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 1 + 2 * kPieces + 2 + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
-  static constexpr size_t kSmem = kOffPieces + kPieces * sizeof(Piece) + 1024;
+  static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
+  static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
+  static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
   static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
 };
 
@@ -297,6 +301,8 @@ struct Walk {
     w.k0 = 0;
     w.k1 = max(w.na, w.nb);
     w.first = w.last = blockIdx.x;
+    // (for the whole item, so that all its CTAs count the same partial states)
+    w.alt = w.nb == 0 && w.na >= 4 && (sq.n - w.tok0) * q.group <= kFewRows;
   }
 
   // Items dealt out whole, longest first, back and forth over the CTAs.
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto pvpart = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
   const uint32_t qfull = bar0 + 8 * (B1 + 4), qfree = bar0 + 8 * (B1 + 5);
   const uint32_t drain = bar0 + 8 * (B1 + 6);
+  const uint32_t altfull = bar0 + 8 * (B1 + 7 + 2 * kPieces), alttaken = altfull + 8;
   auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + i); };
   auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
@@ -398,6 +405,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
   Division* division = reinterpret_cast<Division*>(smem + Cfg::kOffMisc + 64);
   int* failed = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 96);        // [2]
+  float2* alt_ml = reinterpret_cast<float2*>(smem + Cfg::kOffAlt);
   Piece* pieces = reinterpret_cast<Piece*>(smem + Cfg::kOffPieces);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -416,6 +424,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     mbar_init(qfull, 1);
     mbar_init(qfree, 1);
     mbar_init(drain, 1);
+    mbar_init(altfull, 32);
+    mbar_init(alttaken, 32);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(pcfull(i), 1);
       mbar_init(pcfree(i), 11);   // one arrival per reading warp
@@ -474,10 +484,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   };
   Piece w;
   bool ok = true;
-  // 384 threads launch with 168 registers each: 2 x 128 x 208 + 128 x 80 fit in that.
+  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
   // (Set inside each role's branch: where the branches join the smaller count would rule.)
   if (warp == 8 || warp == 9) {
-    leave_registers<80>();
+    leave_registers<72>();
     // ------------------------------------------------------------ K (8) and V (9) tiles
     // Lane j < 8 * D/64 issues box (page j % 8, half j / 8): 16 positions x 64 dims.
     const bool is_v = warp == 9;
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   } else if (warp == 11) {
-    leave_registers<80>();
+    leave_registers<72>();
     // ------------------------------------------------------------ items, Q tiles
     auto point = [&](int e0) {
       const int* e = ends + 6 * e0;
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (c > 0) (void)mbar_wait_bounded(qfull, (c - 1) & 1);   // landed before the CTA ends
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   } else if (warp == 10) {
-    leave_registers<80>();
+    leave_registers<72>();
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
@@ -587,8 +597,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     };
     auto wait_slot = [&](uint32_t j) { return wait_all(full(j % NS), (j / NS) & 1); };
     auto slot16 = [&](uint32_t j) { return (sbase + Cfg::kOffRing + (j % NS) * Cfg::kSlot) >> 4; };
-    auto issue_s = [&](int x, uint32_t jk) {
-      const uint32_t a = (sbase + x * Cfg::kQ) >> 4, b = slot16(jk);
+    auto issue_s = [&](int x, int qtile, uint32_t jk) {
+      const uint32_t a = (sbase + qtile * Cfg::kQ) >> 4, b = slot16(jk);
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
@@ -622,8 +632,57 @@ __global__ void __launch_bounds__(kPThreads, 1)
         break;
       }
       tc_fence_after();
-      if (w.k0 < ea) issue_s(0, 2 * c);
-      if (w.k0 < eb) issue_s(1, 2 * c);
+      if (w.alt) {
+        // tile i to A or B in turn, each with its own S, P and O, both from query tile A
+        const int tiles = w.k1 - w.k0;
+        for (int i = 0; i < min(2, tiles) && ok; ++i) {
+          const uint32_t jk = 2 * (c + i);
+          if (!wait_slot(jk)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          issue_s(i, 0, jk);
+          commit(freed(jk % NS));
+        }
+        if (tiles <= 2) commit(qfree);
+        for (int i = 0; i < tiles && ok; ++i) {
+          const int x = i & 1;
+          const uint32_t jv = 2 * (c + i) + 1, jk = 2 * (c + i) + 4;
+          if (!wait_slot(jv)) {
+            ok = false;
+            break;
+          }
+          for (int h = 0; h < kParts; ++h) {
+            if (!wait_all(pready(x, h), (x ? npb : npa) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(x, h, jv, i >= 2);
+            if (h + 1 < kParts) commit(pvpart(x));
+          }
+          if (!ok) break;
+          x ? ++npb : ++npa;
+          if (i + 2 >= tiles) commit(odone(x));
+          commit(freed(jv % NS));
+          if (i + 2 < tiles) {
+            if (!wait_slot(jk)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_s(x, 0, jk);
+            commit(freed(jk % NS));
+            if (i + 3 == tiles) commit(qfree);
+          }
+        }
+        c += tiles;
+        ++items;
+        continue;
+      }
+      if (w.k0 < ea) issue_s(0, 0, 2 * c);
+      if (w.k0 < eb) issue_s(1, 1, 2 * c);
       commit(freed((2 * c) % NS));
       if (w.k0 + 1 == w.k1) commit(qfree);
       for (int t = w.k0; t < w.k1 && ok; ++t, ++c) {
@@ -658,7 +717,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             have_k = true;
             tc_fence_after();
-            issue_s(x, jk);
+            issue_s(x, x, jk);
           }
         }
         if (ok && more) {
@@ -674,25 +733,43 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncwarp();
     (void)mbar_wait_bounded(drain, 0);
   } else {
-    take_registers<208>();
+    take_registers<216>();
     // ------------------------------------------------------------ softmax of tile X
     const int x = warp >> 2;
     const int r = tid & 127;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
-    const int tok_r = r / q.group;
-    const int head_r = r - tok_r * q.group;
     uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
-    while (ok && next_piece(w, ok)) {
-      const int first_tok = w.tok0 + x * q.tile_tokens;
-      const int kend = min(w.k1, (x ? w.nb : w.na));
-      const int kv_len = w.ctx + w.n;
-      // the last position this row may see (rows behind the sequence: its last)
-      const int lim = w.ctx + min(first_tok + tok_r, w.n - 1);
-      const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;   // rows 0 .. rows - 1 exist
-      const bool live = r < rows;
+    uint32_t nalt = 0;                // items that A and B shared
+    // The item's fields stay in shared memory until its end: the tile loop needs the registers.
+    auto release = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pcfree(pc % kPieces));
+      ++pc;
+    };
+    while (ok) {
+      const Piece& w = pieces[pc % kPieces];
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(pcfull(pc % kPieces), (pc / kPieces) & 1))) {
+        ok = false;
+        break;
+      }
+      if (w.seq < 0) break;
+      const int kbeg = w.k0 + (w.alt ? x : 0), kstep = w.alt ? 2 : 1;
+      const int kend = w.alt ? w.k1 : min(w.k1, (x ? w.nb : w.na));
+      // lim: the last position this row may see (rows behind the sequence: its last);
+      // seen: the last one that all rows of the tile may; vzero: the tile whose V this group mends
+      int lim, seen, vzero;
+      bool live;   // rows 0 .. rows - 1 of the tile exist
+      {
+        const int first_tok = w.tok0 + (w.alt ? 0 : x * q.tile_tokens);
+        lim = w.ctx + min(first_tok + r / q.group, w.n - 1);
+        seen = w.ctx + first_tok;
+        live = r < min(q.tile_tokens, w.n - first_tok) * q.group;
+        vzero = (w.ctx + w.n) % kTile ? (w.ctx + w.n) / kTile : -1;
+        if (!w.alt && x == 1 && vzero < w.na) vzero = -1;
+      }
       float m = kNoMax, l = 0.f;
-      for (int t = w.k0; t < kend; ++t) {
+      for (int t = kbeg; t < kend; t += kstep) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(sfull(x), ns & 1))) {
           ok = false;
           break;
@@ -701,7 +778,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc_fence_after();
         float s[128];
         const int pos0 = t * kTile;
-        const bool diagonal = pos0 + kTile - 1 > w.ctx + first_tok;
+        const bool diagonal = pos0 + kTile - 1 > seen;
         const int cut = lim - pos0;   // the row's last visible position in the tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
@@ -711,15 +788,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int i = 0; i < 128; ++i)
             if (i > cut) s[i] = -INFINITY;
         }
-        if (t == w.k0) {
+        if (t == kbeg) {
           float mx = s[0];
 #pragma unroll
           for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
           m = fmaxf(mx * q.scale_log2, kNoMax);
         }
-        if (pos0 + kTile > kv_len && (x == 0 || t >= w.na)) {
+        if (t == vzero) {
           // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
           const uint32_t j = 2 * (c + (t - w.k0)) + 1;
+          const int kv_len = w.ctx + w.n;
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(j % NS), (j / NS) & 1));
           if (ok && pos0 + r >= kv_len) {
             uint8_t* row = smem + Cfg::kOffRing + (j % NS) * Cfg::kSlot + r * 128;
@@ -769,7 +847,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (h > 0)
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvpart(x), (ns - 1) & 1)) && ok;
             tc_fence_after();
-            if (t > w.k0 || h > 0) {
+            if (t > kbeg || h > 0) {
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 float o[16];
@@ -793,12 +871,46 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (!ok) break;
       }
       c += w.k1 - w.k0;
-      const bool any = kend > w.k0;
+      const bool any = kend > kbeg;
       if (any) {
         if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1))) ok = false;
         ++no;
         tc_fence_after();
       }
+      if (w.alt && (warp & 3) == 0) {
+        // The item's rows lie in tensor-memory lanes 0-31, which both groups' first warps
+        // reach: B's tells its (m, l), A's joins O_B to O_A and says when it has read it.
+        if (x == 1) {
+          alt_ml[lane] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(altfull);
+          if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(alttaken, nalt & 1))) ok = false;
+        } else {
+          if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(altfull, nalt & 1))) ok = false;
+          tc_fence_after();
+          if (ok && w.k1 - w.k0 > 1) {
+            const float2 b = alt_ml[lane];
+            const float m2 = fmaxf(m, b.x), fa = ex2(m - m2), fb = ex2(b.x - m2);
+            m = m2;
+            l = fa * l + fb * b.y;
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              float oa[16], ob[16];
+              tmem_ld16(tl + Cfg::kO + 16 * i, oa);
+              tmem_ld16(tl + Cfg::kO + D + 16 * i, ob);
+              tmem_ld_wait();
+              uint32_t o[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(fa * oa[e] + fb * ob[e]);
+              tmem_st16(tl + Cfg::kO + 16 * i, o);
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(alttaken);
+        }
+      }
+      if (w.alt) ++nalt;
       // a wait that ran out in one warp ends all four, which share the barriers below
       if (!ok) failed[x] = 1;
       named_bar(1 + x, 128);
@@ -806,7 +918,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ok = false;
         break;
       }
-      if ((x ? w.nb : w.na) == 0) continue;   // no such rows
+      if ((x ? w.nb : w.na) == 0) {   // no such rows, or joined to A's
+        release();
+        continue;
+      }
+      const int first_tok = w.tok0 + (w.alt ? 0 : x * q.tile_tokens);
+      const int rows = min(q.tile_tokens, w.n - first_tok) * q.group;
       __nv_bfloat16* out0 = reinterpret_cast<__nv_bfloat16*>(q.out) +
                             ((size_t(w.row0) + first_tok) * q.hq + size_t(w.g) * q.group) * D;
       auto out_row = [&](int rr) {
@@ -815,7 +932,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       };
       if (w.first == w.last) {
         const float inv = 1.f / l;
-        __nv_bfloat16* o_row = out0 + (size_t(tok_r) * q.hq + head_r) * D;
+        __nv_bfloat16* o_row = out_row(r);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
@@ -833,15 +950,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
         tc_fence_before();
+        release();
         continue;
       }
       // A partial item.  Slot 2 * CTA + 1 holds the piece that the CTA leaves
       // unfinished, slot 2 * CTA the end of an item begun by an earlier CTA;
-      // O as [D / 4][128 rows] float4.
+      // O as [D / 4][128 rows] float4.  Whoever arrives last joins the states,
+      // in their fixed order.
       const int first = w.first, last = w.last, me = blockIdx.x;
-      auto slot_of = [&](int cta) { return (2 * cta + (cta == last ? 0 : 1)) * 2 + x; };
-      {
-        float4* po = reinterpret_cast<float4*>(q.part_o) + size_t(slot_of(me)) * (D / 4) * 128;
+      auto slot_of = [&](int cta, int tile) { return (2 * cta + (cta == last ? 0 : 1)) * 2 + tile; };
+      int* ticket = &q.tickets[2 * first + x];
+      const int arrivals = last - first + 1;
+      const float2* ml = reinterpret_cast<const float2*>(q.part_ml);
+      const float4* po = reinterpret_cast<const float4*>(q.part_o);
+      auto leave = [&]() {   // this state, for whoever joins them
+        float4* dst = reinterpret_cast<float4*>(q.part_o) + size_t(slot_of(me, x)) * (D / 4) * 128;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
@@ -855,63 +978,132 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (live) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              po[(8 * i + e) * 128 + r] =
+              dst[(8 * i + e) * 128 + r] =
                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-        tc_fence_before();
         if (live)
-          reinterpret_cast<float2*>(q.part_ml)[size_t(slot_of(me)) * 128 + r] = make_float2(m, l);
-      }
-      __threadfence();
-      named_bar(1 + x, 128);
-      if (r == 0) flags[x] = atomicAdd(&q.tickets[2 * first + x], 1) == last - first;
-      named_bar(1 + x, 128);
-      if (flags[x]) {
+          reinterpret_cast<float2*>(q.part_ml)[size_t(slot_of(me, x)) * 128 + r] =
+              make_float2(m, l);
         __threadfence();
-        const float2* ml = reinterpret_cast<const float2*>(q.part_ml);
-        const float4* po = reinterpret_cast<const float4*>(q.part_o);
-        // thread r: row r % rows, every sub-th float4 of it, eight in flight at a time
-        const int subs = 128 / rows, rr = r % rows, sub = r / rows;
-        if (sub < subs) {
-          float mm = kNoMax;
+        named_bar(1 + x, 128);
+        if (r == 0) flags[x] = atomicAdd(ticket, 1) == arrivals - 1;
+        named_bar(1 + x, 128);
+      };
+      if (rows <= kFewRows) {
+        leave();
+        if (flags[x]) {
+          __threadfence();
+          // thread r: row r % rows, every sub-th float4 of it, four states in flight
+          const int subs = 128 / rows, rr = r % rows, sub = r / rows;
+          if (sub < subs) {
+            float mm = kNoMax;
+#pragma unroll 4
+            for (int cc = first; cc <= last; ++cc)
+              mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x);
+            __nv_bfloat16* o_row = out_row(rr);
+#pragma unroll 1
+            for (int d4 = sub; d4 < D / 4; d4 += subs) {
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+              float lsum = 0.f;
+#pragma unroll 4
+              for (int cc = first; cc <= last; ++cc) {
+                const size_t sl = slot_of(cc, x);
+                const float2 v = __ldcg(&ml[sl * 128 + rr]);
+                const float4 o = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
+                const float f = ex2(v.x - mm);
+                lsum = fmaf(f, v.y, lsum);
+                acc.x = fmaf(f, o.x, acc.x);
+                acc.y = fmaf(f, o.y, acc.y);
+                acc.z = fmaf(f, o.z, acc.z);
+                acc.w = fmaf(f, o.w, acc.w);
+              }
+              const float inv = 1.f / lsum;
+              *reinterpret_cast<uint2*>(o_row + 4 * d4) =
+                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                             pack_bf16x2(acc.z * inv, acc.w * inv));
+            }
+          }
+          if (r == 0) *ticket = 0;
+        }
+      } else {
+        // Many rows, a thread each: the last one to arrive takes its own state from
+        // tensor memory, and need not leave it at all where the others are done.
+        if (r == 0) flags[x] = *reinterpret_cast<volatile int*>(ticket) == arrivals - 1;
+        named_bar(1 + x, 128);
+        const bool done = flags[x];
+        named_bar(1 + x, 128);
+        if (!done) leave();
+        if (done || flags[x]) {
+          __threadfence();
+          const int rr = live ? r : 0;
+          float mm = m, lsum = 0.f;
           for (int cc = first; cc <= last; ++cc)
-            mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]).x);
+            if (cc != me) mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x);
+          for (int cc = first; cc <= last; ++cc) {
+            const float2 v = cc == me ? make_float2(m, l) : __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]);
+            lsum = fmaf(ex2(v.x - mm), v.y, lsum);
+          }
+          const float inv = 1.f / lsum;
           __nv_bfloat16* o_row = out_row(rr);
-          for (int d0 = sub; d0 < D / 4; d0 += 8 * subs) {
-            float4 acc[8];
+          const int others = last - first;
+          auto other = [&](int j) { return first + j + (first + j >= me ? 1 : 0); };
+          float4 next[4];
+          auto fetch = [&](int i, int j) {   // columns 16 i .. of the j-th other state
+            const float4* src = po + size_t(slot_of(other(j), x)) * (D / 4) * 128 + rr;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            float lsum = 0.f;
-            for (int cc = first; cc <= last; ++cc) {
-              const float2 v = __ldcg(&ml[size_t(slot_of(cc)) * 128 + rr]);
-              const float4* src = po + size_t(slot_of(cc)) * (D / 4) * 128 + rr;
-              float4 o[8];
+            for (int e = 0; e < 4; ++e) next[e] = __ldcg(&src[(4 * i + e) * 128]);
+          };
+          fetch(0, 0);
+          const float fo = any ? ex2(m - mm) : 0.f;
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            float o[16], acc[16];
+            if (any) {
+              tmem_ld16(tl + ocol + 16 * i, o);
+              tmem_ld_wait();
+            }
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                o[i] = __ldcg(&src[min(d0 + i * subs, D / 4 - 1) * 128]);
-              const float f = ex2(v.x - mm);
-              lsum += f * v.y;
+            for (int e = 0; e < 16; ++e) {
+              if (!any) o[e] = 0.f;
+              acc[e] = me == first ? fmaf(fo, o[e], 0.f) : 0.f;
+            }
+#pragma unroll 1
+            for (int j = 0; j < others; ++j) {
+              float4 v[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                acc[i].x += f * o[i].x;
-                acc[i].y += f * o[i].y;
-                acc[i].z += f * o[i].z;
-                acc[i].w += f * o[i].w;
+              for (int e = 0; e < 4; ++e) v[e] = next[e];
+              const int cc = other(j);
+              if (j + 1 < others)
+                fetch(i, j + 1);
+              else if (i + 1 < D / 16)
+                fetch(i + 1, 0);
+              const float f = ex2(__ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x - mm);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                acc[4 * e] = fmaf(f, v[e].x, acc[4 * e]);
+                acc[4 * e + 1] = fmaf(f, v[e].y, acc[4 * e + 1]);
+                acc[4 * e + 2] = fmaf(f, v[e].z, acc[4 * e + 2]);
+                acc[4 * e + 3] = fmaf(f, v[e].w, acc[4 * e + 3]);
+              }
+              if (cc + 1 == me) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[e] = fmaf(fo, o[e], acc[e]);
               }
             }
-            const float inv = 1.f / lsum;
+            if (live) {
+              uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (d0 + i * subs < D / 4)
-                *reinterpret_cast<uint2*>(o_row + 4 * (d0 + i * subs)) =
-                    make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
-                               pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+              for (int u = 0; u < 8; ++u) v[u] = pack_bf16x2(acc[2 * u] * inv, acc[2 * u + 1] * inv);
+              store_32_bytes(o_row + 16 * i, v);
+            }
           }
+          if (r == 0) *ticket = 0;
         }
-        if (r == 0) q.tickets[2 * first + x] = 0;
       }
+      tc_fence_before();
       named_bar(1 + x, 128);   // flags[x] is rewritten by the next partial item
+      release();
     }
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   }
