@@ -48,6 +48,7 @@ constexpr int kItemCost = 256;        // an item's fixed cost, in positions
 constexpr int kMinShare = 256;        // a CTA's least share of the cost, in positions
 constexpr int kFewRows = 32;          // an item of at most so many rows is shared by A and B (and joined by any thread)
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
+constexpr int kSplitCostFew = 128;    // the same for items of few rows
 constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
 // Parts of a tile whose P goes to the tensor cores by itself.  (Four parts: 16K prompt 10 % slower.)
 constexpr int kParts = 2;
@@ -176,13 +177,14 @@ __device__ __forceinline__ void ranked(const PromptParams& q, const Seq& sq, int
 __device__ __forceinline__ Division divide(const PromptParams& q) {
   const int lane = threadIdx.x & 31;
   long long w = 0;
-  int items = 0, longest = 0;
+  int items = 0, longest = 0, rows = 0;
   Seq sq{};
   for (int s = lane; s < q.batch; s += 32) {
     sq = load_seq(q, s);
     w += sq.per_head;
     items += sq.pairs;
     if (sq.n > 0) longest = max(longest, sq.ctx + sq.n);
+    rows = max(rows, sq.n);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -193,7 +195,8 @@ __device__ __forceinline__ Division divide(const PromptParams& q) {
   const int grid = gridDim.x;
   d.ncta = (int)min((long long)grid, max(1ll, d.total / kMinShare));
   d.whole = 0;
-  const long long limit = d.total / d.ncta + kSplitCost;
+  rows = __reduce_max_sync(0xffffffffu, rows) * q.group;
+  const long long limit = d.total / d.ncta + (rows <= kFewRows ? kSplitCostFew : kSplitCost);
   if (q.batch <= 32 && longest + kItemCost <= limit) {
     long long span = 0;
     const int rounds = (d.items + grid - 1) / grid, rest = d.items - (rounds - 1) * grid;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(sfull(x), 1);
-      for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 128);
+      for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 4);   // a warp each
       mbar_init(odone(x), 1);
       mbar_init(pvpart(x), 1);
     }
@@ -866,7 +869,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int i = 0; i < P / 32; ++i) tmem_st16(tl + scol + P / 2 * h + 16 * i, pk + 16 * i);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(pready(x, h));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready(x, h));
         }
         if (!ok) break;
       }
