@@ -14,7 +14,8 @@
 //   S_X[128 x 128] = Q_X . K^T      (both operands in shared memory, K-major)
 //   O_X[128 x D]  += P_X . V        (P_X in tensor memory, V MN-major)
 // with S_A, S_B, O_A, O_B in tensor memory; P_X (bf16) overwrites the first 64
-// columns of S_X.  The softmax is the running one: thread r of X's warpgroup
+// columns of S_X at head_dim 128, which fills tensor memory, and has columns of
+// its own at 64.  The softmax is the running one: thread r of X's warpgroup
 // owns row r (tensor-memory lane r) and keeps the row's reference m and sum l
 // in registers.  m is the row's maximum over the item's first tile; any other
 // reference gives the same quotient, so later tiles take p = 2^(x - m) without
@@ -72,15 +73,21 @@ struct PCfg {
   static constexpr int kQ = kHalves * 128 * 128;      // one query tile [half][128 rows][128 B]
   static constexpr int kSlot = kHalves * 128 * 128;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 10;
-  static constexpr int kOffRing = 2 * kQ;
+  // At head_dim 64 tensor memory has room for P beside S, so the next S is computed as soon as
+  // the softmax has read this one, and shared memory for the next item's query tiles.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr int kQBufs = D == 64 ? 2 : 1;
+  static constexpr int kOffRing = 2 * kQBufs * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 1 + 2 * kPieces + 2 + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
   static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
   static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
   static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
+  static constexpr uint32_t kP = kOwnP ? 384 : 0;      // ... of P_A, and the step to P_B
+  static constexpr uint32_t kPStep = kOwnP ? 64 : 128;
 };
 
 // One point of the linear order of all (sequence, KV head, query-tile pair) items.
@@ -394,15 +401,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto full = [&](uint32_t s) { return bar0 + 8 * s; };
   auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
-  constexpr int B1 = 2 * NS + 2 + 2 * kParts;
+  constexpr int B1 = 2 * NS + 2 + 2 * kParts, QB = Cfg::kQBufs, B2 = B1 + 6 + 2 * QB;
   auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + kParts * x + h); };
   auto odone = [&](int x) { return bar0 + 8 * (B1 + x); };
   auto pvpart = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
-  const uint32_t qfull = bar0 + 8 * (B1 + 4), qfree = bar0 + 8 * (B1 + 5);
-  const uint32_t drain = bar0 + 8 * (B1 + 6);
-  const uint32_t altfull = bar0 + 8 * (B1 + 7 + 2 * kPieces), alttaken = altfull + 8;
-  auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + i); };
-  auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 7 + kPieces + i); };
+  auto sread = [&](int x) { return bar0 + 8 * (B1 + 4 + x); };
+  auto qfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + i % QB); };
+  auto qfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + QB + i % QB); };
+  const uint32_t drain = bar0 + 8 * B2, altfull = drain + 8, alttaken = drain + 16;
+  auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + i); };
+  auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + kPieces + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
@@ -423,9 +431,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 4);   // a warp each
       mbar_init(odone(x), 1);
       mbar_init(pvpart(x), 1);
+      mbar_init(sread(x), 4);
     }
-    mbar_init(qfull, 1);
-    mbar_init(qfree, 1);
+    for (int i = 0; i < QB; ++i) {
+      mbar_init(qfull(i), 1);
+      mbar_init(qfree(i), 1);
+    }
     mbar_init(drain, 1);
     mbar_init(altfull, 32);
     mbar_init(alttaken, 32);
@@ -566,174 +577,188 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!more) break;
       const int tiles = w.nb > 0 ? 2 : 1;
       const int qrow = w.row0 + w.tok0;
-      if (c > 0 && lane < tiles * Cfg::kHalves)   // on their way while the last item still uses the buffer
+      if (c >= QB && lane < tiles * Cfg::kHalves)   // on their way while the last item still uses the buffer
         tma_prefetch_3d(&qmap, 64 * (lane % Cfg::kHalves), w.g * q.group,
                         qrow + lane / Cfg::kHalves * q.tile_tokens);
-      if (c > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree, (c - 1) & 1))) {
+      if (c >= QB && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree(c), (c / QB - 1) & 1))) {
         ok = false;
         break;
       }
       const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
       if (lane == 0) {
-        mbar_arrive_expect_tx(qfull, bytes * tiles * Cfg::kHalves);
+        mbar_arrive_expect_tx(qfull(c), bytes * tiles * Cfg::kHalves);
         for (int x = 0; x < tiles; ++x)
           for (int h = 0; h < Cfg::kHalves; ++h)
-            tma_load_3d(sbase + x * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
-                        qrow + x * q.tile_tokens, qfull);
+            tma_load_3d(sbase + (2 * (c % QB) + x) * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
+                        qrow + x * q.tile_tokens, qfull(c));
       }
       __syncwarp();
       ++c;
     }
-    if (c > 0) (void)mbar_wait_bounded(qfull, (c - 1) & 1);   // landed before the CTA ends
+    for (uint32_t i = c > QB ? c - QB : 0; i < c; ++i)   // landed before the CTA ends
+      (void)mbar_wait_bounded(qfull(i), (i / QB) & 1);
     if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
   } else if (warp == 10) {
     leave_registers<72>();
     // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-    constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
-    const bool leader = elect_one();
-    const uint64_t dSw = smem_desc(0, 16, 1024, 2);       // K-major, 128-byte swizzle
-    const uint64_t dVmn = smem_desc(0, 16384, 1024, 2);   // MN-major, 64-dim halves 16 KB apart
-    auto with_addr = [](uint64_t d, uint32_t a16) { return d | uint64_t(a16 & 0x3FFFu); };
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-    };
-    auto wait_slot = [&](uint32_t j) { return wait_all(full(j % NS), (j / NS) & 1); };
-    auto slot16 = [&](uint32_t j) { return (sbase + Cfg::kOffRing + (j % NS) * Cfg::kSlot) >> 4; };
-    auto issue_s = [&](int x, int qtile, uint32_t jk) {
-      const uint32_t a = (sbase + qtile * Cfg::kQ) >> 4, b = slot16(jk);
-      if (leader) {
+    // One thread waits, issues and commits: its instructions lie on the path from a tile's P
+    // to its next S, so ring positions and phases are kept as running values and a step's
+    // descriptors differ from its first one by constants.
+    if (elect_one()) {
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
+      // K-major operands with the 128-byte swizzle; V MN-major, 64-dim halves 16 KB apart.
+      // Addresses are below 2^18, so the descriptor's address field takes plain sums.
+      constexpr uint64_t dSw = smem_desc_const(16, 1024, 2), dVmn = smem_desc_const(16384, 1024, 2);
+      const uint32_t q16 = sbase >> 4, ring16 = (sbase + Cfg::kOffRing) >> 4;
+      struct Ring {          // a position in the ring: slot and phase
+        uint32_t s, ph;
+        __device__ __forceinline__ void next() {   // (K and V take turns)
+          s += 2;
+          if (s >= NS) {
+            s -= NS;
+            ph ^= 1;
+          }
+        }
+      };
+      Ring kr{0, 0}, vr{1, 0};   // the next K to multiply, the next V
+      uint32_t pa = 0, pb = 0;   // phases of A's and B's P
+      uint32_t ra = 0, rb = 0;   // and of their S being read (kOwnP)
+      uint32_t items = 0;
+      auto wait_k = [&]() { return mbar_wait_bounded(full(kr.s), kr.ph); };
+      auto wait_v = [&]() { return mbar_wait_bounded(full(vr.s), vr.ph); };
+      auto free_k = [&]() {
+        tc_commit(freed(kr.s));
+        kr.next();
+      };
+      auto free_v = [&]() {
+        tc_commit(freed(vr.s));
+        vr.next();
+      };
+      auto issue_s = [&](int x, int qtile) {
+        const uint64_t a = dSw + (q16 + (2 * (items % QB) + qtile) * (Cfg::kQ / 16));
+        const uint64_t bk = dSw + (ring16 + kr.s * (Cfg::kSlot / 16));
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + 128 * x, with_addr(dSw, a + (ks >> 2) * 1024 + (ks & 3) * 2),
-                 with_addr(dSw, b + (ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
+          tc_mma(tmem + 128 * x, a + ((ks >> 2) * 1024 + (ks & 3) * 2),
+                 bk + ((ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
         tc_commit(sfull(x));
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int x, int h, uint32_t jv, bool accumulate) {
-      const uint32_t b = slot16(jv);
-      if (leader) {
+      };
+      // where P has its own place, S may be overwritten once the softmax has read it
+      auto wait_read = [&](int x) {
+        if constexpr (!Cfg::kOwnP) return true;
+        uint32_t& ph = x ? rb : ra;
+        const bool read = mbar_wait_bounded(sread(x), ph);
+        ph ^= 1;
+        return read;
+      };
+      // O_X += P_X . V, part by part as the softmax finishes them; last: X's last tile here
+      auto issue_pv = [&](int x, bool accumulate, bool last) {
+        uint32_t& ph = x ? pb : pa;
+        const uint64_t bv = dVmn + (ring16 + vr.s * (Cfg::kSlot / 16));
 #pragma unroll
-        for (int kp = 0; kp < kPart / 16; ++kp)
-          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + 128 * x + (kPart / 2) * h + 8 * kp,
-                    with_addr(dVmn, b + (kPart / 16 * h + kp) * 128), idPV,
-                    accumulate || h > 0 || kp > 0);
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint32_t bar) {
-      if (leader) tc_commit(bar);
-      __syncwarp();
-    };
-    uint32_t c = 0, items = 0;
-    uint32_t npa = 0, npb = 0;   // P tiles consumed of A, B
-    while (ok && next_piece(w, ok)) {
-      const int ea = min(w.k1, w.na), eb = min(w.k1, w.nb);
-      if (!wait_all(qfull, items & 1) || !wait_slot(2 * c)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (w.alt) {
-        // tile i to A or B in turn, each with its own S, P and O, both from query tile A
-        const int tiles = w.k1 - w.k0;
-        for (int i = 0; i < min(2, tiles) && ok; ++i) {
-          const uint32_t jk = 2 * (c + i);
-          if (!wait_slot(jk)) {
-            ok = false;
-            break;
-          }
+        for (int h = 0; h < kParts; ++h) {
+          if (!mbar_wait_bounded(pready(x, h), ph)) return false;
           tc_fence_after();
-          issue_s(i, 0, jk);
-          commit(freed(jk % NS));
+#pragma unroll
+          for (int kp = 0; kp < kPart / 16; ++kp)
+            tc_mma_ts(tmem + Cfg::kO + D * x,
+                      tmem + Cfg::kP + Cfg::kPStep * x + (kPart / 2) * h + 8 * kp,
+                      bv + (kPart / 16 * h + kp) * 128, idPV, accumulate || h > 0 || kp > 0);
+          if (h + 1 < kParts) tc_commit(pvpart(x));
         }
-        if (tiles <= 2) commit(qfree);
-        for (int i = 0; i < tiles && ok; ++i) {
+        ph ^= 1;
+        if (Cfg::kOwnP || last) tc_commit(odone(x));
+        return true;
+      };
+      // false: a wait ran out
+      auto run_pair = [&](int k0, int k1, int ea, int eb) {
+        if (!wait_k()) return false;
+        if (k0 < ea) issue_s(0, 0);
+        if (k0 < eb) issue_s(1, 1);
+        free_k();
+        if (k0 + 1 == k1) tc_commit(qfree(items));
+        for (int t = k0; t < k1; ++t) {
+          bool have_k = false, have_v = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int ex = x ? eb : ea;
+            if (t >= ex) continue;
+            auto next_s = [&]() {
+              if (!wait_read(x)) return false;
+              if (t + 1 >= ex) return true;
+              if (!have_k && !wait_k()) return false;
+              have_k = true;
+              issue_s(x, x);
+              return true;
+            };
+            if (Cfg::kOwnP && !next_s()) return false;
+            if (!have_v && !wait_v()) return false;
+            have_v = true;
+            if (!issue_pv(x, t > k0, t + 1 == ex)) return false;
+            if (!Cfg::kOwnP) {
+              if (x == 1 || t >= eb) free_v();
+              if (!next_s()) return false;
+            }
+          }
+          if (Cfg::kOwnP) free_v();
+          if (t + 1 < k1) {
+            free_k();
+            if (t + 2 == k1) tc_commit(qfree(items));
+          }
+        }
+        return true;
+      };
+      // tile i to A or B in turn, each with its own S, P and O, both from query tile A
+      auto run_alternating = [&](int tiles) {
+        for (int i = 0; i < min(2, tiles); ++i) {
+          if (!wait_k()) return false;
+          issue_s(i, 0);
+          free_k();
+        }
+        if (tiles <= 2) tc_commit(qfree(items));
+        for (int i = 0; i < tiles; ++i) {
           const int x = i & 1;
-          const uint32_t jv = 2 * (c + i) + 1, jk = 2 * (c + i) + 4;
-          if (!wait_slot(jv)) {
-            ok = false;
-            break;
-          }
-          for (int h = 0; h < kParts; ++h) {
-            if (!wait_all(pready(x, h), (x ? npb : npa) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(x, h, jv, i >= 2);
-            if (h + 1 < kParts) commit(pvpart(x));
-          }
-          if (!ok) break;
-          x ? ++npb : ++npa;
-          if (i + 2 >= tiles) commit(odone(x));
-          commit(freed(jv % NS));
-          if (i + 2 < tiles) {
-            if (!wait_slot(jk)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_s(x, 0, jk);
-            commit(freed(jk % NS));
-            if (i + 3 == tiles) commit(qfree);
-          }
+          auto next_s = [&]() {
+            if (!wait_read(x)) return false;
+            if (i + 2 >= tiles) return true;
+            if (!wait_k()) return false;
+            issue_s(x, 0);
+            free_k();
+            if (i + 3 == tiles) tc_commit(qfree(items));
+            return true;
+          };
+          if (Cfg::kOwnP && !next_s()) return false;
+          if (!wait_v() || !issue_pv(x, i >= 2, i + 2 >= tiles)) return false;
+          free_v();
+          if (!Cfg::kOwnP && !next_s()) return false;
         }
-        c += tiles;
-        ++items;
-        continue;
-      }
-      if (w.k0 < ea) issue_s(0, 0, 2 * c);
-      if (w.k0 < eb) issue_s(1, 1, 2 * c);
-      commit(freed((2 * c) % NS));
-      if (w.k0 + 1 == w.k1) commit(qfree);
-      for (int t = w.k0; t < w.k1 && ok; ++t, ++c) {
-        const uint32_t jv = 2 * c + 1, jk = 2 * c + 2;
-        const bool more = t + 1 < w.k1;
-        if (!wait_slot(jv)) {
+        return true;
+      };
+      while (true) {
+        const uint32_t i = pc % kPieces;
+        if (!mbar_wait_bounded(pcfull(i), (pc / kPieces) & 1)) {
           ok = false;
           break;
         }
-        bool have_k = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int ex = x ? eb : ea;
-          if (t >= ex) continue;
-          for (int h = 0; h < kParts; ++h) {   // part by part, as the softmax finishes them
-            if (!wait_all(pready(x, h), (x ? npb : npa) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(x, h, jv, t > w.k0);
-            if (h + 1 < kParts) commit(pvpart(x));
-          }
-          if (!ok) break;
-          x ? ++npb : ++npa;
-          if (t + 1 == ex) commit(odone(x));
-          if (x == 1 || t >= eb) commit(freed(jv % NS));
-          if (t + 1 < ex) {
-            if (!have_k && !wait_slot(jk)) {
-              ok = false;
-              break;
-            }
-            have_k = true;
-            tc_fence_after();
-            issue_s(x, x, jk);
-          }
+        const int seq = pieces[i].seq, k0 = pieces[i].k0, k1 = pieces[i].k1;
+        const int ea = min(k1, pieces[i].na), eb = min(k1, pieces[i].nb), alt = pieces[i].alt;
+        mbar_arrive(pcfree(i));
+        ++pc;
+        if (seq < 0) break;
+        if (!mbar_wait_bounded(qfull(items), (items / QB) & 1) ||
+            !(alt ? run_alternating(k1 - k0) : run_pair(k0, k1, ea, eb))) {
+          ok = false;
+          break;
         }
-        if (ok && more) {
-          commit(freed(jk % NS));
-          if (t + 2 == w.k1) commit(qfree);
-        }
+        ++items;
       }
-      ++items;
+      if (!ok) set_error(q.err, kErrDeviceTimeout);
+      tc_commit(drain);
     }
-    if (!ok && leader) set_error(q.err, kErrDeviceTimeout);
-    // every MMA issued has completed before tensor memory is released
-    if (leader) tc_commit(drain);
     __syncwarp();
+    // every MMA issued has completed before tensor memory is released
     (void)mbar_wait_bounded(drain, 0);
   } else {
     take_registers<216>();
@@ -741,7 +766,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int x = warp >> 2;
     const int r = tid & 127;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
+    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x, pcol = Cfg::kP + Cfg::kPStep * x;
     uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
     uint32_t nalt = 0;                // items that A and B shared
     // The item's fields stay in shared memory until its end: the tile loop needs the registers.
@@ -786,6 +811,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
         tmem_ld_wait();
+        if constexpr (Cfg::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sread(x));
+        }
         if (diagonal) {   // whatever the logits hold
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -836,6 +866,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
             hs = la + lb;
           };
           take();
+          if constexpr (Cfg::kOwnP) {
+            if (h == 0 && t > kbeg) {   // the last tile's P has been used (and its O is complete)
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
+              ++no;
+              tc_fence_after();
+            }
+          }
           if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
             float mx = s[P * h];
 #pragma unroll
@@ -844,8 +881,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float f = ex2(m - m2);
             m = m2;
             l *= f;
-            // O holds the row's earlier tiles (S of this one was issued after their
-            // products), and from the second part on this tile's earlier parts
+            // O holds the row's earlier tiles (complete: waited for above, or S of this one was
+            // issued after their products), and from the second part on this tile's earlier parts
             static_assert(kParts == 2, "one pvpart phase a tile");
             if (h > 0)
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvpart(x), (ns - 1) & 1)) && ok;
@@ -866,7 +903,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           l += hs;
 #pragma unroll
-          for (int i = 0; i < P / 32; ++i) tmem_st16(tl + scol + P / 2 * h + 16 * i, pk + 16 * i);
+          for (int i = 0; i < P / 32; ++i) tmem_st16(tl + pcol + P / 2 * h + 16 * i, pk + 16 * i);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();

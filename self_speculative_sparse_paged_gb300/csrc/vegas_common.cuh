@@ -322,6 +322,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          (uint64_t((sbo >> 4) & 0x3FFF) << 32) | (uint64_t(1) << 46) |
          (uint64_t(layout & 7) << 61);
 }
+// The same without the start address, which is added as (address / 16).
+__host__ __device__ constexpr uint64_t smem_desc_const(uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return (uint64_t((lbo >> 4) & 0x3FFF) << 16) | (uint64_t((sbo >> 4) & 0x3FFF) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(layout & 7) << 61);
+}
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B,
 // A/B major-ness (0 = K-major, 1 = MN-major), N and M.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int a_mn_major, int b_mn_major) {
