@@ -860,12 +860,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
               b = ex2(b);
               sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
               pk[e] = pack_bf16x2(a, b);
+              // (nothing reads it before this part's arrival)
+              if ((e & 15) == 15) tmem_st16(tl + pcol + P / 2 * h + (e & 16), pk + (e & 16));
             }
             float la, lb;
             unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
             hs = la + lb;
           };
-          take();
           if constexpr (Cfg::kOwnP) {
             if (h == 0 && t > kbeg) {   // the last tile's P has been used (and its O is complete)
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
@@ -873,6 +874,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
               tc_fence_after();
             }
           }
+          take();
           if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
             float mx = s[P * h];
 #pragma unroll
@@ -902,8 +904,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
             take();
           }
           l += hs;
-#pragma unroll
-          for (int i = 0; i < P / 32; ++i) tmem_st16(tl + pcol + P / 2 * h + 16 * i, pk + 16 * i);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
