@@ -296,7 +296,7 @@ vegas_status_t vegas_decode_iteration(
  * rows behind the last sequence may hold anything and are never written.  Needs
  * 0 <= ctx_lens[b] and ctx_lens[b] + n_b <= 16 * max_pages_per_seq; a sequence
  * with rows that breaks this is recorded as a device fault and skipped.
- * total_rows < 2^24.
+ * total_rows < 2^24, batch <= 2^16.
  *
  * vegas_rope_append turns the query and key heads of every row by their
  * positions and appends keys and values to the cache.  Pair j < rot_dim / 2

@@ -50,7 +50,7 @@ constexpr int kMinShare = 256;        // a CTA's least share of the cost, in pos
 constexpr int kFewRows = 32;          // an item of at most so many rows is shared by A and B (and joined by any thread)
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr int kSplitCostFew = 128;    // the same for items of few rows
-constexpr float kNoMax = -1e30f;      // reference of a row that has seen nothing
+constexpr float kNoMax = -3e38f;      // reference of a row that has seen nothing
 // Parts of a tile whose P goes to the tensor cores by itself.  (Four parts: 16K prompt 10 % slower.)
 constexpr int kParts = 2;
 constexpr int kPart = kTile / kParts; // positions per part
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           float mx = s[0];
 #pragma unroll
           for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
-          m = fmaxf(mx * q.scale_log2, kNoMax);
+          m = fmaxf(mx, kNoMax);
         }
         if (t == vzero) {
           // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
@@ -854,8 +854,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
             for (int e = 0; e < P / 2; ++e) {
               float a, b;
-              unpair_f32(fma_f32x2(pair_f32(s[P * h + 2 * e], s[P * h + 2 * e + 1]), sc2, nm2), a,
-                         b);
+              unpair_f32(mul_f32x2(add_f32x2(pair_f32(s[P * h + 2 * e], s[P * h + 2 * e + 1]), nm2), sc2),
+                         a, b);
               a = ex2(a);
               b = ex2(b);
               sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
@@ -879,8 +879,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             float mx = s[P * h];
 #pragma unroll
             for (int i = 1; i < P; ++i) mx = fmaxf(mx, s[P * h + i]);
-            const float m2 = fmaxf(m, mx * q.scale_log2);
-            const float f = ex2(m - m2);
+            const float m2 = fmaxf(m, mx);
+            const float f = ex2((m - m2) * q.scale_log2);
             m = m2;
             l *= f;
             // O holds the row's earlier tiles (complete: waited for above, or S of this one was
@@ -931,7 +931,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tc_fence_after();
           if (ok && w.k1 - w.k0 > 1) {
             const float2 b = alt_ml[lane];
-            const float m2 = fmaxf(m, b.x), fa = ex2(m - m2), fb = ex2(b.x - m2);
+            const float m2 = fmaxf(m, b.x);
+            const float fa = ex2((m - m2) * q.scale_log2), fb = ex2((b.x - m2) * q.scale_log2);
             m = m2;
             l = fa * l + fb * b.y;
 #pragma unroll 1
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const size_t sl = slot_of(cc, x);
                 const float2 v = __ldcg(&ml[sl * 128 + rr]);
                 const float4 o = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
-                const float f = ex2(v.x - mm);
+                const float f = ex2((v.x - mm) * q.scale_log2);
                 lsum = fmaf(f, v.y, lsum);
                 acc.x = fmaf(f, o.x, acc.x);
                 acc.y = fmaf(f, o.y, acc.y);
@@ -1083,7 +1084,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (cc != me) mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x);
           for (int cc = first; cc <= last; ++cc) {
             const float2 v = cc == me ? make_float2(m, l) : __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]);
-            lsum = fmaf(ex2(v.x - mm), v.y, lsum);
+            lsum = fmaf(ex2((v.x - mm) * q.scale_log2), v.y, lsum);
           }
           const float inv = 1.f / lsum;
           __nv_bfloat16* o_row = out_row(rr);
@@ -1096,7 +1097,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int e = 0; e < 4; ++e) next[e] = __ldcg(&src[(4 * i + e) * 128]);
           };
           fetch(0, 0);
-          const float fo = any ? ex2(m - mm) : 0.f;
+          const float fo = any ? ex2((m - mm) * q.scale_log2) : 0.f;
 #pragma unroll 1
           for (int i = 0; i < D / 16; ++i) {
             float o[16], acc[16];
@@ -1119,7 +1120,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 fetch(i, j + 1);
               else if (i + 1 < D / 16)
                 fetch(i + 1, 0);
-              const float f = ex2(__ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x - mm);
+              const float f =
+                  ex2((__ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x - mm) * q.scale_log2);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 acc[4 * e] = fmaf(f, v[e].x, acc[4 * e]);

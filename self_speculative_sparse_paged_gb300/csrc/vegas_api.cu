@@ -657,8 +657,9 @@ vegas_status_t check_packed(const int32_t* row_start, const int32_t* ctx_lens, i
   if (!row_start || !ctx_lens) return fail(VEGAS_ERR_INVALID_ARG, "NULL row_start or ctx_lens");
   if (total_rows < 0 || batch < 0)
     return fail(VEGAS_ERR_INVALID_ARG, "total_rows %d, batch %d", total_rows, batch);
-  if (total_rows >= (1 << 24))
-    return fail(VEGAS_ERR_UNSUPPORTED, "total_rows %d (must be < 2^24)", total_rows);
+  if (total_rows >= (1 << 24) || batch > (1 << 16))
+    return fail(VEGAS_ERR_UNSUPPORTED, "total_rows %d (must be < 2^24), batch %d (at most 2^16)",
+                total_rows, batch);
   return VEGAS_OK;
 }
 
@@ -809,6 +810,9 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
   const int G = kv->num_q_heads / kv->num_kv_heads;
   if (G > kMaxPromptGroup)
     return fail(VEGAS_ERR_UNSUPPORTED, "group size %d (at most %d)", G, kMaxPromptGroup);
+  if (kv->num_kv_heads * ((long long)total_rows / (2 * (128 / G)) + batch) >= (1ll << 30))
+    return fail(VEGAS_ERR_UNSUPPORTED, "%d rows of %d KV heads: too many for one call", total_rows,
+                kv->num_kv_heads);
   if (total_rows == 0 || batch == 0) return VEGAS_OK;
   int* err = nullptr;
   int sms = 0;

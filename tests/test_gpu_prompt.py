@@ -265,3 +265,61 @@ def test_cache_beyond_32_bit_offsets():
     assert c.k.numel() > 2 ** 31
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (64, 8, 64), (8, 8, 128)])
+@pytest.mark.parametrize("batch", [1, 7, 31, 32, 33, 150])
+def test_decode_batches(hq, hkv, d, batch):
+    """One to three rows each: items whose tiles both softmax groups share, many a CTA."""
+    rng = np.random.default_rng(batch)
+    rows = [int(x) for x in rng.integers(1, 4, batch)]
+    ctx = [int(x) for x in rng.integers(0, 1500, batch)]
+    c = Prompt(hq, hkv, d, rows, ctx, seed=batch)
+    c.run()
+    c.check(heads=(0, hq // 2, hq - 1))
+    first = c.out.clone()
+    for _ in range(2):
+        c.out[:c.used] = 0
+        c.run()
+        assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,ctx", [([600], [7000]), ([128, 1], [30000, 30000]), ([90, 33], [5000, 12345])])
+def test_items_of_many_rows_split_over_ctas(d, rows, ctx):
+    c = Prompt(8, 2, d, rows, ctx, seed=rows[0])
+    c.run()
+    c.check(heads=(1, 6))
+    first = c.out.clone()
+    for _ in range(4):
+        c.out[:c.used] = 0
+        c.run()
+        assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("jump", [40.0, 400.0, 1e4])
+def test_late_large_logits(d, jump):
+    """Keys that exceed all earlier ones by far, in either half of a tile and in the rows' own
+    positions: rows raise their reference once most of their cache has been summed."""
+    c = Prompt(8, 2, d, [200], [900], seed=17, heavy=False)
+    pg = torch.from_numpy(c.table[0].astype(np.int64)).to(DEV)
+    for pos in (300, 440, 777, 950, 1010, 1099):
+        u = c.q[:, :8 * d].float().view(-1, 8, d).mean((0, 1))
+        c.k[pg[pos // 16], :, pos % 16] = (u / u.norm() * jump).bfloat16()
+    c.run()
+    c.check()
+
+
+def test_very_low_logits_are_no_mask():
+    c = Prompt(4, 2, 64, [70], [100], seed=18, heavy=False)
+    c.q.copy_(torch.full_like(c.q, 1e17))
+    pg = torch.from_numpy(c.table[0].astype(np.int64)).to(DEV)
+    pos = torch.arange(170, device=DEV)
+    c.k[pg[pos // 16], :, pos % 16] = -1e17          # every logit about -8e34
+    c.run()
+    mean = torch.cumsum(c.v[pg[pos // 16], :, pos % 16].double(), 0) / (pos + 1).double()[:, None, None]
+    got = c.out.double().view(70, 2, 2, 64)
+    ref = mean[100:, :, None, :]
+    assert ((got - ref).abs() <= 2.0 ** -7 * (ref.abs() + 1)).all()
+    vg.vegas_read_device_status()

@@ -33,7 +33,7 @@ def test_rope_append_refusals(vg):  # noqa: F811
             (dict(num_axes=3, positions=16), 1, "pair_axis"),
             (dict(rope_scale=float("nan")), 1, "rope_scale"),
             (dict(total_rows=-1), 1, "total_rows"), (dict(batch=-1), 1, "batch"),
-            (dict(total_rows=1 << 24), 2, "total_rows")):
+            (dict(total_rows=1 << 24), 2, "total_rows"), (dict(batch=(1 << 16) + 1), 2, "batch")):
         _refused(lambda: vg.vegas_rope_append(**{**good, **change}), status, word)
     vg.vegas_rope_append(**{**good, "total_rows": 0})       # nothing to do
     vg.vegas_rope_append(**{**good, "batch": 0})
@@ -51,6 +51,9 @@ def test_prompt_attn_refusals(vg):  # noqa: F811
             (dict(out=None), 1, "out"), (dict(out=48), 1, "out"),
             (dict(row_start=None), 1, "row_start"), (dict(ctx_lens=None), 1, "ctx_lens"),
             (dict(total_rows=-2), 1, "total_rows"), (dict(batch=-1), 1, "batch"),
+            (dict(total_rows=1 << 24), 2, "total_rows"), (dict(batch=(1 << 16) + 1), 2, "batch"),
+            (dict(kv=vg.PagedKV(16, 16, 16, 4, 16, 64 * 999, 999, 64, 4), q_stride=64 * 64 * 999,
+                  total_rows=(1 << 24) - 1), 2, "too many"),
             (dict(softmax_scale=0.0), 1, "softmax_scale"),
             (dict(softmax_scale=-0.5), 1, "softmax_scale"),
             (dict(softmax_scale=float("inf")), 1, "softmax_scale")):
