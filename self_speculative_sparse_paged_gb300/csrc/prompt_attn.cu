@@ -36,6 +36,18 @@
 // inside an item; such an item's partial (m, l, O) go through the workspace and
 // the CTA that arrives last joins them in range order.  So a single decode row
 // with a long cache spreads over all SMs, with at most two partial items a CTA.
+//
+// What bounds it: at long lengths the tensor cores and the softmax together.  A
+// pair of tiles needs 2048 tensor cycles a KV tile at head_dim 128; the softmax
+// of one 128 x 128 tile takes a warp about 900 cycles alone and 750 when two
+// share a scheduler (ex2 issues every 4 cycles, beside conversions), and at
+// head_dim 128 S(t + 1) needs tensor memory that P(t) occupies, so a tile's
+// softmax and its two products follow one another and A and B overlap each
+// other's: 2700 cycles a KV tile measured.  A prompt of 16384 rows (32 query
+// heads of 128): 1261 us alone (1.74 PFLOP/s, 0.92 of the measured cuBLAS burst,
+// tensor pipe 75 % active), 1360-1400 us back to back (0.95 of cuBLAS sustained,
+// power-capped as that is); 1000 rows behind 31768 cached: 350 us (1.51 PFLOP/s).
+// One row each of eight sequences of 32000 positions: 160 us (6.6 TB/s).
 #include "kernels.h"
 #include "vegas_common.cuh"
 

@@ -18,7 +18,10 @@
 // lane i turns unit i % (rot / 16) (8 pairs) of head i / (rot / 16) and the heads
 // a fixed stride on, so its cosines and sines stay in registers and a head costs
 // two 16-byte loads, 32 multiply-adds and two 16-byte stores, with no barrier
-// between warps.
+// between warps; the first heads are loaded before the row's sequence, page and
+// angles are looked up.  32768 rows of 32 + 8 + 8 heads of 128: 128 us, 6.3 TB/s of
+// bytes read and written once (0.93 of the measured copy); 32 rows: 3.2 us, launch
+// and three dependent lookups.
 #include "kernels.h"
 #include "vegas_common.cuh"
 
