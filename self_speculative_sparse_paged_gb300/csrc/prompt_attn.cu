@@ -121,6 +121,22 @@ __device__ __forceinline__ int pairs_in(const PromptParams& q, int n) {
   return (int)__umulhi((uint32_t)n, q.pair_inverse);
 }
 
+// floor(a / b) for a quotient below 2^20: one fp32 division, put right (a 64-bit
+// integer division takes several hundred cycles at the start of every call).
+__device__ __forceinline__ int small_quotient(long long a, long long b) {
+  long long q = (long long)((float)a / (float)b);
+  while (q * b > a) --q;
+  while ((q + 1) * b <= a) ++q;
+  return (int)q;
+}
+
+// floor(i * total / n) for i <= n <= 2^16.
+__device__ __forceinline__ long long share_begin(int i, long long total, int n) {
+  if (total >> 31) return i * total / n;
+  const unsigned t = (unsigned)total, q = t / n, r = t - q * n;
+  return (long long)i * q + (unsigned)i * r / n;
+}
+
 __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
   Seq r;
   r.row0 = q.row_start[s];
@@ -212,19 +228,19 @@ __device__ __forceinline__ Division divide(const PromptParams& q) {
   d.items = __reduce_add_sync(0xffffffffu, items) * q.hkv;
   longest = __reduce_max_sync(0xffffffffu, longest);
   const int grid = gridDim.x;
-  d.ncta = (int)min((long long)grid, max(1ll, d.total / kMinShare));
+  d.ncta = (int)min((long long)grid, max(1ll, d.total / kMinShare));   // (a shift)
   d.whole = 0;
   rows = __reduce_max_sync(0xffffffffu, rows) * q.group;
-  const long long limit = d.total / d.ncta + (rows <= kFewRows ? kSplitCostFew : kSplitCost);
+  const long long limit = share_begin(1, d.total, d.ncta) + (rows <= kFewRows ? kSplitCostFew : kSplitCost);
   if (q.batch <= 32 && longest + kItemCost <= limit) {
     long long span = 0;
     const int rounds = (d.items + grid - 1) / grid, rest = d.items - (rounds - 1) * grid;
     if (rounds > 1 && rest < grid) {
       int cost = longest + q.pair_tokens, seq, g, p;
       ranked(q, sq, (rounds - 1) * grid, cost, seq, g, p);
-      span = (long long)(cost + kItemCost) * (grid - rest) / grid;
+      span = share_begin(grid - rest, cost + kItemCost, grid);
     }
-    d.whole = d.total / grid + span <= limit;
+    d.whole = share_begin(1, d.total, grid) + span <= limit;
   }
   if (d.whole) d.ncta = grid;
   return d;
@@ -261,7 +277,7 @@ __device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
       sq.per_head = __shfl_sync(0xffffffffu, sq.per_head, src);
       const long long sbase = base + __shfl_sync(0xffffffffu, incl - mine, src);
       r.seq = s0 + src;
-      r.g = (int)((u - sbase) / sq.per_head);
+      r.g = small_quotient(u - sbase, sq.per_head);
       const long long hbase = sbase + r.g * sq.per_head;
       const long long rem = u - hbase;
       int lo = 0, hi = sq.pairs - 1;   // the last p with cost_before(p) <= rem
@@ -373,8 +389,8 @@ struct Walk {
         // i >= ceil(x * ncta / total); those in [a, b) fall inside the item (locate()).
         const long long a = at.us + kItemCost + 2 * kTile - kTile / 2;
         const long long b = at.us + kItemCost + (long long)kTile * nt - 2 * kTile + kTile / 2;
-        w.first = (int)((a * d.ncta + d.total - 1) / d.total) - 1;
-        w.last = (int)((b * d.ncta + d.total - 1) / d.total) - 1;
+        w.first = small_quotient(a * d.ncta + d.total - 1, d.total) - 1;
+        w.last = small_quotient(b * d.ncta + d.total - 1, d.total) - 1;
       }
       if (stop) {
         at.seq = q.batch;   // done
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       pt.g = pt.p = pt.k = 0;
       pt.us = d.total;
     } else {
-      pt = locate(q, i * d.total / d.ncta);
+      pt = locate(q, share_begin(i, d.total, d.ncta));
     }
     if (lane == 0) {
       int* e = ends + 6 * (warp - 8);
@@ -1102,55 +1118,71 @@ __global__ void __launch_bounds__(kPThreads, 1)
           __nv_bfloat16* o_row = out_row(rr);
           const int others = last - first;
           auto other = [&](int j) { return first + j + (first + j >= me ? 1 : 0); };
-          float4 next[4];
-          auto fetch = [&](int i, int j) {   // columns 16 i .. of the j-th other state
+          float fj[3];   // the first other states' factors
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            fj[j] = j < others
+                        ? ex2((__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x - mm) * q.scale_log2)
+                        : 0.f;
+          auto factor = [&](int j) {
+            return j == 0   ? fj[0]
+                   : j == 1 ? fj[1]
+                   : j == 2
+                       ? fj[2]
+                       : ex2((__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x - mm) *
+                             q.scale_log2);
+          };
+          float4 next[8];
+          auto fetch = [&](int i, int j) {   // columns 32 i .. of the j-th other state
             const float4* src = po + size_t(slot_of(other(j), x)) * (D / 4) * 128 + rr;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) next[e] = __ldcg(&src[(4 * i + e) * 128]);
+            for (int e = 0; e < 8; ++e) next[e] = __ldcg(&src[(8 * i + e) * 128]);
           };
           fetch(0, 0);
           const float fo = any ? ex2((m - mm) * q.scale_log2) : 0.f;
 #pragma unroll 1
-          for (int i = 0; i < D / 16; ++i) {
-            float o[16], acc[16];
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32], acc[32];
             if (any) {
-              tmem_ld16(tl + ocol + 16 * i, o);
+              tmem_ld32(tl + ocol + 32 * i, o);
               tmem_ld_wait();
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
               if (!any) o[e] = 0.f;
               acc[e] = me == first ? fmaf(fo, o[e], 0.f) : 0.f;
             }
 #pragma unroll 1
             for (int j = 0; j < others; ++j) {
-              float4 v[4];
+              float4 v[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = next[e];
-              const int cc = other(j);
+              for (int e = 0; e < 8; ++e) v[e] = next[e];
               if (j + 1 < others)
                 fetch(i, j + 1);
-              else if (i + 1 < D / 16)
+              else if (i + 1 < D / 32)
                 fetch(i + 1, 0);
-              const float f =
-                  ex2((__ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x - mm) * q.scale_log2);
+              const float f = factor(j);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 acc[4 * e] = fmaf(f, v[e].x, acc[4 * e]);
                 acc[4 * e + 1] = fmaf(f, v[e].y, acc[4 * e + 1]);
                 acc[4 * e + 2] = fmaf(f, v[e].z, acc[4 * e + 2]);
                 acc[4 * e + 3] = fmaf(f, v[e].w, acc[4 * e + 3]);
               }
-              if (cc + 1 == me) {
+              if (other(j) + 1 == me) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[e] = fmaf(fo, o[e], acc[e]);
+                for (int e = 0; e < 32; ++e) acc[e] = fmaf(fo, o[e], acc[e]);
               }
             }
             if (live) {
-              uint32_t v[8];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) v[u] = pack_bf16x2(acc[2 * u] * inv, acc[2 * u + 1] * inv);
-              store_32_bytes(o_row + 16 * i, v);
+              for (int e = 0; e < 2; ++e) {
+                uint32_t v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  v[u] = pack_bf16x2(acc[16 * e + 2 * u] * inv, acc[16 * e + 2 * u + 1] * inv);
+                store_32_bytes(o_row + 32 * i + 16 * e, v);
+              }
             }
           }
           if (r == 0) *ticket = 0;
