@@ -14,8 +14,8 @@
 //   S_X[128 x 128] = Q_X . K^T      (both operands in shared memory, K-major)
 //   O_X[128 x D]  += P_X . V        (P_X in tensor memory, V MN-major)
 // with S_A, S_B, O_A, O_B in tensor memory; P_X (bf16) overwrites the first 64
-// columns of S_X at head_dim 128, which fills tensor memory, and has columns of
-// its own at 64.  The softmax is the running one: thread r of X's warpgroup
+// columns of S_X (at head_dim 64 there is room for it elsewhere, so that S(t + 1)
+// need not wait for P(t): no faster, the softmax sets the pace there).  The softmax is the running one: thread r of X's warpgroup
 // owns row r (tensor-memory lane r) and keeps the row's reference m and sum l
 // in registers.  m is the row's maximum over the item's first tile; any other
 // reference gives the same quotient, so later tiles take p = 2^(x - m) without
@@ -85,21 +85,17 @@ struct PCfg {
   static constexpr int kQ = kHalves * 128 * 128;      // one query tile [half][128 rows][128 B]
   static constexpr int kSlot = kHalves * 128 * 128;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 10;
-  // At head_dim 64 tensor memory has room for P beside S, so the next S is computed as soon as
-  // the softmax has read this one, and shared memory for the next item's query tiles.
-  static constexpr bool kOwnP = D == 64;
+  // At head_dim 64 shared memory has room for the next item's query tiles.
   static constexpr int kQBufs = D == 64 ? 2 : 1;
   static constexpr int kOffRing = 2 * kQBufs * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
   static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
   static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
   static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
-  static constexpr uint32_t kP = kOwnP ? 384 : 0;      // ... of P_A, and the step to P_B
-  static constexpr uint32_t kPStep = kOwnP ? 64 : 128;
 };
 
 // One point of the linear order of all (sequence, KV head, query-tile pair) items.
@@ -429,13 +425,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto full = [&](uint32_t s) { return bar0 + 8 * s; };
   auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
-  constexpr int B1 = 2 * NS + 2 + 2 * kParts, QB = Cfg::kQBufs, B2 = B1 + 6 + 2 * QB;
+  constexpr int B1 = 2 * NS + 2 + 2 * kParts, QB = Cfg::kQBufs, B2 = B1 + 4 + 2 * QB;
   auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + kParts * x + h); };
   auto odone = [&](int x) { return bar0 + 8 * (B1 + x); };
   auto pvpart = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
-  auto sread = [&](int x) { return bar0 + 8 * (B1 + 4 + x); };
-  auto qfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + i % QB); };
-  auto qfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + QB + i % QB); };
+  auto qfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 4 + i % QB); };
+  auto qfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 4 + QB + i % QB); };
   const uint32_t drain = bar0 + 8 * B2, altfull = drain + 8, alttaken = drain + 16;
   auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + i); };
   auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + kPieces + i); };
@@ -459,7 +454,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 4);   // a warp each
       mbar_init(odone(x), 1);
       mbar_init(pvpart(x), 1);
-      mbar_init(sread(x), 4);
     }
     for (int i = 0; i < QB; ++i) {
       mbar_init(qfull(i), 1);
@@ -651,7 +645,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       };
       Ring kr{0, 0}, vr{1, 0};   // the next K to multiply, the next V
       uint32_t pa = 0, pb = 0;   // phases of A's and B's P
-      uint32_t ra = 0, rb = 0;   // and of their S being read (kOwnP)
       uint32_t items = 0;
       auto wait_k = [&]() { return mbar_wait_bounded(full(kr.s), kr.ph); };
       auto wait_v = [&]() { return mbar_wait_bounded(full(vr.s), vr.ph); };
@@ -673,14 +666,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                  bk + ((ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
         tc_commit(sfull(x));
       };
-      // where P has its own place, S may be overwritten once the softmax has read it
-      auto wait_read = [&](int x) {
-        if constexpr (!Cfg::kOwnP) return true;
-        uint32_t& ph = x ? rb : ra;
-        const bool read = mbar_wait_bounded(sread(x), ph);
-        ph ^= 1;
-        return read;
-      };
       // O_X += P_X . V, part by part as the softmax finishes them; last: X's last tile here
       auto issue_pv = [&](int x, bool accumulate, bool last) {
         uint32_t& ph = x ? pb : pa;
@@ -692,12 +677,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
           for (int kp = 0; kp < kPart / 16; ++kp)
             tc_mma_ts(tmem + Cfg::kO + D * x,
-                      tmem + Cfg::kP + Cfg::kPStep * x + (kPart / 2) * h + 8 * kp,
+                      tmem + 128 * x + (kPart / 2) * h + 8 * kp,
                       bv + (kPart / 16 * h + kp) * 128, idPV, accumulate || h > 0 || kp > 0);
           if (h + 1 < kParts) tc_commit(pvpart(x));
         }
         ph ^= 1;
-        if (Cfg::kOwnP || last) tc_commit(odone(x));
+        if (last) tc_commit(odone(x));
         return true;
       };
       // false: a wait ran out
@@ -713,24 +698,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int x = 0; x < 2; ++x) {
             const int ex = x ? eb : ea;
             if (t >= ex) continue;
-            auto next_s = [&]() {
-              if (!wait_read(x)) return false;
-              if (t + 1 >= ex) return true;
-              if (!have_k && !wait_k()) return false;
-              have_k = true;
-              issue_s(x, x);
-              return true;
-            };
-            if (Cfg::kOwnP && !next_s()) return false;
             if (!have_v && !wait_v()) return false;
             have_v = true;
             if (!issue_pv(x, t > k0, t + 1 == ex)) return false;
-            if (!Cfg::kOwnP) {
-              if (x == 1 || t >= eb) free_v();
-              if (!next_s()) return false;
-            }
+            if (x == 1 || t >= eb) free_v();
+            if (t + 1 >= ex) continue;
+            if (!have_k && !wait_k()) return false;
+            have_k = true;
+            issue_s(x, x);
           }
-          if (Cfg::kOwnP) free_v();
           if (t + 1 < k1) {
             free_k();
             if (t + 2 == k1) tc_commit(qfree(items));
@@ -748,19 +724,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (tiles <= 2) tc_commit(qfree(items));
         for (int i = 0; i < tiles; ++i) {
           const int x = i & 1;
-          auto next_s = [&]() {
-            if (!wait_read(x)) return false;
-            if (i + 2 >= tiles) return true;
-            if (!wait_k()) return false;
-            issue_s(x, 0);
-            free_k();
-            if (i + 3 == tiles) tc_commit(qfree(items));
-            return true;
-          };
-          if (Cfg::kOwnP && !next_s()) return false;
           if (!wait_v() || !issue_pv(x, i >= 2, i + 2 >= tiles)) return false;
           free_v();
-          if (!Cfg::kOwnP && !next_s()) return false;
+          if (i + 2 >= tiles) continue;
+          if (!wait_k()) return false;
+          issue_s(x, 0);
+          free_k();
+          if (i + 3 == tiles) tc_commit(qfree(items));
         }
         return true;
       };
@@ -794,7 +764,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int x = warp >> 2;
     const int r = tid & 127;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x, pcol = Cfg::kP + Cfg::kPStep * x;
+    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
     uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
     uint32_t nalt = 0;                // items that A and B shared
     // The item's fields stay in shared memory until its end: the tile loop needs the registers.
@@ -839,11 +809,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
         tmem_ld_wait();
-        if constexpr (Cfg::kOwnP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sread(x));
-        }
         if (diagonal) {   // whatever the logits hold
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -889,19 +854,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
               sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
               pk[e] = pack_bf16x2(a, b);
               // (nothing reads it before this part's arrival)
-              if ((e & 15) == 15) tmem_st16(tl + pcol + P / 2 * h + (e & 16), pk + (e & 16));
+              if ((e & 15) == 15) tmem_st16(tl + scol + P / 2 * h + (e & 16), pk + (e & 16));
             }
             float la, lb;
             unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
             hs = la + lb;
           };
-          if constexpr (Cfg::kOwnP) {
-            if (h == 0 && t > kbeg) {   // the last tile's P has been used (and its O is complete)
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
-              ++no;
-              tc_fence_after();
-            }
-          }
           take();
           if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
             float mx = s[P * h];
@@ -911,8 +869,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float f = ex2((m - m2) * q.scale_log2);
             m = m2;
             l *= f;
-            // O holds the row's earlier tiles (complete: waited for above, or S of this one was
-            // issued after their products), and from the second part on this tile's earlier parts
+            // O holds the row's earlier tiles (S of this one was issued after their
+            // products), and from the second part on this tile's earlier parts
             static_assert(kParts == 2, "one pvpart phase a tile");
             if (h > 0)
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvpart(x), (ns - 1) & 1)) && ok;
