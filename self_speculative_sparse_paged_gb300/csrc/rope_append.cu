@@ -18,20 +18,17 @@
 // lane i turns unit i % (rot / 16) (8 pairs) of head i / (rot / 16) and the heads
 // a fixed stride on, so its cosines and sines stay in registers and a head costs
 // two 16-byte loads, 32 multiply-adds and two 16-byte stores, with no barrier
-// between warps; the first heads are loaded before the row's sequence, page and
-// angles are looked up.  32768 rows of 32 + 8 + 8 heads of 128: 128 us, 6.3 TB/s of
-// bytes read and written once (0.93 of the measured copy); 32 rows: 3.2 us, launch
-// and three dependent lookups.
+// between warps; the first heads, the frequencies and the given positions are loaded
+// before the row's sequence and page are looked up.  32768 rows of 32 + 8 + 8 heads of
+// 128: 128 us, 6.3 TB/s of bytes read and written once (0.93 of the measured copy); 32
+// rows: 3.1 us, launch and three dependent lookups.
 #include "kernels.h"
 #include "vegas_common.cuh"
 
 namespace vegas {
 
 namespace {
-constexpr int kRopeWarps = 4;        // warps of a block
-constexpr int Batch = 2;        // heads a lane has in flight
-
-constexpr int kRopeOneWarp = 6000, kRopeTwoWarps = 2000;
+constexpr int kRopeWarps = 4;   // warps of a block
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -71,6 +68,23 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
     }
   };
   if (units) load(h0);   // the first heads are on their way under the lookups below
+  // the frequencies, and the positions where they are given, of the lane's two pairs
+  float freq[2] = {0.f, 0.f};
+  int given[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    if (j >= half) continue;
+    freq[i] = p.inv_freq[j];
+    if (p.positions) {
+      int axis = p.pair_axis ? p.pair_axis[j] : 0;
+      if (axis < 0 || axis >= p.num_axes) {
+        set_error(p.err, kErrDeviceFault);
+        axis = 0;
+      }
+      given[i] = p.positions[size_t(axis) * p.total_rows + row];
+    }
+  }
 
   // The row's sequence: the last one that begins at or before it, found 32 at a time.
   int s = 0;
@@ -100,17 +114,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
   const bool page_ok = page >= 0 && page < p.num_pages;
   if (!page_ok && lane == 0) set_error(p.err, kErrDeviceFault);
 
-  for (int j = lane; j < half; j += 32) {
-    int at = pos;
-    if (p.positions) {
-      int axis = p.pair_axis ? p.pair_axis[j] : 0;
-      if (axis < 0 || axis >= p.num_axes) {
-        set_error(p.err, kErrDeviceFault);
-        axis = 0;
-      }
-      at = p.positions[size_t(axis) * p.total_rows + row];
-    }
-    double turns = double(at) * double(p.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    if (j >= half) continue;
+    const int at = p.positions ? given[i] : pos;
+    double turns = double(at) * double(freq[i]) * 0.15915494309189533577;   // 1 / (2 pi)
     turns -= rint(turns);
     float sn, cn;
     sincospif(2.f * float(turns), &sn, &cn);
