@@ -330,7 +330,7 @@ vegas_status_t vegas_decode_iteration(
  *   workspace: vegas_prompt_workspace_size() bytes for the same total_rows,
  *        batch and kv (a larger one serves smaller calls of the same device;
  *        not one that other entry points use), 256-byte aligned
- * Supported: head_dim 64 and 128, G <= 64, softmax_scale > 0.
+ * Supported: head_dim 64 and 128, G <= 64, 0 < softmax_scale <= 2^100.
  * ---------------------------------------------------------------------- */
 vegas_status_t vegas_rope_append(
     const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -369,7 +369,8 @@ vegas_status_t vegas_prompt_attn(
  *   logprob, entropy: device fp32 [rows]; rank: device int32 [rows]; each may
  *           be NULL
  *   top_ids, top_logprobs: device int32 / fp32 [rows][top_n]
- * Supported: top_n in [0, 32], rows <= 2^26, vocab <= 2^28.  No workspace.
+ * Supported: top_n in [0, 32], rows <= 2^26, vocab <= 2^28, inv_temperature in
+ * [2^-100, 2^100].  No workspace.
  * ---------------------------------------------------------------------- */
 #define VEGAS_DTYPE_BF16 0
 #define VEGAS_DTYPE_FP32 1

@@ -750,6 +750,9 @@ VEGAS_API vegas_status_t vegas_rope_append(
     return fail(VEGAS_ERR_INVALID_ARG, "pair_axis is NULL with %d axes", num_axes);
   if (!std::isfinite(rope_scale)) return fail(VEGAS_ERR_INVALID_ARG, "rope_scale not finite");
   if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  if (q_out == q && q_stride != (int64_t)kv->num_q_heads * d)   // rows would overwrite later ones
+    return fail(VEGAS_ERR_INVALID_ARG, "q_out is q, but q_stride %lld is not %d",
+                (long long)q_stride, kv->num_q_heads * d);
   int* err = nullptr;
   if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
   vegas::RopeParams p{};
@@ -807,6 +810,8 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
     return fail(VEGAS_ERR_INVALID_ARG, "out must be a 32-byte aligned pointer");
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
     return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale must be finite and positive");
+  if (softmax_scale > 0x1p100f)   // (its product with log2 e may leave fp32)
+    return fail(VEGAS_ERR_UNSUPPORTED, "softmax_scale %g above 2^100", (double)softmax_scale);
   const int G = kv->num_q_heads / kv->num_kv_heads;
   if (G > kMaxPromptGroup)
     return fail(VEGAS_ERR_UNSUPPORTED, "group size %d (at most %d)", G, kMaxPromptGroup);
@@ -814,6 +819,8 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
     return fail(VEGAS_ERR_UNSUPPORTED, "%d rows of %d KV heads: too many for one call", total_rows,
                 kv->num_kv_heads);
   if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  if (out == q)   // a query tile may be read after another CTA has written its rows
+    return fail(VEGAS_ERR_INVALID_ARG, "out is q");
   int* err = nullptr;
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
@@ -876,6 +883,10 @@ VEGAS_API vegas_status_t vegas_token_logprobs(const void* logits, int dtype, int
                 vocab);
   if (!std::isfinite(inv_temperature) || !(inv_temperature > 0.f))
     return fail(VEGAS_ERR_INVALID_ARG, "inv_temperature must be finite and positive");
+  // outside, a times a difference of logits, or the distance that 8 powers of two are, leaves fp32
+  if (inv_temperature < 0x1p-100f || inv_temperature > 0x1p100f)
+    return fail(VEGAS_ERR_UNSUPPORTED, "inv_temperature %g outside [2^-100, 2^100]",
+                (double)inv_temperature);
   if ((logprob || rank) && !tokens)
     return fail(VEGAS_ERR_INVALID_ARG, "logprob and rank need tokens");
   if (top_n < 0 || top_n > vegas::kMaxTopLogprobs)

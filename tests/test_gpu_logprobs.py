@@ -186,3 +186,12 @@ def test_a_token_outside_the_vocabulary_is_recorded():
         vg.vegas_read_device_status()
     assert ei.value.status == 5
     assert float(out["logprob"][1]) == 0 and int(out["rank"][1]) == -1
+
+
+@pytest.mark.parametrize("inv_t", [2.0 ** -100, 1e-20, 1e20, 2.0 ** 100])
+def test_temperatures_at_the_ends_of_the_range(inv_t):
+    x, tok = logits(4, 9000, torch.float32, 10)
+    x[1, 100:5000] = -math.inf
+    x[2, 100:5000] = torch.finfo(torch.float32).min
+    x[3, 7] = 1e38
+    check(run(x, tok, 5, inv_t), x, tok, 5, inv_t)

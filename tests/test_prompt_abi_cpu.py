@@ -91,3 +91,31 @@ def test_token_logprobs_refusals(vg):  # noqa: F811
             (dict(logprob=None, entropy=None, rank=None, top_n=0), 1, "no output")):
         _refused(lambda: vg.vegas_token_logprobs(**{**good, **change}), status, word)
     vg.vegas_token_logprobs(**{**good, "rows": 0})
+
+
+def test_scales_whose_exponents_overflow_are_refused(vg):  # noqa: F811
+    good = dict(logits=16, dtype=vg.VEGAS_BF16, row_stride=100, tokens=16, rows=0, vocab=100,
+                inv_temperature=1.0, logprob=16, entropy=16, rank=16, top_n=2, top_ids=16,
+                top_logprobs=16, stream=0)
+    for t in (1e-38, 2.0 ** -101, 2.0 ** 101, 3e38):
+        _refused(lambda: vg.vegas_token_logprobs(**{**good, "inv_temperature": t}), 2,
+                 "inv_temperature")
+    for t in (2.0 ** -100, 2.0 ** 100):
+        vg.vegas_token_logprobs(**{**good, "inv_temperature": t})
+    kv = vg.PagedKV(16, 16, 16, 4, 16, 8, 2, 64, 4)
+    good = dict(kv=kv, q=16, q_stride=512, out=32, row_start=16, ctx_lens=16, total_rows=0,
+                batch=1, softmax_scale=0.1, workspace=256, workspace_bytes=1 << 30, stream=0)
+    _refused(lambda: vg.vegas_prompt_attn(**{**good, "softmax_scale": 3e38}), 2, "softmax_scale")
+    vg.vegas_prompt_attn(**{**good, "softmax_scale": 2.0 ** 100})
+
+
+def test_outputs_over_inputs_are_refused(vg):  # noqa: F811
+    kv = vg.PagedKV(16, 16, 16, 4, 16, 8, 2, 64, 4)
+    _refused(lambda: vg.vegas_prompt_attn(
+        kv=kv, q=512, q_stride=512, out=512, row_start=16, ctx_lens=16, total_rows=5, batch=1,
+        softmax_scale=0.1, workspace=256, workspace_bytes=1 << 30, stream=0), 1, "out is q")
+    _refused(lambda: vg.vegas_rope_append(
+        kv=kv, q=16, q_stride=768, k=1040, k_stride=768, v=1296, v_stride=768, q_out=16,
+        row_start=16, ctx_lens=16, positions=None, pair_axis=None, num_axes=1, inv_freq=16,
+        rot_dim=64, interleaved=False, rope_scale=1.0, total_rows=5, batch=1, stream=0),
+        1, "q_out is q")
