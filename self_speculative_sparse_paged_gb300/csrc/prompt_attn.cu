@@ -14,15 +14,23 @@
 //   S_X[128 x 128] = Q_X . K^T      (both operands in shared memory, K-major)
 //   O_X[128 x D]  += P_X . V        (P_X in tensor memory, V MN-major)
 // with S_A, S_B, O_A, O_B in tensor memory; P_X (bf16) overwrites the first 64
-// columns of S_X (at head_dim 64 there is room for it elsewhere, so that S(t + 1)
-// need not wait for P(t): no faster, the softmax sets the pace there).  The softmax is the running one: thread r of X's warpgroup
-// owns row r (tensor-memory lane r) and keeps the row's reference m and sum l
-// in registers.  m is the row's maximum over the item's first tile; any other
-// reference gives the same quotient, so later tiles take p = 2^(x - m) without
-// looking for their maximum and only check the sum of each part of the tile:
-// past 2^20 (or where nothing had been seen) m is raised to the part's maximum,
-// l and the row of O are rescaled, and the part is taken again.  bf16 and fp32
-// hold numbers of that size as exactly as smaller ones.
+// columns of S_X at head_dim 128, which fills tensor memory, and has columns of
+// its own at 64, where the next S follows as soon as this one is read.  The
+// softmax is the running one: thread r of X's warpgroup owns row r
+// (tensor-memory lane r) and keeps the row's reference m and sum l in registers.
+// m is the row's maximum over the item's first tile; any other reference gives
+// the same quotient, so later tiles take p = 2^(scale s - M), M = fl(scale m), in
+// one fused multiply-add, without looking for their maximum, and only check the
+// tile's sum: past 2^20 (or where nothing had been seen) m is raised to the tile's
+// maximum, l and the row of O are rescaled, and the tile is taken again.  bf16 and
+// fp32 hold numbers of that size as exactly as smaller ones.  Where M itself is
+// past 2^20, what its rounding leaves would show: there the tile is always taken
+// again, as 2^(scale (s - m)).
+//
+// The sum is checked once a tile: with a check in the middle (to hand P over in
+// halves) the two halves' instructions could not overlap, which cost more than the
+// earlier product gained (8192 rows of 64-wide heads 592 us with it, 539 without,
+// 514 with the fused multiply-add too).
 //
 // Warps 0-3: softmax of A; 4-7: softmax of B; 8, 9: TMA of K and V tiles into
 // one ring; 10: MMA issue; 11: walks the CTA's items, publishes them in a small
@@ -63,10 +71,8 @@ constexpr int kFewRows = 32;          // an item of at most so many rows is shar
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr int kSplitCostFew = 128;    // the same for items of few rows
 constexpr float kNoMax = -3e38f;      // reference of a row that has seen nothing
-// Parts of a tile whose P goes to the tensor cores by itself.  (Four parts: 16K prompt 10 % slower.)
-constexpr int kParts = 2;
-constexpr int kPart = kTile / kParts; // positions per part
-constexpr float kSumLimit = 1048576.f;   // a part's sum that makes a row raise its reference
+constexpr float kSumLimit = 1048576.f;   // a tile's sum that makes a row raise its reference
+constexpr float kBigRef = 1048576.f;     // a scaled reference whose rounding would show
 
 // An item, or the part of it in one CTA's range, as published to all warps.
 struct Piece {
@@ -85,17 +91,21 @@ struct PCfg {
   static constexpr int kQ = kHalves * 128 * 128;      // one query tile [half][128 rows][128 B]
   static constexpr int kSlot = kHalves * 128 * 128;   // one K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 10;
-  // At head_dim 64 shared memory has room for the next item's query tiles.
+  // At head_dim 64 tensor memory has room for P beside S, so the next S is computed as soon as
+  // the softmax has read this one, and shared memory for the next item's query tiles.
+  static constexpr bool kOwnP = D == 64;
   static constexpr int kQBufs = D == 64 ? 2 : 1;
   static constexpr int kOffRing = 2 * kQBufs * kQ;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 2 * kParts + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffPieces = kOffMisc + 112;
   static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
   static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
   static constexpr uint32_t kO = 256;                  // first tensor-memory column of O_A
+  static constexpr uint32_t kP = kOwnP ? 384 : 0;      // ... of P_A, and the step to P_B
+  static constexpr uint32_t kPStep = kOwnP ? 64 : 128;
 };
 
 // One point of the linear order of all (sequence, KV head, query-tile pair) items.
@@ -425,12 +435,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto full = [&](uint32_t s) { return bar0 + 8 * s; };
   auto freed = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   auto sfull = [&](int x) { return bar0 + 8 * (2 * NS + x); };
-  constexpr int B1 = 2 * NS + 2 + 2 * kParts, QB = Cfg::kQBufs, B2 = B1 + 4 + 2 * QB;
-  auto pready = [&](int x, int h) { return bar0 + 8 * (2 * NS + 2 + kParts * x + h); };
-  auto odone = [&](int x) { return bar0 + 8 * (B1 + x); };
-  auto pvpart = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
-  auto qfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 4 + i % QB); };
-  auto qfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 4 + QB + i % QB); };
+  constexpr int B1 = 2 * NS + 2, QB = Cfg::kQBufs, B2 = B1 + 6 + 2 * QB;
+  auto pready = [&](int x) { return bar0 + 8 * (B1 + x); };
+  auto odone = [&](int x) { return bar0 + 8 * (B1 + 2 + x); };
+  auto sread = [&](int x) { return bar0 + 8 * (B1 + 4 + x); };
+  auto qfull = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + i % QB); };
+  auto qfree = [&](uint32_t i) { return bar0 + 8 * (B1 + 6 + QB + i % QB); };
   const uint32_t drain = bar0 + 8 * B2, altfull = drain + 8, alttaken = drain + 16;
   auto pcfull = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + i); };
   auto pcfree = [&](uint32_t i) { return bar0 + 8 * (B2 + 3 + kPieces + i); };
@@ -451,9 +461,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(sfull(x), 1);
-      for (int h = 0; h < kParts; ++h) mbar_init(pready(x, h), 4);   // a warp each
+      mbar_init(pready(x), 4);   // a warp each
       mbar_init(odone(x), 1);
-      mbar_init(pvpart(x), 1);
+      mbar_init(sread(x), 4);
     }
     for (int i = 0; i < QB; ++i) {
       mbar_init(qfull(i), 1);
@@ -645,6 +655,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       };
       Ring kr{0, 0}, vr{1, 0};   // the next K to multiply, the next V
       uint32_t pa = 0, pb = 0;   // phases of A's and B's P
+      uint32_t ra = 0, rb = 0;   // and of their S being read (kOwnP)
       uint32_t items = 0;
       auto wait_k = [&]() { return mbar_wait_bounded(full(kr.s), kr.ph); };
       auto wait_v = [&]() { return mbar_wait_bounded(full(vr.s), vr.ph); };
@@ -666,23 +677,26 @@ __global__ void __launch_bounds__(kPThreads, 1)
                  bk + ((ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
         tc_commit(sfull(x));
       };
-      // O_X += P_X . V, part by part as the softmax finishes them; last: X's last tile here
+      // where P has its own place, S may be overwritten once the softmax has read it
+      auto wait_read = [&](int x) {
+        if constexpr (!Cfg::kOwnP) return true;
+        uint32_t& ph = x ? rb : ra;
+        const bool read = mbar_wait_bounded(sread(x), ph);
+        ph ^= 1;
+        return read;
+      };
+      // O_X += P_X . V, once the softmax has left P_X; last: X's last tile here
       auto issue_pv = [&](int x, bool accumulate, bool last) {
         uint32_t& ph = x ? pb : pa;
         const uint64_t bv = dVmn + (ring16 + vr.s * (Cfg::kSlot / 16));
+        if (!mbar_wait_bounded(pready(x), ph)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-          if (!mbar_wait_bounded(pready(x, h), ph)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kp = 0; kp < kPart / 16; ++kp)
-            tc_mma_ts(tmem + Cfg::kO + D * x,
-                      tmem + 128 * x + (kPart / 2) * h + 8 * kp,
-                      bv + (kPart / 16 * h + kp) * 128, idPV, accumulate || h > 0 || kp > 0);
-          if (h + 1 < kParts) tc_commit(pvpart(x));
-        }
+        for (int kp = 0; kp < kTile / 16; ++kp)
+          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + Cfg::kP + Cfg::kPStep * x + 8 * kp, bv + kp * 128,
+                    idPV, accumulate || kp > 0);
         ph ^= 1;
-        if (last) tc_commit(odone(x));
+        if (Cfg::kOwnP || last) tc_commit(odone(x));
         return true;
       };
       // false: a wait ran out
@@ -698,15 +712,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int x = 0; x < 2; ++x) {
             const int ex = x ? eb : ea;
             if (t >= ex) continue;
+            auto next_s = [&]() {
+              if (!wait_read(x)) return false;
+              if (t + 1 >= ex) return true;
+              if (!have_k && !wait_k()) return false;
+              have_k = true;
+              issue_s(x, x);
+              return true;
+            };
+            if (Cfg::kOwnP && !next_s()) return false;
             if (!have_v && !wait_v()) return false;
             have_v = true;
             if (!issue_pv(x, t > k0, t + 1 == ex)) return false;
-            if (x == 1 || t >= eb) free_v();
-            if (t + 1 >= ex) continue;
-            if (!have_k && !wait_k()) return false;
-            have_k = true;
-            issue_s(x, x);
+            if (!Cfg::kOwnP) {
+              if (x == 1 || t >= eb) free_v();
+              if (!next_s()) return false;
+            }
           }
+          if (Cfg::kOwnP) free_v();
           if (t + 1 < k1) {
             free_k();
             if (t + 2 == k1) tc_commit(qfree(items));
@@ -724,13 +747,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (tiles <= 2) tc_commit(qfree(items));
         for (int i = 0; i < tiles; ++i) {
           const int x = i & 1;
+          auto next_s = [&]() {
+            if (!wait_read(x)) return false;
+            if (i + 2 >= tiles) return true;
+            if (!wait_k()) return false;
+            issue_s(x, 0);
+            free_k();
+            if (i + 3 == tiles) tc_commit(qfree(items));
+            return true;
+          };
+          if (Cfg::kOwnP && !next_s()) return false;
           if (!wait_v() || !issue_pv(x, i >= 2, i + 2 >= tiles)) return false;
           free_v();
-          if (i + 2 >= tiles) continue;
-          if (!wait_k()) return false;
-          issue_s(x, 0);
-          free_k();
-          if (i + 3 == tiles) tc_commit(qfree(items));
+          if (!Cfg::kOwnP && !next_s()) return false;
         }
         return true;
       };
@@ -764,9 +793,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int x = warp >> 2;
     const int r = tid & 127;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x;
+    const uint32_t scol = 128 * x, ocol = Cfg::kO + D * x, pcol = Cfg::kP + Cfg::kPStep * x;
     uint32_t c = 0, ns = 0, no = 0;   // ring tiles, S tiles, finished items of X
     uint32_t nalt = 0;                // items that A and B shared
+    // A row's exponents are scale * logit - M with M = m * scale rounded once, which any other
+    // reference could replace; residue() is what the rounding left, for states of another m.
+    // Where M is so large that its rounding would show, the difference is taken before scaling.
+    auto residue = [&](float of) {
+      const float M = of * q.scale_log2;
+      return fabsf(M) < kBigRef ? fmaf(of, q.scale_log2, -M) : 0.f;
+    };
+    // the factor that takes a state of reference `from` to the reference `to`
+    auto moved = [&](float from, float to) {
+      return ex2(fmaf(from - to, q.scale_log2, residue(to) - residue(from)));
+    };
     // The item's fields stay in shared memory until its end: the tile loop needs the registers.
     auto release = [&]() {
       __syncwarp();
@@ -809,6 +849,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
         tmem_ld_wait();
+        if constexpr (Cfg::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sread(x));
+        }
         if (diagonal) {   // whatever the logits hold
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -835,66 +880,67 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2);
-#pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-          constexpr int P = kPart;
-          uint32_t pk[P / 2];   // P to 8 bits of mantissa: the tensor cores' operand type
-          float hs;
-          auto take = [&]() {
-            const uint64_t nm2 = pair_f32(-m, -m);
-            uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int e = 0; e < P / 2; ++e) {
-              float a, b;
-              unpair_f32(mul_f32x2(add_f32x2(pair_f32(s[P * h + 2 * e], s[P * h + 2 * e + 1]), nm2), sc2),
-                         a, b);
-              a = ex2(a);
-              b = ex2(b);
-              sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
-              pk[e] = pack_bf16x2(a, b);
-              // (nothing reads it before this part's arrival)
-              if ((e & 15) == 15) tmem_st16(tl + scol + P / 2 * h + (e & 16), pk + (e & 16));
-            }
-            float la, lb;
-            unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
-            hs = la + lb;
-          };
-          take();
-          if (__any_sync(0xffffffffu, !(hs < kSumLimit) && live)) {
-            float mx = s[P * h];
-#pragma unroll
-            for (int i = 1; i < P; ++i) mx = fmaxf(mx, s[P * h + i]);
-            const float m2 = fmaxf(m, mx);
-            const float f = ex2((m - m2) * q.scale_log2);
-            m = m2;
-            l *= f;
-            // O holds the row's earlier tiles (S of this one was issued after their
-            // products), and from the second part on this tile's earlier parts
-            static_assert(kParts == 2, "one pvpart phase a tile");
-            if (h > 0)
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvpart(x), (ns - 1) & 1)) && ok;
+        if constexpr (Cfg::kOwnP) {
+          if (t > kbeg) {   // the last tile's P has been used (and its O is complete)
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
+            ++no;
             tc_fence_after();
-            if (t > kbeg || h > 0) {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                float o[16];
-                tmem_ld16(tl + ocol + 16 * i, o);
-                tmem_ld_wait();
-                uint32_t ob[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
-                tmem_st16(tl + ocol + 16 * i, ob);
-              }
-            }
-            take();
           }
-          l += hs;
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pready(x, h));
         }
+        const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2);
+        uint32_t pk[kTile / 2];   // P to 8 bits of mantissa: the tensor cores' operand type
+        float ts;
+        auto take = [&](auto exponents) {
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int e = 0; e < kTile / 2; ++e) {
+            float a, b;
+            unpair_f32(exponents(pair_f32(s[2 * e], s[2 * e + 1])), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
+            pk[e] = pack_bf16x2(a, b);
+            // (nothing reads it before this tile's arrival)
+            if ((e & 15) == 15) tmem_st16(tl + pcol + (e - 15), pk + (e - 15));
+          }
+          float la, lb;
+          unpair_f32(add_f32x2(sum[0], sum[1]), la, lb);
+          ts = la + lb;
+        };
+        {
+          const float M = m * q.scale_log2, nm = fabsf(M) < kBigRef ? -M : NAN;
+          const uint64_t nm2 = pair_f32(nm, nm);
+          take([&](uint64_t v) { return fma_f32x2(v, sc2, nm2); });
+        }
+        if (__any_sync(0xffffffffu, !(ts < kSumLimit) && live)) {
+          float mx = s[0];
+#pragma unroll
+          for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
+          const float m2 = fmaxf(m, mx);
+          const float f = moved(m, m2);
+          m = m2;
+          l *= f;
+          if (t > kbeg) {   // O holds the row's earlier tiles, complete (S came after them, or waited for)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              float o[16];
+              tmem_ld16(tl + ocol + 16 * i, o);
+              tmem_ld_wait();
+              uint32_t ob[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
+              tmem_st16(tl + ocol + 16 * i, ob);
+            }
+          }
+          const float rest = residue(m);
+          const uint64_t nm2 = pair_f32(-m, -m), rest2 = pair_f32(rest, rest);
+          take([&](uint64_t v) { return fma_f32x2(add_f32x2(v, nm2), sc2, rest2); });
+        }
+        l += ts;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready(x));
         if (!ok) break;
       }
       c += w.k1 - w.k0;
@@ -918,7 +964,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (ok && w.k1 - w.k0 > 1) {
             const float2 b = alt_ml[lane];
             const float m2 = fmaxf(m, b.x);
-            const float fa = ex2((m - m2) * q.scale_log2), fb = ex2((b.x - m2) * q.scale_log2);
+            const float fa = moved(m, m2), fb = moved(b.x, m2);
             m = m2;
             l = fa * l + fb * b.y;
 #pragma unroll 1
@@ -1039,7 +1085,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const size_t sl = slot_of(cc, x);
                 const float2 v = __ldcg(&ml[sl * 128 + rr]);
                 const float4 o = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
-                const float f = ex2((v.x - mm) * q.scale_log2);
+                const float f = moved(v.x, mm);
                 lsum = fmaf(f, v.y, lsum);
                 acc.x = fmaf(f, o.x, acc.x);
                 acc.y = fmaf(f, o.y, acc.y);
@@ -1070,7 +1116,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (cc != me) mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x);
           for (int cc = first; cc <= last; ++cc) {
             const float2 v = cc == me ? make_float2(m, l) : __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]);
-            lsum = fmaf(ex2((v.x - mm) * q.scale_log2), v.y, lsum);
+            lsum = fmaf(moved(v.x, mm), v.y, lsum);
           }
           const float inv = 1.f / lsum;
           __nv_bfloat16* o_row = out_row(rr);
@@ -1080,15 +1126,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
           for (int j = 0; j < 3; ++j)
             fj[j] = j < others
-                        ? ex2((__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x - mm) * q.scale_log2)
+                        ? moved(__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x, mm)
                         : 0.f;
           auto factor = [&](int j) {
             return j == 0   ? fj[0]
                    : j == 1 ? fj[1]
                    : j == 2
                        ? fj[2]
-                       : ex2((__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x - mm) *
-                             q.scale_log2);
+                       : moved(__ldcg(&ml[size_t(slot_of(other(j), x)) * 128 + rr]).x, mm);
           };
           float4 next[8];
           auto fetch = [&](int i, int j) {   // columns 32 i .. of the j-th other state
@@ -1097,7 +1142,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int e = 0; e < 8; ++e) next[e] = __ldcg(&src[(8 * i + e) * 128]);
           };
           fetch(0, 0);
-          const float fo = any ? ex2((m - mm) * q.scale_log2) : 0.f;
+          const float fo = any ? moved(m, mm) : 0.f;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             float o[32], acc[32];

@@ -323,3 +323,46 @@ def test_very_low_logits_are_no_mask():
     ref = mean[100:, :, None, :]
     assert ((got - ref).abs() <= 2.0 ** -7 * (ref.abs() + 1)).all()
     vg.vegas_read_device_status()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,ctx", [([40], [900]), ([1, 1], [9000, 700]), ([600], [5000]), ([200, 3], [0, 2000])])
+@pytest.mark.parametrize("levels", [(0, 2 ** 19), (2 ** 21, 0), (-2 ** 22, -2 ** 22), (2 ** 22, 2 ** 22),
+                                    (2 ** 20, 2 ** 19, 2 ** 22), (-2 ** 21, -2 ** 19)])
+def test_references_of_any_size(d, rows, ctx, levels):
+    """Logits level + 0 .. -20, exact in fp32, the level changing every 150 positions.
+
+    Only the greatest level seen counts; there |s - m| <= 20, so an exponent (rounded scale and
+    log2 e, one fused step) is off by less than 20 * 1.45 * 3 * 2^-24 < 2^-17, the exponential and
+    the fp32 sums by 2^-16 more: 2^-14 A beside the roundings of P and of the output.
+    """
+    c = Prompt(8, 2, d, rows, ctx, seed=11)
+    c.scale = 1.0
+    g = torch.Generator(device=DEV).manual_seed(12)
+    c.q.zero_()
+    c.q.view(c.total, -1, d)[:, :, :2] = 1
+    for b, n in enumerate(rows):
+        L = ctx[b] + n
+        pos = torch.arange(L, device=DEV)
+        pg = torch.from_numpy(c.table[b].astype(np.int64)).to(DEV)[pos // 16]
+        kk = torch.zeros((L, 2, d), device=DEV)
+        kk[:, :, 0] = torch.tensor(levels, device=DEV, dtype=torch.float32)[(pos // 150) % len(levels)][:, None]
+        kk[:, :, 1] = -torch.randint(0, 21, (L, 2), generator=g, device=DEV).float()
+        c.k[pg, :, pos % 16] = kk.bfloat16()
+    c.run()
+    at = 0
+    for b, n in enumerate(rows):
+        L = ctx[b] + n
+        pg = torch.from_numpy(c.table[b, :(L + 15) // 16].astype(np.int64)).to(DEV)
+        for h in (0, 7):
+            k = c.k[pg, h // 4].reshape(-1, d)[:L].double()
+            v = c.v[pg, h // 4].reshape(-1, d)[:L].double()
+            x = c.q[at:at + n, h * d:(h + 1) * d].double() @ k.t()
+            seen = torch.arange(L, device=DEV)[None] <= (ctx[b] + torch.arange(n, device=DEV))[:, None]
+            p = torch.softmax(torch.where(seen, x, -math.inf), -1)
+            ref, A = p @ v, p @ v.abs()
+            worst = ((c.out[at:at + n, h].double() - ref).abs() /
+                     (1.01 * 2.0 ** -8 * (ref.abs() + A) + 2.0 ** -14 * A)).max()
+            assert worst <= 1, (b, h, float(worst))
+        at += n
+    vg.vegas_read_device_status()
