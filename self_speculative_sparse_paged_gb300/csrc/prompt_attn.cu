@@ -70,6 +70,9 @@ constexpr int kMinShare = 256;        // a CTA's least share of the cost, in pos
 constexpr int kFewRows = 32;          // an item of at most so many rows is shared by A and B (and joined by any thread)
 constexpr int kSplitCost = 1024;      // what sharing items costs a CTA, in positions
 constexpr int kSplitCostFew = 128;    // the same for items of few rows
+// Time of a KV tile of an item of few rows, of a tile of two full query tiles (1850 / 2700 cycles).
+constexpr float kFewWeight = 0.69f;
+constexpr int kFew = 1, kMany = 2;    // sequences of at most kFewRows query rows a KV head, and others
 constexpr float kNoMax = -3e38f;      // reference of a row that has seen nothing
 constexpr float kSumLimit = 1048576.f;   // a tile's sum that makes a row raise its reference
 constexpr float kBigRef = 1048576.f;     // a scaled reference whose rounding would show
@@ -127,10 +130,10 @@ __device__ __forceinline__ int pairs_in(const PromptParams& q, int n) {
   return (int)__umulhi((uint32_t)n, q.pair_inverse);
 }
 
-// floor(a / b) for a quotient below 2^20: one fp32 division, put right (a 64-bit
+// floor(a / b) for a quotient below 2^20: a fast fp32 division, put right (a 64-bit
 // integer division takes several hundred cycles at the start of every call).
 __device__ __forceinline__ int small_quotient(long long a, long long b) {
-  long long q = (long long)((float)a / (float)b);
+  long long q = (long long)__fdividef((float)a, (float)b);
   while (q * b > a) --q;
   while ((q + 1) * b <= a) ++q;
   return (int)q;
@@ -143,7 +146,8 @@ __device__ __forceinline__ long long share_begin(int i, long long total, int n) 
   return (long long)i * q + (unsigned)i * r / n;
 }
 
-__device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
+// A sequence that is not of one of the given classes counts as empty.
+__device__ __forceinline__ Seq load_seq(const PromptParams& q, int s, int classes) {
   Seq r;
   r.row0 = q.row_start[s];
   const int end = q.row_start[s + 1];
@@ -155,6 +159,7 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s) {
     set_error(q.err, kErrDeviceFault);
     r.n = 0;
   }
+  if (!(classes & (r.n * q.group <= kFewRows ? kFew : kMany))) r.n = 0;
   r.pairs = pairs_in(q, r.n + q.pair_tokens - 1);
   const long long P = r.pairs;
   r.per_head = P * (r.ctx + kItemCost) + q.pair_tokens * (P * (P + 1) / 2);
@@ -173,12 +178,13 @@ __device__ __forceinline__ int tiles_of(const PromptParams& q, const Seq& s, int
   return (s.ctx + last) / kTile + 1;
 }
 
-// What the division of the work goes by, the same in every CTA.
+// What the division of the work goes by, the same in every CTA that works on the same classes.
 struct Division {
-  long long total;     // summed cost of all items
+  long long total;     // summed cost of the classes' items
   int items;
-  int ncta;            // CTAs that take part
+  int ncta;            // CTAs that take part: base .. base + ncta - 1
   int whole;           // 1: items are dealt out whole, longest first; 0: equal ranges of the cost
+  int classes, base;
 };
 
 // Items by falling cost: positions up to the item's last row, as ctx + (p + 1) * pair_tokens.
@@ -193,6 +199,15 @@ __device__ __forceinline__ int items_from(const PromptParams& q, const Seq& s, i
 // The item of rank k (whole warp; sq: lane's sequence; hi: an upper bound of its cost, lowered to it).
 __device__ __forceinline__ void ranked(const PromptParams& q, const Seq& sq, int k, int& hi, int& seq,
                                        int& g, int& p) {
+  const unsigned active = __ballot_sync(0xffffffffu, sq.pairs > 0);
+  if ((active & (active - 1)) == 0) {   // one sequence: its last pairs first, a pair's heads in order
+    seq = __ffs(active) - 1;
+    const int back = k / q.hkv;
+    g = k - back * q.hkv;
+    p = __shfl_sync(0xffffffffu, sq.pairs, seq & 31) - 1 - back;
+    hi = __shfl_sync(0xffffffffu, sq.ctx, seq & 31) + (p + 1) * q.pair_tokens;
+    return;
+  }
   int lo = 0;                       // the largest cost c with more than k items of cost >= c
   while (lo < hi) {
     const int mid = lo + (hi - lo + 1) / 2;
@@ -212,49 +227,113 @@ __device__ __forceinline__ void ranked(const PromptParams& q, const Seq& sq, int
   p = __shfl_sync(0xffffffffu, mine, seq & 31);
 }
 
+// The work of one class, from all lanes' sequences.
+struct Load {
+  long long total;
+  int items, longest;   // longest: positions of the longest sequence with rows
+};
+
+__device__ __forceinline__ Load sum_load(const PromptParams& q, long long w, int items, int longest) {
+  // (24 bits at a time: reductions take a tenth of a 64-bit butterfly's time)
+  const unsigned w0 = __reduce_add_sync(0xffffffffu, (unsigned)w & 0xffffffu);
+  const unsigned w1 = __reduce_add_sync(0xffffffffu, (unsigned)(w >> 24) & 0xffffffu);
+  const unsigned w2 = __reduce_add_sync(0xffffffffu, (unsigned)(w >> 48));
+  Load r;
+  r.total = (((long long)w2 << 48) + ((long long)w1 << 24) + w0) * q.hkv;
+  r.items = __reduce_add_sync(0xffffffffu, items) * q.hkv;
+  r.longest = __reduce_max_sync(0xffffffffu, longest);
+  return r;
+}
+
 // Whole items keep every CTA busy when there are enough of them: the makespan is then about the
 // mean plus the part of the last round's items that not every CTA gets, and at least the longest
 // item.  Splitting costs a CTA the partial states it writes and joins (kSplitCost).
+//
+// Where some sequences have few rows (decode) and others many (prompts), a part of the CTAs takes
+// the ones, the rest the others: prompts' items can then stay whole, and the split ones are those
+// that are cheap to join.  Every number of CTAs is tried, against all CTAs taking both.
+// (A 509-row chunk with decode rows of 8100 positions and fewer: 35.5 us without.)
 __device__ __forceinline__ Division divide(const PromptParams& q) {
-  const int lane = threadIdx.x & 31;
-  long long w = 0;
-  int items = 0, longest = 0, rows = 0;
-  Seq sq{};
+  const int lane = threadIdx.x & 31, grid = gridDim.x;
+  long long wf = 0, wm = 0;
+  int itf = 0, itm = 0, lf = 0, lm = 0;
   for (int s = lane; s < q.batch; s += 32) {
-    sq = load_seq(q, s);
-    w += sq.per_head;
-    items += sq.pairs;
-    if (sq.n > 0) longest = max(longest, sq.ctx + sq.n);
-    rows = max(rows, sq.n);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-  Division d;
-  d.total = w * q.hkv;
-  d.items = __reduce_add_sync(0xffffffffu, items) * q.hkv;
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  const int grid = gridDim.x;
-  d.ncta = (int)min((long long)grid, max(1ll, d.total / kMinShare));   // (a shift)
-  d.whole = 0;
-  rows = __reduce_max_sync(0xffffffffu, rows) * q.group;
-  const long long limit = share_begin(1, d.total, d.ncta) + (rows <= kFewRows ? kSplitCostFew : kSplitCost);
-  if (q.batch <= 32 && longest + kItemCost <= limit) {
-    long long span = 0;
-    const int rounds = (d.items + grid - 1) / grid, rest = d.items - (rounds - 1) * grid;
-    if (rounds > 1 && rest < grid) {
-      int cost = longest + q.pair_tokens, seq, g, p;
-      ranked(q, sq, (rounds - 1) * grid, cost, seq, g, p);
-      span = share_begin(grid - rest, cost + kItemCost, grid);
+    const Seq sq = load_seq(q, s, kFew | kMany);
+    const int len = sq.n > 0 ? sq.ctx + sq.n : 0;
+    if (sq.n * q.group <= kFewRows) {
+      wf += sq.per_head;
+      itf += sq.pairs;
+      lf = max(lf, len);
+    } else {
+      wm += sq.per_head;
+      itm += sq.pairs;
+      lm = max(lm, len);
     }
-    d.whole = share_begin(1, d.total, grid) + span <= limit;
   }
-  if (d.whole) d.ncta = grid;
+  const Load few = sum_load(q, wf, itf, lf), many = sum_load(q, wm, itm, lm);
+  Division d;
+  d.classes = kFew | kMany;
+  d.base = 0;
+  d.total = few.total + many.total;
+  d.items = few.items + many.items;
+  d.whole = 0;
+  const bool can_deal = q.batch <= 32;   // (ranked() holds a sequence a lane)
+  int n = grid, longest = max(few.longest, many.longest);
+  if (few.items > 0 && many.items > 0) {
+    const float wmany = (float)many.total, wfew = (float)few.total * kFewWeight;
+    float best = INFINITY;
+    int at = 0;   // CTAs for the sequences of many rows; 0: all CTAs take both
+    for (int c = lane; c < grid; c += 32) {
+      // makespans on n CTAs: in equal ranges, and dealt out whole (the part of the last round's
+      // items, at the mean cost, that not every CTA gets)
+      const float n = c ? c : grid, items = c ? many.items : d.items, w = c ? wmany : wmany + wfew;
+      const float each = __fdividef(1.f, n), mean = w * each;
+      const float rest = items - floorf(items * each) * n;
+      const float gap = rest > 0.5f ? (n - rest) * __fdividef(mean, items) : 0.f;
+      float t = mean + kSplitCost;
+      if (can_deal) t = fminf(t, fmaxf((c ? many.longest : longest) + kItemCost, mean + gap));
+      if (c) t = fmaxf(t, __fdividef(wfew, grid - c) + kSplitCostFew);
+      if (t < best) {
+        best = t;
+        at = c;
+      }
+    }
+    const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(best));
+    const unsigned who = __ballot_sync(0xffffffffu, __float_as_uint(best) == least);
+    at = __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
+    if (at > 0) {
+      const bool mine = (int)blockIdx.x < at;
+      const Load& l = mine ? many : few;
+      d.classes = mine ? kMany : kFew;
+      d.base = mine ? 0 : at;
+      d.total = l.total;
+      d.items = l.items;
+      longest = l.longest;
+      n = mine ? at : grid - at;
+    }
+  }
+  d.ncta = (int)min((long long)n, max(1ll, d.total / kMinShare));   // (a shift)
+  const bool only_few = d.classes == kFew || many.items == 0;
+  const long long limit = share_begin(1, d.total, d.ncta) + (only_few ? kSplitCostFew : kSplitCost);
+  if (can_deal && longest + kItemCost <= limit) {
+    long long span = 0;
+    const int rounds = (d.items + n - 1) / n, rest = d.items - (rounds - 1) * n;
+    if (rounds > 1 && rest < n) {
+      Seq sq{};
+      if (lane < q.batch) sq = load_seq(q, lane, d.classes);
+      int cost = longest + q.pair_tokens, seq, g, p;
+      ranked(q, sq, (rounds - 1) * n, cost, seq, g, p);
+      span = share_begin(n - rest, cost + kItemCost, n);
+    }
+    d.whole = share_begin(1, d.total, n) + span <= limit;
+  }
+  if (d.whole) d.ncta = n;
   return d;
 }
 
 // The point at cost u, moved to an item boundary when it would leave fewer
 // than two tiles on one side of it (whole warp; every lane gets the result).
-__device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
+__device__ __forceinline__ Point locate(const PromptParams& q, int classes, long long u) {
   const int lane = threadIdx.x & 31;
   Point r;
   r.seq = q.batch;
@@ -264,7 +343,7 @@ __device__ __forceinline__ Point locate(const PromptParams& q, long long u) {
   for (int s0 = 0; s0 < q.batch; s0 += 32) {
     const int s = s0 + lane;
     Seq sq{};
-    if (s < q.batch) sq = load_seq(q, s);
+    if (s < q.batch) sq = load_seq(q, s, classes);
     const long long mine = sq.per_head * q.hkv;
     long long incl = mine;
 #pragma unroll
@@ -354,11 +433,11 @@ struct Walk {
     const int lane = threadIdx.x & 31;
     if (round == 0) {
       s = Seq{};
-      if (lane < q.batch) s = load_seq(q, lane);
+      if (lane < q.batch) s = load_seq(q, lane, d.classes);
       cost = __reduce_max_sync(0xffffffffu, s.pairs > 0 ? s.ctx + s.pairs * q.pair_tokens : 0);
     }
-    const int N = gridDim.x;
-    const int k = round * N + ((round & 1) ? N - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    const int N = d.ncta, me = (int)blockIdx.x - d.base;
+    const int k = round * N + ((round & 1) ? N - 1 - me : me);
     ++round;
     if (k >= d.items) return false;
     int seq, g, p;
@@ -376,7 +455,7 @@ struct Walk {
     while (true) {
       if (at.seq >= q.batch || at.seq > end.seq) return false;
       if (!have) {
-        s = load_seq(q, at.seq);
+        s = load_seq(q, at.seq, d.classes);
         have = true;
       }
       if (s.pairs == 0) {
@@ -395,8 +474,8 @@ struct Walk {
         // i >= ceil(x * ncta / total); those in [a, b) fall inside the item (locate()).
         const long long a = at.us + kItemCost + 2 * kTile - kTile / 2;
         const long long b = at.us + kItemCost + (long long)kTile * nt - 2 * kTile + kTile / 2;
-        w.first = small_quotient(a * d.ncta + d.total - 1, d.total) - 1;
-        w.last = small_quotient(b * d.ncta + d.total - 1, d.total) - 1;
+        w.first = d.base + small_quotient(a * d.ncta + d.total - 1, d.total) - 1;
+        w.last = d.base + small_quotient(b * d.ncta + d.total - 1, d.total) - 1;
       }
       if (stop) {
         at.seq = q.batch;   // done
@@ -490,14 +569,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // The CTA's range of the summed cost: warp 8 finds its begin, warp 9 its end.
   if (warp >= 8 && warp < 10) {
     const Division d = divide(q);
-    const int i = (int)blockIdx.x + (warp - 8);
+    const int i = (int)blockIdx.x - d.base + (warp - 8);
     Point pt;
     if (i >= d.ncta || d.total == 0 || d.whole) {
       pt.seq = q.batch;
       pt.g = pt.p = pt.k = 0;
       pt.us = d.total;
     } else {
-      pt = locate(q, share_begin(i, d.total, d.ncta));
+      pt = locate(q, d.classes, share_begin(i, d.total, d.ncta));
     }
     if (lane == 0) {
       int* e = ends + 6 * (warp - 8);
@@ -848,6 +927,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int cut = lim - pos0;   // the row's last visible position in the tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tl + scol + 32 * i, s + 32 * i);
+        if constexpr (Cfg::kOwnP) {
+          if (t > kbeg) {   // the last tile's P has been used (and its O is complete)
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
+            ++no;
+            tc_fence_after();
+          }
+        }
         tmem_ld_wait();
         if constexpr (Cfg::kOwnP) {
           tc_fence_before();
@@ -879,13 +965,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 *reinterpret_cast<uint4*>(row + h * 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-        }
-        if constexpr (Cfg::kOwnP) {
-          if (t > kbeg) {   // the last tile's P has been used (and its O is complete)
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(odone(x), no & 1)) && ok;
-            ++no;
-            tc_fence_after();
-          }
         }
         const uint64_t sc2 = pair_f32(q.scale_log2, q.scale_log2);
         uint32_t pk[kTile / 2];   // P to 8 bits of mantissa: the tensor cores' operand type
@@ -1068,29 +1147,45 @@ __global__ void __launch_bounds__(kPThreads, 1)
         leave();
         if (flags[x]) {
           __threadfence();
-          // thread r: row r % rows, every sub-th float4 of it, four states in flight
+          // thread r: row r % rows, every sub-th float4 of it, kJoin states in flight (those past
+          // the last are read again and count nothing: a remainder loop would take a state a round)
+          constexpr int kJoin = 8;
           const int subs = 128 / rows, rr = r % rows, sub = r / rows;
           if (sub < subs) {
             float mm = kNoMax;
-#pragma unroll 4
-            for (int cc = first; cc <= last; ++cc)
-              mm = fmaxf(mm, __ldcg(&ml[size_t(slot_of(cc, x)) * 128 + rr]).x);
+#pragma unroll 1
+            for (int c0 = first; c0 <= last; c0 += kJoin) {
+              float v[kJoin];
+#pragma unroll
+              for (int i = 0; i < kJoin; ++i)
+                v[i] = __ldcg(&ml[size_t(slot_of(min(c0 + i, last), x)) * 128 + rr]).x;
+#pragma unroll
+              for (int i = 0; i < kJoin; ++i) mm = fmaxf(mm, v[i]);
+            }
             __nv_bfloat16* o_row = out_row(rr);
 #pragma unroll 1
             for (int d4 = sub; d4 < D / 4; d4 += subs) {
               float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
               float lsum = 0.f;
-#pragma unroll 4
-              for (int cc = first; cc <= last; ++cc) {
-                const size_t sl = slot_of(cc, x);
-                const float2 v = __ldcg(&ml[sl * 128 + rr]);
-                const float4 o = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
-                const float f = moved(v.x, mm);
-                lsum = fmaf(f, v.y, lsum);
-                acc.x = fmaf(f, o.x, acc.x);
-                acc.y = fmaf(f, o.y, acc.y);
-                acc.z = fmaf(f, o.z, acc.z);
-                acc.w = fmaf(f, o.w, acc.w);
+#pragma unroll 1
+              for (int c0 = first; c0 <= last; c0 += kJoin) {
+                float2 v[kJoin];
+                float4 o[kJoin];
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i) {
+                  const size_t sl = slot_of(min(c0 + i, last), x);
+                  v[i] = __ldcg(&ml[sl * 128 + rr]);
+                  o[i] = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
+                }
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i) {
+                  const float f = c0 + i <= last ? moved(v[i].x, mm) : 0.f;
+                  lsum = fmaf(f, v[i].y, lsum);
+                  acc.x = fmaf(f, o[i].x, acc.x);
+                  acc.y = fmaf(f, o[i].y, acc.y);
+                  acc.z = fmaf(f, o[i].z, acc.z);
+                  acc.w = fmaf(f, o[i].w, acc.w);
+                }
               }
               const float inv = 1.f / lsum;
               *reinterpret_cast<uint2*>(o_row + 4 * d4) =
