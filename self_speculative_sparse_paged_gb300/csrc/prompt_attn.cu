@@ -44,11 +44,14 @@
 // inside an item; such an item's partial (m, l, O) go through the workspace and
 // the CTA that arrives last joins them in range order.  So a single decode row
 // with a long cache spreads over all SMs, with at most two partial items a CTA.
+// Sequences of few rows (decode) and of many (prompts) in one batch get CTAs of
+// their own, so that only items that are cheap to join are split: divide().
 //
 // What bounds it: at long lengths the tensor cores and the softmax together.  A
 // pair of tiles needs 2048 tensor cycles a KV tile at head_dim 128; the softmax
 // of one 128 x 128 tile takes a warp about 900 cycles alone and 750 when two
-// share a scheduler (ex2 issues every 4 cycles, beside conversions), and at
+// share a scheduler (ex2 issues every 4 cycles, beside conversions; in the kernel
+// 1100, where A and B, the fetches and the checks meet), and at
 // head_dim 128 S(t + 1) needs tensor memory that P(t) occupies, so a tile's
 // softmax and its two products follow one another and A and B overlap each
 // other's: 2700 cycles a KV tile measured.  A prompt of 16384 rows (32 query
@@ -962,7 +965,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int h = 0; h < Cfg::kHalves; ++h)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(row + h * 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(row + h * 16384 + 16 * ((e + r) & 7)) =
+                    make_uint4(0, 0, 0, 0);   // (8 lanes, 8 banks)
           }
           fence_proxy_async_smem();
         }
@@ -1164,33 +1168,40 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             __nv_bfloat16* o_row = out_row(rr);
 #pragma unroll 1
-            for (int d4 = sub; d4 < D / 4; d4 += subs) {
-              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int d0 = sub; d0 < D / 4; d0 += 2 * subs) {
+              const int d1 = min(d0 + subs, D / 4 - 1);   // (twice the last one at the end)
+              float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
               float lsum = 0.f;
 #pragma unroll 1
               for (int c0 = first; c0 <= last; c0 += kJoin) {
                 float2 v[kJoin];
-                float4 o[kJoin];
+                float4 o[kJoin][2];
 #pragma unroll
                 for (int i = 0; i < kJoin; ++i) {
                   const size_t sl = slot_of(min(c0 + i, last), x);
                   v[i] = __ldcg(&ml[sl * 128 + rr]);
-                  o[i] = __ldcg(&po[(sl * (D / 4) + d4) * 128 + rr]);
+                  o[i][0] = __ldcg(&po[(sl * (D / 4) + d0) * 128 + rr]);
+                  o[i][1] = __ldcg(&po[(sl * (D / 4) + d1) * 128 + rr]);
                 }
 #pragma unroll
                 for (int i = 0; i < kJoin; ++i) {
                   const float f = c0 + i <= last ? moved(v[i].x, mm) : 0.f;
                   lsum = fmaf(f, v[i].y, lsum);
-                  acc.x = fmaf(f, o[i].x, acc.x);
-                  acc.y = fmaf(f, o[i].y, acc.y);
-                  acc.z = fmaf(f, o[i].z, acc.z);
-                  acc.w = fmaf(f, o[i].w, acc.w);
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    acc[j].x = fmaf(f, o[i][j].x, acc[j].x);
+                    acc[j].y = fmaf(f, o[i][j].y, acc[j].y);
+                    acc[j].z = fmaf(f, o[i][j].z, acc[j].z);
+                    acc[j].w = fmaf(f, o[i][j].w, acc[j].w);
+                  }
                 }
               }
               const float inv = 1.f / lsum;
-              *reinterpret_cast<uint2*>(o_row + 4 * d4) =
-                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                             pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint2*>(o_row + 4 * (j ? d1 : d0)) =
+                    make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv),
+                               pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
             }
           }
           if (r == 0) *ticket = 0;

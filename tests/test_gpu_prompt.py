@@ -366,3 +366,21 @@ def test_references_of_any_size(d, rows, ctx, levels):
             assert worst <= 1, (b, h, float(worst))
         at += n
     vg.vegas_read_device_status()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 2, 64)])
+@pytest.mark.parametrize("rows,ctx", [
+    ([300, 1, 0, 1, 3], [700, 9000, 3, 5000, 4100]),       # a part of the CTAs for each kind
+    ([1, 1, 900, 2, 33], [20, 60, 0, 4000, 6000]),
+    ([1] * 40 + [200] + [1] * 9, [1000 + 77 * i for i in range(40)] + [500] + [9] * 9),
+    ([500, 400, 1], [0, 0, 0]),                            # next to nothing of the one kind
+    ([9, 1, 1], [0, 30000, 12000]),
+])
+def test_decode_rows_beside_prompts(hq, hkv, d, rows, ctx):
+    c = Prompt(hq, hkv, d, rows, ctx, seed=21, pad=1)
+    c.run()
+    c.check(heads=(0, hq // 2, hq - 1), rows=24)
+    first = c.out.clone()
+    c.out[:c.used] = 0
+    c.run()
+    assert torch.equal(first, c.out)
