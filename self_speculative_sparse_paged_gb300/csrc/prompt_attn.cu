@@ -54,11 +54,12 @@
 // 1100, where A and B, the fetches and the checks meet), and at
 // head_dim 128 S(t + 1) needs tensor memory that P(t) occupies, so a tile's
 // softmax and its two products follow one another and A and B overlap each
-// other's: 2700 cycles a KV tile measured.  A prompt of 16384 rows (32 query
-// heads of 128): 1261 us alone (1.74 PFLOP/s, 0.92 of the measured cuBLAS burst,
-// tensor pipe 75 % active), 1360-1400 us back to back (0.95 of cuBLAS sustained,
-// power-capped as that is); 1000 rows behind 31768 cached: 350 us (1.51 PFLOP/s).
-// One row each of eight sequences of 32000 positions: 160 us (6.6 TB/s).
+// other's: 2580 cycles a KV tile measured.  A prompt of 16384 rows (32 query
+// heads of 128): 1223 us alone (1.80 PFLOP/s, 0.95 of the measured cuBLAS burst,
+// tensor pipe 79 % active), 1305-1350 us back to back (power-capped, as cuBLAS
+// is); 1000 rows behind 31768 cached: 338 us alone (1.56 PFLOP/s).  At head_dim 64
+// the softmax alone sets the pace (7128 packed rows: 141 us).  One row each of
+// eight sequences of 32000 positions: 160 us (6.6 TB/s).
 #include "kernels.h"
 #include "vegas_common.cuh"
 
