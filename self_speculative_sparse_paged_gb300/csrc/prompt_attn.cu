@@ -55,7 +55,7 @@
 // head_dim 128 S(t + 1) needs tensor memory that P(t) occupies, so a tile's
 // softmax and its two products follow one another and A and B overlap each
 // other's: 2580 cycles a KV tile measured.  A prompt of 16384 rows (32 query
-// heads of 128): 1223 us alone (1.80 PFLOP/s, 0.95 of the measured cuBLAS burst,
+// heads of 128): 1223 us alone (1.80 PFLOP/s, 0.94 of the measured cuBLAS burst,
 // tensor pipe 79 % active), 1305-1350 us back to back (power-capped, as cuBLAS
 // is); 1000 rows behind 31768 cached: 338 us alone (1.56 PFLOP/s).  At head_dim 64
 // the softmax alone sets the pace (7128 packed rows: 141 us).  One row each of
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // slots past the sequence may hold anything: zero their V rows, as 0 * NaN is NaN
           const uint32_t j = 2 * (c + (t - w.k0)) + 1;
           const int kv_len = w.ctx + w.n;
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(j % NS), (j / NS) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(full(j % NS), (j / NS) & 1)) && ok;
           if (ok && pos0 + r >= kv_len) {
             uint8_t* row = smem + Cfg::kOffRing + (j % NS) * Cfg::kSlot + r * 128;
 #pragma unroll
