@@ -997,6 +997,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           take([&](uint64_t v) { return fma_f32x2(v, sc2, nm2); });
         }
         if (__any_sync(0xffffffffu, !(ts < kSumLimit) && live)) {
+          tmem_st_wait();   // stores are asynchronous: this P lies before the next goes over it
           float mx = s[0];
 #pragma unroll
           for (int i = 1; i < 128; ++i) mx = fmaxf(mx, s[i]);
