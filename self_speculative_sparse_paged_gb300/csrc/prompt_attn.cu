@@ -106,7 +106,7 @@ struct PCfg {
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
   static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kOffPieces = kOffMisc + 112;
+  static constexpr int kOffPieces = kOffMisc + 96;
   static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
   static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
@@ -531,13 +531,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
   Division* division = reinterpret_cast<Division*>(smem + Cfg::kOffMisc + 64);
-  int* failed = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 96);        // [2]
   float2* alt_ml = reinterpret_cast<float2*>(smem + Cfg::kOffAlt);
   Piece* pieces = reinterpret_cast<Piece*>(smem + Cfg::kOffPieces);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    failed[0] = failed[1] = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
       mbar_init(freed(s), 1);
@@ -896,13 +894,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) mbar_arrive(pcfree(pc % kPieces));
       ++pc;
     };
-    while (ok) {
+    // The group's four warps leave this loop together, by a vote that all of them see: here, or
+    // at the end of an item.  A warp that left by itself after a wait that ran out would be
+    // missed, for good, at the group's next barrier by warps whose wait just ended in time.
+    while (true) {
       const Piece& w = pieces[pc % kPieces];
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(pcfull(pc % kPieces), (pc / kPieces) & 1))) {
-        ok = false;
+      const bool got =
+          __all_sync(0xffffffffu, mbar_wait_bounded(pcfull(pc % kPieces), (pc / kPieces) & 1));
+      if (!got || w.seq < 0) {
+        ok = !named_bar_any(1 + x, 128, !got);
         break;
       }
-      if (w.seq < 0) break;
       const int kbeg = w.k0 + (w.alt ? x : 0), kstep = w.alt ? 2 : 1;
       const int kend = w.alt ? w.k1 : min(w.k1, (x ? w.nb : w.na));
       // lim: the last position this row may see (rows behind the sequence: its last);
@@ -1070,13 +1072,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       if (w.alt) ++nalt;
-      // a wait that ran out in one warp ends all four, which share the barriers below
-      if (!ok) failed[x] = 1;
-      named_bar(1 + x, 128);
-      if (failed[x]) {
-        ok = false;
-        break;
-      }
+      ok = !named_bar_any(1 + x, 128, !ok);
+      if (!ok) break;
       if ((x ? w.nb : w.na) == 0) {   // no such rows, or joined to A's
         release();
         continue;
