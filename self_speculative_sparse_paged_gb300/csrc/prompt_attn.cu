@@ -611,263 +611,264 @@ __global__ void __launch_bounds__(kPThreads, 1)
   };
   Piece w;
   bool ok = true;
-  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
-  // (Set inside each role's branch: where the branches join the smaller count would rule.)
-  if (warp == 8 || warp == 9) {
+  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.  Each
+  // warpgroup's instruction stands inside its branch (where the branches join the smaller count
+  // would rule) and is one for all its warps, whatever their roles.
+  if (warp >= 8) {
     leave_registers<72>();
-    // ------------------------------------------------------------ K (8) and V (9) tiles
-    // Lane j < 8 * D/64 issues box (page j % 8, half j / 8): 16 positions x 64 dims.
-    const bool is_v = warp == 9;
-    const CUtensorMap* map = is_v ? &vmap : &kmap;
-    const int page = lane & 7, half = lane >> 3;
-    uint32_t c = 0;       // tiles so far
-    uint32_t issued = 0;  // of them, issued
-    while (ok && next_piece(w, ok)) {
-      const int32_t* row = q.block_table + size_t(w.seq) * q.max_pages;
-      const int npages = (w.ctx + w.n + 15) / 16;
-      int phys = __ldg(&row[min(8 * w.k0 + page, npages - 1)]);
-      for (int t = w.k0; t < w.k1; ++t, ++c) {
-        // a tile's pages past the sequence's end are loaded as its last page (their
-        // positions are masked)
-        const int now = phys;
-        if (t + 1 < w.k1) phys = __ldg(&row[min(8 * (t + 1) + page, npages - 1)]);
-        int pg = now;
-        if (pg < 0 || pg >= q.num_pages) {
-          set_error(q.err, kErrDeviceFault);
-          pg = 0;
+    if (warp < 10) {
+      // ------------------------------------------------------------ K (8) and V (9) tiles
+      // Lane j < 8 * D/64 issues box (page j % 8, half j / 8): 16 positions x 64 dims.
+      const bool is_v = warp == 9;
+      const CUtensorMap* map = is_v ? &vmap : &kmap;
+      const int page = lane & 7, half = lane >> 3;
+      uint32_t c = 0;       // tiles so far
+      uint32_t issued = 0;  // of them, issued
+      while (ok && next_piece(w, ok)) {
+        const int32_t* row = q.block_table + size_t(w.seq) * q.max_pages;
+        const int npages = (w.ctx + w.n + 15) / 16;
+        int phys = __ldg(&row[min(8 * w.k0 + page, npages - 1)]);
+        for (int t = w.k0; t < w.k1; ++t, ++c) {
+          // a tile's pages past the sequence's end are loaded as its last page (their
+          // positions are masked)
+          const int now = phys;
+          if (t + 1 < w.k1) phys = __ldg(&row[min(8 * (t + 1) + page, npages - 1)]);
+          int pg = now;
+          if (pg < 0 || pg >= q.num_pages) {
+            set_error(q.err, kErrDeviceFault);
+            pg = 0;
+          }
+          const uint32_t j = 2 * c + (is_v ? 1 : 0), s = j % NS, use = j / NS;
+          if (use > 0 &&
+              !__all_sync(0xffffffffu, mbar_wait_bounded(freed(s), (use - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(s), Cfg::kSlot);
+          __syncwarp();
+          if (half < Cfg::kHalves)
+            tma_load_2d(sbase + Cfg::kOffRing + s * Cfg::kSlot + half * 16384 + page * 2048, map,
+                        64 * half, (pg * q.hkv + w.g) * 16, full(s));
+          __syncwarp();
+          issued = c + 1;
         }
-        const uint32_t j = 2 * c + (is_v ? 1 : 0), s = j % NS, use = j / NS;
-        if (use > 0 &&
-            !__all_sync(0xffffffffu, mbar_wait_bounded(freed(s), (use - 1) & 1))) {
+      }
+      // every copy in flight lands before the CTA ends (the ring's last NS tiles)
+      for (uint32_t t = issued > NS ? issued - NS : 0; t < issued; ++t) {
+        const uint32_t j = 2 * t + (is_v ? 1 : 0);
+        if (j + NS >= 2 * issued) (void)mbar_wait_bounded(full(j % NS), (j / NS) & 1);
+      }
+      if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ items, Q tiles
+      auto point = [&](int e0) {
+        const int* e = ends + 6 * e0;
+        Point r;
+        r.seq = e[0];
+        r.g = e[1];
+        r.p = e[2];
+        r.k = e[3];
+        r.us = ((long long)e[5] << 32) | (uint32_t)e[4];
+        return r;
+      };
+      Walk walk(point(0), point(1));
+      const Division d = *division;
+      uint32_t c = 0;
+      while (ok) {
+        const bool more = walk.next(q, d, w);
+        if (!more) w.seq = -1;
+        const uint32_t i = c % kPieces;
+        if (c >= kPieces &&
+            !__all_sync(0xffffffffu, mbar_wait_bounded(pcfree(i), (c / kPieces - 1) & 1))) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(full(s), Cfg::kSlot);
-        __syncwarp();
-        if (half < Cfg::kHalves)
-          tma_load_2d(sbase + Cfg::kOffRing + s * Cfg::kSlot + half * 16384 + page * 2048, map,
-                      64 * half, (pg * q.hkv + w.g) * 16, full(s));
-        __syncwarp();
-        issued = c + 1;
-      }
-    }
-    // every copy in flight lands before the CTA ends (the ring's last NS tiles)
-    for (uint32_t t = issued > NS ? issued - NS : 0; t < issued; ++t) {
-      const uint32_t j = 2 * t + (is_v ? 1 : 0);
-      if (j + NS >= 2 * issued) (void)mbar_wait_bounded(full(j % NS), (j / NS) & 1);
-    }
-    if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
-  } else if (warp == 11) {
-    leave_registers<72>();
-    // ------------------------------------------------------------ items, Q tiles
-    auto point = [&](int e0) {
-      const int* e = ends + 6 * e0;
-      Point r;
-      r.seq = e[0];
-      r.g = e[1];
-      r.p = e[2];
-      r.k = e[3];
-      r.us = ((long long)e[5] << 32) | (uint32_t)e[4];
-      return r;
-    };
-    Walk walk(point(0), point(1));
-    const Division d = *division;
-    uint32_t c = 0;
-    while (ok) {
-      const bool more = walk.next(q, d, w);
-      if (!more) w.seq = -1;
-      const uint32_t i = c % kPieces;
-      if (c >= kPieces &&
-          !__all_sync(0xffffffffu, mbar_wait_bounded(pcfree(i), (c / kPieces - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        pieces[i] = w;
-        mbar_arrive(pcfull(i));
-      }
-      __syncwarp();
-      if (!more) break;
-      const int tiles = w.nb > 0 ? 2 : 1;
-      const int qrow = w.row0 + w.tok0;
-      if (c >= QB && lane < tiles * Cfg::kHalves)   // on their way while the last item still uses the buffer
-        tma_prefetch_3d(&qmap, 64 * (lane % Cfg::kHalves), w.g * q.group,
-                        qrow + lane / Cfg::kHalves * q.tile_tokens);
-      if (c >= QB && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree(c), (c / QB - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
-      if (lane == 0) {
-        mbar_arrive_expect_tx(qfull(c), bytes * tiles * Cfg::kHalves);
-        for (int x = 0; x < tiles; ++x)
-          for (int h = 0; h < Cfg::kHalves; ++h)
-            tma_load_3d(sbase + (2 * (c % QB) + x) * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
-                        qrow + x * q.tile_tokens, qfull(c));
-      }
-      __syncwarp();
-      ++c;
-    }
-    for (uint32_t i = c > QB ? c - QB : 0; i < c; ++i)   // landed before the CTA ends
-      (void)mbar_wait_bounded(qfull(i), (i / QB) & 1);
-    if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
-  } else if (warp == 10) {
-    leave_registers<72>();
-    // ------------------------------------------------------------ MMA issue
-    // One thread waits, issues and commits: its instructions lie on the path from a tile's P
-    // to its next S, so ring positions and phases are kept as running values and a step's
-    // descriptors differ from its first one by constants.
-    if (elect_one()) {
-      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
-      // K-major operands with the 128-byte swizzle; V MN-major, 64-dim halves 16 KB apart.
-      // Addresses are below 2^18, so the descriptor's address field takes plain sums.
-      constexpr uint64_t dSw = smem_desc_const(16, 1024, 2), dVmn = smem_desc_const(16384, 1024, 2);
-      const uint32_t q16 = sbase >> 4, ring16 = (sbase + Cfg::kOffRing) >> 4;
-      struct Ring {          // a position in the ring: slot and phase
-        uint32_t s, ph;
-        __device__ __forceinline__ void next() {   // (K and V take turns)
-          s += 2;
-          if (s >= NS) {
-            s -= NS;
-            ph ^= 1;
-          }
+        if (lane == 0) {
+          pieces[i] = w;
+          mbar_arrive(pcfull(i));
         }
-      };
-      Ring kr{0, 0}, vr{1, 0};   // the next K to multiply, the next V
-      uint32_t pa = 0, pb = 0;   // phases of A's and B's P
-      uint32_t ra = 0, rb = 0;   // and of their S being read (kOwnP)
-      uint32_t items = 0;
-      auto wait_k = [&]() { return mbar_wait_bounded(full(kr.s), kr.ph); };
-      auto wait_v = [&]() { return mbar_wait_bounded(full(vr.s), vr.ph); };
-      auto free_k = [&]() {
-        tc_commit(freed(kr.s));
-        kr.next();
-      };
-      auto free_v = [&]() {
-        tc_commit(freed(vr.s));
-        vr.next();
-      };
-      auto issue_s = [&](int x, int qtile) {
-        const uint64_t a = dSw + (q16 + (2 * (items % QB) + qtile) * (Cfg::kQ / 16));
-        const uint64_t bk = dSw + (ring16 + kr.s * (Cfg::kSlot / 16));
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + 128 * x, a + ((ks >> 2) * 1024 + (ks & 3) * 2),
-                 bk + ((ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
-        tc_commit(sfull(x));
-      };
-      // where P has its own place, S may be overwritten once the softmax has read it
-      auto wait_read = [&](int x) {
-        if constexpr (!Cfg::kOwnP) return true;
-        uint32_t& ph = x ? rb : ra;
-        const bool read = mbar_wait_bounded(sread(x), ph);
-        ph ^= 1;
-        return read;
-      };
-      // O_X += P_X . V, once the softmax has left P_X; last: X's last tile here
-      auto issue_pv = [&](int x, bool accumulate, bool last) {
-        uint32_t& ph = x ? pb : pa;
-        const uint64_t bv = dVmn + (ring16 + vr.s * (Cfg::kSlot / 16));
-        if (!mbar_wait_bounded(pready(x), ph)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kp = 0; kp < kTile / 16; ++kp)
-          tc_mma_ts(tmem + Cfg::kO + D * x, tmem + Cfg::kP + Cfg::kPStep * x + 8 * kp, bv + kp * 128,
-                    idPV, accumulate || kp > 0);
-        ph ^= 1;
-        if (Cfg::kOwnP || last) tc_commit(odone(x));
-        return true;
-      };
-      // false: a wait ran out
-      auto run_pair = [&](int k0, int k1, int ea, int eb) {
-        if (!wait_k()) return false;
-        if (k0 < ea) issue_s(0, 0);
-        if (k0 < eb) issue_s(1, 1);
-        free_k();
-        if (k0 + 1 == k1) tc_commit(qfree(items));
-        for (int t = k0; t < k1; ++t) {
-          bool have_k = false, have_v = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int ex = x ? eb : ea;
-            if (t >= ex) continue;
+        __syncwarp();
+        if (!more) break;
+        const int tiles = w.nb > 0 ? 2 : 1;
+        const int qrow = w.row0 + w.tok0;
+        if (c >= QB && lane < tiles * Cfg::kHalves)   // on their way while the last item still uses the buffer
+          tma_prefetch_3d(&qmap, 64 * (lane % Cfg::kHalves), w.g * q.group,
+                          qrow + lane / Cfg::kHalves * q.tile_tokens);
+        if (c >= QB && !__all_sync(0xffffffffu, mbar_wait_bounded(qfree(c), (c / QB - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint32_t bytes = uint32_t(q.tile_tokens * q.group) * 128;   // one box
+        if (lane == 0) {
+          mbar_arrive_expect_tx(qfull(c), bytes * tiles * Cfg::kHalves);
+          for (int x = 0; x < tiles; ++x)
+            for (int h = 0; h < Cfg::kHalves; ++h)
+              tma_load_3d(sbase + (2 * (c % QB) + x) * Cfg::kQ + h * 16384, &qmap, 64 * h, w.g * q.group,
+                          qrow + x * q.tile_tokens, qfull(c));
+        }
+        __syncwarp();
+        ++c;
+      }
+      for (uint32_t i = c > QB ? c - QB : 0; i < c; ++i)   // landed before the CTA ends
+        (void)mbar_wait_bounded(qfull(i), (i / QB) & 1);
+      if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ MMA issue
+      // One thread waits, issues and commits: its instructions lie on the path from a tile's P
+      // to its next S, so ring positions and phases are kept as running values and a step's
+      // descriptors differ from its first one by constants.
+      if (elect_one()) {
+        constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
+        // K-major operands with the 128-byte swizzle; V MN-major, 64-dim halves 16 KB apart.
+        // Addresses are below 2^18, so the descriptor's address field takes plain sums.
+        constexpr uint64_t dSw = smem_desc_const(16, 1024, 2), dVmn = smem_desc_const(16384, 1024, 2);
+        const uint32_t q16 = sbase >> 4, ring16 = (sbase + Cfg::kOffRing) >> 4;
+        struct Ring {          // a position in the ring: slot and phase
+          uint32_t s, ph;
+          __device__ __forceinline__ void next() {   // (K and V take turns)
+            s += 2;
+            if (s >= NS) {
+              s -= NS;
+              ph ^= 1;
+            }
+          }
+        };
+        Ring kr{0, 0}, vr{1, 0};   // the next K to multiply, the next V
+        uint32_t pa = 0, pb = 0;   // phases of A's and B's P
+        uint32_t ra = 0, rb = 0;   // and of their S being read (kOwnP)
+        uint32_t items = 0;
+        auto wait_k = [&]() { return mbar_wait_bounded(full(kr.s), kr.ph); };
+        auto wait_v = [&]() { return mbar_wait_bounded(full(vr.s), vr.ph); };
+        auto free_k = [&]() {
+          tc_commit(freed(kr.s));
+          kr.next();
+        };
+        auto free_v = [&]() {
+          tc_commit(freed(vr.s));
+          vr.next();
+        };
+        auto issue_s = [&](int x, int qtile) {
+          const uint64_t a = dSw + (q16 + (2 * (items % QB) + qtile) * (Cfg::kQ / 16));
+          const uint64_t bk = dSw + (ring16 + kr.s * (Cfg::kSlot / 16));
+          tc_fence_after();
+  #pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_mma(tmem + 128 * x, a + ((ks >> 2) * 1024 + (ks & 3) * 2),
+                   bk + ((ks >> 2) * 1024 + (ks & 3) * 2), idS, ks > 0);
+          tc_commit(sfull(x));
+        };
+        // where P has its own place, S may be overwritten once the softmax has read it
+        auto wait_read = [&](int x) {
+          if constexpr (!Cfg::kOwnP) return true;
+          uint32_t& ph = x ? rb : ra;
+          const bool read = mbar_wait_bounded(sread(x), ph);
+          ph ^= 1;
+          return read;
+        };
+        // O_X += P_X . V, once the softmax has left P_X; last: X's last tile here
+        auto issue_pv = [&](int x, bool accumulate, bool last) {
+          uint32_t& ph = x ? pb : pa;
+          const uint64_t bv = dVmn + (ring16 + vr.s * (Cfg::kSlot / 16));
+          if (!mbar_wait_bounded(pready(x), ph)) return false;
+          tc_fence_after();
+  #pragma unroll
+          for (int kp = 0; kp < kTile / 16; ++kp)
+            tc_mma_ts(tmem + Cfg::kO + D * x, tmem + Cfg::kP + Cfg::kPStep * x + 8 * kp, bv + kp * 128,
+                      idPV, accumulate || kp > 0);
+          ph ^= 1;
+          if (Cfg::kOwnP || last) tc_commit(odone(x));
+          return true;
+        };
+        // false: a wait ran out
+        auto run_pair = [&](int k0, int k1, int ea, int eb) {
+          if (!wait_k()) return false;
+          if (k0 < ea) issue_s(0, 0);
+          if (k0 < eb) issue_s(1, 1);
+          free_k();
+          if (k0 + 1 == k1) tc_commit(qfree(items));
+          for (int t = k0; t < k1; ++t) {
+            bool have_k = false, have_v = false;
+  #pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int ex = x ? eb : ea;
+              if (t >= ex) continue;
+              auto next_s = [&]() {
+                if (!wait_read(x)) return false;
+                if (t + 1 >= ex) return true;
+                if (!have_k && !wait_k()) return false;
+                have_k = true;
+                issue_s(x, x);
+                return true;
+              };
+              if (Cfg::kOwnP && !next_s()) return false;
+              if (!have_v && !wait_v()) return false;
+              have_v = true;
+              if (!issue_pv(x, t > k0, t + 1 == ex)) return false;
+              if (!Cfg::kOwnP) {
+                if (x == 1 || t >= eb) free_v();
+                if (!next_s()) return false;
+              }
+            }
+            if (Cfg::kOwnP) free_v();
+            if (t + 1 < k1) {
+              free_k();
+              if (t + 2 == k1) tc_commit(qfree(items));
+            }
+          }
+          return true;
+        };
+        // tile i to A or B in turn, each with its own S, P and O, both from query tile A
+        auto run_alternating = [&](int tiles) {
+          for (int i = 0; i < min(2, tiles); ++i) {
+            if (!wait_k()) return false;
+            issue_s(i, 0);
+            free_k();
+          }
+          if (tiles <= 2) tc_commit(qfree(items));
+          for (int i = 0; i < tiles; ++i) {
+            const int x = i & 1;
             auto next_s = [&]() {
               if (!wait_read(x)) return false;
-              if (t + 1 >= ex) return true;
-              if (!have_k && !wait_k()) return false;
-              have_k = true;
-              issue_s(x, x);
+              if (i + 2 >= tiles) return true;
+              if (!wait_k()) return false;
+              issue_s(x, 0);
+              free_k();
+              if (i + 3 == tiles) tc_commit(qfree(items));
               return true;
             };
             if (Cfg::kOwnP && !next_s()) return false;
-            if (!have_v && !wait_v()) return false;
-            have_v = true;
-            if (!issue_pv(x, t > k0, t + 1 == ex)) return false;
-            if (!Cfg::kOwnP) {
-              if (x == 1 || t >= eb) free_v();
-              if (!next_s()) return false;
-            }
+            if (!wait_v() || !issue_pv(x, i >= 2, i + 2 >= tiles)) return false;
+            free_v();
+            if (!Cfg::kOwnP && !next_s()) return false;
           }
-          if (Cfg::kOwnP) free_v();
-          if (t + 1 < k1) {
-            free_k();
-            if (t + 2 == k1) tc_commit(qfree(items));
+          return true;
+        };
+        while (true) {
+          const uint32_t i = pc % kPieces;
+          if (!mbar_wait_bounded(pcfull(i), (pc / kPieces) & 1)) {
+            ok = false;
+            break;
           }
+          const int seq = pieces[i].seq, k0 = pieces[i].k0, k1 = pieces[i].k1;
+          const int ea = min(k1, pieces[i].na), eb = min(k1, pieces[i].nb), alt = pieces[i].alt;
+          mbar_arrive(pcfree(i));
+          ++pc;
+          if (seq < 0) break;
+          if (!mbar_wait_bounded(qfull(items), (items / QB) & 1) ||
+              !(alt ? run_alternating(k1 - k0) : run_pair(k0, k1, ea, eb))) {
+            ok = false;
+            break;
+          }
+          ++items;
         }
-        return true;
-      };
-      // tile i to A or B in turn, each with its own S, P and O, both from query tile A
-      auto run_alternating = [&](int tiles) {
-        for (int i = 0; i < min(2, tiles); ++i) {
-          if (!wait_k()) return false;
-          issue_s(i, 0);
-          free_k();
-        }
-        if (tiles <= 2) tc_commit(qfree(items));
-        for (int i = 0; i < tiles; ++i) {
-          const int x = i & 1;
-          auto next_s = [&]() {
-            if (!wait_read(x)) return false;
-            if (i + 2 >= tiles) return true;
-            if (!wait_k()) return false;
-            issue_s(x, 0);
-            free_k();
-            if (i + 3 == tiles) tc_commit(qfree(items));
-            return true;
-          };
-          if (Cfg::kOwnP && !next_s()) return false;
-          if (!wait_v() || !issue_pv(x, i >= 2, i + 2 >= tiles)) return false;
-          free_v();
-          if (!Cfg::kOwnP && !next_s()) return false;
-        }
-        return true;
-      };
-      while (true) {
-        const uint32_t i = pc % kPieces;
-        if (!mbar_wait_bounded(pcfull(i), (pc / kPieces) & 1)) {
-          ok = false;
-          break;
-        }
-        const int seq = pieces[i].seq, k0 = pieces[i].k0, k1 = pieces[i].k1;
-        const int ea = min(k1, pieces[i].na), eb = min(k1, pieces[i].nb), alt = pieces[i].alt;
-        mbar_arrive(pcfree(i));
-        ++pc;
-        if (seq < 0) break;
-        if (!mbar_wait_bounded(qfull(items), (items / QB) & 1) ||
-            !(alt ? run_alternating(k1 - k0) : run_pair(k0, k1, ea, eb))) {
-          ok = false;
-          break;
-        }
-        ++items;
+        if (!ok) set_error(q.err, kErrDeviceTimeout);
+        tc_commit(drain);
       }
-      if (!ok) set_error(q.err, kErrDeviceTimeout);
-      tc_commit(drain);
+      __syncwarp();
+      // every MMA issued has completed before tensor memory is released
+      (void)mbar_wait_bounded(drain, 0);
     }
-    __syncwarp();
-    // every MMA issued has completed before tensor memory is released
-    (void)mbar_wait_bounded(drain, 0);
   } else {
     take_registers<216>();
     // ------------------------------------------------------------ softmax of tile X

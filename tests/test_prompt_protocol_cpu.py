@@ -33,3 +33,17 @@ def test_the_softmax_warps_leave_their_items_only_by_a_common_vote():
     for at in exits:
         assert "named_bar_any(1 + x, 128" in items[max(0, at - 80):at], items[max(0, at - 120):at + 6]
     assert "while (true)" in text[role:text.index("for (int t = kbeg", role)]
+
+
+def test_each_warpgroup_sets_its_registers_by_one_instruction():
+    """setmaxnreg wants all warps of a warpgroup at the same instruction, and the shares together
+    may not pass what the block was launched with, or the taking ones would wait for ever."""
+    with open(os.path.join(CSRC, "prompt_attn.cu")) as f:
+        text = f.read()
+    leave = [int(x) for x in re.findall(r"leave_registers<(\d+)>\(\)", text)]
+    take = [int(x) for x in re.findall(r"take_registers<(\d+)>\(\)", text)]
+    assert len(leave) == 1 and len(take) == 1          # warps 8-11; warps 0-3 and 4-7
+    threads = int(re.search(r"kPThreads = (\d+)", text).group(1))
+    assert threads == 384
+    launch = 65536 // threads // 8 * 8                 # registers a thread of the only CTA of an SM
+    assert 128 * leave[0] + 256 * take[0] <= threads * launch
