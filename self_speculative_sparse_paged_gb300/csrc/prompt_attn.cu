@@ -61,6 +61,7 @@
 // the softmax alone sets the pace (7128 packed rows: 141 us).  One row each of
 // eight sequences of 32000 positions: 160 us (6.6 TB/s).
 #include "kernels.h"
+#include "ticket.h"
 #include "vegas_common.cuh"
 
 namespace vegas {
@@ -92,6 +93,13 @@ struct Piece {
 };
 constexpr int kPieces = 4;   // depth of the ring of published items
 
+// The items that a CTA shares with others, at most two: the end of one that an earlier CTA began
+// (0), and the one that it leaves unfinished (1).
+struct Owed {
+  int first, arrivals, tiles;   // the item's ticket, its CTAs (0: no such item), its query tiles
+  int arrived[2];               // query tile x's group has arrived on its ticket
+};
+
 template <int D>
 struct PCfg {
   static constexpr int kHalves = D / 64;
@@ -106,7 +114,7 @@ struct PCfg {
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
   static constexpr int kNumBars = 2 * kSlots + 2 + 2 + 2 + 2 + 2 * kQBufs + 1 + 2 * kPieces + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kOffPieces = kOffMisc + 96;
+  static constexpr int kOffPieces = kOffMisc + 96 + 2 * (int)sizeof(Owed);
   static constexpr int kOffAlt = kOffPieces + kPieces * (int)sizeof(Piece);   // (m, l) of 32 rows
   static constexpr size_t kSmem = kOffAlt + 32 * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 && kOffAlt % 8 == 0 && kOffPieces % 8 == 0, "shared memory");
@@ -531,6 +539,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int* flags = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 4);          // [2]
   int* ends = reinterpret_cast<int*>(smem + Cfg::kOffMisc + 16);          // [2][6]
   Division* division = reinterpret_cast<Division*>(smem + Cfg::kOffMisc + 64);
+  Owed* owed = reinterpret_cast<Owed*>(smem + Cfg::kOffMisc + 96);        // [2]
   float2* alt_ml = reinterpret_cast<float2*>(smem + Cfg::kOffAlt);
   Piece* pieces = reinterpret_cast<Piece*>(smem + Cfg::kOffPieces);
 
@@ -559,6 +568,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     fence_mbar_init();
   }
+  if (warp == 4 && lane < 2) owed[lane] = Owed{};
   if (tid == 32) prefetch_tensormap(&kmap);
   if (tid == 64) prefetch_tensormap(&vmap);
   if (tid == 96) prefetch_tensormap(&qmap);
@@ -674,8 +684,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
       Walk walk(point(0), point(1));
       const Division d = *division;
       uint32_t c = 0;
+      auto owe = [&]() {   // (read once every warp is done)
+        if (lane == 0 && w.first != w.last) {
+          Owed& o = owed[w.last == (int)blockIdx.x ? 0 : 1];
+          o.first = w.first;
+          o.arrivals = w.last - w.first + 1;
+          o.tiles = w.nb > 0 ? 2 : 1;
+        }
+      };
       while (ok) {
         const bool more = walk.next(q, d, w);
+        if (more) owe();
         if (!more) w.seq = -1;
         const uint32_t i = c % kPieces;
         if (c >= kPieces &&
@@ -712,6 +731,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (uint32_t i = c > QB ? c - QB : 0; i < c; ++i)   // landed before the CTA ends
         (void)mbar_wait_bounded(qfull(i), (i / QB) & 1);
       if (!ok && lane == 0) set_error(q.err, kErrDeviceTimeout);
+      if (!ok)
+        while (walk.next(q, d, w)) owe();
     } else if (warp == 10) {
       // ------------------------------------------------------------ MMA issue
       // One thread waits, issues and commits: its instructions lie on the path from a tile's P
@@ -1117,6 +1138,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int first = w.first, last = w.last, me = blockIdx.x;
       auto slot_of = [&](int cta, int tile) { return (2 * cta + (cta == last ? 0 : 1)) * 2 + tile; };
       int* ticket = &q.tickets[2 * first + x];
+      int* arrived = &owed[me == last ? 0 : 1].arrived[x];
       const int arrivals = last - first + 1;
       const float2* ml = reinterpret_cast<const float2*>(q.part_ml);
       const float4* po = reinterpret_cast<const float4*>(q.part_o);
@@ -1144,7 +1166,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
               make_float2(m, l);
         __threadfence();
         named_bar(1 + x, 128);
-        if (r == 0) flags[x] = atomicAdd(ticket, 1) == arrivals - 1;
+        if (r == 0) {
+          const TicketTurn turn = ticket_turn(atomicAdd(ticket, kTicketLeft), arrivals, false);
+          if (turn.last && !turn.join) *ticket = 0;
+          flags[x] = turn.join;
+          *arrived = 1;
+        }
         named_bar(1 + x, 128);
       };
       if (rows <= kFewRows) {
@@ -1212,6 +1239,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (r == 0) flags[x] = *reinterpret_cast<volatile int*>(ticket) == arrivals - 1;
         named_bar(1 + x, 128);
         const bool done = flags[x];
+        if (done && r == 0) *arrived = 1;
         named_bar(1 + x, 128);
         if (!done) leave();
         if (done || flags[x]) {
@@ -1305,6 +1333,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // after a wait that ran out: the shared items that this CTA leaves no state of
+  if (tid < 4) {
+    const int x = tid & 1;
+    const Owed& o = owed[tid >> 1];
+    if (x < o.tiles && !o.arrived[x]) {
+      int* ticket = &q.tickets[2 * o.first + x];
+      if (ticket_turn(atomicAdd(ticket, kTicketGivenUp), o.arrivals, true).last) *ticket = 0;
+    }
+  }
   if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -61,3 +61,15 @@ def test_tiles_taken_again_leave_their_second_probabilities(hq, hkv, d, rows, ct
         c.out[:c.used] = 0
         assert torch.equal(c.run(), first)
     vg.vegas_read_device_status()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (32, 8, 128)])
+@pytest.mark.parametrize("rows,ctx", [([1], [40000]), ([600], [9000]), ([300, 1, 2], [700, 9000, 4100])])
+def test_shared_items_leave_the_counters_at_zero(hq, hkv, d, rows, ctx):
+    c = Prompt(hq, hkv, d, rows, ctx, seed=33)
+    counters = c.workspace()[:2 * torch.cuda.get_device_properties(0).multi_processor_count * 4]
+    for _ in range(3):
+        c.out[:c.used] = 0
+        c.run()
+        assert not counters.any()
+    c.check(heads=(0, hq - 1), rows=24)
