@@ -295,7 +295,8 @@ vegas_status_t vegas_decode_iteration(
  * total_rows is the number of rows in the tensors, at least row_start[batch]:
  * rows behind the last sequence may hold anything and are never written.  Needs
  * 0 <= ctx_lens[b] and ctx_lens[b] + n_b <= 16 * max_pages_per_seq; a sequence
- * with rows that breaks this is recorded as a device fault and skipped.
+ * with rows that breaks this is recorded as a device fault and skipped.  In
+ * one without rows ctx_lens[b] and the block table's row may hold anything.
  * total_rows < 2^24, batch <= 2^16.
  *
  * vegas_rope_append turns the query and key heads of every row by their

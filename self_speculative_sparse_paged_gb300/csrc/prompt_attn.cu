@@ -158,19 +158,21 @@ __device__ __forceinline__ long long share_begin(int i, long long total, int n) 
   return (long long)i * q + (unsigned)i * r / n;
 }
 
-// A sequence that is not of one of the given classes counts as empty.
+// A sequence that is not of one of the given classes counts as empty.  The cached length of one
+// without rows may hold anything.
 __device__ __forceinline__ Seq load_seq(const PromptParams& q, int s, int classes) {
   Seq r;
   r.row0 = q.row_start[s];
   const int end = q.row_start[s + 1];
   r.ctx = q.ctx_lens[s];
   r.n = end - r.row0;
-  const bool bad = r.row0 < 0 || end < r.row0 || end > q.total_rows || r.ctx < 0 ||
-                   (long long)r.ctx + r.n > (long long)q.max_pages * 16;
-  if (bad) {
-    set_error(q.err, kErrDeviceFault);
-    r.n = 0;
-  }
+  // (one test for ctx and its upper limit, and no branch before it: the loads stay together;
+  // n <= total_rows < 2^24 and 16 max_pages < 2^24, so nothing wraps where the rows are sound)
+  const bool rows = r.row0 >= 0 & end >= r.row0 & end <= q.total_rows;
+  const bool fits = (unsigned)r.ctx <= (unsigned)(q.max_pages * 16 - r.n) & r.n <= q.max_pages * 16;
+  const bool sound = rows & (end == r.row0 | fits);
+  if (!sound) set_error(q.err, kErrDeviceFault);
+  if (!sound | end == r.row0) r.n = r.ctx = 0;
   if (!(classes & (r.n * q.group <= kFewRows ? kFew : kMany))) r.n = 0;
   r.pairs = pairs_in(q, r.n + q.pair_tokens - 1);
   const long long P = r.pairs;
