@@ -208,6 +208,13 @@ __device__ __forceinline__ void move_sums(float from, float to, float k, float& 
   }
 }
 
+// a (x - m) for finite x <= m.  The difference alone may pass fp32's largest number (the lowest
+// value beside a large maximum) where a brings it back: halves do not, and but for subnormal
+// differences they round the same.
+__device__ __forceinline__ float scaled_gap(float x, float m, float a) {
+  return 2.f * ((0.5f * x - 0.5f * m) * a);
+}
+
 }  // namespace
 
 template <typename T>
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
       sh.ln_z = ln_z;
       if (p.logprob) {
         float lp = 0.f;
-        if (tok >= 0) lp = xt > -INFINITY ? (xt - M) * p.inv_temperature - ln_z : -INFINITY;
+        if (tok >= 0) lp = xt > -INFINITY ? scaled_gap(xt, M, p.inv_temperature) - ln_z : -INFINITY;
         p.logprob[row] = lp;
       }
       if (p.rank) p.rank[row] = tok >= 0 ? count : -1;
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
       if (larger < n && lane == 0) {
         p.top_ids[size_t(row) * n + larger] = index_of(mine);
         p.top_logprobs[size_t(row) * n + larger] =
-            (value_of(mine) - sh.row_max) * p.inv_temperature - sh.ln_z;
+            scaled_gap(value_of(mine), sh.row_max, p.inv_temperature) - sh.ln_z;
       }
     }
     if (tid >= found && tid < n) {   // fewer than n logits are left
