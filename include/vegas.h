@@ -311,7 +311,8 @@ vegas_status_t vegas_decode_iteration(
  *            contiguous elements *_stride elements apart (a multiple of 8; the
  *            parts of one fused projection are three pointers into it)
  *   q_out: device bf16 [total_rows][Hq][head_dim], 16-byte aligned; may be q
- *          when q_stride = Hq * head_dim
+ *          when q_stride = Hq * head_dim, and lies over no rows of q, k or v
+ *          otherwise
  *   positions: device int32 [num_axes][total_rows], or NULL for the cache
  *          position on every axis
  *   pair_axis: device int32 [rot_dim / 2], each in [0, num_axes); NULL = axis 0
@@ -327,7 +328,8 @@ vegas_status_t vegas_decode_iteration(
  * sequence's last position may hold anything; K and V inside it must be finite.
  *   q:   device bf16, 16-byte aligned, rows q_stride elements apart (a
  *        multiple of 8, at least Hq * head_dim)
- *   out: device bf16 [total_rows][Hq][head_dim], 32-byte aligned, not q
+ *   out: device bf16 [total_rows][Hq][head_dim], 32-byte aligned, not over q's
+ *        rows
  *   workspace: vegas_prompt_workspace_size() bytes for the same total_rows,
  *        batch and kv (a larger one serves smaller calls of the same device;
  *        not one that other entry points use), 256-byte aligned

@@ -677,6 +677,13 @@ vegas_status_t check_rows(const char* name, const void* p, int64_t stride, int h
   return VEGAS_OK;
 }
 
+// Contiguous output rows of `width` elements over the span of input rows `stride` apart?
+bool lies_over(const void* out, int64_t width, const void* in, int64_t stride, int64_t in_width,
+               int rows) {
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+  return o < i + 2 * ((rows - 1) * (uint64_t)stride + in_width) && i < o + 2 * (uint64_t)rows * width;
+}
+
 // Largest query group of the prompt kernel (a query tile holds whole tokens).
 constexpr int kMaxPromptGroup = 64;
 
@@ -753,6 +760,11 @@ VEGAS_API vegas_status_t vegas_rope_append(
   if (q_out == q && q_stride != (int64_t)kv->num_q_heads * d)   // rows would overwrite later ones
     return fail(VEGAS_ERR_INVALID_ARG, "q_out is q, but q_stride %lld is not %d",
                 (long long)q_stride, kv->num_q_heads * d);
+  const int64_t wq = (int64_t)kv->num_q_heads * d, wkv = (int64_t)kv->num_kv_heads * d;
+  if ((q_out != q && lies_over(q_out, wq, q, q_stride, wq, total_rows)) ||
+      lies_over(q_out, wq, k, k_stride, wkv, total_rows) ||
+      lies_over(q_out, wq, v, v_stride, wkv, total_rows))   // other warps may not have read yet
+    return fail(VEGAS_ERR_INVALID_ARG, "q_out lies over rows of q, k or v");
   int* err = nullptr;
   if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
   vegas::RopeParams p{};
@@ -821,6 +833,9 @@ VEGAS_API vegas_status_t vegas_prompt_attn(const vegas_paged_kv_t* kv, const voi
   if (total_rows == 0 || batch == 0) return VEGAS_OK;
   if (out == q)   // a query tile may be read after another CTA has written its rows
     return fail(VEGAS_ERR_INVALID_ARG, "out is q");
+  const int64_t width = (int64_t)kv->num_q_heads * kv->head_dim;
+  if (lies_over(out, width, q, q_stride, width, total_rows))
+    return fail(VEGAS_ERR_INVALID_ARG, "out lies over rows of q");
   int* err = nullptr;
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
