@@ -180,8 +180,16 @@ __device__ __forceinline__ int index_of(unsigned long long k) { return (int)~(ui
 
 constexpr int kLpLead = 4;              // thread maxima a warp offers for the bound
 
+// The sums of some logits relative to their maximum m: e = 2^((x - m) k) adds up to ones + s and
+// e (x - m) to t.  The ones are kept apart: where one token has nearly all the probability, ln Z is
+// ln(1 + s) of a small s, which the sum 1 + s would hold to 2^-24 only.
+struct RowSums {
+  float m, s, t;
+  int ones;
+};
+
 struct LpShared {
-  float m[kLpWarps], s[kLpWarps], t[kLpWarps];
+  RowSums sums[kLpWarps];
   int cnt[kLpWarps];
   uint32_t lead[kLpWarps * kLpLead];    // as order_of()
   uint32_t bound;
@@ -190,7 +198,7 @@ struct LpShared {
   unsigned long long best[kLpWarps];
   unsigned long long list[kLpList];
   // in the cluster's first CTA: what every CTA pushed
-  float M[kMaxLogprobCluster], S[kMaxLogprobCluster], Tt[kMaxLogprobCluster];
+  RowSums parts[kMaxLogprobCluster];
   int count[kMaxLogprobCluster];
   unsigned long long all[kMaxLogprobCluster * kMaxTopLogprobs];
   float row_max, ln_z;
@@ -205,6 +213,22 @@ __device__ __forceinline__ void move_sums(float from, float to, float k, float& 
     s *= f;
   } else {
     s = t = 0.f;
+  }
+}
+
+// The sums of the first 2 * half lanes (the others hold none), joined at the largest maximum M.
+__device__ __forceinline__ void join_sums(RowSums& v, float M, float k, int half) {
+  if (v.m != M) {
+    v.s += (float)v.ones;
+    v.ones = 0;
+    move_sums(v.m, M, k, v.s, v.t);
+    v.m = M;
+  }
+  v.ones = __reduce_add_sync(0xffffffffu, v.ones);
+#pragma unroll
+  for (int o = half; o > 0; o >>= 1) {
+    v.s += __shfl_xor_sync(0xffffffffu, v.s, o);
+    v.t += __shfl_xor_sync(0xffffffffu, v.t, o);
   }
 }
 
@@ -379,19 +403,20 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
     float s, t, sb, tb;
     unpair_f32(s2, s, sb);
     unpair_f32(t2, t, tb);
-    s += sb;
-    t += tb;
-    move_sums(m, Mw, k, s, t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
+    // the thread's maximum (one of it) leaves the sums, as it was added, and counts one
+    RowSums v{tm, 0.f, 0.f, 0};
+    if (tm > -INFINITY) {
+      const float u = fmaxf(tm - m, -FLT_MAX), e = ex2(u * k);
+      const float sum = s + sb, z = sum - s, low = (s - (sum - z)) + (sb - z);   // sum + low = s + sb
+      v.ones = 1;
+      v.s = (sum - e) + low;
+      v.t = t + fmaf(-e, u, tb);
+      move_sums(m, tm, k, v.s, v.t);
     }
+    join_sums(v, Mw, k, 16);
     cnt = __reduce_add_sync(0xffffffffu, cnt + (int)many);
     if (lane == 0) {
-      sh.m[warp] = Mw;
-      sh.s[warp] = s;
-      sh.t[warp] = t;
+      sh.sums[warp] = v;
       sh.cnt[warp] = cnt;
     }
   }
@@ -402,21 +427,14 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   // the CTA's sums (last warp) and the bound on its n-th largest logit (first warps)
   if (warp == kLpWarps - 1) {
     const bool has = lane < kLpWarps;
-    float M = has ? sh.m[lane] : -INFINITY, s = has ? sh.s[lane] : 0.f, t = has ? sh.t[lane] : 0.f;
-    const float from = M;
+    RowSums v = has ? sh.sums[lane] : RowSums{-INFINITY, 0.f, 0.f, 0};
+    float M = v.m;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    move_sums(from, M, k, s, t);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
+    join_sums(v, M, k, 8);
     const int total = __reduce_add_sync(0xffffffffu, has ? sh.cnt[lane] : 0);
     if (lane == 0) {
-      first->M[r] = M;
-      first->S[r] = s;
-      first->Tt[r] = t;
+      first->parts[r] = v;
       first->count[r] = total;
     }
   }
@@ -522,19 +540,15 @@ __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 2 ? 3 : 2)
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (warp == 0) {
     const bool has = lane < C;
-    float M = has ? sh.M[lane] : -INFINITY, s = has ? sh.S[lane] : 0.f, t = has ? sh.Tt[lane] : 0.f;
-    const float from = M;
+    RowSums v = has ? sh.parts[lane] : RowSums{-INFINITY, 0.f, 0.f, 0};
+    float M = v.m;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    move_sums(from, M, k, s, t);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
+    join_sums(v, M, k, 8);
+    const float s = (float)v.ones + v.s, t = v.t;
     const int count = __reduce_add_sync(0xffffffffu, has ? sh.count[lane] : 0);
     if (lane == 0) {
-      const float ln_z = s > 0.f ? logf(s) : 0.f;
+      const float ln_z = v.ones == 1 ? log1pf(v.s) : s > 0.f ? logf(s) : 0.f;
       sh.row_max = M;
       sh.ln_z = ln_z;
       if (p.logprob) {
