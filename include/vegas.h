@@ -325,7 +325,12 @@ vegas_status_t vegas_decode_iteration(
  * reads positions [0, ctx_lens[b] + t] of KV head h / G,
  *   o = sum_i softmax(softmax_scale * q . k_i) v_i,
  * with K and V of the rows themselves already in the cache.  Slots past a
- * sequence's last position may hold anything; K and V inside it must be finite.
+ * sequence's last position may hold anything; inside it K must be finite, with
+ * logits that fp32 holds, and |V| below 2^90 (sums of up to 2^37 times it are
+ * kept in fp32).  Logits, exponentials and sums are fp32; each p_i is rounded
+ * to bf16, the tensor cores' operand type, before it meets v_i (half a step,
+ * 2^-8 of it), and the output once more.  A form that keeps p_i in fp32 has
+ * about 0.7 to 0.85 times the error.
  *   q:   device bf16, 16-byte aligned, rows q_stride elements apart (a
  *        multiple of 8, at least Hq * head_dim)
  *   out: device bf16 [total_rows][Hq][head_dim], 32-byte aligned, not over q's
@@ -365,7 +370,9 @@ vegas_status_t vegas_prompt_attn(
  * row whose mask leaves nothing has entropy 0 and log probabilities -inf.
  * tokens[r] < 0 means no token: logprob 0, rank -1 (a token >= vocab is
  * recorded as a device fault and treated so).  NaN and +inf logits are outside
- * the contract (they spoil their own row only).
+ * the contract (they spoil their own row only).  Sums are fp32 and
+ * exponentials the hardware's: log probabilities and entropies are off by some
+ * 1e-7 of themselves, by more only where they come near 0.
  *   logits: device, dtype VEGAS_DTYPE_BF16 or VEGAS_DTYPE_FP32, rows
  *           row_stride >= vocab elements apart, aligned to the type
  *   tokens: device int32 [rows]; may be NULL when logprob and rank are

@@ -55,11 +55,13 @@
 // head_dim 128 S(t + 1) needs tensor memory that P(t) occupies, so a tile's
 // softmax and its two products follow one another and A and B overlap each
 // other's: 2580 cycles a KV tile measured.  A prompt of 16384 rows (32 query
-// heads of 128): 1223 us alone (1.80 PFLOP/s, 0.94 of the measured cuBLAS burst,
-// tensor pipe 79 % active), 1305-1350 us back to back (power-capped, as cuBLAS
-// is); 1000 rows behind 31768 cached: 338 us alone (1.56 PFLOP/s).  At head_dim 64
-// the softmax alone sets the pace (7128 packed rows: 141 us).  One row each of
-// eight sequences of 32000 positions: 160 us (6.6 TB/s).
+// heads of 128): 1190 us alone (1.85 PFLOP/s, 0.96 of the measured cuBLAS burst,
+// tensor pipe 79 % active), 1280-1390 us back to back (power-capped, as cuBLAS
+// is); 1000 rows behind 31768 cached: 332 us alone (1.59 PFLOP/s).  At head_dim 64
+// the softmax sets the pace by its latency (7128 packed rows: 142 us, no pipe more
+// than 47 % busy; among other things each tile waits for the last one's P.V before
+// it reads its S).  One row each of eight sequences of 32000 positions: 162 us
+// (6.5 TB/s, 0.96 of the measured copy).
 #include "kernels.h"
 #include "ticket.h"
 #include "vegas_common.cuh"

@@ -20,8 +20,8 @@
 // two 16-byte loads, 32 multiply-adds and two 16-byte stores, with no barrier
 // between warps; the first heads, the frequencies and the given positions are loaded
 // before the row's sequence and page are looked up.  32768 rows of 32 + 8 + 8 heads of
-// 128: 128 us, 6.3 TB/s of bytes read and written once (0.93 of the measured copy); 32
-// rows: 3.1 us, launch and three dependent lookups.
+// 128: 127 us, 6.35 TB/s of bytes read and written once (0.93 of the measured copy); 32
+// rows: 3.2 us, launch and three dependent lookups.
 #include "kernels.h"
 #include "vegas_common.cuh"
 
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append_kernel(const Rope
 
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
   // Warps a row: one when the rows alone keep the SMs busy, else two, else four (32 query and
-  // 8 KV heads of 128: 1000 rows 11.6 / 8.3 / 6.7 us, 2000 rows 14.6 / 13.1 / 14.5 us, 4000 rows
-  // 20.7 / 22.0 / 24.3 us with one / two / four).
+  // 8 KV heads of 128: 1000 rows 14.1 / 10.3 / 9.0 us, 2000 rows 14.8 / 13.2 / 15.2 us, 4000 rows
+  // 21.0 / 22.0 / 24.9 us with one / two / four; no other shape of heads was measured).
   const int split = p.total_rows >= 3000 ? 1 : p.total_rows >= 1500 ? 2 : kRopeWarps;
   const int rows = kRopeWarps / split;
   cudaLaunchConfig_t cfg = {};
@@ -200,7 +200,7 @@ cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Heads in flight: four of 64, two of 128 (3021 rows of 64: 15.1 us against 17.2 with two;
+  // Heads in flight: four of 64, two of 128 (3021 rows of 64: 14.7 us against 17.2 with two;
   // 32768 rows of 128: 131 us against 128 with four).
   if (split == 1)
     return p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, rope_append_kernel<1, 4>, p)
