@@ -391,6 +391,97 @@ vegas_status_t vegas_token_logprobs(
     int32_t* top_ids, float* top_logprobs, void* stream);
 
 /* ------------------------------------------------------------------------
+ * (7) The paged cache in 8 bits: half the bytes of K and V to read and to keep.
+ * The paper's cache is 16-bit; its loop runs over this one the same way: append,
+ * verify with captured scores, vegas_select_topk, sparse draft steps.
+ *
+ * Layout and paging are those of vegas_paged_kv_t with one byte an element, an
+ * e4m3 code c (largest 448), and a scale for each block, i.e. for each page of
+ * each KV head, K and V apart: the element is c * 2^e, the scale a byte holding
+ * e + 127 with e in [-60, 60] (bytes outside are read as the nearest end).
+ * Every c * 2^e is exact in bf16.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* k_cache;                /* device, e4m3 [num_pages][num_kv_heads][16][head_dim], 16-byte aligned */
+  void* v_cache;                /* the same */
+  uint8_t* k_scale;             /* device [num_pages][num_kv_heads] */
+  uint8_t* v_scale;             /* device [num_pages][num_kv_heads] */
+  const int32_t* block_table;   /* device, int32 [batch][max_pages_per_seq] */
+  int32_t num_pages;
+  int32_t page_size;            /* must be 16 */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128 */
+  int32_t max_pages_per_seq;
+} vegas_paged_kv8_t;
+
+/*
+ * vegas_rope_append_kv8: vegas_rope_append (section 5: its rows, positions,
+ * arguments, limits and refusals) into the 8-bit cache.  A key is turned and
+ * rounded to bf16 as there, a value taken as it is.  With a the largest finite
+ * magnitude of a page's new rows of a head (0 counts as the smallest scale),
+ *   e_new = min { e in [-60, 60] : a <= 448 * 2^e }
+ * (60 where none is enough), and e = e_new where the page's first row is new,
+ * e = max(e_new, its old e) where the page holds rows of earlier calls, i.e.
+ * slots before ctx_lens[b] % 16 of a sequence's first page.  New rows become
+ * e4m3(y * 2^-e), to the nearest, ties to even, beyond 448 (and infinities)
+ * to +-448, NaN staying NaN; where e has grown the held rows' codes become
+ * e4m3(c * 2^(e_old - e)), exact but for codes that fall below 2^-6.  So a
+ * rejected draft row that is written over may leave its page's scale raised.
+ * Slots behind the new rows keep their codes.  No two sequences of a call may
+ * append to the same page.
+ *
+ * vegas_kv8_read: positions [first[b], upto[b]) of every sequence, as bf16, into
+ * the same positions of the bf16 cache `to` through its own block table, which
+ * must not map one page twice for positions read; first may be NULL (all 0).  Pages may
+ * be read that another sequence shares.  The result is exact.  For bf16 calls over
+ * an 8-bit prefix, vegas_prompt_attn above all.  A sequence with upto[b] <= first[b] is
+ * left alone; one with first[b] < 0 or upto[b] past either table's capacity is
+ * recorded as a device fault and skipped.  batch <= 65535.
+ *
+ * vegas_verify_attn_kv8: vegas_verify_attn_capture_rows over the 8-bit cache,
+ * window rows 0 .. gamma at positions ctx_lens[b] .. ctx_lens[b] + gamma already
+ * appended; gamma = 0 is plain decode attention of one token a sequence.  Logits
+ * are exact products of the codes with q in two e4m3 parts (8 bits, each row
+ * scaled by a power of two; elements 2^-10 below their row's largest are rounded
+ * to 2^-19 of it), summed in fp32; captured scores take the summed
+ * query in six parts.  Exponentials are rounded to f16 (half a step, 2^-11 of
+ * it) before they meet V's codes, sums are fp32, the output is rounded once to bf16.
+ * scores may be NULL (nothing captured; capture_row_mask is then ignored).  K and V
+ * of attended positions must be finite codes, |q| below 2^40; other slots may hold
+ * anything.
+ *   workspace: vegas_verify_kv8_workspace_size() bytes, 256-byte aligned (the
+ *        size of another context capacity, batch or gamma may be larger or smaller)
+ * Supported: (gamma + 1) * G <= 64 at head_dim 64 and <= 40 at head_dim 128, gamma in
+ * [0, 15], |softmax_scale| <= 2^20.
+ *
+ * vegas_sparse_decode_attn_kv8: vegas_sparse_decode_attn (section 3: its lists,
+ * limits and refusals) over the 8-bit cache, roundings as above but q itself
+ * exact in f16 (elements 2^-21 below their head's largest rounded to 2^-39 of it).
+ */
+vegas_status_t vegas_rope_append_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
+    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
+    int batch, void* stream);
+
+vegas_status_t vegas_kv8_read(const vegas_paged_kv8_t* kv, const vegas_paged_kv_t* to,
+                              const int32_t* first, const int32_t* upto, int batch, void* stream);
+
+size_t vegas_verify_kv8_workspace_size(const vegas_paged_kv8_t* kv, int batch, int gamma);
+
+vegas_status_t vegas_verify_attn_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, void* out, float* scores, int score_stride,
+    const int32_t* ctx_lens, int batch, int gamma, uint32_t capture_row_mask,
+    float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+vegas_status_t vegas_sparse_decode_attn_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, void* out, const int32_t* idx, int k_max,
+    const int32_t* k_per_seq, const int32_t* tail_start, const int32_t* tail_len, int max_tail,
+    int batch, float softmax_scale, void* stream);
+
+/* ------------------------------------------------------------------------
  * Failure-detection check (the paper has no counterpart).
  *
  * Every wait of these kernels on an on-chip barrier (a TMA tile landing, an

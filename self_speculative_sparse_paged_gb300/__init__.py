@@ -25,6 +25,8 @@ __all__ = [
     "vegas_decode_iteration",
     "vegas_rope_append", "vegas_prompt_workspace_size", "vegas_prompt_attn",
     "vegas_token_logprobs", "VEGAS_BF16", "VEGAS_FP32",
+    "PagedKV8", "paged_kv8", "vegas_rope_append_kv8", "vegas_kv8_read",
+    "vegas_verify_kv8_workspace_size", "vegas_verify_attn_kv8", "vegas_sparse_decode_attn_kv8",
     "vegas_read_device_status", "vegas_status_string", "vegas_last_error_detail",
     "vegas_abi_version",
 ]
@@ -62,6 +64,23 @@ class PagedKV(ctypes.Structure):
     ]
 
 
+class PagedKV8(ctypes.Structure):
+    """Mirror of vegas_paged_kv8_t."""
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -80,6 +99,7 @@ lib = _load()
 _c_void_p, _i32, _sz, _f32, _u64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t,
                                     ctypes.c_float, ctypes.c_uint64)
 _P_KV = ctypes.POINTER(PagedKV)
+_P_KV8 = ctypes.POINTER(PagedKV8)
 
 
 def _sig(name, res, args):
@@ -147,6 +167,11 @@ _prompt = _sig("vegas_prompt_attn", _i32,
 _logprobs = _sig("vegas_token_logprobs", _i32,
                  [_c_void_p, _i32, _i64, _c_void_p, _i32, _i32, _f32, _c_void_p, _c_void_p,
                   _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p])
+_rope8 = _sig("vegas_rope_append_kv8", _i32, [_P_KV8] + _rope.argtypes[1:])
+_read8 = _sig("vegas_kv8_read", _i32, [_P_KV8, _P_KV, _c_void_p, _c_void_p, _i32, _c_void_p])
+_verify8_ws = _sig("vegas_verify_kv8_workspace_size", _sz, [_P_KV8, _i32, _i32])
+_verify8 = _sig("vegas_verify_attn_kv8", _i32, [_P_KV8] + _verify_rows.argtypes[1:])
+_sparse8 = _sig("vegas_sparse_decode_attn_kv8", _i32, [_P_KV8] + _sparse.argtypes[1:])
 _wait_check = _sig("vegas_check_bounded_wait", _i32, [_i32, _c_void_p, _c_void_p])
 _read_status = _sig("vegas_read_device_status", _i32, [_c_void_p])
 _status_string = _sig("vegas_status_string", ctypes.c_char_p, [_i32])
@@ -198,6 +223,14 @@ def paged_kv(k_cache, v_cache, block_table, num_q_heads: int) -> PagedKV:
     num_pages, hkv, page, d = k_cache.shape
     return PagedKV(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), num_pages, page,
                    num_q_heads, hkv, d, block_table.shape[-1])
+
+
+def paged_kv8(k_cache, v_cache, k_scale, v_scale, block_table, num_q_heads: int) -> PagedKV8:
+    """vegas_paged_kv8_t for e4m3 caches [pages][Hkv][16][d] (torch.float8_e4m3fn or bytes), their
+    scale bytes [pages][Hkv] and an int32 block table."""
+    num_pages, hkv, page, d = k_cache.shape
+    return PagedKV8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                    num_pages, page, num_q_heads, hkv, d, block_table.shape[-1])
 
 
 def vegas_verify_workspace_size(kv: PagedKV, batch: int, gamma: int) -> int:
@@ -342,6 +375,45 @@ def vegas_token_logprobs(logits, dtype: int, row_stride: int, tokens, rows: int,
     _check(_logprobs(_ptr(logits), dtype, row_stride, _ptr(tokens), rows, vocab,
                      inv_temperature, _ptr(logprob), _ptr(entropy), _ptr(rank), top_n,
                      _ptr(top_ids), _ptr(top_logprobs), _stream(stream)))
+
+
+def vegas_rope_append_kv8(kv: PagedKV8, q, q_stride: int, k, k_stride: int, v, v_stride: int, q_out,
+                          row_start, ctx_lens, positions, pair_axis, num_axes: int, inv_freq,
+                          rot_dim: int, interleaved: bool, rope_scale: float, total_rows: int,
+                          batch: int, stream=None) -> None:
+    """vegas_rope_append into the 8-bit cache, its blocks' scales kept up."""
+    _check(_rope8(ctypes.byref(kv), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                  _ptr(q_out), _ptr(row_start), _ptr(ctx_lens), _ptr(positions), _ptr(pair_axis),
+                  num_axes, _ptr(inv_freq), rot_dim, int(interleaved), rope_scale, total_rows,
+                  batch, _stream(stream)))
+
+
+def vegas_kv8_read(kv: PagedKV8, to: PagedKV, first, upto, batch: int, stream=None) -> None:
+    """Positions [first, upto) of every sequence of the 8-bit cache into a bf16 one."""
+    _check(_read8(ctypes.byref(kv), ctypes.byref(to), _ptr(first), _ptr(upto), batch,
+                  _stream(stream)))
+
+
+def vegas_verify_kv8_workspace_size(kv: PagedKV8, batch: int, gamma: int) -> int:
+    return _verify8_ws(ctypes.byref(kv), batch, gamma)
+
+
+def vegas_verify_attn_kv8(kv: PagedKV8, q, out, scores, score_stride: int, ctx_lens, batch: int,
+                          gamma: int, capture_row_mask: int, softmax_scale: float, workspace,
+                          workspace_bytes: int, stream=None) -> None:
+    """vegas_verify_attn_capture_rows over the 8-bit cache; scores may be None."""
+    _check(_verify8(ctypes.byref(kv), _ptr(q), _ptr(out), _ptr(scores), score_stride,
+                    _ptr(ctx_lens), batch, gamma, capture_row_mask, softmax_scale,
+                    _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def vegas_sparse_decode_attn_kv8(kv: PagedKV8, q, out, idx, k_max: int, k_per_seq, tail_start,
+                                 tail_len, max_tail: int, batch: int, softmax_scale: float,
+                                 stream=None) -> None:
+    """vegas_sparse_decode_attn over the 8-bit cache."""
+    _check(_sparse8(ctypes.byref(kv), _ptr(q), _ptr(out), _ptr(idx), k_max, _ptr(k_per_seq),
+                    _ptr(tail_start), _ptr(tail_len), max_tail, batch, softmax_scale,
+                    _stream(stream)))
 
 
 def vegas_check_bounded_wait(limit_us: int, outcome=None, stream=None) -> None:

@@ -253,8 +253,13 @@ __device__ __forceinline__ void reduce_row_sums(WarpState<D, NT>& st) {
 // A part with m_s = -inf has no attended position and weight 0.
 // ---------------------------------------------------------------------------
 
+// The dim that element o[mt][.][2 * hi + .] of lane row r = lane / 4 holds.
+struct MmaDims {
+  __device__ __forceinline__ static int dim(int mt, int r, int hi) { return mt * 16 + r + 8 * hi; }
+};
+
 // Stages one warp's O^T fragments as rows [n][D+4] (fp32) at cO + slot.
-template <int D, int NT>
+template <int D, int NT, class Dims = MmaDims>
 __device__ __forceinline__ void stage_warp_o(const WarpState<D, NT>& st, float* cO, int slot) {
   constexpr int NPAD = NT * 8;
   constexpr int OS = D + 4;
@@ -268,7 +273,7 @@ __device__ __forceinline__ void stage_warp_o(const WarpState<D, NT>& st, float* 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = nt * 8 + c + (i & 1);
-        const int dim = mt * 16 + r + 8 * (i >> 1);
+        const int dim = Dims::dim(mt, r, i >> 1);
         ow[n * OS + dim] = st.o[mt][nt][i];
       }
 }

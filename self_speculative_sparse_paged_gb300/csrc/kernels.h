@@ -20,6 +20,8 @@ struct VerifyParams {
   const void* q;            // bf16 [B][T][Hq][D]
   void* out;                // bf16 [B][T][Hq][D]
   float* scores;            // fp32 [B][Hkv][score_stride] or null
+  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes of the 8-bit cache, or null
+  const uint8_t* v_scale;
   const int32_t* ctx_lens;  // [B]
   const int32_t* block_table;
   int score_stride;
@@ -46,8 +48,10 @@ struct VerifyParams {
 struct SparseParams {
   const void* q;            // bf16 [B][Hq][D]
   void* out;                // bf16 [B][Hq][D]
-  const void* k_cache;      // bf16 [pages][Hkv][16][D]
+  const void* k_cache;      // bf16 [pages][Hkv][16][D], or e4m3 with scales
   const void* v_cache;
+  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes of the 8-bit cache, or null
+  const uint8_t* v_scale;
   const int32_t* block_table;
   const int32_t* idx;       // [B][Hkv][k_max]
   const int32_t* k_per_seq;
@@ -117,6 +121,38 @@ struct RopeParams {
   int total_rows, batch;
   int num_pages, max_pages;
   int hq, hkv, head_dim;
+  int* err;
+};
+
+struct RopeKv8Params {
+  const void *q, *k, *v;    // bf16 rows, strides in elements
+  long long q_stride, k_stride, v_stride;
+  void* q_out;              // bf16 [total_rows][Hq][D]
+  void *k_cache, *v_cache;  // e4m3 [pages][Hkv][16][D]
+  uint8_t *k_scale, *v_scale;   // [pages][Hkv]
+  const int32_t* block_table;
+  const int32_t* row_start; // [B + 1]
+  const int32_t* ctx_lens;  // [B]
+  const int32_t* positions; // [num_axes][total_rows], or null: the cache position
+  const int32_t* pair_axis; // [rot / 2], or null: axis 0
+  const float* inv_freq;    // [rot / 2]
+  int num_axes, rot, interleaved;
+  float scale;
+  int total_rows, batch;
+  int num_pages, max_pages;
+  int hq, hkv, head_dim;
+  int* err;
+};
+
+struct Kv8ReadParams {
+  const void *k_cache, *v_cache;        // e4m3 [pages][Hkv][16][D]
+  const uint8_t *k_scale, *v_scale;     // [pages][Hkv]
+  const int32_t* block_table;
+  void *to_k, *to_v;                    // bf16 [pages][Hkv][16][D]
+  const int32_t* to_block_table;
+  const int32_t *first, *upto;          // [B]; first may be null
+  int num_pages, max_pages, to_num_pages, to_max_pages;
+  int hkv, head_dim;
   int* err;
 };
 
@@ -213,13 +249,29 @@ inline int verify_tc_max_active_clusters(int head_dim, int nq, bool capture, int
   return head_dim == 64 ? verify_tc_max_active_clusters_d64(nq, capture, cluster)
                         : verify_tc_max_active_clusters_d128(nq, capture, cluster);
 }
+// The tcgen05 verify kernel of the 8-bit cache: as many query columns as verify_tc's softmax takes.
+inline bool verify_kv8_supported(int head_dim, int nq) {
+  return nq >= 1 && nq <= (head_dim == 128 ? 40 : 64);
+}
+cudaError_t launch_verify_kv8_d64(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                  const VerifyParams& p, bool capture, int batch,
+                                  cudaStream_t stream);
+cudaError_t launch_verify_kv8_d128(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   const VerifyParams& p, bool capture, int batch,
+                                   cudaStream_t stream);
+int verify_kv8_max_active_clusters_d64(int nq, bool capture, int cluster);
+int verify_kv8_max_active_clusters_d128(int nq, bool capture, int cluster);
+inline int verify_kv8_max_active_clusters(int head_dim, int nq, bool capture, int cluster) {
+  return head_dim == 64 ? verify_kv8_max_active_clusters_d64(nq, capture, cluster)
+                        : verify_kv8_max_active_clusters_d128(nq, capture, cluster);
+}
 template <int D, bool CAP>
 cudaError_t launch_verify_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const VerifyParams& p, int ntiles, int batch, cudaStream_t stream);
 
 size_t sparse_smem_bytes(int head_dim, int ntiles);
 // Clusters of `cluster` draft-kernel CTAs resident at once (0: none / error).
-int sparse_max_active_clusters(int head_dim, int ntiles, int cluster);
+int sparse_max_active_clusters(int head_dim, int ntiles, int cluster, bool kv8);
 cudaError_t launch_sparse(const SparseParams& p, int head_dim, int ntiles, int batch,
                           cudaStream_t stream);
 
@@ -235,6 +287,8 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const PromptParams& p, int head_dim, int grid,
                           cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_kv8_append(const RopeKv8Params& p, cudaStream_t stream);
+cudaError_t launch_kv8_read(const Kv8ReadParams& p, int batch, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, bool bf16, cudaStream_t stream);
 
 // One CTA waits on an mbarrier nothing arrives on, bounded by limit_ns; on

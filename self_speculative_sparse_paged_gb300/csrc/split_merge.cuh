@@ -120,7 +120,7 @@ __device__ __forceinline__ void finish_splits(const SplitWorkspace& ws, int unit
 // output), for n < nq.  Called by every thread after reduce_row_sums; `area`
 // is free shared memory of `area_bytes` (the drained stage buffers), distinct
 // from the out arrays.
-template <int D, int NT, int W>
+template <int D, int NT, int W, class Dims = MmaDims>
 __device__ __forceinline__ void cta_merge_to_smem(const WarpState<D, NT>& st, uint8_t* area,
                                                   size_t area_bytes, int nq, float* outM,
                                                   float* outL, float* outO) {
@@ -167,7 +167,7 @@ __device__ __forceinline__ void cta_merge_to_smem(const WarpState<D, NT>& st, ui
 #pragma unroll
   for (int j = 0; j < E; ++j) acc[j] = 0.f;
   for (int w0 = 0; w0 < W; w0 += C) {
-    if (warp >= w0 && warp < w0 + C) stage_warp_o<D, NT>(st, cO, warp - w0);
+    if (warp >= w0 && warp < w0 + C) stage_warp_o<D, NT, Dims>(st, cO, warp - w0);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < E; ++j) {

@@ -94,18 +94,21 @@ vegas_status_t get_encoder(EncodeTiledFn* fn) {
 }
 
 // 2-D view of a paged cache: rows = num_pages * Hkv * 16, head_dim bf16 each;
-// box 16 rows x 64 elements (128 bytes), 128-byte swizzle.
-vegas_status_t make_cache_map(CUtensorMap* map, const void* base, const vegas_paged_kv_t* kv) {
+// box 16 rows x 64 elements (128 bytes), 128-byte swizzle.  kv8: head_dim bytes a row, the box 16
+// whole rows, swizzled over the row's length.
+vegas_status_t make_cache_map(CUtensorMap* map, const void* base, const vegas_paged_kv_t* kv,
+                              bool kv8 = false) {
   EncodeTiledFn enc;
   vegas_status_t st = get_encoder(&enc);
   if (st != VEGAS_OK) return st;
   cuuint64_t dims[2] = {(cuuint64_t)kv->head_dim,
                         (cuuint64_t)kv->num_pages * kv->num_kv_heads * VEGAS_PAGE_SIZE};
-  cuuint64_t strides[1] = {(cuuint64_t)kv->head_dim * 2};
-  cuuint32_t box[2] = {64, 16};
+  cuuint64_t strides[1] = {(cuuint64_t)kv->head_dim * (kv8 ? 1 : 2)};
+  cuuint32_t box[2] = {kv8 ? (cuuint32_t)kv->head_dim : 64u, 16};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = enc(map, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   kv8 && kv->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(VEGAS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return VEGAS_OK;
@@ -134,6 +137,33 @@ vegas_status_t check_kv(const vegas_paged_kv_t* kv) {
     return fail(VEGAS_ERR_UNSUPPORTED, "cache rows (num_pages * Hkv * 16) must be < 2^31");
   if ((long long)kv->max_pages_per_seq * VEGAS_PAGE_SIZE >= (1ll << 24))
     return fail(VEGAS_ERR_UNSUPPORTED, "sequence capacity must be < 2^24 positions");
+  return VEGAS_OK;
+}
+
+// An 8-bit cache's shape as a bf16 one of the same addresses, for what both kinds share.
+vegas_paged_kv_t shape_of(const vegas_paged_kv8_t* kv) {
+  vegas_paged_kv_t s{};
+  s.k_cache = kv->k_cache;
+  s.v_cache = kv->v_cache;
+  s.block_table = kv->block_table;
+  s.num_pages = kv->num_pages;
+  s.page_size = kv->page_size;
+  s.num_q_heads = kv->num_q_heads;
+  s.num_kv_heads = kv->num_kv_heads;
+  s.head_dim = kv->head_dim;
+  s.max_pages_per_seq = kv->max_pages_per_seq;
+  return s;
+}
+
+// With |q| below 2^40 and scales of 2^60 at most every factor of a logit stays in fp32.
+constexpr float kMaxKv8SoftmaxScale = 0x1p20f;
+
+vegas_status_t check_kv8(const vegas_paged_kv8_t* kv) {
+  if (!kv) return fail(VEGAS_ERR_INVALID_ARG, "kv is NULL");
+  const vegas_paged_kv_t s = shape_of(kv);
+  const vegas_status_t st = check_kv(&s);
+  if (st != VEGAS_OK) return st;
+  if (!kv->k_scale || !kv->v_scale) return fail(VEGAS_ERR_INVALID_ARG, "kv: NULL scales");
   return VEGAS_OK;
 }
 
@@ -171,14 +201,15 @@ struct VerifyPlan {
 // two columns holding the summed captured query (at the next even index).
 int verify_columns(int nq, bool capture) { return capture ? ((nq + 1) & ~1) + 2 : nq; }
 
+// kv8: the kernel of the 8-bit cache (its shapes are checked by the caller).
 VerifyPlan plan_verify(const vegas_paged_kv_t* kv, int batch, int gamma, int sms, bool capture,
-                       bool with_device) {
+                       bool with_device, bool kv8 = false) {
   VerifyPlan pl{};
   const int G = kv->num_q_heads / kv->num_kv_heads;
   pl.nq = (gamma + 1) * G;
   pl.ncols = verify_columns(pl.nq, capture);
   pl.ntiles = (pl.ncols + 7) / 8;
-  pl.tc = vegas::verify_tc_supported(kv->head_dim, pl.nq, capture);
+  pl.tc = kv8 || vegas::verify_tc_supported(kv->head_dim, pl.nq, capture);
   const int units = std::max(1, batch * kv->num_kv_heads);
   if (pl.tc && units < sms && with_device) {
     // C clusters of S CTAs per unit, every CTA resident (one wave), >= one tile
@@ -189,7 +220,8 @@ VerifyPlan plan_verify(const vegas_paged_kv_t* kv, int batch, int gamma, int sms
     int bestS = 0, bestC = 0, oneS = 0;
     for (int S = std::min(vegas::kMaxVerifyCluster, sms / units); S >= 2; --S) {
       const int resident =
-          vegas::verify_tc_max_active_clusters(kv->head_dim, pl.nq, capture, S);
+          kv8 ? vegas::verify_kv8_max_active_clusters(kv->head_dim, pl.nq, capture, S)
+              : vegas::verify_tc_max_active_clusters(kv->head_dim, pl.nq, capture, S);
       if (!oneS && S <= max_splits && resident >= units) oneS = S;
       // (the cross-cluster merge takes one lane per cluster: C <= 32)
       int C = std::min(std::min(sms / (units * S), max_splits / S), 32);
@@ -253,7 +285,8 @@ struct SparsePlan {
 // whose clusters are all resident at once, so every SM gathers.  Many units:
 // one wave of units x cluster <= SMs when every CTA's share fits its row
 // table, else the fewest CTAs that fit it.
-SparsePlan plan_sparse(const vegas_paged_kv_t* kv, int batch, int k_max, int max_tail, int sms) {
+SparsePlan plan_sparse(const vegas_paged_kv_t* kv, int batch, int k_max, int max_tail, int sms,
+                       bool kv8) {
   SparsePlan pl{};
   const int G = kv->num_q_heads / kv->num_kv_heads;
   pl.ntiles = (G + 7) / 8;
@@ -265,7 +298,7 @@ SparsePlan plan_sparse(const vegas_paged_kv_t* kv, int batch, int k_max, int max
     cl = std::min(vegas::kMaxSparseCluster, std::max(fit, std::min(sms / units,
                                                                    (rows_max + 63) / 64)));
     while (cl > std::max(fit, 1) &&
-           vegas::sparse_max_active_clusters(kv->head_dim, pl.ntiles, cl) < units)
+           vegas::sparse_max_active_clusters(kv->head_dim, pl.ntiles, cl, kv8) < units)
       --cl;
   } else {
     cl = std::max(fit, std::min(vegas::kMaxSparseCluster, std::max(1, sms / units)));
@@ -311,7 +344,8 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
                            int score_stride, const int32_t* ctx_lens, int batch, int gamma,
                            uint32_t row_mask, float softmax_scale, void* workspace,
                            size_t workspace_bytes, void* stream, float* raw = nullptr,
-                           int raw_stride = 0, vegas::ScratchFn scratch = nullptr);
+                           int raw_stride = 0, vegas::ScratchFn scratch = nullptr,
+                           const vegas_paged_kv8_t* kv8 = nullptr);
 }  // namespace
 
 namespace vegas {
@@ -409,8 +443,8 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
                            int score_stride, const int32_t* ctx_lens, int batch, int gamma,
                            uint32_t row_mask, float softmax_scale, void* workspace,
                            size_t workspace_bytes, void* stream, float* raw, int raw_stride,
-                           vegas::ScratchFn scratch) {
-  vegas_status_t st = check_kv(kv);
+                           vegas::ScratchFn scratch, const vegas_paged_kv8_t* kv8) {
+  vegas_status_t st = kv8 ? check_kv8(kv8) : check_kv(kv);
   if (st != VEGAS_OK) return st;
   if (batch < 0) return fail(VEGAS_ERR_INVALID_ARG, "batch %d", batch);
   if (gamma < 0 || gamma > 15) return fail(VEGAS_ERR_UNSUPPORTED, "gamma %d (0..15)", gamma);
@@ -418,10 +452,15 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
   if (!aligned16(q) || !aligned16(out))
     return fail(VEGAS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (!std::isfinite(softmax_scale)) return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale not finite");
+  if (kv8 && std::fabs(softmax_scale) > kMaxKv8SoftmaxScale)
+    return fail(VEGAS_ERR_UNSUPPORTED, "softmax_scale %g beyond 2^20", (double)softmax_scale);
   const int G = kv->num_q_heads / kv->num_kv_heads;
   const int nq = (gamma + 1) * G;
   const int ncols = verify_columns(nq, scores != nullptr);
-  if ((ncols + 7) / 8 > vegas::verify_max_ntiles(kv->head_dim))
+  if (kv8 && !vegas::verify_kv8_supported(kv->head_dim, nq))
+    return fail(VEGAS_ERR_UNSUPPORTED, "(gamma+1)*G = %d query rows: too many for head_dim %d", nq,
+                kv->head_dim);
+  if (!kv8 && (ncols + 7) / 8 > vegas::verify_max_ntiles(kv->head_dim))
     return fail(VEGAS_ERR_UNSUPPORTED,
                 "(gamma+1)*G = %d query rows (+2 capture columns) exceeds %d for head_dim %d", nq,
                 8 * vegas::verify_max_ntiles(kv->head_dim), kv->head_dim);
@@ -431,7 +470,7 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
   int* err = nullptr;
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
-  const VerifyPlan pl = plan_verify(kv, batch, gamma, sms, scores != nullptr, true);
+  const VerifyPlan pl = plan_verify(kv, batch, gamma, sms, scores != nullptr, true, kv8 != nullptr);
   const bool needs_ws = pl.needs_ws;
   if (scratch) {
     // A library-owned scratch serves exactly the shapes whose reported
@@ -451,12 +490,16 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
       return fail(VEGAS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
   CUtensorMap km, vm;
-  if ((st = make_cache_map(&km, kv->k_cache, kv)) != VEGAS_OK) return st;
-  if ((st = make_cache_map(&vm, kv->v_cache, kv)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&km, kv->k_cache, kv, kv8 != nullptr)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&vm, kv->v_cache, kv, kv8 != nullptr)) != VEGAS_OK) return st;
   vegas::VerifyParams p{};
   p.q = q;
   p.out = out;
   p.scores = scores;
+  if (kv8) {
+    p.k_scale = kv8->k_scale;
+    p.v_scale = kv8->v_scale;
+  }
   p.ctx_lens = ctx_lens;
   p.block_table = kv->block_table;
   p.score_stride = score_stride;
@@ -490,7 +533,12 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
     if (e != cudaSuccess) return cuda_fail(e, "clear scratch counters");
   }
   cudaError_t e =
-      pl.tc ? vegas::launch_verify_tc(km, vm, p, kv->head_dim, scores != nullptr, batch,
+      kv8 ? (kv->head_dim == 64 ? vegas::launch_verify_kv8_d64(km, vm, p, scores != nullptr, batch,
+                                                               static_cast<cudaStream_t>(stream))
+                                : vegas::launch_verify_kv8_d128(km, vm, p, scores != nullptr, batch,
+                                                                static_cast<cudaStream_t>(stream)))
+      : pl.tc
+          ? vegas::launch_verify_tc(km, vm, p, kv->head_dim, scores != nullptr, batch,
                                       static_cast<cudaStream_t>(stream))
             : launch_verify_any(km, vm, p, kv->head_dim, pl.ntiles, scores != nullptr, batch,
                                 static_cast<cudaStream_t>(stream));
@@ -498,6 +546,37 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
   return VEGAS_OK;
 }
 }  // namespace
+
+VEGAS_API size_t vegas_verify_kv8_workspace_size(const vegas_paged_kv8_t* kv, int batch,
+                                                 int gamma) {
+  if (check_kv8(kv) != VEGAS_OK || batch < 0 || gamma < 0 || gamma > 15) return 0;
+  const vegas_paged_kv_t shape = shape_of(kv);
+  if (!vegas::verify_kv8_supported(kv->head_dim,
+                                   (gamma + 1) * (kv->num_q_heads / kv->num_kv_heads)))
+    return 0;
+  int sms = 0;
+  const bool dev = device_info(nullptr, &sms) == VEGAS_OK && sms > 0;
+  if (!dev) sms = 148;
+  return std::max(plan_verify(&shape, batch, gamma, sms, true, dev, true).bytes,
+                  plan_verify(&shape, batch, gamma, sms, false, dev, true).bytes);
+}
+
+VEGAS_API vegas_status_t vegas_verify_attn_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, void* out, float* scores, int score_stride,
+    const int32_t* ctx_lens, int batch, int gamma, uint32_t capture_row_mask, float softmax_scale,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!kv) return fail(VEGAS_ERR_INVALID_ARG, "kv is NULL");
+  if (scores) {
+    if (gamma < 0 || gamma > 15) return fail(VEGAS_ERR_UNSUPPORTED, "gamma %d (0..15)", gamma);
+    if (capture_row_mask == 0 || (capture_row_mask >> (gamma + 1)) != 0)
+      return fail(VEGAS_ERR_INVALID_ARG, "capture row mask 0x%x: needs rows in [0, %d]",
+                  capture_row_mask, gamma);
+  }
+  const vegas_paged_kv_t shape = shape_of(kv);
+  return verify_impl(&shape, q, out, scores, score_stride, ctx_lens, batch, gamma,
+                     capture_row_mask, softmax_scale, workspace, workspace_bytes, stream, nullptr,
+                     0, nullptr, kv);
+}
 
 // =========================================================================
 // Top-k select
@@ -597,12 +676,13 @@ VEGAS_API vegas_status_t vegas_select_window(const int32_t* ctx_lens, int num_si
 // =========================================================================
 // Sparse draft-decode attention
 // =========================================================================
-VEGAS_API vegas_status_t vegas_sparse_decode_attn(
-    const vegas_paged_kv_t* kv, const void* q, void* out, const int32_t* idx, int k_max,
+namespace {
+// k_scale, v_scale: the 8-bit cache's exponents, or NULL for a bf16 one.
+vegas_status_t sparse_impl(
+    const vegas_paged_kv_t* kv, const uint8_t* k_scale, const uint8_t* v_scale, const void* q, void* out, const int32_t* idx, int k_max,
     const int32_t* k_per_seq, const int32_t* tail_start, const int32_t* tail_len, int max_tail,
     int batch, float softmax_scale, void* stream) {
-  vegas_status_t st = check_kv(kv);
-  if (st != VEGAS_OK) return st;
+  vegas_status_t st;
   if (batch < 0 || k_max < 0 || max_tail < 0)
     return fail(VEGAS_ERR_INVALID_ARG, "batch %d, k_max %d, max_tail %d", batch, k_max, max_tail);
   if (k_max + max_tail < 1) return fail(VEGAS_ERR_INVALID_ARG, "empty attention set");
@@ -610,6 +690,8 @@ VEGAS_API vegas_status_t vegas_sparse_decode_attn(
     return fail(VEGAS_ERR_INVALID_ARG, "NULL pointer argument");
   if (!aligned16(q)) return fail(VEGAS_ERR_INVALID_ARG, "q must be 16-byte aligned");
   if (!std::isfinite(softmax_scale)) return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale not finite");
+  if (k_scale && std::fabs(softmax_scale) > kMaxKv8SoftmaxScale)
+    return fail(VEGAS_ERR_UNSUPPORTED, "softmax_scale %g beyond 2^20", (double)softmax_scale);
   const int G = kv->num_q_heads / kv->num_kv_heads;
   if (G > 16) return fail(VEGAS_ERR_UNSUPPORTED, "group size %d (at most 16)", G);
   if ((long long)k_max + max_tail > vegas::kMaxSparseCluster * vegas::kMaxSparseRowsPerCta)
@@ -619,12 +701,14 @@ VEGAS_API vegas_status_t vegas_sparse_decode_attn(
   int* err = nullptr;
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
-  const SparsePlan pl = plan_sparse(kv, batch, k_max, max_tail, sms);
+  const SparsePlan pl = plan_sparse(kv, batch, k_max, max_tail, sms, k_scale != nullptr);
   vegas::SparseParams p{};
   p.q = q;
   p.out = out;
   p.k_cache = kv->k_cache;
   p.v_cache = kv->v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
   p.block_table = kv->block_table;
   p.idx = idx;
   p.k_per_seq = k_per_seq;
@@ -644,6 +728,28 @@ VEGAS_API vegas_status_t vegas_sparse_decode_attn(
                                        static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "sparse launch");
   return VEGAS_OK;
+}
+}  // namespace
+
+VEGAS_API vegas_status_t vegas_sparse_decode_attn(
+    const vegas_paged_kv_t* kv, const void* q, void* out, const int32_t* idx, int k_max,
+    const int32_t* k_per_seq, const int32_t* tail_start, const int32_t* tail_len, int max_tail,
+    int batch, float softmax_scale, void* stream) {
+  const vegas_status_t st = check_kv(kv);
+  if (st != VEGAS_OK) return st;
+  return sparse_impl(kv, nullptr, nullptr, q, out, idx, k_max, k_per_seq, tail_start, tail_len,
+                     max_tail, batch, softmax_scale, stream);
+}
+
+VEGAS_API vegas_status_t vegas_sparse_decode_attn_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, void* out, const int32_t* idx, int k_max,
+    const int32_t* k_per_seq, const int32_t* tail_start, const int32_t* tail_len, int max_tail,
+    int batch, float softmax_scale, void* stream) {
+  const vegas_status_t st = check_kv8(kv);
+  if (st != VEGAS_OK) return st;
+  const vegas_paged_kv_t shape = shape_of(kv);
+  return sparse_impl(&shape, kv->k_scale, kv->v_scale, q, out, idx, k_max, k_per_seq, tail_start,
+                     tail_len, max_tail, batch, softmax_scale, stream);
 }
 
 // =========================================================================
@@ -732,14 +838,14 @@ vegas_status_t make_rows_map(CUtensorMap* map, const void* base, const vegas_pag
 
 }  // namespace
 
-VEGAS_API vegas_status_t vegas_rope_append(
+namespace {
+// What both appends ask of their rows (a bf16 cache's shape stands for either cache).
+vegas_status_t check_append(
     const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const void* v, int64_t v_stride, const void* q_out, const int32_t* row_start,
     const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
-    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
-    int batch, void* stream) {
-  vegas_status_t st = check_kv(kv);
-  if (st != VEGAS_OK) return st;
+    const float* inv_freq, int rot_dim, float rope_scale, int total_rows, int batch) {
+  vegas_status_t st;
   if ((st = check_packed(row_start, ctx_lens, total_rows, batch)) != VEGAS_OK) return st;
   const int d = kv->head_dim;
   if ((st = check_rows("q", q, q_stride, kv->num_q_heads, d)) != VEGAS_OK) return st;
@@ -765,9 +871,16 @@ VEGAS_API vegas_status_t vegas_rope_append(
       lies_over(q_out, wq, k, k_stride, wkv, total_rows) ||
       lies_over(q_out, wq, v, v_stride, wkv, total_rows))   // other warps may not have read yet
     return fail(VEGAS_ERR_INVALID_ARG, "q_out lies over rows of q, k or v");
-  int* err = nullptr;
-  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
-  vegas::RopeParams p{};
+  return VEGAS_OK;
+}
+
+// The fields that both appends' parameters have.
+template <class Params, class Cache>
+void fill_append(Params& p, const Cache* kv, const void* q, int64_t q_stride, const void* k,
+                 int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                 const int32_t* row_start, const int32_t* ctx_lens, const int32_t* positions,
+                 const int32_t* pair_axis, int num_axes, const float* inv_freq, int rot_dim,
+                 int interleaved, float rope_scale, int total_rows, int batch, int* err) {
   p.q = q;
   p.k = k;
   p.v = v;
@@ -793,10 +906,97 @@ VEGAS_API vegas_status_t vegas_rope_append(
   p.max_pages = kv->max_pages_per_seq;
   p.hq = kv->num_q_heads;
   p.hkv = kv->num_kv_heads;
-  p.head_dim = d;
+  p.head_dim = kv->head_dim;
   p.err = err;
+}
+}  // namespace
+
+VEGAS_API vegas_status_t vegas_rope_append(
+    const vegas_paged_kv_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
+    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
+    int batch, void* stream) {
+  vegas_status_t st = check_kv(kv);
+  if (st != VEGAS_OK) return st;
+  if ((st = check_append(kv, q, q_stride, k, k_stride, v, v_stride, q_out, row_start, ctx_lens,
+                         positions, pair_axis, num_axes, inv_freq, rot_dim, rope_scale, total_rows,
+                         batch)) != VEGAS_OK)
+    return st;
+  if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
+  vegas::RopeParams p{};
+  fill_append(p, kv, q, q_stride, k, k_stride, v, v_stride, q_out, row_start, ctx_lens, positions,
+              pair_axis, num_axes, inv_freq, rot_dim, interleaved, rope_scale, total_rows, batch,
+              err);
   cudaError_t e = vegas::launch_rope_append(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope append launch");
+  return VEGAS_OK;
+}
+
+VEGAS_API vegas_status_t vegas_rope_append_kv8(
+    const vegas_paged_kv8_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, void* q_out, const int32_t* row_start,
+    const int32_t* ctx_lens, const int32_t* positions, const int32_t* pair_axis, int num_axes,
+    const float* inv_freq, int rot_dim, int interleaved, float rope_scale, int total_rows,
+    int batch, void* stream) {
+  vegas_status_t st = check_kv8(kv);
+  if (st != VEGAS_OK) return st;
+  const vegas_paged_kv_t shape = shape_of(kv);
+  if ((st = check_append(&shape, q, q_stride, k, k_stride, v, v_stride, q_out, row_start, ctx_lens,
+                         positions, pair_axis, num_axes, inv_freq, rot_dim, rope_scale, total_rows,
+                         batch)) != VEGAS_OK)
+    return st;
+  if (total_rows == 0 || batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
+  vegas::RopeKv8Params p{};
+  fill_append(p, kv, q, q_stride, k, k_stride, v, v_stride, q_out, row_start, ctx_lens, positions,
+              pair_axis, num_axes, inv_freq, rot_dim, interleaved, rope_scale, total_rows, batch,
+              err);
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  cudaError_t e = vegas::launch_kv8_append(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "quantised append launch");
+  return VEGAS_OK;
+}
+
+VEGAS_API vegas_status_t vegas_kv8_read(const vegas_paged_kv8_t* kv, const vegas_paged_kv_t* to,
+                                        const int32_t* first, const int32_t* upto, int batch,
+                                        void* stream) {
+  vegas_status_t st = check_kv8(kv);
+  if (st != VEGAS_OK) return st;
+  if ((st = check_kv(to)) != VEGAS_OK) return st;
+  if (kv->num_kv_heads != to->num_kv_heads || kv->head_dim != to->head_dim)
+    return fail(VEGAS_ERR_INVALID_ARG, "caches differ: %d KV heads of %d, and %d of %d",
+                kv->num_kv_heads, kv->head_dim, to->num_kv_heads, to->head_dim);
+  if (!upto) return fail(VEGAS_ERR_INVALID_ARG, "upto is NULL");
+  if (batch < 0) return fail(VEGAS_ERR_INVALID_ARG, "batch %d", batch);
+  if (batch > 65535) return fail(VEGAS_ERR_UNSUPPORTED, "batch %d (at most 65535)", batch);
+  if (batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
+  vegas::Kv8ReadParams p{};
+  p.k_cache = kv->k_cache;
+  p.v_cache = kv->v_cache;
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  p.block_table = kv->block_table;
+  p.to_k = const_cast<void*>(to->k_cache);
+  p.to_v = const_cast<void*>(to->v_cache);
+  p.to_block_table = to->block_table;
+  p.first = first;
+  p.upto = upto;
+  p.num_pages = kv->num_pages;
+  p.max_pages = kv->max_pages_per_seq;
+  p.to_num_pages = to->num_pages;
+  p.to_max_pages = to->max_pages_per_seq;
+  p.hkv = kv->num_kv_heads;
+  p.head_dim = kv->head_dim;
+  p.err = err;
+  cudaError_t e = vegas::launch_kv8_read(p, batch, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit cache read launch");
   return VEGAS_OK;
 }
 
