@@ -7,16 +7,19 @@
 //
 //   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
 //       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
-//       parts (4 + 4 bits of bf16's 8), so the products are exact and S takes two passes over the
-//       same accumulator.  Captured scores take the summed captured query (fp32) in six parts: three
-//       more columns of two parts each, 2^8 apart.  (kind::f8f6f4 sums e4m3 products to fp32's
-//       precision here: 2.3e-7 of the terms' sum at worst, measured over random codes.)
-//   z = S 2^(e_k - k) scale log2(e) + e_v,  P = 2^(z - r) in f16, r a reference for the column:
+//       parts (4 + 4 bits of bf16's 8), so the products are exact.  Captured scores take the
+//       summed captured query (fp32) in six parts, two and two 2^8 apart.  (kind::f8f6f4
+//       sums e4m3 products to fp32's precision here: 2.3e-7 of the terms' sum at worst, measured
+//       over random codes.)
+//   z = S 2^(e_k - k) scale log2(e) + e_v,  P = 2^(z - r) with r a reference for the column:
 //       e_k costs nothing (a thread's one factor), and 2^e_v goes into P instead of V.  Row sums
 //       take P 2^-e_v in fp32.
 //   O^T[D x N] += V'^T P^T   kind::f16, M = D: V' are V's codes as f16, exact; each thread of a
-//       softmax group turns its own position's row (16 codes: one load, 8 conversions, two stores).
+//       softmax group turns its own position's row (16 codes: one load, 8 conversions, two stores)
+//       while the tensor cores still work on S of the tile.
 //
+// The two parts of the queries lie side by side in N (one pass over K; an MMA takes 45 clocks up
+// to N = 64 and 64 at 128) up to 40 columns, else they share an accumulator.
 // P <= 2^15 (f16 ends at 65504) and the largest P is 2^7 or more when r was raised, so P's grid
 // reaches 2^-31 below the largest.  e_v spans 120, so that no term that weighs in a row sum is lost to
 // fp32's smallest number (its P is at least 2^-121).
@@ -31,16 +34,16 @@ namespace vegas {
 
 namespace {
 constexpr float kTop = 15.f, kRaise = 7.f;   // log2 of the largest P, and of P at a raised reference
-constexpr int kCapColumns = 3;
+constexpr int kCapParts = 6;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
-// Instruction descriptors, fp32 accumulator: e4m3 by e4m3 (K = 32), f16 by f16 (K = 16).
+// Instruction descriptors, fp32 accumulator: e4m3 by e4m3, K-major (K = 32); f16 by f16,
+// MN-major (K = 16).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int a_mn_major, int b_mn_major) {
-  return (1u << 4) | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) |
-         (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int m, int n) {
+  return (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, bool accumulate) {
@@ -50,22 +53,33 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// Four consecutive fp32 columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
-  uint32_t r[4];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr)
-               : "memory");
+// Lane l gets op over the warp's lanes of their v[l]: in five steps a lane exchanges half of the
+// columns it still holds for the other half of another lane's (31 shuffles for 32 columns).
+template <class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[32], Op op) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool upper = lane & w;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float give = upper ? v[j] : v[j + w], keep = upper ? v[j + w] : v[j];
+      v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
+    }
+  }
+  return v[0];
 }
 }  // namespace
 
 template <int D, int NQC, bool CAPTURE>
 struct Kv8Cfg {
-  static constexpr int NS = (NQC + (CAPTURE ? kCapColumns : 0) + 15) / 16 * 16;   // N of S
-  static constexpr int NP = (NQC + 15) / 16 * 16;                                 // N of PV
+  // S: [high parts | low parts | capture parts] side by side, or the two parts of NQC + 3 columns
+  // one after the other.
+  static constexpr bool kSideS = NQC <= 40;
+  static constexpr int kCap = CAPTURE ? (kSideS ? kCapParts : kCapParts / 2) : 0;
+  static constexpr int kCap0 = kSideS ? 2 * NQC : NQC;    // first capture column
+  static constexpr int NS = (kCap0 + kCap + 15) / 16 * 16;   // N of S
+  static constexpr int NP = (NQC + 15) / 16 * 16;     // N of PV
   static constexpr int kTile = 128 * D;               // one K tile (and one V tile): 8 pages
   // Ring slots (16 KB at head_dim 128, 8 KB at 64): as many as fit beside the rest.
   static constexpr int KS = D == 64 ? 8 : 4;
@@ -73,25 +87,28 @@ struct Kv8Cfg {
   static constexpr int kV16 = 128 * D * 2;            // a tile's V' [half][128][128 B], one a group
   static constexpr int kPRow = NQC <= 32 ? 64 : 128;  // bytes of a position's P row
   static constexpr int kP = 128 * kPRow;
-  static constexpr int kQ = NS * D;                   // one part of the queries
+  static constexpr int kQ = NS * D;                   // Q^T operand, one a pass
+  static constexpr int kPasses = kSideS ? 1 : 2;
   static constexpr int kThreads = 384;
   static constexpr int kSCol = (NS + 31) / 32 * 32, kOCol = (NP + 31) / 32 * 32;
   static constexpr uint32_t kTmemCols =
       2 * (kSCol + kOCol) <= 128 ? 128 : 2 * (kSCol + kOCol) <= 256 ? 256 : 512;
+  static_assert(2 * (kSCol + kOCol) <= 512, "tensor memory");
   static constexpr int kOffV = KS * kTile;
   static constexpr int kOffV16 = kOffV + VS * kTile;
   static constexpr int kOffP = kOffV16 + 2 * kV16;
   static constexpr int kOffQ = kOffP + 2 * kP;
-  static constexpr int kOffBar = kOffQ + 2 * kQ;
+  static constexpr int kOffBar = kOffQ + kPasses * kQ;
   static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 1;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  // misc: tmem slot, flag, capture exponent, uniform flag; votes[2][4]; colmax[2][4][NQC],
-  // colsum[2][4][NQC], col[NQC], nref[2][NQC]; tlim[NQC]; rowexp[NQC]; qsum[256]
-  static constexpr size_t kMisc = 16 + 32 + 4 * (16 * NQC + 3 * NQC + 2 * NQC + 256);
+  // misc: tmem slot, flag, capture exponent, uniform flag; votes[2][2][4]; colmax[2][4][NQC],
+  // colsum[2][4][NQC], col[NQC], nref[2][NQC]; tlim[NQC]; rowexp[NQC]
+  static constexpr size_t kMisc = 16 + 64 + 4 * (16 * NQC + 3 * NQC + 2 * NQC);
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
+  static constexpr int kMergeOff = (merge_receive_bytes<D, NQC>() + 1023) / 1024 * 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(merge_receive_bytes<D, NQC>() <= kOffV16, "receive area (the rings)");
-  static_assert(kMergeWeightBytes <= 2 * kV16, "merge weights");
+  static_assert(kMergeOff + kMergeWeightBytes <= kOffP, "merge areas");
+  static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
 };
 
 template <int D, int NQC, bool CAPTURE>
@@ -100,6 +117,7 @@ __global__ void __launch_bounds__(384, 1)
                       const __grid_constant__ CUtensorMap vmap, const VerifyParams p) {
   using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
   constexpr int KS = Cfg::KS, VS = Cfg::VS, NS = Cfg::NS, NP = Cfg::NP;
+  constexpr bool kSideS = Cfg::kSideS;
   static_assert(NQC % 8 == 0 && (D == 64 || D == 128), "columns, head_dim");
 
   griddep_launch_dependents();
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(384, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + Cfg::kOffBar;
-  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P (and V')
+  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P and V'
   // ready, PV done (per softmax group); MMA drain
   auto kfull = [&](int s) { return bar0 + 8 * s; };
   auto kfree = [&](int s) { return bar0 + 8 * (KS + s); };
@@ -125,14 +143,14 @@ __global__ void __launch_bounds__(384, 1)
   int* flag = reinterpret_cast<int*>(misc + 4);
   int* capexp = reinterpret_cast<int*>(misc + 8);
   int* uniform = reinterpret_cast<int*>(misc + 12);
-  int* votes = reinterpret_cast<int*>(misc + 16);                // [2][4]
-  float* colmax = reinterpret_cast<float*>(misc + 48);           // [2][4][NQC]
+  int* votes = reinterpret_cast<int*>(misc + 16);                // [2][2][4]
+  float* colmax = reinterpret_cast<float*>(misc + 80);           // [2][4][NQC]
   float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
   float* colfac = colsum + 8 * NQC;                              // [NQC] scale log2(e) 2^-k
   float* nrefs = colfac + NQC;                                   // [2][NQC] -reference
   int* tlim = reinterpret_cast<int*>(nrefs + 2 * NQC);           // [NQC]
   int* rowexp = tlim + NQC;                                      // [NQC]
-  float* qsum = reinterpret_cast<float*>(rowexp + NQC);          // [256 / D][D] parts of the captured sum
+  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffP);     // [8][D] parts of the captured sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
@@ -215,9 +233,12 @@ __global__ void __launch_bounds__(384, 1)
   const int grp = (warp - 2) >> 2;          // 0: even tiles, 1: odd tiles
   const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
   const int i = 32 * q4 + lane;             // tile position owned
+  // (volatile, here and for the scales: the compiler may not move the loads down to their uses)
   auto scale_block = [&](int t) {           // the page's block of scales, by its table entry
     const int page = min(pbeg + 8 * t + (i >> 4), p.max_pages - 1);
-    return __ldg(&bt_row[page]);
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(bt_row + page));
+    return v;
   };
   int phys0 = 0, phys1 = 0;
   if (softmax_warp) {
@@ -258,17 +279,23 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) rowexp[warp - 2 + 8 * u] = most ? max(-100, int(most >> 7) - 127) : -1000;
       }
       if (CAPTURE) {
-        // the captured query, summed over its rows and heads: a thread takes one dim, 256 / D
-        // threads share it
-        const int ct = tid - 64, dim = ct % D;
-        float acc = 0.f;
-        for (int t = 0; t <= p.gamma; ++t) {
-          if (!((p.row_mask >> t) & 1u)) continue;
-          for (int h2 = ct / D; h2 < p.group; h2 += 256 / D)
-            acc += __bfloat162float(
-                qbase[((size_t(b) * T + t) * p.hq + g * p.group + h2) * D + dim]);
+        // the captured query, summed over its rows and heads: this warp's rows
+        float acc[D / 64][2] = {};
+#pragma unroll
+        for (int u = 0; u < QPER; ++u) {
+          const int n = warp - 2 + 8 * u;
+          if (n < p.nq && ((p.row_mask >> (n / p.group)) & 1u)) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              acc[h][0] += __uint_as_float(qreg[u][h] << 16);
+              acc[h][1] += __uint_as_float(qreg[u][h] & 0xffff0000u);
+            }
+          }
         }
-        qsum[ct] = acc;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<float2*>(qsum + (warp - 2) * D + 64 * h + 2 * lane) =
+              make_float2(acc[h][0], acc[h][1]);
       }
     }
     for (int n = tid - 32; n < NQC; n += SN) tlim[n] = n < p.nq ? n / p.group : -1;
@@ -285,15 +312,15 @@ __global__ void __launch_bounds__(384, 1)
     least = __reduce_min_sync(0xffffffffu, least);
     const bool one = most - least <= 4;
     if (most == -1000) most = 0;
-    // x as two parts, hi + lo, of e4m3: |x| < 2^8
-    auto put_parts = [&](int n, int k, float x0, float x1, uint8_t* first, uint8_t* second) {
-      const uint32_t hi = e4m3x2_from_f32(x0, x1);
+    // The next e4m3 part of (x0, x1), |x| < 2^8, to row n of a pass; x keeps the rest.
+    auto put_part = [&](int pass, int n, int k, float& x0, float& x1) {
+      const uint32_t c = e4m3x2_from_f32(x0, x1);
+      *reinterpret_cast<uint16_t*>(qs + pass * Cfg::kQ + qoff(n, k)) = uint16_t(c);
       uint32_t h, unused;
-      f16x2_from_e4m3x4(hi, h, unused);
+      f16x2_from_e4m3x4(c, h, unused);
       const float2 v = f32x2_from_f16x2(h);
-      const uint32_t lo = e4m3x2_from_f32(x0 - v.x, x1 - v.y);
-      *reinterpret_cast<uint16_t*>(first + qoff(n, k)) = uint16_t(hi);
-      *reinterpret_cast<uint16_t*>(second + qoff(n, k)) = uint16_t(lo);
+      x0 -= v.x;
+      x1 -= v.y;
     };
     if (softmax_warp) {
 #pragma unroll
@@ -302,53 +329,54 @@ __global__ void __launch_bounds__(384, 1)
         const int e = rowexp[n], k = 7 - (one ? most : e == -1000 ? 0 : e);
         const float f = two_to(k);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          put_parts(n, 64 * h + 2 * lane, __uint_as_float(qreg[u][h] << 16) * f,
-                    __uint_as_float(qreg[u][h] & 0xffff0000u) * f, qs, qs + Cfg::kQ);
+        for (int h = 0; h < D / 64; ++h) {
+          float x0 = __uint_as_float(qreg[u][h] << 16) * f;
+          float x1 = __uint_as_float(qreg[u][h] & 0xffff0000u) * f;
+          put_part(0, n, 64 * h + 2 * lane, x0, x1);
+          put_part(kSideS ? 0 : 1, kSideS ? NQC + n : n, 64 * h + 2 * lane, x0, x1);
+        }
         if (lane == 0) colfac[n] = one ? 1.f : two_to(-k);
       }
     } else {
       // warp 1: the captured query's parts, and the rows that fill up N
-      int row = NQC;
+      int row = Cfg::kCap0;
       if constexpr (CAPTURE) {
-        row += kCapColumns;
+        row += Cfg::kCap;
         float x[D / 64][2];
         float top = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
+        for (int h = 0; h < D / 64; ++h) {
+          float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = 0.f;
-#pragma unroll
-            for (int j = 0; j < 256 / D; ++j) v += qsum[j * D + 64 * h + 2 * lane + e];
-            x[h][e] = v;
-            top = fmaxf(top, fabsf(v));
+          for (int j = 0; j < 8; ++j) {
+            const float2 w = *reinterpret_cast<const float2*>(qsum + j * D + 64 * h + 2 * lane);
+            v.x += w.x;
+            v.y += w.y;
           }
+          x[h][0] = v.x;
+          x[h][1] = v.y;
+          top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         const int k = 7 - max(-100, int(bits >> 23) - 127);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
           float x0 = x[h][0] * two_to(k), x1 = x[h][1] * two_to(k);
 #pragma unroll
-          for (int j = 0; j < kCapColumns; ++j) {
-            // two parts leave less than 2^-8 of the largest: the next two start 2^8 lower
-            const int kk = 64 * h + 2 * lane;
-            put_parts(NQC + j, kk, x0, x1, qs, qs + Cfg::kQ);
-            uint32_t a, c, unused;
-            f16x2_from_e4m3x4(*reinterpret_cast<uint16_t*>(qs + qoff(NQC + j, kk)), a, unused);
-            f16x2_from_e4m3x4(*reinterpret_cast<uint16_t*>(qs + Cfg::kQ + qoff(NQC + j, kk)), c,
-                              unused);
-            const float2 va = f32x2_from_f16x2(a), vc = f32x2_from_f16x2(c);
-            x0 = (x0 - va.x - vc.x) * 256.f;
-            x1 = (x1 - va.y - vc.y) * 256.f;
+          for (int j = 0; j < kCapParts; ++j) {
+            put_part(kSideS ? 0 : j & 1, Cfg::kCap0 + (kSideS ? j : j >> 1), 64 * h + 2 * lane, x0, x1);
+            if (j & 1) {   // two parts leave less than 2^-8 of the largest: the next two start 2^8 lower
+              x0 *= 256.f;
+              x1 *= 256.f;
+            }
           }
         }
         if (lane == 0) *capexp = -k;
       }
-      for (int j = lane; j < (NS - row) * D / 4; j += 32) {
-        reinterpret_cast<uint32_t*>(qs + row * D)[j] = 0;
-        reinterpret_cast<uint32_t*>(qs + Cfg::kQ + row * D)[j] = 0;
-      }
+      for (int j = lane; j < (NS - row) * D / 4; j += 32)
+#pragma unroll
+        for (int pass = 0; pass < Cfg::kPasses; ++pass)
+          reinterpret_cast<uint32_t*>(qs + pass * Cfg::kQ + row * D)[j] = 0;
       if (lane == 0) *uniform = one ? most - 7 : kMixed;
     }
     // Generic-proxy writes of Q must be visible to the tensor cores (async proxy).
@@ -417,7 +445,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idS = idesc_e4m3(128, NS);
-    constexpr uint32_t idPV = idesc_f16(D, NP, 1, 1);
+    constexpr uint32_t idPV = idesc_f16_mn(D, NP);
     const bool leader = elect_one();
     // K and Q rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one; V' and
     // P MN-major, P's rows of 128 or 64 bytes
@@ -453,10 +481,10 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t kb = (sbase + s * Cfg::kTile) >> 4;
       if (leader) {
 #pragma unroll
-        for (int j = 0; j < 2 * (D / 32); ++j) {
-          const int part = j / (D / 32), ks = j % (D / 32);
+        for (int j = 0; j < Cfg::kPasses * (D / 32); ++j) {
+          const int pass = j / (D / 32), ks = j % (D / 32);
           tc_mma_e4m3(tmem + Cfg::kSCol * gg, with_addr(dKQ, kb + 2 * ks),
-                      with_addr(dKQ, qb + part * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
+                    with_addr(dKQ, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
         }
         tc_commit(sfull(gg));
         tc_commit(kfree(s));
@@ -504,7 +532,41 @@ __global__ void __launch_bounds__(384, 1)
     auto scale_at = [&](int phys) {
       return size_t(phys < 0 || phys >= p.num_pages ? 0 : phys) * p.hkv + g;
     };
-    uint8_t ekb = p.k_scale[scale_at(phys0)], evb = p.v_scale[scale_at(phys0)];
+    auto load_scale = [](const uint8_t* at) {
+      uint32_t v;
+      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(at));
+      return v;
+    };
+    uint32_t ekb = load_scale(p.k_scale + scale_at(phys0)), evb = load_scale(p.v_scale + scale_at(phys0));
+    // S of columns 8 c .. 8 c + 7, the parts added
+    auto load_chunk = [&](uint32_t at, int c, float* y) {
+      float v8[8], w8[8];
+      tmem_ld8(at + 8 * c, v8);
+      if constexpr (kSideS) tmem_ld8(at + NQC + 8 * c, w8);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = kSideS ? v8[e] + w8[e] : v8[e];
+    };
+    // of all columns, up to three chunks in flight
+    auto load_all = [&](uint32_t at, float* y) {
+#pragma unroll
+      for (int c0 = 0; c0 < NQC / 8; c0 += 3) {
+        float v8[3][8], w8[3][8];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (c0 + c >= NQC / 8) continue;
+          tmem_ld8(at + 8 * (c0 + c), v8[c]);
+          if constexpr (kSideS) tmem_ld8(at + NQC + 8 * (c0 + c), w8[c]);
+        }
+        if (kSideS || c0 + 3 >= NQC / 8) tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (c0 + c >= NQC / 8) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[8 * (c0 + c) + e] = kSideS ? v8[c][e] + w8[c][e] : v8[c][e];
+        }
+      }
+    };
     int mytiles = 0;
     // A failed (timed-out) wait is carried to the group vote below, so the 128
     // threads of a group always leave the loop together.
@@ -515,96 +577,140 @@ __global__ void __launch_bounds__(384, 1)
       const int pos = page * 16 + (i & 15);
       // this position's scales; the next tile's are requested, and the page after that
       // (a row past the range holds the tile's first page again: its scales change nothing)
-      const int e_k = kv8_exponent(ekb), e_v = kv8_exponent(evb);
-      ekb = __ldg(&p.k_scale[scale_at(phys1)]);
-      evb = __ldg(&p.v_scale[scale_at(phys1)]);
+      const int e_k = kv8_exponent(uint8_t(ekb)), e_v = kv8_exponent(uint8_t(evb));
+      ekb = load_scale(p.k_scale + scale_at(phys1));
+      evb = load_scale(p.v_scale + scale_at(phys1));
       phys1 = scale_block(t + 4);
-      bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
-      tc_fence_after();
-      float y[NQC];
-      float cx[4] = {0.f, 0.f, 0.f, 0.f};   // the capture columns
+      // V' row i: the codes as f16 (zeros behind the window, where a code may be NaN), once PV of
+      // the group's last tile has read the buffer; S of this tile follows that PV in the tensor pipe,
+      // so this work hides behind it
+      bool okt = ok && (k == 0 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
+      okt = okt && mbar_wait_bounded(vfull(s), (t / VS) & 1);
+      {
+        const int lpos = (live ? page : pbeg + 8 * t) * 16 + (i & 15);   // position loaded in row i
+        const uint8_t* vrow = smem + Cfg::kOffV + s * Cfg::kTile + i * D;
+        uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
+        const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
+        uint4 v[D / 16];   // (all loads ahead of the first store, which they might alias)
 #pragma unroll
-      for (int n = 0; n < NQC; ++n) y[n] = 0.f;
+        for (int c = 0; c < D / 16; ++c)
+          v[c] = *reinterpret_cast<const uint4*>(vrow + ((c ^ sw) << 4));
+        if (lpos > last_valid) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint4 a, d;
+          f16x2_from_e4m3x4(v[c].x, a.x, a.y);
+          f16x2_from_e4m3x4(v[c].y, a.z, a.w);
+          f16x2_from_e4m3x4(v[c].z, d.x, d.y);
+          f16x2_from_e4m3x4(v[c].w, d.z, d.w);
+          uint8_t* dst = v16 + (c >> 2) * 16384;
+          const int cc = 2 * (c & 3);
+          *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
+          *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
+        }
+        mbar_arrive(vfree(s));
+      }
+      const float f_k = two_to(e_k), un = two_to(-e_v);
+      const float f = live ? base * f_k : 0.f, add = live ? float(e_v) : -INFINITY;
+      const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
+      okt = okt && mbar_wait_bounded(sfull(grp), k & 1);
+      tc_fence_after();
+      // z of columns 8 c .. 8 c + 7 less their references; positions past the range are masked
+      auto z_chunk = [&](int c, float* y) {   // (y: S in, z out)
+        if (mixed) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] *= colfac[8 * c + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          float4 r4;
+          if constexpr (kSmemRef)
+            r4 = reinterpret_cast<const float4*>(nrg)[2 * c + e / 4];
+          else
+            r4 = make_float4(nr[8 * c + e], nr[8 * c + e + 1], nr[8 * c + e + 2], nr[8 * c + e + 3]);
+          const uint64_t a = add_f32x2(fma_f32x2(pair_f32(y[e], y[e + 1]), f2, add2), pair_f32(r4.x, r4.y));
+          const uint64_t d =
+              add_f32x2(fma_f32x2(pair_f32(y[e + 2], y[e + 3]), f2, add2), pair_f32(r4.z, r4.w));
+          unpair_f32(a, y[e], y[e + 1]);
+          unpair_f32(d, y[e + 2], y[e + 3]);
+        }
+        if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (pos > L + tlim[8 * c + e]) y[e] = -INFINITY;
+        }
+      };
+      // P = 2^y of a chunk, eight f16 in 16 bytes of position i's row of columns, swizzled
+      uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
+      const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
+      auto p_chunk = [&](int c, const float* y, bool sum) {
+        uint32_t w4[4];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float p0 = ex2(y[e]), p1 = ex2(y[e + 1]);
+          if (sum) ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
+          w4[e / 2] = pack_f16x2(p0, p1);
+        }
+        *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+      };
+      bool need = empty != 0;
       if (okt) {
+        float y[NQC];
+        float cx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // the capture columns
+        if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+        load_all(tl + s_col, y);
+        if (CAPTURE && pos < Lcap && live) {
+          if constexpr (kSideS) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
+          }
+          srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
+        }
+        float ym = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NQC / 8; ++c) {
-          float v8[8];
-          tmem_ld8(tl + s_col + 8 * c, v8);
+          z_chunk(c, y + 8 * c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[8 * c + e] = v8[e];
+          for (int e = 0; e < 8; e += 2) ym = fmaxf(fmaxf(ym, y[8 * c + e]), y[8 * c + e + 1]);
         }
-        if constexpr (CAPTURE) tmem_ld4(tl + s_col + NQC, cx);
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(sread(grp));
-      }
-      const float f_k = two_to(e_k);
-      if (CAPTURE && okt && pos < Lcap && live)
-        srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
-      // z less the reference; positions past the range are masked
-      if (mixed) {
+        need = __any_sync(0xffffffffu, need || ym > kTop);
+        // a warp that needs a higher reference leaves P and its sums to the raise below
+        if (!need) {
 #pragma unroll
-        for (int c = 0; c < NQC / 4; ++c) {
-          const float4 v = reinterpret_cast<const float4*>(colfac)[c];
-          y[4 * c] *= v.x;
-          y[4 * c + 1] *= v.y;
-          y[4 * c + 2] *= v.z;
-          y[4 * c + 3] *= v.w;
+          for (int c = 0; c < NQC / 8; ++c) p_chunk(c, y + 8 * c, true);
         }
       }
-      const float f = live ? base * f_k : 0.f, add = live ? float(e_v) : -INFINITY;
-      const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add);
+      // (columns that fill up N are never read; their P may be anything)
+      const bool all_ok = __all_sync(0xffffffffu, okt);
+      if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
+      if (named_bar_any(1 + grp, 128, need || !okt)) {
+        const int* vt = votes + (k & 1) * 8 + grp * 4;
+        if (vt[0] | vt[1] | vt[2] | vt[3]) {
+          ok = false;
+          break;
+        }
+        // Raise: column maxima over the group's 128 positions, from S once more.  PV of the group's
+        // last tile is done (above), so O^T may be rescaled.
+        float* cm = colmax + grp * 4 * NQC;
 #pragma unroll
-      for (int c = 0; c < NQC / 4; ++c) {
-        float4 r4;
-        if constexpr (kSmemRef)
-          r4 = reinterpret_cast<const float4*>(nrg)[c];
-        else
-          r4 = make_float4(nr[4 * c], nr[4 * c + 1], nr[4 * c + 2], nr[4 * c + 3]);
-        uint64_t a = fma_f32x2(pair_f32(y[4 * c], y[4 * c + 1]), f2, add2);
-        uint64_t d = fma_f32x2(pair_f32(y[4 * c + 2], y[4 * c + 3]), f2, add2);
-        a = add_f32x2(a, pair_f32(r4.x, r4.y));
-        d = add_f32x2(d, pair_f32(r4.z, r4.w));
-        unpair_f32(a, y[4 * c], y[4 * c + 1]);
-        unpair_f32(d, y[4 * c + 2], y[4 * c + 3]);
-      }
-      if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
+        for (int c0 = 0; c0 < NQC; c0 += 32) {
+          constexpr float kNone = -INFINITY;
+          float y[32];
 #pragma unroll
-        for (int n = 0; n < NQC; ++n)
-          if (pos > L + tlim[n]) y[n] = -INFINITY;
-      }
-      float ym[2] = {-INFINITY, -INFINITY};
+          for (int e = 0; e < 32; ++e) y[e] = kNone;
 #pragma unroll
-      for (int n = 0; n < NQC; n += 4) {
-        ym[0] = fmaxf(fmaxf(ym[0], y[n]), y[n + 1]);
-        ym[1] = fmaxf(fmaxf(ym[1], y[n + 2]), y[n + 3]);
-      }
-      const bool need = fmaxf(ym[0], ym[1]) > kTop;
-      // V's codes of this position have landed
-      okt = okt && mbar_wait_bounded(vfull(s), (t / VS) & 1);
-      const int wvote = (__any_sync(0xffffffffu, need) ? 1 : 0) | (__any_sync(0xffffffffu, !okt) ? 2 : 0);
-      if (lane == 0) votes[grp * 4 + q4] = wvote;
-      named_bar(1 + grp, 128);
-      const int allv = votes[grp * 4] | votes[grp * 4 + 1] | votes[grp * 4 + 2] | votes[grp * 4 + 3];
-      if (allv & 2) {
-        ok = false;
-        break;
-      }
-      // The group's previous PV (tile t - 2) must have finished before its O^T is rescaled or its
-      // P^T and V' buffers are rewritten.
-      const bool pv_ok = k == 0 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1);
-      tc_fence_after();
-      if ((allv & 1) || empty) {
-        // column maxima over the group's 128 positions
-#pragma unroll
-        for (int n = 0; n < NQC; ++n) {
-          float v = y[n];
-#pragma unroll
-          for (int o2 = 16; o2 > 0; o2 >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o2));
-          if (lane == 0) colmax[(grp * 4 + q4) * NQC + n] = v;
+          for (int c = 0; c < 4; ++c) {
+            if (c0 + 8 * c >= NQC) continue;
+            load_chunk(tl + s_col, c0 / 8 + c, y + 8 * c);
+            z_chunk(c0 / 8 + c, y + 8 * c);
+          }
+          const float top = reduce_columns(y, [](float a, float d) { return fmaxf(a, d); });
+          if (c0 + lane < NQC) cm[q4 * NQC + c0 + lane] = top;
         }
         named_bar(1 + grp, 128);
-        const float* cm = colmax + grp * 4 * NQC;
         // column n's new reference, at least kRaise below the largest z (cm is relative to the old one)
         auto raised = [&](int n, float nro, float& old) {
           const float top = fmaxf(fmaxf(cm[n], cm[NQC + n]), fmaxf(cm[2 * NQC + n], cm[3 * NQC + n]));
@@ -612,35 +718,31 @@ __global__ void __launch_bounds__(384, 1)
           return fmaxf(old, top - nro - kRaise);
         };
         uint64_t empty2 = empty;
+        float fac[NQC];
 #pragma unroll
-        for (int c = 0; c < NQC / 8; ++c) {
-          float f8[8];
+        for (int n = 0; n < NQC; ++n) {
+          const float nro = kSmemRef ? nrg[n] : nr[kSmemRef ? 0 : n];
+          float old;
+          const float now = raised(n, nro, old);
+          const bool now_empty = now == kEmptyMax;
+          fac[n] = ex2(old - now);
+          if (!now_empty) empty2 &= ~(1ull << n);
+          if constexpr (!kSmemRef) nr[n] = now_empty ? 0.f : -now;
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int n = 8 * c + e;
-            const float nro = kSmemRef ? nrg[n] : nr[kSmemRef ? 0 : n];
-            float old;
-            const float now = raised(n, nro, old);
-            const bool now_empty = now == kEmptyMax;
-            f8[e] = ex2(old - now);
-            if (!now_empty) empty2 &= ~(1ull << n);
-            const float nrn = now_empty ? 0.f : -now;
-            y[n] += nrn - nro;
-            if constexpr (!kSmemRef) nr[n] = nrn;
-          }
+        for (int n = 0; n < NQC; n += 2) ls2[n / 2] = mul_f32x2(ls2[n / 2], pair_f32(fac[n], fac[n + 1]));
+        if (k > 0) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2)
-            ls2[4 * c + e / 2] = mul_f32x2(ls2[4 * c + e / 2], pair_f32(f8[e], f8[e + 1]));
-          if (k > 0 && pv_ok) {
+          for (int c = 0; c < NQC / 8; ++c) {
             float v8[8];
             tmem_ld8(tl + o_col + 8 * c, v8);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v8[e] *= f8[e];
+            for (int e = 0; e < 8; ++e) v8[e] *= fac[8 * c + e];
             tmem_st8(tl + o_col + 8 * c, v8);
           }
         }
-        if (k > 0 && pv_ok) tmem_st_wait();
+        if (k > 0) tmem_st_wait();
         named_bar(1 + grp, 128);   // colmax (and nrg) read; colmax is rewritten at the next raise
         if constexpr (kSmemRef) {
           if (i < NQC) {
@@ -652,50 +754,19 @@ __global__ void __launch_bounds__(384, 1)
           named_bar(1 + grp, 128);   // new references visible
         }
         empty = empty2;
-      }
-      // P = 2^y, position i's row of columns, eight f16 a 16-byte chunk, swizzled
-      const float un = two_to(-e_v);
-      const uint64_t un2 = pair_f32(un, un);
-      uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
-      const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
+        // P of this tile with the new references; the sums of a warp that has them were rescaled
 #pragma unroll
-      for (int c = 0; c < NP / 8; ++c) {
-        uint32_t w4[4] = {0u, 0u, 0u, 0u};
-        if (8 * c < NQC) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int n = 8 * c + e;
-            const float p0 = ex2(y[n]), p1 = ex2(y[n + 1]);
-            ls2[n / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[n / 2]);
-            w4[e / 2] = pack_f16x2(p0, p1);
-          }
+        for (int c = 0; c < NQC / 8; ++c) {
+          float y[8];
+          load_chunk(tl + s_col, c, y);
+          z_chunk(c, y);
+          p_chunk(c, y, need);
         }
-        *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
-      // V' row i: the codes as f16 (zeros behind the window, where a code may be NaN)
-      const int lpos = (live ? page : pbeg + 8 * t) * 16 + (i & 15);   // position loaded in row i
-      const uint8_t* vrow = smem + Cfg::kOffV + s * Cfg::kTile + i * D;
-      uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
-        uint4 v = *reinterpret_cast<const uint4*>(vrow + ((c ^ sw) << 4));
-        if (lpos > last_valid) v = make_uint4(0, 0, 0, 0);
-        uint4 a, d;
-        f16x2_from_e4m3x4(v.x, a.x, a.y);
-        f16x2_from_e4m3x4(v.y, a.z, a.w);
-        f16x2_from_e4m3x4(v.z, d.x, d.y);
-        f16x2_from_e4m3x4(v.w, d.z, d.w);
-        uint8_t* dst = v16 + (c >> 2) * 16384;
-        const int cc = 2 * (c & 3);
-        *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
-        *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
-      }
-      mbar_arrive(vfree(s));
-      fence_proxy_async_smem();
       tc_fence_before();
+      mbar_arrive(sread(grp));
+      fence_proxy_async_smem();
       mbar_arrive(pready(grp));
-      if (!pv_ok) ok = false;   // the group leaves at the next vote
       mytiles = k + 1;
     }
     // The group's last PV completes its O^T.
@@ -705,15 +776,15 @@ __global__ void __launch_bounds__(384, 1)
 
     // Each group's (m, l, O^T) is a partial state of its own.  Row sums over its 128 positions:
 #pragma unroll
-    for (int n = 0; n < NQC; n += 2) {
-      float v[2];
-      unpair_f32(ls2[n / 2], v[0], v[1]);
+    for (int c0 = 0; c0 < NQC; c0 += 32) {
+      float v[32];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o2 = 16; o2 > 0; o2 >>= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o2);
-        if (lane == 0) colsum[(grp * 4 + q4) * NQC + n + e] = v[e];
+      for (int n = 0; n < 32; n += 2) {
+        v[n] = v[n + 1] = 0.f;
+        if (c0 + n < NQC) unpair_f32(ls2[(c0 + n) / 2], v[n], v[n + 1]);
       }
+      const float sum = reduce_columns(v, [](float a, float d) { return a + d; });
+      if (c0 + lane < NQC) colsum[(grp * 4 + q4) * NQC + c0 + lane] = sum;
     }
 #pragma unroll
     for (int n = 0; n < NQC; ++n) o[n] = 0.f;
@@ -769,7 +840,7 @@ __global__ void __launch_bounds__(384, 1)
   };
   if (on_chip) {
     merge_on_chip<D, NQC, Cfg::kThreads>(p, unit, split, softmax_warp ? grp : -1, dim, i, o, Mg,
-                                         Lg, smem, reinterpret_cast<float*>(smem + Cfg::kOffV16),
+                                         Lg, smem, reinterpret_cast<float*>(smem + Cfg::kMergeOff),
                                          flag, out_row);
   } else {
     SplitWorkspace ws{p.tickets, p.part_ml, p.part_o};
