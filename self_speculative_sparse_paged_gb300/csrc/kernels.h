@@ -20,8 +20,6 @@ struct VerifyParams {
   const void* q;            // bf16 [B][T][Hq][D]
   void* out;                // bf16 [B][T][Hq][D]
   float* scores;            // fp32 [B][Hkv][score_stride] or null
-  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes of the 8-bit cache, or null
-  const uint8_t* v_scale;
   const int32_t* ctx_lens;  // [B]
   const int32_t* block_table;
   int score_stride;
@@ -44,6 +42,27 @@ struct VerifyParams {
   float* part_o;
   int* err;
 };
+
+struct VerifyKv8Params {
+  const void* q;            // bf16 [B][T][Hq][D]
+  void* out;                // bf16 [B][T][Hq][D]
+  float* scores;            // fp32 [B][Hkv][score_stride] or null
+  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes
+  const uint8_t* v_scale;
+  const int32_t* ctx_lens;  // [B]
+  const int32_t* block_table;
+  int score_stride;
+  int num_pages, max_pages, batch;
+  int hq, hkv, group, gamma, nq;
+  uint32_t row_mask;        // capture rows: bit t set -> window row t is captured
+  float scale;              // softmax scale (logit units)
+  float scale_log2;         // scale * log2(e)
+  int* tickets;             // [B * Hkv]
+  float* part_ml;           // [CTAs][2][nq] (m, l)
+  float* part_o;            // [CTAs][2][nq][D]
+  int* err;
+};
+constexpr int kMaxKv8Ctas = 192;   // CTAs of the 8-bit verify kernel (one an SM)
 
 struct SparseParams {
   const void* q;            // bf16 [B][Hq][D]
@@ -254,17 +273,11 @@ inline bool verify_kv8_supported(int head_dim, int nq) {
   return nq >= 1 && nq <= (head_dim == 128 ? 40 : 64);
 }
 cudaError_t launch_verify_kv8_d64(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                  const VerifyParams& p, bool capture, int batch,
+                                  const VerifyKv8Params& p, bool capture, int grid,
                                   cudaStream_t stream);
 cudaError_t launch_verify_kv8_d128(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                   const VerifyParams& p, bool capture, int batch,
+                                   const VerifyKv8Params& p, bool capture, int grid,
                                    cudaStream_t stream);
-int verify_kv8_max_active_clusters_d64(int nq, bool capture, int cluster);
-int verify_kv8_max_active_clusters_d128(int nq, bool capture, int cluster);
-inline int verify_kv8_max_active_clusters(int head_dim, int nq, bool capture, int cluster) {
-  return head_dim == 64 ? verify_kv8_max_active_clusters_d64(nq, capture, cluster)
-                        : verify_kv8_max_active_clusters_d128(nq, capture, cluster);
-}
 template <int D, bool CAP>
 cudaError_t launch_verify_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const VerifyParams& p, int ntiles, int batch, cudaStream_t stream);

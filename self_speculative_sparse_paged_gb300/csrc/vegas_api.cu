@@ -201,15 +201,14 @@ struct VerifyPlan {
 // two columns holding the summed captured query (at the next even index).
 int verify_columns(int nq, bool capture) { return capture ? ((nq + 1) & ~1) + 2 : nq; }
 
-// kv8: the kernel of the 8-bit cache (its shapes are checked by the caller).
 VerifyPlan plan_verify(const vegas_paged_kv_t* kv, int batch, int gamma, int sms, bool capture,
-                       bool with_device, bool kv8 = false) {
+                       bool with_device) {
   VerifyPlan pl{};
   const int G = kv->num_q_heads / kv->num_kv_heads;
   pl.nq = (gamma + 1) * G;
   pl.ncols = verify_columns(pl.nq, capture);
   pl.ntiles = (pl.ncols + 7) / 8;
-  pl.tc = kv8 || vegas::verify_tc_supported(kv->head_dim, pl.nq, capture);
+  pl.tc = vegas::verify_tc_supported(kv->head_dim, pl.nq, capture);
   const int units = std::max(1, batch * kv->num_kv_heads);
   if (pl.tc && units < sms && with_device) {
     // C clusters of S CTAs per unit, every CTA resident (one wave), >= one tile
@@ -220,8 +219,7 @@ VerifyPlan plan_verify(const vegas_paged_kv_t* kv, int batch, int gamma, int sms
     int bestS = 0, bestC = 0, oneS = 0;
     for (int S = std::min(vegas::kMaxVerifyCluster, sms / units); S >= 2; --S) {
       const int resident =
-          kv8 ? vegas::verify_kv8_max_active_clusters(kv->head_dim, pl.nq, capture, S)
-              : vegas::verify_tc_max_active_clusters(kv->head_dim, pl.nq, capture, S);
+          vegas::verify_tc_max_active_clusters(kv->head_dim, pl.nq, capture, S);
       if (!oneS && S <= max_splits && resident >= units) oneS = S;
       // (the cross-cluster merge takes one lane per cluster: C <= 32)
       int C = std::min(std::min(sms / (units * S), max_splits / S), 32);
@@ -344,8 +342,7 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
                            int score_stride, const int32_t* ctx_lens, int batch, int gamma,
                            uint32_t row_mask, float softmax_scale, void* workspace,
                            size_t workspace_bytes, void* stream, float* raw = nullptr,
-                           int raw_stride = 0, vegas::ScratchFn scratch = nullptr,
-                           const vegas_paged_kv8_t* kv8 = nullptr);
+                           int raw_stride = 0, vegas::ScratchFn scratch = nullptr);
 }  // namespace
 
 namespace vegas {
@@ -443,8 +440,8 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
                            int score_stride, const int32_t* ctx_lens, int batch, int gamma,
                            uint32_t row_mask, float softmax_scale, void* workspace,
                            size_t workspace_bytes, void* stream, float* raw, int raw_stride,
-                           vegas::ScratchFn scratch, const vegas_paged_kv8_t* kv8) {
-  vegas_status_t st = kv8 ? check_kv8(kv8) : check_kv(kv);
+                           vegas::ScratchFn scratch) {
+  vegas_status_t st = check_kv(kv);
   if (st != VEGAS_OK) return st;
   if (batch < 0) return fail(VEGAS_ERR_INVALID_ARG, "batch %d", batch);
   if (gamma < 0 || gamma > 15) return fail(VEGAS_ERR_UNSUPPORTED, "gamma %d (0..15)", gamma);
@@ -452,15 +449,10 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
   if (!aligned16(q) || !aligned16(out))
     return fail(VEGAS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (!std::isfinite(softmax_scale)) return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale not finite");
-  if (kv8 && std::fabs(softmax_scale) > kMaxKv8SoftmaxScale)
-    return fail(VEGAS_ERR_UNSUPPORTED, "softmax_scale %g beyond 2^20", (double)softmax_scale);
   const int G = kv->num_q_heads / kv->num_kv_heads;
   const int nq = (gamma + 1) * G;
   const int ncols = verify_columns(nq, scores != nullptr);
-  if (kv8 && !vegas::verify_kv8_supported(kv->head_dim, nq))
-    return fail(VEGAS_ERR_UNSUPPORTED, "(gamma+1)*G = %d query rows: too many for head_dim %d", nq,
-                kv->head_dim);
-  if (!kv8 && (ncols + 7) / 8 > vegas::verify_max_ntiles(kv->head_dim))
+  if ((ncols + 7) / 8 > vegas::verify_max_ntiles(kv->head_dim))
     return fail(VEGAS_ERR_UNSUPPORTED,
                 "(gamma+1)*G = %d query rows (+2 capture columns) exceeds %d for head_dim %d", nq,
                 8 * vegas::verify_max_ntiles(kv->head_dim), kv->head_dim);
@@ -470,7 +462,7 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
   int* err = nullptr;
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
-  const VerifyPlan pl = plan_verify(kv, batch, gamma, sms, scores != nullptr, true, kv8 != nullptr);
+  const VerifyPlan pl = plan_verify(kv, batch, gamma, sms, scores != nullptr, true);
   const bool needs_ws = pl.needs_ws;
   if (scratch) {
     // A library-owned scratch serves exactly the shapes whose reported
@@ -490,16 +482,12 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
       return fail(VEGAS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
   CUtensorMap km, vm;
-  if ((st = make_cache_map(&km, kv->k_cache, kv, kv8 != nullptr)) != VEGAS_OK) return st;
-  if ((st = make_cache_map(&vm, kv->v_cache, kv, kv8 != nullptr)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&km, kv->k_cache, kv)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&vm, kv->v_cache, kv)) != VEGAS_OK) return st;
   vegas::VerifyParams p{};
   p.q = q;
   p.out = out;
   p.scores = scores;
-  if (kv8) {
-    p.k_scale = kv8->k_scale;
-    p.v_scale = kv8->v_scale;
-  }
   p.ctx_lens = ctx_lens;
   p.block_table = kv->block_table;
   p.score_stride = score_stride;
@@ -533,12 +521,7 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
     if (e != cudaSuccess) return cuda_fail(e, "clear scratch counters");
   }
   cudaError_t e =
-      kv8 ? (kv->head_dim == 64 ? vegas::launch_verify_kv8_d64(km, vm, p, scores != nullptr, batch,
-                                                               static_cast<cudaStream_t>(stream))
-                                : vegas::launch_verify_kv8_d128(km, vm, p, scores != nullptr, batch,
-                                                                static_cast<cudaStream_t>(stream)))
-      : pl.tc
-          ? vegas::launch_verify_tc(km, vm, p, kv->head_dim, scores != nullptr, batch,
+      pl.tc ? vegas::launch_verify_tc(km, vm, p, kv->head_dim, scores != nullptr, batch,
                                       static_cast<cudaStream_t>(stream))
             : launch_verify_any(km, vm, p, kv->head_dim, pl.ntiles, scores != nullptr, batch,
                                 static_cast<cudaStream_t>(stream));
@@ -547,35 +530,111 @@ vegas_status_t verify_impl(const vegas_paged_kv_t* kv, const void* q, void* out,
 }
 }  // namespace
 
+// =========================================================================
+// Verify attention over the 8-bit cache
+// =========================================================================
+namespace {
+struct VerifyKv8Plan {
+  int nq, grid;
+  size_t ml_off, o_off, bytes;
+};
+
+// One CTA an SM, each with up to two pieces of shared units in the workspace; fewer where the
+// tables hold fewer tiles.  Tickets come first, for every unit, and the pieces' room does not
+// depend on the call's tables.
+VerifyKv8Plan plan_verify_kv8(const vegas_paged_kv8_t* kv, int batch, int gamma, int sms) {
+  VerifyKv8Plan pl{};
+  pl.nq = (gamma + 1) * (kv->num_q_heads / kv->num_kv_heads);
+  const int most = std::min(sms, vegas::kMaxKv8Ctas);
+  const long long tiles =
+      (long long)batch * kv->num_kv_heads * ((kv->max_pages_per_seq + 7) / 8);
+  pl.grid = (int)std::max(1ll, std::min((long long)most, tiles));
+  pl.ml_off = align256(size_t(batch) * kv->num_kv_heads * sizeof(int));
+  pl.o_off = pl.ml_off + align256(size_t(most) * 2 * pl.nq * 2 * sizeof(float));
+  pl.bytes = pl.o_off + size_t(most) * 2 * pl.nq * kv->head_dim * sizeof(float);
+  return pl;
+}
+}  // namespace
+
 VEGAS_API size_t vegas_verify_kv8_workspace_size(const vegas_paged_kv8_t* kv, int batch,
                                                  int gamma) {
   if (check_kv8(kv) != VEGAS_OK || batch < 0 || gamma < 0 || gamma > 15) return 0;
-  const vegas_paged_kv_t shape = shape_of(kv);
   if (!vegas::verify_kv8_supported(kv->head_dim,
                                    (gamma + 1) * (kv->num_q_heads / kv->num_kv_heads)))
     return 0;
   int sms = 0;
-  const bool dev = device_info(nullptr, &sms) == VEGAS_OK && sms > 0;
-  if (!dev) sms = 148;
-  return std::max(plan_verify(&shape, batch, gamma, sms, true, dev, true).bytes,
-                  plan_verify(&shape, batch, gamma, sms, false, dev, true).bytes);
+  if (device_info(nullptr, &sms) != VEGAS_OK || sms < 1) sms = 148;
+  return plan_verify_kv8(kv, batch, gamma, sms).bytes;
 }
 
 VEGAS_API vegas_status_t vegas_verify_attn_kv8(
     const vegas_paged_kv8_t* kv, const void* q, void* out, float* scores, int score_stride,
     const int32_t* ctx_lens, int batch, int gamma, uint32_t capture_row_mask, float softmax_scale,
     void* workspace, size_t workspace_bytes, void* stream) {
-  if (!kv) return fail(VEGAS_ERR_INVALID_ARG, "kv is NULL");
+  vegas_status_t st = check_kv8(kv);
+  if (st != VEGAS_OK) return st;
+  if (batch < 0) return fail(VEGAS_ERR_INVALID_ARG, "batch %d", batch);
+  if (batch > (1 << 16)) return fail(VEGAS_ERR_UNSUPPORTED, "batch %d (at most 2^16)", batch);
+  if (gamma < 0 || gamma > 15) return fail(VEGAS_ERR_UNSUPPORTED, "gamma %d (0..15)", gamma);
+  if (!q || !out || !ctx_lens) return fail(VEGAS_ERR_INVALID_ARG, "NULL q, out or ctx_lens");
+  if (!aligned16(q) || !aligned16(out))
+    return fail(VEGAS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (!std::isfinite(softmax_scale)) return fail(VEGAS_ERR_INVALID_ARG, "softmax_scale not finite");
+  if (std::fabs(softmax_scale) > kMaxKv8SoftmaxScale)
+    return fail(VEGAS_ERR_UNSUPPORTED, "softmax_scale %g beyond 2^20", (double)softmax_scale);
+  const int G = kv->num_q_heads / kv->num_kv_heads;
+  if (!vegas::verify_kv8_supported(kv->head_dim, (gamma + 1) * G))
+    return fail(VEGAS_ERR_UNSUPPORTED, "(gamma+1)*G = %d query rows: too many for head_dim %d",
+                (gamma + 1) * G, kv->head_dim);
   if (scores) {
-    if (gamma < 0 || gamma > 15) return fail(VEGAS_ERR_UNSUPPORTED, "gamma %d (0..15)", gamma);
     if (capture_row_mask == 0 || (capture_row_mask >> (gamma + 1)) != 0)
       return fail(VEGAS_ERR_INVALID_ARG, "capture row mask 0x%x: needs rows in [0, %d]",
                   capture_row_mask, gamma);
+    if (score_stride < 1) return fail(VEGAS_ERR_INVALID_ARG, "score_stride %d", score_stride);
   }
+  if (batch == 0) return VEGAS_OK;
+  int* err = nullptr;
+  int sms = 0;
+  if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
+  const VerifyKv8Plan pl = plan_verify_kv8(kv, batch, gamma, sms);
+  if (!workspace || workspace_bytes < pl.bytes)
+    return fail(VEGAS_ERR_WORKSPACE_TOO_SMALL, "verify workspace %zu < %zu bytes", workspace_bytes,
+                pl.bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(VEGAS_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const vegas_paged_kv_t shape = shape_of(kv);
-  return verify_impl(&shape, q, out, scores, score_stride, ctx_lens, batch, gamma,
-                     capture_row_mask, softmax_scale, workspace, workspace_bytes, stream, nullptr,
-                     0, nullptr, kv);
+  CUtensorMap km, vm;
+  if ((st = make_cache_map(&km, kv->k_cache, &shape, true)) != VEGAS_OK) return st;
+  if ((st = make_cache_map(&vm, kv->v_cache, &shape, true)) != VEGAS_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  vegas::VerifyKv8Params p{};
+  p.q = q;
+  p.out = out;
+  p.scores = scores;
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  p.ctx_lens = ctx_lens;
+  p.block_table = kv->block_table;
+  p.score_stride = score_stride;
+  p.num_pages = kv->num_pages;
+  p.max_pages = kv->max_pages_per_seq;
+  p.batch = batch;
+  p.hq = kv->num_q_heads;
+  p.hkv = kv->num_kv_heads;
+  p.group = G;
+  p.gamma = gamma;
+  p.nq = pl.nq;
+  p.row_mask = capture_row_mask;
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.tickets = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pl.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + pl.o_off);
+  p.err = err;
+  const auto launch = kv->head_dim == 64 ? vegas::launch_verify_kv8_d64 : vegas::launch_verify_kv8_d128;
+  cudaError_t e = launch(km, vm, p, scores != nullptr, pl.grid, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit verify launch");
+  return VEGAS_OK;
 }
 
 // =========================================================================

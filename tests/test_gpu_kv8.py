@@ -374,6 +374,19 @@ def test_verify(hq, hkv, d, gamma, mask, ctx):
     check_verify(c, q, out, scores, ctx, gamma, mask, scale)
 
 
+def test_verify_many_sequences():
+    """More sequences than the lengths' first pass takes at once, most of them short."""
+    rng = np.random.default_rng(21)
+    ctx = [int(x) for x in rng.integers(0, 40, 900)]
+    ctx[500], ctx[899] = 1000, 300
+    c = Cache(rng, [(n + 2 + 15) // 16 for n in ctx], 2, 1, 64)
+    spoil_unused(c, ctx, 2)
+    c.upload()
+    q = queries(rng, (900, 2, 2, 64))
+    out, scores = run_verify(c, q, ctx, 1, 0b11, 0.125)
+    check_verify(c, q, out, scores, ctx, 1, 0b11, 0.125)
+
+
 def test_verify_long_table_short_sequence():
     """A table with far more pages than the sequences have: most splits are empty."""
     rng = np.random.default_rng(4)
