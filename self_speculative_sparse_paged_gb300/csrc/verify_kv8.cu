@@ -4,12 +4,13 @@
 // The work is that of verify_tc.cu on half the bytes, laid out so that its length goes by what the
 // sequences hold, not by what their tables could: the 128-position tiles of all (sequence, KV
 // head) units stand in one row, and each CTA (one an SM) takes an equal run of it, whole units or
-// pieces, with the K/V stream going on from one unit to the next.  Twelve warps:
-//   warps 0-7   two softmax groups of four warps that alternate tiles; a thread owns a position
-//               of a tile, and a head dimension of the group's O^T.  They also build the query operand
-//               of a unit and finish it.
-//   warps 8, 9  TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
-//   warp 10     issues the MMAs
+// pieces, with the K/V stream going on from one unit to the next.  Sixteen warps:
+//   warps 0-7    two softmax groups of four warps that alternate tiles; a thread owns a position
+//                of a tile, and a head dimension of the group's O^T.  They also build the query operand
+//                of a unit and finish it.
+//   warps 8-11   turn V's codes into f16, a thread a position
+//   warps 12, 13 TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
+//   warp 14      issues the MMAs
 //
 //   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
 //       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
@@ -20,9 +21,8 @@
 //   z = S 2^(e_k - k) scale log2(e) + e_v,  P = 2^(z - r) with r a reference for the column:
 //       e_k costs nothing (a thread's one factor), and 2^e_v goes into P instead of V.  Row sums
 //       take P 2^-e_v in fp32.
-//   O^T[D x N] += V'^T P^T   kind::f16, M = D: V' are V's codes as f16, exact; each thread of a
-//       softmax group turns its own position's row (16 codes: one load, 8 conversions, two stores)
-//       while the tensor cores still work on S of the tile.
+//   O^T[D x N] += V'^T P^T   kind::f16, M = D: V' are V's codes as f16, exact (16 codes: one load,
+//       8 conversions, two stores).
 //
 // The two parts of the queries lie side by side in N (one pass over K; an MMA takes 45 clocks up
 // to N = 64 and 64 at 128) up to 40 columns, else they share an accumulator.
@@ -46,7 +46,9 @@ namespace vegas {
 namespace {
 constexpr float kTop = 15.f, kRaise = 7.f;   // log2 of the largest P, and of P at a raised reference
 constexpr int kCapParts = 6;
-constexpr int kLeastTiles = 2;   // of a CTA that takes part
+// In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
+// reference and end), and a CTA takes part for kLeastRun tiles or more.
+constexpr int kUnitTiles = 3, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
 // Instruction descriptors, fp32 accumulator: e4m3 by e4m3, K-major (K = 32); f16 by f16,
@@ -65,21 +67,25 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// Lane l gets op over the warp's lanes of their v[l]: in five steps a lane exchanges half of the
-// columns it still holds for the other half of another lane's (31 shuffles for 32 columns).
+// op over the warp's lanes of each of eight columns: lane l gets column l / 4's.  In three steps a
+// lane exchanges half of the columns it still holds for the other half of another lane's.
 template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[32], Op op) {
+__device__ __forceinline__ float reduce_chunk(const float* x, Op op) {
   const int lane = threadIdx.x & 31;
+  float v[8];
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
+  for (int j = 0; j < 8; ++j) v[j] = x[j];
+#pragma unroll
+  for (int w = 16; w >= 4; w >>= 1) {
     const bool upper = lane & w;
 #pragma unroll
-    for (int j = 0; j < w; ++j) {
-      const float give = upper ? v[j] : v[j + w], keep = upper ? v[j + w] : v[j];
+    for (int j = 0; j < w / 4; ++j) {
+      const float give = upper ? v[j] : v[j + w / 4], keep = upper ? v[j + w / 4] : v[j];
       v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
     }
   }
-  return v[0];
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 }  // namespace
 
@@ -110,27 +116,30 @@ struct Kv8Cfg {
   static constexpr int kOffP = kOffV16 + 2 * kV16;
   static constexpr int kOffQ = kOffP + 2 * kP;
   static constexpr int kOffBar = kOffQ + kPasses * kQ;
-  static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 2;
+  static constexpr int kNumBars = 2 * KS + 2 * VS + 5 * 2 + 2;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  // misc: 16 words; votes[2][2][4]; warp sums[12] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
-  // colfac[NQC], nref[2][NQC], fac[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
-  static constexpr size_t kMisc = 64 + 64 + 96 + 4 * size_t(16 + 3 + 2 + 2 + 2) * NQC;
+  // misc: 16 words; votes[2][2][4]; warp sums[16] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
+  // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
+  static constexpr size_t kMisc = 64 + 64 + 128 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // a piece's merge weights (one a row and piece) in the V' and P buffers
-  static_assert(NQC * 4 * kMaxKv8Ctas <= 2 * kV16 + 2 * kP, "merge weights");
-  static_assert(NQC / 2 * D * 4 <= kV16, "exchange of half the columns");
+  static_assert(NQC * D * 4 <= 2 * kP, "a group's O^T handed over in P's buffers");
   static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
 };
 
 // A place in the row of tiles: tile t of KV head g of sequence b.
 struct Place {
-  long long left;          // tiles of this CTA from here on
+  long long left;          // of the CTA's run from here on
   int b, g, t, tiles, L;   // tiles: of each unit of sequence b; L: its context length
+  int pre;                 // of the run, before tile t
+  // tiles of the unit in the run; 0: the run is over
+  __device__ int here() const {
+    return left > pre ? int(min((long long)(tiles - t), left - pre)) : 0;
+  }
 };
 
 template <int D, int NQC, bool CAPTURE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const VerifyKv8Params p) {
   using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
@@ -144,8 +153,8 @@ __global__ void __launch_bounds__(384, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + Cfg::kOffBar;
-  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P and V'
-  // ready, PV done (per softmax group); queries ready, MMA drain
+  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P ready, PV done,
+  // V' ready (per softmax group); queries ready, MMA drain
   auto kfull = [&](int s) { return bar0 + 8 * s; };
   auto kfree = [&](int s) { return bar0 + 8 * (KS + s); };
   auto vfull = [&](int s) { return bar0 + 8 * (2 * KS + s); };
@@ -155,20 +164,22 @@ __global__ void __launch_bounds__(384, 1)
   auto sread = [&](int g2) { return bar0 + 8 * (B1 + 2 + g2); };
   auto pready = [&](int g2) { return bar0 + 8 * (B1 + 4 + g2); };
   auto pvdone = [&](int g2) { return bar0 + 8 * (B1 + 6 + g2); };
-  const uint32_t qready = bar0 + 8 * (B1 + 8), drain = bar0 + 8 * (B1 + 9);
+  auto vready = [&](int g2) { return bar0 + 8 * (B1 + 8 + g2); };
+  const uint32_t qready = bar0 + 8 * (B1 + 10), drain = bar0 + 8 * (B1 + 11);
   uint8_t* misc = smem + Cfg::kOffMisc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   int* flag = reinterpret_cast<int*>(misc + 4);
   int* capexp = reinterpret_cast<int*>(misc + 8);
   int* uniform = reinterpret_cast<int*>(misc + 12);
   int* votes = reinterpret_cast<int*>(misc + 64);                // [2][2][4]
-  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [12] tiles a head of a warp's sequences
-  float* colmax = reinterpret_cast<float*>(misc + 224);          // [2][4][NQC]
+  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [16] a warp's sequences
+  float* colmax = reinterpret_cast<float*>(misc + 256);          // [2][4][NQC]
   float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
   float* colfac = colsum + 8 * NQC;                              // [NQC] 2^-k of rows of unlike size
   float* nrefs = colfac + NQC;                                   // [2][NQC] -reference
-  float* fac = nrefs + 2 * NQC;                                  // [2][NQC] weights of the groups
-  float* colM = fac + 2 * NQC;                                   // [NQC] maximum, and sum, of a piece
+  float* facs = nrefs + 2 * NQC;                                 // [2][NQC] factors of a raise
+  float* wgt = facs + 2 * NQC;                                   // [2][NQC] weights of the groups
+  float* colM = wgt + 2 * NQC;                                   // [NQC] maximum, and sum, of a piece
   float* colL = colM + NQC;
   int* tlim = reinterpret_cast<int*>(colL + NQC);                // [NQC]
   int* rowexp = tlim + NQC;                                      // [NQC]
@@ -192,47 +203,70 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(sread(i), 128);
       mbar_init(pready(i), 128);
       mbar_init(pvdone(i), 1);
+      mbar_init(vready(i), 128);
     }
     mbar_init(qready, 256);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 10) {
+  if (warp == 14) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();   // (the barriers are initialised, and tensor memory is there)
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   // Nothing above reads or writes global memory, so it overlaps the tail of
   // the previous kernel of the stream.
   griddep_wait();
 
-  // ---- this CTA's run of tiles.  A sequence's units have ceil((L + T) / 128) tiles each.
+  // ---- this CTA's run.  A sequence's units have ceil((L + T) / 128) tiles each.
   auto length = [&](int b) {
     const int L = p.ctx_lens[b];
     return L < 0 || L + T > cap ? max(0, min(L, cap - T)) : L;   // (recorded below)
   };
   auto tiles_of = [&](int L) { return (L + T + 127) >> 7; };
-  // warp w counts sequences [w * chunk, (w + 1) * chunk)
-  const int chunk = (p.batch + 383) / 384 * 32;
-  {
+  auto span_of = [&](int L) { return (long long)(tiles_of(L) + kUnitTiles) * p.hkv; };
+  // Up to 32 sequences every warp scans by itself; else warp w first counts [w * chunk, (w + 1) *
+  // chunk).
+  const int chunk = (p.batch + 511) / 512 * 32;
+  long long all = 0;
+  int first_chunk = 0;
+  if (p.batch > 32) {
     long long sum = 0;
-    for (int b = warp * chunk + lane; b < min(p.batch, (warp + 1) * chunk); b += 32) {
-      const int L = p.ctx_lens[b];
-      if (cta == 0 && (L < 0 || L + T > cap)) set_error(p.err, kErrDeviceFault);
-      sum += tiles_of(length(b));
-    }
+    for (int b = warp * chunk + lane; b < min(p.batch, (warp + 1) * chunk); b += 32)
+      sum += span_of(length(b));
 #pragma unroll
     for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
     if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < 16; ++w) all += wsum[w];
   }
-  tc_fence_before();
-  __syncthreads();   // (and the barriers are initialised before anyone waits on them)
-  tc_fence_after();
-  long long all = 0;
+  long long upto = 0;    // this lane's sequence and those before it, of 32
+  int mylen = 0;
+  auto scan = [&](int b0) {
+    const int b = b0 + lane;
+    mylen = b < p.batch ? length(b) : 0;
+    upto = b < p.batch ? span_of(mylen) : 0;
 #pragma unroll
-  for (int w = 0; w < 12; ++w) all += wsum[w];
-  all *= p.hkv;
-  // CTAs that take part: at least kLeastTiles each
-  const int n = int(max(1ll, min((long long)gridDim.x, all / kLeastTiles)));
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o2);
+      if (lane >= o2) upto += v;
+    }
+  };
+  if (p.batch <= 32) {
+    scan(0);
+    all = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (cta == 0)   // lengths out of range are recorded once
+    for (int b = tid; b < p.batch; b += 512) {
+      const int L = p.ctx_lens[b];
+      if (L < 0 || L + T > cap) set_error(p.err, kErrDeviceFault);
+    }
+  // CTAs that take part
+  const int n = int(max(1ll, min((long long)gridDim.x, all / kLeastRun)));
   // (64-bit quotients take a few hundred clocks: 32-bit ones while they do)
   const bool small = all < (1 << 24);   // (n < 2^8)
   auto quotient = [&](long long a, long long d) {
@@ -240,39 +274,40 @@ __global__ void __launch_bounds__(384, 1)
   };
   auto run_begin = [&](int c) { return quotient(c * all, n); };
   const long long begin = cta < n ? run_begin(cta) : 0, end = cta < n ? run_begin(cta + 1) : 0;
-  // the CTA that holds tile x: the last c with run_begin(c) <= x
+  // the CTA that holds place x: the last c with run_begin(c) <= x
   auto cta_of = [&](long long x) { return int(quotient((x + 1) * n - 1, all)); };
-  Place start{end - begin, 0, 0, 0, 1, 0};
-  long long base = 0;   // first tile of sequence start.b
+  Place start{end - begin, 0, 0, 0, 1, 0, 0};
+  long long base = 0;   // where sequence start.b begins
   if (begin < end) {
-    int w = 0;
-    while (w < 11 && base + wsum[w] * p.hkv <= begin) base += wsum[w++] * p.hkv;
-    for (int b0 = w * chunk;; b0 += 32) {
-      const int b = b0 + lane;
-      const int L = b < p.batch ? length(b) : 0;
-      const long long mine = b < p.batch ? (long long)tiles_of(L) * p.hkv : 0;
-      long long upto = mine;
-#pragma unroll
-      for (int o2 = 1; o2 < 32; o2 <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o2);
-        if (lane >= o2) upto += v;
-      }
+    int b0 = 0;
+    if (p.batch > 32) {
+      for (; first_chunk < 15 && base + wsum[first_chunk] <= begin; ++first_chunk)
+        base += wsum[first_chunk];
+      b0 = first_chunk * chunk;
+    }
+    for (;; b0 += 32) {
+      if (p.batch > 32) scan(b0);
       const unsigned beyond = __ballot_sync(0xffffffffu, base + upto > begin);
       if (beyond || b0 + 32 >= p.batch) {
         const int l = beyond ? __ffs(beyond) - 1 : 31;   // (there is one: begin < end <= all)
         start.b = min(b0 + l, p.batch - 1);
-        start.L = __shfl_sync(0xffffffffu, L, l);
-        base += __shfl_sync(0xffffffffu, upto - mine, l);
+        start.L = __shfl_sync(0xffffffffu, mylen, l);
+        base += __shfl_sync(0xffffffffu, upto, l) - span_of(start.L);
         break;
       }
       base += __shfl_sync(0xffffffffu, upto, 31);
     }
     start.tiles = tiles_of(start.L);
-    start.g = int(quotient(begin - base, start.tiles));
-    start.t = int((begin - base) - (long long)start.g * start.tiles);
+    const int span = start.tiles + kUnitTiles;
+    start.g = int(quotient(begin - base, span));
+    const int off = int((begin - base) - (long long)start.g * span);   // in the unit's span
+    start.t = max(0, off - kUnitTiles);
+    start.pre = max(0, kUnitTiles - off);
   }
-  auto next_unit = [&](Place& q) {   // (left counted down by the caller)
+  auto next_unit = [&](Place& q, int done) {   // (done: tiles of the unit that were here)
+    q.left -= q.pre + done;
     q.t = 0;
+    q.pre = kUnitTiles;
     if (++q.g == p.hkv) {
       q.g = 0;
       if (q.left > 0) {
@@ -281,17 +316,16 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   };
-  const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
-  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
-  if (warp >= 8) {
-    leave_registers<72>();
-    if (warp < 10) {
-      // ---------------------------------------------------------- producers: K (8), V (9)
+  // 512 threads launch with 128 registers each: 2 x 128 x 192 + 2 x 128 x 64 are that.
+  if (warp >= 12) {
+    leave_registers<64>();
+    if (warp < 14) {
+      // ---------------------------------------------------------- producers: K (12), V (13)
       // Lane j < 8 loads page j of a tile; a page past the sequence's last is that one again (its
       // positions are masked).
-      const bool is_k = warp == 8;
+      const bool is_k = warp == 12;
       const int depth = is_k ? KS : VS;
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       const uint32_t ring = sbase + (is_k ? 0 : Cfg::kOffV);
@@ -299,26 +333,35 @@ __global__ void __launch_bounds__(384, 1)
       const uint64_t stream_pol = l2_evict_first_policy();
       const int j8 = lane & 7;
       Place ahead = start;
-      // a tile's table entry, requested four tiles before its use, and its KV head
+      int rest = ahead.here(), done = rest;   // tiles of the unit still to be requested, and of them all
+      // a tile's table entry, requested four tiles before its use, and its KV head (-1: no tile)
       int held[4], head[4];
       auto request = [&](int j) {
-        held[j] = head[j] = 0;
-        if (ahead.left > 0) {
+        held[j] = 0;
+        head[j] = -1;
+        if (rest > 0) {
           const int page = min(8 * ahead.t + j8, (ahead.L + T - 1) >> 4);
           held[j] = __ldg(&p.block_table[size_t(ahead.b) * p.max_pages + page]);
           head[j] = ahead.g;
-          --ahead.left;
-          if (++ahead.t == ahead.tiles) next_unit(ahead);
+          ++ahead.t;
+          if (--rest == 0) {
+            next_unit(ahead, done);
+            rest = done = ahead.here();
+          }
         }
       };
 #pragma unroll
       for (int j = 0; j < 4; ++j) request(j);
-      long long issued = 0;
+      int issued = 0;
       int s = 0, round = 0;
-      for (long long it0 = 0; it0 < start.left && ok; it0 += 4) {
+      bool more = true;
+      while (more && ok) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (it0 + j >= start.left) break;
+          if (head[j] < 0) {
+            more = false;
+            break;
+          }
           const uint32_t full = is_k ? kfull(s) : vfull(s);
           const uint32_t freed = is_k ? kfree(s) : vfree(s);
           if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(freed, (round - 1) & 1))) {
@@ -338,20 +381,24 @@ __global__ void __launch_bounds__(384, 1)
             tma_load_2d_hint(ring + s * Cfg::kTile + j8 * 16 * D, map, 0, (phys * p.hkv + g) * 16,
                              full, stream_pol);
           __syncwarp();
-          issued = it0 + j + 1;
+          if (issued < depth) ++issued;
           if (++s == depth) {
             s = 0;
             ++round;
           }
         }
       }
-      if (!ok) {
+      if (!ok) {   // what is in flight lands before the CTA ends
         if (lane == 0) set_error(p.err, kErrDeviceTimeout);
-        for (long long t = issued > depth ? issued - depth : 0; t < issued; ++t)
-          (void)mbar_wait_bounded(is_k ? kfull(int(t % depth)) : vfull(int(t % depth)),
-                                  int(t / depth) & 1);
+        for (int k = 0; k < issued; ++k) {
+          if (--s < 0) {
+            s = depth - 1;
+            --round;
+          }
+          (void)mbar_wait_bounded(is_k ? kfull(s) : vfull(s), round & 1);
+        }
       }
-    } else if (warp == 10) {
+    } else if (warp == 14) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t idS = idesc_e4m3(128, NS);
       constexpr uint32_t idPV = idesc_f16_mn(D, NP);
@@ -369,6 +416,7 @@ __global__ void __launch_bounds__(384, 1)
       // PV of the CTA's tile it (first: its group's first tile of the unit)
       auto issue_pv = [&](uint32_t it, bool first) -> bool {
         const int gg = it & 1;
+        if (!wait_all(vready(gg), (it >> 1) & 1)) return false;
         if (!wait_all(pready(gg), (it >> 1) & 1)) return false;
         tc_fence_after();
         const uint32_t vb = (sbase + Cfg::kOffV16 + gg * Cfg::kV16) >> 4;
@@ -386,8 +434,7 @@ __global__ void __launch_bounds__(384, 1)
       Place at = start;
       uint32_t it = 0;
       int s = 0, round = 0, seg = 0;
-      while (at.left > 0 && ok) {
-        const int tiles = int(min((long long)(at.tiles - at.t), at.left));
+      for (int tiles = at.here(); tiles > 0 && ok; tiles = at.here()) {
         if (!wait_all(qready, seg++ & 1)) {
           ok = false;
           break;
@@ -417,8 +464,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         // the unit's last PV, before the next unit's queries are waited for
         if (ok && !issue_pv(it - 1, tiles - 1 < 2)) ok = false;
-        at.left -= tiles;
-        if (at.left > 0) next_unit(at);
+        next_unit(at, tiles);
       }
       if (!ok && leader) set_error(p.err, kErrDeviceTimeout);
       // every MMA issued has completed before tensor memory is released
@@ -426,8 +472,62 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       (void)mbar_wait_bounded(drain, 0);
     }
+  } else if (warp >= 8) {
+    leave_registers<64>();
+    // ------------------------------------------------------------ V' (warps 8-11)
+    // Row i of a tile: its codes as f16, or zeros behind the window, where a code may be NaN.
+    const int i = tid & 127;
+    Place at = start;
+    uint32_t it = 0;
+    int s = 0, round = 0;
+    for (int tiles = at.here(); tiles > 0 && ok; tiles = at.here()) {
+      for (int t = 0; t < tiles; ++t, ++it) {
+        const int grp = it & 1;
+        // (a wait that ran out is seen by every thread of the four warps for itself)
+        if (!mbar_wait_bounded(vfull(s), round & 1) ||
+            (it >= 2 && !mbar_wait_bounded(pvdone(grp), ((it >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* vrow = smem + Cfg::kOffV + s * Cfg::kTile + i * D;
+        uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
+        const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
+        constexpr int B = 4;   // chunks in flight (loads ahead of the stores, which they might alias)
+        const bool behind = 128 * (at.t + t) + i > at.L + p.gamma;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 16; c0 += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int c = 0; c < B; ++c) {
+            v[c] = *reinterpret_cast<const uint4*>(vrow + (((c0 + c) ^ sw) << 4));
+            if (behind) v[c] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int c = 0; c < B; ++c) {
+            uint4 a, d;
+            f16x2_from_e4m3x4(v[c].x, a.x, a.y);
+            f16x2_from_e4m3x4(v[c].y, a.z, a.w);
+            f16x2_from_e4m3x4(v[c].z, d.x, d.y);
+            f16x2_from_e4m3x4(v[c].w, d.z, d.w);
+            uint8_t* dst = v16 + ((c0 + c) >> 2) * 16384;
+            const int cc = 2 * ((c0 + c) & 3);
+            *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
+          }
+        }
+        mbar_arrive(vfree(s));
+        fence_proxy_async_smem();
+        mbar_arrive(vready(grp));
+        if (++s == VS) {
+          s = 0;
+          ++round;
+        }
+      }
+      next_unit(at, tiles);
+    }
+    if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
   } else {
-    take_registers<216>();
+    take_registers<192>();
     // ------------------------------------------------------------ softmax groups (warps 0-7)
     const int grp = warp >> 2;                // 0: even tiles, 1: odd tiles
     const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
@@ -436,8 +536,8 @@ __global__ void __launch_bounds__(384, 1)
     const int dim = D == 128 ? i : lane < 16 ? 16 * q4 + lane : -1;
     const uint32_t tl = tmem + (uint32_t(32 * q4) << 16);
     const uint32_t s_col = Cfg::kSCol * grp, o_col = 2 * Cfg::kSCol + Cfg::kOCol * grp;
-    // Column references r (P = 2^(z - r)) are kept as -r, in registers up to 32 columns, else in
-    // shared memory; 0 while `empty` says that the column has seen no unmasked logit.
+    // Column references r (P = 2^(z - r)) are kept as -r in shared memory, up to 32 columns in
+    // registers too; 0 while `hollow` says that the column has seen no unmasked logit.
     constexpr bool kSmemRef = NQC > 32;
     constexpr int QPER = NQC / 8;
     uint8_t* qs = smem + Cfg::kOffQ;
@@ -495,14 +595,10 @@ __global__ void __launch_bounds__(384, 1)
     };
 
     Place at = start;
-    long long unit0 = base + (long long)start.g * start.tiles;   // first tile of the unit
+    long long unit0 = base + (long long)start.g * (start.tiles + kUnitTiles);   // its span's begin
     uint32_t it0 = 0;             // the CTA's tile with which the unit begins
-    uint32_t vs0 = 0;             // (it0 modulo the V ring, and the ring's round)
-    uint32_t vround0 = 0;
-    while (at.left > 0) {
-      const int tiles = int(min((long long)(at.tiles - at.t), at.left));
+    for (int tiles = at.here(); tiles > 0; tiles = at.here()) {
       const int L = at.L, g = at.g, b = at.b;
-      const int last_valid = L + p.gamma;
       const uint32_t first = it0 + ((it0 ^ uint32_t(grp)) & 1);   // this group's first tile
 
       // ---------------------------------------------------------- the unit's queries
@@ -631,7 +727,7 @@ __global__ void __launch_bounds__(384, 1)
               reinterpret_cast<uint32_t*>(qs + pass * Cfg::kQ + row * D)[j] = 0;
           if (lane == 0) *uniform = one ? most - 7 : kMixed;
         }
-        if (kSmemRef && i < NQC) nrg[i] = 0.f;
+        if (i < NQC) nrg[i] = 0.f;
         // Generic-proxy writes of Q must be visible to the tensor cores (async proxy).
         fence_proxy_async_smem();
         mbar_arrive(qready);
@@ -646,7 +742,7 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (!kSmemRef) nr[n2] = 0.f;
         if (n2 % 2 == 0) ls2[n2 / 2] = 0;
       }
-      uint64_t empty = NQC == 64 ? ~0ull : (1ull << NQC) - 1;
+      uint64_t hollow = NQC == 64 ? ~0ull : (1ull << NQC) - 1;   // columns without a reference
       const int uni = *uniform;
       const bool mixed = uni == kMixed;
       const float scale0 = mixed ? p.scale_log2 : p.scale_log2 * two_to(uni);
@@ -656,11 +752,6 @@ __global__ void __launch_bounds__(384, 1)
       if (CAPTURE && L > p.score_stride) {
         if (i == 0 && grp == 0) set_error(p.err, kErrDeviceFault);
         Lcap = p.score_stride;
-      }
-      uint32_t vs = vs0 + (first - it0), vround = vround0;
-      if (vs >= VS) {
-        vs -= VS;
-        ++vround;
       }
       bool any = false;   // this group has a tile of the unit
       // A failed (timed-out) wait is carried to the group vote below, so the 128
@@ -674,45 +765,11 @@ __global__ void __launch_bounds__(384, 1)
         ekb = load_scale(p.k_scale, phys1, g);
         evb = load_scale(p.v_scale, phys1, g);
         phys1 = load_page(at, t + 4);
-        // V' row i: the codes as f16 (zeros behind the window, where a code may be NaN), once PV of
-        // the group's last tile has read the buffer; S of this tile follows that PV in the tensor
-        // pipe, so this work hides behind it
-        bool okt = ok && (it < 2 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
-        okt = okt && mbar_wait_bounded(vfull(vs), vround & 1);
-        {
-          const uint8_t* vrow = smem + Cfg::kOffV + vs * Cfg::kTile + i * D;
-          uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
-          const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
-          uint4 v[D / 16];   // (all loads ahead of the first store, which they might alias)
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            v[c] = *reinterpret_cast<const uint4*>(vrow + ((c ^ sw) << 4));
-          if (pos > last_valid) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) v[c] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint4 a, d;
-            f16x2_from_e4m3x4(v[c].x, a.x, a.y);
-            f16x2_from_e4m3x4(v[c].y, a.z, a.w);
-            f16x2_from_e4m3x4(v[c].z, d.x, d.y);
-            f16x2_from_e4m3x4(v[c].w, d.z, d.w);
-            uint8_t* dst = v16 + (c >> 2) * 16384;
-            const int cc = 2 * (c & 3);
-            *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
-          }
-          mbar_arrive(vfree(vs));
-        }
-        vs += 2;
-        if (vs >= VS) {
-          vs -= VS;
-          ++vround;
-        }
         const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
         const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
-        okt = okt && mbar_wait_bounded(sfull(grp), k & 1);
+        // S of this tile follows PV of the group's last tile in the tensor pipe: P's buffer is free
+        // then, and O^T may be rescaled
+        const bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
         tc_fence_after();
         // z of columns 8 c .. 8 c + 7 less their references (y: S in, z out)
         auto z_chunk = [&](int c, float* y) {
@@ -740,127 +797,119 @@ __global__ void __launch_bounds__(384, 1)
               if (pos > L + tlim[8 * c + e]) y[e] = -INFINITY;
           }
         };
-        // P = 2^y of a chunk, eight f16 in 16 bytes of position i's row of columns, swizzled
-        // (columns that fill up N are never read; their P may be anything)
-        uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
-        const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
-        auto p_chunk = [&](int c, const float* y, bool sum) {
-          uint32_t w4[4];
+        float y[NQC];
+        float cx[8] = {};   // the capture columns
+        bool left = false, forced = hollow != 0;
+        while (true) {
+          bool need = forced;
+          if (okt) {
+            if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+            load_all(tl + s_col, y);
+            float ym = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float p0 = ex2(y[e]), p1 = ex2(y[e + 1]);
-            if (sum) ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
-            w4[e / 2] = pack_f16x2(p0, p1);
-          }
-          *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        };
-        bool need = empty != 0;
-        if (okt) {
-          float y[NQC];
-          float cx[8] = {};   // the capture columns
-          if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-          load_all(tl + s_col, y);
-          if (CAPTURE && pos < Lcap) {
-            if constexpr (kSideS) {
+            for (int c = 0; c < NQC / 8; ++c) {
+              z_chunk(c, y + 8 * c);
 #pragma unroll
-              for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
+              for (int e = 0; e < 8; e += 2) ym = fmaxf(fmaxf(ym, y[8 * c + e]), y[8 * c + e + 1]);
             }
-            srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
+            need |= ym > kTop;
           }
-          float ym = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < NQC / 8; ++c) {
-            z_chunk(c, y + 8 * c);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) ym = fmaxf(fmaxf(ym, y[8 * c + e]), y[8 * c + e + 1]);
-          }
-          need = __any_sync(0xffffffffu, need || ym > kTop);
-          // a warp that needs a higher reference leaves P and its sums to the raise below
-          if (!need) {
-#pragma unroll
-            for (int c = 0; c < NQC / 8; ++c) p_chunk(c, y + 8 * c, true);
-          }
-        }
-        const bool all_ok = __all_sync(0xffffffffu, okt);
-        if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
-        if (named_bar_any(1 + grp, 128, need || !okt)) {
+          const bool all_ok = __all_sync(0xffffffffu, okt);
+          if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
+          if (!named_bar_any(1 + grp, 128, need || !okt)) break;
           const int* vt = votes + (k & 1) * 8 + grp * 4;
           if (vt[0] | vt[1] | vt[2] | vt[3]) {
-            ok = false;
+            left = true;
             break;
           }
-          // Raise: column maxima over the group's 128 positions, from S once more.  PV of the
-          // group's last tile is done (above), so O^T may be rescaled.
+          // Raise: column maxima over the group's 128 positions
           float* cm = colmax + grp * 4 * NQC;
 #pragma unroll
-          for (int c0 = 0; c0 < NQC; c0 += 32) {
-            float y[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c0 + 8 * c >= NQC) continue;
-              load_chunk(tl + s_col, c0 / 8 + c, y + 8 * c);
-              z_chunk(c0 / 8 + c, y + 8 * c);
-            }
-            const float top = reduce_columns(y, [](float a, float d) { return fmaxf(a, d); });
-            if (c0 + lane < NQC) cm[q4 * NQC + c0 + lane] = top;
+          for (int c = 0; c < NQC / 8; ++c) {
+            const float top = reduce_chunk(y + 8 * c, [](float a, float d) { return fmaxf(a, d); });
+            if ((lane & 3) == 0) cm[q4 * NQC + 8 * c + (lane >> 2)] = top;
           }
           named_bar(1 + grp, 128);
-          // column n2's new reference, at least kRaise below the largest z (cm is relative to the
-          // old one)
-          auto raised = [&](int n2, float nro, float& old) {
-            const float top =
-                fmaxf(fmaxf(cm[n2], cm[NQC + n2]), fmaxf(cm[2 * NQC + n2], cm[3 * NQC + n2]));
-            old = ((empty >> n2) & 1) ? kEmptyMax : -nro;
-            return fmaxf(old, top - nro - kRaise);
-          };
-          uint64_t empty2 = empty;
-          float f1[NQC];
-#pragma unroll
-          for (int n2 = 0; n2 < NQC; ++n2) {
-            const float nro = kSmemRef ? nrg[n2] : nr[kSmemRef ? 0 : n2];
-            float old;
-            const float now = raised(n2, nro, old);
-            const bool now_empty = now == kEmptyMax;
-            f1[n2] = ex2(old - now);
-            if (!now_empty) empty2 &= ~(1ull << n2);
-            if constexpr (!kSmemRef) nr[n2] = now_empty ? 0.f : -now;
+          // a column's new reference, at least kRaise below its largest z (cm is relative to the old
+          // one), and the factor that its sums take
+          if (i < NQC) {
+            const float nro = nrg[i];
+            const float top = fmaxf(fmaxf(cm[i], cm[NQC + i]), fmaxf(cm[2 * NQC + i], cm[3 * NQC + i]));
+            const float old = ((hollow >> i) & 1) ? kEmptyMax : -nro;
+            const float now = fmaxf(old, top - nro - kRaise);
+            facs[grp * NQC + i] = ex2(old - now);
+            nrg[i] = now == kEmptyMax ? 0.f : -now;
+            colmax[grp * 4 * NQC + i] = now;   // (its own column: read above by this thread alone)
           }
+          named_bar(1 + grp, 128);
+          // (columns with masked logits only stay without one until the next tile)
+          hollow = 0;
 #pragma unroll
-          for (int n2 = 0; n2 < NQC; n2 += 2)
-            ls2[n2 / 2] = mul_f32x2(ls2[n2 / 2], pair_f32(f1[n2], f1[n2 + 1]));
+          for (int c0 = 0; c0 < NQC; c0 += 32) {
+            const bool still = c0 + lane < NQC && colmax[grp * 4 * NQC + c0 + lane] == kEmptyMax;
+            hollow |= uint64_t(__ballot_sync(0xffffffffu, still)) << c0;
+          }
+          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC);
+#pragma unroll
+          for (int c = 0; c < NQC / 4; ++c) {
+            const float4 v = fc[c];
+            ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
+            ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
+            if constexpr (!kSmemRef) {
+              const float4 r4 = reinterpret_cast<const float4*>(nrg)[c];
+              nr[4 * c] = r4.x;
+              nr[4 * c + 1] = r4.y;
+              nr[4 * c + 2] = r4.z;
+              nr[4 * c + 3] = r4.w;
+            }
+          }
           if (any) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NQC / 8; ++c) {
               float v8[8];
               tmem_ld8(tl + o_col + 8 * c, v8);
               tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v8[e] *= f1[8 * c + e];
+              const float4 a = fc[2 * c], d = fc[2 * c + 1];
+              v8[0] *= a.x;
+              v8[1] *= a.y;
+              v8[2] *= a.z;
+              v8[3] *= a.w;
+              v8[4] *= d.x;
+              v8[5] *= d.y;
+              v8[6] *= d.z;
+              v8[7] *= d.w;
               tmem_st8(tl + o_col + 8 * c, v8);
             }
             tmem_st_wait();
           }
-          named_bar(1 + grp, 128);   // colmax (and nrg) read; colmax is rewritten at the next raise
-          if constexpr (kSmemRef) {
-            if (i < NQC) {
-              const float nro = nrg[i];
-              float old;
-              const float now = raised(i, nro, old);
-              nrg[i] = now == kEmptyMax ? 0.f : -now;
-            }
-            named_bar(1 + grp, 128);   // new references visible
-          }
-          empty = empty2;
-          // P of this tile with the new references; the sums of a warp that has them were rescaled
+          forced = false;
+          named_bar(1 + grp, 128);   // colmax and the factors are read
+        }
+        if (left) {
+          ok = false;
+          break;
+        }
+        if (CAPTURE && pos < Lcap) {
+          if constexpr (kSideS) {
 #pragma unroll
-          for (int c = 0; c < NQC / 8; ++c) {
-            float y[8];
-            load_chunk(tl + s_col, c, y);
-            z_chunk(c, y);
-            p_chunk(c, y, need);
+            for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
           }
+          srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
+        }
+        // P = 2^y, eight f16 in 16 bytes of position i's row of columns, swizzled (columns that fill
+        // up N are never read; their P may be anything)
+        uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
+        const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
+#pragma unroll
+        for (int c = 0; c < NQC / 8; ++c) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float p0 = ex2(y[8 * c + e]), p1 = ex2(y[8 * c + e + 1]);
+            ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
+            w4[e / 2] = pack_f16x2(p0, p1);
+          }
+          *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
         tc_fence_before();
         mbar_arrive(sread(grp));
@@ -870,85 +919,59 @@ __global__ void __launch_bounds__(384, 1)
       }
 
       // ---------------------------------------------------------- the unit's end
-      // The group's last PV completes its O^T.
+      // row sums over the group's 128 positions
+#pragma unroll
+      for (int c = 0; c < NQC / 8; ++c) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) unpair_f32(ls2[4 * c + e / 2], v[e], v[e + 1]);
+        const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
+        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
+      }
+      // The group's last PV completes its O^T; group 1 hands its own over in P's buffers, once both
+      // groups' PVs have read them.
       if (any && ok) {
         const uint32_t last = it0 + uint32_t(tiles) - 1 - ((it0 + uint32_t(tiles) - 1 - uint32_t(grp)) & 1);
         if (!mbar_wait_bounded(pvdone(grp), (last >> 1) & 1)) ok = false;
       }
       tc_fence_after();
-      // row sums over the group's 128 positions, references, O^T
-#pragma unroll
-      for (int c0 = 0; c0 < NQC; c0 += 32) {
-        float v[32];
-#pragma unroll
-        for (int n2 = 0; n2 < 32; n2 += 2) {
-          v[n2] = v[n2 + 1] = 0.f;
-          if (c0 + n2 < NQC) unpair_f32(ls2[(c0 + n2) / 2], v[n2], v[n2 + 1]);
-        }
-        const float sum = reduce_columns(v, [](float a, float d) { return a + d; });
-        if (c0 + lane < NQC) colsum[(grp * 4 + q4) * NQC + c0 + lane] = sum;
-      }
-      if (q4 == 0 && !kSmemRef) {
-#pragma unroll
-        for (int n2 = 0; n2 < NQC; ++n2)
-          if (lane == n2) nrg[n2] = nr[kSmemRef ? 0 : n2];
-      }
-      // (a group without a tile: an empty reference; threads of a group agree on `empty`)
-      float o[NQC];
-#pragma unroll
-      for (int n2 = 0; n2 < NQC; ++n2) o[n2] = 0.f;
-      if (any && ok) {
-#pragma unroll
-        for (int c = 0; c < NQC / 8; ++c) {
-          float v8[8];
-          tmem_ld8(tl + o_col + 8 * c, v8);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[8 * c + e] = v8[e];
-        }
-        tmem_ld_wait();
-      }
+      if (i < NQC && ((hollow >> i) & 1)) colmax[grp * 4 * NQC + i] = kEmptyMax;
+      else if (i < NQC) colmax[grp * 4 * NQC + i] = -nrg[i];
       tc_fence_before();
       if (named_bar_any(3, 256, !ok)) {   // both groups leave together
         if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
         break;
       }
-      // weights of the two groups' states, by the threads of a group that own a column
-      if (i < NQC) {
-        const float m = ((empty >> i) & 1) ? kEmptyMax : -nrg[i];
-        const float* cs = colsum + grp * 4 * NQC;
-        const float l = cs[i] + cs[NQC + i] + cs[2 * NQC + i] + cs[3 * NQC + i];
-        fac[grp * NQC + i] = m;
-        colmax[grp * 4 * NQC + i] = l;
+      // the piece's maximum and sum of a column, and the weights of the two groups' states
+      if (tid < NQC) {
+        const float m0 = colmax[tid], m1 = colmax[4 * NQC + tid], M = fmaxf(m0, m1);
+        const float w0 = ex2(m0 - M), w1 = ex2(m1 - M);
+        const float* cs = colsum + tid;
+        wgt[tid] = w0;
+        wgt[NQC + tid] = w1;
+        colM[tid] = M;
+        colL[tid] = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
+                    w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
       }
-      named_bar(3, 256);
-      // Group 0 finishes the first half of the columns, group 1 the second: each hands its part of
-      // the other's half over in its V' buffer, weighted.
-      constexpr int H = NQC / 2;
-      auto weight = [&](int n2, float& M) {   // of this group's state of column n2
-        const float m0 = fac[n2], m1 = fac[NQC + n2];
-        M = fmaxf(m0, m1);
-        return ex2((grp ? m1 : m0) - M);
-      };
-      float* give = reinterpret_cast<float*>(smem + Cfg::kOffV16 + grp * Cfg::kV16);
-      const float* get = reinterpret_cast<const float*>(smem + Cfg::kOffV16 + (grp ^ 1) * Cfg::kV16);
-      float mine[H];
+      float* hand = reinterpret_cast<float*>(smem + Cfg::kOffP);   // [NQC][D]
+      const bool any1 = tiles > 1 || (it0 & 1);                    // group 1 has a tile
+      const bool any0 = tiles > 1 || !(it0 & 1);
+      if (grp == 1 && any1) {
+#pragma unroll 1
+        for (int c = 0; c < NQC / 8; ++c) {
+          float v8[8];
+          tmem_ld8(tl + o_col + 8 * c, v8);
+          tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        float M;
-        const int other = grp ? j : H + j, own = grp ? H + j : j;
-        const float w = weight(other, M);
-        if (dim >= 0) give[j * D + dim] = (grp ? o[j] : o[H + j]) * w;
-        mine[j] = (grp ? o[H + j] : o[j]) * weight(own, M);
-      }
-      if (i < H) {   // the piece's maximum and sum of the columns that this group finishes
-        const int n2 = grp ? H + i : i;
-        const float m0 = fac[n2], m1 = fac[NQC + n2], M = fmaxf(m0, m1);
-        colM[n2] = M;
-        colL[n2] = ex2(m0 - M) * colmax[n2] + ex2(m1 - M) * colmax[4 * NQC + n2];
+          for (int e = 0; e < 8; ++e)
+            if (dim >= 0) hand[(8 * c + e) * D + dim] = v8[e];
+        }
+        tc_fence_before();
       }
       named_bar(3, 256);
-      const long long unit1 = unit0 + at.tiles;
-      const int c0 = cta_of(unit0), c1 = cta_of(unit1 - 1);
+      // the CTAs that hold tiles of the unit
+      const long long tile0 = unit0 + kUnitTiles;
+      const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
       const size_t unit = size_t(b) * p.hkv + g;
       auto out_row = [&](int n2) {
         const int t = n2 / p.group, hl = n2 - t * p.group;
@@ -958,87 +981,96 @@ __global__ void __launch_bounds__(384, 1)
       // where that is another; of a unit's CTAs only the first can have it as its last.
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
+      if (grp == 0) {
+#pragma unroll 1
+        for (int c = 0; c < NQC / 8; ++c) {
+          float v8[8] = {};
+          if (any0) {
+            tmem_ld8(tl + o_col + 8 * c, v8);
+            tmem_ld_wait();
+          }
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        const int n2 = grp ? H + j : j;
-        if (dim < 0 || n2 >= p.nq) continue;
-        const float v = mine[j] + get[j * D + dim];
-        if (c0 == c1)
-          out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
-        else
-          p.part_o[(slot * p.nq + n2) * D + dim] = v;
+          for (int e = 0; e < 8; ++e) {
+            const int n2 = 8 * c + e;
+            if (dim < 0 || n2 >= p.nq) continue;
+            float v = any0 ? v8[e] * wgt[n2] : 0.f;
+            if (any1) v = fmaf(hand[n2 * D + dim], wgt[NQC + n2], v);
+            if (c0 == c1)
+              out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
+            else
+              p.part_o[(slot * p.nq + n2) * D + dim] = v;
+          }
+        }
+        tc_fence_before();
+        if (c0 != c1 && tid < p.nq)
+          reinterpret_cast<float2*>(p.part_ml)[slot * p.nq + tid] = make_float2(colM[tid], colL[tid]);
       }
       if (c0 != c1) {
-        if (tid < p.nq) {
-          p.part_ml[2 * (slot * p.nq + tid)] = colM[tid];
-          p.part_ml[2 * (slot * p.nq + tid) + 1] = colL[tid];
-        }
-        __threadfence();
         named_bar(3, 256);
-        if (tid == 0) *flag = atomicAdd(&p.tickets[unit], 1) == c1 - c0;
+        if (tid == 0) {   // (the fence covers what the barrier made visible to this thread)
+          __threadfence();
+          *flag = atomicAdd(&p.tickets[unit], 1) == c1 - c0;
+          __threadfence();
+        }
         named_bar(3, 256);
         if (*flag) {
           // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m).
-          __threadfence();
           const int pieces = c1 - c0 + 1;
           auto slot_of = [&](int c) { return size_t(c == 0 ? slot0 : 2 * (c0 + c)); };
-          float* wts = reinterpret_cast<float*>(smem + Cfg::kOffV16);   // [nq][pieces]
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+#pragma unroll 1
           for (int n2 = warp; n2 < p.nq; n2 += 8) {
-            float M = kEmptyMax;
-            for (int c = lane; c < pieces; c += 32)
-              M = fmaxf(M, __ldcg(&p.part_ml[2 * (slot_of(c) * p.nq + n2)]));
-#pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
-            float sum = 0.f;
+            float M = kEmptyMax, sum = 0.f;
+#pragma unroll 1
             for (int c = lane; c < pieces; c += 32) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) +
-                                       slot_of(c) * p.nq + n2);
-              const float F = ex2(ml.x - M);
-              wts[n2 * pieces + c] = F;
-              sum += F * ml.y;
+              const float2 v = __ldcg(ml + slot_of(c) * p.nq + n2);
+              const float now = fmaxf(M, v.x);
+              sum = sum * ex2(M - now) + v.y * ex2(v.x - now);
+              M = now;
             }
+            float top = M;
+#pragma unroll
+            for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+            sum *= ex2(M - top);
 #pragma unroll
             for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-            const float inv = 1.f / sum;
-            for (int c = lane; c < pieces; c += 32) wts[n2 * pieces + c] *= inv;
+            if (lane == 0) {
+              colM[n2] = top;
+              colL[n2] = 1.f / sum;
+            }
           }
           named_bar(3, 256);
+#pragma unroll 1
           for (int e = tid; e < p.nq * (D / 4); e += 256) {
             const int n2 = e / (D / 4), d = 4 * (e - n2 * (D / 4));
-            const float* w = wts + n2 * pieces;
+            const float M = colM[n2], inv = colL[n2];
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int c = 0; c < pieces; ++c) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                  p.part_o + (slot_of(c) * p.nq + n2) * D + d));
-              acc.x += w[c] * v.x;
-              acc.y += w[c] * v.y;
-              acc.z += w[c] * v.z;
-              acc.w += w[c] * v.w;
+              const size_t row = slot_of(c) * p.nq + n2;
+              const float w = ex2(__ldcg(&p.part_ml[2 * row]) - M);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
+              acc.x += w * v.x;
+              acc.y += w * v.y;
+              acc.z += w * v.z;
+              acc.w += w * v.w;
             }
-            const uint2 pk = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            *reinterpret_cast<uint2*>(out_row(n2) + d) = pk;
+            *reinterpret_cast<uint2*>(out_row(n2) + d) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
           }
           if (tid == 0) p.tickets[unit] = 0;
         }
       }
-      named_bar(3, 256);   // the exchange buffers and columns are free again
-      unit0 = unit1;
+      named_bar(3, 256);   // the buffers and columns are free again
+      unit0 += at.tiles + kUnitTiles;
       it0 += uint32_t(tiles);
-      vs0 += uint32_t(tiles) % VS;
-      vround0 += uint32_t(tiles) / VS;
-      if (vs0 >= VS) {
-        vs0 -= VS;
-        ++vround0;
-      }
-      at.left -= tiles;
-      if (at.left > 0) next_unit(at);
+      next_unit(at, tiles);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == 14) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
@@ -1056,7 +1088,7 @@ static cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(384, 1, 1);
+  cfg.blockDim = dim3(512, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
