@@ -15,6 +15,8 @@ constexpr int kAttnWarps = 8;          // warps per attention CTA
 constexpr int kMaxSplits = 128;        // split-KV partials per (sequence, KV head)
 constexpr int kMaxSparseCluster = 16;  // CTAs per (sequence, KV head) in the draft kernel
 constexpr int kMaxSparseRowsPerCta = 2048;
+// (rows of half the bytes leave room for a longer table: fewer CTAs a list, and one wave of them)
+constexpr int sparse_rows_per_cta(bool kv8) { return kv8 ? 2 * kMaxSparseRowsPerCta : kMaxSparseRowsPerCta; }
 
 struct VerifyParams {
   const void* q;            // bf16 [B][T][Hq][D]

@@ -25,7 +25,6 @@
 namespace vegas {
 
 namespace {
-constexpr int kAppendThreads = 512;
 constexpr int kQueryBatch = 4;   // query units a thread has in flight
 
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
@@ -91,8 +90,9 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float f) {
 }
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv8Params p) {
+template <int D, int Threads>
+__global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
+    kv8_append_kernel(const RopeKv8Params p) {
   constexpr int U = D / 16;              // units of a head
   constexpr int RowsPerPass = 32 / U, Passes = 16 / RowsPerPass;
   // (cos, sin) of pairs 2j, 2j + 1 of unit u of a row at [row][j][u]: eight lanes with
@@ -101,20 +101,31 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_begin();
 
-  // The slot's sequence: the last b with floor(row_start[b] / 16) + 2 b <= slot, 32 at a time.
+  // The slot's sequence: the last b with floor(row_start[b] / 16) + 2 b <= slot, 32 at a time; the
+  // last step brings the sequence's rows and context along.
   const int slot = blockIdx.x;
-  int s = 0;
+  int s = 0, beg = 0, end = 0, ctx = 0;
   for (int n = p.batch; n > 0;) {
     const int step = (n + 31) >> 5, at = s + lane * step;
-    const bool before = lane * step < n && (p.row_start[at] >> 4) + 2 * at <= slot;
-    const unsigned m = __ballot_sync(0xffffffffu, before);
+    const bool there = lane * step < n;
+    const int first = there ? p.row_start[at] : 0;
+    int next = 0, held_rows = 0;
+    if (step == 1 && there) {
+      next = p.row_start[at + 1];
+      held_rows = p.ctx_lens[at];
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, there && (first >> 4) + 2 * at <= slot);
     if (!m) return;
     const int l = 31 - __clz(m);
     n = min(step, n - l * step);
     s += l * step;
-    if (step == 1) break;
+    if (step == 1) {
+      beg = __shfl_sync(0xffffffffu, first, l);
+      end = __shfl_sync(0xffffffffu, next, l);
+      ctx = __shfl_sync(0xffffffffu, held_rows, l);
+      break;
+    }
   }
-  const int beg = p.row_start[s], end = p.row_start[s + 1], ctx = p.ctx_lens[s];
   const int j = slot - ((beg >> 4) + 2 * s);
   if (end == beg) return;                // (without rows ctx may be anything)
   if (end < beg || beg < 0 || end > p.total_rows || ctx < 0 ||
@@ -128,8 +139,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
   if (R <= 0) return;
   const int o = ctx + t0 - page * 16, row0 = beg + t0;
   const int phys = p.block_table[size_t(s) * p.max_pages + page];
-  const bool page_ok = phys >= 0 && phys < p.num_pages;
-  if (!page_ok && tid == 0) set_error(p.err, kErrDeviceFault);
   const bool held = j == 0 && o > 0;     // slots 0 .. o - 1 hold rows of earlier calls
 
   const int u = lane % U, half = p.rot >> 1;
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
   const int o1 = !turned || p.interleaved ? o0 + 8 : o0 + half;
 
   // The warp's first (KV head, K or V): its rows are on their way under the sines below.
-  const int tasks = page_ok ? 2 * p.hkv : 0;
+  const int tasks = 2 * p.hkv;
   uint4 A[Passes], B[Passes];
   auto load_task = [&](int t) {
     const bool is_v = t >= p.hkv;
@@ -160,8 +169,38 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
   };
   if (warp < tasks) load_task(warp);
 
+  // Queries: item i is unit i % U of head (i / U) % hq of row i / (U hq).
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + size_t(row0) * p.q_stride;
+  uint16_t* qo = reinterpret_cast<uint16_t*>(p.q_out) + size_t(row0) * p.hq * D;
+  constexpr int Step = Threads / U;   // heads from one item of a thread to its next
+  const int step_r = Step / p.hq, step_h = Step - step_r * p.hq;
+  int r = (tid / U) / p.hq, h = tid / U - r * p.hq;
+  uint4 a[kQueryBatch], b[kQueryBatch];
+  int rr[kQueryBatch], hh[kQueryBatch];
+  auto load_queries = [&]() {
+#pragma unroll
+    for (int i = 0; i < kQueryBatch; ++i) {
+      rr[i] = r;
+      hh[i] = h;
+      if (r < R) {
+        const uint16_t* at = q + r * size_t(p.q_stride) + h * D;
+        a[i] = *reinterpret_cast<const uint4*>(at + o0);
+        b[i] = *reinterpret_cast<const uint4*>(at + o1);
+      }
+      h += step_h;
+      r += step_r;
+      if (h >= p.hq) {
+        h -= p.hq;
+        ++r;
+      }
+    }
+  };
+  // few threads a page (many pages): other CTAs hide the latency, and registers are short
+  constexpr bool kEarly = Threads > 256;
+  if (kEarly) load_queries();
+
   float2* cs2 = reinterpret_cast<float2*>(cs_all);
-  for (int i = tid; i < R * half; i += kAppendThreads) {
+  for (int i = tid; i < R * half; i += Threads) {
     const int r = i / half, pair = i - r * half;
     int at = ctx + t0 + r;
     if (p.positions) {
@@ -179,9 +218,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
     const int unit = pair >> 3, e = pair & 7;
     cs2[((r * 4 + (e >> 1)) * U + unit) * 2 + (e & 1)] = make_float2(cn * p.scale, sn * p.scale);
   }
+  const bool page_ok = phys >= 0 && phys < p.num_pages;
+  if (!page_ok && tid == 0) set_error(p.err, kErrDeviceFault);
   __syncthreads();
 
-  for (int t = warp; t < tasks; t += kAppendThreads / 32) {
+  for (int t = page_ok ? warp : tasks; t < tasks; t += Threads / 32) {
     if (t != warp) load_task(t);
     const bool is_v = t >= p.hkv;
     const int g = is_v ? t - p.hkv : t;
@@ -220,31 +261,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
     if (lane == 0) *scale = uint8_t(e + kKv8Bias);
   }
 
-  // Queries: item i is unit i % U of head (i / U) % hq of row i / (U hq).
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + size_t(row0) * p.q_stride;
-  uint16_t* qo = reinterpret_cast<uint16_t*>(p.q_out) + size_t(row0) * p.hq * D;
-  constexpr int Step = kAppendThreads / U;   // heads from one item of a thread to its next
-  const int step_r = Step / p.hq, step_h = Step - step_r * p.hq;
-  int r = (tid / U) / p.hq, h = tid / U - r * p.hq;
-  while (r < R) {
-    uint4 a[kQueryBatch], b[kQueryBatch];
-    int rr[kQueryBatch], hh[kQueryBatch];
-#pragma unroll
-    for (int i = 0; i < kQueryBatch; ++i) {
-      rr[i] = r;
-      hh[i] = h;
-      if (r < R) {
-        const uint16_t* at = q + r * size_t(p.q_stride) + h * D;
-        a[i] = *reinterpret_cast<const uint4*>(at + o0);
-        b[i] = *reinterpret_cast<const uint4*>(at + o1);
-      }
-      h += step_h;
-      r += step_r;
-      if (h >= p.hq) {
-        h -= p.hq;
-        ++r;
-      }
-    }
+  bool loaded = kEarly;
+  while (true) {
+    if (!loaded) load_queries();
+    loaded = false;
 #pragma unroll
     for (int i = 0; i < kQueryBatch; ++i) {
       if (rr[i] >= R) continue;
@@ -253,21 +273,27 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const RopeKv
       *reinterpret_cast<uint4*>(at + o0) = a[i];
       *reinterpret_cast<uint4*>(at + o1) = b[i];
     }
+    if (rr[kQueryBatch - 1] >= R) break;
   }
 }
 
-cudaError_t launch_kv8_append(const RopeKv8Params& p, cudaStream_t stream) {
+template <int Threads>
+static cudaError_t launch_threads(const RopeKv8Params& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.total_rows / 16 + 2 * p.batch, 1, 1);
-  cfg.blockDim = dim3(kAppendThreads, 1, 1);
+  cfg.blockDim = dim3(Threads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, kv8_append_kernel<64>, p)
-                          : cudaLaunchKernelEx(&cfg, kv8_append_kernel<128>, p);
+  return p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, kv8_append_kernel<64, Threads>, p)
+                          : cudaLaunchKernelEx(&cfg, kv8_append_kernel<128, Threads>, p);
+}
+
+cudaError_t launch_kv8_append(const RopeKv8Params& p, cudaStream_t stream) {
+  return p.total_rows >= 4000 ? launch_threads<256>(p, stream) : launch_threads<512>(p, stream);
 }
 
 }  // namespace vegas

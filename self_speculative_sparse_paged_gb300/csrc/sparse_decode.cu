@@ -46,7 +46,7 @@ struct SparseCfg {
   static constexpr int kRow = KV8 ? D : D * 2 + 16;   // row stride, padded in bf16
   static constexpr int kTile = 16 * kRow;
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kMaxRows = kMaxSparseRowsPerCta;
+  static constexpr int kMaxRows = sparse_rows_per_cta(KV8);
   static constexpr size_t kStageBytes = size_t(kWarps) * kStages * kStage;
 };
 

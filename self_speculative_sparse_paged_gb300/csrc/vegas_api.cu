@@ -290,7 +290,7 @@ SparsePlan plan_sparse(const vegas_paged_kv_t* kv, int batch, int k_max, int max
   pl.ntiles = (G + 7) / 8;
   const int units = std::max(1, batch * kv->num_kv_heads);
   const int rows_max = std::max(1, k_max + max_tail);
-  const int fit = (rows_max + vegas::kMaxSparseRowsPerCta - 1) / vegas::kMaxSparseRowsPerCta;
+  const int fit = (rows_max + vegas::sparse_rows_per_cta(kv8) - 1) / vegas::sparse_rows_per_cta(kv8);
   int cl;
   if (2 * units < sms) {
     cl = std::min(vegas::kMaxSparseCluster, std::max(fit, std::min(sms / units,
