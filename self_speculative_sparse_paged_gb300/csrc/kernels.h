@@ -302,7 +302,7 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, const PromptParams& p, int head_dim, int grid,
                           cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream);
-cudaError_t launch_kv8_append(const RopeKv8Params& p, cudaStream_t stream);
+cudaError_t launch_kv8_append(const RopeKv8Params& p, int sms, cudaStream_t stream);
 cudaError_t launch_kv8_read(const Kv8ReadParams& p, int batch, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, bool bf16, cudaStream_t stream);
 

@@ -14,7 +14,10 @@
 // registers: lane l has unit l % (d / 16) (two chunks of 8 elements: the two halves of 8 pairs)
 // of every (32 / (d / 16))-th row, so the maximum is a warp reduction and no row is read twice.
 // The queries of the page's rows are then turned by all warps, an item a unit.  Cosines and
-// sines are made once per (row, pair), the angle in fp64, and shared by all heads.
+// sines are made once per (row, pair) and shared by all heads.  The angle in turns is taken modulo 1
+// by 64-bit integers: a pair's frequency over 2 pi, from fp64, as a fraction F of 2^64, and p F
+// wraps by itself.  (In fp64, of which an SM does two operations a clock, the angles of 16K rows took
+// 10 us of 70, and as much again for every part that the heads were divided into.)
 //
 // Pages are dealt out by slots: sequence b owns the slots from floor(row_start[b] / 16) + 2 b on,
 // at least floor(n / 16) + 2 of them, and n rows touch at most that many pages; a slot without a
@@ -98,8 +101,13 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
   // (cos, sin) of pairs 2j, 2j + 1 of unit u of a row at [row][j][u]: eight lanes with
   // consecutive units read consecutive 16 bytes
   __shared__ float4 cs_all[16 * 4 * U];
+  __shared__ unsigned long long turn_all[D / 2];   // F of a pair
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_begin();
+  if (tid < (p.rot >> 1)) {
+    const double c = double(p.inv_freq[tid]) * 0.15915494309189533577;   // 1 / (2 pi)
+    turn_all[tid] = __double2ull_rn((c - floor(c)) * 18446744073709551616.0);
+  }
 
   // The slot's sequence: the last b with floor(row_start[b] / 16) + 2 b <= slot, 32 at a time; the
   // last step brings the sequence's rows and context along.
@@ -147,7 +155,10 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
   const int o1 = !turned || p.interleaved ? o0 + 8 : o0 + half;
 
   // The warp's first (KV head, K or V): its rows are on their way under the sines below.
-  const int tasks = 2 * p.hkv;
+  // this CTA's share of the heads: every gridDim.y-th (KV head, K or V), a run of query heads
+  const int part = blockIdx.y, parts = gridDim.y;
+  const int tasks = 2 * p.hkv, task0 = part + parts * warp;
+  const int q0 = p.hq * part / parts, hq = p.hq * (part + 1) / parts - q0;
   uint4 A[Passes], B[Passes];
   auto load_task = [&](int t) {
     const bool is_v = t >= p.hkv;
@@ -167,14 +178,14 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
       }
     }
   };
-  if (warp < tasks) load_task(warp);
+  if (task0 < tasks) load_task(task0);
 
-  // Queries: item i is unit i % U of head (i / U) % hq of row i / (U hq).
-  const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + size_t(row0) * p.q_stride;
-  uint16_t* qo = reinterpret_cast<uint16_t*>(p.q_out) + size_t(row0) * p.hq * D;
+  // Queries: item i is unit i % U of head q0 + (i / U) % hq of row i / (U hq).
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + size_t(row0) * p.q_stride + q0 * D;
+  uint16_t* qo = reinterpret_cast<uint16_t*>(p.q_out) + (size_t(row0) * p.hq + q0) * D;
   constexpr int Step = Threads / U;   // heads from one item of a thread to its next
-  const int step_r = Step / p.hq, step_h = Step - step_r * p.hq;
-  int r = (tid / U) / p.hq, h = tid / U - r * p.hq;
+  const int step_r = hq ? Step / hq : 0, step_h = Step - step_r * hq;
+  int r = hq ? (tid / U) / hq : R, h = tid / U - r * hq;
   uint4 a[kQueryBatch], b[kQueryBatch];
   int rr[kQueryBatch], hh[kQueryBatch];
   auto load_queries = [&]() {
@@ -189,8 +200,8 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
       }
       h += step_h;
       r += step_r;
-      if (h >= p.hq) {
-        h -= p.hq;
+      if (h >= hq) {
+        h -= hq;
         ++r;
       }
     }
@@ -199,6 +210,7 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
   constexpr bool kEarly = Threads > 256;
   if (kEarly) load_queries();
 
+  __syncthreads();
   float2* cs2 = reinterpret_cast<float2*>(cs_all);
   for (int i = tid; i < R * half; i += Threads) {
     const int r = i / half, pair = i - r * half;
@@ -211,10 +223,9 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
       }
       at = p.positions[size_t(axis) * p.total_rows + row0 + r];
     }
-    double turns = double(at) * double(p.inv_freq[pair]) * 0.15915494309189533577;   // 1 / (2 pi)
-    turns -= rint(turns);
+    const float turns = __ll2float_rn((long long)at * (long long)turn_all[pair]) * 0x1p-64f;
     float sn, cn;
-    sincospif(2.f * float(turns), &sn, &cn);
+    sincospif(2.f * turns, &sn, &cn);
     const int unit = pair >> 3, e = pair & 7;
     cs2[((r * 4 + (e >> 1)) * U + unit) * 2 + (e & 1)] = make_float2(cn * p.scale, sn * p.scale);
   }
@@ -222,8 +233,8 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
   if (!page_ok && tid == 0) set_error(p.err, kErrDeviceFault);
   __syncthreads();
 
-  for (int t = page_ok ? warp : tasks; t < tasks; t += Threads / 32) {
-    if (t != warp) load_task(t);
+  for (int t = page_ok ? task0 : tasks; t < tasks; t += parts * (Threads / 32)) {
+    if (t != task0) load_task(t);
     const bool is_v = t >= p.hkv;
     const int g = is_v ? t - p.hkv : t;
     const size_t block = size_t(phys) * p.hkv + g;
@@ -278,9 +289,9 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
 }
 
 template <int Threads>
-static cudaError_t launch_threads(const RopeKv8Params& p, cudaStream_t stream) {
+static cudaError_t launch_threads(const RopeKv8Params& p, int parts, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.total_rows / 16 + 2 * p.batch, 1, 1);
+  cfg.gridDim = dim3(p.total_rows / 16 + 2 * p.batch, parts, 1);
   cfg.blockDim = dim3(Threads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -292,8 +303,14 @@ static cudaError_t launch_threads(const RopeKv8Params& p, cudaStream_t stream) {
                           : cudaLaunchKernelEx(&cfg, kv8_append_kernel<128, Threads>, p);
 }
 
-cudaError_t launch_kv8_append(const RopeKv8Params& p, cudaStream_t stream) {
-  return p.total_rows >= 4000 ? launch_threads<256>(p, stream) : launch_threads<512>(p, stream);
+cudaError_t launch_kv8_append(const RopeKv8Params& p, int sms, cudaStream_t stream) {
+  // Two CTAs a page, each half of the heads.  While they are about one wave of SMs, 512 threads
+  // each; from there on 256, three on an SM, so that one's lookups run under another's stream
+  // (32 query and 8 KV heads of 128; 512 / 256 threads: 32 pages of a row 4.0 / 4.8 us, 63 pages 6.0 /
+  // 11.4, 126 pages 15.1 / 12.8, 500 pages 46.8 / 31.3, 1024 pages 87 / 58; with one CTA a page and
+  // 256 threads 60, with four 68, as each makes the page's sines anew).
+  const long long pages = p.total_rows / 16 + (long long)p.batch;
+  return 2 * pages <= sms ? launch_threads<512>(p, 2, stream) : launch_threads<256>(p, 2, stream);
 }
 
 }  // namespace vegas

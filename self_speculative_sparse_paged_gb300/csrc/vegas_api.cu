@@ -1009,14 +1009,15 @@ VEGAS_API vegas_status_t vegas_rope_append_kv8(
     return st;
   if (total_rows == 0 || batch == 0) return VEGAS_OK;
   int* err = nullptr;
-  if ((st = device_info(&err, nullptr)) != VEGAS_OK) return st;
+  int sms = 0;
+  if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
   vegas::RopeKv8Params p{};
   fill_append(p, kv, q, q_stride, k, k_stride, v, v_stride, q_out, row_start, ctx_lens, positions,
               pair_axis, num_axes, inv_freq, rot_dim, interleaved, rope_scale, total_rows, batch,
               err);
   p.k_scale = kv->k_scale;
   p.v_scale = kv->v_scale;
-  cudaError_t e = vegas::launch_kv8_append(p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = vegas::launch_kv8_append(p, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "quantised append launch");
   return VEGAS_OK;
 }
