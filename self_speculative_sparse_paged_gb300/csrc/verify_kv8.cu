@@ -4,13 +4,12 @@
 // The work is that of verify_tc.cu on half the bytes, laid out so that its length goes by what the
 // sequences hold, not by what their tables could: the 128-position tiles of all (sequence, KV
 // head) units stand in one row, and each CTA (one an SM) takes an equal run of it, whole units or
-// pieces, with the K/V stream going on from one unit to the next.  Sixteen warps:
-//   warps 0-7    two softmax groups of four warps that alternate tiles; a thread owns a position
-//                of a tile, and a head dimension of the group's O^T.  They also build the query operand
-//                of a unit and finish it.
-//   warps 8-11   turn V's codes into f16, a thread a position
-//   warps 12, 13 TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
-//   warp 14      issues the MMAs
+// pieces, with the K/V stream going on from one unit to the next.  Twelve warps:
+//   warps 0-7   two softmax groups of four warps that alternate tiles; a thread owns a position
+//               of a tile, and a head dimension of the group's O^T.  They also build the query operand
+//               of a unit and finish it.
+//   warps 8, 9  TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
+//   warp 10     issues the MMAs
 //
 //   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
 //       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
@@ -21,13 +20,17 @@
 //   z = S 2^(e_k - k) scale log2(e) + e_v,  P = 2^(z - r) with r a reference for the column:
 //       e_k costs nothing (a thread's one factor), and 2^e_v goes into P instead of V.  Row sums
 //       take P 2^-e_v in fp32.
-//   O^T[D x N] += V'^T P^T   kind::f16, M = D: V' are V's codes as f16, exact (16 codes: one load,
-//       8 conversions, two stores).
+//   O^T[D x N] += V^T P^T   kind::f8f6f4, M = D: V's codes as they lie (read MN-major), P as the
+//       sum of three e5m2 parts.  e5m2 is the upper byte of f16, so the parts are cut off P's f16
+//       (each takes three bits or more, the last is rounded: 2^-9 of P at most), with f16's range.
+//       Turning V into f16 instead moved 1200-1300 clocks' worth of a tile's 1425 through
+//       shared memory at head_dim 128, which bounded that kernel (172-179 us on a batch of eight
+//       of 49K-64K); this one moves about 750.
 //
-// The two parts of the queries lie side by side in N (one pass over K; an MMA takes 45 clocks up
-// to N = 64 and 64 at 128) up to 40 columns, else they share an accumulator.
-// P <= 2^15 (f16 ends at 65504) and the largest P is 2^7 or more when r was raised, so P's grid
-// reaches 2^-31 below the largest.  e_v spans 120, so that no term that weighs in a row sum is lost to
+// Parts lie side by side in N where tensor memory holds their columns (one pass over the A
+// operand; an MMA takes 45 clocks up to N = 64 and 64 at 128), else they share an accumulator.
+// P <= 2^15 (f16 ends at 65504) and the largest P is 2^11 or more when r was raised, so P's grid
+// reaches 2^-28 below the largest.  e_v spans 120, so that no term that weighs in a row sum is lost to
 // fp32's smallest number (its P is at least 2^-121).
 //
 // A unit that one CTA covers is written by it; the pieces of a shared one go to the workspace
@@ -44,28 +47,31 @@
 namespace vegas {
 
 namespace {
-constexpr float kTop = 15.f, kRaise = 7.f;   // log2 of the largest P, and of P at a raised reference
+constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P at a raised reference
 constexpr int kCapParts = 6;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
 // reference and end), and a CTA takes part for kLeastRun tiles or more.
 constexpr int kUnitTiles = 3, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
-// Instruction descriptors, fp32 accumulator: e4m3 by e4m3, K-major (K = 32); f16 by f16,
-// MN-major (K = 16).
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
-  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4 (K = 32), fp32 accumulator: A e4m3, B e4m3 or e5m2, both
+// K-major or both MN-major (N in whole 16-byte units then).
+__host__ __device__ constexpr uint32_t idesc_f8(int m, int n, int b_e5m2, int mn_major) {
+  return (1u << 4) | (uint32_t(b_e5m2) << 10) | (uint32_t(mn_major) << 15) |
+         (uint32_t(mn_major) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
-__host__ __device__ constexpr uint32_t idesc_f16_mn(int m, int n) {
-  return (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
-}
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 // op over the warp's lanes of each of eight columns: lane l gets column l / 4's.  In three steps a
 // lane exchanges half of the columns it still holds for the other half of another lane's.
@@ -97,14 +103,18 @@ struct Kv8Cfg {
   static constexpr int kCap = CAPTURE ? (kSideS ? kCapParts : kCapParts / 2) : 0;
   static constexpr int kCap0 = kSideS ? 2 * NQC : NQC;    // first capture column
   static constexpr int NS = (kCap0 + kCap + 15) / 16 * 16;   // N of S
-  static constexpr int NP = (NQC + 15) / 16 * 16;     // N of PV
+  // PV: three parts side by side, or one after the other (NQC = 64)
+  static constexpr bool kSideP = NQC <= 56;
+  static constexpr int kPCols = kSideP ? 3 * NQC : NQC;
+  static constexpr int NP = (kPCols + 15) / 16 * 16;  // N of PV
   static constexpr int kTile = 128 * D;               // one K tile (and one V tile): 8 pages
+  // P of a position: rows of 128 bytes in blocks of 128 positions, [part][NQC] over the blocks, or a
+  // block a part
+  static constexpr int kBlocks = kSideP ? (NP + 127) / 128 : 3;
+  static constexpr int kP = kBlocks * 128 * 128;
   // Ring slots (16 KB at head_dim 128, 8 KB at 64): as many as fit beside the rest.
-  static constexpr int KS = D == 64 ? 8 : 4;
-  static constexpr int VS = D == 64 ? 8 : NQC <= 32 ? 4 : 3;
-  static constexpr int kV16 = 128 * D * 2;            // a tile's V' [half][128][128 B], one a group
-  static constexpr int kPRow = NQC <= 32 ? 64 : 128;  // bytes of a position's P row
-  static constexpr int kP = 128 * kPRow;
+  static constexpr int KS = D == 128 ? 5 : kBlocks == 3 ? 6 : 8;
+  static constexpr int VS = D == 128 ? 6 : kBlocks == 3 ? 6 : kBlocks == 2 ? 8 : 10;
   static constexpr int kQ = NS * D;                   // Q^T operand, one a pass
   static constexpr int kPasses = kSideS ? 1 : 2;
   static constexpr int kSCol = (NS + 31) / 32 * 32, kOCol = (NP + 31) / 32 * 32;
@@ -112,13 +122,12 @@ struct Kv8Cfg {
       2 * (kSCol + kOCol) <= 128 ? 128 : 2 * (kSCol + kOCol) <= 256 ? 256 : 512;
   static_assert(2 * (kSCol + kOCol) <= 512, "tensor memory");
   static constexpr int kOffV = KS * kTile;
-  static constexpr int kOffV16 = kOffV + VS * kTile;
-  static constexpr int kOffP = kOffV16 + 2 * kV16;
+  static constexpr int kOffP = kOffV + VS * kTile;
   static constexpr int kOffQ = kOffP + 2 * kP;
   static constexpr int kOffBar = kOffQ + kPasses * kQ;
-  static constexpr int kNumBars = 2 * KS + 2 * VS + 5 * 2 + 2;
+  static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 2;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  // misc: 16 words; votes[2][2][4]; warp sums[16] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
+  // misc: 16 words; votes[2][2][4]; warp sums[12] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
   // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
   static constexpr size_t kMisc = 64 + 64 + 128 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
@@ -139,12 +148,12 @@ struct Place {
 };
 
 template <int D, int NQC, bool CAPTURE>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(384, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const VerifyKv8Params p) {
   using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
   constexpr int KS = Cfg::KS, VS = Cfg::VS, NS = Cfg::NS, NP = Cfg::NP;
-  constexpr bool kSideS = Cfg::kSideS;
+  constexpr bool kSideS = Cfg::kSideS, kSideP = Cfg::kSideP;
   static_assert(NQC % 8 == 0 && (D == 64 || D == 128), "columns, head_dim");
 
   griddep_launch_dependents();
@@ -153,8 +162,8 @@ __global__ void __launch_bounds__(512, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + Cfg::kOffBar;
-  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P ready, PV done,
-  // V' ready (per softmax group); queries ready, MMA drain
+  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P ready, PV done
+  // (per softmax group); queries ready, MMA drain
   auto kfull = [&](int s) { return bar0 + 8 * s; };
   auto kfree = [&](int s) { return bar0 + 8 * (KS + s); };
   auto vfull = [&](int s) { return bar0 + 8 * (2 * KS + s); };
@@ -164,15 +173,14 @@ __global__ void __launch_bounds__(512, 1)
   auto sread = [&](int g2) { return bar0 + 8 * (B1 + 2 + g2); };
   auto pready = [&](int g2) { return bar0 + 8 * (B1 + 4 + g2); };
   auto pvdone = [&](int g2) { return bar0 + 8 * (B1 + 6 + g2); };
-  auto vready = [&](int g2) { return bar0 + 8 * (B1 + 8 + g2); };
-  const uint32_t qready = bar0 + 8 * (B1 + 10), drain = bar0 + 8 * (B1 + 11);
+  const uint32_t qready = bar0 + 8 * (B1 + 8), drain = bar0 + 8 * (B1 + 9);
   uint8_t* misc = smem + Cfg::kOffMisc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   int* flag = reinterpret_cast<int*>(misc + 4);
   int* capexp = reinterpret_cast<int*>(misc + 8);
   int* uniform = reinterpret_cast<int*>(misc + 12);
   int* votes = reinterpret_cast<int*>(misc + 64);                // [2][2][4]
-  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [16] a warp's sequences
+  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [12] a warp's sequences
   float* colmax = reinterpret_cast<float*>(misc + 256);          // [2][4][NQC]
   float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
   float* colfac = colsum + 8 * NQC;                              // [NQC] 2^-k of rows of unlike size
@@ -196,20 +204,19 @@ __global__ void __launch_bounds__(512, 1)
     }
     for (int s = 0; s < VS; ++s) {
       mbar_init(vfull(s), 1);
-      mbar_init(vfree(s), 128);
+      mbar_init(vfree(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull(i), 1);
       mbar_init(sread(i), 128);
       mbar_init(pready(i), 128);
       mbar_init(pvdone(i), 1);
-      mbar_init(vready(i), 128);
     }
     mbar_init(qready, 256);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 14) {
+  if (warp == 10) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(512, 1)
   auto span_of = [&](int L) { return (long long)(tiles_of(L) + kUnitTiles) * p.hkv; };
   // Up to 32 sequences every warp scans by itself; else warp w first counts [w * chunk, (w + 1) *
   // chunk).
-  const int chunk = (p.batch + 511) / 512 * 32;
+  const int chunk = (p.batch + 383) / 384 * 32;
   long long all = 0;
   int first_chunk = 0;
   if (p.batch > 32) {
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(512, 1)
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
 #pragma unroll 1
-    for (int w = 0; w < 16; ++w) all += wsum[w];
+    for (int w = 0; w < 12; ++w) all += wsum[w];
   }
   long long upto = 0;    // this lane's sequence and those before it, of 32
   int mylen = 0;
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(512, 1)
     all = __shfl_sync(0xffffffffu, upto, 31);
   }
   if (cta == 0)   // lengths out of range are recorded once
-    for (int b = tid; b < p.batch; b += 512) {
+    for (int b = tid; b < p.batch; b += 384) {
       const int L = p.ctx_lens[b];
       if (L < 0 || L + T > cap) set_error(p.err, kErrDeviceFault);
     }
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(512, 1)
   if (begin < end) {
     int b0 = 0;
     if (p.batch > 32) {
-      for (; first_chunk < 15 && base + wsum[first_chunk] <= begin; ++first_chunk)
+      for (; first_chunk < 11 && base + wsum[first_chunk] <= begin; ++first_chunk)
         base += wsum[first_chunk];
       b0 = first_chunk * chunk;
     }
@@ -318,14 +325,14 @@ __global__ void __launch_bounds__(512, 1)
   };
   bool ok = true;
 
-  // 512 threads launch with 128 registers each: 2 x 128 x 192 + 2 x 128 x 64 are that.
-  if (warp >= 12) {
-    leave_registers<64>();
-    if (warp < 14) {
-      // ---------------------------------------------------------- producers: K (12), V (13)
+  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
+  if (warp >= 8) {
+    leave_registers<72>();
+    if (warp < 10) {
+      // ---------------------------------------------------------- producers: K (8), V (9)
       // Lane j < 8 loads page j of a tile; a page past the sequence's last is that one again (its
       // positions are masked).
-      const bool is_k = warp == 12;
+      const bool is_k = warp == 8;
       const int depth = is_k ? KS : VS;
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       const uint32_t ring = sbase + (is_k ? 0 : Cfg::kOffV);
@@ -398,37 +405,43 @@ __global__ void __launch_bounds__(512, 1)
           (void)mbar_wait_bounded(is_k ? kfull(s) : vfull(s), round & 1);
         }
       }
-    } else if (warp == 14) {
+    } else if (warp == 10) {
       // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t idS = idesc_e4m3(128, NS);
-      constexpr uint32_t idPV = idesc_f16_mn(D, NP);
+      constexpr uint32_t idS = idesc_f8(128, NS, 0, 0);
+      constexpr uint32_t idPV = idesc_f8(D, NP, 1, 1);
       const bool leader = elect_one();
-      // K and Q rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one; V' and
-      // P MN-major, P's rows of 128 or 64 bytes
-      const uint64_t dKQ = smem_desc(0, 16, 8 * D, D == 128 ? 2 : 4);
-      const uint64_t dV = smem_desc(0, 16384, 1024, 2);
-      const uint64_t dP = smem_desc(0, 16384, 8 * Cfg::kPRow, Cfg::kPRow == 128 ? 2 : 4);
+      // K, Q and V rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one (V
+      // MN-major: the stride leads from 8 positions to the next 8); P MN-major, rows of 128 bytes
+      const uint64_t dKQV = smem_desc(0, 16, 8 * D, D == 128 ? 2 : 4);
+      const uint64_t dP = smem_desc(0, 16384, 1024, 2);
       auto with_addr = [](uint64_t d, uint32_t a16) { return d | uint64_t(a16 & 0x3FFFu); };
       const uint32_t qb = (sbase + Cfg::kOffQ) >> 4;
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
       };
+      int vs = 0, vround = 0;
       // PV of the CTA's tile it (first: its group's first tile of the unit)
       auto issue_pv = [&](uint32_t it, bool first) -> bool {
         const int gg = it & 1;
-        if (!wait_all(vready(gg), (it >> 1) & 1)) return false;
+        if (!wait_all(vfull(vs), vround & 1)) return false;
         if (!wait_all(pready(gg), (it >> 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t vb = (sbase + Cfg::kOffV16 + gg * Cfg::kV16) >> 4;
+        const uint32_t vb = (sbase + Cfg::kOffV + vs * Cfg::kTile) >> 4;
         const uint32_t pb = (sbase + Cfg::kOffP + gg * Cfg::kP) >> 4;
         if (leader) {
+          constexpr int Passes = kSideP ? 1 : 3;
 #pragma unroll
-          for (int kp = 0; kp < 8; ++kp)
-            tc_mma(tmem + 2 * Cfg::kSCol + Cfg::kOCol * gg, with_addr(dV, vb + kp * 128),
-                   with_addr(dP, pb + kp * Cfg::kPRow), idPV, !first || kp > 0);
+          for (int j = 0; j < 4 * Passes; ++j)   // 32 positions an MMA
+            tc_mma_f8(tmem + 2 * Cfg::kSCol + Cfg::kOCol * gg, with_addr(dKQV, vb + (j & 3) * 2 * D),
+                      with_addr(dP, pb + (j >> 2) * 1024 + (j & 3) * 256), idPV, !first || j > 0);
           tc_commit(pvdone(gg));
+          tc_commit(vfree(vs));
         }
         __syncwarp();
+        if (++vs == VS) {
+          vs = 0;
+          ++vround;
+        }
         return true;
       };
       Place at = start;
@@ -449,8 +462,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int j = 0; j < Cfg::kPasses * (D / 32); ++j) {
               const int pass = j / (D / 32), ks = j % (D / 32);
-              tc_mma_e4m3(tmem + Cfg::kSCol * gg, with_addr(dKQ, kb + 2 * ks),
-                          with_addr(dKQ, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
+              tc_mma_f8(tmem + Cfg::kSCol * gg, with_addr(dKQV, kb + 2 * ks),
+                          with_addr(dKQV, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
             }
             tc_commit(sfull(gg));
             tc_commit(kfree(s));
@@ -472,62 +485,8 @@ __global__ void __launch_bounds__(512, 1)
       __syncwarp();
       (void)mbar_wait_bounded(drain, 0);
     }
-  } else if (warp >= 8) {
-    leave_registers<64>();
-    // ------------------------------------------------------------ V' (warps 8-11)
-    // Row i of a tile: its codes as f16, or zeros behind the window, where a code may be NaN.
-    const int i = tid & 127;
-    Place at = start;
-    uint32_t it = 0;
-    int s = 0, round = 0;
-    for (int tiles = at.here(); tiles > 0 && ok; tiles = at.here()) {
-      for (int t = 0; t < tiles; ++t, ++it) {
-        const int grp = it & 1;
-        // (a wait that ran out is seen by every thread of the four warps for itself)
-        if (!mbar_wait_bounded(vfull(s), round & 1) ||
-            (it >= 2 && !mbar_wait_bounded(pvdone(grp), ((it >> 1) - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        const uint8_t* vrow = smem + Cfg::kOffV + s * Cfg::kTile + i * D;
-        uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
-        const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
-        constexpr int B = 4;   // chunks in flight (loads ahead of the stores, which they might alias)
-        const bool behind = 128 * (at.t + t) + i > at.L + p.gamma;
-#pragma unroll
-        for (int c0 = 0; c0 < D / 16; c0 += B) {
-          uint4 v[B];
-#pragma unroll
-          for (int c = 0; c < B; ++c) {
-            v[c] = *reinterpret_cast<const uint4*>(vrow + (((c0 + c) ^ sw) << 4));
-            if (behind) v[c] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int c = 0; c < B; ++c) {
-            uint4 a, d;
-            f16x2_from_e4m3x4(v[c].x, a.x, a.y);
-            f16x2_from_e4m3x4(v[c].y, a.z, a.w);
-            f16x2_from_e4m3x4(v[c].z, d.x, d.y);
-            f16x2_from_e4m3x4(v[c].w, d.z, d.w);
-            uint8_t* dst = v16 + ((c0 + c) >> 2) * 16384;
-            const int cc = 2 * ((c0 + c) & 3);
-            *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
-          }
-        }
-        mbar_arrive(vfree(s));
-        fence_proxy_async_smem();
-        mbar_arrive(vready(grp));
-        if (++s == VS) {
-          s = 0;
-          ++round;
-        }
-      }
-      next_unit(at, tiles);
-    }
-    if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
   } else {
-    take_registers<192>();
+    take_registers<216>();
     // ------------------------------------------------------------ softmax groups (warps 0-7)
     const int grp = warp >> 2;                // 0: even tiles, 1: odd tiles
     const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
@@ -572,6 +531,19 @@ __global__ void __launch_bounds__(512, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = kSideS ? v8[e] + w8[e] : v8[e];
+    };
+    // O^T of columns 8 c .. 8 c + 7, the parts added
+    auto load_o = [&](int c, float (&v)[8]) {
+      tmem_ld8(tl + o_col + 8 * c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int part = 1; part < Cfg::kPCols / NQC; ++part) {
+        float w8[8];
+        tmem_ld8(tl + o_col + part * NQC + 8 * c, w8);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w8[e];
+      }
     };
     // of all columns, up to three chunks in flight
     auto load_all = [&](uint32_t at, float* y) {
@@ -866,19 +838,22 @@ __global__ void __launch_bounds__(512, 1)
           if (any) {
 #pragma unroll 1
             for (int c = 0; c < NQC / 8; ++c) {
-              float v8[8];
-              tmem_ld8(tl + o_col + 8 * c, v8);
-              tmem_ld_wait();
               const float4 a = fc[2 * c], d = fc[2 * c + 1];
-              v8[0] *= a.x;
-              v8[1] *= a.y;
-              v8[2] *= a.z;
-              v8[3] *= a.w;
-              v8[4] *= d.x;
-              v8[5] *= d.y;
-              v8[6] *= d.z;
-              v8[7] *= d.w;
-              tmem_st8(tl + o_col + 8 * c, v8);
+#pragma unroll
+              for (int part = 0; part < Cfg::kPCols / NQC; ++part) {
+                float v8[8];
+                tmem_ld8(tl + o_col + part * NQC + 8 * c, v8);
+                tmem_ld_wait();
+                v8[0] *= a.x;
+                v8[1] *= a.y;
+                v8[2] *= a.z;
+                v8[3] *= a.w;
+                v8[4] *= d.x;
+                v8[5] *= d.y;
+                v8[6] *= d.z;
+                v8[7] *= d.w;
+                tmem_st8(tl + o_col + part * NQC + 8 * c, v8);
+              }
             }
             tmem_st_wait();
           }
@@ -896,20 +871,43 @@ __global__ void __launch_bounds__(512, 1)
           }
           srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
         }
-        // P = 2^y, eight f16 in 16 bytes of position i's row of columns, swizzled (columns that fill
-        // up N are never read; their P may be anything)
-        uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
-        const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
+        // P = 2^y in three e5m2 parts (upper bytes of f16: cut, cut, rounded), eight columns of a part in
+        // eight bytes of position i's row, 16-byte chunks swizzled (columns that fill up N are never
+        // read; their P may be anything)
+        uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * 128;
 #pragma unroll
         for (int c = 0; c < NQC / 8; ++c) {
-          uint32_t w4[4];
+          uint32_t x[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float p0 = ex2(y[8 * c + e]), p1 = ex2(y[8 * c + e + 1]);
             ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
-            w4[e / 2] = pack_f16x2(p0, p1);
+            x[e / 2] = pack_f16x2(p0, p1);
           }
-          *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            if (part == 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] += 0x00800080u;   // (finite, >= 0: a carry rounds up)
+            }
+            const uint2 code = make_uint2(__byte_perm(x[0], x[1], 0x7531), __byte_perm(x[2], x[3], 0x7531));
+            if (part < 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = sub_f16x2(x[e], x[e] & 0xff00ff00u);
+            }
+            const int byte = kSideP ? part * NQC + 8 * c : part * 128 + 8 * c;
+            *reinterpret_cast<uint2*>(prow + (byte >> 7) * 16384 +
+                                      ((((byte & 127) >> 4) ^ (i & 7)) << 4) + (byte & 8)) = code;
+          }
+        }
+        if (pos > L + p.gamma) {
+          // a cache slot behind the window: zero its V row, whose codes may be NaN
+          const uint32_t vs = it % VS;
+          if (mbar_wait_bounded(vfull(vs), (it / VS) & 1)) {
+            uint4* vrow = reinterpret_cast<uint4*>(smem + Cfg::kOffV + vs * Cfg::kTile + i * D);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) vrow[c] = make_uint4(0, 0, 0, 0);
+          }
         }
         tc_fence_before();
         mbar_arrive(sread(grp));
@@ -960,8 +958,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
         for (int c = 0; c < NQC / 8; ++c) {
           float v8[8];
-          tmem_ld8(tl + o_col + 8 * c, v8);
-          tmem_ld_wait();
+          load_o(c, v8);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (dim >= 0) hand[(8 * c + e) * D + dim] = v8[e];
@@ -985,10 +982,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
         for (int c = 0; c < NQC / 8; ++c) {
           float v8[8] = {};
-          if (any0) {
-            tmem_ld8(tl + o_col + 8 * c, v8);
-            tmem_ld_wait();
-          }
+          if (any0) load_o(c, v8);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int n2 = 8 * c + e;
@@ -1070,7 +1064,7 @@ __global__ void __launch_bounds__(512, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 14) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
@@ -1088,7 +1082,7 @@ static cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(512, 1, 1);
+  cfg.blockDim = dim3(384, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

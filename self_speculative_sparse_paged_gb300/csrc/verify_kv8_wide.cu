@@ -1,0 +1,1136 @@
+// Verify attention with captured scores over the 8-bit cache, on the 5th-generation tensor cores
+// (compiled once per head_dim, VEGAS_KV8_D).
+//
+// The work is that of verify_tc.cu on half the bytes, laid out so that its length goes by what the
+// sequences hold, not by what their tables could: the 128-position tiles of all (sequence, KV
+// head) units stand in one row, and each CTA (one an SM) takes an equal run of it, whole units or
+// pieces, with the K/V stream going on from one unit to the next.  Sixteen warps:
+//   warps 0-7    two softmax groups of four warps that alternate tiles; a thread owns a position
+//                of a tile, and a head dimension of the group's O^T.  They also build the query operand
+//                of a unit and finish it.
+//   warps 8-11   turn V's codes into f16, a thread a position
+//   warps 12, 13 TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
+//   warp 14      issues the MMAs
+//
+//   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
+//       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
+//       parts (4 + 4 bits of bf16's 8), so the products are exact.  Captured scores take the
+//       summed captured query (fp32) in six parts, two and two 2^8 apart.  (kind::f8f6f4
+//       sums e4m3 products to fp32's precision here: 2.3e-7 of the terms' sum at worst, measured
+//       over random codes.)
+//   z = S 2^(e_k - k) scale log2(e) + e_v,  P = 2^(z - r) with r a reference for the column:
+//       e_k costs nothing (a thread's one factor), and 2^e_v goes into P instead of V.  Row sums
+//       take P 2^-e_v in fp32.
+//   O^T[D x N] += V'^T P^T   kind::f16, M = D: V' are V's codes as f16, exact (16 codes: one load,
+//       8 conversions, two stores).
+//
+// The two parts of the queries lie side by side in N (one pass over K; an MMA takes 45 clocks up
+// to N = 64 and 64 at 128) up to 40 columns, else they share an accumulator.
+// P <= 2^15 (f16 ends at 65504) and the largest P is 2^7 or more when r was raised, so P's grid
+// reaches 2^-31 below the largest.  e_v spans 120, so that no term that weighs in a row sum is lost to
+// fp32's smallest number (its P is at least 2^-121).
+//
+// A unit that one CTA covers is written by it; the pieces of a shared one go to the workspace
+// (fp32 O, maximum and sum of each row), and the CTA that arrives last on the unit's ticket merges
+// them.  No CTA waits for another.
+#include "attn_core.cuh"
+#include "kernels.h"
+#include "kv8.cuh"
+
+#ifndef VEGAS_KV8_D
+#error "compile with -DVEGAS_KV8_D=64 or -DVEGAS_KV8_D=128"
+#endif
+
+namespace vegas {
+
+namespace {
+constexpr float kTop = 15.f, kRaise = 7.f;   // log2 of the largest P, and of P at a raised reference
+constexpr int kCapParts = 6;
+// In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
+// reference and end), and a CTA takes part for kLeastRun tiles or more.
+constexpr int kUnitTiles = 3, kLeastRun = 4;
+constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
+
+// Instruction descriptors, fp32 accumulator: e4m3 by e4m3, K-major (K = 32); f16 by f16,
+// MN-major (K = 16).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int m, int n) {
+  return (1u << 4) | (1u << 15) | (1u << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// op over the warp's lanes of each of eight columns: lane l gets column l / 4's.  In three steps a
+// lane exchanges half of the columns it still holds for the other half of another lane's.
+template <class Op>
+__device__ __forceinline__ float reduce_chunk(const float* x, Op op) {
+  const int lane = threadIdx.x & 31;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = x[j];
+#pragma unroll
+  for (int w = 16; w >= 4; w >>= 1) {
+    const bool upper = lane & w;
+#pragma unroll
+    for (int j = 0; j < w / 4; ++j) {
+      const float give = upper ? v[j] : v[j + w / 4], keep = upper ? v[j + w / 4] : v[j];
+      v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
+    }
+  }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+}  // namespace
+
+template <int D, int NQC, bool CAPTURE>
+struct Kv8Cfg {
+  // S: [high parts | low parts | capture parts] side by side, or the two parts of NQC + 3 columns
+  // one after the other.
+  static constexpr bool kSideS = NQC <= 40;
+  static constexpr int kCap = CAPTURE ? (kSideS ? kCapParts : kCapParts / 2) : 0;
+  static constexpr int kCap0 = kSideS ? 2 * NQC : NQC;    // first capture column
+  static constexpr int NS = (kCap0 + kCap + 15) / 16 * 16;   // N of S
+  static constexpr int NP = (NQC + 15) / 16 * 16;     // N of PV
+  static constexpr int kTile = 128 * D;               // one K tile (and one V tile): 8 pages
+  // Ring slots (16 KB at head_dim 128, 8 KB at 64): as many as fit beside the rest.
+  static constexpr int KS = D == 64 ? 8 : 4;
+  static constexpr int VS = D == 64 ? 8 : NQC <= 32 ? 4 : 3;
+  static constexpr int kV16 = 128 * D * 2;            // a tile's V' [half][128][128 B], one a group
+  static constexpr int kPRow = NQC <= 32 ? 64 : 128;  // bytes of a position's P row
+  static constexpr int kP = 128 * kPRow;
+  static constexpr int kQ = NS * D;                   // Q^T operand, one a pass
+  static constexpr int kPasses = kSideS ? 1 : 2;
+  static constexpr int kSCol = (NS + 31) / 32 * 32, kOCol = (NP + 31) / 32 * 32;
+  static constexpr uint32_t kTmemCols =
+      2 * (kSCol + kOCol) <= 128 ? 128 : 2 * (kSCol + kOCol) <= 256 ? 256 : 512;
+  static_assert(2 * (kSCol + kOCol) <= 512, "tensor memory");
+  static constexpr int kOffV = KS * kTile;
+  static constexpr int kOffV16 = kOffV + VS * kTile;
+  static constexpr int kOffP = kOffV16 + 2 * kV16;
+  static constexpr int kOffQ = kOffP + 2 * kP;
+  static constexpr int kOffBar = kOffQ + kPasses * kQ;
+  static constexpr int kNumBars = 2 * KS + 2 * VS + 5 * 2 + 2;
+  static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
+  // misc: 16 words; votes[2][2][4]; warp sums[16] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
+  // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
+  static constexpr size_t kMisc = 64 + 64 + 128 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
+  static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(NQC * D * 4 <= 2 * kP, "a group's O^T handed over in P's buffers");
+  static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
+};
+
+// A place in the row of tiles: tile t of KV head g of sequence b.
+struct Place {
+  long long left;          // of the CTA's run from here on
+  int b, g, t, tiles, L;   // tiles: of each unit of sequence b; L: its context length
+  int pre;                 // of the run, before tile t
+  // tiles of the unit in the run; 0: the run is over
+  __device__ int here() const {
+    return left > pre ? int(min((long long)(tiles - t), left - pre)) : 0;
+  }
+};
+
+template <int D, int NQC, bool CAPTURE>
+__global__ void __launch_bounds__(512, 1)
+    verify_kv8_kernel(const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const VerifyKv8Params p) {
+  using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
+  constexpr int KS = Cfg::KS, VS = Cfg::VS, NS = Cfg::NS, NP = Cfg::NP;
+  constexpr bool kSideS = Cfg::kSideS;
+  static_assert(NQC % 8 == 0 && (D == 64 || D == 128), "columns, head_dim");
+
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + Cfg::kOffBar;
+  // barriers: K full/free (per K slot), V full/free (per V slot); S full, S read, P ready, PV done,
+  // V' ready (per softmax group); queries ready, MMA drain
+  auto kfull = [&](int s) { return bar0 + 8 * s; };
+  auto kfree = [&](int s) { return bar0 + 8 * (KS + s); };
+  auto vfull = [&](int s) { return bar0 + 8 * (2 * KS + s); };
+  auto vfree = [&](int s) { return bar0 + 8 * (2 * KS + VS + s); };
+  constexpr int B1 = 2 * KS + 2 * VS;
+  auto sfull = [&](int g2) { return bar0 + 8 * (B1 + g2); };
+  auto sread = [&](int g2) { return bar0 + 8 * (B1 + 2 + g2); };
+  auto pready = [&](int g2) { return bar0 + 8 * (B1 + 4 + g2); };
+  auto pvdone = [&](int g2) { return bar0 + 8 * (B1 + 6 + g2); };
+  auto vready = [&](int g2) { return bar0 + 8 * (B1 + 8 + g2); };
+  const uint32_t qready = bar0 + 8 * (B1 + 10), drain = bar0 + 8 * (B1 + 11);
+  uint8_t* misc = smem + Cfg::kOffMisc;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  int* flag = reinterpret_cast<int*>(misc + 4);
+  int* capexp = reinterpret_cast<int*>(misc + 8);
+  int* uniform = reinterpret_cast<int*>(misc + 12);
+  int* votes = reinterpret_cast<int*>(misc + 64);                // [2][2][4]
+  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [16] a warp's sequences
+  float* colmax = reinterpret_cast<float*>(misc + 256);          // [2][4][NQC]
+  float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
+  float* colfac = colsum + 8 * NQC;                              // [NQC] 2^-k of rows of unlike size
+  float* nrefs = colfac + NQC;                                   // [2][NQC] -reference
+  float* facs = nrefs + 2 * NQC;                                 // [2][NQC] factors of a raise
+  float* wgt = facs + 2 * NQC;                                   // [2][NQC] weights of the groups
+  float* colM = wgt + 2 * NQC;                                   // [NQC] maximum, and sum, of a piece
+  float* colL = colM + NQC;
+  int* tlim = reinterpret_cast<int*>(colL + NQC);                // [NQC]
+  int* rowexp = tlim + NQC;                                      // [NQC]
+  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffP);     // [8][D] parts of the captured sum
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int T = p.gamma + 1;
+  const int cap = p.max_pages * 16;
+
+  if (tid == 0) {
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kfree(s), 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(vfull(s), 1);
+      mbar_init(vfree(s), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sfull(i), 1);
+      mbar_init(sread(i), 128);
+      mbar_init(pready(i), 128);
+      mbar_init(pvdone(i), 1);
+      mbar_init(vready(i), 128);
+    }
+    mbar_init(qready, 256);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 14) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();   // (the barriers are initialised, and tensor memory is there)
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Nothing above reads or writes global memory, so it overlaps the tail of
+  // the previous kernel of the stream.
+  griddep_wait();
+
+  // ---- this CTA's run.  A sequence's units have ceil((L + T) / 128) tiles each.
+  auto length = [&](int b) {
+    const int L = p.ctx_lens[b];
+    return L < 0 || L + T > cap ? max(0, min(L, cap - T)) : L;   // (recorded below)
+  };
+  auto tiles_of = [&](int L) { return (L + T + 127) >> 7; };
+  auto span_of = [&](int L) { return (long long)(tiles_of(L) + kUnitTiles) * p.hkv; };
+  // Up to 32 sequences every warp scans by itself; else warp w first counts [w * chunk, (w + 1) *
+  // chunk).
+  const int chunk = (p.batch + 511) / 512 * 32;
+  long long all = 0;
+  int first_chunk = 0;
+  if (p.batch > 32) {
+    long long sum = 0;
+    for (int b = warp * chunk + lane; b < min(p.batch, (warp + 1) * chunk); b += 32)
+      sum += span_of(length(b));
+#pragma unroll
+    for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < 16; ++w) all += wsum[w];
+  }
+  long long upto = 0;    // this lane's sequence and those before it, of 32
+  int mylen = 0;
+  auto scan = [&](int b0) {
+    const int b = b0 + lane;
+    mylen = b < p.batch ? length(b) : 0;
+    upto = b < p.batch ? span_of(mylen) : 0;
+#pragma unroll
+    for (int o2 = 1; o2 < 32; o2 <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o2);
+      if (lane >= o2) upto += v;
+    }
+  };
+  if (p.batch <= 32) {
+    scan(0);
+    all = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (cta == 0)   // lengths out of range are recorded once
+    for (int b = tid; b < p.batch; b += 512) {
+      const int L = p.ctx_lens[b];
+      if (L < 0 || L + T > cap) set_error(p.err, kErrDeviceFault);
+    }
+  // CTAs that take part
+  const int n = int(max(1ll, min((long long)gridDim.x, all / kLeastRun)));
+  // (64-bit quotients take a few hundred clocks: 32-bit ones while they do)
+  const bool small = all < (1 << 24);   // (n < 2^8)
+  auto quotient = [&](long long a, long long d) {
+    return small ? (long long)(uint32_t(a) / uint32_t(d)) : a / d;
+  };
+  auto run_begin = [&](int c) { return quotient(c * all, n); };
+  const long long begin = cta < n ? run_begin(cta) : 0, end = cta < n ? run_begin(cta + 1) : 0;
+  // the CTA that holds place x: the last c with run_begin(c) <= x
+  auto cta_of = [&](long long x) { return int(quotient((x + 1) * n - 1, all)); };
+  Place start{end - begin, 0, 0, 0, 1, 0, 0};
+  long long base = 0;   // where sequence start.b begins
+  if (begin < end) {
+    int b0 = 0;
+    if (p.batch > 32) {
+      for (; first_chunk < 15 && base + wsum[first_chunk] <= begin; ++first_chunk)
+        base += wsum[first_chunk];
+      b0 = first_chunk * chunk;
+    }
+    for (;; b0 += 32) {
+      if (p.batch > 32) scan(b0);
+      const unsigned beyond = __ballot_sync(0xffffffffu, base + upto > begin);
+      if (beyond || b0 + 32 >= p.batch) {
+        const int l = beyond ? __ffs(beyond) - 1 : 31;   // (there is one: begin < end <= all)
+        start.b = min(b0 + l, p.batch - 1);
+        start.L = __shfl_sync(0xffffffffu, mylen, l);
+        base += __shfl_sync(0xffffffffu, upto, l) - span_of(start.L);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    start.tiles = tiles_of(start.L);
+    const int span = start.tiles + kUnitTiles;
+    start.g = int(quotient(begin - base, span));
+    const int off = int((begin - base) - (long long)start.g * span);   // in the unit's span
+    start.t = max(0, off - kUnitTiles);
+    start.pre = max(0, kUnitTiles - off);
+  }
+  auto next_unit = [&](Place& q, int done) {   // (done: tiles of the unit that were here)
+    q.left -= q.pre + done;
+    q.t = 0;
+    q.pre = kUnitTiles;
+    if (++q.g == p.hkv) {
+      q.g = 0;
+      if (q.left > 0) {
+        q.L = length(++q.b);
+        q.tiles = tiles_of(q.L);
+      }
+    }
+  };
+  bool ok = true;
+
+  // 512 threads launch with 128 registers each: 2 x 128 x 192 + 2 x 128 x 64 are that.
+  if (warp >= 12) {
+    leave_registers<64>();
+    if (warp < 14) {
+      // ---------------------------------------------------------- producers: K (12), V (13)
+      // Lane j < 8 loads page j of a tile; a page past the sequence's last is that one again (its
+      // positions are masked).
+      const bool is_k = warp == 12;
+      const int depth = is_k ? KS : VS;
+      const CUtensorMap* map = is_k ? &kmap : &vmap;
+      const uint32_t ring = sbase + (is_k ? 0 : Cfg::kOffV);
+      // The cache is streamed once per pass: its lines leave L2 first.
+      const uint64_t stream_pol = l2_evict_first_policy();
+      const int j8 = lane & 7;
+      Place ahead = start;
+      int rest = ahead.here(), done = rest;   // tiles of the unit still to be requested, and of them all
+      // a tile's table entry, requested four tiles before its use, and its KV head (-1: no tile)
+      int held[4], head[4];
+      auto request = [&](int j) {
+        held[j] = 0;
+        head[j] = -1;
+        if (rest > 0) {
+          const int page = min(8 * ahead.t + j8, (ahead.L + T - 1) >> 4);
+          held[j] = __ldg(&p.block_table[size_t(ahead.b) * p.max_pages + page]);
+          head[j] = ahead.g;
+          ++ahead.t;
+          if (--rest == 0) {
+            next_unit(ahead, done);
+            rest = done = ahead.here();
+          }
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < 4; ++j) request(j);
+      int issued = 0;
+      int s = 0, round = 0;
+      bool more = true;
+      while (more && ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (head[j] < 0) {
+            more = false;
+            break;
+          }
+          const uint32_t full = is_k ? kfull(s) : vfull(s);
+          const uint32_t freed = is_k ? kfree(s) : vfree(s);
+          if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(freed, (round - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          int phys = held[j];
+          const int g = head[j];
+          request(j);
+          if (phys < 0 || phys >= p.num_pages) {
+            set_error(p.err, kErrDeviceFault);
+            phys = 0;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kTile);
+          __syncwarp();
+          if (lane < 8)
+            tma_load_2d_hint(ring + s * Cfg::kTile + j8 * 16 * D, map, 0, (phys * p.hkv + g) * 16,
+                             full, stream_pol);
+          __syncwarp();
+          if (issued < depth) ++issued;
+          if (++s == depth) {
+            s = 0;
+            ++round;
+          }
+        }
+      }
+      if (!ok) {   // what is in flight lands before the CTA ends
+        if (lane == 0) set_error(p.err, kErrDeviceTimeout);
+        for (int k = 0; k < issued; ++k) {
+          if (--s < 0) {
+            s = depth - 1;
+            --round;
+          }
+          (void)mbar_wait_bounded(is_k ? kfull(s) : vfull(s), round & 1);
+        }
+      }
+    } else if (warp == 14) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t idS = idesc_e4m3(128, NS);
+      constexpr uint32_t idPV = idesc_f16_mn(D, NP);
+      const bool leader = elect_one();
+      // K and Q rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one; V' and
+      // P MN-major, P's rows of 128 or 64 bytes
+      const uint64_t dKQ = smem_desc(0, 16, 8 * D, D == 128 ? 2 : 4);
+      const uint64_t dV = smem_desc(0, 16384, 1024, 2);
+      const uint64_t dP = smem_desc(0, 16384, 8 * Cfg::kPRow, Cfg::kPRow == 128 ? 2 : 4);
+      auto with_addr = [](uint64_t d, uint32_t a16) { return d | uint64_t(a16 & 0x3FFFu); };
+      const uint32_t qb = (sbase + Cfg::kOffQ) >> 4;
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+      };
+      // PV of the CTA's tile it (first: its group's first tile of the unit)
+      auto issue_pv = [&](uint32_t it, bool first) -> bool {
+        const int gg = it & 1;
+        if (!wait_all(vready(gg), (it >> 1) & 1)) return false;
+        if (!wait_all(pready(gg), (it >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint32_t vb = (sbase + Cfg::kOffV16 + gg * Cfg::kV16) >> 4;
+        const uint32_t pb = (sbase + Cfg::kOffP + gg * Cfg::kP) >> 4;
+        if (leader) {
+#pragma unroll
+          for (int kp = 0; kp < 8; ++kp)
+            tc_mma(tmem + 2 * Cfg::kSCol + Cfg::kOCol * gg, with_addr(dV, vb + kp * 128),
+                   with_addr(dP, pb + kp * Cfg::kPRow), idPV, !first || kp > 0);
+          tc_commit(pvdone(gg));
+        }
+        __syncwarp();
+        return true;
+      };
+      Place at = start;
+      uint32_t it = 0;
+      int s = 0, round = 0, seg = 0;
+      for (int tiles = at.here(); tiles > 0 && ok; tiles = at.here()) {
+        if (!wait_all(qready, seg++ & 1)) {
+          ok = false;
+          break;
+        }
+        for (int t = 0; t < tiles && ok; ++t, ++it) {
+          const int gg = it & 1;
+          if (!wait_all(kfull(s), round & 1)) { ok = false; break; }
+          if (it >= 2 && !wait_all(sread(gg), ((it >> 1) - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t kb = (sbase + s * Cfg::kTile) >> 4;
+          if (leader) {
+#pragma unroll
+            for (int j = 0; j < Cfg::kPasses * (D / 32); ++j) {
+              const int pass = j / (D / 32), ks = j % (D / 32);
+              tc_mma_e4m3(tmem + Cfg::kSCol * gg, with_addr(dKQ, kb + 2 * ks),
+                          with_addr(dKQ, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
+            }
+            tc_commit(sfull(gg));
+            tc_commit(kfree(s));
+          }
+          __syncwarp();
+          if (++s == KS) {
+            s = 0;
+            ++round;
+          }
+          if (t >= 1 && !issue_pv(it - 1, t - 1 < 2)) ok = false;
+        }
+        // the unit's last PV, before the next unit's queries are waited for
+        if (ok && !issue_pv(it - 1, tiles - 1 < 2)) ok = false;
+        next_unit(at, tiles);
+      }
+      if (!ok && leader) set_error(p.err, kErrDeviceTimeout);
+      // every MMA issued has completed before tensor memory is released
+      if (leader) tc_commit(drain);
+      __syncwarp();
+      (void)mbar_wait_bounded(drain, 0);
+    }
+  } else if (warp >= 8) {
+    leave_registers<64>();
+    // ------------------------------------------------------------ V' (warps 8-11)
+    // Row i of a tile: its codes as f16, or zeros behind the window, where a code may be NaN.
+    const int i = tid & 127;
+    Place at = start;
+    uint32_t it = 0;
+    int s = 0, round = 0;
+    for (int tiles = at.here(); tiles > 0 && ok; tiles = at.here()) {
+      for (int t = 0; t < tiles; ++t, ++it) {
+        const int grp = it & 1;
+        // (a wait that ran out is seen by every thread of the four warps for itself)
+        if (!mbar_wait_bounded(vfull(s), round & 1) ||
+            (it >= 2 && !mbar_wait_bounded(pvdone(grp), ((it >> 1) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* vrow = smem + Cfg::kOffV + s * Cfg::kTile + i * D;
+        uint8_t* v16 = smem + Cfg::kOffV16 + grp * Cfg::kV16 + i * 128;
+        const int sw = D == 128 ? i & 7 : (i >> 1) & 3;
+        constexpr int B = 4;   // chunks in flight (loads ahead of the stores, which they might alias)
+        const bool behind = 128 * (at.t + t) + i > at.L + p.gamma;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 16; c0 += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int c = 0; c < B; ++c) {
+            v[c] = *reinterpret_cast<const uint4*>(vrow + (((c0 + c) ^ sw) << 4));
+            if (behind) v[c] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int c = 0; c < B; ++c) {
+            uint4 a, d;
+            f16x2_from_e4m3x4(v[c].x, a.x, a.y);
+            f16x2_from_e4m3x4(v[c].y, a.z, a.w);
+            f16x2_from_e4m3x4(v[c].z, d.x, d.y);
+            f16x2_from_e4m3x4(v[c].w, d.z, d.w);
+            uint8_t* dst = v16 + ((c0 + c) >> 2) * 16384;
+            const int cc = 2 * ((c0 + c) & 3);
+            *reinterpret_cast<uint4*>(dst + ((cc ^ (i & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(dst + (((cc + 1) ^ (i & 7)) << 4)) = d;
+          }
+        }
+        mbar_arrive(vfree(s));
+        fence_proxy_async_smem();
+        mbar_arrive(vready(grp));
+        if (++s == VS) {
+          s = 0;
+          ++round;
+        }
+      }
+      next_unit(at, tiles);
+    }
+    if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
+  } else {
+    take_registers<192>();
+    // ------------------------------------------------------------ softmax groups (warps 0-7)
+    const int grp = warp >> 2;                // 0: even tiles, 1: odd tiles
+    const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
+    const int i = 32 * q4 + lane;             // tile position owned
+    // head dimension owned: M = 64 puts 16 rows in each quarter of the lanes
+    const int dim = D == 128 ? i : lane < 16 ? 16 * q4 + lane : -1;
+    const uint32_t tl = tmem + (uint32_t(32 * q4) << 16);
+    const uint32_t s_col = Cfg::kSCol * grp, o_col = 2 * Cfg::kSCol + Cfg::kOCol * grp;
+    // Column references r (P = 2^(z - r)) are kept as -r in shared memory, up to 32 columns in
+    // registers too; 0 while `hollow` says that the column has seen no unmasked logit.
+    constexpr bool kSmemRef = NQC > 32;
+    constexpr int QPER = NQC / 8;
+    uint8_t* qs = smem + Cfg::kOffQ;
+    // Element (n, k) of a query part: n * D + the 16-byte chunk k / 16 swizzled with the row.
+    auto qoff = [](int n2, int k) {
+      const int c = k >> 4, sw = D == 128 ? n2 & 7 : (n2 >> 1) & 3;
+      return n2 * D + ((c ^ sw) << 4) + (k & 15);
+    };
+    const __nv_bfloat16* qbase = reinterpret_cast<const __nv_bfloat16*>(p.q);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
+    float* nrg = nrefs + grp * NQC;
+    // (pages outside the pool: the producers record and clamp them)
+    auto load_page = [&](const Place& u, int t) {   // volatile, here and below: the compiler may not
+      const int page = min(8 * t + (i >> 4), (u.L + T - 1) >> 4);   // move the loads down to their uses
+      int v;
+      asm volatile("ld.global.nc.s32 %0, [%1];"
+                   : "=r"(v)
+                   : "l"(p.block_table + size_t(u.b) * p.max_pages + page));
+      return v;
+    };
+    auto load_scale = [&](const uint8_t* scales, int phys, int g) {
+      uint32_t v;
+      const size_t block = size_t(phys < 0 || phys >= p.num_pages ? 0 : phys) * p.hkv + g;
+      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(scales + block));
+      return v;
+    };
+    // S of columns 8 c .. 8 c + 7, the parts added
+    auto load_chunk = [&](uint32_t at, int c, float* y) {
+      float v8[8], w8[8];
+      tmem_ld8(at + 8 * c, v8);
+      if constexpr (kSideS) tmem_ld8(at + NQC + 8 * c, w8);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = kSideS ? v8[e] + w8[e] : v8[e];
+    };
+    // of all columns, up to three chunks in flight
+    auto load_all = [&](uint32_t at, float* y) {
+#pragma unroll
+      for (int c0 = 0; c0 < NQC / 8; c0 += 3) {
+        float v8[3][8], w8[3][8];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (c0 + c >= NQC / 8) continue;
+          tmem_ld8(at + 8 * (c0 + c), v8[c]);
+          if constexpr (kSideS) tmem_ld8(at + NQC + 8 * (c0 + c), w8[c]);
+        }
+        if (kSideS || c0 + 3 >= NQC / 8) tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (c0 + c >= NQC / 8) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[8 * (c0 + c) + e] = kSideS ? v8[c][e] + w8[c][e] : v8[c][e];
+        }
+      }
+    };
+
+    Place at = start;
+    long long unit0 = base + (long long)start.g * (start.tiles + kUnitTiles);   // its span's begin
+    uint32_t it0 = 0;             // the CTA's tile with which the unit begins
+    for (int tiles = at.here(); tiles > 0; tiles = at.here()) {
+      const int L = at.L, g = at.g, b = at.b;
+      const uint32_t first = it0 + ((it0 ^ uint32_t(grp)) & 1);   // this group's first tile
+
+      // ---------------------------------------------------------- the unit's queries
+      int phys1 = 0;
+      uint32_t ekb, evb;
+      {
+        const int phys0 = load_page(at, at.t + int(first - it0));
+        phys1 = load_page(at, at.t + int(first - it0) + 2);
+        uint32_t qreg[QPER][D / 64];
+#pragma unroll
+        for (int u = 0; u < QPER; ++u) {
+          const int n2 = warp + 8 * u, t = n2 / p.group, hl = n2 - t * p.group;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            qreg[u][h] = n2 < p.nq ? reinterpret_cast<const uint32_t*>(
+                                         qbase + ((size_t(b) * T + t) * p.hq + g * p.group + hl) * D)
+                                         [32 * h + lane]
+                                   : 0u;
+        }
+        // a row's exponent: its largest element lies in [2^n, 2^(n + 1))
+#pragma unroll
+        for (int u = 0; u < QPER; ++u) {
+          uint32_t most = 0;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) most = __vmaxu2(most, qreg[u][h] & 0x7fff7fffu);
+          most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+          if (lane == 0) rowexp[warp + 8 * u] = most ? max(-100, int(most >> 7) - 127) : -1000;
+        }
+        ekb = load_scale(p.k_scale, phys0, g);
+        evb = load_scale(p.v_scale, phys0, g);
+        if (CAPTURE) {
+          // the captured query, summed over its rows and heads: this warp's rows
+          float acc[D / 64][2] = {};
+#pragma unroll
+          for (int u = 0; u < QPER; ++u) {
+            const int n2 = warp + 8 * u;
+            if (n2 < p.nq && ((p.row_mask >> (n2 / p.group)) & 1u)) {
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h) {
+                acc[h][0] += __uint_as_float(qreg[u][h] << 16);
+                acc[h][1] += __uint_as_float(qreg[u][h] & 0xffff0000u);
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<float2*>(qsum + warp * D + 64 * h + 2 * lane) =
+                make_float2(acc[h][0], acc[h][1]);
+        }
+        if (tid < NQC) tlim[tid] = tid < p.nq ? tid / p.group : -1;
+        named_bar(3, 256);
+        // One exponent for all rows while they are within 2^4 of each other (a part's grid then
+        // reaches 2^-13 of the smallest row's largest element, and 2^-17 of the unit's), else one a
+        // row.
+        int most = -1000, least = 1000;
+        for (int n2 = lane; n2 < NQC; n2 += 32) {
+          const int e = rowexp[n2];
+          most = max(most, e);
+          if (e > -1000) least = min(least, e);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
+        const bool one = most - least <= 4;
+        if (most == -1000) most = 0;
+        // The next e4m3 part of (x0, x1), |x| < 2^8, to row n2 of a pass; x keeps the rest.
+        auto put_part = [&](int pass, int n2, int k, float& x0, float& x1) {
+          const uint32_t c = e4m3x2_from_f32(x0, x1);
+          *reinterpret_cast<uint16_t*>(qs + pass * Cfg::kQ + qoff(n2, k)) = uint16_t(c);
+          uint32_t h, unused;
+          f16x2_from_e4m3x4(c, h, unused);
+          const float2 v = f32x2_from_f16x2(h);
+          x0 -= v.x;
+          x1 -= v.y;
+        };
+#pragma unroll
+        for (int u = 0; u < QPER; ++u) {
+          const int n2 = warp + 8 * u;
+          const int e = rowexp[n2], k = 7 - (one ? most : e == -1000 ? 0 : e);
+          const float f = two_to(k);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            float x0 = __uint_as_float(qreg[u][h] << 16) * f;
+            float x1 = __uint_as_float(qreg[u][h] & 0xffff0000u) * f;
+            put_part(0, n2, 64 * h + 2 * lane, x0, x1);
+            put_part(kSideS ? 0 : 1, kSideS ? NQC + n2 : n2, 64 * h + 2 * lane, x0, x1);
+          }
+          if (lane == 0) colfac[n2] = one ? 1.f : two_to(-k);
+        }
+        if (CAPTURE && warp == 7) {
+          float x[D / 64][2];
+          float top = 0.f;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 w = *reinterpret_cast<const float2*>(qsum + j * D + 64 * h + 2 * lane);
+              v.x += w.x;
+              v.y += w.y;
+            }
+            x[h][0] = v.x;
+            x[h][1] = v.y;
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+          const int k = 7 - max(-100, int(bits >> 23) - 127);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            float x0 = x[h][0] * two_to(k), x1 = x[h][1] * two_to(k);
+#pragma unroll
+            for (int j = 0; j < kCapParts; ++j) {
+              put_part(kSideS ? 0 : j & 1, Cfg::kCap0 + (kSideS ? j : j >> 1), 64 * h + 2 * lane, x0, x1);
+              if (j & 1) {   // two parts leave less than 2^-8 of the largest: the next start 2^8 lower
+                x0 *= 256.f;
+                x1 *= 256.f;
+              }
+            }
+          }
+          if (lane == 0) *capexp = -k;
+        }
+        if (warp == 6) {   // rows that fill up N
+          constexpr int row = Cfg::kCap0 + Cfg::kCap;
+          for (int j = lane; j < (NS - row) * D / 4; j += 32)
+#pragma unroll
+            for (int pass = 0; pass < Cfg::kPasses; ++pass)
+              reinterpret_cast<uint32_t*>(qs + pass * Cfg::kQ + row * D)[j] = 0;
+          if (lane == 0) *uniform = one ? most - 7 : kMixed;
+        }
+        if (i < NQC) nrg[i] = 0.f;
+        // Generic-proxy writes of Q must be visible to the tensor cores (async proxy).
+        fence_proxy_async_smem();
+        mbar_arrive(qready);
+        named_bar(3, 256);   // (what was written above is read by all)
+      }
+
+      // ---------------------------------------------------------- its tiles
+      float nr[kSmemRef ? 2 : NQC];
+      uint64_t ls2[NQC / 2];   // row sums, two columns each
+#pragma unroll
+      for (int n2 = 0; n2 < NQC; ++n2) {
+        if constexpr (!kSmemRef) nr[n2] = 0.f;
+        if (n2 % 2 == 0) ls2[n2 / 2] = 0;
+      }
+      uint64_t hollow = NQC == 64 ? ~0ull : (1ull << NQC) - 1;   // columns without a reference
+      const int uni = *uniform;
+      const bool mixed = uni == kMixed;
+      const float scale0 = mixed ? p.scale_log2 : p.scale_log2 * two_to(uni);
+      const float cap_scale = CAPTURE ? p.scale * two_to(*capexp) : 0.f;
+      float* srow = CAPTURE ? p.scores + (size_t(b) * p.hkv + g) * p.score_stride : nullptr;
+      int Lcap = L;
+      if (CAPTURE && L > p.score_stride) {
+        if (i == 0 && grp == 0) set_error(p.err, kErrDeviceFault);
+        Lcap = p.score_stride;
+      }
+      bool any = false;   // this group has a tile of the unit
+      // A failed (timed-out) wait is carried to the group vote below, so the 128
+      // threads of a group always leave the loop together.
+      for (uint32_t it = first; it < it0 + uint32_t(tiles); it += 2) {
+        const uint32_t k = it >> 1;
+        const int t = at.t + int(it - it0);
+        const int pos = 128 * t + i;
+        // this position's scales; the next tile's are requested, and the page after that
+        const int e_k = kv8_exponent(uint8_t(ekb)), e_v = kv8_exponent(uint8_t(evb));
+        ekb = load_scale(p.k_scale, phys1, g);
+        evb = load_scale(p.v_scale, phys1, g);
+        phys1 = load_page(at, t + 4);
+        const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
+        const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
+        // S of this tile follows PV of the group's last tile in the tensor pipe: P's buffer is free
+        // then, and O^T may be rescaled
+        const bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
+        tc_fence_after();
+        // z of columns 8 c .. 8 c + 7 less their references (y: S in, z out)
+        auto z_chunk = [&](int c, float* y) {
+          if (mixed) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= colfac[8 * c + e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            float4 r4;
+            if constexpr (kSmemRef)
+              r4 = reinterpret_cast<const float4*>(nrg)[2 * c + e / 4];
+            else
+              r4 = make_float4(nr[8 * c + e], nr[8 * c + e + 1], nr[8 * c + e + 2], nr[8 * c + e + 3]);
+            const uint64_t a =
+                add_f32x2(fma_f32x2(pair_f32(y[e], y[e + 1]), f2, add2), pair_f32(r4.x, r4.y));
+            const uint64_t d =
+                add_f32x2(fma_f32x2(pair_f32(y[e + 2], y[e + 3]), f2, add2), pair_f32(r4.z, r4.w));
+            unpair_f32(a, y[e], y[e + 1]);
+            unpair_f32(d, y[e + 2], y[e + 3]);
+          }
+          if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (pos > L + tlim[8 * c + e]) y[e] = -INFINITY;
+          }
+        };
+        float y[NQC];
+        float cx[8] = {};   // the capture columns
+        bool left = false, forced = hollow != 0;
+        while (true) {
+          bool need = forced;
+          if (okt) {
+            if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+            load_all(tl + s_col, y);
+            float ym = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NQC / 8; ++c) {
+              z_chunk(c, y + 8 * c);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) ym = fmaxf(fmaxf(ym, y[8 * c + e]), y[8 * c + e + 1]);
+            }
+            need |= ym > kTop;
+          }
+          const bool all_ok = __all_sync(0xffffffffu, okt);
+          if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
+          if (!named_bar_any(1 + grp, 128, need || !okt)) break;
+          const int* vt = votes + (k & 1) * 8 + grp * 4;
+          if (vt[0] | vt[1] | vt[2] | vt[3]) {
+            left = true;
+            break;
+          }
+          // Raise: column maxima over the group's 128 positions
+          float* cm = colmax + grp * 4 * NQC;
+#pragma unroll
+          for (int c = 0; c < NQC / 8; ++c) {
+            const float top = reduce_chunk(y + 8 * c, [](float a, float d) { return fmaxf(a, d); });
+            if ((lane & 3) == 0) cm[q4 * NQC + 8 * c + (lane >> 2)] = top;
+          }
+          named_bar(1 + grp, 128);
+          // a column's new reference, at least kRaise below its largest z (cm is relative to the old
+          // one), and the factor that its sums take
+          if (i < NQC) {
+            const float nro = nrg[i];
+            const float top = fmaxf(fmaxf(cm[i], cm[NQC + i]), fmaxf(cm[2 * NQC + i], cm[3 * NQC + i]));
+            const float old = ((hollow >> i) & 1) ? kEmptyMax : -nro;
+            const float now = fmaxf(old, top - nro - kRaise);
+            facs[grp * NQC + i] = ex2(old - now);
+            nrg[i] = now == kEmptyMax ? 0.f : -now;
+            colmax[grp * 4 * NQC + i] = now;   // (its own column: read above by this thread alone)
+          }
+          named_bar(1 + grp, 128);
+          // (columns with masked logits only stay without one until the next tile)
+          hollow = 0;
+#pragma unroll
+          for (int c0 = 0; c0 < NQC; c0 += 32) {
+            const bool still = c0 + lane < NQC && colmax[grp * 4 * NQC + c0 + lane] == kEmptyMax;
+            hollow |= uint64_t(__ballot_sync(0xffffffffu, still)) << c0;
+          }
+          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC);
+#pragma unroll
+          for (int c = 0; c < NQC / 4; ++c) {
+            const float4 v = fc[c];
+            ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
+            ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
+            if constexpr (!kSmemRef) {
+              const float4 r4 = reinterpret_cast<const float4*>(nrg)[c];
+              nr[4 * c] = r4.x;
+              nr[4 * c + 1] = r4.y;
+              nr[4 * c + 2] = r4.z;
+              nr[4 * c + 3] = r4.w;
+            }
+          }
+          if (any) {
+#pragma unroll 1
+            for (int c = 0; c < NQC / 8; ++c) {
+              float v8[8];
+              tmem_ld8(tl + o_col + 8 * c, v8);
+              tmem_ld_wait();
+              const float4 a = fc[2 * c], d = fc[2 * c + 1];
+              v8[0] *= a.x;
+              v8[1] *= a.y;
+              v8[2] *= a.z;
+              v8[3] *= a.w;
+              v8[4] *= d.x;
+              v8[5] *= d.y;
+              v8[6] *= d.z;
+              v8[7] *= d.w;
+              tmem_st8(tl + o_col + 8 * c, v8);
+            }
+            tmem_st_wait();
+          }
+          forced = false;
+          named_bar(1 + grp, 128);   // colmax and the factors are read
+        }
+        if (left) {
+          ok = false;
+          break;
+        }
+        if (CAPTURE && pos < Lcap) {
+          if constexpr (kSideS) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
+          }
+          srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
+        }
+        // P = 2^y, eight f16 in 16 bytes of position i's row of columns, swizzled (columns that fill
+        // up N are never read; their P may be anything)
+        uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * Cfg::kPRow;
+        const int psw = Cfg::kPRow == 128 ? i & 7 : (i >> 1) & 3;
+#pragma unroll
+        for (int c = 0; c < NQC / 8; ++c) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float p0 = ex2(y[8 * c + e]), p1 = ex2(y[8 * c + e + 1]);
+            ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
+            w4[e / 2] = pack_f16x2(p0, p1);
+          }
+          *reinterpret_cast<uint4*>(prow + ((c ^ psw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        tc_fence_before();
+        mbar_arrive(sread(grp));
+        fence_proxy_async_smem();
+        mbar_arrive(pready(grp));
+        any = true;
+      }
+
+      // ---------------------------------------------------------- the unit's end
+      // row sums over the group's 128 positions
+#pragma unroll
+      for (int c = 0; c < NQC / 8; ++c) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) unpair_f32(ls2[4 * c + e / 2], v[e], v[e + 1]);
+        const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
+        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
+      }
+      // The group's last PV completes its O^T; group 1 hands its own over in P's buffers, once both
+      // groups' PVs have read them.
+      if (any && ok) {
+        const uint32_t last = it0 + uint32_t(tiles) - 1 - ((it0 + uint32_t(tiles) - 1 - uint32_t(grp)) & 1);
+        if (!mbar_wait_bounded(pvdone(grp), (last >> 1) & 1)) ok = false;
+      }
+      tc_fence_after();
+      if (i < NQC && ((hollow >> i) & 1)) colmax[grp * 4 * NQC + i] = kEmptyMax;
+      else if (i < NQC) colmax[grp * 4 * NQC + i] = -nrg[i];
+      tc_fence_before();
+      if (named_bar_any(3, 256, !ok)) {   // both groups leave together
+        if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
+        break;
+      }
+      // the piece's maximum and sum of a column, and the weights of the two groups' states
+      if (tid < NQC) {
+        const float m0 = colmax[tid], m1 = colmax[4 * NQC + tid], M = fmaxf(m0, m1);
+        const float w0 = ex2(m0 - M), w1 = ex2(m1 - M);
+        const float* cs = colsum + tid;
+        wgt[tid] = w0;
+        wgt[NQC + tid] = w1;
+        colM[tid] = M;
+        colL[tid] = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
+                    w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
+      }
+      float* hand = reinterpret_cast<float*>(smem + Cfg::kOffP);   // [NQC][D]
+      const bool any1 = tiles > 1 || (it0 & 1);                    // group 1 has a tile
+      const bool any0 = tiles > 1 || !(it0 & 1);
+      if (grp == 1 && any1) {
+#pragma unroll 1
+        for (int c = 0; c < NQC / 8; ++c) {
+          float v8[8];
+          tmem_ld8(tl + o_col + 8 * c, v8);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (dim >= 0) hand[(8 * c + e) * D + dim] = v8[e];
+        }
+        tc_fence_before();
+      }
+      named_bar(3, 256);
+      // the CTAs that hold tiles of the unit
+      const long long tile0 = unit0 + kUnitTiles;
+      const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
+      const size_t unit = size_t(b) * p.hkv + g;
+      auto out_row = [&](int n2) {
+        const int t = n2 / p.group, hl = n2 - t * p.group;
+        return out + ((size_t(b) * T + t) * p.hq + g * p.group + hl) * D;
+      };
+      // Workspace slots: 2 c for the unit that CTA c's run begins in or with, 2 c + 1 for its last one
+      // where that is another; of a unit's CTAs only the first can have it as its last.
+      const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
+      const size_t slot = cta == c0 ? slot0 : 2 * cta;
+      if (grp == 0) {
+#pragma unroll 1
+        for (int c = 0; c < NQC / 8; ++c) {
+          float v8[8] = {};
+          if (any0) {
+            tmem_ld8(tl + o_col + 8 * c, v8);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int n2 = 8 * c + e;
+            if (dim < 0 || n2 >= p.nq) continue;
+            float v = any0 ? v8[e] * wgt[n2] : 0.f;
+            if (any1) v = fmaf(hand[n2 * D + dim], wgt[NQC + n2], v);
+            if (c0 == c1)
+              out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
+            else
+              p.part_o[(slot * p.nq + n2) * D + dim] = v;
+          }
+        }
+        tc_fence_before();
+        if (c0 != c1 && tid < p.nq)
+          reinterpret_cast<float2*>(p.part_ml)[slot * p.nq + tid] = make_float2(colM[tid], colL[tid]);
+      }
+      if (c0 != c1) {
+        named_bar(3, 256);
+        if (tid == 0) {   // (the fence covers what the barrier made visible to this thread)
+          __threadfence();
+          *flag = atomicAdd(&p.tickets[unit], 1) == c1 - c0;
+          __threadfence();
+        }
+        named_bar(3, 256);
+        if (*flag) {
+          // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m).
+          const int pieces = c1 - c0 + 1;
+          auto slot_of = [&](int c) { return size_t(c == 0 ? slot0 : 2 * (c0 + c)); };
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+#pragma unroll 1
+          for (int n2 = warp; n2 < p.nq; n2 += 8) {
+            float M = kEmptyMax, sum = 0.f;
+#pragma unroll 1
+            for (int c = lane; c < pieces; c += 32) {
+              const float2 v = __ldcg(ml + slot_of(c) * p.nq + n2);
+              const float now = fmaxf(M, v.x);
+              sum = sum * ex2(M - now) + v.y * ex2(v.x - now);
+              M = now;
+            }
+            float top = M;
+#pragma unroll
+            for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+            sum *= ex2(M - top);
+#pragma unroll
+            for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+            if (lane == 0) {
+              colM[n2] = top;
+              colL[n2] = 1.f / sum;
+            }
+          }
+          named_bar(3, 256);
+#pragma unroll 1
+          for (int e = tid; e < p.nq * (D / 4); e += 256) {
+            const int n2 = e / (D / 4), d = 4 * (e - n2 * (D / 4));
+            const float M = colM[n2], inv = colL[n2];
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = 0; c < pieces; ++c) {
+              const size_t row = slot_of(c) * p.nq + n2;
+              const float w = ex2(__ldcg(&p.part_ml[2 * row]) - M);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
+              acc.x += w * v.x;
+              acc.y += w * v.y;
+              acc.z += w * v.z;
+              acc.w += w * v.w;
+            }
+            *reinterpret_cast<uint2*>(out_row(n2) + d) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          }
+          if (tid == 0) p.tickets[unit] = 0;
+        }
+      }
+      named_bar(3, 256);   // the buffers and columns are free again
+      unit0 += at.tiles + kUnitTiles;
+      it0 += uint32_t(tiles);
+      next_unit(at, tiles);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 14) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+template <int D, int NQC, bool CAP>
+static cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              const VerifyKv8Params& p, int grid, cudaStream_t stream) {
+  using Cfg = Kv8Cfg<D, NQC, CAP>;
+  static std::atomic<uint32_t> configured{0};
+  cudaError_t e = once_per_device(configured, [] {
+    return cudaFuncSetAttribute(verify_kv8_kernel<D, NQC, CAP>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(512, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kv8_kernel<D, NQC, CAP>, kmap, vmap, p);
+}
+
+// The softmax's columns: nq rounded up to 8.
+template <int D, bool CAP>
+static cudaError_t launch_cols(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const VerifyKv8Params& p, int grid, cudaStream_t s) {
+  if (!verify_kv8_supported(D, p.nq)) return cudaErrorInvalidValue;
+  switch ((p.nq + 7) / 8) {
+    case 1: return launch_one<D, 8, CAP>(kmap, vmap, p, grid, s);
+    case 2: return launch_one<D, 16, CAP>(kmap, vmap, p, grid, s);
+    case 3: return launch_one<D, 24, CAP>(kmap, vmap, p, grid, s);
+    case 4: return launch_one<D, 32, CAP>(kmap, vmap, p, grid, s);
+    case 5: return launch_one<D, 40, CAP>(kmap, vmap, p, grid, s);
+  }
+  if constexpr (D == 64) {
+    switch ((p.nq + 7) / 8) {
+      case 6: return launch_one<D, 48, CAP>(kmap, vmap, p, grid, s);
+      case 7: return launch_one<D, 56, CAP>(kmap, vmap, p, grid, s);
+      case 8: return launch_one<D, 64, CAP>(kmap, vmap, p, grid, s);
+    }
+  }
+  return cudaErrorInvalidValue;
+}
+
+#define VEGAS_CAT2(a, b) a##b
+#define VEGAS_CAT(a, b) VEGAS_CAT2(a, b)
+
+cudaError_t VEGAS_CAT(launch_verify_kv8_d, VEGAS_KV8_D)(const CUtensorMap& kmap,
+                                                       const CUtensorMap& vmap,
+                                                       const VerifyKv8Params& p, bool capture,
+                                                       int grid, cudaStream_t stream) {
+  constexpr int D = VEGAS_KV8_D;
+  return capture ? launch_cols<D, true>(kmap, vmap, p, grid, stream)
+                 : launch_cols<D, false>(kmap, vmap, p, grid, stream);
+}
+
+}  // namespace vegas

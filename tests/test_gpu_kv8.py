@@ -2,7 +2,11 @@
 
 Tolerances: an output's own rounding is half a step of bf16, 2^-8 of it.  A softmax weight is
 off by f16's half step 2^-11 and by the error d of its logit (twice that, numerator and sum), so
-an output by at most (2^-11 + 2 d + 2^-16) sum_i p_i |v_i| more, where d = 2^-17 times the unit's
+an output by at most (2^-11 + 2 d + 2^-16) sum_i p_i |v_i| more; in verify attention by 2^-9 more
+for the weights' three e5m2 parts (of p in [2^e, 2^(e + 1)) the first cut leaves less than 2^(e - 2),
+the second, of a leading bit of 2^(e - 3) at most, less than 2^(e - 5), and the last part, of a
+leading bit of 2^(e - 6) at most, is rounded by half a step, 2^(e - 9)) and 2^-13 for weights below
+their grid (2^-28 of the largest, of up to 2^15 positions); where d = 2^-17 times the unit's
 largest |q| times the largest sum_j |k_ij| (the grid of the queries' two parts; 0 for drafts),
 plus 2^-20 sum_j |q_j k_ij| (fp32 sums), times the softmax scale.  A captured score is off by
 2^-17 of its terms' magnitudes: the fp32 sum of up to 64 query rows (63 * 2^-24), the tensor cores'
@@ -291,6 +295,9 @@ def queries(rng, shape, size=1.0):
     return torch.from_numpy(rng.standard_normal(shape) * size).bfloat16()
 
 
+P_PARTS = 2.0 ** -9 + 2.0 ** -13      # of the weights in verify attention
+
+
 def check_verify(c, q, out, scores, ctx, gamma, mask, scale):
     batch, t, hq, d = q.shape
     g = hq // c.hkv
@@ -308,7 +315,7 @@ def check_verify(c, q, out, scores, ctx, gamma, mask, scale):
                 want, mag, _ = k8.attend(qq[i], k[:n + i + 1], v[:n + i + 1], scale)
                 terms = (np.abs(qq[i]) @ np.abs(k[:n + i + 1]).T).max()
                 d_logit = abs(scale) * (grid + 2.0 ** -20 * terms)
-                tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * d_logit + 2.0 ** -16) * mag + 1e-30
+                tol = 2.0 ** -8 * np.abs(want) + (P_PARTS + 2.0 ** -11 + 2 * d_logit + 2.0 ** -16) * mag + 1e-30
                 err = np.abs(od[b, i, h * g:(h + 1) * g] - want)
                 assert (err <= tol).all(), (b, h, i, float((err / tol).max()))
             if sd is not None:
@@ -424,7 +431,7 @@ def test_verify_rows_of_unlike_size(d, spread):
             want, mag, _ = k8.attend(qq, k[:700 + i + 1], v[:700 + i + 1], 0.1)
             d_logit = 0.1 * (2.0 ** -17 * np.abs(qq).max() * np.abs(k).sum(-1).max()
                              + 2.0 ** -20 * (np.abs(qq) @ np.abs(k).T).max())
-            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * d_logit + 2.0 ** -16) * mag
+            tol = 2.0 ** -8 * np.abs(want) + (P_PARTS + 2.0 ** -11 + 2 * d_logit + 2.0 ** -16) * mag
             assert (np.abs(out[0, i, h].double().cpu().numpy() - want) <= tol).all()
 
 
