@@ -44,7 +44,7 @@ UNITS = [
     ("kv8_append.cu", "kv8_append.o", []),
     ("kv8_read.cu", "kv8_read.o", []),
     ("verify_kv8.cu", "verify_kv8_d128.o", ["-DVEGAS_KV8_D=128"]),
-    ("verify_kv8_wide.cu", "verify_kv8_d64.o", ["-DVEGAS_KV8_D=64"]),
+    ("verify_kv8.cu", "verify_kv8_d64.o", ["-DVEGAS_KV8_D=64"]),
     ("verify_attn.cu", "verify_d128_c1.o", ["-DVEGAS_D=128", "-DVEGAS_CAP=1"]),
     ("verify_attn.cu", "verify_d128_c0.o", ["-DVEGAS_D=128", "-DVEGAS_CAP=0"]),
     ("verify_attn.cu", "verify_d64_c1.o", ["-DVEGAS_D=64", "-DVEGAS_CAP=1"]),
