@@ -68,6 +68,76 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
+// Consecutive fp32 columns of this thread's lane as pairs; complete on return.
+template <int N>
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v) {
+  static_assert(N == 8 || N == 16 || N == 24 || N == 32, "columns");
+  if constexpr (N == 8) {
+    asm volatile(
+        "{\n .reg .b32 t<8>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7}, [%4];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3])
+        : "r"(a)
+        : "memory");
+  }
+  if constexpr (N == 16) {
+    asm volatile(
+        "{\n .reg .b32 t<16>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15}, [%8];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7])
+        : "r"(a)
+        : "memory");
+  }
+  if constexpr (N == 24) {
+    asm volatile(
+        "{\n .reg .b32 t<24>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15}, [%12];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t16, t17, t18, t19, t20, t21, t22, t23}, [%13];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11])
+        : "r"(a), "r"(a + 16)
+        : "memory");
+  }
+  if constexpr (N == 32) {
+    asm volatile(
+        "{\n .reg .b32 t<32>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15, "
+        "t16, t17, t18, t19, t20, t21, t22, t23, "
+        "t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]),
+          "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
+        : "r"(a)
+        : "memory");
+  }
+}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -523,15 +593,6 @@ __global__ void __launch_bounds__(384, 1)
       asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(scales + block));
       return v;
     };
-    // S of columns 8 c .. 8 c + 7, the parts added
-    auto load_chunk = [&](uint32_t at, int c, float* y) {
-      float v8[8], w8[8];
-      tmem_ld8(at + 8 * c, v8);
-      if constexpr (kSideS) tmem_ld8(at + NQC + 8 * c, w8);
-      tmem_ld_wait();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = kSideS ? v8[e] + w8[e] : v8[e];
-    };
     // O^T of columns 8 c .. 8 c + 7, the parts added
     auto load_o = [&](int c, float (&v)[8]) {
       tmem_ld8(tl + o_col + 8 * c, v);
@@ -545,23 +606,22 @@ __global__ void __launch_bounds__(384, 1)
         for (int e = 0; e < 8; ++e) v[e] += w8[e];
       }
     };
-    // of all columns, up to three chunks in flight
-    auto load_all = [&](uint32_t at, float* y) {
+    // S of all columns in pairs, the parts added
+    auto load_all = [&](uint32_t at, uint64_t (&y2)[NQC / 2]) {
+      constexpr int kFirst = NQC < 32 ? NQC : 32, kRest = NQC > 32 ? NQC - 32 : 8;
+      uint64_t low[16];
+      tmem_ld_pairs<kFirst>(at, y2);
+      if constexpr (kSideS) {
+        tmem_ld_pairs<kFirst>(at + NQC, low);
 #pragma unroll
-      for (int c0 = 0; c0 < NQC / 8; c0 += 3) {
-        float v8[3][8], w8[3][8];
+        for (int j = 0; j < kFirst / 2; ++j) y2[j] = add_f32x2(y2[j], low[j]);
+      }
+      if constexpr (NQC > 32) {
+        tmem_ld_pairs<kRest>(at + 32, y2 + 16);
+        if constexpr (kSideS) {
+          tmem_ld_pairs<kRest>(at + NQC + 32, low);
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          if (c0 + c >= NQC / 8) continue;
-          tmem_ld8(at + 8 * (c0 + c), v8[c]);
-          if constexpr (kSideS) tmem_ld8(at + NQC + 8 * (c0 + c), w8[c]);
-        }
-        if (kSideS || c0 + 3 >= NQC / 8) tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          if (c0 + c >= NQC / 8) continue;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[8 * (c0 + c) + e] = kSideS ? v8[c][e] + w8[c][e] : v8[c][e];
+          for (int j = 0; j < kRest / 2; ++j) y2[16 + j] = add_f32x2(y2[16 + j], low[j]);
         }
       }
     };
@@ -707,12 +767,12 @@ __global__ void __launch_bounds__(384, 1)
       }
 
       // ---------------------------------------------------------- its tiles
-      float nr[kSmemRef ? 2 : NQC];
-      uint64_t ls2[NQC / 2];   // row sums, two columns each
+      uint64_t nr2[kSmemRef ? 1 : NQC / 2];
+      uint64_t ls2[NQC / 2];   // row sums
 #pragma unroll
-      for (int n2 = 0; n2 < NQC; ++n2) {
-        if constexpr (!kSmemRef) nr[n2] = 0.f;
-        if (n2 % 2 == 0) ls2[n2 / 2] = 0;
+      for (int c = 0; c < NQC / 2; ++c) {
+        if constexpr (!kSmemRef) nr2[c] = 0;
+        ls2[c] = 0;
       }
       uint64_t hollow = NQC == 64 ? ~0ull : (1ull << NQC) - 1;   // columns without a reference
       const int uni = *uniform;
@@ -743,48 +803,47 @@ __global__ void __launch_bounds__(384, 1)
         // then, and O^T may be rescaled
         const bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
         tc_fence_after();
-        // z of columns 8 c .. 8 c + 7 less their references (y: S in, z out)
-        auto z_chunk = [&](int c, float* y) {
-          if (mixed) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= colfac[8 * c + e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            float4 r4;
-            if constexpr (kSmemRef)
-              r4 = reinterpret_cast<const float4*>(nrg)[2 * c + e / 4];
-            else
-              r4 = make_float4(nr[8 * c + e], nr[8 * c + e + 1], nr[8 * c + e + 2], nr[8 * c + e + 3]);
-            const uint64_t a =
-                add_f32x2(fma_f32x2(pair_f32(y[e], y[e + 1]), f2, add2), pair_f32(r4.x, r4.y));
-            const uint64_t d =
-                add_f32x2(fma_f32x2(pair_f32(y[e + 2], y[e + 3]), f2, add2), pair_f32(r4.z, r4.w));
-            unpair_f32(a, y[e], y[e + 1]);
-            unpair_f32(d, y[e + 2], y[e + 3]);
-          }
-          if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (pos > L + tlim[8 * c + e]) y[e] = -INFINITY;
-          }
-        };
-        float y[NQC];
+        // z of all columns less their references, two to a register pair
+        uint64_t y2[NQC / 2];
         float cx[8] = {};   // the capture columns
         bool left = false, forced = hollow != 0;
         while (true) {
           bool need = forced;
           if (okt) {
             if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-            load_all(tl + s_col, y);
-            float ym = -INFINITY;
+            load_all(tl + s_col, y2);
+            if (mixed) {
 #pragma unroll
-            for (int c = 0; c < NQC / 8; ++c) {
-              z_chunk(c, y + 8 * c);
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) ym = fmaxf(fmaxf(ym, y[8 * c + e]), y[8 * c + e + 1]);
+              for (int c = 0; c < NQC / 2; ++c)
+                y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac)[c]);
             }
-            need |= ym > kTop;
+#pragma unroll
+            for (int c = 0; c < NQC / 4; ++c) {
+              ulonglong2 r;
+              if constexpr (kSmemRef)
+                r = reinterpret_cast<const ulonglong2*>(nrg)[c];
+              else
+                r = make_ulonglong2(nr2[2 * c], nr2[2 * c + 1]);
+              y2[2 * c] = add_f32x2(fma_f32x2(y2[2 * c], f2, add2), r.x);
+              y2[2 * c + 1] = add_f32x2(fma_f32x2(y2[2 * c + 1], f2, add2), r.y);
+            }
+            if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
+#pragma unroll
+              for (int c = 0; c < NQC / 2; ++c) {
+                float a, d;
+                unpair_f32(y2[c], a, d);
+                y2[c] = pair_f32(pos > L + tlim[2 * c] ? -INFINITY : a,
+                                 pos > L + tlim[2 * c + 1] ? -INFINITY : d);
+              }
+            }
+            float ym[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < NQC / 2; ++c) {
+              float a, d;
+              unpair_f32(y2[c], a, d);
+              ym[c & 1] = fmaxf(fmaxf(ym[c & 1], a), d);
+            }
+            need |= fmaxf(ym[0], ym[1]) > kTop;
           }
           const bool all_ok = __all_sync(0xffffffffu, okt);
           if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
@@ -798,7 +857,10 @@ __global__ void __launch_bounds__(384, 1)
           float* cm = colmax + grp * 4 * NQC;
 #pragma unroll
           for (int c = 0; c < NQC / 8; ++c) {
-            const float top = reduce_chunk(y + 8 * c, [](float a, float d) { return fmaxf(a, d); });
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) unpair_f32(y2[4 * c + e / 2], v[e], v[e + 1]);
+            const float top = reduce_chunk(v, [](float a, float d) { return fmaxf(a, d); });
             if ((lane & 3) == 0) cm[q4 * NQC + 8 * c + (lane >> 2)] = top;
           }
           named_bar(1 + grp, 128);
@@ -828,11 +890,9 @@ __global__ void __launch_bounds__(384, 1)
             ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
             ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
             if constexpr (!kSmemRef) {
-              const float4 r4 = reinterpret_cast<const float4*>(nrg)[c];
-              nr[4 * c] = r4.x;
-              nr[4 * c + 1] = r4.y;
-              nr[4 * c + 2] = r4.z;
-              nr[4 * c + 3] = r4.w;
+              const ulonglong2 r = reinterpret_cast<const ulonglong2*>(nrg)[c];
+              nr2[2 * c] = r.x;
+              nr2[2 * c + 1] = r.y;
             }
           }
           if (any) {
@@ -880,7 +940,10 @@ __global__ void __launch_bounds__(384, 1)
           uint32_t x[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float p0 = ex2(y[8 * c + e]), p1 = ex2(y[8 * c + e + 1]);
+            float p0, p1;
+            unpair_f32(y2[4 * c + e / 2], p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
             ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
             x[e / 2] = pack_f16x2(p0, p1);
           }
