@@ -138,6 +138,12 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v) {
         : "memory");
   }
 }
+// Takes a ticket, with everything before it released and everything after it acquired.
+__device__ __forceinline__ int ticket_acq_rel(int* t) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(t) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -989,8 +995,9 @@ __global__ void __launch_bounds__(384, 1)
         const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
         if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
       }
-      // The group's last PV completes its O^T; group 1 hands its own over in P's buffers, once both
-      // groups' PVs have read them.
+      // The group's last PV completes its O^T.  Group 0 finishes the first half of the columns, group
+      // 1 the second; each hands its part of the other half over in P's buffers, once both groups'
+      // PVs have read them.
       if (any && ok) {
         const uint32_t last = it0 + uint32_t(tiles) - 1 - ((it0 + uint32_t(tiles) - 1 - uint32_t(grp)) & 1);
         if (!mbar_wait_bounded(pvdone(grp), (last >> 1) & 1)) ok = false;
@@ -1015,18 +1022,19 @@ __global__ void __launch_bounds__(384, 1)
                     w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
       }
       float* hand = reinterpret_cast<float*>(smem + Cfg::kOffP);   // [NQC][D]
-      const bool any1 = tiles > 1 || (it0 & 1);                    // group 1 has a tile
-      const bool any0 = tiles > 1 || !(it0 & 1);
-      if (grp == 1 && any1) {
+      // groups with a tile
+      const bool mine = any, other = tiles > 1 || (((it0 ^ uint32_t(grp)) & 1) != 0);
+      constexpr int kChunks = NQC / 8, kHalf = (kChunks + 1) / 2;
+      const int own0 = grp ? kHalf : 0, own1 = grp ? kChunks : kHalf;
+      if (mine) {
 #pragma unroll 1
-        for (int c = 0; c < NQC / 8; ++c) {
+        for (int c = grp ? 0 : kHalf; c < (grp ? kHalf : kChunks); ++c) {
           float v8[8];
           load_o(c, v8);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (dim >= 0) hand[(8 * c + e) * D + dim] = v8[e];
         }
-        tc_fence_before();
       }
       named_bar(3, 256);
       // the CTAs that hold tiles of the unit
@@ -1041,79 +1049,75 @@ __global__ void __launch_bounds__(384, 1)
       // where that is another; of a unit's CTAs only the first can have it as its last.
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
-      if (grp == 0) {
 #pragma unroll 1
-        for (int c = 0; c < NQC / 8; ++c) {
-          float v8[8] = {};
-          if (any0) load_o(c, v8);
+      for (int c = own0; c < own1; ++c) {
+        float v8[8] = {};
+        if (mine) load_o(c, v8);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int n2 = 8 * c + e;
-            if (dim < 0 || n2 >= p.nq) continue;
-            float v = any0 ? v8[e] * wgt[n2] : 0.f;
-            if (any1) v = fmaf(hand[n2 * D + dim], wgt[NQC + n2], v);
-            if (c0 == c1)
-              out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
-            else
-              p.part_o[(slot * p.nq + n2) * D + dim] = v;
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int n2 = 8 * c + e;
+          if (dim < 0 || n2 >= p.nq) continue;
+          float v = mine ? v8[e] * wgt[grp * NQC + n2] : 0.f;
+          if (other) v = fmaf(hand[n2 * D + dim], wgt[(grp ^ 1) * NQC + n2], v);
+          if (c0 == c1)
+            out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
+          else
+            p.part_o[(slot * p.nq + n2) * D + dim] = v;
         }
-        tc_fence_before();
-        if (c0 != c1 && tid < p.nq)
-          reinterpret_cast<float2*>(p.part_ml)[slot * p.nq + tid] = make_float2(colM[tid], colL[tid]);
       }
+      tc_fence_before();
+      if (c0 != c1 && tid < p.nq)
+        reinterpret_cast<float2*>(p.part_ml)[slot * p.nq + tid] = make_float2(colM[tid], colL[tid]);
       if (c0 != c1) {
         named_bar(3, 256);
-        if (tid == 0) {   // (the fence covers what the barrier made visible to this thread)
-          __threadfence();
-          *flag = atomicAdd(&p.tickets[unit], 1) == c1 - c0;
-          __threadfence();
-        }
+        // (released and acquired by one thread: the barriers carry that to and from the others)
+        if (tid == 0) *flag = ticket_acq_rel(&p.tickets[unit]) == c1 - c0;
         named_bar(3, 256);
         if (*flag) {
-          // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m).
+          // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m), in one pass
+          // over the pieces with the running maximum.  All of a thread's elements have their loads in
+          // flight together.
           const int pieces = c1 - c0 + 1;
-          auto slot_of = [&](int c) { return size_t(c == 0 ? slot0 : 2 * (c0 + c)); };
           const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-#pragma unroll 1
-          for (int n2 = warp; n2 < p.nq; n2 += 8) {
-            float M = kEmptyMax, sum = 0.f;
-#pragma unroll 1
-            for (int c = lane; c < pieces; c += 32) {
-              const float2 v = __ldcg(ml + slot_of(c) * p.nq + n2);
-              const float now = fmaxf(M, v.x);
-              sum = sum * ex2(M - now) + v.y * ex2(v.x - now);
-              M = now;
+          constexpr int E = (NQC * (D / 4) + 255) / 256;
+          float M[E], sum[E];
+          float4 acc[E];
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            M[j] = kEmptyMax;
+            sum[j] = 0.f;
+            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll 2
+          for (int c = 0; c < pieces; ++c) {
+            const size_t rows = size_t(c == 0 ? slot0 : 2 * (c0 + c)) * p.nq;
+            float2 m[E];
+            float4 v[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              const int e = tid + 256 * j, n2 = min(e / (D / 4), p.nq - 1);
+              m[j] = __ldcg(ml + rows + n2);
+              v[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (rows + n2) * D) + e % (D / 4));
             }
-            float top = M;
 #pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-            sum *= ex2(M - top);
-#pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-            if (lane == 0) {
-              colM[n2] = top;
-              colL[n2] = 1.f / sum;
+            for (int j = 0; j < E; ++j) {
+              const float now = fmaxf(M[j], m[j].x), a = ex2(M[j] - now), w = ex2(m[j].x - now);
+              M[j] = now;
+              sum[j] = sum[j] * a + w * m[j].y;
+              acc[j].x = acc[j].x * a + w * v[j].x;
+              acc[j].y = acc[j].y * a + w * v[j].y;
+              acc[j].z = acc[j].z * a + w * v[j].z;
+              acc[j].w = acc[j].w * a + w * v[j].w;
             }
           }
-          named_bar(3, 256);
-#pragma unroll 1
-          for (int e = tid; e < p.nq * (D / 4); e += 256) {
-            const int n2 = e / (D / 4), d = 4 * (e - n2 * (D / 4));
-            const float M = colM[n2], inv = colL[n2];
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = 0; c < pieces; ++c) {
-              const size_t row = slot_of(c) * p.nq + n2;
-              const float w = ex2(__ldcg(&p.part_ml[2 * row]) - M);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
-              acc.x += w * v.x;
-              acc.y += w * v.y;
-              acc.z += w * v.z;
-              acc.w += w * v.w;
-            }
-            *reinterpret_cast<uint2*>(out_row(n2) + d) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const int e = tid + 256 * j, n2 = e / (D / 4);
+            if (n2 >= p.nq) continue;
+            const float inv = 1.f / sum[j];
+            reinterpret_cast<uint2*>(out_row(n2))[e % (D / 4)] =
+                make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv),
+                           pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
           }
           if (tid == 0) p.tickets[unit] = 0;
         }
