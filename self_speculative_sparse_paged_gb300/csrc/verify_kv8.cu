@@ -4,12 +4,13 @@
 // The work is that of verify_tc.cu on half the bytes, laid out so that its length goes by what the
 // sequences hold, not by what their tables could: the 128-position tiles of all (sequence, KV
 // head) units stand in one row, and each CTA (one an SM) takes an equal run of it, whole units or
-// pieces, with the K/V stream going on from one unit to the next.  Twelve warps:
-//   warps 0-7   two softmax groups of four warps that alternate tiles; a thread owns a position
-//               of a tile, and a head dimension of the group's O^T.  They also build the query operand
-//               of a unit and finish it.
-//   warps 8, 9  TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
-//   warp 10     issues the MMAs
+// pieces, with the K/V stream going on from one unit to the next.  Twelve
+// warps, or twenty with more than 32 columns:
+//   softmax    two groups alternate tiles, each of one team of four warps or (wide) of two that halve
+//              the columns; a thread owns a position of a tile, and a head dimension of O^T.  They
+//              also build the query operand of a unit and finish it.
+//   producers  two warps, K and V: 8 pages a tile by TMA into rings, block-table entries prefetched
+//   MMA        one warp issues
 //
 //   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
 //       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
@@ -51,7 +52,7 @@ constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P
 constexpr int kCapParts = 6;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
 // reference and end), and a CTA takes part for kLeastRun tiles or more.
-constexpr int kUnitTiles = 3, kLeastRun = 4;
+constexpr int kUnitTiles = 8, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
 // Instruction descriptor, kind::f8f6f4 (K = 32), fp32 accumulator: A e4m3, B e4m3 or e5m2, both
@@ -138,6 +139,17 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v) {
         : "memory");
   }
 }
+// Whether the phase with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Takes a ticket, with everything before it released and everything after it acquired.
 __device__ __forceinline__ int ticket_acq_rel(int* t) {
   int v;
@@ -203,13 +215,17 @@ struct Kv8Cfg {
   static constexpr int kOffBar = kOffQ + kPasses * kQ;
   static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 2;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  // misc: 16 words; votes[2][2][4]; warp sums[12] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
+  // Softmax threads: two groups of HN teams of 128; a team has up to NC columns, HN > 1 keeps a
+  // thread's share of wide tiles in registers and halves its chain.
+  static constexpr int HN = 1;
+  static constexpr int NC = HN == 2 ? (NQC / 8 + 1) / 2 * 8 : NQC;
+  static constexpr int kSoft = 256 * HN, kThreads = kSoft + 128;
+  // misc: 16 words; votes[2][teams][4]; warp sums[20] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
   // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
-  static constexpr size_t kMisc = 64 + 64 + 128 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
+  static constexpr size_t kMisc = 64 + 128 + 160 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(NQC * D * 4 <= 2 * kP, "a group's O^T handed over in P's buffers");
-  static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
+  static_assert(8 * HN * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
 };
 
 // A place in the row of tiles: tile t of KV head g of sequence b.
@@ -224,12 +240,15 @@ struct Place {
 };
 
 template <int D, int NQC, bool CAPTURE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const VerifyKv8Params p) {
   using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
   constexpr int KS = Cfg::KS, VS = Cfg::VS, NS = Cfg::NS, NP = Cfg::NP;
   constexpr bool kSideS = Cfg::kSideS, kSideP = Cfg::kSideP;
+  constexpr int HN = Cfg::HN, NC = Cfg::NC, kSoft = Cfg::kSoft, kThreads = Cfg::kThreads;
+  constexpr int kSoftWarps = kSoft / 32, kWarps = kThreads / 32;
+  constexpr int kAllBar = 5;   // named barriers: 1 + team, and all softmax threads
   static_assert(NQC % 8 == 0 && (D == 64 || D == 128), "columns, head_dim");
 
   griddep_launch_dependents();
@@ -255,9 +274,9 @@ __global__ void __launch_bounds__(384, 1)
   int* flag = reinterpret_cast<int*>(misc + 4);
   int* capexp = reinterpret_cast<int*>(misc + 8);
   int* uniform = reinterpret_cast<int*>(misc + 12);
-  int* votes = reinterpret_cast<int*>(misc + 64);                // [2][2][4]
-  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [12] a warp's sequences
-  float* colmax = reinterpret_cast<float*>(misc + 256);          // [2][4][NQC]
+  int* votes = reinterpret_cast<int*>(misc + 64);                // [2][teams][4]
+  long long* wsum = reinterpret_cast<long long*>(misc + 192);    // [20] a warp's sequences
+  float* colmax = reinterpret_cast<float*>(misc + 352);          // [2][4][NQC]
   float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
   float* colfac = colsum + 8 * NQC;                              // [NQC] 2^-k of rows of unlike size
   float* nrefs = colfac + NQC;                                   // [2][NQC] -reference
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(384, 1)
   float* colL = colM + NQC;
   int* tlim = reinterpret_cast<int*>(colL + NQC);                // [NQC]
   int* rowexp = tlim + NQC;                                      // [NQC]
-  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffP);     // [8][D] parts of the captured sum
+  float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffP);     // [softmax warps][D] of the captured sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int T = p.gamma + 1;
@@ -284,15 +303,15 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull(i), 1);
-      mbar_init(sread(i), 128);
-      mbar_init(pready(i), 128);
+      mbar_init(sread(i), 128 * HN);
+      mbar_init(pready(i), 128 * HN);
       mbar_init(pvdone(i), 1);
     }
-    mbar_init(qready, 256);
+    mbar_init(qready, kSoft);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 10) {
+  if (warp == kSoftWarps + 2) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -313,7 +332,7 @@ __global__ void __launch_bounds__(384, 1)
   auto span_of = [&](int L) { return (long long)(tiles_of(L) + kUnitTiles) * p.hkv; };
   // Up to 32 sequences every warp scans by itself; else warp w first counts [w * chunk, (w + 1) *
   // chunk).
-  const int chunk = (p.batch + 383) / 384 * 32;
+  const int chunk = (p.batch + kThreads - 1) / kThreads * 32;
   long long all = 0;
   int first_chunk = 0;
   if (p.batch > 32) {
@@ -325,7 +344,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
 #pragma unroll 1
-    for (int w = 0; w < 12; ++w) all += wsum[w];
+    for (int w = 0; w < kWarps; ++w) all += wsum[w];
   }
   long long upto = 0;    // this lane's sequence and those before it, of 32
   int mylen = 0;
@@ -344,7 +363,7 @@ __global__ void __launch_bounds__(384, 1)
     all = __shfl_sync(0xffffffffu, upto, 31);
   }
   if (cta == 0)   // lengths out of range are recorded once
-    for (int b = tid; b < p.batch; b += 384) {
+    for (int b = tid; b < p.batch; b += kThreads) {
       const int L = p.ctx_lens[b];
       if (L < 0 || L + T > cap) set_error(p.err, kErrDeviceFault);
     }
@@ -364,7 +383,7 @@ __global__ void __launch_bounds__(384, 1)
   if (begin < end) {
     int b0 = 0;
     if (p.batch > 32) {
-      for (; first_chunk < 11 && base + wsum[first_chunk] <= begin; ++first_chunk)
+      for (; first_chunk < kWarps - 1 && base + wsum[first_chunk] <= begin; ++first_chunk)
         base += wsum[first_chunk];
       b0 = first_chunk * chunk;
     }
@@ -401,14 +420,15 @@ __global__ void __launch_bounds__(384, 1)
   };
   bool ok = true;
 
-  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
-  if (warp >= 8) {
-    leave_registers<72>();
-    if (warp < 10) {
-      // ---------------------------------------------------------- producers: K (8), V (9)
+  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that; 640 with 96: 4 x
+  // 128 x 104 + 128 x 64.
+  if (warp >= kSoftWarps) {
+    leave_registers<HN == 2 ? 64 : 72>();
+    if (warp < kSoftWarps + 2) {
+      // ---------------------------------------------------------- producers: K, V
       // Lane j < 8 loads page j of a tile; a page past the sequence's last is that one again (its
       // positions are masked).
-      const bool is_k = warp == 8;
+      const bool is_k = warp == kSoftWarps;
       const int depth = is_k ? KS : VS;
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       const uint32_t ring = sbase + (is_k ? 0 : Cfg::kOffV);
@@ -481,7 +501,7 @@ __global__ void __launch_bounds__(384, 1)
           (void)mbar_wait_bounded(is_k ? kfull(s) : vfull(s), round & 1);
         }
       }
-    } else if (warp == 10) {
+    } else if (warp == kSoftWarps + 2) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t idS = idesc_f8(128, NS, 0, 0);
       constexpr uint32_t idPV = idesc_f8(D, NP, 1, 1);
@@ -528,18 +548,16 @@ __global__ void __launch_bounds__(384, 1)
           ok = false;
           break;
         }
-        for (int t = 0; t < tiles && ok; ++t, ++it) {
+        auto issue_s = [&]() {
           const int gg = it & 1;
-          if (!wait_all(kfull(s), round & 1)) { ok = false; break; }
-          if (it >= 2 && !wait_all(sread(gg), ((it >> 1) - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
           const uint32_t kb = (sbase + s * Cfg::kTile) >> 4;
+          tc_fence_after();
           if (leader) {
 #pragma unroll
             for (int j = 0; j < Cfg::kPasses * (D / 32); ++j) {
               const int pass = j / (D / 32), ks = j % (D / 32);
               tc_mma_f8(tmem + Cfg::kSCol * gg, with_addr(dKQV, kb + 2 * ks),
-                          with_addr(dKQV, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
+                        with_addr(dKQV, qb + pass * (Cfg::kQ / 16) + 2 * ks), idS, j > 0);
             }
             tc_commit(sfull(gg));
             tc_commit(kfree(s));
@@ -549,9 +567,21 @@ __global__ void __launch_bounds__(384, 1)
             s = 0;
             ++round;
           }
-          if (t >= 1 && !issue_pv(it - 1, t - 1 < 2)) ok = false;
+        };
+        for (int t = 0; t < tiles && ok; ++t, ++it) {
+          // S of tile t overwrites that of tile t - 2, whose P (if of this unit) waits for its PV.  S
+          // goes first when its K tile is there: the group waits for nothing else.
+          if (it >= 2 && !wait_all(sread(it & 1), ((it >> 1) - 1) & 1)) { ok = false; break; }
+          const bool early = __all_sync(0xffffffffu, mbar_test(kfull(s), round & 1));
+          if (early) issue_s();
+          if (t >= 2 && !issue_pv(it - 2, t - 2 < 2)) { ok = false; break; }
+          if (!early) {
+            if (!wait_all(kfull(s), round & 1)) { ok = false; break; }
+            issue_s();
+          }
         }
-        // the unit's last PV, before the next unit's queries are waited for
+        // the unit's last PVs, before the next unit's queries are waited for
+        if (ok && tiles >= 2 && !issue_pv(it - 2, tiles - 2 < 2)) ok = false;
         if (ok && !issue_pv(it - 1, tiles - 1 < 2)) ok = false;
         next_unit(at, tiles);
       }
@@ -562,9 +592,13 @@ __global__ void __launch_bounds__(384, 1)
       (void)mbar_wait_bounded(drain, 0);
     }
   } else {
-    take_registers<216>();
-    // ------------------------------------------------------------ softmax groups (warps 0-7)
-    const int grp = warp >> 2;                // 0: even tiles, 1: odd tiles
+    take_registers<HN == 2 ? 104 : 216>();
+    // ------------------------------------------------------------ softmax teams
+    const int team = warp >> 2, grp = team & 1;   // group 0: even tiles, 1: odd tiles
+    const int half = team >> 1;               // the team's columns: col0 .. col0 + ncol - 1
+    const int col0 = half * NC, ncol = half ? NQC - NC : NC;
+    // chunk c of a team's columns is there
+    auto has = [&](int c) { return 8 * c < NQC - NC * (HN - 1) || half == 0; };
     const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
     const int i = 32 * q4 + lane;             // tile position owned
     // head dimension owned: M = 64 puts 16 rows in each quarter of the lanes
@@ -573,8 +607,8 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t s_col = Cfg::kSCol * grp, o_col = 2 * Cfg::kSCol + Cfg::kOCol * grp;
     // Column references r (P = 2^(z - r)) are kept as -r in shared memory, up to 32 columns in
     // registers too; 0 while `hollow` says that the column has seen no unmasked logit.
-    constexpr bool kSmemRef = NQC > 32;
-    constexpr int QPER = NQC / 8;
+    constexpr bool kSmemRef = NC > 32;
+    constexpr int QPER = (NQC + kSoftWarps - 1) / kSoftWarps;
     uint8_t* qs = smem + Cfg::kOffQ;
     // Element (n, k) of a query part: n * D + the 16-byte chunk k / 16 swizzled with the row.
     auto qoff = [](int n2, int k) {
@@ -583,7 +617,7 @@ __global__ void __launch_bounds__(384, 1)
     };
     const __nv_bfloat16* qbase = reinterpret_cast<const __nv_bfloat16*>(p.q);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
-    float* nrg = nrefs + grp * NQC;
+    float* nrg = nrefs + grp * NQC + col0;   // of the team's columns
     // (pages outside the pool: the producers record and clamp them)
     auto load_page = [&](const Place& u, int t) {   // volatile, here and below: the compiler may not
       const int page = min(8 * t + (i >> 4), (u.L + T - 1) >> 4);   // move the loads down to their uses
@@ -599,22 +633,23 @@ __global__ void __launch_bounds__(384, 1)
       asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(scales + block));
       return v;
     };
-    // O^T of columns 8 c .. 8 c + 7, the parts added
-    auto load_o = [&](int c, float (&v)[8]) {
-      tmem_ld8(tl + o_col + 8 * c, v);
+    // group gg's O^T of columns 8 c .. 8 c + 7, the parts added
+    auto load_o = [&](int gg, int c, float (&v)[8]) {
+      const uint32_t at = tl + 2 * Cfg::kSCol + Cfg::kOCol * gg + 8 * c;
+      tmem_ld8(at, v);
       tmem_ld_wait();
 #pragma unroll
       for (int part = 1; part < Cfg::kPCols / NQC; ++part) {
         float w8[8];
-        tmem_ld8(tl + o_col + part * NQC + 8 * c, w8);
+        tmem_ld8(at + part * NQC, w8);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += w8[e];
       }
     };
-    // S of all columns in pairs, the parts added
-    auto load_all = [&](uint32_t at, uint64_t (&y2)[NQC / 2]) {
-      constexpr int kFirst = NQC < 32 ? NQC : 32, kRest = NQC > 32 ? NQC - 32 : 8;
+    // S of the team's columns in pairs, the parts added
+    auto load_all = [&](uint32_t at, uint64_t (&y2)[NC / 2]) {
+      constexpr int kFirst = NC < 32 ? NC : 32, kRest = NC > 32 ? NC - 32 : 8;
       uint64_t low[16];
       tmem_ld_pairs<kFirst>(at, y2);
       if constexpr (kSideS) {
@@ -622,7 +657,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int j = 0; j < kFirst / 2; ++j) y2[j] = add_f32x2(y2[j], low[j]);
       }
-      if constexpr (NQC > 32) {
+      if constexpr (NC > 32) {
         tmem_ld_pairs<kRest>(at + 32, y2 + 16);
         if constexpr (kSideS) {
           tmem_ld_pairs<kRest>(at + NQC + 32, low);
@@ -648,7 +683,7 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t qreg[QPER][D / 64];
 #pragma unroll
         for (int u = 0; u < QPER; ++u) {
-          const int n2 = warp + 8 * u, t = n2 / p.group, hl = n2 - t * p.group;
+          const int n2 = warp + kSoftWarps * u, t = n2 / p.group, hl = n2 - t * p.group;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
             qreg[u][h] = n2 < p.nq ? reinterpret_cast<const uint32_t*>(
@@ -663,7 +698,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) most = __vmaxu2(most, qreg[u][h] & 0x7fff7fffu);
           most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
-          if (lane == 0) rowexp[warp + 8 * u] = most ? max(-100, int(most >> 7) - 127) : -1000;
+          if (lane == 0 && warp + kSoftWarps * u < NQC)
+            rowexp[warp + kSoftWarps * u] = most ? max(-100, int(most >> 7) - 127) : -1000;
         }
         ekb = load_scale(p.k_scale, phys0, g);
         evb = load_scale(p.v_scale, phys0, g);
@@ -672,7 +708,7 @@ __global__ void __launch_bounds__(384, 1)
           float acc[D / 64][2] = {};
 #pragma unroll
           for (int u = 0; u < QPER; ++u) {
-            const int n2 = warp + 8 * u;
+            const int n2 = warp + kSoftWarps * u;
             if (n2 < p.nq && ((p.row_mask >> (n2 / p.group)) & 1u)) {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h) {
@@ -687,7 +723,7 @@ __global__ void __launch_bounds__(384, 1)
                 make_float2(acc[h][0], acc[h][1]);
         }
         if (tid < NQC) tlim[tid] = tid < p.nq ? tid / p.group : -1;
-        named_bar(3, 256);
+        named_bar(kAllBar, kSoft);
         // One exponent for all rows while they are within 2^4 of each other (a part's grid then
         // reaches 2^-13 of the smallest row's largest element, and 2^-17 of the unit's), else one a
         // row.
@@ -713,7 +749,8 @@ __global__ void __launch_bounds__(384, 1)
         };
 #pragma unroll
         for (int u = 0; u < QPER; ++u) {
-          const int n2 = warp + 8 * u;
+          const int n2 = warp + kSoftWarps * u;
+          if (n2 >= NQC) continue;
           const int e = rowexp[n2], k = 7 - (one ? most : e == -1000 ? 0 : e);
           const float f = two_to(k);
 #pragma unroll
@@ -732,7 +769,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int h = 0; h < D / 64; ++h) {
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kSoftWarps; ++j) {
               const float2 w = *reinterpret_cast<const float2*>(qsum + j * D + 64 * h + 2 * lane);
               v.x += w.x;
               v.y += w.y;
@@ -765,22 +802,22 @@ __global__ void __launch_bounds__(384, 1)
               reinterpret_cast<uint32_t*>(qs + pass * Cfg::kQ + row * D)[j] = 0;
           if (lane == 0) *uniform = one ? most - 7 : kMixed;
         }
-        if (i < NQC) nrg[i] = 0.f;
+        if (i < ncol) nrg[i] = 0.f;
         // Generic-proxy writes of Q must be visible to the tensor cores (async proxy).
         fence_proxy_async_smem();
         mbar_arrive(qready);
-        named_bar(3, 256);   // (what was written above is read by all)
+        named_bar(kAllBar, kSoft);   // (what was written above is read by all)
       }
 
       // ---------------------------------------------------------- its tiles
-      uint64_t nr2[kSmemRef ? 1 : NQC / 2];
-      uint64_t ls2[NQC / 2];   // row sums
+      uint64_t nr2[kSmemRef ? 1 : NC / 2];
+      uint64_t ls2[NC / 2];   // row sums
 #pragma unroll
-      for (int c = 0; c < NQC / 2; ++c) {
+      for (int c = 0; c < NC / 2; ++c) {
         if constexpr (!kSmemRef) nr2[c] = 0;
         ls2[c] = 0;
       }
-      uint64_t hollow = NQC == 64 ? ~0ull : (1ull << NQC) - 1;   // columns without a reference
+      uint64_t hollow = ncol == 64 ? ~0ull : (1ull << ncol) - 1;   // columns without a reference
       const int uni = *uniform;
       const bool mixed = uni == kMixed;
       const float scale0 = mixed ? p.scale_log2 : p.scale_log2 * two_to(uni);
@@ -788,7 +825,7 @@ __global__ void __launch_bounds__(384, 1)
       float* srow = CAPTURE ? p.scores + (size_t(b) * p.hkv + g) * p.score_stride : nullptr;
       int Lcap = L;
       if (CAPTURE && L > p.score_stride) {
-        if (i == 0 && grp == 0) set_error(p.err, kErrDeviceFault);
+        if (tid == 0) set_error(p.err, kErrDeviceFault);
         Lcap = p.score_stride;
       }
       bool any = false;   // this group has a tile of the unit
@@ -805,26 +842,26 @@ __global__ void __launch_bounds__(384, 1)
         phys1 = load_page(at, t + 4);
         const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
         const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
-        // S of this tile follows PV of the group's last tile in the tensor pipe: P's buffer is free
-        // then, and O^T may be rescaled
-        const bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
+        bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
         tc_fence_after();
         // z of all columns less their references, two to a register pair
-        uint64_t y2[NQC / 2];
+        uint64_t y2[NC / 2];
         float cx[8] = {};   // the capture columns
         bool left = false, forced = hollow != 0;
         while (true) {
           bool need = forced;
           if (okt) {
-            if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-            load_all(tl + s_col, y2);
+            if constexpr (CAPTURE) {
+              if (half == 0) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+            }
+            load_all(tl + s_col + col0, y2);
             if (mixed) {
 #pragma unroll
-              for (int c = 0; c < NQC / 2; ++c)
-                y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac)[c]);
+              for (int c = 0; c < NC / 2; ++c)
+                if (has(c / 4)) y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac + col0)[c]);
             }
 #pragma unroll
-            for (int c = 0; c < NQC / 4; ++c) {
+            for (int c = 0; c < NC / 4; ++c) {
               ulonglong2 r;
               if constexpr (kSmemRef)
                 r = reinterpret_cast<const ulonglong2*>(nrg)[c];
@@ -835,63 +872,68 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
 #pragma unroll
-              for (int c = 0; c < NQC / 2; ++c) {
+              for (int c = 0; c < NC / 2; ++c) {
+                if (!has(c / 4)) continue;
                 float a, d;
                 unpair_f32(y2[c], a, d);
-                y2[c] = pair_f32(pos > L + tlim[2 * c] ? -INFINITY : a,
-                                 pos > L + tlim[2 * c + 1] ? -INFINITY : d);
+                y2[c] = pair_f32(pos > L + tlim[col0 + 2 * c] ? -INFINITY : a,
+                                 pos > L + tlim[col0 + 2 * c + 1] ? -INFINITY : d);
               }
             }
             float ym[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < NQC / 2; ++c) {
+            for (int c = 0; c < NC / 2; ++c) {
+              if (!has(c / 4)) continue;
               float a, d;
               unpair_f32(y2[c], a, d);
               ym[c & 1] = fmaxf(fmaxf(ym[c & 1], a), d);
             }
             need |= fmaxf(ym[0], ym[1]) > kTop;
           }
+          // PV of the group's last tile is done with P's buffer, and with O^T
+          okt = okt && (it < 2 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
           const bool all_ok = __all_sync(0xffffffffu, okt);
-          if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
-          if (!named_bar_any(1 + grp, 128, need || !okt)) break;
-          const int* vt = votes + (k & 1) * 8 + grp * 4;
+          if (lane == 0) votes[(k & 1) * 8 * HN + team * 4 + q4] = all_ok ? 0 : 1;
+          if (!named_bar_any(1 + team, 128, need || !okt)) break;
+          const int* vt = votes + (k & 1) * 8 * HN + team * 4;
           if (vt[0] | vt[1] | vt[2] | vt[3]) {
             left = true;
             break;
           }
           // Raise: column maxima over the group's 128 positions
-          float* cm = colmax + grp * 4 * NQC;
+          tc_fence_after();
+          float* cm = colmax + grp * 4 * NQC + col0;
 #pragma unroll
-          for (int c = 0; c < NQC / 8; ++c) {
+          for (int c = 0; c < NC / 8; ++c) {
+            if (!has(c)) continue;
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) unpair_f32(y2[4 * c + e / 2], v[e], v[e + 1]);
             const float top = reduce_chunk(v, [](float a, float d) { return fmaxf(a, d); });
             if ((lane & 3) == 0) cm[q4 * NQC + 8 * c + (lane >> 2)] = top;
           }
-          named_bar(1 + grp, 128);
+          named_bar(1 + team, 128);
           // a column's new reference, at least kRaise below its largest z (cm is relative to the old
           // one), and the factor that its sums take
-          if (i < NQC) {
+          if (i < ncol) {
             const float nro = nrg[i];
             const float top = fmaxf(fmaxf(cm[i], cm[NQC + i]), fmaxf(cm[2 * NQC + i], cm[3 * NQC + i]));
             const float old = ((hollow >> i) & 1) ? kEmptyMax : -nro;
             const float now = fmaxf(old, top - nro - kRaise);
-            facs[grp * NQC + i] = ex2(old - now);
+            facs[grp * NQC + col0 + i] = ex2(old - now);
             nrg[i] = now == kEmptyMax ? 0.f : -now;
-            colmax[grp * 4 * NQC + i] = now;   // (its own column: read above by this thread alone)
+            cm[i] = now;   // (its own column: read above by this thread alone)
           }
-          named_bar(1 + grp, 128);
+          named_bar(1 + team, 128);
           // (columns with masked logits only stay without one until the next tile)
-          hollow = 0;
+          hollow = __ballot_sync(0xffffffffu, lane < ncol && cm[lane] == kEmptyMax);
+          if constexpr (NC > 32)
+            hollow |= uint64_t(__ballot_sync(0xffffffffu, lane + 32 < ncol && cm[lane + 32] == kEmptyMax))
+                      << 32;
+          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC + col0);
 #pragma unroll
-          for (int c0 = 0; c0 < NQC; c0 += 32) {
-            const bool still = c0 + lane < NQC && colmax[grp * 4 * NQC + c0 + lane] == kEmptyMax;
-            hollow |= uint64_t(__ballot_sync(0xffffffffu, still)) << c0;
-          }
-          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC);
-#pragma unroll
-          for (int c = 0; c < NQC / 4; ++c) {
+          for (int c = 0; c < NC / 4; ++c) {
+            if (!has(c / 2)) continue;
             const float4 v = fc[c];
             ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
             ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
@@ -903,12 +945,12 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (any) {
 #pragma unroll 1
-            for (int c = 0; c < NQC / 8; ++c) {
+            for (int c = 0; c < ncol / 8; ++c) {
               const float4 a = fc[2 * c], d = fc[2 * c + 1];
 #pragma unroll
               for (int part = 0; part < Cfg::kPCols / NQC; ++part) {
                 float v8[8];
-                tmem_ld8(tl + o_col + part * NQC + 8 * c, v8);
+                tmem_ld8(tl + o_col + col0 + part * NQC + 8 * c, v8);
                 tmem_ld_wait();
                 v8[0] *= a.x;
                 v8[1] *= a.y;
@@ -918,19 +960,19 @@ __global__ void __launch_bounds__(384, 1)
                 v8[5] *= d.y;
                 v8[6] *= d.z;
                 v8[7] *= d.w;
-                tmem_st8(tl + o_col + part * NQC + 8 * c, v8);
+                tmem_st8(tl + o_col + col0 + part * NQC + 8 * c, v8);
               }
             }
             tmem_st_wait();
           }
           forced = false;
-          named_bar(1 + grp, 128);   // colmax and the factors are read
+          named_bar(1 + team, 128);   // colmax and the factors are read
         }
         if (left) {
           ok = false;
           break;
         }
-        if (CAPTURE && pos < Lcap) {
+        if (CAPTURE && half == 0 && pos < Lcap) {
           if constexpr (kSideS) {
 #pragma unroll
             for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
@@ -941,35 +983,46 @@ __global__ void __launch_bounds__(384, 1)
         // eight bytes of position i's row, 16-byte chunks swizzled (columns that fill up N are never
         // read; their P may be anything)
         uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * 128;
+        // (a step for all columns before the next: one column's steps are a chain of 70 clocks)
+        uint32_t x[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NQC / 8; ++c) {
-          uint32_t x[4];
+        for (int j = 0; j < NC / 2; ++j) {
+          if (!has(j / 4)) continue;
+          float p0, p1;
+          unpair_f32(y2[j], p0, p1);
+          y2[j] = pair_f32(ex2(p0), ex2(p1));
+        }
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            float p0, p1;
-            unpair_f32(y2[4 * c + e / 2], p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            ls2[4 * c + e / 2] = fma_f32x2(pair_f32(p0, p1), un2, ls2[4 * c + e / 2]);
-            x[e / 2] = pack_f16x2(p0, p1);
+        for (int j = 0; j < NC / 2; ++j) {
+          if (!has(j / 4)) continue;
+          float p0, p1;
+          unpair_f32(y2[j], p0, p1);
+          ls2[j] = fma_f32x2(y2[j], un2, ls2[j]);
+          x[j] = pack_f16x2(p0, p1);
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          if (part == 2) {
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j)
+              if (has(j / 4)) x[j] += 0x00800080u;   // (finite, >= 0: a carry rounds up)
           }
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            if (part == 2) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] += 0x00800080u;   // (finite, >= 0: a carry rounds up)
-            }
-            const uint2 code = make_uint2(__byte_perm(x[0], x[1], 0x7531), __byte_perm(x[2], x[3], 0x7531));
-            if (part < 2) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = sub_f16x2(x[e], x[e] & 0xff00ff00u);
-            }
-            const int byte = kSideP ? part * NQC + 8 * c : part * 128 + 8 * c;
+          for (int c = 0; c < NC / 8; ++c) {
+            if (!has(c)) continue;
+            const int byte = (kSideP ? part * NQC : part * 128) + col0 + 8 * c;
             *reinterpret_cast<uint2*>(prow + (byte >> 7) * 16384 +
-                                      ((((byte & 127) >> 4) ^ (i & 7)) << 4) + (byte & 8)) = code;
+                                      ((((byte & 127) >> 4) ^ (i & 7)) << 4) + (byte & 8)) =
+                make_uint2(__byte_perm(x[4 * c], x[4 * c + 1], 0x7531),
+                           __byte_perm(x[4 * c + 2], x[4 * c + 3], 0x7531));
+          }
+          if (part < 2) {
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j)
+              if (has(j / 4)) x[j] = sub_f16x2(x[j], x[j] & 0xff00ff00u);
           }
         }
-        if (pos > L + p.gamma) {
+        if (half == 0 && pos > L + p.gamma) {
           // a cache slot behind the window: zero its V row, whose codes may be NaN
           const uint32_t vs = it % VS;
           if (mbar_wait_bounded(vfull(vs), (it / VS) & 1)) {
@@ -988,25 +1041,23 @@ __global__ void __launch_bounds__(384, 1)
       // ---------------------------------------------------------- the unit's end
       // row sums over the group's 128 positions
 #pragma unroll
-      for (int c = 0; c < NQC / 8; ++c) {
+      for (int c = 0; c < NC / 8; ++c) {
+        if (!has(c)) continue;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) unpair_f32(ls2[4 * c + e / 2], v[e], v[e + 1]);
         const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
-        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
+        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + col0 + 8 * c + (lane >> 2)] = sum;
       }
-      // The group's last PV completes its O^T.  Group 0 finishes the first half of the columns, group
-      // 1 the second; each hands its part of the other half over in P's buffers, once both groups'
-      // PVs have read them.
+      // The group's last PV completes its O^T.
       if (any && ok) {
         const uint32_t last = it0 + uint32_t(tiles) - 1 - ((it0 + uint32_t(tiles) - 1 - uint32_t(grp)) & 1);
         if (!mbar_wait_bounded(pvdone(grp), (last >> 1) & 1)) ok = false;
       }
       tc_fence_after();
-      if (i < NQC && ((hollow >> i) & 1)) colmax[grp * 4 * NQC + i] = kEmptyMax;
-      else if (i < NQC) colmax[grp * 4 * NQC + i] = -nrg[i];
+      if (i < ncol) colmax[grp * 4 * NQC + col0 + i] = ((hollow >> i) & 1) ? kEmptyMax : -nrg[i];
       tc_fence_before();
-      if (named_bar_any(3, 256, !ok)) {   // both groups leave together
+      if (named_bar_any(kAllBar, kSoft, !ok)) {   // all teams leave together
         if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
         break;
       }
@@ -1021,22 +1072,10 @@ __global__ void __launch_bounds__(384, 1)
         colL[tid] = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
                     w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
       }
-      float* hand = reinterpret_cast<float*>(smem + Cfg::kOffP);   // [NQC][D]
-      // groups with a tile
-      const bool mine = any, other = tiles > 1 || (((it0 ^ uint32_t(grp)) & 1) != 0);
-      constexpr int kChunks = NQC / 8, kHalf = (kChunks + 1) / 2;
-      const int own0 = grp ? kHalf : 0, own1 = grp ? kChunks : kHalf;
-      if (mine) {
-#pragma unroll 1
-        for (int c = grp ? 0 : kHalf; c < (grp ? kHalf : kChunks); ++c) {
-          float v8[8];
-          load_o(c, v8);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (dim >= 0) hand[(8 * c + e) * D + dim] = v8[e];
-        }
-      }
-      named_bar(3, 256);
+      // groups with a tile of the unit
+      const bool has0 = tiles > 1 || !(it0 & 1), has1 = tiles > 1 || (it0 & 1);
+      named_bar(kAllBar, kSoft);
+      tc_fence_after();   // (the other group's PVs are done: its threads waited, above)
       // the CTAs that hold tiles of the unit
       const long long tile0 = unit0 + kUnitTiles;
       const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
@@ -1049,16 +1088,17 @@ __global__ void __launch_bounds__(384, 1)
       // where that is another; of a unit's CTAs only the first can have it as its last.
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
+      // every team finishes some columns, from both groups' O^T
 #pragma unroll 1
-      for (int c = own0; c < own1; ++c) {
-        float v8[8] = {};
-        if (mine) load_o(c, v8);
+      for (int c = team; c < NQC / 8; c += 2 * HN) {
+        float a[8] = {}, d[8] = {};
+        if (has0) load_o(0, c, a);
+        if (has1) load_o(1, c, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int n2 = 8 * c + e;
           if (dim < 0 || n2 >= p.nq) continue;
-          float v = mine ? v8[e] * wgt[grp * NQC + n2] : 0.f;
-          if (other) v = fmaf(hand[n2 * D + dim], wgt[(grp ^ 1) * NQC + n2], v);
+          const float v = a[e] * wgt[n2] + d[e] * wgt[NQC + n2];
           if (c0 == c1)
             out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
           else
@@ -1069,17 +1109,17 @@ __global__ void __launch_bounds__(384, 1)
       if (c0 != c1 && tid < p.nq)
         reinterpret_cast<float2*>(p.part_ml)[slot * p.nq + tid] = make_float2(colM[tid], colL[tid]);
       if (c0 != c1) {
-        named_bar(3, 256);
+        named_bar(kAllBar, kSoft);
         // (released and acquired by one thread: the barriers carry that to and from the others)
         if (tid == 0) *flag = ticket_acq_rel(&p.tickets[unit]) == c1 - c0;
-        named_bar(3, 256);
+        named_bar(kAllBar, kSoft);
         if (*flag) {
           // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m), in one pass
           // over the pieces with the running maximum.  All of a thread's elements have their loads in
           // flight together.
           const int pieces = c1 - c0 + 1;
           const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-          constexpr int E = (NQC * (D / 4) + 255) / 256;
+          constexpr int E = (NQC * (D / 4) + kSoft - 1) / kSoft;
           float M[E], sum[E];
           float4 acc[E];
 #pragma unroll
@@ -1095,7 +1135,7 @@ __global__ void __launch_bounds__(384, 1)
             float4 v[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-              const int e = tid + 256 * j, n2 = min(e / (D / 4), p.nq - 1);
+              const int e = tid + kSoft * j, n2 = min(e / (D / 4), p.nq - 1);
               m[j] = __ldcg(ml + rows + n2);
               v[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (rows + n2) * D) + e % (D / 4));
             }
@@ -1112,7 +1152,7 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int j = 0; j < E; ++j) {
-            const int e = tid + 256 * j, n2 = e / (D / 4);
+            const int e = tid + kSoft * j, n2 = e / (D / 4);
             if (n2 >= p.nq) continue;
             const float inv = 1.f / sum[j];
             reinterpret_cast<uint2*>(out_row(n2))[e % (D / 4)] =
@@ -1122,7 +1162,7 @@ __global__ void __launch_bounds__(384, 1)
           if (tid == 0) p.tickets[unit] = 0;
         }
       }
-      named_bar(3, 256);   // the buffers and columns are free again
+      named_bar(kAllBar, kSoft);   // the buffers and columns are free again
       unit0 += at.tiles + kUnitTiles;
       it0 += uint32_t(tiles);
       next_unit(at, tiles);
@@ -1131,7 +1171,7 @@ __global__ void __launch_bounds__(384, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == kSoftWarps + 2) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }
@@ -1149,7 +1189,7 @@ static cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(384, 1, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
