@@ -5,12 +5,11 @@
 // sequences hold, not by what their tables could: the 128-position tiles of all (sequence, KV
 // head) units stand in one row, and each CTA (one an SM) takes an equal run of it, whole units or
 // pieces, with the K/V stream going on from one unit to the next.  Twelve
-// warps, or twenty with more than 32 columns:
-//   softmax    two groups alternate tiles, each of one team of four warps or (wide) of two that halve
-//              the columns; a thread owns a position of a tile, and a head dimension of O^T.  They
-//              also build the query operand of a unit and finish it.
-//   producers  two warps, K and V: 8 pages a tile by TMA into rings, block-table entries prefetched
-//   MMA        one warp issues
+// warps:
+//   0-7   two softmax groups of four warps that alternate tiles; a thread owns a position of a tile,
+//         and a head dimension of O^T.  They also build the query operand of a unit and finish it.
+//   8, 9  TMA producers: 8 pages a tile into K and V rings, block-table entries prefetched
+//   10    issues the MMAs
 //
 //   S^T[128 pos x N] = K Q^T   kind::f8f6f4, M = 128: K's codes go to the tensor cores as the
 //       TMA left them.  A query row, scaled by a power of two 2^k, is the sum of two e4m3
@@ -50,6 +49,7 @@ namespace vegas {
 namespace {
 constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P at a raised reference
 constexpr int kCapParts = 6;
+constexpr int kSoftWarps = 8, kWarps = 12, kSoft = 32 * kSoftWarps, kThreads = 32 * kWarps;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
 // reference and end), and a CTA takes part for kLeastRun tiles or more.
 constexpr int kUnitTiles = 8, kLeastRun = 4;
@@ -139,6 +139,106 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v) {
         : "memory");
   }
 }
+// The same of two column ranges at once.
+template <int N>
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v, uint32_t b, uint64_t* w) {
+  if constexpr (N == 8) {
+    asm volatile(
+        "{\n .reg .b32 t<16>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7}, [%8];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t8, t9, t10, t11, t12, t13, t14, t15}, [%9];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(w[0]), "=l"(w[1]), "=l"(w[2]),
+          "=l"(w[3])
+        : "r"(a), "r"(b)
+        : "memory");
+  }
+  if constexpr (N == 16) {
+    asm volatile(
+        "{\n .reg .b32 t<32>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15}, [%16];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t16, t17, t18, t19, t20, t21, t22, t23, "
+        "t24, t25, t26, t27, t28, t29, t30, t31}, [%17];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7]), "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3]), "=l"(w[4]), "=l"(w[5]),
+          "=l"(w[6]), "=l"(w[7])
+        : "r"(a), "r"(b)
+        : "memory");
+  }
+  if constexpr (N == 24) {
+    asm volatile(
+        "{\n .reg .b32 t<48>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15}, [%24];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t16, t17, t18, t19, t20, t21, t22, t23}, [%25];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "t24, t25, t26, t27, t28, t29, t30, t31, "
+        "t32, t33, t34, t35, t36, t37, t38, t39}, [%26];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "t40, t41, t42, t43, t44, t45, t46, t47}, [%27];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
+        " mov.b64 %16, {t32, t33}; mov.b64 %17, {t34, t35}; mov.b64 %18, {t36, t37}; mov.b64 %19, {t38, t39};\n"
+        " mov.b64 %20, {t40, t41}; mov.b64 %21, {t42, t43}; mov.b64 %22, {t44, t45}; mov.b64 %23, {t46, t47};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(w[0]),
+          "=l"(w[1]), "=l"(w[2]), "=l"(w[3]), "=l"(w[4]), "=l"(w[5]), "=l"(w[6]), "=l"(w[7]),
+          "=l"(w[8]), "=l"(w[9]), "=l"(w[10]), "=l"(w[11])
+        : "r"(a), "r"(a + 16), "r"(b), "r"(b + 16)
+        : "memory");
+  }
+  if constexpr (N == 32) {
+    asm volatile(
+        "{\n .reg .b32 t<64>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "t0, t1, t2, t3, t4, t5, t6, t7, "
+        "t8, t9, t10, t11, t12, t13, t14, t15, "
+        "t16, t17, t18, t19, t20, t21, t22, t23, "
+        "t24, t25, t26, t27, t28, t29, t30, t31}, [%32];\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "t32, t33, t34, t35, t36, t37, t38, t39, "
+        "t40, t41, t42, t43, t44, t45, t46, t47, "
+        "t48, t49, t50, t51, t52, t53, t54, t55, "
+        "t56, t57, t58, t59, t60, t61, t62, t63}, [%33];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
+        " mov.b64 %16, {t32, t33}; mov.b64 %17, {t34, t35}; mov.b64 %18, {t36, t37}; mov.b64 %19, {t38, t39};\n"
+        " mov.b64 %20, {t40, t41}; mov.b64 %21, {t42, t43}; mov.b64 %22, {t44, t45}; mov.b64 %23, {t46, t47};\n"
+        " mov.b64 %24, {t48, t49}; mov.b64 %25, {t50, t51}; mov.b64 %26, {t52, t53}; mov.b64 %27, {t54, t55};\n"
+        " mov.b64 %28, {t56, t57}; mov.b64 %29, {t58, t59}; mov.b64 %30, {t60, t61}; mov.b64 %31, {t62, t63};\n"
+        "}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+          "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]),
+          "=l"(v[13]), "=l"(v[14]), "=l"(v[15]), "=l"(w[0]), "=l"(w[1]), "=l"(w[2]),
+          "=l"(w[3]), "=l"(w[4]), "=l"(w[5]), "=l"(w[6]), "=l"(w[7]), "=l"(w[8]), "=l"(w[9]),
+          "=l"(w[10]), "=l"(w[11]), "=l"(w[12]), "=l"(w[13]), "=l"(w[14]), "=l"(w[15])
+        : "r"(a), "r"(b)
+        : "memory");
+  }
+}
 // Whether the phase with the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -193,10 +293,13 @@ struct Kv8Cfg {
   static constexpr int NS = (kCap0 + kCap + 15) / 16 * 16;   // N of S
   // PV: three parts side by side, or one after the other (NQC = 64)
   static constexpr bool kSideP = NQC <= 56;
-  static constexpr int kPCols = kSideP ? 3 * NQC : NQC;
+  // columns from one part to the next: whole 16-byte chunks, where P's room holds them
+  static constexpr int PS = !kSideP ? 128 : NQC == 40 ? 40 : (NQC + 15) / 16 * 16;
+  static constexpr int kParts = kSideP ? 3 : 1;       // accumulators
+  static constexpr int kPCols = kSideP ? 3 * PS : NQC;
   static constexpr int NP = (kPCols + 15) / 16 * 16;  // N of PV
   static constexpr int kTile = 128 * D;               // one K tile (and one V tile): 8 pages
-  // P of a position: rows of 128 bytes in blocks of 128 positions, [part][NQC] over the blocks, or a
+  // P of a position: rows of 128 bytes in blocks of 128 positions, [part][PS] over the blocks, or a
   // block a part
   static constexpr int kBlocks = kSideP ? (NP + 127) / 128 : 3;
   static constexpr int kP = kBlocks * 128 * 128;
@@ -215,17 +318,12 @@ struct Kv8Cfg {
   static constexpr int kOffBar = kOffQ + kPasses * kQ;
   static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 2;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  // Softmax threads: two groups of HN teams of 128; a team has up to NC columns, HN > 1 keeps a
-  // thread's share of wide tiles in registers and halves its chain.
-  static constexpr int HN = 1;
-  static constexpr int NC = HN == 2 ? (NQC / 8 + 1) / 2 * 8 : NQC;
-  static constexpr int kSoft = 256 * HN, kThreads = kSoft + 128;
-  // misc: 16 words; votes[2][teams][4]; warp sums[20] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
+  // misc: 16 words; votes[2][2][4]; warp sums[12] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
   // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
-  static constexpr size_t kMisc = 64 + 128 + 160 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
+  static constexpr size_t kMisc = 64 + 64 + 96 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(8 * HN * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
+  static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
 };
 
 // A place in the row of tiles: tile t of KV head g of sequence b.
@@ -240,15 +338,13 @@ struct Place {
 };
 
 template <int D, int NQC, bool CAPTURE>
-__global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const VerifyKv8Params p) {
   using Cfg = Kv8Cfg<D, NQC, CAPTURE>;
   constexpr int KS = Cfg::KS, VS = Cfg::VS, NS = Cfg::NS, NP = Cfg::NP;
   constexpr bool kSideS = Cfg::kSideS, kSideP = Cfg::kSideP;
-  constexpr int HN = Cfg::HN, NC = Cfg::NC, kSoft = Cfg::kSoft, kThreads = Cfg::kThreads;
-  constexpr int kSoftWarps = kSoft / 32, kWarps = kThreads / 32;
-  constexpr int kAllBar = 5;   // named barriers: 1 + team, and all softmax threads
+  constexpr int kAllBar = 3;   // named barriers: 1 + group, and all softmax threads
   static_assert(NQC % 8 == 0 && (D == 64 || D == 128), "columns, head_dim");
 
   griddep_launch_dependents();
@@ -274,9 +370,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
   int* flag = reinterpret_cast<int*>(misc + 4);
   int* capexp = reinterpret_cast<int*>(misc + 8);
   int* uniform = reinterpret_cast<int*>(misc + 12);
-  int* votes = reinterpret_cast<int*>(misc + 64);                // [2][teams][4]
-  long long* wsum = reinterpret_cast<long long*>(misc + 192);    // [20] a warp's sequences
-  float* colmax = reinterpret_cast<float*>(misc + 352);          // [2][4][NQC]
+  int* votes = reinterpret_cast<int*>(misc + 64);                // [2][2][4]
+  long long* wsum = reinterpret_cast<long long*>(misc + 128);    // [12] a warp's sequences
+  float* colmax = reinterpret_cast<float*>(misc + 224);          // [2][4][NQC]
   float* colsum = colmax + 8 * NQC;                              // [2][4][NQC]
   float* colfac = colsum + 8 * NQC;                              // [NQC] 2^-k of rows of unlike size
   float* nrefs = colfac + NQC;                                   // [2][NQC] -reference
@@ -303,8 +399,8 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull(i), 1);
-      mbar_init(sread(i), 128 * HN);
-      mbar_init(pready(i), 128 * HN);
+      mbar_init(sread(i), 128);
+      mbar_init(pready(i), 128);
       mbar_init(pvdone(i), 1);
     }
     mbar_init(qready, kSoft);
@@ -420,10 +516,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
   };
   bool ok = true;
 
-  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that; 640 with 96: 4 x
-  // 128 x 104 + 128 x 64.
+  // 384 threads launch with 168 registers each: 2 x 128 x 216 + 128 x 72 are that.
   if (warp >= kSoftWarps) {
-    leave_registers<HN == 2 ? 64 : 72>();
+    leave_registers<72>();
     if (warp < kSoftWarps + 2) {
       // ---------------------------------------------------------- producers: K, V
       // Lane j < 8 loads page j of a tile; a page past the sequence's last is that one again (its
@@ -592,13 +687,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
       (void)mbar_wait_bounded(drain, 0);
     }
   } else {
-    take_registers<HN == 2 ? 104 : 216>();
-    // ------------------------------------------------------------ softmax teams
-    const int team = warp >> 2, grp = team & 1;   // group 0: even tiles, 1: odd tiles
-    const int half = team >> 1;               // the team's columns: col0 .. col0 + ncol - 1
-    const int col0 = half * NC, ncol = half ? NQC - NC : NC;
-    // chunk c of a team's columns is there
-    auto has = [&](int c) { return 8 * c < NQC - NC * (HN - 1) || half == 0; };
+    take_registers<216>();
+    // ------------------------------------------------------------ softmax groups
+    const int grp = warp >> 2;                // 0: even tiles, 1: odd tiles
     const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
     const int i = 32 * q4 + lane;             // tile position owned
     // head dimension owned: M = 64 puts 16 rows in each quarter of the lanes
@@ -607,7 +698,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
     const uint32_t s_col = Cfg::kSCol * grp, o_col = 2 * Cfg::kSCol + Cfg::kOCol * grp;
     // Column references r (P = 2^(z - r)) are kept as -r in shared memory, up to 32 columns in
     // registers too; 0 while `hollow` says that the column has seen no unmasked logit.
-    constexpr bool kSmemRef = NC > 32;
+    constexpr bool kSmemRef = NQC > 32;
     constexpr int QPER = (NQC + kSoftWarps - 1) / kSoftWarps;
     uint8_t* qs = smem + Cfg::kOffQ;
     // Element (n, k) of a query part: n * D + the 16-byte chunk k / 16 swizzled with the row.
@@ -617,19 +708,17 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
     };
     const __nv_bfloat16* qbase = reinterpret_cast<const __nv_bfloat16*>(p.q);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
-    float* nrg = nrefs + grp * NQC + col0;   // of the team's columns
+    float* nrg = nrefs + grp * NQC;
     // (pages outside the pool: the producers record and clamp them)
-    auto load_page = [&](const Place& u, int t) {   // volatile, here and below: the compiler may not
-      const int page = min(8 * t + (i >> 4), (u.L + T - 1) >> 4);   // move the loads down to their uses
+    // (volatile: the compiler may not move the loads down to their uses)
+    auto load_page = [&](const int32_t* row, int last, int t) {
       int v;
-      asm volatile("ld.global.nc.s32 %0, [%1];"
-                   : "=r"(v)
-                   : "l"(p.block_table + size_t(u.b) * p.max_pages + page));
+      asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(row + min(8 * t + (i >> 4), last)));
       return v;
     };
-    auto load_scale = [&](const uint8_t* scales, int phys, int g) {
+    auto load_scale = [&](const uint8_t* scales, int phys) {   // scales: of the unit's KV head
       uint32_t v;
-      const size_t block = size_t(phys < 0 || phys >= p.num_pages ? 0 : phys) * p.hkv + g;
+      const uint32_t block = uint32_t(uint32_t(phys) < uint32_t(p.num_pages) ? phys : 0) * p.hkv;
       asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(scales + block));
       return v;
     };
@@ -639,31 +728,31 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
       tmem_ld8(at, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int part = 1; part < Cfg::kPCols / NQC; ++part) {
+      for (int part = 1; part < Cfg::kParts; ++part) {
         float w8[8];
-        tmem_ld8(at + part * NQC, w8);
+        tmem_ld8(at + part * Cfg::PS, w8);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += w8[e];
       }
     };
-    // S of the team's columns in pairs, the parts added
-    auto load_all = [&](uint32_t at, uint64_t (&y2)[NC / 2]) {
-      constexpr int kFirst = NC < 32 ? NC : 32, kRest = NC > 32 ? NC - 32 : 8;
-      uint64_t low[16];
-      tmem_ld_pairs<kFirst>(at, y2);
+    // S of all columns in pairs, the parts added
+    auto load_all = [&](uint32_t at, uint64_t (&y2)[NQC / 2]) {
+      constexpr int kFirst = NQC < 32 ? NQC : 32, kRest = NQC > 32 ? NQC - 32 : 8;
       if constexpr (kSideS) {
-        tmem_ld_pairs<kFirst>(at + NQC, low);
+        uint64_t low[16];
+        tmem_ld_pairs<kFirst>(at, y2, at + NQC, low);
 #pragma unroll
         for (int j = 0; j < kFirst / 2; ++j) y2[j] = add_f32x2(y2[j], low[j]);
-      }
-      if constexpr (NC > 32) {
-        tmem_ld_pairs<kRest>(at + 32, y2 + 16);
-        if constexpr (kSideS) {
-          tmem_ld_pairs<kRest>(at + NQC + 32, low);
+        if constexpr (NQC > 32) {
+          tmem_ld_pairs<kRest>(at + 32, y2 + 16, at + NQC + 32, low);
 #pragma unroll
           for (int j = 0; j < kRest / 2; ++j) y2[16 + j] = add_f32x2(y2[16 + j], low[j]);
         }
+      } else {   // (more than 40 columns)
+        tmem_ld_pairs<kRest>(at, y2, at + kRest, y2 + kRest / 2);
+        if constexpr (NQC - 2 * kRest > 0)
+          tmem_ld_pairs<NQC - 2 * kRest>(at + 2 * kRest, y2 + kRest);
       }
     };
 
@@ -672,14 +761,17 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
     uint32_t it0 = 0;             // the CTA's tile with which the unit begins
     for (int tiles = at.here(); tiles > 0; tiles = at.here()) {
       const int L = at.L, g = at.g, b = at.b;
+      const int32_t* row = p.block_table + size_t(b) * p.max_pages;
+      const int last_page = (L + p.gamma) >> 4;
+      const uint8_t *k_scales = p.k_scale + g, *v_scales = p.v_scale + g;
       const uint32_t first = it0 + ((it0 ^ uint32_t(grp)) & 1);   // this group's first tile
 
       // ---------------------------------------------------------- the unit's queries
       int phys1 = 0;
       uint32_t ekb, evb;
       {
-        const int phys0 = load_page(at, at.t + int(first - it0));
-        phys1 = load_page(at, at.t + int(first - it0) + 2);
+        const int phys0 = load_page(row, last_page, at.t + int(first - it0));
+        phys1 = load_page(row, last_page, at.t + int(first - it0) + 2);
         uint32_t qreg[QPER][D / 64];
 #pragma unroll
         for (int u = 0; u < QPER; ++u) {
@@ -701,8 +793,8 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
           if (lane == 0 && warp + kSoftWarps * u < NQC)
             rowexp[warp + kSoftWarps * u] = most ? max(-100, int(most >> 7) - 127) : -1000;
         }
-        ekb = load_scale(p.k_scale, phys0, g);
-        evb = load_scale(p.v_scale, phys0, g);
+        ekb = load_scale(k_scales, phys0);
+        evb = load_scale(v_scales, phys0);
         if (CAPTURE) {
           // the captured query, summed over its rows and heads: this warp's rows
           float acc[D / 64][2] = {};
@@ -802,7 +894,7 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
               reinterpret_cast<uint32_t*>(qs + pass * Cfg::kQ + row * D)[j] = 0;
           if (lane == 0) *uniform = one ? most - 7 : kMixed;
         }
-        if (i < ncol) nrg[i] = 0.f;
+        if (i < NQC) nrg[i] = 0.f;
         // Generic-proxy writes of Q must be visible to the tensor cores (async proxy).
         fence_proxy_async_smem();
         mbar_arrive(qready);
@@ -810,14 +902,14 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
       }
 
       // ---------------------------------------------------------- its tiles
-      uint64_t nr2[kSmemRef ? 1 : NC / 2];
-      uint64_t ls2[NC / 2];   // row sums
+      uint64_t nr2[kSmemRef ? 1 : NQC / 2];
+      uint64_t ls2[NQC / 2];   // row sums
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) {
+      for (int c = 0; c < NQC / 2; ++c) {
         if constexpr (!kSmemRef) nr2[c] = 0;
         ls2[c] = 0;
       }
-      uint64_t hollow = ncol == 64 ? ~0ull : (1ull << ncol) - 1;   // columns without a reference
+      uint64_t hollow = NQC == 64 ? ~0ull : (1ull << NQC) - 1;   // columns without a reference
       const int uni = *uniform;
       const bool mixed = uni == kMixed;
       const float scale0 = mixed ? p.scale_log2 : p.scale_log2 * two_to(uni);
@@ -837,53 +929,57 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
         const int pos = 128 * t + i;
         // this position's scales; the next tile's are requested, and the page after that
         const int e_k = kv8_exponent(uint8_t(ekb)), e_v = kv8_exponent(uint8_t(evb));
-        ekb = load_scale(p.k_scale, phys1, g);
-        evb = load_scale(p.v_scale, phys1, g);
-        phys1 = load_page(at, t + 4);
+        ekb = load_scale(k_scales, phys1);
+        evb = load_scale(v_scales, phys1);
+        phys1 = load_page(row, last_page, t + 4);
         const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
         const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
+        // (wide: half of the references come to registers while S is on its way, the other half under
+        // the first one's arithmetic; all of them do not fit)
+        constexpr int kPre = kSmemRef ? NQC / 4 : 1;   // pairs
+        uint64_t pre[kPre];
+        auto load_refs = [&](int from) {
+#pragma unroll
+          for (int c = 0; c < kPre; c += 2) {
+            const ulonglong2 r = reinterpret_cast<const ulonglong2*>(nrg)[(from + c) / 2];
+            pre[c] = r.x;
+            pre[c + 1] = r.y;
+          }
+        };
+        if constexpr (kSmemRef) load_refs(0);
         bool okt = ok && mbar_wait_bounded(sfull(grp), k & 1);
         tc_fence_after();
         // z of all columns less their references, two to a register pair
-        uint64_t y2[NC / 2];
+        uint64_t y2[NQC / 2];
         float cx[8] = {};   // the capture columns
         bool left = false, forced = hollow != 0;
         while (true) {
           bool need = forced;
           if (okt) {
-            if constexpr (CAPTURE) {
-              if (half == 0) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-            }
-            load_all(tl + s_col + col0, y2);
+            if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+            load_all(tl + s_col, y2);
             if (mixed) {
 #pragma unroll
-              for (int c = 0; c < NC / 2; ++c)
-                if (has(c / 4)) y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac + col0)[c]);
+              for (int c = 0; c < NQC / 2; ++c)
+                y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac)[c]);
             }
 #pragma unroll
-            for (int c = 0; c < NC / 4; ++c) {
-              ulonglong2 r;
-              if constexpr (kSmemRef)
-                r = reinterpret_cast<const ulonglong2*>(nrg)[c];
-              else
-                r = make_ulonglong2(nr2[2 * c], nr2[2 * c + 1]);
-              y2[2 * c] = add_f32x2(fma_f32x2(y2[2 * c], f2, add2), r.x);
-              y2[2 * c + 1] = add_f32x2(fma_f32x2(y2[2 * c + 1], f2, add2), r.y);
+            for (int c = 0; c < NQC / 2; ++c) {
+              if (kSmemRef && c == NQC / 4) load_refs(NQC / 4);
+              y2[c] = add_f32x2(fma_f32x2(y2[c], f2, add2), kSmemRef ? pre[kSmemRef ? c % kPre : 0] : nr2[kSmemRef ? 0 : c]);
             }
             if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
 #pragma unroll
-              for (int c = 0; c < NC / 2; ++c) {
-                if (!has(c / 4)) continue;
+              for (int c = 0; c < NQC / 2; ++c) {
                 float a, d;
                 unpair_f32(y2[c], a, d);
-                y2[c] = pair_f32(pos > L + tlim[col0 + 2 * c] ? -INFINITY : a,
-                                 pos > L + tlim[col0 + 2 * c + 1] ? -INFINITY : d);
+                y2[c] = pair_f32(pos > L + tlim[2 * c] ? -INFINITY : a,
+                                 pos > L + tlim[2 * c + 1] ? -INFINITY : d);
               }
             }
             float ym[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-              if (!has(c / 4)) continue;
+            for (int c = 0; c < NQC / 2; ++c) {
               float a, d;
               unpair_f32(y2[c], a, d);
               ym[c & 1] = fmaxf(fmaxf(ym[c & 1], a), d);
@@ -893,47 +989,45 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
           // PV of the group's last tile is done with P's buffer, and with O^T
           okt = okt && (it < 2 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
           const bool all_ok = __all_sync(0xffffffffu, okt);
-          if (lane == 0) votes[(k & 1) * 8 * HN + team * 4 + q4] = all_ok ? 0 : 1;
-          if (!named_bar_any(1 + team, 128, need || !okt)) break;
-          const int* vt = votes + (k & 1) * 8 * HN + team * 4;
+          if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
+          if (!named_bar_any(1 + grp, 128, need || !okt)) break;
+          const int* vt = votes + (k & 1) * 8 + grp * 4;
           if (vt[0] | vt[1] | vt[2] | vt[3]) {
             left = true;
             break;
           }
           // Raise: column maxima over the group's 128 positions
           tc_fence_after();
-          float* cm = colmax + grp * 4 * NQC + col0;
+          float* cm = colmax + grp * 4 * NQC;
 #pragma unroll
-          for (int c = 0; c < NC / 8; ++c) {
-            if (!has(c)) continue;
+          for (int c = 0; c < NQC / 8; ++c) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) unpair_f32(y2[4 * c + e / 2], v[e], v[e + 1]);
             const float top = reduce_chunk(v, [](float a, float d) { return fmaxf(a, d); });
             if ((lane & 3) == 0) cm[q4 * NQC + 8 * c + (lane >> 2)] = top;
           }
-          named_bar(1 + team, 128);
+          named_bar(1 + grp, 128);
           // a column's new reference, at least kRaise below its largest z (cm is relative to the old
           // one), and the factor that its sums take
-          if (i < ncol) {
+          if (i < NQC) {
             const float nro = nrg[i];
             const float top = fmaxf(fmaxf(cm[i], cm[NQC + i]), fmaxf(cm[2 * NQC + i], cm[3 * NQC + i]));
             const float old = ((hollow >> i) & 1) ? kEmptyMax : -nro;
             const float now = fmaxf(old, top - nro - kRaise);
-            facs[grp * NQC + col0 + i] = ex2(old - now);
+            facs[grp * NQC + i] = ex2(old - now);
             nrg[i] = now == kEmptyMax ? 0.f : -now;
             cm[i] = now;   // (its own column: read above by this thread alone)
           }
-          named_bar(1 + team, 128);
+          named_bar(1 + grp, 128);
           // (columns with masked logits only stay without one until the next tile)
-          hollow = __ballot_sync(0xffffffffu, lane < ncol && cm[lane] == kEmptyMax);
-          if constexpr (NC > 32)
-            hollow |= uint64_t(__ballot_sync(0xffffffffu, lane + 32 < ncol && cm[lane + 32] == kEmptyMax))
+          hollow = __ballot_sync(0xffffffffu, lane < NQC && cm[lane] == kEmptyMax);
+          if constexpr (NQC > 32)
+            hollow |= uint64_t(__ballot_sync(0xffffffffu, lane + 32 < NQC && cm[lane + 32] == kEmptyMax))
                       << 32;
-          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC + col0);
+          const float4* fc = reinterpret_cast<const float4*>(facs + grp * NQC);
 #pragma unroll
-          for (int c = 0; c < NC / 4; ++c) {
-            if (!has(c / 2)) continue;
+          for (int c = 0; c < NQC / 4; ++c) {
             const float4 v = fc[c];
             ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
             ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
@@ -943,14 +1037,15 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
               nr2[2 * c + 1] = r.y;
             }
           }
+          if constexpr (kSmemRef) load_refs(0);
           if (any) {
 #pragma unroll 1
-            for (int c = 0; c < ncol / 8; ++c) {
+            for (int c = 0; c < NQC / 8; ++c) {
               const float4 a = fc[2 * c], d = fc[2 * c + 1];
 #pragma unroll
-              for (int part = 0; part < Cfg::kPCols / NQC; ++part) {
+              for (int part = 0; part < Cfg::kParts; ++part) {
                 float v8[8];
-                tmem_ld8(tl + o_col + col0 + part * NQC + 8 * c, v8);
+                tmem_ld8(tl + o_col + part * Cfg::PS + 8 * c, v8);
                 tmem_ld_wait();
                 v8[0] *= a.x;
                 v8[1] *= a.y;
@@ -960,19 +1055,19 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
                 v8[5] *= d.y;
                 v8[6] *= d.z;
                 v8[7] *= d.w;
-                tmem_st8(tl + o_col + col0 + part * NQC + 8 * c, v8);
+                tmem_st8(tl + o_col + part * Cfg::PS + 8 * c, v8);
               }
             }
             tmem_st_wait();
           }
           forced = false;
-          named_bar(1 + team, 128);   // colmax and the factors are read
+          named_bar(1 + grp, 128);   // colmax and the factors are read
         }
         if (left) {
           ok = false;
           break;
         }
-        if (CAPTURE && half == 0 && pos < Lcap) {
+        if (CAPTURE && pos < Lcap) {
           if constexpr (kSideS) {
 #pragma unroll
             for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
@@ -984,17 +1079,15 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
         // read; their P may be anything)
         uint8_t* prow = smem + Cfg::kOffP + grp * Cfg::kP + i * 128;
         // (a step for all columns before the next: one column's steps are a chain of 70 clocks)
-        uint32_t x[NC / 2];
+        uint32_t x[NQC / 2];
 #pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          if (!has(j / 4)) continue;
+        for (int j = 0; j < NQC / 2; ++j) {
           float p0, p1;
           unpair_f32(y2[j], p0, p1);
           y2[j] = pair_f32(ex2(p0), ex2(p1));
         }
 #pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          if (!has(j / 4)) continue;
+        for (int j = 0; j < NQC / 2; ++j) {
           float p0, p1;
           unpair_f32(y2[j], p0, p1);
           ls2[j] = fma_f32x2(y2[j], un2, ls2[j]);
@@ -1004,25 +1097,27 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
         for (int part = 0; part < 3; ++part) {
           if (part == 2) {
 #pragma unroll
-            for (int j = 0; j < NC / 2; ++j)
-              if (has(j / 4)) x[j] += 0x00800080u;   // (finite, >= 0: a carry rounds up)
+            for (int j = 0; j < NQC / 2; ++j)
+              x[j] += 0x00800080u;   // (finite, >= 0: a carry rounds up)
           }
+          auto code = [&](int j) { return __byte_perm(x[j], x[j + 1], 0x7531); };
 #pragma unroll
-          for (int c = 0; c < NC / 8; ++c) {
-            if (!has(c)) continue;
-            const int byte = (kSideP ? part * NQC : part * 128) + col0 + 8 * c;
-            *reinterpret_cast<uint2*>(prow + (byte >> 7) * 16384 +
-                                      ((((byte & 127) >> 4) ^ (i & 7)) << 4) + (byte & 8)) =
-                make_uint2(__byte_perm(x[4 * c], x[4 * c + 1], 0x7531),
-                           __byte_perm(x[4 * c + 2], x[4 * c + 3], 0x7531));
+          for (int c = 0; c < NQC / 8; ++c) {
+            const int byte = part * Cfg::PS + 8 * c;
+            uint8_t* at16 = prow + (byte >> 7) * 16384 + ((((byte & 127) >> 4) ^ (i & 7)) << 4);
+            if (Cfg::PS % 16 == 0 && c % 2 == 0 && c + 1 < NQC / 8)   // (no bank twice in a phase)
+              *reinterpret_cast<uint4*>(at16) =
+                  make_uint4(code(4 * c), code(4 * c + 2), code(4 * c + 4), code(4 * c + 6));
+            else if (Cfg::PS % 16 != 0 || c % 2 == 0)
+              *reinterpret_cast<uint2*>(at16 + (byte & 8)) = make_uint2(code(4 * c), code(4 * c + 2));
           }
           if (part < 2) {
 #pragma unroll
-            for (int j = 0; j < NC / 2; ++j)
-              if (has(j / 4)) x[j] = sub_f16x2(x[j], x[j] & 0xff00ff00u);
+            for (int j = 0; j < NQC / 2; ++j)
+              x[j] = sub_f16x2(x[j], x[j] & 0xff00ff00u);
           }
         }
-        if (half == 0 && pos > L + p.gamma) {
+        if (pos > L + p.gamma) {
           // a cache slot behind the window: zero its V row, whose codes may be NaN
           const uint32_t vs = it % VS;
           if (mbar_wait_bounded(vfull(vs), (it / VS) & 1)) {
@@ -1041,13 +1136,12 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
       // ---------------------------------------------------------- the unit's end
       // row sums over the group's 128 positions
 #pragma unroll
-      for (int c = 0; c < NC / 8; ++c) {
-        if (!has(c)) continue;
+      for (int c = 0; c < NQC / 8; ++c) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) unpair_f32(ls2[4 * c + e / 2], v[e], v[e + 1]);
         const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
-        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + col0 + 8 * c + (lane >> 2)] = sum;
+        if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
       }
       // The group's last PV completes its O^T.
       if (any && ok) {
@@ -1055,9 +1149,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
         if (!mbar_wait_bounded(pvdone(grp), (last >> 1) & 1)) ok = false;
       }
       tc_fence_after();
-      if (i < ncol) colmax[grp * 4 * NQC + col0 + i] = ((hollow >> i) & 1) ? kEmptyMax : -nrg[i];
+      if (i < NQC) colmax[grp * 4 * NQC + i] = ((hollow >> i) & 1) ? kEmptyMax : -nrg[i];
       tc_fence_before();
-      if (named_bar_any(kAllBar, kSoft, !ok)) {   // all teams leave together
+      if (named_bar_any(kAllBar, kSoft, !ok)) {   // both groups leave together
         if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
         break;
       }
@@ -1088,9 +1182,9 @@ __global__ void __launch_bounds__(Kv8Cfg<D, NQC, CAPTURE>::kThreads, 1)
       // where that is another; of a unit's CTAs only the first can have it as its last.
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
-      // every team finishes some columns, from both groups' O^T
+      // each group finishes some columns, from both groups' O^T
 #pragma unroll 1
-      for (int c = team; c < NQC / 8; c += 2 * HN) {
+      for (int c = grp; c < NQC / 8; c += 2) {
         float a[8] = {}, d[8] = {};
         if (has0) load_o(0, c, a);
         if (has1) load_o(1, c, d);
@@ -1189,7 +1283,7 @@ static cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
