@@ -132,10 +132,13 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   // k_b and the tail (entries past k_b are replaced below), so the index and
   // length loads take one round trip.
   constexpr int kPer = (SparseCfg<D, NT, KV8>::kMaxRows + NTH - 1) / NTH;   // entries a thread
+  // (KV8) its table is four times as long: a split's own length ends the walks over it early
+  [[maybe_unused]] auto past = [&](int u) { return KV8 && u * NTH >= p.rows_per_split; };
   const int rbeg = rank * p.rows_per_split;
   int pos[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
+    if (past(u)) break;
     const int i = tid + u * NTH, e = rbeg + i;
     pos[u] = (i < p.rows_per_split && e < p.k_max) ? __ldcg(&p.idx[size_t(unit) * p.k_max + e]) : 0;
   }
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     int phys[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
+      if (past(u)) break;
       const int i = tid + u * NTH;
       const int e = rbeg + i;
       if (i >= nrows) pos[u] = 0;
@@ -180,6 +184,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
+      if (past(u)) break;
       if (pos[u] < 0 || pos[u] >= cap) {
         set_error(p.err, kErrDeviceFault);
         pos[u] = 0;
@@ -188,6 +193,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
+      if (past(u)) break;
       const int i = tid + u * NTH;
       if (i < nrows) {
         if (phys[u] < 0 || phys[u] >= p.num_pages) {
@@ -200,6 +206,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     if constexpr (KV8) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
+        if (past(u)) break;
         if (tid + u * NTH >= nrows) continue;
         const size_t block = size_t(phys[u]) * p.hkv + g;
         ek[u] = __ldg(&p.k_scale[block]);
@@ -252,6 +259,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     // the scale bytes were requested before the first rows; every warp reads its entries' below
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
+      if (past(u)) break;
       const int i = tid + u * NTH;
       if (i < nrows)
         exps[i] = uint16_t(uint8_t(kv8_exponent(ek[u]))) | uint16_t(uint8_t(kv8_exponent(ev[u]))) << 8;
