@@ -43,6 +43,7 @@ UNITS = [
     ("token_logprobs.cu", "token_logprobs.o", []),
     ("kv8_append.cu", "kv8_append.o", []),
     ("kv8_read.cu", "kv8_read.o", []),
+    ("draft_kv8.cu", "draft_kv8.o", []),
     ("verify_kv8.cu", "verify_kv8_d128.o", ["-DVEGAS_KV8_D=128"]),
     ("verify_kv8.cu", "verify_kv8_d64.o", ["-DVEGAS_KV8_D=64"]),
     ("verify_attn.cu", "verify_d128_c1.o", ["-DVEGAS_D=128", "-DVEGAS_CAP=1"]),

@@ -15,8 +15,9 @@ constexpr int kAttnWarps = 8;          // warps per attention CTA
 constexpr int kMaxSplits = 128;        // split-KV partials per (sequence, KV head)
 constexpr int kMaxSparseCluster = 16;  // CTAs per (sequence, KV head) in the draft kernel
 constexpr int kMaxSparseRowsPerCta = 2048;
-// (rows of half the bytes leave room for a longer table: fewer CTAs a list, and one wave of them)
-constexpr int sparse_rows_per_cta(bool kv8) { return kv8 ? 2 * kMaxSparseRowsPerCta : kMaxSparseRowsPerCta; }
+// the same of an 8-bit list (rows of half the bytes leave room for a longer table: fewer CTAs a
+// list, and one wave of them: 35 -> 22 us for 4 lists of 10,008 entries)
+constexpr int kMaxDraftKv8Rows = 2 * kMaxSparseRowsPerCta;
 
 struct VerifyParams {
   const void* q;            // bf16 [B][T][Hq][D]
@@ -69,10 +70,8 @@ constexpr int kMaxKv8Ctas = 192;   // CTAs of the 8-bit verify kernel (one an SM
 struct SparseParams {
   const void* q;            // bf16 [B][Hq][D]
   void* out;                // bf16 [B][Hq][D]
-  const void* k_cache;      // bf16 [pages][Hkv][16][D], or e4m3 with scales
+  const void* k_cache;      // bf16 [pages][Hkv][16][D]
   const void* v_cache;
-  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes of the 8-bit cache, or null
-  const uint8_t* v_scale;
   const int32_t* block_table;
   const int32_t* idx;       // [B][Hkv][k_max]
   const int32_t* k_per_seq;
@@ -85,6 +84,12 @@ struct SparseParams {
   int rows_per_split;       // list entries per CTA of the cluster
   int num_splits;           // CTAs per cluster (one cluster per unit)
   int* err;
+};
+
+// The same over the cache in 8 bits (k_cache, v_cache: e4m3 [pages][Hkv][16][D]).
+struct DraftKv8Params : SparseParams {
+  const uint8_t* k_scale;   // [pages][Hkv] exponent bytes
+  const uint8_t* v_scale;
 };
 
 struct SelectParams {
@@ -286,9 +291,12 @@ cudaError_t launch_verify_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
 
 size_t sparse_smem_bytes(int head_dim, int ntiles);
 // Clusters of `cluster` draft-kernel CTAs resident at once (0: none / error).
-int sparse_max_active_clusters(int head_dim, int ntiles, int cluster, bool kv8);
+int sparse_max_active_clusters(int head_dim, int ntiles, int cluster);
 cudaError_t launch_sparse(const SparseParams& p, int head_dim, int ntiles, int batch,
                           cudaStream_t stream);
+int draft_kv8_max_active_clusters(int head_dim, int ntiles, int cluster);
+cudaError_t launch_draft_kv8(const DraftKv8Params& p, int head_dim, int ntiles, int batch,
+                             cudaStream_t stream);
 
 cudaError_t launch_select_window(const WindowParams& p, int batch, cudaStream_t stream);
 cudaError_t launch_raw_aggregate(const RawAggParams& p, int batch, int max_len,

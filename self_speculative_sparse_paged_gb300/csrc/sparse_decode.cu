@@ -18,22 +18,16 @@
 // states meet in distributed shared memory: each CTA pushes the slices of its
 // state to the CTAs that own them, then merges and writes the slice it owns,
 // with no global scratch and no second pass.
-//
-// The 8-bit variant (KV8) does the same over the 8-bit cache: rows of half the bytes, each entry's
-// two scale exponents resolved with its row, and the warp core of kv8_core.cuh.
 #include <cooperative_groups.h>
 
-#include <type_traits>
-
 #include "kernels.h"
-#include "kv8_core.cuh"
 #include "split_merge.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace vegas {
 
-template <int D, int NT, bool KV8>
+template <int D, int NT>
 struct SparseCfg {
   // Warps, each with two 16-row groups in flight: sixteen at head_dim 64 (a
   // group is half the bytes of a head_dim-128 one; 3% faster than eight warps
@@ -41,47 +35,44 @@ struct SparseCfg {
   // than eight with three), eight with two column tiles (the shared memory
   // holds no more there).  More warps keep the same bytes in flight with more
   // groups computed at once.
-  static constexpr int kWarps = KV8 ? (D == 128 && NT == 2 ? 12 : 16) : D == 64 ? 16 : (NT == 1 ? 12 : kAttnWarps);
+  static constexpr int kWarps = D == 64 ? 16 : (NT == 1 ? 12 : kAttnWarps);
   static constexpr int kStages = 2;
-  static constexpr int kRow = KV8 ? D : D * 2 + 16;   // row stride, padded in bf16
+  static constexpr int kRow = D * 2 + 16;           // padded row stride
   static constexpr int kTile = 16 * kRow;
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kMaxRows = sparse_rows_per_cta(KV8);
+  static constexpr int kMaxRows = kMaxSparseRowsPerCta;
   static constexpr size_t kStageBytes = size_t(kWarps) * kStages * kStage;
 };
 
-template <int D, int NT, bool KV8>
+template <int D, int NT>
 constexpr size_t sparse_smem_layout_bytes() {
-  using Cfg = SparseCfg<D, NT, KV8>;
+  using Cfg = SparseCfg<D, NT>;
   return Cfg::kStageBytes                                          // stages
-         + (KV8 ? 0 : size_t(NT) * 8 * (2 * D + 16))               // Q tile
+         + size_t(NT) * 8 * (2 * D + 16)                           // Q tile
          + (size_t(Cfg::kWarps) * Cfg::kStages + 1) * 8            // mbarriers (+ receive)
-         + size_t(Cfg::kMaxRows) * (KV8 ? 6 : 4)                   // row table, scale exponents
+         + size_t(Cfg::kMaxRows) * 4                               // row table
          + size_t(NT) * 8 * (D + 2) * 4                            // CTA partial
          + (size_t(NT) * 8 * D + 4 * kMaxSparseCluster) * 4 + 16   // received output slices
          + size_t(kMaxSparseCluster) * NT * 8 * 2 * 4              // received m, l
          + 1024;
 }
-template <bool KV8>
-constexpr bool sparse_smem_fits() {
-  return sparse_smem_layout_bytes<128, 1, KV8>() <= 227 * 1024 &&
-         sparse_smem_layout_bytes<128, 2, KV8>() <= 227 * 1024 &&
-         sparse_smem_layout_bytes<64, 1, KV8>() <= 227 * 1024 &&
-         sparse_smem_layout_bytes<64, 2, KV8>() <= 227 * 1024;
-}
-static_assert(sparse_smem_fits<false>() && sparse_smem_fits<true>(), "shared memory of a draft CTA");
+static_assert(sparse_smem_layout_bytes<128, 1>() <= 227 * 1024 &&
+                  sparse_smem_layout_bytes<128, 2>() <= 227 * 1024 &&
+                  sparse_smem_layout_bytes<64, 1>() <= 227 * 1024 &&
+                  sparse_smem_layout_bytes<64, 2>() <= 227 * 1024,
+              "shared memory of a draft CTA");
 
-template <int D, int NT, bool KV8>
-__global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(SparseCfg<D, NT>::kWarps * 32, 1)
     sparse_decode_kernel(const SparseParams p) {
-  constexpr int W = SparseCfg<D, NT, KV8>::kWarps;
+  constexpr int W = SparseCfg<D, NT>::kWarps;
   constexpr int NTH = W * 32;
   constexpr int NPAD = NT * 8;
-  constexpr int STAGES = SparseCfg<D, NT, KV8>::kStages;
-  constexpr int ROW = SparseCfg<D, NT, KV8>::kRow;
-  constexpr int TILE = SparseCfg<D, NT, KV8>::kTile;
-  constexpr int STAGE = SparseCfg<D, NT, KV8>::kStage;
-  constexpr int QROW = KV8 ? 0 : 2 * D + 16;
+  constexpr int STAGES = SparseCfg<D, NT>::kStages;
+  constexpr int ROW = SparseCfg<D, NT>::kRow;
+  constexpr int TILE = SparseCfg<D, NT>::kTile;
+  constexpr int STAGE = SparseCfg<D, NT>::kStage;
+  constexpr int QROW = 2 * D + 16;
   using Tile = PaddedTile<D>;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -92,7 +83,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* stage_area = smem;
-  uint8_t* qs = smem + SparseCfg<D, NT, KV8>::kStageBytes;
+  uint8_t* qs = smem + SparseCfg<D, NT>::kStageBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(qs + NPAD * QROW);
   uint64_t* recv_bar = bars + W * STAGES;   // completes when every peer's state has landed
   int32_t* rows = reinterpret_cast<int32_t*>(recv_bar + 1);
@@ -111,9 +102,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   // every CTA has arrived).
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   griddep_begin();
-  // (KV8) entry i's exponents, K's in the low byte and V's in the high one
-  uint16_t* exps = reinterpret_cast<uint16_t*>(rows + SparseCfg<D, NT, KV8>::kMaxRows);
-  float* pM = reinterpret_cast<float*>(exps + (KV8 ? SparseCfg<D, NT, KV8>::kMaxRows : 0));   // [NPAD] CTA partial
+  float* pM = reinterpret_cast<float*>(rows + SparseCfg<D, NT>::kMaxRows);   // [NPAD] CTA partial
   float* pL = pM + NPAD;                                                 // [NPAD]
   float* pO = pL + NPAD;                                                 // [NPAD][D]
   // [CL][per] output slices received (16-byte aligned: they arrive in 16-byte stores;
@@ -131,14 +120,11 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   // The selected positions of this CTA's range are requested together with
   // k_b and the tail (entries past k_b are replaced below), so the index and
   // length loads take one round trip.
-  constexpr int kPer = (SparseCfg<D, NT, KV8>::kMaxRows + NTH - 1) / NTH;   // entries a thread
-  // (KV8) its table is four times as long: a split's own length ends the walks over it early
-  [[maybe_unused]] auto past = [&](int u) { return KV8 && u * NTH >= p.rows_per_split; };
+  constexpr int kPer = (SparseCfg<D, NT>::kMaxRows + NTH - 1) / NTH;   // entries a thread
   const int rbeg = rank * p.rows_per_split;
   int pos[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    if (past(u)) break;
     const int i = tid + u * NTH, e = rbeg + i;
     pos[u] = (i < p.rows_per_split && e < p.k_max) ? __ldcg(&p.idx[size_t(unit) * p.k_max + e]) : 0;
   }
@@ -158,7 +144,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   constexpr int QCH = NPAD * (D / 8);
   static_assert(QCH <= NTH, "one Q chunk per thread");
   uint4 qchunk = make_uint4(0, 0, 0, 0);
-  if (!KV8 && tid < QCH && tid / (D / 8) < p.group)
+  if (tid < QCH && tid / (D / 8) < p.group)
     qchunk = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
                                             (size_t(b) * p.hq + g * p.group + tid / (D / 8)) * D)
         [tid % (D / 8)];
@@ -171,12 +157,10 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   // Entry e of the list: T[e] for e < k_b, else tail_start + (e - k_b).
   // Resolved in batches: every index of a thread (loaded above), then every
   // page load.
-  [[maybe_unused]] uint8_t ek[KV8 ? kPer : 1], ev[KV8 ? kPer : 1];   // the entries' scale bytes
   {
     int phys[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      if (past(u)) break;
       const int i = tid + u * NTH;
       const int e = rbeg + i;
       if (i >= nrows) pos[u] = 0;
@@ -184,7 +168,6 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      if (past(u)) break;
       if (pos[u] < 0 || pos[u] >= cap) {
         set_error(p.err, kErrDeviceFault);
         pos[u] = 0;
@@ -193,7 +176,6 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      if (past(u)) break;
       const int i = tid + u * NTH;
       if (i < nrows) {
         if (phys[u] < 0 || phys[u] >= p.num_pages) {
@@ -203,18 +185,8 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
         rows[i] = (phys[u] * p.hkv + g) * 16 + (pos[u] & 15);
       }
     }
-    if constexpr (KV8) {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        if (past(u)) break;
-        if (tid + u * NTH >= nrows) continue;
-        const size_t block = size_t(phys[u]) * p.hkv + g;
-        ek[u] = __ldg(&p.k_scale[block]);
-        ev[u] = __ldg(&p.v_scale[block]);
-      }
-    }
   }
-  if (!KV8 && tid < QCH)
+  if (tid < QCH)
     *reinterpret_cast<uint4*>(qs + (tid / (D / 8)) * QROW + (tid % (D / 8)) * 16) = qchunk;
   __syncthreads();
 
@@ -222,15 +194,14 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   const int nmy = warp < ngroups ? (ngroups - warp + W - 1) / W : 0;
   const uint32_t stage0 = smem_u32(stage_area + warp * STAGES * STAGE);
   const uint32_t bar0 = smem_u32(&bars[warp * STAGES]);
-  const uint8_t* kc = reinterpret_cast<const uint8_t*>(p.k_cache);
-  const uint8_t* vc = reinterpret_cast<const uint8_t*>(p.v_cache);
+  const __nv_bfloat16* kc = reinterpret_cast<const __nv_bfloat16*>(p.k_cache);
+  const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(p.v_cache);
 
   // The warp copies the group's 16 K rows and 16 V rows with 16-byte cp.async
   // (consecutive lanes cover consecutive 16-byte chunks of a row); rows past
   // the range repeat the group's first row (masked later).  Each lane then
   // arrives on the stage barrier when its own copies have landed.
-  constexpr int kBytes = KV8 ? D : 2 * D;          // of a row
-  constexpr int CPR = kBytes / 16;                 // 16-byte chunks per row
+  constexpr int CPR = D / 8;                       // 16-byte chunks per row
   auto issue = [&](int i) {
     const int grp = warp + i * W;
     const int s = i % STAGES;
@@ -241,40 +212,15 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
       const int r = r32 & 15;
       const int li = grp * 16 + r;
       const int row = rows[li < nrows ? li : grp * 16];
-      const uint8_t* src = (r32 < 16 ? kc : vc) + size_t(row) * kBytes + cc * 16;
-      uint32_t at;
-      if constexpr (KV8)
-        at = r32 < 16 ? Kv8Rows<D>::k(r, cc) : TILE + Kv8Rows<D>::v(r, cc);
-      else
-        at = (r32 < 16 ? 0 : TILE) + r * ROW + cc * 16;
-      cp_async16(stage0 + s * STAGE + at, src);
+      const __nv_bfloat16* src = (r32 < 16 ? kc : vc) + size_t(row) * D + cc * 8;
+      cp_async16(stage0 + s * STAGE + (r32 < 16 ? 0 : TILE) + r * ROW + cc * 16, src);
     }
     cp_async_arrive_noinc(bar0 + s * 8);
   };
   for (int i = 0; i < min(STAGES, nmy); ++i) issue(i);
 
   uint32_t qf[D / 16][NT][2];
-  [[maybe_unused]] float col[NT][2];   // (KV8) logit units of column 2 (lane % 4) + e, log2
-  if constexpr (KV8) {
-    // the scale bytes were requested before the first rows; every warp reads its entries' below
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      if (past(u)) break;
-      const int i = tid + u * NTH;
-      if (i < nrows)
-        exps[i] = uint16_t(uint8_t(kv8_exponent(ek[u]))) | uint16_t(uint8_t(kv8_exponent(ev[u]))) << 8;
-    }
-    kv8_load_q<D, NT>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                          (size_t(b) * p.hq + g * p.group) * D,
-                      p.group, qf, col);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) col[nt][e] *= p.scale_log2;
-    __syncthreads();
-  } else {
-    load_q_frags<D, NT>(smem_u32(qs), qf);
-  }
+  load_q_frags<D, NT>(smem_u32(qs), qf);
   WarpState<D, NT> st;
   st.init();
 
@@ -288,41 +234,21 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
       break;
     }
     const int grp = warp + i * W;
+    const uint32_t kb_s[1] = {stage0 + s * STAGE};
+    const uint32_t vb_s[1] = {stage0 + s * STAGE + TILE};
+    float sc[1][NT][4];
+    tile_scores<D, NT, 1, Tile>(kb_s, qf, sc);
+    float x[1][NT][4];
     const int valid = nrows - grp * 16;   // rows of this group inside the range
-    if constexpr (KV8) {
-      float z[NT][4];
-      kv8_scores<D, NT>(stage0 + s * STAGE, qf, z);
-      float unscale[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = (lane >> 2) + 8 * j;
-        const uint16_t ex = exps[grp * 16 + (r < valid ? r : 0)];
-        const int e_v = int8_t(ex >> 8);
-        const float f = two_to(int8_t(ex)), zv = r < valid ? float(e_v) : -INFINITY;
-        unscale[j] = two_to(-e_v);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)   // (columns past the group have zero queries)
-            z[nt][2 * j + e] = fmaf(z[nt][2 * j + e], col[nt][e] * f, zv);
+      for (int k = 0; k < 4; ++k) {
+        const int r = (lane >> 2) + 8 * (k >> 1);
+        const int n = nt * 8 + 2 * (lane & 3) + (k & 1);
+        x[0][nt][k] = (r < valid && n < p.group) ? sc[0][nt][k] * p.scale_log2 : -INFINITY;
       }
-      kv8_softmax_pv<D, NT>(st, z, unscale, stage0 + s * STAGE + TILE);
-    } else {
-      const uint32_t kb_s[1] = {stage0 + s * STAGE};
-      const uint32_t vb_s[1] = {stage0 + s * STAGE + TILE};
-      float sc[1][NT][4];
-      tile_scores<D, NT, 1, Tile>(kb_s, qf, sc);
-      float x[1][NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = (lane >> 2) + 8 * (k >> 1);
-          const int n = nt * 8 + 2 * (lane & 3) + (k & 1);
-          x[0][nt][k] = (r < valid && n < p.group) ? sc[0][nt][k] * p.scale_log2 : -INFINITY;
-        }
-      tile_softmax_pv<D, NT, 1, Tile>(st, x, vb_s);
-    }
+    tile_softmax_pv<D, NT, 1, Tile>(st, x, vb_s);
     __syncwarp();
     if (i + STAGES < nmy) {
       fence_proxy_async_smem();
@@ -336,8 +262,7 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
   }
   reduce_row_sums<D, NT>(st);
   __syncthreads();
-  using Dims = std::conditional_t<KV8, Kv8Dims<D>, MmaDims>;
-  cta_merge_to_smem<D, NT, W, Dims>(st, stage_area, SparseCfg<D, NT, KV8>::kStageBytes, p.group, pM, pL, pO);
+  cta_merge_to_smem<D, NT, W>(st, stage_area, SparseCfg<D, NT>::kStageBytes, p.group, pM, pL, pO);
   __syncthreads();   // the pushes below read elements other threads merged
 
   // Cluster merge: CTA r owns the output elements [r * per, (r + 1) * per) of
@@ -409,22 +334,22 @@ __global__ void __launch_bounds__(SparseCfg<D, NT, KV8>::kWarps * 32, 1)
 
 // Launches, or with `clusters` set, reports how many clusters of p.num_splits
 // CTAs can be resident at once.
-template <int D, int NT, bool KV8>
+template <int D, int NT>
 static cudaError_t launch_sparse_one(const SparseParams& p, int batch, cudaStream_t stream,
                                      int* clusters = nullptr) {
-  constexpr size_t smem = sparse_smem_layout_bytes<D, NT, KV8>();
+  constexpr size_t smem = sparse_smem_layout_bytes<D, NT>();
   static std::atomic<uint32_t> configured{0};
   cudaError_t e = once_per_device(configured, [] {
-    cudaError_t r = cudaFuncSetAttribute(sparse_decode_kernel<D, NT, KV8>,
+    cudaError_t r = cudaFuncSetAttribute(sparse_decode_kernel<D, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(sparse_decode_kernel<D, NT, KV8>,
+    return cudaFuncSetAttribute(sparse_decode_kernel<D, NT>,
                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_splits, p.hkv, batch);
-  cfg.blockDim = dim3(SparseCfg<D, NT, KV8>::kWarps * 32, 1, 1);
+  cfg.blockDim = dim3(SparseCfg<D, NT>::kWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -436,46 +361,43 @@ static cudaError_t launch_sparse_one(const SparseParams& p, int batch, cudaStrea
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = clusters ? 1 : 2;
-  if (clusters) return cudaOccupancyMaxActiveClusters(clusters, sparse_decode_kernel<D, NT, KV8>, &cfg);
-  return cudaLaunchKernelEx(&cfg, sparse_decode_kernel<D, NT, KV8>, p);
+  if (clusters) return cudaOccupancyMaxActiveClusters(clusters, sparse_decode_kernel<D, NT>, &cfg);
+  return cudaLaunchKernelEx(&cfg, sparse_decode_kernel<D, NT>, p);
 }
 
-template <bool KV8>
 static cudaError_t launch_sparse_any(const SparseParams& p, int head_dim, int ntiles, int batch,
                                      cudaStream_t stream, int* clusters) {
   if (p.num_splits < 1 || p.num_splits > kMaxSparseCluster) return cudaErrorInvalidValue;
   if (head_dim == 128) {
-    if (ntiles == 1) return launch_sparse_one<128, 1, KV8>(p, batch, stream, clusters);
-    if (ntiles == 2) return launch_sparse_one<128, 2, KV8>(p, batch, stream, clusters);
+    if (ntiles == 1) return launch_sparse_one<128, 1>(p, batch, stream, clusters);
+    if (ntiles == 2) return launch_sparse_one<128, 2>(p, batch, stream, clusters);
   } else if (head_dim == 64) {
-    if (ntiles == 1) return launch_sparse_one<64, 1, KV8>(p, batch, stream, clusters);
-    if (ntiles == 2) return launch_sparse_one<64, 2, KV8>(p, batch, stream, clusters);
+    if (ntiles == 1) return launch_sparse_one<64, 1>(p, batch, stream, clusters);
+    if (ntiles == 2) return launch_sparse_one<64, 2>(p, batch, stream, clusters);
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_sparse(const SparseParams& p, int head_dim, int ntiles, int batch,
                           cudaStream_t stream) {
-  return p.k_scale ? launch_sparse_any<true>(p, head_dim, ntiles, batch, stream, nullptr)
-                   : launch_sparse_any<false>(p, head_dim, ntiles, batch, stream, nullptr);
+  return launch_sparse_any(p, head_dim, ntiles, batch, stream, nullptr);
 }
 
-int sparse_max_active_clusters(int head_dim, int ntiles, int cluster, bool kv8) {
+int sparse_max_active_clusters(int head_dim, int ntiles, int cluster) {
   if (cluster < 1 || cluster > kMaxSparseCluster || ntiles < 1 || ntiles > 2) return 0;
   constexpr int kDevices = 32;
-  // [device][bf16 / 8-bit][head_dim 64/128][ntiles][cluster]: 0 unknown, -1 none, else the count
-  static std::atomic<int> cache[kDevices][2][2][3][kMaxSparseCluster + 1];
+  // [device][head_dim 64/128][ntiles][cluster]: 0 unknown, -1 none, else the count
+  static std::atomic<int> cache[kDevices][2][3][kMaxSparseCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-  std::atomic<int>& slot = cache[dev][kv8 ? 1 : 0][head_dim == 128 ? 1 : 0][ntiles][cluster];
+  std::atomic<int>& slot = cache[dev][head_dim == 128 ? 1 : 0][ntiles][cluster];
   int c = slot.load(std::memory_order_acquire);
   if (c == 0) {
     SparseParams p{};
     p.hkv = 1;
     p.num_splits = cluster;
     int n = 0;
-    if ((kv8 ? launch_sparse_any<true>(p, head_dim, ntiles, 1, 0, &n)
-             : launch_sparse_any<false>(p, head_dim, ntiles, 1, 0, &n)) != cudaSuccess) {
+    if (launch_sparse_any(p, head_dim, ntiles, 1, 0, &n) != cudaSuccess) {
       (void)cudaGetLastError();
       n = 0;
     }

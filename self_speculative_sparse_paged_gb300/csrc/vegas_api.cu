@@ -290,14 +290,14 @@ SparsePlan plan_sparse(const vegas_paged_kv_t* kv, int batch, int k_max, int max
   pl.ntiles = (G + 7) / 8;
   const int units = std::max(1, batch * kv->num_kv_heads);
   const int rows_max = std::max(1, k_max + max_tail);
-  const int fit = (rows_max + vegas::sparse_rows_per_cta(kv8) - 1) / vegas::sparse_rows_per_cta(kv8);
+  const int room = kv8 ? vegas::kMaxDraftKv8Rows : vegas::kMaxSparseRowsPerCta;
+  const int fit = (rows_max + room - 1) / room;
+  const auto resident = kv8 ? vegas::draft_kv8_max_active_clusters : vegas::sparse_max_active_clusters;
   int cl;
   if (2 * units < sms) {
     cl = std::min(vegas::kMaxSparseCluster, std::max(fit, std::min(sms / units,
                                                                    (rows_max + 63) / 64)));
-    while (cl > std::max(fit, 1) &&
-           vegas::sparse_max_active_clusters(kv->head_dim, pl.ntiles, cl, kv8) < units)
-      --cl;
+    while (cl > std::max(fit, 1) && resident(kv->head_dim, pl.ntiles, cl) < units) --cl;
   } else {
     cl = std::max(fit, std::min(vegas::kMaxSparseCluster, std::max(1, sms / units)));
   }
@@ -738,9 +738,9 @@ VEGAS_API vegas_status_t vegas_select_window(const int32_t* ctx_lens, int num_si
 namespace {
 // k_scale, v_scale: the 8-bit cache's exponents, or NULL for a bf16 one.
 vegas_status_t sparse_impl(
-    const vegas_paged_kv_t* kv, const uint8_t* k_scale, const uint8_t* v_scale, const void* q, void* out, const int32_t* idx, int k_max,
-    const int32_t* k_per_seq, const int32_t* tail_start, const int32_t* tail_len, int max_tail,
-    int batch, float softmax_scale, void* stream) {
+    const vegas_paged_kv_t* kv, const uint8_t* k_scale, const uint8_t* v_scale, const void* q,
+    void* out, const int32_t* idx, int k_max, const int32_t* k_per_seq, const int32_t* tail_start,
+    const int32_t* tail_len, int max_tail, int batch, float softmax_scale, void* stream) {
   vegas_status_t st;
   if (batch < 0 || k_max < 0 || max_tail < 0)
     return fail(VEGAS_ERR_INVALID_ARG, "batch %d, k_max %d, max_tail %d", batch, k_max, max_tail);
@@ -761,7 +761,7 @@ vegas_status_t sparse_impl(
   int sms = 0;
   if ((st = device_info(&err, &sms)) != VEGAS_OK) return st;
   const SparsePlan pl = plan_sparse(kv, batch, k_max, max_tail, sms, k_scale != nullptr);
-  vegas::SparseParams p{};
+  vegas::DraftKv8Params p{};
   p.q = q;
   p.out = out;
   p.k_cache = kv->k_cache;
@@ -783,8 +783,9 @@ vegas_status_t sparse_impl(
   p.rows_per_split = pl.rows_per_cta;
   p.num_splits = pl.cluster;
   p.err = err;
-  cudaError_t e = vegas::launch_sparse(p, kv->head_dim, pl.ntiles, batch,
-                                       static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = k_scale ? vegas::launch_draft_kv8(p, kv->head_dim, pl.ntiles, batch, s)
+                                : vegas::launch_sparse(p, kv->head_dim, pl.ntiles, batch, s);
   if (e != cudaSuccess) return cuda_fail(e, "sparse launch");
   return VEGAS_OK;
 }

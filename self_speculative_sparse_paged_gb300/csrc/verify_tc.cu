@@ -39,11 +39,16 @@
 // thread-block cluster (every group pushes its state to the rank that owns the
 // output row, through distributed shared memory; no workspace), or through the
 // workspace in the last-arriving CTA.
-#include "cluster_merge.cuh"
+#include <cooperative_groups.h>
+
+#include "kernels.h"
 
 #ifndef VEGAS_TC_D
 #error "compile with -DVEGAS_TC_D=64 or -DVEGAS_TC_D=128"
 #endif
+#include "split_merge.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace vegas {
 
@@ -87,6 +92,13 @@ struct TcCfg {
   static constexpr size_t kMisc = 16 + 32 + 4 * (18 * NQC + 2 * NQP) + (kSmemMax ? 16 : 0);
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
 };
+
+// Cluster-wide barrier of every thread (release / acquire): shared-memory
+// writes before it, local or remote, are visible to every CTA after it.
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <int D, int NQP, int NQC, bool CAPTURE>
 __global__ void __launch_bounds__(384, 1)
@@ -752,15 +764,151 @@ __global__ void __launch_bounds__(384, 1)
     return out + ((size_t(b) * T + t) * p.hq + g * p.group + hl2) * D;
   };
   if (on_chip) {
-    // (into the K ring, weights in the V ring)
-    static_assert(merge_receive_bytes<D, NQC>() <= KS * Cfg::kKV, "receive area");
-    static_assert(kMergeWeightBytes <= VS * Cfg::kVS, "merge weights fit the V ring");
-    const bool softmax = warp >= 2 && warp <= 9;
-    const int i = 32 * (warp & 3) + lane;
-    merge_on_chip<D, NQC, Cfg::kThreads>(p, unit, split, softmax ? (warp - 2) >> 2 : -1,
-                                         i < D ? i : -1, i, o, Mg, Lg, smem,
-                                         reinterpret_cast<float*>(smem + Cfg::kOffV), flag,
-                                         out_row);
+    // Split-KV merge on chip (one split: a cluster of one CTA).  Row n of the
+    // output belongs to cluster rank n % S, which receives in its K ring, at
+    // slot n / S, the 2S partial states of the row (state 2 * rank + group of
+    // each sender, O[D] then m and l), pushed with distributed-shared-memory
+    // stores; one cluster barrier publishes them and each rank merges its rows
+    // from local shared memory: O = sum_q 2^(m_q - M) O_q / sum_q 2^(m_q - M) l_q
+    // with M = max_q m_q.  Nothing reads another CTA's shared memory, so no
+    // barrier precedes the exit.
+    constexpr int RS = D + 4;   // one received state: O[D], m, l, padding to 16 bytes
+    static_assert(2 * (NQC + kMaxVerifyCluster) * RS * 4 <= KS * Cfg::kKV, "receive area");
+    static_assert(2 * kMaxVerifyCluster <= 32, "one lane per state in the weight pass");
+    cg::cluster_group cluster = cg::this_cluster();
+    const int S = p.cluster_merge ? p.cluster_size : 1, r = (int)cluster.block_rank();
+    const int C = p.num_splits / S, c = split / S;   // clusters of the unit, this one's index
+    const float* recv = reinterpret_cast<const float*>(smem);
+    if (warp >= 2 && warp <= 9) {
+      const int grp = (warp - 2) >> 2, i = 32 * (warp & 3) + lane;
+      const int q = 2 * r + grp;
+      int owner = 0, slot = 0;
+#pragma unroll
+      for (int n = 0; n < NQC; ++n) {
+        if (n < p.nq && i < D)
+          st_cluster_f32(cluster_map(sbase + 4 * ((slot * 2 * S + q) * RS + i), owner), o[n]);
+        if (++owner == S) {
+          owner = 0;
+          ++slot;
+        }
+      }
+      if (i < p.nq) {
+        const uint32_t dst = cluster_map(sbase + 4 * (((i / S) * 2 * S + q) * RS + D), i % S);
+        st_cluster_f32(dst, Mg);
+        st_cluster_f32(dst + 4, Lg);
+      }
+    }
+    cluster_sync_all();
+    const int nown = r < p.nq ? (p.nq - r + S - 1) / S : 0;
+    // Weights 2^(m_q - M) / sum_q' 2^(m_q' - M) l_q' of the 2S states of each
+    // owned row (one warp per row, lane q), into the free V ring, with the
+    // row's cluster-level maximum M and sum (used when C > 1) ...
+    // (nown <= NQC <= 64 rows, 2S <= 32 states, C <= 32 clusters)
+    static_assert((64 * 2 * kMaxVerifyCluster + 2 * 64 + 64 * 32) * 4 <= VS * Cfg::kVS,
+                  "merge weights fit the V ring");
+    float* wts = reinterpret_cast<float*>(smem + Cfg::kOffV);   // [nown][2S]
+    float* rowml = wts + 64 * 2 * kMaxVerifyCluster;           // [nown][2]
+    for (int k = warp; k < nown; k += Cfg::kThreads / 32) {
+      const float* st = recv + k * 2 * S * RS;
+      const bool has = lane < 2 * S;
+      const float m = has ? st[lane * RS + D] : kEmptyMax;
+      const float l = has ? st[lane * RS + D + 1] : 0.f;
+      float M = m;
+#pragma unroll
+      for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+      const float f = has ? ex2(m - M) : 0.f;
+      float Lsum = f * l;
+#pragma unroll
+      for (int o2 = 16; o2 > 0; o2 >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, o2);
+      if (has) wts[k * 2 * S + lane] = Lsum > 0.f ? f / Lsum : 0.f;
+      if (lane == 0) {
+        rowml[2 * k] = M;
+        rowml[2 * k + 1] = Lsum;
+      }
+    }
+    __syncthreads();
+    // ... then four output elements per thread: sum_q w_q O_q[d .. d + 3]
+    for (int e = tid; e < nown * (D / 4); e += Cfg::kThreads) {
+      const int k = e / (D / 4), d = 4 * (e - k * (D / 4));
+      const float* st = recv + k * 2 * S * RS + d;
+      const float* wk = wts + k * 2 * S;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int q = 0; q < 2 * S; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(st + q * RS);
+        const float wq = wk[q];
+        acc.x += wq * v.x;
+        acc.y += wq * v.y;
+        acc.z += wq * v.z;
+        acc.w += wq * v.w;
+      }
+      if (C == 1) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+        uint2 pk;
+        pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+        pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+        *reinterpret_cast<uint2*>(out_row(r + k * S) + d) = pk;
+      } else {
+        // this cluster's normalised row, merged across the unit's clusters below
+        const size_t row = (size_t(unit) * C + c) * p.nq + (r + k * S);
+        *reinterpret_cast<float4*>(p.part_o + row * D + d) = acc;
+      }
+    }
+    if (C > 1) {
+      // Cross-cluster merge through the workspace, per owner rank: rank r of
+      // every cluster of the unit writes its rows' (o_c, M_c, L_c), takes the
+      // ticket of (unit, r), and the last to arrive combines them:
+      // out = sum_c F_c o_c / sum_c F_c with F_c = 2^(M_c - max M) L_c.
+      for (int k = tid; k < nown; k += Cfg::kThreads) {
+        const size_t row = (size_t(unit) * C + c) * p.nq + (r + k * S);
+        p.part_ml[2 * row] = rowml[2 * k];
+        p.part_ml[2 * row + 1] = rowml[2 * k + 1];
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) *flag = atomicAdd(&p.tickets[unit * S + r], 1) == C - 1;
+      __syncthreads();
+      if (*flag) {
+        __threadfence();
+        float* w2 = rowml + 2 * 64;   // [nown][C]
+        for (int k = warp; k < nown; k += Cfg::kThreads / 32) {
+          const bool has = lane < C;
+          const size_t row = (size_t(unit) * C + lane) * p.nq + (r + k * S);
+          const float m = has ? __ldcg(&p.part_ml[2 * row]) : kEmptyMax;
+          const float l = has ? __ldcg(&p.part_ml[2 * row + 1]) : 0.f;
+          float M = m;
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o2));
+          const float F = has ? ex2(m - M) * l : 0.f;
+          float Fs = F;
+#pragma unroll
+          for (int o2 = 16; o2 > 0; o2 >>= 1) Fs += __shfl_xor_sync(0xffffffffu, Fs, o2);
+          if (has) w2[k * C + lane] = Fs > 0.f ? F / Fs : 0.f;
+        }
+        __syncthreads();
+        for (int e = tid; e < nown * (D / 4); e += Cfg::kThreads) {
+          const int k = e / (D / 4), d = 4 * (e - k * (D / 4));
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int q = 0; q < C; ++q) {
+            const size_t row = (size_t(unit) * C + q) * p.nq + (r + k * S);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
+            const float wq = w2[k * C + q];
+            acc.x += wq * v.x;
+            acc.y += wq * v.y;
+            acc.z += wq * v.z;
+            acc.w += wq * v.w;
+          }
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+          uint2 pk;
+          pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+          pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+          *reinterpret_cast<uint2*>(out_row(r + k * S) + d) = pk;
+        }
+        if (tid == 0) p.tickets[unit * S + r] = 0;
+      }
+    }
   } else {
     SplitWorkspace ws{p.tickets, p.part_ml, p.part_o};
     finish_splits<D, Cfg::kThreads, NQC>(ws, unit, p.num_splits, 2 * p.num_splits, p.nq, out_row,
