@@ -5,6 +5,11 @@
 // exponents of their blocks, each warp gathers 16 rows of K and V at a time with 16-byte copies
 // (D bytes a row), and the warp core of kv8_core.cuh turns them into logits and weighted sums.  The
 // CTAs' softmax states meet in distributed shared memory, with no global scratch and no second pass.
+//
+// What bounds it: rows at random places come at 4.7 TB/s where they have 128 bytes and at 2.3 where
+// they have 64 (a plain gather of 4 million of them), and short lists at the length of the chain
+// index -> page -> row -> merge.  5.6 us at 1,645 entries x 8 heads of 128; 4 lists of 3,933
+// entries x 8 heads of 64: 11.0; 8 of 2,908 x 8 of 128: 16.7; 4 of 10,008 x 8 of 128: 22.0.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -15,11 +20,17 @@ namespace cg = cooperative_groups;
 
 namespace vegas {
 
+// W warps, each with two 16-row groups in flight.  Long lists: sixteen, twelve where two column tiles
+// of head_dim 128 leave no registers for more (8 -> 16: 26.8 -> 22.4 us for 4 lists of 10,008
+// entries).  Up to kFewRows entries a CTA eight have them all in flight too, and merge fewer states
+// (16 -> 8: 5.9 -> 5.6 us at 1,645 entries; at head_dim 64, with half the state, 4.9 -> 5.3).
+constexpr int kFewWarps = 8, kFewRows = 2 * 16 * kFewWarps;
 template <int D, int NT>
+constexpr int draft_kv8_warps(bool few) { return D == 64 ? 16 : few ? kFewWarps : NT == 2 ? 12 : 16; }
+
+template <int D, int NT, int W>
 struct DraftKv8Cfg {
-  // Warps, each with two 16-row groups in flight: sixteen, twelve where two column tiles of
-  // head_dim 128 leave no registers for more.
-  static constexpr int kWarps = D == 128 && NT == 2 ? 12 : 16;
+  static constexpr int kWarps = W;
   static constexpr int kStages = 2;
   static constexpr int kTile = 16 * D;
   static constexpr int kStage = 2 * kTile;
@@ -27,9 +38,9 @@ struct DraftKv8Cfg {
   static constexpr size_t kStageBytes = size_t(kWarps) * kStages * kStage;
 };
 
-template <int D, int NT>
+template <int D, int NT, int W>
 constexpr size_t draft_kv8_smem_bytes() {
-  using Cfg = DraftKv8Cfg<D, NT>;
+  using Cfg = DraftKv8Cfg<D, NT, W>;
   return Cfg::kStageBytes                                          // stages
          + (size_t(Cfg::kWarps) * Cfg::kStages + 1) * 8            // mbarriers (+ receive)
          + size_t(Cfg::kMaxRows) * 6                               // row table, scale exponents
@@ -38,21 +49,20 @@ constexpr size_t draft_kv8_smem_bytes() {
          + size_t(kMaxSparseCluster) * NT * 8 * 2 * 4              // received m, l
          + 1024;
 }
-static_assert(draft_kv8_smem_bytes<128, 1>() <= 227 * 1024 &&
-                  draft_kv8_smem_bytes<128, 2>() <= 227 * 1024 &&
-                  draft_kv8_smem_bytes<64, 1>() <= 227 * 1024 &&
-                  draft_kv8_smem_bytes<64, 2>() <= 227 * 1024,
+static_assert(draft_kv8_smem_bytes<128, 1, 16>() <= 227 * 1024 &&
+                  draft_kv8_smem_bytes<128, 2, 12>() <= 227 * 1024 &&
+                  draft_kv8_smem_bytes<64, 1, 16>() <= 227 * 1024 &&
+                  draft_kv8_smem_bytes<64, 2, 16>() <= 227 * 1024,
               "shared memory of a draft CTA");
 
-template <int D, int NT>
-__global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
     draft_kv8_kernel(const DraftKv8Params p) {
-  constexpr int W = DraftKv8Cfg<D, NT>::kWarps;
   constexpr int NTH = W * 32;
   constexpr int NPAD = NT * 8;
-  constexpr int STAGES = DraftKv8Cfg<D, NT>::kStages;
-  constexpr int TILE = DraftKv8Cfg<D, NT>::kTile;
-  constexpr int STAGE = DraftKv8Cfg<D, NT>::kStage;
+  constexpr int STAGES = DraftKv8Cfg<D, NT, W>::kStages;
+  constexpr int TILE = DraftKv8Cfg<D, NT, W>::kTile;
+  constexpr int STAGE = DraftKv8Cfg<D, NT, W>::kStage;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -62,7 +72,7 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* stage_area = smem;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + DraftKv8Cfg<D, NT>::kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + DraftKv8Cfg<D, NT, W>::kStageBytes);
   uint64_t* recv_bar = bars + W * STAGES;   // completes when every peer's state has landed
   int32_t* rows = reinterpret_cast<int32_t*>(recv_bar + 1);
   const int nel = p.group * D;              // output elements of the unit (G x D)
@@ -81,8 +91,8 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   griddep_begin();
   // entry i's exponents, K's in the low byte and V's in the high one
-  uint16_t* exps = reinterpret_cast<uint16_t*>(rows + DraftKv8Cfg<D, NT>::kMaxRows);
-  float* pM = reinterpret_cast<float*>(exps + DraftKv8Cfg<D, NT>::kMaxRows);   // [NPAD] CTA partial
+  uint16_t* exps = reinterpret_cast<uint16_t*>(rows + DraftKv8Cfg<D, NT, W>::kMaxRows);
+  float* pM = reinterpret_cast<float*>(exps + DraftKv8Cfg<D, NT, W>::kMaxRows);   // [NPAD] CTA partial
   float* pL = pM + NPAD;                                                 // [NPAD]
   float* pO = pL + NPAD;                                                 // [NPAD][D]
   // [CL][per] output slices received (16-byte aligned: they arrive in 16-byte stores;
@@ -100,7 +110,7 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
   // The selected positions of this CTA's range are requested together with
   // k_b and the tail (entries past k_b are replaced below), so the index and
   // length loads take one round trip.
-  constexpr int kPer = (DraftKv8Cfg<D, NT>::kMaxRows + NTH - 1) / NTH;   // entries a thread
+  constexpr int kPer = (DraftKv8Cfg<D, NT, W>::kMaxRows + NTH - 1) / NTH;   // entries a thread
   // (a split's own length ends the walks over the table early: 6.3 -> 5.9 us at 1,645 entries)
   auto past = [&](int u) { return u * NTH >= p.rows_per_split; };
   const int rbeg = rank * p.rows_per_split;
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
   }
   reduce_row_sums<D, NT>(st);
   __syncthreads();
-  cta_merge_to_smem<D, NT, W, Kv8Dims<D>>(st, stage_area, DraftKv8Cfg<D, NT>::kStageBytes, p.group,
+  cta_merge_to_smem<D, NT, W, Kv8Dims<D>>(st, stage_area, DraftKv8Cfg<D, NT, W>::kStageBytes, p.group,
                                           pM, pL, pO);
   __syncthreads();   // the pushes below read elements other threads merged
 
@@ -336,22 +346,22 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT>::kWarps * 32, 1)
 
 // Launches, or with `clusters` set, reports how many clusters of p.num_splits
 // CTAs can be resident at once.
-template <int D, int NT>
-static cudaError_t launch_draft_kv8_one(const DraftKv8Params& p, int batch, cudaStream_t stream,
-                                        int* clusters = nullptr) {
-  constexpr size_t smem = draft_kv8_smem_bytes<D, NT>();
+template <int D, int NT, int W>
+static cudaError_t launch_draft_kv8_w(const DraftKv8Params& p, int batch, cudaStream_t stream,
+                                      int* clusters = nullptr) {
+  constexpr size_t smem = draft_kv8_smem_bytes<D, NT, W>();
   static std::atomic<uint32_t> configured{0};
   cudaError_t e = once_per_device(configured, [] {
-    cudaError_t r = cudaFuncSetAttribute(draft_kv8_kernel<D, NT>,
+    cudaError_t r = cudaFuncSetAttribute(draft_kv8_kernel<D, NT, W>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(draft_kv8_kernel<D, NT>,
+    return cudaFuncSetAttribute(draft_kv8_kernel<D, NT, W>,
                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_splits, p.hkv, batch);
-  cfg.blockDim = dim3(DraftKv8Cfg<D, NT>::kWarps * 32, 1, 1);
+  cfg.blockDim = dim3(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -363,8 +373,17 @@ static cudaError_t launch_draft_kv8_one(const DraftKv8Params& p, int batch, cuda
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = clusters ? 1 : 2;
-  if (clusters) return cudaOccupancyMaxActiveClusters(clusters, draft_kv8_kernel<D, NT>, &cfg);
-  return cudaLaunchKernelEx(&cfg, draft_kv8_kernel<D, NT>, p);
+  if (clusters) return cudaOccupancyMaxActiveClusters(clusters, draft_kv8_kernel<D, NT, W>, &cfg);
+  return cudaLaunchKernelEx(&cfg, draft_kv8_kernel<D, NT, W>, p);
+}
+
+template <int D, int NT>
+static cudaError_t launch_draft_kv8_one(const DraftKv8Params& p, int batch, cudaStream_t stream,
+                                        int* clusters) {
+  // (the count of resident clusters is the larger kernel's)
+  return !clusters && p.rows_per_split <= kFewRows
+             ? launch_draft_kv8_w<D, NT, draft_kv8_warps<D, NT>(true)>(p, batch, stream)
+             : launch_draft_kv8_w<D, NT, draft_kv8_warps<D, NT>(false)>(p, batch, stream, clusters);
 }
 
 static cudaError_t launch_draft_kv8_any(const DraftKv8Params& p, int head_dim, int ntiles, int batch,
