@@ -1222,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[j] = 0.f;
             acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           }
-#pragma unroll 2
+#pragma unroll 4
           for (int c = 0; c < pieces; ++c) {
             const size_t rows = size_t(c == 0 ? slot0 : 2 * (c0 + c)) * p.nq;
             float2 m[E];
