@@ -1067,6 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        tc_fence_before();
+        mbar_arrive(sread(grp));   // S of the group's next tile may come
         if (CAPTURE && pos < Lcap) {
           if constexpr (kSideS) {
 #pragma unroll
@@ -1126,8 +1128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < D / 16; ++c) vrow[c] = make_uint4(0, 0, 0, 0);
           }
         }
-        tc_fence_before();
-        mbar_arrive(sread(grp));
         fence_proxy_async_smem();
         mbar_arrive(pready(grp));
         any = true;
