@@ -442,22 +442,29 @@ typedef struct {
  * vegas_verify_attn_kv8: vegas_verify_attn_capture_rows over the 8-bit cache,
  * window rows 0 .. gamma at positions ctx_lens[b] .. ctx_lens[b] + gamma already
  * appended; gamma = 0 is plain decode attention of one token a sequence.  Logits
- * are exact products of the codes with q in two e4m3 parts (8 bits, each row
- * scaled by a power of two; elements 2^-10 below their row's largest are rounded
- * to 2^-19 of it), summed in fp32; captured scores take the summed
- * query in six parts.  Exponentials are rounded to f16 (half a step, 2^-11 of
- * it) before they meet V's codes, sums are fp32, the output is rounded once to bf16.
+ * are exact products of the codes with q in two e4m3 parts, summed in fp32.  The
+ * parts hold an element of q exactly from 2^-9 of the largest on and are off by at
+ * most 2^-17 of the largest below; the largest is that of all window rows of the
+ * KV head's queries where their own lie within a factor of 2^4, else the row's.
+ * Captured scores take the summed query in six parts.  Exponentials (times
+ * 2^e of V's block) meet V's codes in f16 cut into three e5m2 parts, within 2^-9 +
+ * 2^-13 of each and 2^-28 of the row's largest; the row's sum takes them in fp32,
+ * sums are fp32, the output is rounded once to bf16.
  * scores may be NULL (nothing captured; capture_row_mask is then ignored).  K and V
  * of attended positions must be finite codes, |q| below 2^40; other slots may hold
  * anything.
- *   workspace: vegas_verify_kv8_workspace_size() bytes, 256-byte aligned (the
- *        size of another context capacity, batch or gamma may be larger or smaller)
+ *   workspace: vegas_verify_kv8_workspace_size() bytes, 256-byte aligned.  Calls of
+ *        other batches, capacities and gammas may use the same one in turn, if it holds
+ *        the largest of their sizes; after a reported VEGAS_ERR_DEVICE_TIMEOUT it has to
+ *        be zero-filled again.
  * Supported: (gamma + 1) * G <= 64 at head_dim 64 and <= 40 at head_dim 128, gamma in
- * [0, 15], |softmax_scale| <= 2^20.
+ * [0, 15], |softmax_scale| <= 2^20, batch <= 2^16.  A workspace is always needed.
  *
  * vegas_sparse_decode_attn_kv8: vegas_sparse_decode_attn (section 3: its lists,
- * limits and refusals) over the 8-bit cache, roundings as above but q itself
- * exact in f16 (elements 2^-21 below their head's largest rounded to 2^-39 of it).
+ * limits and refusals) over the 8-bit cache; q exact in f16 (an element below 2^-31
+ * of its head's largest is off by at most 2^-39 of it), exponentials rounded to f16
+ * (half a step, 2^-11 of each, or 2^-31 of the row's largest), the rest as above;
+ * |softmax_scale| <= 2^20.
  */
 vegas_status_t vegas_rope_append_kv8(
     const vegas_paged_kv8_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

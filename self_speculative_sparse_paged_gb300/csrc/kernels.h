@@ -60,7 +60,7 @@ struct VerifyKv8Params {
   uint32_t row_mask;        // capture rows: bit t set -> window row t is captured
   float scale;              // softmax scale (logit units)
   float scale_log2;         // scale * log2(e)
-  int* tickets;             // [B * Hkv]
+  int* tickets;             // [CTAs]
   float* part_ml;           // [CTAs][2][nq] (m, l)
   float* part_o;            // [CTAs][2][nq][D]
   int* err;

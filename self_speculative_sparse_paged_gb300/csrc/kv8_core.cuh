@@ -68,7 +68,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 
 // The group's query heads as f16 fragments, each head scaled by a power of two to a largest
-// element in [2^14, 2^15): a bf16 element is then exact in f16 unless it is below 2^-21 of its
+// element in [2^14, 2^15): a bf16 element is then exact in f16 unless it is below 2^-31 of its
 // head's largest, and off by at most 2^-39 of that there.  q: the unit's first head (rows of D bf16);
 // back[nt][e]: 1 / scale of column 8 nt + 2 (lane % 4) + e.
 template <int D, int NT>

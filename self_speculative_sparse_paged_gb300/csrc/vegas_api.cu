@@ -540,8 +540,9 @@ struct VerifyKv8Plan {
 };
 
 // One CTA an SM, each with up to two pieces of shared units in the workspace; fewer where the
-// tables hold fewer tiles.  Tickets come first, for every unit, and the pieces' room does not
-// depend on the call's tables.
+// tables hold fewer tiles.  Tickets come first, one a CTA for the shared unit that begins in its run,
+// and neither their room nor the pieces' depends on the batch or its tables: no call's partial states
+// may come to lie where another call keeps its counters.
 VerifyKv8Plan plan_verify_kv8(const vegas_paged_kv8_t* kv, int batch, int gamma, int sms) {
   VerifyKv8Plan pl{};
   pl.nq = (gamma + 1) * (kv->num_q_heads / kv->num_kv_heads);
@@ -549,7 +550,7 @@ VerifyKv8Plan plan_verify_kv8(const vegas_paged_kv8_t* kv, int batch, int gamma,
   const long long tiles =
       (long long)batch * kv->num_kv_heads * ((kv->max_pages_per_seq + 7) / 8);
   pl.grid = (int)std::max(1ll, std::min((long long)most, tiles));
-  pl.ml_off = align256(size_t(batch) * kv->num_kv_heads * sizeof(int));
+  pl.ml_off = align256(vegas::kMaxKv8Ctas * sizeof(int));
   pl.o_off = pl.ml_off + align256(size_t(most) * 2 * pl.nq * 2 * sizeof(float));
   pl.bytes = pl.o_off + size_t(most) * 2 * pl.nq * kv->head_dim * sizeof(float);
   return pl;

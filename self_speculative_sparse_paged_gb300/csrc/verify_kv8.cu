@@ -36,6 +36,15 @@
 // A unit that one CTA covers is written by it; the pieces of a shared one go to the workspace
 // (fp32 O, maximum and sum of each row), and the CTA that arrives last on the unit's ticket merges
 // them.  No CTA waits for another.
+//
+// What bounds it.  Long batches of 24 columns at head_dim 128: the DRAM stream (a tile's 735 ns at
+// the copy peak, of which the softmax needs about 300).  One long sequence: what comes before and
+// behind the stream (division of the work 1.2 us, queries 1.5, end 1.2, partial state and ticket 2.4,
+// merge 1.6-3).  Many short sequences: the same a unit.  56 columns at head_dim 64: the softmax's
+// latency, 2100 clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us
+// of 224 less, with P in one f16 part and V turned by four more warps 29 us more).
+//   8 x 49K-64K, 24 columns of 128    160 us (0.89 of the copy peak)      32K: 24.9
+//   4 x 128K, 56 columns of 64        224 us (0.36)            one token each of 12 up to 8K: 18.7    2K, 20 of 64: 12.0
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
@@ -51,7 +60,10 @@ constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P
 constexpr int kCapParts = 6;
 constexpr int kSoftWarps = 8, kWarps = 12, kSoft = 32 * kSoftWarps, kThreads = 32 * kWarps;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
-// reference and end), and a CTA takes part for kLeastRun tiles or more.
+// reference and end; with 3, 6, 8, 10: 12 ragged single tokens 20.4, 18.3, 18.7, 19.6 us, 8 x 2K 21.5,
+// 20.0, 19.3, 19.0, 4 x 128K of 64 228, 226, 224, 223, 32K 24.9, 24.9, 24.8, 25.4, 64 x 1K 53.5, 54.3,
+// 54.4, 55.1), and a CTA takes part for kLeastRun tiles or more (1, 4, 8: one of 4K 15.3, 14.1, 15.4 us,
+// one of 2K 11.8, 12.0, 14.3).
 constexpr int kUnitTiles = 8, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
@@ -1173,13 +1185,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the CTAs that hold tiles of the unit
       const long long tile0 = unit0 + kUnitTiles;
       const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
-      const size_t unit = size_t(b) * p.hkv + g;
       auto out_row = [&](int n2) {
         const int t = n2 / p.group, hl = n2 - t * p.group;
         return out + ((size_t(b) * T + t) * p.hq + g * p.group + hl) * D;
       };
       // Workspace slots: 2 c for the unit that CTA c's run begins in or with, 2 c + 1 for its last one
-      // where that is another; of a unit's CTAs only the first can have it as its last.
+      // where that is another; of a unit's CTAs only the first can have it as its last.  So a CTA is the
+      // first of one shared unit at most, whose ticket is tickets[c0].
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
       // each group finishes some columns, from both groups' O^T
@@ -1205,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c0 != c1) {
         named_bar(kAllBar, kSoft);
         // (released and acquired by one thread: the barriers carry that to and from the others)
-        if (tid == 0) *flag = ticket_acq_rel(&p.tickets[unit]) == c1 - c0;
+        if (tid == 0) *flag = ticket_acq_rel(&p.tickets[c0]) == c1 - c0;
         named_bar(kAllBar, kSoft);
         if (*flag) {
           // Last to arrive: out = sum_c F_c o_c / sum_c F_c l_c with F_c = 2^(m_c - max m), in one pass
@@ -1253,7 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv),
                            pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
           }
-          if (tid == 0) p.tickets[unit] = 0;
+          if (tid == 0) p.tickets[c0] = 0;
         }
       }
       named_bar(kAllBar, kSoft);   // the buffers and columns are free again

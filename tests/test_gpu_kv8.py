@@ -499,6 +499,8 @@ DRAFTS = [
     (32, 8, 128, [4000], [205], [6]), (16, 1, 64, [333, 40], [40, 40], [2, 17]), (9, 1, 128, [90], [17], [4]),
     (16, 1, 128, [2500], [1300], [5]), (64, 8, 64, [3000, 2999], [90, 93], [8, 11]),
     (5, 1, 64, [70] * 40, [11] * 40, [1] * 40), (2, 1, 128, [40000], [32000], [16]),
+    (16, 1, 128, [9000], [6000], [3]), (16, 2, 64, [9000], [7000], [9]),    # long lists, wide groups
+    (8, 8, 128, [3500] * 10, [3000] * 10, [5] * 10),                        # one CTA a list
 ]
 
 

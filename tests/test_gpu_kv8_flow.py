@@ -95,8 +95,8 @@ class Step:
             call(kv, self.qd, out, self.idx, 20, self.k, self.window_ctx, self.tail, 4, 3, self.scale)
 
     def results(self):
-        return [t.clone() for t in (self.k8, self.v8, self.ks, self.vs, self.k16.nan_to_num(), self.out8, self.s8,
-                                    self.idx, self.d8, self.chunks[1]["out"])]
+        return [t.clone() for t in (self.k8, self.v8, self.ks, self.vs, self.k16.nan_to_num(), self.out8,
+                                    self.s8, self.idx, self.d8, self.chunks[1]["out"])]
 
     def clear(self):
         for t in (self.k8, self.v8):
@@ -222,3 +222,29 @@ def test_replays_follow_the_lengths():
             assert (scores[b, :, n:] == -1).all()
     vg.vegas_read_device_status()
     assert not ws[:16].any()                          # the tickets are at zero again
+
+
+def test_one_workspace_for_calls_of_many_sizes():
+    """Batches and windows of every size through one workspace in turn, against workspaces of their
+    own: what one call leaves there is not another's counter."""
+    rng = np.random.default_rng(8)
+    hq, hkv, d, pages = 8, 2, 128, 64
+    cache = [torch.from_numpy(rng.integers(0, 126, (60 * pages, hkv, 16, d), dtype=np.uint8)).to(DEV)
+             for _ in range(2)]
+    scales = [torch.full((60 * pages, hkv), b, dtype=torch.uint8, device=DEV) for b in (118, 120)]
+    bt = torch.from_numpy(rng.permutation(60 * pages).astype(np.int32).reshape(60, pages)).to(DEV)
+    kv = vg.paged_kv8(*cache, *scales, bt, hq)
+    cases = [(1, 4, [900]), (60, 0, [11 * i for i in range(60)]), (3, 9, [1000, 1, 500]), (60, 4, [1000] * 60),
+             (2, 4, [1000, 1000]), (17, 1, [63 * i for i in range(17)])]
+    one = torch.zeros(max(vg.vegas_verify_kv8_workspace_size(kv, b, g) for b, g, _ in cases),
+                      dtype=torch.uint8, device=DEV)
+    for batch, gamma, lens in cases + cases[::-1]:
+        q = torch.from_numpy(rng.standard_normal((batch, gamma + 1, hq, d))).bfloat16().to(DEV)
+        outs = []
+        for ws in (one, torch.zeros_like(one)):
+            out = torch.full_like(q, float("nan"))
+            vg.vegas_verify_attn_kv8(kv, q, out, None, 0, ints(lens), batch, gamma, 0, 0.05, ws, ws.numel())
+            outs.append(out)
+        vg.vegas_read_device_status()
+        assert not outs[1].isnan().any()
+        assert torch.equal(*outs), (batch, gamma)

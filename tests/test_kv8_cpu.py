@@ -100,6 +100,7 @@ def test_verify_refusals(vg):  # noqa: F811
     changes += [
         (dict(q=None), 1, "NULL q"), (dict(out=None), 1, "NULL q"), (dict(ctx_lens=None), 1, "NULL q"),
         (dict(q=8), 1, "16-byte"), (dict(out=24), 1, "16-byte"), (dict(batch=-1), 1, "batch"),
+        (dict(batch=(1 << 16) + 1), 2, "batch"),
         (dict(gamma=-1), 2, "gamma"), (dict(gamma=16), 2, "gamma"),
         (dict(gamma=16, scores=None), 2, "gamma"), (dict(capture_row_mask=0), 1, "mask"),
         (dict(capture_row_mask=32), 1, "mask"), (dict(score_stride=0), 1, "score_stride"),
