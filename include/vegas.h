@@ -429,7 +429,8 @@ typedef struct {
  * e4m3(c * 2^(e_old - e)), exact but for codes that fall below 2^-6.  So a
  * rejected draft row that is written over may leave its page's scale raised.
  * Slots behind the new rows keep their codes.  No two sequences of a call may
- * append to the same page.
+ * append to the same page, and a page that is appended to is the sequence's own: the
+ * codes that it holds may change.
  *
  * vegas_kv8_read: positions [first[b], upto[b]) of every sequence, as bf16, into
  * the same positions of the bf16 cache `to` through its own block table, which

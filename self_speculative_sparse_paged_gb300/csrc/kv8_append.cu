@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
       }
       at = p.positions[size_t(axis) * p.total_rows + row0 + r];
     }
-    const float turns = __ll2float_rn((long long)at * (long long)turn_all[pair]) * 0x1p-64f;
+    const float turns = __ll2float_rn((long long)((unsigned long long)at * turn_all[pair])) * 0x1p-64f;
     float sn, cn;
     sincospif(2.f * turns, &sn, &cn);
     const int unit = pair >> 3, e = pair & 7;

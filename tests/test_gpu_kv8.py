@@ -248,7 +248,8 @@ def test_append_faults_are_recorded():
 # ------------------------------------------------------------------ read
 @pytest.mark.parametrize("hkv,d,first,upto", [
     (1, 64, [0], [1]), (2, 64, [0, 5, 40], [700, 5, 41]), (8, 128, [0, 16, 31, 0], [33, 32, 200, 0]),
-    (3, 128, None, [100, 16]), (5, 64, [15, 0], [17, 300])])
+    (3, 128, None, [100, 16]), (5, 64, [15, 0], [17, 300]),
+    (1, 64, [0] * 63 + [37], [5 * i for i in range(63)] + [6001])])         # a long one among many
 def test_read(hkv, d, first, upto):
     rng = np.random.default_rng(d + hkv)
     c = Cache(rng, [(u + 15) // 16 for u in upto], hkv, hkv, d, wild=True, spread=110)
