@@ -331,8 +331,9 @@ struct Kv8Cfg {
   static constexpr int kNumBars = 2 * KS + 2 * VS + 4 * 2 + 2;
   static constexpr int kOffMisc = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   // misc: 16 words; votes[2][2][4]; warp sums[12] (64 bits); colmax[2][4][NQC], colsum[2][4][NQC],
-  // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC]
-  static constexpr size_t kMisc = 64 + 64 + 96 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2) * NQC;
+  // colfac[NQC], nref[2][NQC], fac[2][NQC], wgt[2][NQC], colM[NQC], colL[NQC]; tlim[NQC]; rowexp[NQC];
+  // rowat[NQC]
+  static constexpr size_t kMisc = 64 + 64 + 96 + 4 * size_t(16 + 1 + 2 + 2 + 2 + 2 + 2 + 1) * NQC;
   static constexpr size_t kSmem = size_t(kOffMisc) + kMisc + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(8 * D * 4 <= kP, "partial sums of the captured query (P's buffer)");
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* colL = colM + NQC;
   int* tlim = reinterpret_cast<int*>(colL + NQC);                // [NQC]
   int* rowexp = tlim + NQC;                                      // [NQC]
+  int* rowat = rowexp + NQC;   // [NQC] where a column's row of q and out is, from the unit's first
   float* qsum = reinterpret_cast<float*>(smem + Cfg::kOffP);     // [softmax warps][D] of the captured sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -422,6 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kSoftWarps + 2) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
+  }
+  // (once, and not in every unit: quotients by a number known at run time take a hundred clocks)
+  for (int n2 = tid; n2 < NQC; n2 += kThreads) {
+    const int t = n2 / p.group, hl = n2 - t * p.group;
+    tlim[n2] = n2 < p.nq ? t : -1;
+    rowat[n2] = (t * p.hq + hl) * D;
   }
   tc_fence_before();
   __syncthreads();   // (the barriers are initialised, and tensor memory is there)
@@ -784,15 +792,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const int phys0 = load_page(row, last_page, at.t + int(first - it0));
         phys1 = load_page(row, last_page, at.t + int(first - it0) + 2);
+        const __nv_bfloat16* qunit = qbase + (size_t(b) * T * p.hq + g * p.group) * D;
         uint32_t qreg[QPER][D / 64];
 #pragma unroll
         for (int u = 0; u < QPER; ++u) {
-          const int n2 = warp + kSoftWarps * u, t = n2 / p.group, hl = n2 - t * p.group;
+          const int n2 = warp + kSoftWarps * u;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            qreg[u][h] = n2 < p.nq ? reinterpret_cast<const uint32_t*>(
-                                         qbase + ((size_t(b) * T + t) * p.hq + g * p.group + hl) * D)
-                                         [32 * h + lane]
+            qreg[u][h] = n2 < p.nq ? reinterpret_cast<const uint32_t*>(qunit + rowat[n2])[32 * h + lane]
                                    : 0u;
         }
         // a row's exponent: its largest element lies in [2^n, 2^(n + 1))
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < QPER; ++u) {
             const int n2 = warp + kSoftWarps * u;
-            if (n2 < p.nq && ((p.row_mask >> (n2 / p.group)) & 1u)) {
+            if (n2 < p.nq && ((p.row_mask >> tlim[n2]) & 1u)) {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h) {
                 acc[h][0] += __uint_as_float(qreg[u][h] << 16);
@@ -826,7 +833,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float2*>(qsum + warp * D + 64 * h + 2 * lane) =
                 make_float2(acc[h][0], acc[h][1]);
         }
-        if (tid < NQC) tlim[tid] = tid < p.nq ? tid / p.group : -1;
         named_bar(kAllBar, kSoft);
         // One exponent for all rows while they are within 2^4 of each other (a part's grid then
         // reaches 2^-13 of the smallest row's largest element, and 2^-17 of the unit's), else one a
@@ -1167,28 +1173,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && i == 0) set_error(p.err, kErrDeviceTimeout);
         break;
       }
+      // the CTAs that hold tiles of the unit
+      const long long tile0 = unit0 + kUnitTiles;
+      const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
       // the piece's maximum and sum of a column, and the weights of the two groups' states
       if (tid < NQC) {
         const float m0 = colmax[tid], m1 = colmax[4 * NQC + tid], M = fmaxf(m0, m1);
         const float w0 = ex2(m0 - M), w1 = ex2(m1 - M);
         const float* cs = colsum + tid;
-        wgt[tid] = w0;
-        wgt[NQC + tid] = w1;
+        const float sum = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
+                          w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
+        const float share = c0 == c1 ? 1.f / sum : 1.f;   // (a whole unit is divided by its sums here)
+        wgt[tid] = w0 * share;
+        wgt[NQC + tid] = w1 * share;
         colM[tid] = M;
-        colL[tid] = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
-                    w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
+        colL[tid] = sum;
       }
       // groups with a tile of the unit
       const bool has0 = tiles > 1 || !(it0 & 1), has1 = tiles > 1 || (it0 & 1);
       named_bar(kAllBar, kSoft);
       tc_fence_after();   // (the other group's PVs are done: its threads waited, above)
-      // the CTAs that hold tiles of the unit
-      const long long tile0 = unit0 + kUnitTiles;
-      const int c0 = cta_of(tile0), c1 = cta_of(tile0 + at.tiles - 1);
-      auto out_row = [&](int n2) {
-        const int t = n2 / p.group, hl = n2 - t * p.group;
-        return out + ((size_t(b) * T + t) * p.hq + g * p.group + hl) * D;
-      };
+      __nv_bfloat16* ounit = out + (size_t(b) * T * p.hq + g * p.group) * D;
       // Workspace slots: 2 c for the unit that CTA c's run begins in or with, 2 c + 1 for its last one
       // where that is another; of a unit's CTAs only the first can have it as its last.  So a CTA is the
       // first of one shared unit at most, whose ticket is tickets[c0].
@@ -1206,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (dim < 0 || n2 >= p.nq) continue;
           const float v = a[e] * wgt[n2] + d[e] * wgt[NQC + n2];
           if (c0 == c1)
-            out_row(n2)[dim] = __float2bfloat16_rn(v / colL[n2]);
+            ounit[rowat[n2] + dim] = __float2bfloat16_rn(v);
           else
             p.part_o[(slot * p.nq + n2) * D + dim] = v;
         }
@@ -1261,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = tid + kSoft * j, n2 = e / (D / 4);
             if (n2 >= p.nq) continue;
             const float inv = 1.f / sum[j];
-            reinterpret_cast<uint2*>(out_row(n2))[e % (D / 4)] =
+            reinterpret_cast<uint2*>(ounit + rowat[n2])[e % (D / 4)] =
                 make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv),
                            pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
           }
