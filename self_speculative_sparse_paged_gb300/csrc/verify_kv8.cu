@@ -251,6 +251,11 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t a, uint64_t* v, uint32_t 
         : "memory");
   }
 }
+__device__ __forceinline__ void tmem_ld4(uint32_t a, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(a));
+}
 // Whether the phase with the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -742,19 +747,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(scales + block));
       return v;
     };
-    // group gg's O^T of columns 8 c .. 8 c + 7, the parts added
-    auto load_o = [&](int gg, int c, float (&v)[8]) {
-      const uint32_t at = tl + 2 * Cfg::kSCol + Cfg::kOCol * gg + 8 * c;
-      tmem_ld8(at, v);
-      tmem_ld_wait();
+    // group gg's O^T of columns 4 c .. 4 c + 3, part by part: there after a wait
+    auto load_o = [&](int gg, int c, float (&v)[Cfg::kParts][4]) {
+      const uint32_t at = tl + 2 * Cfg::kSCol + Cfg::kOCol * gg + 4 * c;
 #pragma unroll
-      for (int part = 1; part < Cfg::kParts; ++part) {
-        float w8[8];
-        tmem_ld8(at + part * Cfg::PS, w8);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w8[e];
-      }
+      for (int part = 0; part < Cfg::kParts; ++part) tmem_ld4(at + part * Cfg::PS, v[part]);
     };
     // S of all columns in pairs, the parts added
     auto load_all = [&](uint32_t at, uint64_t (&y2)[NQC / 2]) {
@@ -1199,17 +1196,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first of one shared unit at most, whose ticket is tickets[c0].
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
-      // each group finishes some columns, from both groups' O^T
-#pragma unroll 1
-      for (int c = grp; c < NQC / 8; c += 2) {
-        float a[8] = {}, d[8] = {};
-        if (has0) load_o(0, c, a);
-        if (has1) load_o(1, c, d);
+      // each group finishes half of the columns, from both groups' O^T
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int n2 = 8 * c + e;
+      for (int c = grp; c < NQC / 4; c += 2) {
+        float o0[Cfg::kParts][4] = {}, o1[Cfg::kParts][4] = {};
+        if (has0) load_o(0, c, o0);
+        if (has1) load_o(1, c, o1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4 * Cfg::kParts; ++j)   // (no use of them may move ahead of the wait)
+          asm volatile("" : "+f"(o0[j >> 2][j & 3]), "+f"(o1[j >> 2][j & 3]));
+        const float4 w0 = reinterpret_cast<const float4*>(wgt)[c];
+        const float4 w1 = reinterpret_cast<const float4*>(wgt + NQC)[c];
+        const float f0[4] = {w0.x, w0.y, w0.z, w0.w}, f1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n2 = 4 * c + e;
           if (dim < 0 || n2 >= p.nq) continue;
-          const float v = a[e] * wgt[n2] + d[e] * wgt[NQC + n2];
+          float a = o0[0][e], d = o1[0][e];
+#pragma unroll
+          for (int part = 1; part < Cfg::kParts; ++part) {
+            a += o0[part][e];
+            d += o1[part][e];
+          }
+          const float v = a * f0[e] + d * f1[e];
           if (c0 == c1)
             ounit[rowat[n2] + dim] = __float2bfloat16_rn(v);
           else
