@@ -39,12 +39,13 @@
 //
 // What bounds it.  Long batches of 24 columns at head_dim 128: the DRAM stream (a tile's 735 ns at
 // the copy peak, of which the softmax needs about 300).  One long sequence: what comes before and
-// behind the stream (division of the work 1.2 us, queries 1.5, end 1.2, partial state and ticket 2.4,
-// merge 1.6-3).  Many short sequences: the same a unit.  56 columns at head_dim 64: the softmax's
-// latency, 2100 clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us
-// of 224 less, with P in one f16 part and V turned by four more warps 29 us more).
-//   8 x 49K-64K, 24 columns of 128    160 us (0.89 of the copy peak)      32K: 24.9
-//   4 x 128K, 56 columns of 64        224 us (0.36)            one token each of 12 up to 8K: 18.7    2K, 20 of 64: 12.0
+// behind the stream (division of the work 1.2 us, queries 0.9, first tile 1.9, end 1.2, partial state and
+// ticket 2, merge 1.6-3).  Many short sequences: 5.5 us a unit beside the stream (queries 1800 clocks,
+// first S 1300, first reference 2400, end 3000).  56 columns at head_dim 64: the softmax's latency, 2000
+// clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us of 224 less, with P
+// in one f16 part and V turned by four more warps 29 us more).
+//   8 x 49K-64K, 24 columns of 128    159 us (0.89 of the copy peak)     32K: 24.2     64 x 1000: 46
+//   4 x 128K, 56 columns of 64        215 us (0.38)    one token each of 12 up to 8K: 18.2    2K, 20 of 64: 10.8
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
@@ -60,11 +61,11 @@ constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P
 constexpr int kCapParts = 6;
 constexpr int kSoftWarps = 8, kWarps = 12, kSoft = 32 * kSoftWarps, kThreads = 32 * kWarps;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
-// reference and end; with 3, 6, 8, 10: 12 ragged single tokens 20.4, 18.3, 18.7, 19.6 us, 8 x 2K 21.5,
-// 20.0, 19.3, 19.0, 4 x 128K of 64 228, 226, 224, 223, 32K 24.9, 24.9, 24.8, 25.4, 64 x 1K 53.5, 54.3,
-// 54.4, 55.1), and a CTA takes part for kLeastRun tiles or more (1, 4, 8: one of 4K 15.3, 14.1, 15.4 us,
-// one of 2K 11.8, 12.0, 14.3).
-constexpr int kUnitTiles = 8, kLeastRun = 4;
+// reference and end; with 4, 6, 7, 8: 12 ragged single tokens 18.5, 18.0, 18.3, 18.4 us, 8 x 2K 19.1,
+// 18.3, 17.6, 17.7, 4 x 128K of 64 217, 216, 215, 215, one of 2K 11.0, 10.8, 10.8, 11.0), and a CTA takes
+// part for kLeastRun tiles or more (1, 4, 8, with 8 before: one of 4K 15.3, 14.1, 15.4 us, one of 2K
+// 11.8, 12.0, 14.3).
+constexpr int kUnitTiles = 7, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
 // Instruction descriptor, kind::f8f6f4 (K = 32), fp32 accumulator: A e4m3, B e4m3 or e5m2, both
