@@ -1197,6 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first of one shared unit at most, whose ticket is tickets[c0].
       const int slot0 = 2 * c0 + (run_begin(c0) >= unit0 ? 0 : 1);
       const size_t slot = cta == c0 ? slot0 : 2 * cta;
+      float* part = p.part_o + (slot * p.nq + 4 * grp) * D + max(dim, 0);
       // each group finishes half of the columns, from both groups' O^T
 #pragma unroll
       for (int c = grp; c < NQC / 4; c += 2) {
@@ -1209,22 +1210,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("" : "+f"(o0[j >> 2][j & 3]), "+f"(o1[j >> 2][j & 3]));
         const float4 w0 = reinterpret_cast<const float4*>(wgt)[c];
         const float4 w1 = reinterpret_cast<const float4*>(wgt + NQC)[c];
+        const int4 to = reinterpret_cast<const int4*>(rowat)[c];
         const float f0[4] = {w0.x, w0.y, w0.z, w0.w}, f1[4] = {w1.x, w1.y, w1.z, w1.w};
+        const int row_at[4] = {to.x, to.y, to.z, to.w};
+        float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int n2 = 4 * c + e;
-          if (dim < 0 || n2 >= p.nq) continue;
           float a = o0[0][e], d = o1[0][e];
 #pragma unroll
-          for (int part = 1; part < Cfg::kParts; ++part) {
-            a += o0[part][e];
-            d += o1[part][e];
+          for (int k = 1; k < Cfg::kParts; ++k) {
+            a += o0[k][e];
+            d += o1[k][e];
           }
-          const float v = a * f0[e] + d * f1[e];
-          if (c0 == c1)
-            ounit[rowat[n2] + dim] = __float2bfloat16_rn(v);
-          else
-            p.part_o[(slot * p.nq + n2) * D + dim] = v;
+          v[e] = a * f0[e] + d * f1[e];
+        }
+        const int here = dim < 0 ? 0 : p.nq - 4 * c;   // columns of the four that there are
+        if (c0 == c1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < here) ounit[row_at[e] + dim] = __float2bfloat16_rn(v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < here) part[e * D] = v[e];
+          part += 8 * D;
         }
       }
       tc_fence_before();
