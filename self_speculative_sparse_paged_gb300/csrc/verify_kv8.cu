@@ -321,9 +321,11 @@ struct Kv8Cfg {
   // block a part
   static constexpr int kBlocks = kSideP ? (NP + 127) / 128 : 3;
   static constexpr int kP = kBlocks * 128 * 128;
-  // Ring slots (16 KB at head_dim 128, 8 KB at 64): as many as fit beside the rest.
-  static constexpr int KS = D == 128 ? 5 : kBlocks == 3 ? 6 : 8;
-  static constexpr int VS = D == 128 ? 6 : kBlocks == 3 ? 6 : kBlocks == 2 ? 8 : 10;
+  // Ring slots of K and V (16 KB at head_dim 128, 8 KB at 64).  Few: what more of them ask for ahead only
+  // disturbs the memory (128, K and V slots 5 + 6, 4 + 5, 3 + 5, 2 + 5: batch of eight 163.8, 161.5, 156.3,
+  // 169.9 us, 32K 23.4, 22.7, 23.0, 23.3; 64, 8 + 10, 6 + 6, 5 + 5, 4 + 4: 4 x 128K 202, 196, 195, 194, 8 x 50K
+  // with 24 columns -, -, 111.9, 114.0).
+  static constexpr int KS = D == 128 ? 3 : 5, VS = 5;
   static constexpr int kQ = NS * D;                   // Q^T operand, one a pass
   static constexpr int kPasses = kSideS ? 1 : 2;
   static constexpr int kSCol = (NS + 31) / 32 * 32, kOCol = (NP + 31) / 32 * 32;
@@ -943,11 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k = it >> 1;
         const int t = at.t + int(it - it0);
         const int pos = 128 * t + i;
-        // this position's scales; the next tile's are requested, and the page after that
+        // this position's scales (the next tile's are requested below)
         const int e_k = kv8_exponent(uint8_t(ekb)), e_v = kv8_exponent(uint8_t(evb));
-        ekb = load_scale(k_scales, phys1);
-        evb = load_scale(v_scales, phys1);
-        phys1 = load_page(row, last_page, t + 4);
         const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
         const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
         // (wide: half of the references come to registers while S is on its way, the other half under
@@ -968,50 +967,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         // z of all columns less their references, two to a register pair
         uint64_t y2[NQC / 2];
         float cx[8] = {};   // the capture columns
-        bool left = false, forced = hollow != 0;
-        while (true) {
-          bool need = forced;
-          if (okt) {
-            if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-            load_all(tl + s_col, y2);
-            if (mixed) {
+        bool left = false, need = hollow != 0;
+        if (okt) {
+          if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
+          load_all(tl + s_col, y2);
+          if (mixed) {
 #pragma unroll
-              for (int c = 0; c < NQC / 2; ++c)
-                y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac)[c]);
-            }
+            for (int c = 0; c < NQC / 2; ++c)
+              y2[c] = mul_f32x2(y2[c], reinterpret_cast<const uint64_t*>(colfac)[c]);
+          }
 #pragma unroll
-            for (int c = 0; c < NQC / 2; ++c) {
-              if (kSmemRef && c == NQC / 4) load_refs(NQC / 4);
-              y2[c] = add_f32x2(fma_f32x2(y2[c], f2, add2), kSmemRef ? pre[kSmemRef ? c % kPre : 0] : nr2[kSmemRef ? 0 : c]);
-            }
-            if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
-#pragma unroll
-              for (int c = 0; c < NQC / 2; ++c) {
-                float a, d;
-                unpair_f32(y2[c], a, d);
-                y2[c] = pair_f32(pos > L + tlim[2 * c] ? -INFINITY : a,
-                                 pos > L + tlim[2 * c + 1] ? -INFINITY : d);
-              }
-            }
-            float ym[2] = {-INFINITY, -INFINITY};
+          for (int c = 0; c < NQC / 2; ++c) {
+            if (kSmemRef && c == NQC / 4) load_refs(NQC / 4);
+            y2[c] = add_f32x2(fma_f32x2(y2[c], f2, add2), kSmemRef ? pre[kSmemRef ? c % kPre : 0] : nr2[kSmemRef ? 0 : c]);
+          }
+          if (pos > L) {   // window positions that a row may not see yet, and what lies behind them
 #pragma unroll
             for (int c = 0; c < NQC / 2; ++c) {
               float a, d;
               unpair_f32(y2[c], a, d);
-              ym[c & 1] = fmaxf(fmaxf(ym[c & 1], a), d);
+              y2[c] = pair_f32(pos > L + tlim[2 * c] ? -INFINITY : a,
+                               pos > L + tlim[2 * c + 1] ? -INFINITY : d);
             }
-            need |= fmaxf(ym[0], ym[1]) > kTop;
           }
-          // PV of the group's last tile is done with P's buffer, and with O^T
-          okt = okt && (it < 2 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
-          const bool all_ok = __all_sync(0xffffffffu, okt);
-          if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
-          if (!named_bar_any(1 + grp, 128, need || !okt)) break;
-          const int* vt = votes + (k & 1) * 8 + grp * 4;
-          if (vt[0] | vt[1] | vt[2] | vt[3]) {
-            left = true;
-            break;
+          float ym[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < NQC / 2; ++c) {
+            float a, d;
+            unpair_f32(y2[c], a, d);
+            ym[c & 1] = fmaxf(fmaxf(ym[c & 1], a), d);
           }
+          need |= fmaxf(ym[0], ym[1]) > kTop;
+        }
+        // PV of the group's last tile is done with P's buffer, and with O^T
+        okt = okt && (it < 2 || mbar_wait_bounded(pvdone(grp), (k - 1) & 1));
+        const bool all_ok = __all_sync(0xffffffffu, okt);
+        if (lane == 0) votes[(k & 1) * 8 + grp * 4 + q4] = all_ok ? 0 : 1;
+        const bool agreed = named_bar_any(1 + grp, 128, need || !okt);
+        const int* vt = votes + (k & 1) * 8 + grp * 4;
+        if (agreed) left = vt[0] | vt[1] | vt[2] | vt[3];
+        if (agreed && !left) {
           // Raise: column maxima over the group's 128 positions
           tc_fence_after();
           float* cm = colmax + grp * 4 * NQC;
@@ -1034,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             facs[grp * NQC + i] = ex2(old - now);
             nrg[i] = now == kEmptyMax ? 0.f : -now;
             cm[i] = now;   // (its own column: read above by this thread alone)
+            cm[NQC + i] = nrg[i] - nro;   // what its logits take
           }
           named_bar(1 + grp, 128);
           // (columns with masked logits only stay without one until the next tile)
@@ -1053,7 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               nr2[2 * c + 1] = r.y;
             }
           }
-          if constexpr (kSmemRef) load_refs(0);
+          const ulonglong2* moved = reinterpret_cast<const ulonglong2*>(cm + NQC);
+#pragma unroll
+          for (int c = 0; c < NQC / 4; ++c) {
+            const ulonglong2 r = moved[c];
+            y2[2 * c] = add_f32x2(y2[2 * c], r.x);
+            y2[2 * c + 1] = add_f32x2(y2[2 * c + 1], r.y);
+          }
           if (any) {
 #pragma unroll 1
             for (int c = 0; c < NQC / 8; ++c) {
@@ -1076,7 +1078,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-          forced = false;
           named_bar(1 + grp, 128);   // colmax and the factors are read
         }
         if (left) {
@@ -1084,6 +1085,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_before();
+        // the next tile's scales and the page after that, behind the vote: ahead of it they were in the way
+        // of the logits (4 x 128K of 64: 207 -> 202 us)
+        ekb = load_scale(k_scales, phys1);
+        evb = load_scale(v_scales, phys1);
+        phys1 = load_page(row, last_page, t + 4);
         mbar_arrive(sread(grp));   // S of the group's next tile may come
         if (CAPTURE && pos < Lcap) {
           if constexpr (kSideS) {
