@@ -39,13 +39,13 @@
 //
 // What bounds it.  Long batches of 24 columns at head_dim 128: the DRAM stream (a tile's 735 ns at
 // the copy peak, of which the softmax needs about 300).  One long sequence: what comes before and
-// behind the stream (division of the work 1.2 us, queries 0.9, first tile 1.9, end 1.2, partial state and
-// ticket 2, merge 1.6-3).  Many short sequences: 5.5 us a unit beside the stream (queries 1800 clocks,
-// first S 1300, first reference 2400, end 3000).  56 columns at head_dim 64: the softmax's latency, 2000
+// behind the stream (launch, division of the work 1.2 us, queries 0.9, first tile 1.5, end 1, partial state
+// and ticket 1.8, merge 1.6-3).  Many short sequences: 5 us a unit beside the stream (queries 1800 clocks,
+// first S 1300, first reference 1600, end 2500).  56 columns at head_dim 64: the softmax's latency, 1900
 // clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us of 224 less, with P
 // in one f16 part and V turned by four more warps 29 us more).
-//   8 x 49K-64K, 24 columns of 128    159 us (0.89 of the copy peak)     32K: 24.2     64 x 1000: 46
-//   4 x 128K, 56 columns of 64        215 us (0.38)    one token each of 12 up to 8K: 18.2    2K, 20 of 64: 10.8
+//   8 x 49K-64K, 24 columns of 128    158 us (0.90 of the copy peak)     32K: 23.0     64 x 1000: 44.5
+//   4 x 128K, 56 columns of 64        195 us (0.42)    one token each of 12 up to 8K: 17.8    2K, 20 of 64: 10.1
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
