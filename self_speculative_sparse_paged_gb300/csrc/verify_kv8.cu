@@ -44,8 +44,8 @@
 // first S 1300, first reference 1600, end 2500).  56 columns at head_dim 64: the softmax's latency, 1900
 // clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us of 224 less, with P
 // in one f16 part and V turned by four more warps 29 us more).
-//   8 x 49K-64K, 24 columns of 128    158 us (0.90 of the copy peak)     32K: 23.0     64 x 1000: 44.5
-//   4 x 128K, 56 columns of 64        195 us (0.42)    one token each of 12 up to 8K: 17.8    2K, 20 of 64: 10.1
+//   8 x 49K-64K, 24 columns of 128    157 us (0.90 of the copy peak)     32K: 23.0     64 x 1000: 44.0
+//   4 x 128K, 56 columns of 64        196 us (0.42)    one token each of 12 up to 8K: 17.5    2K, 20 of 64: 10.1
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
@@ -61,11 +61,10 @@ constexpr float kTop = 15.f, kRaise = 11.f;   // log2 of the largest P, and of P
 constexpr int kCapParts = 6;
 constexpr int kSoftWarps = 8, kWarps = 12, kSoft = 32 * kSoftWarps, kThreads = 32 * kWarps;
 // In the division of the work a unit counts kUnitTiles tiles more than it has (its queries, first
-// reference and end; with 4, 6, 7, 8: 12 ragged single tokens 18.5, 18.0, 18.3, 18.4 us, 8 x 2K 19.1,
-// 18.3, 17.6, 17.7, 4 x 128K of 64 217, 216, 215, 215, one of 2K 11.0, 10.8, 10.8, 11.0), and a CTA takes
-// part for kLeastRun tiles or more (1, 4, 8, with 8 before: one of 4K 15.3, 14.1, 15.4 us, one of 2K
-// 11.8, 12.0, 14.3).
-constexpr int kUnitTiles = 7, kLeastRun = 4;
+// reference and end; with 5, 6, 7: 12 ragged single tokens 17.2, 17.5, 17.9 us, 8 x 2K 17.6, 17.2, 17.0,
+// 4 x 128K of 64 196.6, 195.9, 195.0), and a CTA takes part for kLeastRun tiles or more (1, 4, 8, by an
+// earlier kernel: one of 4K 15.3, 14.1, 15.4 us, one of 2K 11.8, 12.0, 14.3).
+constexpr int kUnitTiles = 6, kLeastRun = 4;
 constexpr int kMixed = 1000;   // (in place of the rows' common exponent) rows have their own
 
 // Instruction descriptor, kind::f8f6f4 (K = 32), fp32 accumulator: A e4m3, B e4m3 or e5m2, both
@@ -779,6 +778,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     Place at = start;
     long long unit0 = base + (long long)start.g * (start.tiles + kUnitTiles);   // its span's begin
     uint32_t it0 = 0;             // the CTA's tile with which the unit begins
+    // A unit's first requests: its queries, and the table entries of this thread's position in the
+    // group's first two tiles.  Up to 32 columns they are made under the end of the unit before (256 x 100:
+    // 73.9 -> 71.4 us, 64 x 4000 99.8 -> 98.5; with 56 columns they cost registers, 4 x 128K 195 -> 202).
+    constexpr bool kAhead = !kSmemRef;
+    uint32_t qnext[kAhead ? QPER : 1][D / 64];
+    int pnext[2];
+    // (from: the CTA's tile with which the unit begins)
+    auto request = [&](const Place& u, uint32_t from, uint32_t (*q)[D / 64], int* pages) {
+      const int32_t* row = p.block_table + size_t(u.b) * p.max_pages;
+      const int last_page = (u.L + p.gamma) >> 4, t0 = u.t + int((from ^ uint32_t(grp)) & 1);
+      pages[0] = load_page(row, last_page, t0);
+      pages[1] = load_page(row, last_page, t0 + 2);
+      const __nv_bfloat16* qunit = qbase + (size_t(u.b) * T * p.hq + u.g * p.group) * D;
+#pragma unroll
+      for (int k = 0; k < QPER; ++k) {
+        const int n2 = warp + kSoftWarps * k;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const uint32_t* from_row = reinterpret_cast<const uint32_t*>(qunit + rowat[n2]) + 32 * h + lane;
+          q[k][h] = 0;
+          if constexpr (kAhead) {   // (volatile: asked for here)
+            if (n2 < p.nq) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(q[k][h]) : "l"(from_row));
+          } else {
+            if (n2 < p.nq) q[k][h] = *from_row;
+          }
+        }
+      }
+    };
+    if (kAhead && at.here() > 0) request(at, 0, qnext, pnext);
     for (int tiles = at.here(); tiles > 0; tiles = at.here()) {
       const int L = at.L, g = at.g, b = at.b;
       const int32_t* row = p.block_table + size_t(b) * p.max_pages;
@@ -790,18 +818,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       int phys1 = 0;
       uint32_t ekb, evb;
       {
-        const int phys0 = load_page(row, last_page, at.t + int(first - it0));
-        phys1 = load_page(row, last_page, at.t + int(first - it0) + 2);
-        const __nv_bfloat16* qunit = qbase + (size_t(b) * T * p.hq + g * p.group) * D;
         uint32_t qreg[QPER][D / 64];
+        int pages[2];
+        if constexpr (kAhead) {
+          pages[0] = pnext[0];
+          pages[1] = pnext[1];
 #pragma unroll
-        for (int u = 0; u < QPER; ++u) {
-          const int n2 = warp + kSoftWarps * u;
+          for (int u = 0; u < QPER; ++u)
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            qreg[u][h] = n2 < p.nq ? reinterpret_cast<const uint32_t*>(qunit + rowat[n2])[32 * h + lane]
-                                   : 0u;
+            for (int h = 0; h < D / 64; ++h) qreg[u][h] = qnext[u][h];
+        } else {
+          request(at, it0, qreg, pages);
         }
+        const int phys0 = pages[0];
+        phys1 = pages[1];
         // a row's exponent: its largest element lies in [2^n, 2^(n + 1))
 #pragma unroll
         for (int u = 0; u < QPER; ++u) {
@@ -1165,6 +1195,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sum = reduce_chunk(v, [](float a, float d) { return a + d; });
         if ((lane & 3) == 0) colsum[(grp * 4 + q4) * NQC + 8 * c + (lane >> 2)] = sum;
       }
+      [[maybe_unused]] Place next;
+      if constexpr (kAhead) {
+        next = at;
+        next_unit(next, tiles);
+        if (next.here() > 0) request(next, it0 + uint32_t(tiles), qnext, pnext);
+      }
       // The group's last PV completes its O^T.
       if (any && ok) {
         const uint32_t last = it0 + uint32_t(tiles) - 1 - ((it0 + uint32_t(tiles) - 1 - uint32_t(grp)) & 1);
@@ -1302,7 +1338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar(kAllBar, kSoft);   // the buffers and columns are free again
       unit0 += at.tiles + kUnitTiles;
       it0 += uint32_t(tiles);
-      next_unit(at, tiles);
+      if constexpr (kAhead)
+        at = next;
+      else
+        next_unit(at, tiles);
     }
   }
 
