@@ -49,6 +49,7 @@
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
+#include "lengths.h"
 
 #ifndef VEGAS_KV8_D
 #error "compile with -DVEGAS_KV8_D=64 or -DVEGAS_KV8_D=128"
@@ -447,10 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
 
   // ---- this CTA's run.  A sequence's units have ceil((L + T) / 128) tiles each.
-  auto length = [&](int b) {
-    const int L = p.ctx_lens[b];
-    return L < 0 || L + T > cap ? max(0, min(L, cap - T)) : L;   // (recorded below)
-  };
+  auto length = [&](int b) { return nearest_length(p.ctx_lens[b], T, cap); };   // (recorded below)
   auto tiles_of = [&](int L) { return (L + T + 127) >> 7; };
   auto span_of = [&](int L) { return (long long)(tiles_of(L) + kUnitTiles) * p.hkv; };
   // Up to 32 sequences every warp scans by itself; else warp w first counts [w * chunk, (w + 1) *
@@ -486,10 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     all = __shfl_sync(0xffffffffu, upto, 31);
   }
   if (cta == 0)   // lengths out of range are recorded once
-    for (int b = tid; b < p.batch; b += kThreads) {
-      const int L = p.ctx_lens[b];
-      if (L < 0 || L + T > cap) set_error(p.err, kErrDeviceFault);
-    }
+    for (int b = tid; b < p.batch; b += kThreads)
+      if (!length_fits(p.ctx_lens[b], T, cap)) set_error(p.err, kErrDeviceFault);
   // CTAs that take part
   const int n = int(max(1ll, min((long long)gridDim.x, all / kLeastRun)));
   // (64-bit quotients take a few hundred clocks: 32-bit ones while they do)
