@@ -24,6 +24,7 @@
 // the sum of those two columns of the same S^T tile, times the scale.  The
 // two columns take no part in the softmax.
 #include "kernels.h"
+#include "lengths.h"
 #include "split_merge.cuh"
 
 namespace vegas {
@@ -71,9 +72,9 @@ __global__ void __launch_bounds__(VerifyCfg<D, NT>::W * 32, 1)
   const int T = p.gamma + 1;
   const int cap = p.max_pages * 16;
   int L = p.ctx_lens[b];
-  if (L < 0 || L + T > cap) {
+  if (!length_fits(L, T, cap)) {
     if (tid == 0) set_error(p.err, kErrDeviceFault);
-    L = max(0, min(L, cap - T));
+    L = nearest_length(L, T, cap);
   }
   const int npages = (L + T + 15) / 16;
   const int pbeg = split * p.pages_per_split;

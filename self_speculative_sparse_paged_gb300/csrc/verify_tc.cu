@@ -42,6 +42,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.h"
+#include "lengths.h"
 
 #ifndef VEGAS_TC_D
 #error "compile with -DVEGAS_TC_D=64 or -DVEGAS_TC_D=128"
@@ -231,9 +232,9 @@ __global__ void __launch_bounds__(384, 1)
   }
 
   int L = p.ctx_lens[b];
-  if (L < 0 || L + T > cap) {
+  if (!length_fits(L, T, cap)) {
     if (tid == 0) set_error(p.err, kErrDeviceFault);
-    L = max(0, min(L, cap - T));
+    L = nearest_length(L, T, cap);
   }
   const int npages = (L + T + 15) / 16;
   const int pend = min(pnext, npages);

@@ -61,3 +61,8 @@ def test_lengths_near_2_to_31_do_not_fit(tmp_path):
 
 def test_the_8_bit_verify_uses_it():
     _uses_the_test_of_lengths("verify_kv8.cu")
+
+
+def test_the_bf16_verifies_use_it():
+    _uses_the_test_of_lengths("verify_tc.cu")
+    _uses_the_test_of_lengths("verify_attn.cu")
