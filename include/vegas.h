@@ -462,7 +462,8 @@ typedef struct {
  * [0, 15], |softmax_scale| <= 2^20, batch <= 2^16.  A workspace is always needed.
  *
  * vegas_sparse_decode_attn_kv8: vegas_sparse_decode_attn (section 3: its lists,
- * limits and refusals) over the 8-bit cache; q exact in f16 (an element below 2^-31
+ * limits and refusals) over the 8-bit cache; a tail_len[b] above max_tail is recorded as a
+ * device fault and cut to it; q exact in f16 (an element below 2^-31
  * of its head's largest is off by at most 2^-39 of it), exponentials rounded to f16
  * (half a step, 2^-11 of each, or 2^-31 of the row's largest), the rest as above;
  * |softmax_scale| <= 2^20.

@@ -127,7 +127,11 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
     kb = max(0, min(kb, p.k_max));
   }
   const int tstart = p.tail_start[b];
-  const int tlen = max(0, p.tail_len[b]);
+  int tlen = max(0, p.tail_len[b]);
+  if (tlen > p.max_tail) {   // (before it is added to anything: it may be as large as an int)
+    if (tid == 0 && g == 0 && rank == 0) set_error(p.err, kErrDeviceFault);
+    tlen = p.max_tail;
+  }
   const int total = kb + tlen;
   const int rend = min(rbeg + p.rows_per_split, total);
   const int nrows = max(0, rend - rbeg);

@@ -90,6 +90,7 @@ struct SparseParams {
 struct DraftKv8Params : SparseParams {
   const uint8_t* k_scale;   // [pages][Hkv] exponent bytes
   const uint8_t* v_scale;
+  int max_tail;
 };
 
 struct SelectParams {

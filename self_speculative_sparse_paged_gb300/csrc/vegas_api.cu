@@ -774,6 +774,7 @@ vegas_status_t sparse_impl(
   p.k_per_seq = k_per_seq;
   p.tail_start = tail_start;
   p.tail_len = tail_len;
+  p.max_tail = max_tail;
   p.k_max = k_max;
   p.num_pages = kv->num_pages;
   p.max_pages = kv->max_pages_per_seq;

@@ -45,3 +45,30 @@ def test_verify_records_a_length_that_no_table_holds(ctx, masked):
     call(held)                                              # the workspace serves the next call
     vg.vegas_read_device_status()
     assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("long_tail", [7, 200, TOP - 11, TOP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_draft_records_a_tail_longer_than_the_calls(d, long_tail):
+    """A tail above max_tail is recorded and cut to it (its sum with the list may pass 2^31), and the
+    sequence beside it is answered as if it were alone."""
+    rng = np.random.default_rng(d)
+    hq, hkv, max_tail = 8, 2, 6
+    c = Cache(rng, [10, 10], hq, hkv, d)
+    c.upload()
+    q = queries(rng, (2, hq, d)).to(DEV)
+    idx = dev(np.sort(rng.choice(100, (2, hkv, 12)), -1).astype(np.int32))
+    k = dev(np.array([12, 12], np.int32))
+    results = []
+    for tails in ([4, long_tail], [4, max_tail]):
+        out = torch.full_like(q, float("nan"))
+        vg.vegas_read_device_status()
+        vg.vegas_sparse_decode_attn_kv8(c.kv, q, out, idx, 12, k, dev(np.array([100, 100], np.int32)),
+                                        dev(np.array(tails, np.int32)), max_tail, 2, 0.1)
+        if tails[1] != max_tail:
+            with pytest.raises(vg.VegasError) as e:
+                vg.vegas_read_device_status()
+            assert e.value.status == 5
+        vg.vegas_read_device_status()
+        results.append(out)
+    assert torch.isfinite(results[0]).all() and torch.equal(*results)
