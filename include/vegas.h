@@ -449,8 +449,9 @@ typedef struct {
  * KV head's queries where their own lie within a factor of 2^4, else the row's.
  * Captured scores take the summed query in six parts.  Exponentials (times
  * 2^e of V's block) meet V's codes in f16 cut into three e5m2 parts, within 2^-9 +
- * 2^-13 of each and 2^-28 of the row's largest; the row's sum takes them in fp32,
- * sums are fp32, the output is rounded once to bf16.
+ * 2^-13 of each and 2^-28 of the row's largest; the row's sum takes them in fp32 by
+ * their logits alone, whatever the scales of V's blocks (terms 2^-45 of the row's heaviest
+ * and less may be left out), sums are fp32, the output is rounded once to bf16.
  * scores may be NULL (nothing captured; capture_row_mask is then ignored).  K and V
  * of attended positions must be finite codes, |q| below 2^40; other slots may hold
  * anything.

@@ -22,6 +22,19 @@ __device__ __forceinline__ int kv8_exponent(uint8_t byte) {
 }
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
+// Row sums over blocks whose scales lie far apart.  With x a logit in binades and e_v the block's exponent,
+// P = 2^(x + e_v - r) multiplies the codes and P 2^-e_v goes into the row's sum.  References r follow
+// x + e_v, so they lie up to 120 binades above what a term of the sum alone would need, and what weighs in
+// the sum may have a P that fp32 does not hold (the exponential gives 0 below 2^-126).  Hence
+//  - a sum that moves from one reference to another takes 2^(d / 2) twice for 2^d: after the first its own
+//    2^-e_v has it in range;
+//  - blocks of e_v < kKv8Deep take their terms of the sum from an exponential that is 2^kKv8Lift larger.
+// As r <= max(x + e_v) - 7, a term is lost 45 binades below the row's heaviest (126 + kKv8Deep - 60 + 7), one
+// of a deep block 77 below it.
+constexpr int kKv8Deep = -28, kKv8Lift = 64;
+// The factor of a sum that moves by 2^d, to be taken twice.
+__device__ __forceinline__ float half_weight(float d) { return ex2(0.5f * d); }
+
 // The least exponent whose block holds a magnitude of these bf16 bits (sign removed, finite):
 // x = 1.f * 2^n <= 1.75 * 2^8 * 2^e.
 __device__ __forceinline__ int kv8_exponent_for(uint32_t bf16_bits) {

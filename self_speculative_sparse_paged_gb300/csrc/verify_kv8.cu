@@ -30,8 +30,8 @@
 // Parts lie side by side in N where tensor memory holds their columns (one pass over the A
 // operand; an MMA takes 45 clocks up to N = 64 and 64 at 128), else they share an accumulator.
 // P <= 2^15 (f16 ends at 65504) and the largest P is 2^11 or more when r was raised, so P's grid
-// reaches 2^-28 below the largest.  e_v spans 120, so that no term that weighs in a row sum is lost to
-// fp32's smallest number (its P is at least 2^-121).
+// reaches 2^-28 below the largest.  e_v spans 120 binades, and row sums keep what weighs in them all the
+// same (kv8.cuh).
 //
 // A unit that one CTA covers is written by it; the pieces of a shared one go to the workspace
 // (fp32 O, maximum and sum of each row), and the CTA that arrives last on the unit's ticket merges
@@ -278,6 +278,16 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// sum += 2^(y + kKv8Lift) f, of a pair.  (In one piece: as separate steps their temporaries cost the
+// registers of the whole loop, 8 x 50K with 64 columns of 64: 207 -> 222 us.)
+__device__ __forceinline__ void add_lifted(uint64_t& sum, uint64_t y, float f) {
+  asm volatile(
+      "{\n .reg .f32 a, b, c, d;\n mov.b64 {a, b}, %1;\n mov.b64 {c, d}, %0;\n"
+      " add.f32 a, a, %3;\n add.f32 b, b, %3;\n ex2.approx.ftz.f32 a, a;\n ex2.approx.ftz.f32 b, b;\n"
+      " fma.rn.f32 c, a, %2, c;\n fma.rn.f32 d, b, %2, d;\n mov.b64 %0, {c, d};\n}"
+      : "+l"(sum)
+      : "l"(y), "f"(f), "f"(float(kKv8Lift)));
 }
 // op over the warp's lanes of each of eight columns: lane l gets column l / 4's.  In three steps a
 // lane exchanges half of the columns it still holds for the other half of another lane's.
@@ -973,7 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = 128 * t + i;
         // this position's scales (the next tile's are requested below)
         const int e_k = kv8_exponent(uint8_t(ekb)), e_v = kv8_exponent(uint8_t(evb));
-        const float f_k = two_to(e_k), un = two_to(-e_v), f = scale0 * f_k, add = float(e_v);
+        const bool deep = e_v < kKv8Deep;   // (its part of the row sums is made beside a raise, not from P)
+        const float f_k = two_to(e_k), un = deep ? 0.f : two_to(-e_v), f = scale0 * f_k, add = float(e_v);
         const uint64_t f2 = pair_f32(f, f), add2 = pair_f32(add, add), un2 = pair_f32(un, un);
         // (wide: half of the references come to registers while S is on its way, the other half under
         // the first one's arithmetic; all of them do not fit)
@@ -993,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // z of all columns less their references, two to a register pair
         uint64_t y2[NQC / 2];
         float cx[8] = {};   // the capture columns
-        bool left = false, need = hollow != 0;
+        bool left = false, need = hollow != 0 || deep;
         if (okt) {
           if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
           load_all(tl + s_col, y2);
@@ -1052,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top = fmaxf(fmaxf(cm[i], cm[NQC + i]), fmaxf(cm[2 * NQC + i], cm[3 * NQC + i]));
             const float old = ((hollow >> i) & 1) ? kEmptyMax : -nro;
             const float now = fmaxf(old, top - nro - kRaise);
-            facs[grp * NQC + i] = ex2(old - now);
+            facs[grp * NQC + i] = half_weight(old - now);
             nrg[i] = now == kEmptyMax ? 0.f : -now;
             cm[i] = now;   // (its own column: read above by this thread alone)
             cm[NQC + i] = nrg[i] - nro;   // what its logits take
@@ -1067,8 +1078,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NQC / 4; ++c) {
             const float4 v = fc[c];
-            ls2[2 * c] = mul_f32x2(ls2[2 * c], pair_f32(v.x, v.y));
-            ls2[2 * c + 1] = mul_f32x2(ls2[2 * c + 1], pair_f32(v.z, v.w));
+            const uint64_t xy = pair_f32(v.x, v.y), zw = pair_f32(v.z, v.w);
+            ls2[2 * c] = mul_f32x2(mul_f32x2(ls2[2 * c], xy), xy);
+            ls2[2 * c + 1] = mul_f32x2(mul_f32x2(ls2[2 * c + 1], zw), zw);
             if constexpr (!kSmemRef) {
               const ulonglong2 r = reinterpret_cast<const ulonglong2*>(nrg)[c];
               nr2[2 * c] = r.x;
@@ -1082,10 +1094,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             y2[2 * c] = add_f32x2(y2[2 * c], r.x);
             y2[2 * c + 1] = add_f32x2(y2[2 * c + 1], r.y);
           }
+          if (__any_sync(0xffffffffu, deep)) {
+            const float lifted = deep ? two_to(-e_v - kKv8Lift) : 0.f;
+#pragma unroll
+            for (int c = 0; c < NQC / 2; ++c) add_lifted(ls2[c], y2[c], lifted);
+          }
           if (any) {
 #pragma unroll 1
             for (int c = 0; c < NQC / 8; ++c) {
-              const float4 a = fc[2 * c], d = fc[2 * c + 1];
+              float4 a = fc[2 * c], d = fc[2 * c + 1];
+              a = make_float4(a.x * a.x, a.y * a.y, a.z * a.z, a.w * a.w);
+              d = make_float4(d.x * d.x, d.y * d.y, d.z * d.z, d.w * d.w);
 #pragma unroll
               for (int part = 0; part < Cfg::kParts; ++part) {
                 float v8[8];
@@ -1215,10 +1234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the piece's maximum and sum of a column, and the weights of the two groups' states
       if (tid < NQC) {
         const float m0 = colmax[tid], m1 = colmax[4 * NQC + tid], M = fmaxf(m0, m1);
-        const float w0 = ex2(m0 - M), w1 = ex2(m1 - M);
+        const float h0 = half_weight(m0 - M), h1 = half_weight(m1 - M), w0 = h0 * h0, w1 = h1 * h1;
         const float* cs = colsum + tid;
-        const float sum = w0 * (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) +
-                          w1 * (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]);
+        const float sum = (cs[0] + cs[NQC] + cs[2 * NQC] + cs[3 * NQC]) * h0 * h0 +
+                          (cs[4 * NQC] + cs[5 * NQC] + cs[6 * NQC] + cs[7 * NQC]) * h1 * h1;
         const float share = c0 == c1 ? 1.f / sum : 1.f;   // (a whole unit is divided by its sums here)
         wgt[tid] = w0 * share;
         wgt[NQC + tid] = w1 * share;
@@ -1310,9 +1329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-              const float now = fmaxf(M[j], m[j].x), a = ex2(M[j] - now), w = ex2(m[j].x - now);
-              M[j] = now;
-              sum[j] = sum[j] * a + w * m[j].y;
+              const float d = M[j] - m[j].x, h = half_weight(-fabsf(d));
+              const bool up = d < 0.f;
+              const float a = up ? h * h : 1.f, w = up ? 1.f : h * h;
+              M[j] = fmaxf(M[j], m[j].x);
+              sum[j] = up ? fmaf(sum[j] * h, h, m[j].y) : fmaf(m[j].y * h, h, sum[j]);
               acc[j].x = acc[j].x * a + w * v[j].x;
               acc[j].y = acc[j].y * a + w * v[j].y;
               acc[j].z = acc[j].z * a + w * v[j].z;
