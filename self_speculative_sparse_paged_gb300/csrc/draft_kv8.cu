@@ -221,12 +221,15 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
   uint32_t qf[D / 16][NT][2];
   float col[NT][2];   // logit units of column 2 (lane % 4) + e, log2
   // the scale bytes were requested before the first rows; every warp reads its entries' below
+  bool deep = false;   // the CTA's range has blocks far below the others
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     if (past(u)) break;
     const int i = tid + u * NTH;
-    if (i < nrows)
+    if (i < nrows) {
       exps[i] = uint16_t(uint8_t(kv8_exponent(ek[u]))) | uint16_t(uint8_t(kv8_exponent(ev[u]))) << 8;
+      deep |= kv8_exponent(ev[u]) < kKv8Deep;
+    }
   }
   kv8_load_q<D, NT>(reinterpret_cast<const __nv_bfloat16*>(p.q) + (size_t(b) * p.hq + g * p.group) * D,
                     p.group, qf, col);
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) col[nt][e] *= p.scale_log2;
-  __syncthreads();
+  deep = __syncthreads_or(deep);
   WarpState<D, NT> st;
   st.init();
 
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
         for (int e = 0; e < 2; ++e)   // (columns past the group have zero queries)
           z[nt][2 * j + e] = fmaf(z[nt][2 * j + e], col[nt][e] * f, zv);
     }
-    kv8_softmax_pv<D, NT>(st, z, unscale, stage0 + s * STAGE + TILE);
+    kv8_softmax_pv<D, NT>(st, z, unscale, deep, stage0 + s * STAGE + TILE);
     __syncwarp();
     if (i + STAGES < nmy) {
       fence_proxy_async_smem();
@@ -279,8 +282,8 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
   }
   reduce_row_sums<D, NT>(st);
   __syncthreads();
-  cta_merge_to_smem<D, NT, W, Kv8Dims<D>>(st, stage_area, DraftKv8Cfg<D, NT, W>::kStageBytes, p.group,
-                                          pM, pL, pO);
+  cta_merge_to_smem<D, NT, W, Kv8Dims<D>, true>(st, stage_area, DraftKv8Cfg<D, NT, W>::kStageBytes,
+                                                p.group, pM, pL, pO);
   __syncthreads();   // the pushes below read elements other threads merged
 
   // Cluster merge: CTA r owns the output elements [r * per, (r + 1) * per) of
@@ -338,9 +341,9 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
       float L = 0.f, a = 0.f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float f = r < CL ? ex2(mr[r] - M) : 0.f;
-        L += f * lr[r];
-        a += f * v[r];
+        const float h = r < CL ? half_weight(mr[r] - M) : 0.f;
+        L += lr[r] * h * h;
+        a += h * h * v[r];
       }
       out[(size_t(b) * p.hq + g * p.group + n) * D + (e % D)] =
           __float2bfloat16_rn(L > 0.f ? a / L : 0.f);

@@ -32,8 +32,6 @@ __device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t
 // As r <= max(x + e_v) - 7, a term is lost 45 binades below the row's heaviest (126 + kKv8Deep - 60 + 7), one
 // of a deep block 77 below it.
 constexpr int kKv8Deep = -28, kKv8Lift = 64;
-// The factor of a sum that moves by 2^d, to be taken twice.
-__device__ __forceinline__ float half_weight(float d) { return ex2(0.5f * d); }
 
 // The least exponent whose block holds a magnitude of these bf16 bits (sign removed, finite):
 // x = 1.f * 2^n <= 1.75 * 2^8 * 2^e.

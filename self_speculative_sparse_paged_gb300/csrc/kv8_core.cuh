@@ -11,10 +11,10 @@
 //      (D / 8) r + 2 mt (row r) and + 2 mt + 1 (row r + 8).
 //
 // Scales: with x the logit in log2 units and V's exponent e_v, z = x + e_v and P = 2^(z - m)
-// multiplies V's codes, while the row sum takes P 2^-e_v = 2^(x - m) in fp32.  m is a reference
-// with P <= 2^15 (f16 ends at 65504), at least 7 below the largest z when it is raised, so that P's
-// f16 grid reaches 2^-31 below the largest and its roundings are 2^-11 of each.  e_v spans 120 at
-// most, so a term of the row sum that weighs anything is far above fp32's smallest.
+// multiplies V's codes, while the row sum takes P 2^-e_v = 2^(x - m) in fp32 (of a deep block from
+// 2^(z - m + kKv8Lift): kv8.cuh).  m is a reference with P <= 2^15 (f16 ends at 65504), at least 7
+// below the largest z when it is raised, so that P's f16 grid reaches 2^-31 below the largest and
+// its roundings are 2^-11 of each.
 #pragma once
 
 #include "attn_core.cuh"
@@ -138,10 +138,10 @@ __device__ __forceinline__ void kv8_scores(uint32_t k_base, const uint32_t (&qf)
 }
 
 // Online softmax with the group's z (masked entries -inf) and O^T += V^T P^T.  unscale[0], [1]:
-// 2^-e_v of positions r and r + 8.
+// 2^-e_v of positions r and r + 8 (changed here).  deep: some of the CTA's blocks lie below 2^kKv8Deep.
 template <int D, int NT>
 __device__ __forceinline__ void kv8_softmax_pv(WarpState<D, NT>& st, const float (&z)[NT][4],
-                                               const float (&unscale)[2], uint32_t v_base) {
+                                               float (&unscale)[2], bool deep, uint32_t v_base) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   bool need = false;
 #pragma unroll
@@ -158,15 +158,28 @@ __device__ __forceinline__ void kv8_softmax_pv(WarpState<D, NT>& st, const float
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         const float mnew = fmaxf(st.m[nt][e], mx - kKv8Raise);
-        const float alpha = ex2(st.m[nt][e] - mnew);
+        const float h = half_weight(st.m[nt][e] - mnew), alpha = h * h;
         st.m[nt][e] = mnew;
-        st.l[nt][e] *= alpha;
+        st.l[nt][e] = st.l[nt][e] * h * h;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
           st.o[mt][nt][e] *= alpha;
           st.o[mt][nt][2 + e] *= alpha;
         }
       }
+  }
+  if (deep) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (unscale[j] <= two_to(-kKv8Deep)) continue;
+      const float lifted = unscale[j] * two_to(-kKv8Lift);
+      unscale[j] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          st.l[nt][e] = fmaf(ex2(z[nt][2 * j + e] - st.m[nt][e] + float(kKv8Lift)), lifted, st.l[nt][e]);
+    }
   }
   uint32_t pb[NT][2];
 #pragma unroll

@@ -119,8 +119,9 @@ __device__ __forceinline__ void finish_splits(const SplitWorkspace& ws, int unit
 // (running max and row sum of column n) and outO[n * D + dim] (unnormalised
 // output), for n < nq.  Called by every thread after reduce_row_sums; `area`
 // is free shared memory of `area_bytes` (the drained stage buffers), distinct
-// from the out arrays.
-template <int D, int NT, int W, class Dims = MmaDims>
+// from the out arrays.  FarSums: a row sum may weigh although 2^(m - M) is below
+// fp32's smallest (the 8-bit cache's, kv8.cuh).
+template <int D, int NT, int W, class Dims = MmaDims, bool FarSums = false>
 __device__ __forceinline__ void cta_merge_to_smem(const WarpState<D, NT>& st, uint8_t* area,
                                                   size_t area_bytes, int nq, float* outM,
                                                   float* outL, float* outO) {
@@ -154,6 +155,12 @@ __device__ __forceinline__ void cta_merge_to_smem(const WarpState<D, NT>& st, ui
     float lsum = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
+      if constexpr (FarSums) {
+        const float h = half_weight(cm[w * NPAD + n] - M);
+        cm[w * NPAD + n] = h * h;
+        lsum += cl[w * NPAD + n] * h * h;
+        continue;
+      }
       const float f = ex2(cm[w * NPAD + n] - M);
       cm[w * NPAD + n] = f;
       lsum += f * cl[w * NPAD + n];

@@ -197,6 +197,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^(d / 2): a factor 2^d taken in two steps, for what is in fp32's range after the first.
+__device__ __forceinline__ float half_weight(float d) { return ex2(0.5f * d); }
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 // Tensor memory allocation (one full warp), columns a power of two >= 32.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {

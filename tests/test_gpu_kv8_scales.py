@@ -107,3 +107,26 @@ def test_verify_sums_whatever_the_scales(hq, d, n, batch, case):
     for got in out.double().cpu().numpy()[::max(1, batch // 8)]:
         for t in range(2):
             c.check(q[0, t].double().numpy(), got[t], np.arange(ctx + t + 1), P_PARTS)
+
+
+@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("hq,d,n,batch", [(4, 128, 20000, 1), (8, 64, 20000, 1), (16, 128, 6000, 3), (3, 64, 300, 1),
+                                          (16, 64, 20000, 4), (2, 128, 4000, 200), (1, 64, 4000, 200)])
+def test_drafts_sum_whatever_the_scales(hq, d, n, batch, case):
+    """Lists over one cluster, over a few CTAs, and of one CTA each."""
+    rng = np.random.default_rng(n + hq)
+    c = Logits(rng, *CASES[case](rng, n), d, hq)
+    kv = c.kv(batch)
+    q = queries(rng, (1, hq, d))
+    q[..., 0] = 1
+    k, tail = n - 20, 4
+    dq = q.to(DEV).expand(batch, hq, d).contiguous()
+    out = torch.full_like(dq, float("nan"))
+    idx = dev(np.tile(np.arange(k, dtype=np.int32), (batch, 1, 1)))
+    vg.vegas_sparse_decode_attn_kv8(kv, dq, out, idx, k, dev(np.full(batch, k, np.int32)),
+                                    dev(np.full(batch, n - tail, np.int32)), dev(np.full(batch, tail, np.int32)), tail,
+                                    batch, LN2)
+    vg.vegas_read_device_status()
+    at = np.concatenate([np.arange(k), n - tail + np.arange(tail)])
+    for got in out.double().cpu().numpy()[::max(1, batch // 8)]:
+        c.check(q[0].double().numpy(), got, at, 0.0)
