@@ -257,6 +257,13 @@ __device__ __forceinline__ void tmem_ld4(uint32_t a, float (&v)[4]) {
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                : "r"(a));
 }
+// Behind the wait for loads of v (of its first Used elements): the wait does not name them, and no use of
+// them may move ahead of it.
+template <int Used = 0, int N>
+__device__ __forceinline__ void loaded(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < (Used ? Used : N); ++i) asm volatile("" : "+f"(v[i]));
+}
 // Whether the phase with the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -1007,7 +1014,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool left = false, need = hollow != 0 || deep;
         if (okt) {
           if constexpr (CAPTURE) tmem_ld8(tl + s_col + Cfg::kCap0, cx);
-          load_all(tl + s_col, y2);
+          load_all(tl + s_col, y2);   // (waits for both)
+          if constexpr (CAPTURE) {
+            loaded<Cfg::kCap>(cx);
+            if constexpr (kSideS) {
+#pragma unroll
+              for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
+            }
+          }
           if (mixed) {
 #pragma unroll
             for (int c = 0; c < NQC / 2; ++c)
@@ -1110,6 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v8[8];
                 tmem_ld8(tl + o_col + part * Cfg::PS + 8 * c, v8);
                 tmem_ld_wait();
+                loaded(v8);
                 v8[0] *= a.x;
                 v8[1] *= a.y;
                 v8[2] *= a.z;
@@ -1137,10 +1152,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         phys1 = load_page(row, last_page, t + 4);
         mbar_arrive(sread(grp));   // S of the group's next tile may come
         if (CAPTURE && pos < Lcap) {
-          if constexpr (kSideS) {
-#pragma unroll
-            for (int j = 0; j < 3; ++j) cx[j] = cx[2 * j] + cx[2 * j + 1];
-          }
           srow[pos] = fmaf(fmaf(cx[2], 0x1p-8f, cx[1]), 0x1p-8f, cx[0]) * (f_k * cap_scale);
         }
         // P = 2^y in three e5m2 parts (upper bytes of f16: cut, cut, rounded), eight columns of a part in
@@ -1263,8 +1274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (has1) load_o(1, c, o1);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4 * Cfg::kParts; ++j)   // (no use of them may move ahead of the wait)
-          asm volatile("" : "+f"(o0[j >> 2][j & 3]), "+f"(o1[j >> 2][j & 3]));
+        for (int k = 0; k < Cfg::kParts; ++k) {
+          loaded(o0[k]);
+          loaded(o1[k]);
+        }
         const float4 w0 = reinterpret_cast<const float4*>(wgt)[c];
         const float4 w1 = reinterpret_cast<const float4*>(wgt + NQC)[c];
         const int4 to = reinterpret_cast<const int4*>(rowat)[c];
