@@ -179,7 +179,7 @@ struct Kv8ReadParams {
   const int32_t* to_block_table;
   const int32_t *first, *upto;          // [B]; first may be null
   int num_pages, max_pages, to_num_pages, to_max_pages;
-  int hkv, head_dim;
+  int hkv, head_dim, batch;
   int* err;
 };
 
@@ -312,7 +312,7 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap,
                           cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv8_append(const RopeKv8Params& p, int sms, cudaStream_t stream);
-cudaError_t launch_kv8_read(const Kv8ReadParams& p, int batch, cudaStream_t stream);
+cudaError_t launch_kv8_read(const Kv8ReadParams& p, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, bool bf16, cudaStream_t stream);
 
 // One CTA waits on an mbarrier nothing arrives on, bounded by limit_ns; on

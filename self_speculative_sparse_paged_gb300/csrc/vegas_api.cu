@@ -1057,8 +1057,9 @@ VEGAS_API vegas_status_t vegas_kv8_read(const vegas_paged_kv8_t* kv, const vegas
   p.to_max_pages = to->max_pages_per_seq;
   p.hkv = kv->num_kv_heads;
   p.head_dim = kv->head_dim;
+  p.batch = batch;
   p.err = err;
-  cudaError_t e = vegas::launch_kv8_read(p, batch, static_cast<cudaStream_t>(stream));
+  cudaError_t e = vegas::launch_kv8_read(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "8-bit cache read launch");
   return VEGAS_OK;
 }
