@@ -448,13 +448,14 @@ typedef struct {
  * most 2^-17 of the largest below; the largest is that of all window rows of the
  * KV head's queries where their own lie within a factor of 2^4, else the row's.
  * Captured scores take the summed query in six parts.  Exponentials (times
- * 2^e of V's block) meet V's codes in f16 cut into three e5m2 parts, within 2^-9 +
- * 2^-13 of each and 2^-28 of the row's largest; the row's sum takes them in fp32 by
- * their logits alone, whatever the scales of V's blocks (terms 2^-45 of the row's heaviest
- * and less may be left out), sums are fp32, the output is rounded once to bf16.
+ * 2^e of V's block) meet V's codes in f16 cut into three e5m2 parts, within
+ * 1.1 * 2^-9 of each (the rounding to f16 among it) and 1.01 * 2^-28 of the row's
+ * largest.  The row's sum takes them in fp32 by their logits alone, whatever the
+ * scales of V's blocks (terms of 2^-45 of the row's heaviest and less may be left
+ * out).  Sums are fp32, the output is rounded once to bf16.
  * scores may be NULL (nothing captured; capture_row_mask is then ignored).  K and V
- * of attended positions must be finite codes, |q| below 2^40; other slots may hold
- * anything.
+ * of attended positions must be finite codes, |q| below 2^40 and logits below 2^96 in
+ * magnitude; other slots may hold anything.
  *   workspace: vegas_verify_kv8_workspace_size() bytes, 256-byte aligned.  Calls of
  *        other batches, capacities and gammas may use the same one in turn, if it holds
  *        the largest of their sizes; after a reported VEGAS_ERR_DEVICE_TIMEOUT it has to
@@ -463,11 +464,11 @@ typedef struct {
  * [0, 15], |softmax_scale| <= 2^20, batch <= 2^16.  A workspace is always needed.
  *
  * vegas_sparse_decode_attn_kv8: vegas_sparse_decode_attn (section 3: its lists,
- * limits and refusals) over the 8-bit cache; a tail_len[b] above max_tail is recorded as a
- * device fault and cut to it; q exact in f16 (an element below 2^-31
- * of its head's largest is off by at most 2^-39 of it), exponentials rounded to f16
- * (half a step, 2^-11 of each, or 2^-31 of the row's largest), the rest as above;
- * |softmax_scale| <= 2^20.
+ * limits and refusals) over the 8-bit cache; a tail_len[b] above max_tail is recorded
+ * as a device fault and cut to it.  q is exact in f16 (an element below 2^-31 of its
+ * head's largest is off by at most 2^-39 of it), exponentials are rounded to f16 (half
+ * a step, 2^-11 of each, or 2^-31 of the row's largest), the rest is as above, the
+ * limits of q and of logits among it; |softmax_scale| <= 2^20.
  */
 vegas_status_t vegas_rope_append_kv8(
     const vegas_paged_kv8_t* kv, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

@@ -22,7 +22,8 @@
 //       take P 2^-e_v in fp32.
 //   O^T[D x N] += V^T P^T   kind::f8f6f4, M = D: V's codes as they lie (read MN-major), P as the
 //       sum of three e5m2 parts.  e5m2 is the upper byte of f16, so the parts are cut off P's f16
-//       (each takes three bits or more, the last is rounded: 2^-9 of P at most), with f16's range.
+//       (each takes three bits or more, the last is rounded: with f16's own rounding 1.1 * 2^-9 of P at
+//       most, just below 1.1426 * 2^e), with f16's range.
 //       Turning V into f16 instead moved 1200-1300 clocks' worth of a tile's 1425 through
 //       shared memory at head_dim 128, which bounded that kernel (172-179 us on a batch of eight
 //       of 49K-64K); this one moves about 750.
