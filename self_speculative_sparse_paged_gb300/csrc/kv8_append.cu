@@ -9,15 +9,16 @@
 // holds rows of earlier calls (positions before ctx), whose codes become e4m3(c * 2^(e_old - e))
 // when e is larger.  An exponent never falls while its page holds rows.
 //
-// A block's maximum needs all of its rows, so the unit of work is a page: one CTA takes the (at
-// most 16) new rows of a page, all heads.  A warp holds one KV head's rows of the page in
-// registers: lane l has unit l % (d / 16) (two chunks of 8 elements: the two halves of 8 pairs)
-// of every (32 / (d / 16))-th row, so the maximum is a warp reduction and no row is read twice.
-// The queries of the page's rows are then turned by all warps, an item a unit.  Cosines and
-// sines are made once per (row, pair) and shared by all heads.  The angle in turns is taken modulo 1
-// by 64-bit integers: a pair's frequency over 2 pi, from fp64, as a fraction F of 2^64, and p F
-// wraps by itself.  (In fp64, of which an SM does two operations a clock, the angles of 16K rows took
-// 10 us of 70, and as much again for every part that the heads were divided into.)
+// A block's maximum needs all of its rows, so the unit of work is a page: two CTAs take the (at
+// most 16) new rows of a page, each every other (KV head, K or V) and half of the query heads.  A warp
+// holds one KV head's rows of the page in registers: lane l has unit l % (d / 16) (two chunks of 8
+// elements: the two halves of 8 pairs) of every (32 / (d / 16))-th row, so the maximum is a warp
+// reduction and no row is read twice.  The queries of the page's rows are then turned by all warps, an
+// item a unit.  Each CTA makes the cosines and sines once per (row, pair), for all of its heads.  The
+// angle in turns is taken modulo 1 by 64-bit integers: a pair's frequency over 2 pi, from fp64, as a
+// fraction F of 2^64, and p F wraps by itself.  (In fp64, of which an SM does two operations a clock, the
+// angles of 16K rows took 10 us of 70, and as much again for every part that the heads were divided
+// into.)
 //
 // Pages are dealt out by slots: sequence b owns the slots from floor(row_start[b] / 16) + 2 b on,
 // at least floor(n / 16) + 2 of them, and n rows touch at most that many pages; a slot without a
@@ -156,7 +157,6 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
   const int o0 = !turned || p.interleaved ? 16 * u : 8 * u;
   const int o1 = !turned || p.interleaved ? o0 + 8 : o0 + half;
 
-  // The warp's first (KV head, K or V): its rows are on their way under the sines below.
   // this CTA's share of the heads: every gridDim.y-th (KV head, K or V), a run of query heads
   const int part = blockIdx.y, parts = gridDim.y;
   const int tasks = 2 * p.hkv, task0 = part + parts * warp;
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(Threads, Threads == 256 ? 3 : 1)
       }
     }
   };
+  // The warp's first (KV head, K or V): its rows are on their way under the sines below.
   if (task0 < tasks) load_task(task0);
 
   // Queries: item i is unit i % U of head q0 + (i / U) % hq of row i / (U hq).
