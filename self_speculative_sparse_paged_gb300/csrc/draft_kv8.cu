@@ -8,8 +8,8 @@
 //
 // What bounds it: rows at random places come at 4.7 TB/s where they have 128 bytes and at 2.3 where
 // they have 64 (a plain gather of 4 million of them), and short lists at the length of the chain
-// index -> page -> row -> merge.  5.6 us at 1,645 entries x 8 heads of 128; 4 lists of 3,933
-// entries x 8 heads of 64: 11.0; 8 of 2,908 x 8 of 128: 16.7; 4 of 10,008 x 8 of 128: 22.0.
+// index -> page -> row -> merge.  5.8 us at 1,645 entries x 8 heads of 128; 4 lists of 3,933
+// entries x 8 heads of 64: 11.3; 8 of 2,908 x 8 of 128: 17.0; 4 of 10,008 x 8 of 128: 22.6.
 #include <cooperative_groups.h>
 
 #include "kernels.h"

@@ -5,8 +5,8 @@
 // goes by those and not by what its tables could hold.  A thread takes eight codes of one row (an 8-byte load,
 // a 16-byte store, both contiguous across the warp) at the same place of every head's block, K and V, a few
 // heads in flight; a block's exponent is one byte that all of its threads read.  Memory bounds it, at 6 d
-// bytes a position and head: 90,000 positions of 8 heads of 128 in 85.3 us, 0.95 of the copy peak; 700 of 2
-// heads of 64 1.8 us, a launch and two dependent loads.
+// bytes a position and head: 90,000 positions of 8 heads of 128 in 85.7 us, 0.95 of the copy peak; 700 of 2
+// heads of 64 1.7 us, a launch and two dependent loads.
 #include <algorithm>
 
 #include "kernels.h"

@@ -45,8 +45,8 @@
 // first S 1300, first reference 1600, end 2500).  56 columns at head_dim 64: the softmax's latency, 1900
 // clocks a tile with two warps a scheduler (no step above 550; without the row sums 8 us of 224 less, with P
 // in one f16 part and V turned by four more warps 29 us more).
-//   8 x 49K-64K, 24 columns of 128    157 us (0.90 of the copy peak)     32K: 23.0     64 x 1000: 44.0
-//   4 x 128K, 56 columns of 64        196 us (0.42)    one token each of 12 up to 8K: 17.5    2K, 20 of 64: 10.1
+//   8 x 49K-64K, 24 columns of 128    158 us (0.90 of the copy peak)     32K: 23.4     64 x 1000: 44.4
+//   4 x 128K, 56 columns of 64        197 us (0.42)    one token each of 12 up to 8K: 17.6    2K, 20 of 64: 10.2
 #include "attn_core.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
