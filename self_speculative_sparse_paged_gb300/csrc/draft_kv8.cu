@@ -10,13 +10,10 @@
 // they have 64 (a plain gather of 4 million of them), and short lists at the length of the chain
 // index -> page -> row -> merge.  5.8 us at 1,645 entries x 8 heads of 128; 4 lists of 3,933
 // entries x 8 heads of 64: 11.3; 8 of 2,908 x 8 of 128: 17.0; 4 of 10,008 x 8 of 128: 22.6.
-#include <cooperative_groups.h>
-
+#include "draft_cluster.cuh"
 #include "kernels.h"
 #include "kv8_core.cuh"
 #include "split_merge.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace vegas {
 
@@ -44,9 +41,7 @@ constexpr size_t draft_kv8_smem_bytes() {
   return Cfg::kStageBytes                                          // stages
          + (size_t(Cfg::kWarps) * Cfg::kStages + 1) * 8            // mbarriers (+ receive)
          + size_t(Cfg::kMaxRows) * 6                               // row table, scale exponents
-         + size_t(NT) * 8 * (D + 2) * 4                            // CTA partial
-         + (size_t(NT) * 8 * D + 4 * kMaxSparseCluster) * 4 + 16   // received output slices
-         + size_t(kMaxSparseCluster) * NT * 8 * 2 * 4              // received m, l
+         + DraftCluster<D, NT * 8>::kBytes                         // states of this CTA and of its peers
          + 1024;
 }
 static_assert(draft_kv8_smem_bytes<128, 1, 16>() <= 227 * 1024 &&
@@ -64,43 +59,20 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
   constexpr int TILE = DraftKv8Cfg<D, NT, W>::kTile;
   constexpr int STAGE = DraftKv8Cfg<D, NT, W>::kStage;
 
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int CL = (int)cluster.num_blocks();
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* stage_area = smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + DraftKv8Cfg<D, NT, W>::kStageBytes);
-  uint64_t* recv_bar = bars + W * STAGES;   // completes when every peer's state has landed
+  uint64_t* recv_bar = bars + W * STAGES;   // the cluster's receive barrier
   int32_t* rows = reinterpret_cast<int32_t*>(recv_bar + 1);
-  const int nel = p.group * D;              // output elements of the unit (G x D)
-  const int per = ((nel + CL - 1) / CL + 3) & ~3;   // CTA r owns [r * per, (r + 1) * per); 4 | per
-  if (threadIdx.x == 0) {
-    // Every CTA sends this one its slice of the partial output and its G row
-    // maxima and sums: 4 * CL * (slice + 2G) bytes, counted by st.async.
-    mbar_init(smem_u32(recv_bar), 1);
-    const int mine = max(0, min(per, nel - rank * per));
-    mbar_arrive_expect_tx(smem_u32(recv_bar), uint32_t(4 * CL * (mine + 2 * p.group)));
-    fence_mbar_init();
-  }
-  // First phase of the cluster barrier: this CTA has started and its receive
-  // barrier is set up (its shared memory may receive other CTAs' stores once
-  // every CTA has arrived).
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  griddep_begin();
   // entry i's exponents, K's in the low byte and V's in the high one
   uint16_t* exps = reinterpret_cast<uint16_t*>(rows + DraftKv8Cfg<D, NT, W>::kMaxRows);
-  float* pM = reinterpret_cast<float*>(exps + DraftKv8Cfg<D, NT, W>::kMaxRows);   // [NPAD] CTA partial
-  float* pL = pM + NPAD;                                                 // [NPAD]
-  float* pO = pL + NPAD;                                                 // [NPAD][D]
-  // [CL][per] output slices received (16-byte aligned: they arrive in 16-byte stores;
-  // CL * per <= G * D + 4 * CL - 1)
-  float* rO = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(pO + NPAD * D) + 15) &
-                                       ~uintptr_t(15));
-  float* rM = rO + NPAD * D + 4 * kMaxSparseCluster;   // [CL][NPAD] maxima received
-  float* rL = rM + kMaxSparseCluster * NPAD;     // [CL][NPAD] row sums received
+  DraftCluster<D, NPAD> peers;
+  peers.begin(recv_bar, p.group);
+  griddep_begin();
+  peers.set_areas(exps + DraftKv8Cfg<D, NT, W>::kMaxRows);
+  const int rank = peers.rank;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.y, b = blockIdx.z;
@@ -283,105 +255,18 @@ __global__ void __launch_bounds__(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1)
   reduce_row_sums<D, NT>(st);
   __syncthreads();
   cta_merge_to_smem<D, NT, W, Kv8Dims<D>, true>(st, stage_area, DraftKv8Cfg<D, NT, W>::kStageBytes,
-                                                p.group, pM, pL, pO);
+                                                p.group, peers.m, peers.l, peers.o);
   __syncthreads();   // the pushes below read elements other threads merged
 
-  // Cluster merge: CTA r owns the output elements [r * per, (r + 1) * per) of
-  // the G x D (per a multiple of four).  Every CTA pushes the slices of its
-  // state to their owners' receive areas with asynchronous distributed-
-  // shared-memory stores, 16 bytes each (four elements of one owner), and its
-  // G row maxima and sums to every CTA, one (CTA, row) pair a thread; each
-  // store counts against the owner's receive barrier, and an owner merges as
-  // soon as that barrier has counted every byte it expects:
-  // M = max_r m_r, O = sum_r 2^(m_r - M) O_r / sum_r 2^(m_r - M) l_r.
-  // The receive areas are used by nothing else, so only the
-  // barrier phase begun at entry (every CTA has started, its receive barrier
-  // is ready) precedes the stores, and no cluster barrier follows them.
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  {
-    const uint32_t rO_s = smem_u32(rO), rM_s = smem_u32(rM), rL_s = smem_u32(rL);
-    const uint32_t rb = smem_u32(recv_bar);
-    for (int e = 4 * tid; e < nel; e += 4 * NTH) {   // 4 | nel (D is 64 or 128)
-      const int owner = e / per;                      // e .. e + 3 share it
-      st_async_f32x4(cluster_map(rO_s + 4 * (rank * per + e - owner * per), owner), pO[e],
-                     pO[e + 1], pO[e + 2], pO[e + 3], cluster_map(rb, owner));
-    }
-    static_assert(kMaxSparseCluster * 16 <= NTH, "one (CTA, row) pair a thread");
-    const int t = NTH - 1 - tid;   // the last threads, which carry fewer elements
-    if (t < CL * p.group) {        // CL * G <= 256 <= NTH
-      const int r = t / p.group, n = t - r * p.group;
-      st_async_f32(cluster_map(rM_s + 4 * (rank * NPAD + n), r), pM[n], cluster_map(rb, r));
-      st_async_f32(cluster_map(rL_s + 4 * (rank * NPAD + n), r), pL[n], cluster_map(rb, r));
-    }
-  }
-  if (!mbar_wait_cluster_bounded(smem_u32(recv_bar), 0)) {
-    if (tid == 0) set_error(p.err, kErrDeviceTimeout);
-    return;
-  }
-  {
-    constexpr int R = kMaxSparseCluster;
-    const int e0 = rank * per, e1 = min(nel, e0 + per);
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
-    for (int e = e0 + tid; e < e1; e += NTH) {
-      const int n = e / D;
-      float mr[R], lr[R], v[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        mr[r] = -INFINITY;
-        lr[r] = v[r] = 0.f;
-        if (r < CL) {
-          mr[r] = rM[r * NPAD + n];
-          lr[r] = rL[r * NPAD + n];
-          v[r] = rO[r * per + e - e0];
-        }
-      }
-      float M = -INFINITY;
-#pragma unroll
-      for (int r = 0; r < R; ++r) M = fmaxf(M, mr[r]);
-      float L = 0.f, a = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float h = r < CL ? half_weight(mr[r] - M) : 0.f;
-        L += lr[r] * h * h;
-        a += h * h * v[r];
-      }
-      out[(size_t(b) * p.hq + g * p.group + n) * D + (e % D)] =
-          __float2bfloat16_rn(L > 0.f ? a / L : 0.f);
-    }
-  }
+  peers.template merge<NTH, true>(
+      reinterpret_cast<__nv_bfloat16*>(p.out) + (size_t(b) * p.hq + g * p.group) * D, p.err);
 }
 
-// Launches, or with `clusters` set, reports how many clusters of p.num_splits
-// CTAs can be resident at once.
 template <int D, int NT, int W>
 static cudaError_t launch_draft_kv8_w(const DraftKv8Params& p, int batch, cudaStream_t stream,
-                                      int* clusters = nullptr) {
-  constexpr size_t smem = draft_kv8_smem_bytes<D, NT, W>();
-  static std::atomic<uint32_t> configured{0};
-  cudaError_t e = once_per_device(configured, [] {
-    cudaError_t r = cudaFuncSetAttribute(draft_kv8_kernel<D, NT, W>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(draft_kv8_kernel<D, NT, W>,
-                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.num_splits, p.hkv, batch);
-  cfg.blockDim = dim3(DraftKv8Cfg<D, NT, W>::kWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.num_splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = clusters ? 1 : 2;
-  if (clusters) return cudaOccupancyMaxActiveClusters(clusters, draft_kv8_kernel<D, NT, W>, &cfg);
-  return cudaLaunchKernelEx(&cfg, draft_kv8_kernel<D, NT, W>, p);
+                                      int* clusters) {
+  return launch_draft_cluster<draft_kv8_kernel<D, NT, W>>(p, draft_kv8_smem_bytes<D, NT, W>(), W * 32, batch,
+                                                          stream, clusters);
 }
 
 template <int D, int NT>
@@ -389,7 +274,7 @@ static cudaError_t launch_draft_kv8_one(const DraftKv8Params& p, int batch, cuda
                                         int* clusters) {
   // (the count of resident clusters is the larger kernel's)
   return !clusters && p.rows_per_split <= kFewRows
-             ? launch_draft_kv8_w<D, NT, draft_kv8_warps<D, NT>(true)>(p, batch, stream)
+             ? launch_draft_kv8_w<D, NT, draft_kv8_warps<D, NT>(true)>(p, batch, stream, nullptr)
              : launch_draft_kv8_w<D, NT, draft_kv8_warps<D, NT>(false)>(p, batch, stream, clusters);
 }
 
@@ -412,27 +297,7 @@ cudaError_t launch_draft_kv8(const DraftKv8Params& p, int head_dim, int ntiles, 
 }
 
 int draft_kv8_max_active_clusters(int head_dim, int ntiles, int cluster) {
-  if (cluster < 1 || cluster > kMaxSparseCluster || ntiles < 1 || ntiles > 2) return 0;
-  constexpr int kDevices = 32;
-  // [device][head_dim 64/128][ntiles][cluster]: 0 unknown, -1 none, else the count
-  static std::atomic<int> cache[kDevices][2][3][kMaxSparseCluster + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-  std::atomic<int>& slot = cache[dev][head_dim == 128 ? 1 : 0][ntiles][cluster];
-  int c = slot.load(std::memory_order_acquire);
-  if (c == 0) {
-    DraftKv8Params p{};
-    p.hkv = 1;
-    p.num_splits = cluster;
-    int n = 0;
-    if (launch_draft_kv8_any(p, head_dim, ntiles, 1, 0, &n) != cudaSuccess) {
-      (void)cudaGetLastError();
-      n = 0;
-    }
-    c = n > 0 ? n : -1;
-    slot.store(c, std::memory_order_release);
-  }
-  return c > 0 ? c : 0;
+  return resident_draft_clusters<DraftKv8Params, launch_draft_kv8_any>(head_dim, ntiles, cluster);
 }
 
 }  // namespace vegas
