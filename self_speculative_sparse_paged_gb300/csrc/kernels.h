@@ -276,8 +276,9 @@ inline int verify_tc_max_active_clusters(int head_dim, int nq, bool capture, int
   return head_dim == 64 ? verify_tc_max_active_clusters_d64(nq, capture, cluster)
                         : verify_tc_max_active_clusters_d128(nq, capture, cluster);
 }
-// The query columns of the verify over the 8-bit cache.  (At head_dim 128 the bf16 one takes more; 48 and 56
-// columns would fit this kernel's shared and tensor memory, 64 not, but are not built.)
+// The query columns of the verify over the 8-bit cache: as many as verify_tc's.  (At head_dim 128 the bf16 call
+// takes 48, the last of them by its mma.sync kernel; 48 and 56 would fit this one's shared and tensor memory,
+// 64 not, but are not built.)
 inline bool verify_kv8_supported(int head_dim, int nq) {
   return nq >= 1 && nq <= (head_dim == 128 ? 40 : 64);
 }
